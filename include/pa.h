@@ -67,7 +67,7 @@ enum {
 };
 
 /* Element types. */
-enum { PA_F16 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2, PA_I32 = 3, PA_I64 = 4 };
+enum { PA_F16 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2, PA_I32 = 3, PA_I64 = 4, PA_F32 = 5 };
 
 /* kv_dtype argument: cache elements have the dtype of k/q (PA_KV_AUTO), or are
  * OCP e4m3 codes (uint8) with per-tensor scales (PA_KV_FP8_E4M3). */
@@ -78,8 +78,15 @@ enum {
   PA_DEVERR_BLOCK_ID = 1,  /* a block table entry outside [0, num_blocks) */
   PA_DEVERR_SEQ_LEN = 2,   /* seq_len < 0 or > max_blocks_per_seq * block_size */
   PA_DEVERR_SLOT = 4,      /* a slot_mapping entry >= num_blocks * block_size */
-  PA_DEVERR_TIMEOUT = 8    /* a pipeline wait gave up (should never happen, except
+  PA_DEVERR_TIMEOUT = 8,   /* a pipeline wait gave up (should never happen, except
                               in pa_selftest_bounded_wait) */
+  PA_DEVERR_POOL = 16,     /* pa_pool_extend: not enough free blocks; pa_pool_release:
+                              more blocks than the free list holds */
+  PA_DEVERR_TOKENS = 32,   /* pa_pool_extend: a negative request, or more new tokens
+                              than slot_mapping has rows */
+  PA_DEVERR_POSITION = 64, /* a position outside the rows of cos_sin */
+  PA_DEVERR_GROUP = 128    /* group_starts that decrease or leave [0, B], or a prefix
+                              that its group's tables cannot hold */
 };
 
 #define PA_MAX_DIMS 6
@@ -119,6 +126,101 @@ pa_status pa_reshape_and_cache(const pa_tensor* k, const pa_tensor* v,
                                const pa_tensor* key_cache, const pa_tensor* value_cache,
                                const pa_tensor* slot_mapping, int32_t kv_dtype,
                                float k_scale, float v_scale, pa_stream stream);
+
+/*
+ * pa_norm_rope_and_cache — the step from a projection's output rows to the
+ * cache and the attention's queries: per-head RMS norm of q and k, position
+ * rotation, and the write of k and v to their slots, in one pass.
+ * For every row t and every head x of q (weight q_weight) and k (k_weight):
+ *   y = x * w / sqrt(mean(x^2) + eps)      (y = x where the weight is NULL)
+ * and, with (c, s) the cosines and sines of row positions[t] of cos_sin, pair
+ * i < R / 2 of y's first R elements becomes
+ *   (a, b) -> (a c_i - b s_i, b c_i + a s_i),
+ * (a, b) = elements (i, i + R / 2), or (2 i, 2 i + 1) if `interleaved` is not
+ * zero. All in fp32 from the inputs to the one rounding of each result.
+ *   q_out[t, h, :] = rotated q;  key_cache, value_cache at slot_mapping[t]
+ *   = enc(rotated k), enc(v), with slots, enc and scales as in
+ *   pa_reshape_and_cache (for PA_KV_AUTO v is a bit copy).
+ * A row with a negative slot writes nothing to the caches; its q_out row is
+ * computed all the same. A position outside [0, P) uses the nearest row and is
+ * flagged (PA_DEVERR_POSITION).
+ *
+ *   q             [T, Hq, D] f16/bf16; k, v [T, Hkv, D] of the same dtype;
+ *                 dims 1 and 2 contiguous, dim 0 any stride (views of one
+ *                 packed projection row, for instance); rows 16-byte aligned.
+ *   q_out         [T, Hq, D], as q; q itself (same data and row stride) for
+ *                 an update in place, else it overlaps no other tensor.
+ *   cos_sin       [P, R] f32 contiguous, 16-byte aligned: R / 2 cosines, then
+ *                 R / 2 sines a row; R = 0: no rotation.
+ *   positions     [T] int32.
+ *   q_weight, k_weight  [D] of q's dtype, 16-byte aligned, or NULL.
+ *   caches, slot_mapping, kv_dtype, scales: as for pa_reshape_and_cache.
+ * D: a multiple of 16, at most 256; R: a multiple of 16, at most D.
+ * The launch lets its dependents start early; it writes none of block_tables,
+ * seq_lens or a workspace, so pa_decode and pa_prefill_chunk, which read q
+ * and the caches only behind their dependency wait, may follow directly.
+ */
+pa_status pa_norm_rope_and_cache(const pa_tensor* q_out, const pa_tensor* q, const pa_tensor* k,
+                                 const pa_tensor* v, const pa_tensor* key_cache,
+                                 const pa_tensor* value_cache, const pa_tensor* slot_mapping,
+                                 const pa_tensor* positions, const pa_tensor* cos_sin,
+                                 const pa_tensor* q_weight, const pa_tensor* k_weight, float eps,
+                                 int32_t interleaved, int32_t kv_dtype, float k_scale,
+                                 float v_scale, pa_stream stream);
+
+/* ------------------------------------------------------- block pool on the GPU */
+
+/*
+ * A block pool that lives on the GPU, for steps that are enqueued or replayed
+ * (CUDA graphs) without the host in between: where pa_alloc_* builds tables on
+ * the host, these two calls build them from lengths in device memory.
+ *   free_list     [NB] int32: the ids free_list[0 .. count) are free, the last
+ *                 is taken first; ids are in [0, NB).
+ *   pool_state    [2] int32: {count, 0}. The second word is the library's
+ *                 during a call and zero between calls.
+ *   block_tables  [B, MB] int32 contiguous; seq_lens [B] int32, as pa_decode
+ *                 reads them. B <= 4096.
+ * seq_lens_out and pool_state_out receive the state after the call; each may be
+ * the input itself (the same data pointer), and overlaps nothing else.
+ * Both calls are all-or-nothing: if anything is out of range the whole call
+ * leaves tables, free list, lengths and count as they were (copied to the
+ * outputs) and sets a bit of the device error word. Results do not depend on
+ * the order in which the GPU works. Calls on one pool that overlap on the GPU
+ * race and must not be issued.
+ *
+ * pa_pool_extend — grows sequence b by n = new_tokens[b] >= 0 tokens: pops
+ * ceil((L + n) / bs) - ceil(L / bs) blocks, sequences in order, into the next
+ * entries of its table (no other entry is written). Its new tokens are rows
+ * [query_start[b], query_start[b + 1]) of the step, row query_start[b] + i at
+ *   positions[.] = L + i,  slot_mapping[.] = table[p / bs] * bs + p % bs;
+ * the rows behind the last sequence's get slot -1 (which the write path skips)
+ * and position 0. The slot of a token whose table entry is not in [0, NB) is
+ * -1 (PA_DEVERR_BLOCK_ID).
+ *   query_start   [B + 1] int32; slot_mapping [T] int64; positions [T] int32.
+ * Refused as a whole: too few free blocks (PA_DEVERR_POOL), a negative request
+ * or more than T new tokens (PA_DEVERR_TOKENS), L < 0 or L + n > MB * bs
+ * (PA_DEVERR_SEQ_LEN); then query_start is all zero and every row has slot -1.
+ *
+ * pa_pool_release — gives the blocks of every sequence with released[b] != 0
+ * back: pushes its table entries from shared_tokens[b] / bs (0 where
+ * shared_tokens is NULL) up to ceil(L / bs), sequences in order, and sets its
+ * length to 0. Leading blocks that other sequences share stay with the
+ * caller. Tables are not written. Entries must be block ids (one that is not
+ * in [0, NB) is pushed and flagged PA_DEVERR_BLOCK_ID; pa_pool_extend flags it
+ * again when it is popped).
+ *   released      [B] int32; shared_tokens [B] int32 or NULL.
+ */
+pa_status pa_pool_extend(const pa_tensor* block_tables, const pa_tensor* seq_lens,
+                         const pa_tensor* new_tokens, const pa_tensor* free_list,
+                         const pa_tensor* pool_state, const pa_tensor* seq_lens_out,
+                         const pa_tensor* pool_state_out, const pa_tensor* query_start,
+                         const pa_tensor* slot_mapping, const pa_tensor* positions,
+                         int32_t block_size, pa_stream stream);
+pa_status pa_pool_release(const pa_tensor* block_tables, const pa_tensor* seq_lens,
+                          const pa_tensor* released, const pa_tensor* shared_tokens,
+                          const pa_tensor* free_list, const pa_tensor* pool_state,
+                          const pa_tensor* seq_lens_out, const pa_tensor* pool_state_out,
+                          int32_t block_size, pa_stream stream);
 
 /* ---------------------------------------------------------------- decode */
 

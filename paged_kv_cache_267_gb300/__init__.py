@@ -13,9 +13,10 @@ import torch
 
 from .build import LIB_PATH
 
-PA_F16, PA_BF16, PA_FP8_E4M3, PA_I32, PA_I64 = 0, 1, 2, 3, 4
+PA_F16, PA_BF16, PA_FP8_E4M3, PA_I32, PA_I64, PA_F32 = 0, 1, 2, 3, 4, 5
 PA_KV_AUTO, PA_KV_FP8_E4M3 = 0, 2
 DEVERR_BLOCK_ID, DEVERR_SEQ_LEN, DEVERR_SLOT, DEVERR_TIMEOUT = 1, 2, 4, 8
+DEVERR_POOL, DEVERR_TOKENS, DEVERR_POSITION, DEVERR_GROUP = 16, 32, 64, 128
 _MAX_DIMS = 6
 
 _STATUS = {0: "PA_OK", -1: "PA_ERR_INVALID_ARG", -2: "PA_ERR_UNSUPPORTED", -3: "PA_ERR_LAYOUT",
@@ -54,6 +55,9 @@ def lib() -> ctypes.CDLL:
                                  ctypes.c_int32)
         sig = {
             "pa_reshape_and_cache": (st, [P, P, P, P, P, i32, f32, f32, vp]),
+            "pa_norm_rope_and_cache": (st, [P] * 11 + [f32, i32, i32, f32, f32, vp]),
+            "pa_pool_extend": (st, [P] * 10 + [i32, vp]),
+            "pa_pool_release": (st, [P] * 8 + [i32, vp]),
             "pa_decode": (st, [P, P, P, P, P, P, i32, f32, i32, i32, i32, f32, f32, vp]),
             "pa_decode_noalloc": (st, [P, P, P, P, P, P, i32, f32, i32, i32, i32, f32, f32, vp]),
             "pa_decode_workspace_size": (st, [i64, i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)]),
@@ -106,7 +110,8 @@ def _check(status: int) -> None:
 
 
 _TORCH_TO_PA = {torch.float16: PA_F16, torch.bfloat16: PA_BF16, torch.uint8: PA_FP8_E4M3,
-                torch.float8_e4m3fn: PA_FP8_E4M3, torch.int32: PA_I32, torch.int64: PA_I64}
+                torch.float8_e4m3fn: PA_FP8_E4M3, torch.int32: PA_I32, torch.int64: PA_I64,
+                torch.float32: PA_F32}
 
 
 def tensor_desc(t: torch.Tensor) -> PaTensor:
@@ -149,6 +154,60 @@ def reshape_and_cache(k, v, key_cache, value_cache, slot_mapping, kv_dtype="auto
     descs = [tensor_desc(x) for x in (k, v, key_cache, value_cache, slot_mapping)]
     _check(lib().pa_reshape_and_cache(*[ctypes.byref(d) for d in descs], _kv(kv_dtype),
                                       float(k_scale), float(v_scale), _stream(stream)))
+
+
+def _ref(t):
+    """Descriptor argument of a tensor, or NULL for None."""
+    return None if t is None else ctypes.byref(tensor_desc(t))
+
+
+def norm_rope_and_cache(q, k, v, key_cache, value_cache, slot_mapping, positions, cos_sin, *,
+                        q_weight=None, k_weight=None, eps: float = 1e-6,
+                        interleaved: bool = False, kv_dtype="auto", k_scale: float = 1.0,
+                        v_scale: float = 1.0, out=None, stream=None):
+    """RMS norm of every q and k head (where its weight is given), rotation of
+    the first cos_sin.shape[1] elements by row positions[t] of cos_sin (f32
+    [P, R], cosines then sines), and the write of k and v to slot_mapping, in
+    one pass over the rows q [T, Hq, D], k, v [T, Hkv, D]. Returns the queries
+    [T, Hq, D] (allocated if `out` is not given; `out=q` updates in place)."""
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    _check(lib().pa_norm_rope_and_cache(
+        *[_ref(x) for x in (out, q, k, v, key_cache, value_cache, slot_mapping, positions,
+                            cos_sin, q_weight, k_weight)],
+        float(eps), int(bool(interleaved)), _kv(kv_dtype), float(k_scale), float(v_scale),
+        _stream(stream)))
+    return out
+
+
+def pool_extend(block_tables, seq_lens, new_tokens, free_list, pool_state, *, block_size: int,
+                slot_mapping, positions, query_start, seq_lens_out=None, pool_state_out=None,
+                stream=None) -> None:
+    """Grow every sequence b by new_tokens[b] tokens on the GPU: pops the
+    blocks it needs off free_list[:pool_state[0]] into block_tables, and
+    writes query_start [B + 1], slot_mapping [T] and positions [T] of the new
+    tokens (slot -1 behind the last). Lengths and pool state are updated in
+    place unless outputs are given. A step that does not fit changes nothing
+    and sets DEVERR_POOL, DEVERR_TOKENS or DEVERR_SEQ_LEN."""
+    _check(lib().pa_pool_extend(
+        *[_ref(x) for x in (block_tables, seq_lens, new_tokens, free_list, pool_state,
+                            seq_lens if seq_lens_out is None else seq_lens_out,
+                            pool_state if pool_state_out is None else pool_state_out,
+                            query_start, slot_mapping, positions)],
+        int(block_size), _stream(stream)))
+
+
+def pool_release(block_tables, seq_lens, released, free_list, pool_state, *, block_size: int,
+                 shared_tokens=None, seq_lens_out=None, pool_state_out=None,
+                 stream=None) -> None:
+    """Give the blocks of the sequences with released[b] != 0 back to the free
+    list (all but the leading ones that hold shared_tokens[b] tokens) and set
+    their lengths to 0, in place unless outputs are given."""
+    _check(lib().pa_pool_release(
+        *[_ref(x) for x in (block_tables, seq_lens, released, shared_tokens, free_list,
+                            pool_state, seq_lens if seq_lens_out is None else seq_lens_out,
+                            pool_state if pool_state_out is None else pool_state_out)],
+        int(block_size), _stream(stream)))
 
 
 def decode(q, key_cache, value_cache, block_tables, seq_lens, *, num_kv_heads: int,

@@ -19,6 +19,7 @@
 #include <tuple>
 
 #include "pa.h"
+#include "pa_host.h"
 #include "pa_internal.h"
 
 namespace pa {
@@ -51,13 +52,15 @@ constexpr int kDefaultPieceFp8 = 8;
 constexpr int kPiecesPerWorker = 4;        // pool pieces per worker warp, at most
 constexpr int kMaxCtasPerSm = 2;
 constexpr int kWarpsPerCta = 8;  // most worker warps of any decode variant
-constexpr int64_t kMaxBatch = 4096;
 constexpr int64_t kMaxChunk = 4096;        // query tokens per sequence in a chunk call
-constexpr double kMaxTensorBytes = 1125899906842624.0;  // 2^50: no tensor is larger
 // Chunks with more (query, head) columns per KV head than this go to the
 // tensor-memory kernel (head dim 128, 16-bit or e4m3 caches): the persistent kernel
 // reads each K/V tile once per 16 columns.
 constexpr int64_t kTcMinColumns = 32;
+
+}  // namespace
+
+namespace pa {
 
 pa_status fail(pa_status code, const char* fmt, ...) {
   va_list ap;
@@ -81,7 +84,8 @@ int elem_size(int32_t dt) {
     case PA_F16:
     case PA_BF16: return 2;
     case PA_FP8_E4M3: return 1;
-    case PA_I32: return 4;
+    case PA_I32:
+    case PA_F32: return 4;
     case PA_I64: return 8;
     default: return 0;
   }
@@ -177,6 +181,12 @@ pa_status check_accessible(const pa_tensor* t, const char* name) {
   if (!t || numel(t) == 0 || !t->data) return PA_OK;
   return check_accessible_ptr(t->data, name);
 }
+
+}  // namespace pa
+
+namespace {
+
+using namespace pa;  // the checking helpers (pa_host.h)
 
 // ------------------------------------------------------------ device state
 
@@ -1025,4 +1035,16 @@ pa_status decode_in_buffer(const pa_tensor* out, const pa_tensor* q, const pa_te
 namespace pa {
 pa_status set_error(pa_status code, const char* msg) { return fail(code, "%s", msg); }
 pa_status set_cuda_error(cudaError_t e, const char* what) { return cuda_fail(e, what); }
+}  // namespace pa
+
+namespace pa {
+pa_status device_info(DeviceInfo* out) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  DeviceState* st;
+  const pa_status s = device_state(&st, nullptr);
+  if (s) return s;
+  *out = DeviceInfo{st->err_word, st->num_sms};
+  return PA_OK;
+}
+void count_launches(int n) { g_launches += static_cast<uint64_t>(n); }
 }  // namespace pa
