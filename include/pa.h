@@ -314,6 +314,43 @@ pa_status pa_decode_noalloc(const pa_tensor* out, const pa_tensor* q,
                             int32_t window, int32_t kv_dtype, float k_scale, float v_scale,
                             pa_stream stream);
 
+/*
+ * pa_decode_shared — pa_decode for a batch whose sequences share prefixes: the
+ * shared positions of a group are read and multiplied once for all of its
+ * sequences instead of once for each. The result is pa_decode's (up to the
+ * order of summation).
+ *   group_starts  [NG + 1] int32, non-decreasing: group g is the rows
+ *                 [group_starts[g], group_starts[g + 1]) of the batch. Rows in
+ *                 no group are decoded by themselves.
+ *   prefix_lens   [NG] int32: the rows of group g have the same physical blocks
+ *                 in their first prefix_lens[g] / bs table entries (as pa_alloc_fork
+ *                 and pa_alloc_add_cached leave them). Tokens of a last, partial
+ *                 block count to the tails.
+ *   every other argument as for pa_decode. NG <= 4096; NG = 0 is pa_decode.
+ * A sequence takes part in its group's shared pass if it attends to all of
+ * the prefix (it is at least that long and no window cuts it); any other one,
+ * an idle row of length 0 among them, is decoded by itself, as is a group with
+ * fewer than two that do. The prefix is read through the table of the
+ * group's first row that takes part.
+ * Data errors: a prefix length outside [0, MB * bs] or group starts that
+ * decrease or leave [0, B] are clamped and flagged (PA_DEVERR_GROUP).
+ * Like pa_decode, the call reads group_starts, prefix_lens, seq_lens and
+ * block_tables before it waits for the previous kernel of the stream, and q
+ * and the caches after.
+ * Workspace: pa_decode_shared_workspace_size() bytes, from the same source as
+ * pa_decode's and under the same rules. Errors as for pa_decode.
+ */
+pa_status pa_decode_shared(const pa_tensor* out, const pa_tensor* q, const pa_tensor* key_cache,
+                           const pa_tensor* value_cache, const pa_tensor* block_tables,
+                           const pa_tensor* seq_lens, const pa_tensor* prefix_lens,
+                           const pa_tensor* group_starts, int32_t num_kv_heads, float scale,
+                           int32_t block_size, int32_t window, int32_t kv_dtype, float k_scale,
+                           float v_scale, pa_stream stream);
+
+/* Workspace bytes pa_decode_shared needs on the current device. */
+pa_status pa_decode_shared_workspace_size(int64_t batch, int64_t num_groups, int32_t num_q_heads,
+                                          int32_t num_kv_heads, int32_t head_dim, size_t* bytes);
+
 /* Workspace bytes pa_decode needs on the current device for a batch of
  * `batch` sequences with these head counts and head_dim. */
 pa_status pa_decode_workspace_size(int64_t batch, int32_t num_q_heads, int32_t num_kv_heads,

@@ -60,6 +60,9 @@ def lib() -> ctypes.CDLL:
             "pa_pool_release": (st, [P] * 8 + [i32, vp]),
             "pa_decode": (st, [P, P, P, P, P, P, i32, f32, i32, i32, i32, f32, f32, vp]),
             "pa_decode_noalloc": (st, [P, P, P, P, P, P, i32, f32, i32, i32, i32, f32, f32, vp]),
+            "pa_decode_shared": (st, [P] * 8 + [i32, f32, i32, i32, i32, f32, f32, vp]),
+            "pa_decode_shared_workspace_size": (st, [i64, i64, i32, i32, i32,
+                                                     ctypes.POINTER(ctypes.c_size_t)]),
             "pa_decode_workspace_size": (st, [i64, i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)]),
             "pa_prefill_chunk": (st, [P, P, P, P, P, P, i32, f32, i32, i32, i32, f32, f32, vp]),
             "pa_prefill_chunk_workspace_size": (st, [i64, i32, i32, i32, i32,
@@ -223,6 +226,24 @@ def decode(q, key_cache, value_cache, block_tables, seq_lens, *, num_kv_heads: i
     return out
 
 
+def decode_shared(q, key_cache, value_cache, block_tables, seq_lens, prefix_lens, group_starts, *,
+                  num_kv_heads: int, scale: float, block_size: int, window: int = 0,
+                  kv_dtype="auto", k_scale: float = 1.0, v_scale: float = 1.0, out=None,
+                  stream=None):
+    """One paged decode step of a batch whose rows [group_starts[g],
+    group_starts[g + 1]) share their first prefix_lens[g] tokens (the same
+    blocks in their tables): the shared positions are attended to once for
+    the whole group. Returns what decode returns."""
+    if out is None:
+        out = torch.empty_like(q)
+    _check(lib().pa_decode_shared(
+        *[_ref(x) for x in (out, q, key_cache, value_cache, block_tables, seq_lens, prefix_lens,
+                            group_starts)],
+        int(num_kv_heads), float(scale), int(block_size), int(window), _kv(kv_dtype),
+        float(k_scale), float(v_scale), _stream(stream)))
+    return out
+
+
 def prefill_chunk(q, key_cache, value_cache, block_tables, seq_lens, *, num_kv_heads: int,
                   scale: float, block_size: int, window: int = 0, kv_dtype="auto",
                   k_scale: float = 1.0, v_scale: float = 1.0, out=None, stream=None):
@@ -255,6 +276,14 @@ def workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: in
     n = ctypes.c_size_t(0)
     _check(lib().pa_decode_workspace_size(batch, num_q_heads, num_kv_heads, head_dim,
                                           ctypes.byref(n)))
+    return n.value
+
+
+def decode_shared_workspace_size(batch: int, num_groups: int, num_q_heads: int,
+                                 num_kv_heads: int, head_dim: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().pa_decode_shared_workspace_size(batch, num_groups, num_q_heads, num_kv_heads,
+                                                 head_dim, ctypes.byref(n)))
     return n.value
 
 

@@ -64,6 +64,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "attn_tc.cuh"
 #include "pa_internal.h"
 #include "ptx.cuh"
 #include "tc.cuh"
@@ -120,40 +121,6 @@ constexpr float kFloor = -1e30f;             // reference-max start
 constexpr float kRescaleAbove = 8.f;         // log2 units
 constexpr unsigned kFull = 0xffffffffu;
 
-__device__ __forceinline__ void sts_v4(uint32_t addr, uint4 v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
-               "r"(v.z), "r"(v.w)
-               : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack16x2(float lo, float hi) {
-  if constexpr (BF16) {
-    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&v);
-  } else {
-    __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&v);
-  }
-}
-// max of three (one instruction on sm_103a)
-__device__ __forceinline__ float fmax3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-// Two consecutive 32-bit tensor-memory values as an fp32 pair.
-__device__ __forceinline__ float2 score_pair(const uint32_t* v, int i) {
-  return make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity) {
   return __all_sync(kFull, mbar_wait_bounded(bar, parity, kWaitNs));
 }

@@ -51,6 +51,11 @@
 // running maxima start at a finite floor so that a column with no position in
 // a segment yields m = floor, l = 0 and a zero output.
 //
+// Shared prefixes (SH = true, single queries). Part of the batch has its leading
+// positions covered by the prefix kernel: every sequence's range starts at the
+// position the step's shared plan gives (shared_plan.cuh) instead of the
+// window's start, and is empty where the prefix is all there is.
+//
 // FP8 e4m3 caches: codes are converted to f16 in registers (exact), Q is
 // converted once per segment to f16 after a power-of-two rescale so its
 // largest magnitude lies in [2^14, 2^15), and k_scale, v_scale and the rescale
@@ -65,6 +70,7 @@
 #include "pa_internal.h"
 #include "plan.cuh"
 #include "ptx.cuh"
+#include "shared_plan.cuh"
 
 namespace pa {
 
@@ -158,7 +164,7 @@ constexpr unsigned kFlagStart = 1, kFlagEnd = 2, kFlagPool = 4;
 constexpr float kMaskedFloor = -1e30f;  // running-max start of chunked columns
 constexpr float kRefSlack = 8.f;        // log2 units a score may exceed the reference max
 
-template <int CT, int QT, int D, int NT, int WARPS, int STAGES, bool MQ>
+template <int CT, int QT, int D, int NT, int WARPS, int STAGES, bool MQ, bool SH>
 __global__ void __launch_bounds__(WARPS * 32, 2)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const DecodeArgs a) {
@@ -176,6 +182,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
   int* s_meta = reinterpret_cast<int*>(gbase + WARPS * Gm::RING_BYTES + WARPS * STAGES * 8);
   int* s_len = s_meta + 2 * WARPS * STAGES;
   int* s_pref = s_len + a.B;
+  int* s_first = s_pref + a.B + 1;  // SH: first position of each sequence's range
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t4 = lane & 3;
@@ -209,7 +216,15 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
   pin.min_tiles = a.min_tiles;
   pin.np_max = a.np_max;
   pin.piece_min = a.piece_min;
-  const StepPlan pl = plan_step(pin, s_len, s_pref);
+  if constexpr (SH) {
+    for (int b = tid; b < a.B; b += blockDim.x) s_first[b] = a.shared_rows[b].start;
+  }
+  // first position of sequence b's range
+  auto start_of = [&](int b) -> int {
+    if constexpr (SH) return s_first[b];
+    else return win_start(s_len[b], a.span);
+  };
+  const StepPlan pl = plan_step<SH>(pin, s_len, s_pref, s_first);
   const int total = pl.total, ws = pl.ws, ts = pl.ts;
   const int nw = pin.nw;
   const int pool_tiles = total - ts;
@@ -317,8 +332,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
       // static range about to end: claim the first pool piece now
       if (phase == 0 && pool_tiles > 0 && !claim_issued) issue_claim();
     }
-    const int L = s_len[pc.b];
-    const int pt = win_start(L, a.span) / kTile + pc.t;  // tile index in position space
+    const int pt = start_of(pc.b) / kTile + pc.t;  // tile index in position space
     const int lb = (pt * kTile) / a.bs;
     refresh_window(pc.b, lb);
     int phys = __shfl_sync(FULL, id_val, lb - id_lb0);
@@ -354,10 +368,14 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
   if (f0 < f1) {
     Cursor c0;
     cursor_locate(c0, f0, s_pref, a.B, a.Hv);
-    const int pt0 = win_start(s_len[c0.b], a.span) / kTile + c0.t;
+    const int pt0 = start_of(c0.b) / kTile + c0.t;
     refresh_window(c0.b, (pt0 * kTile) / a.bs);
   }
-  griddep_wait();  // the caches may have been written by the previous kernel
+  // The caches may have been written by the previous kernel. SH: that is the
+  // prefix kernel, which starts this one only after what it waited for itself,
+  // the write path among it, has finished, and writes nothing read here; the
+  // wait comes at the end, so that what follows this kernel follows both.
+  if constexpr (!SH) griddep_wait();
   for (int i = 0; i < STAGES; ++i) {
     if (!produce(produced % STAGES)) break;
     ++produced;
@@ -504,7 +522,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
 
     // tile position and edge masks
     const int L = s_len[cc.b];
-    const int st = win_start(L, a.span);
+    const int st = start_of(cc.b);
     const int p0 = (st / kTile + cc.t) * kTile;
     const bool edge = (p0 < st) || (p0 + kTile > L);  // outside the pair's union range
     auto valid = [&](int r) { return !edge || (p0 + r >= st && p0 + r < L); };
@@ -742,15 +760,16 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
     for (int k = consumed; k < produced; ++k)
       (void)mbar_wait_bounded(wbars + 8 * (k % STAGES), (k / STAGES) & 1, kDrainLimitNs);
   }
+  if constexpr (SH) griddep_wait();
 }
 
 // ---------------------------------------------------------------- host side
 
-template <int CT, int QT, int D, int NT, int WARPS, int STAGES, bool MQ>
+template <int CT, int QT, int D, int NT, int WARPS, int STAGES, bool MQ, bool SH>
 struct DecodeKernel {
   using Gm = Geometry<CT, D, STAGES>;
   static void* fn() {
-    return reinterpret_cast<void*>(&paged_decode_kernel<CT, QT, D, NT, WARPS, STAGES, MQ>);
+    return reinterpret_cast<void*>(&paged_decode_kernel<CT, QT, D, NT, WARPS, STAGES, MQ, SH>);
   }
   static DecodeVariant variant() { return DecodeVariant{WARPS, STAGES, WARPS * Gm::RING_BYTES}; }
   static cudaError_t prepare(int smem, int* ctas_per_sm) {
@@ -771,7 +790,7 @@ struct DecodeKernel {
     attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_decode_kernel<CT, QT, D, NT, WARPS, STAGES, MQ>, tk,
+    return cudaLaunchKernelEx(&cfg, paged_decode_kernel<CT, QT, D, NT, WARPS, STAGES, MQ, SH>, tk,
                               tv, a);
   }
 };
@@ -795,33 +814,33 @@ constexpr int stages_for() {
 }
 
 // Expands `BODY` with the kernel type K for a runtime (D, NT) pair.
-#define PA_DECODE_DISPATCH(CT, QT, MQ, D_, NT_, BODY)                             \
+#define PA_DECODE_DISPATCH(CT, QT, MQ, SH, D_, NT_, BODY)                         \
   do {                                                                            \
     if ((D_) == 64 && (NT_) == 1 && (CT) != kE4M3) {                              \
       constexpr int D0 = (CT) != kE4M3 ? 64 : 128;                                \
       using K = DecodeKernel<CT, QT, D0, 1, warps_for<CT, D0, 1>(),               \
-                             stages_for<CT, D0, 1>(), MQ>;                        \
+                             stages_for<CT, D0, 1>(), MQ, SH>;                        \
       BODY;                                                                       \
     } else if ((D_) == 64 && (NT_) == 2 && (CT) != kE4M3) {                       \
       constexpr int D0 = (CT) != kE4M3 ? 64 : 128;                                \
       using K = DecodeKernel<CT, QT, D0, 2, warps_for<CT, D0, 2>(),               \
-                             stages_for<CT, D0, 2>(), MQ>;                        \
+                             stages_for<CT, D0, 2>(), MQ, SH>;                        \
       BODY;                                                                       \
     } else if ((D_) == 128 && (NT_) == 1) {                                       \
       using K = DecodeKernel<CT, QT, 128, 1, warps_for<CT, 128, 1>(),            \
-                             stages_for<CT, 128, 1>(), MQ>;                      \
+                             stages_for<CT, 128, 1>(), MQ, SH>;                      \
       BODY;                                                                       \
     } else if ((D_) == 128 && (NT_) == 2) {                                       \
       using K = DecodeKernel<CT, QT, 128, 2, warps_for<CT, 128, 2>(),            \
-                             stages_for<CT, 128, 2>(), MQ>;                      \
+                             stages_for<CT, 128, 2>(), MQ, SH>;                      \
       BODY;                                                                       \
     } else if ((D_) == 256 && (NT_) == 1) {                                       \
       using K = DecodeKernel<CT, QT, 256, 1, warps_for<CT, 256, 1>(),            \
-                             stages_for<CT, 256, 1>(), MQ>;                      \
+                             stages_for<CT, 256, 1>(), MQ, SH>;                      \
       BODY;                                                                       \
     } else if ((D_) == 256 && (NT_) == 2) {                                       \
       using K = DecodeKernel<CT, QT, 256, 2, warps_for<CT, 256, 2>(),            \
-                             stages_for<CT, 256, 2>(), MQ>;                      \
+                             stages_for<CT, 256, 2>(), MQ, SH>;                      \
       BODY;                                                                       \
     } else {                                                                      \
       return cudaErrorInvalidValue;                                               \
@@ -830,20 +849,20 @@ constexpr int stages_for() {
 
 // The three entry points of one (cache type, q type, chunked) family; each
 // translation unit defines one or two families so that they build in parallel.
-#define PA_DECODE_FAMILY(NAME, CT, QT, MQ)                                             \
+#define PA_DECODE_FAMILY(NAME, CT, QT, MQ, SH)                                         \
   cudaError_t decode_variant_##NAME(int D, int nt, DecodeVariant* v) {                  \
-    PA_DECODE_DISPATCH(CT, QT, MQ, D, nt, {                                            \
+    PA_DECODE_DISPATCH(CT, QT, MQ, SH, D, nt, {                                            \
       *v = K::variant();                                                               \
       return cudaSuccess;                                                              \
     });                                                                                \
   }                                                                                    \
   cudaError_t decode_prepare_##NAME(int D, int nt, int smem, int* ctas_per_sm) {        \
-    PA_DECODE_DISPATCH(CT, QT, MQ, D, nt, { return K::prepare(smem, ctas_per_sm); });  \
+    PA_DECODE_DISPATCH(CT, QT, MQ, SH, D, nt, { return K::prepare(smem, ctas_per_sm); });  \
   }                                                                                    \
   cudaError_t decode_launch_##NAME(int D, int nt, const CUtensorMap& tk,                \
                                    const CUtensorMap& tv, const DecodeArgs& a, int grid, \
                                    int smem, cudaStream_t s, bool pdl) {               \
-    PA_DECODE_DISPATCH(CT, QT, MQ, D, nt,                                              \
+    PA_DECODE_DISPATCH(CT, QT, MQ, SH, D, nt,                                              \
                        { return K::launch(tk, tv, a, grid, smem, s, pdl); });          \
   }
 

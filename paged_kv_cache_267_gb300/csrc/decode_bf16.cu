@@ -3,6 +3,6 @@
 
 namespace pa {
 
-PA_DECODE_FAMILY(bf16, kBF16, kBF16, false)
+PA_DECODE_FAMILY(bf16, kBF16, kBF16, false, false)
 
 }  // namespace pa

@@ -3,6 +3,6 @@
 
 namespace pa {
 
-PA_DECODE_FAMILY(f16, kF16, kF16, false)
+PA_DECODE_FAMILY(f16, kF16, kF16, false, false)
 
 }  // namespace pa

@@ -3,7 +3,7 @@
 
 namespace pa {
 
-PA_DECODE_FAMILY(fp8_bf16, kE4M3, kBF16, false)
-PA_DECODE_FAMILY(fp8_f16, kE4M3, kF16, false)
+PA_DECODE_FAMILY(fp8_bf16, kE4M3, kBF16, false, false)
+PA_DECODE_FAMILY(fp8_f16, kE4M3, kF16, false, false)
 
 }  // namespace pa

@@ -3,6 +3,6 @@
 
 namespace pa {
 
-PA_DECODE_FAMILY(mq_bf16, kBF16, kBF16, true)
+PA_DECODE_FAMILY(mq_bf16, kBF16, kBF16, true, false)
 
 }  // namespace pa

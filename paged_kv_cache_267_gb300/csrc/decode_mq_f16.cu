@@ -3,6 +3,6 @@
 
 namespace pa {
 
-PA_DECODE_FAMILY(mq_f16, kF16, kF16, true)
+PA_DECODE_FAMILY(mq_f16, kF16, kF16, true, false)
 
 }  // namespace pa

@@ -3,7 +3,7 @@
 
 namespace pa {
 
-PA_DECODE_FAMILY(mq_fp8_bf16, kE4M3, kBF16, true)
-PA_DECODE_FAMILY(mq_fp8_f16, kE4M3, kF16, true)
+PA_DECODE_FAMILY(mq_fp8_bf16, kE4M3, kBF16, true, false)
+PA_DECODE_FAMILY(mq_fp8_f16, kE4M3, kF16, true, false)
 
 }  // namespace pa

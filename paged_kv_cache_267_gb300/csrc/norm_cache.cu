@@ -22,6 +22,7 @@
 
 #include "pa_internal.h"
 #include "ptx.cuh"
+#include "step_ops.h"
 
 namespace pa {
 namespace {

@@ -21,6 +21,8 @@
 #include "pa.h"
 #include "pa_host.h"
 #include "pa_internal.h"
+#include "shared_plan.cuh"
+#include "step_ops.h"
 
 namespace pa {
 // Defined in selftest.cu: one CTA whose two waits (an mbarrier phase, a
@@ -49,6 +51,8 @@ constexpr int kDefaultPiece = 4;           // least tiles per pool piece
 // e4m3 caches, one query: every piece is a segment whose start (q converted
 // and rescaled to f16) costs issue slots in that issue-bound variant
 constexpr int kDefaultPieceFp8 = 8;
+// least K/V tiles a CTA of the prefix kernel takes
+constexpr int kPrefixMinTiles = 2;
 constexpr int kPiecesPerWorker = 4;        // pool pieces per worker warp, at most
 constexpr int kMaxCtasPerSm = 2;
 constexpr int kWarpsPerCta = 8;  // most worker warps of any decode variant
@@ -203,7 +207,7 @@ struct DeviceState {
   bool chunk_tc_ready = false;              // tensor-memory kernel configured
   Workspace user_ws;                        // caller-owned (pa_set_workspace)
   std::map<uintptr_t, Workspace> lib_ws;    // library-owned, one per stream
-  std::map<std::tuple<int, int, int, int, int, bool>, int> occupancy;
+  std::map<std::tuple<int, int, int, int, int, int>, int> occupancy;
 };
 
 std::mutex g_mu;
@@ -236,11 +240,14 @@ size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Section offsets of the decode workspace (layout described in pa_internal.h).
 struct WsLayout {
-  size_t pool, plan, part, total;
+  size_t pool, plan, shared, part, total;
+  size_t shared_slot0;  // first slot of a shared-prefix step's prefix partials
 };
 
 // Hv pairs per sequence with CG columns each (Hkv and G for single-query decode).
-WsLayout ws_layout(int64_t B, int Hv, int CG, int D, int64_t workers) {
+// NG groups and shared_slots prefix partials: shared-prefix steps (else 0).
+WsLayout ws_layout(int64_t B, int Hv, int CG, int D, int64_t workers, int64_t NG = 0,
+                   size_t shared_slots = 0) {
   const size_t S = static_cast<size_t>(B) * Hv;
   const size_t nslot = 2 * S + workers + static_cast<size_t>(workers) * kPiecesPerWorker;
   WsLayout L;
@@ -249,9 +256,20 @@ WsLayout ws_layout(int64_t B, int Hv, int CG, int D, int64_t workers) {
   // whatever their shapes, and each step's merge only resets its own copy.
   L.pool = o;  o += 256;
   L.plan = o;  o += round_up(static_cast<size_t>(pa::plan_words(static_cast<int>(B))) * 4, 256);
-  L.part = o;  o += nslot * static_cast<size_t>(pa::part_stride(CG, D)) * sizeof(float);
+  L.shared = o;
+  if (shared_slots) o += round_up(pa::shared_plan_words(B, NG) * 4, 256);
+  L.shared_slot0 = nslot;
+  L.part = o;  o += (nslot + shared_slots) * static_cast<size_t>(pa::part_stride(CG, D)) * sizeof(float);
   L.total = o;
   return L;
+}
+
+// Most prefix partials a shared-prefix step can have (see shared_plan.cuh): a
+// group's (KV head, unit) list has at most 2 Hkv n slots, and every CTA that
+// starts inside a group adds one unit's.
+size_t most_shared_slots(int64_t B, int64_t Hkv, int G, int D, int grid) {
+  const int64_t unit = std::min<int64_t>(2 * B, pa::prefix_shape(D).unit_rows / G);
+  return static_cast<size_t>(2 * Hkv * B + grid * std::max<int64_t>(unit, 1));
 }
 
 int tuned_pool_permille() {
@@ -299,7 +317,11 @@ pa_status make_cache_map(CUtensorMap* map, const void* base, int64_t rows, int D
 
 // ------------------------------------------------------------ dispatch glue
 
-// The kernel family of a (cache type, q type, chunked) combination.
+// What a decode family is built for: single queries, chunked queries, the
+// tails of a shared-prefix step.
+enum DecodeKind { kSingle = 0, kChunked = 1, kTails = 2 };
+
+// The kernel family of a (cache type, q type, kind) combination.
 struct Family {
   cudaError_t (*variant)(int D, int nt, pa::DecodeVariant* v);
   cudaError_t (*prepare)(int D, int nt, int smem, int* ctas_per_sm);
@@ -310,14 +332,14 @@ struct Family {
 #define PA_FAMILY(NAME) \
   Family { pa::decode_variant_##NAME, pa::decode_prepare_##NAME, pa::decode_launch_##NAME }
 
-Family family_of(int ct, int qt, bool mq) {
-  if (ct == pa::kE4M3) {
-    if (qt == pa::kBF16) return mq ? PA_FAMILY(mq_fp8_bf16) : PA_FAMILY(fp8_bf16);
-    return mq ? PA_FAMILY(mq_fp8_f16) : PA_FAMILY(fp8_f16);
-  }
-  if (ct == pa::kBF16) return mq ? PA_FAMILY(mq_bf16) : PA_FAMILY(bf16);
-  return mq ? PA_FAMILY(mq_f16) : PA_FAMILY(f16);
+#define PA_FAMILY_OF(NAME) \
+  (kind == kTails ? PA_FAMILY(sh_##NAME) : (kind == kChunked ? PA_FAMILY(mq_##NAME) : PA_FAMILY(NAME)))
+
+Family family_of(int ct, int qt, int kind) {
+  if (ct == pa::kE4M3) return qt == pa::kBF16 ? PA_FAMILY_OF(fp8_bf16) : PA_FAMILY_OF(fp8_f16);
+  return ct == pa::kBF16 ? PA_FAMILY_OF(bf16) : PA_FAMILY_OF(f16);
 }
+#undef PA_FAMILY_OF
 #undef PA_FAMILY
 
 struct DecodePlan {
@@ -343,16 +365,16 @@ void chunk_columns(int64_t T, int G, int* CG, int* NCG) {
   *CG = *NCG == 1 ? static_cast<int>(cols) : 16;
 }
 
-pa_status plan_decode(DeviceState* st, int ct, int qt, bool mq, int64_t B, int CG, int D,
+pa_status plan_decode(DeviceState* st, int ct, int qt, int kind, int64_t B, int CG, int D,
                       DecodePlan* p) {
-  p->fam = family_of(ct, qt, mq);
+  p->fam = family_of(ct, qt, kind);
   p->nt = CG > 8 ? 2 : 1;
   cudaError_t e = p->fam.variant(D, p->nt, &p->var);
   if (e != cudaSuccess) return fail(PA_ERR_UNSUPPORTED, "no decode kernel for this dtype/head_dim");
   const size_t smem = 1024 + p->var.ring_bytes + p->var.warps * p->var.stages * (8 + 8) +
-                      static_cast<size_t>(2 * B + 1) * sizeof(int32_t);
+                      static_cast<size_t>((kind == kTails ? 3 : 2) * B + 1) * sizeof(int32_t);
   p->smem = static_cast<int>(round_up(smem, 1024));
-  auto key = std::make_tuple(ct, qt, D, p->nt, p->smem, mq);
+  auto key = std::make_tuple(ct, qt, D, p->nt, p->smem, kind);
   auto it = st->occupancy.find(key);
   int ctas = 0;
   if (it == st->occupancy.end()) {
@@ -375,7 +397,7 @@ pa_status plan_decode(DeviceState* st, int ct, int qt, bool mq, int64_t B, int C
   const int mt = g_tune_min_tiles.load();
   p->min_tiles = mt > 0 ? mt : kDefaultMinTiles;
   p->pool_permille = tuned_pool_permille();
-  p->piece = tuned_piece(ct == pa::kE4M3 && !mq);
+  p->piece = tuned_piece(ct == pa::kE4M3 && kind != kChunked);
   return PA_OK;
 }
 
@@ -500,7 +522,8 @@ pa_status pa_set_workspace(void* ptr, size_t bytes) {
 namespace {
 
 pa_status workspace_size(int64_t batch, int64_t num_queries, int32_t num_q_heads,
-                         int32_t num_kv_heads, int32_t head_dim, size_t* bytes) {
+                         int32_t num_kv_heads, int32_t head_dim, size_t* bytes,
+                         int64_t num_groups = 0) {
   if (!bytes) return fail(PA_ERR_INVALID_ARG, "bytes is null");
   if (num_queries < 1 || num_queries > kMaxChunk)
     return fail(PA_ERR_UNSUPPORTED, "num_queries %lld", (long long)num_queries);
@@ -519,7 +542,12 @@ pa_status workspace_size(int64_t batch, int64_t num_queries, int32_t num_q_heads
   int64_t workers = static_cast<int64_t>(st->num_sms) * kMaxCtasPerSm * kWarpsPerCta;
   const int cap = g_tune_max_ctas.load();
   if (cap > 0 && cap * kWarpsPerCta < workers) workers = static_cast<int64_t>(cap) * kWarpsPerCta;
-  *bytes = ws_layout(batch, static_cast<int>(Hv), CG, head_dim, workers).total;
+  *bytes = ws_layout(batch, static_cast<int>(Hv), CG, head_dim, workers, num_groups,
+                     num_groups > 0 ? most_shared_slots(batch, num_kv_heads,
+                                                        num_q_heads / num_kv_heads, head_dim,
+                                                        st->num_sms)
+                                    : 0)
+               .total;
   return ok();
 }
 
@@ -531,6 +559,15 @@ pa_status pa_decode_workspace_size(int64_t batch, int32_t num_q_heads, int32_t n
                                    int32_t head_dim, size_t* bytes) {
   return pa::abi_guard([&]() -> pa_status {
     return workspace_size(batch, 1, num_q_heads, num_kv_heads, head_dim, bytes);
+  });
+}
+
+pa_status pa_decode_shared_workspace_size(int64_t batch, int64_t num_groups, int32_t num_q_heads,
+                                          int32_t num_kv_heads, int32_t head_dim, size_t* bytes) {
+  return pa::abi_guard([&]() -> pa_status {
+    if (num_groups < 0 || num_groups > kMaxBatch)
+      return fail(PA_ERR_UNSUPPORTED, "num_groups %lld", (long long)num_groups);
+    return workspace_size(batch, 1, num_q_heads, num_kv_heads, head_dim, bytes, num_groups);
   });
 }
 
@@ -771,8 +808,17 @@ pa_status check_decode(const pa_tensor* out, const pa_tensor* q, const pa_tensor
   return PA_OK;
 }
 
-pa_status plan_call(DeviceState* st, const DecodeCall& c, DecodePlan* plan, WsLayout* layout) {
-  pa_status s = plan_decode(st, c.ct, c.qt, c.T > 1, c.B, c.CG, static_cast<int>(c.D), plan);
+// The shared-prefix part of a decode call: rows [group_starts[g],
+// group_starts[g + 1]) share their first prefix_lens[g] tokens.
+struct SharedCall {
+  const pa_tensor *group_starts, *prefix_lens;
+  int64_t NG;
+};
+
+pa_status plan_call(DeviceState* st, const DecodeCall& c, DecodePlan* plan, WsLayout* layout,
+                    const SharedCall* sh = nullptr) {
+  pa_status s = plan_decode(st, c.ct, c.qt, sh ? kTails : (c.T > 1 ? kChunked : kSingle), c.B, c.CG,
+                            static_cast<int>(c.D), plan);
   if (s) return s;
   // No more worker warps than the step can fill at min_tiles each: its
   // tiles are at most B * Hv pairs times the 16-token tiles of the longest
@@ -788,7 +834,8 @@ pa_status plan_call(DeviceState* st, const DecodeCall& c, DecodePlan* plan, WsLa
     plan->grid = static_cast<int>(std::max<int64_t>(ctas, 1));
     plan->workers = plan->grid * plan->var.warps;
   }
-  *layout = ws_layout(c.B, c.Hv, c.CG, static_cast<int>(c.D), plan->workers);
+  *layout = ws_layout(c.B, c.Hv, c.CG, static_cast<int>(c.D), plan->workers, sh ? sh->NG : 0,
+                      sh ? most_shared_slots(c.B, c.Hkv, c.G, static_cast<int>(c.D), st->num_sms) : 0);
   return PA_OK;
 }
 
@@ -797,7 +844,8 @@ pa_status plan_call(DeviceState* st, const DecodeCall& c, DecodePlan* plan, WsLa
 // fails after the decode kernel ran, so that its pool counter is cleared
 // before the next use.
 pa_status run_decode(const DecodeCall& c, DeviceState* st, const DecodePlan& plan,
-                     const WsLayout& layout, void* ws, Workspace* wsp, cudaStream_t cs) {
+                     const WsLayout& layout, void* ws, Workspace* wsp, cudaStream_t cs,
+                     const SharedCall* sh = nullptr) {
   pa_status s;
   const int elt = c.fp8 ? 1 : 2;
   const int D = static_cast<int>(c.D);
@@ -843,6 +891,52 @@ pa_status run_decode(const DecodeCall& c, DeviceState* st, const DecodePlan& pla
 
   const bool prof = g_prof_before && g_prof_after;
   cudaError_t e;
+  a.shared_rows = nullptr;
+  if (sh) {
+    // the plan, then the shared positions; the decode kernel below covers the
+    // tails, and the merge joins both
+    const int grid = st->num_sms;
+    const pa::PrefixShape shape = pa::prefix_shape(D);
+    pa::SharedPlanArgs p;
+    p.group_starts = static_cast<const int32_t*>(sh->group_starts->data);
+    p.prefix_lens = static_cast<const int32_t*>(sh->prefix_lens->data);
+    p.seq_lens = a.seq_lens;
+    p.plan = reinterpret_cast<int32_t*>(wsb + layout.shared);
+    p.err = st->err_word;
+    p.B = a.B;
+    p.NG = static_cast<int>(sh->NG);
+    p.MB = a.MB;
+    p.bs = a.bs;
+    p.Hkv = a.Hkv;
+    p.G = a.G;
+    p.window = a.window;
+    p.kv = shape.kv;
+    p.unit_rows = shape.unit_rows;
+    p.halves = shape.halves;
+    p.grid = grid;
+    p.min_tiles = kPrefixMinTiles;
+    e = pa::shared_plan_launch(p, cs, !prof);
+    if (e != cudaSuccess) return cuda_fail(e, "shared plan launch");
+    pa::PrefixArgs x;
+    x.q = a.q;
+    x.block_tables = a.block_tables;
+    x.plan = p.plan;
+    x.part = a.part + layout.shared_slot0 * pa::part_stride(a.CG, D);
+    x.err = a.err;
+    x.NG = p.NG;
+    x.Hq = a.Hq;
+    x.Hkv = a.Hkv;
+    x.G = a.G;
+    x.bs = a.bs;
+    x.MB = a.MB;
+    x.NB = a.NB;
+    x.score_scale = a.score_scale;
+    x.v_scale = a.v_scale;
+    e = pa::prefix_launch(c.qt, c.fp8, D, tk, tv, x, grid, cs, !prof);
+    if (e != cudaSuccess) return cuda_fail(e, "prefix kernel launch");
+    g_launches += 2;
+    a.shared_rows = reinterpret_cast<const pa::SharedRow*>(p.plan + pa::kSharedHead + 12 * p.NG);
+  }
   if (prof && (e = cudaEventRecord(static_cast<cudaEvent_t>(g_prof_before), cs)) != cudaSuccess)
     return cuda_fail(e, "profile event");
   e = plan.fam.launch(D, plan.nt, tk, tv, a, plan.grid, plan.smem, cs, !prof);
@@ -864,6 +958,9 @@ pa_status run_decode(const DecodeCall& c, DeviceState* st, const DecodePlan& pla
   m.NCG = a.NCG;
   m.CG = a.CG;
   m.Hv = a.Hv;
+  m.shared_rows = a.shared_rows;
+  m.shared_head = sh ? reinterpret_cast<const int32_t*>(wsb + layout.shared) : nullptr;
+  m.shared_part0 = static_cast<int>(layout.shared_slot0);
   // three CTAs per SM, and no more than output columns (a wide column takes
   // one CTA, a narrow one a warp)
   const int64_t cols = static_cast<int64_t>(m.B) * m.Hv * m.CG;
@@ -944,7 +1041,8 @@ pa_status decode_entry(const pa_tensor* out, const pa_tensor* q, const pa_tensor
                        const pa_tensor* value_cache, const pa_tensor* block_tables,
                        const pa_tensor* seq_lens, int32_t num_kv_heads, float scale,
                        int32_t block_size, int32_t window, int32_t kv_dtype, float k_scale,
-                       float v_scale, pa_stream stream, bool chunked) {
+                       float v_scale, pa_stream stream, bool chunked,
+                       const SharedCall* sh = nullptr) {
   DecodeCall c;
   pa_status s = check_decode(out, q, key_cache, value_cache, block_tables, seq_lens,
                              num_kv_heads, scale, block_size, window, kv_dtype, k_scale, v_scale,
@@ -960,11 +1058,11 @@ pa_status decode_entry(const pa_tensor* out, const pa_tensor* q, const pa_tensor
   Workspace* wsp = nullptr;
   {
     std::lock_guard<std::mutex> lk(g_mu);
-    if ((s = device_state(&st, nullptr)) || (s = plan_call(st, c, &plan, &layout)) ||
+    if ((s = device_state(&st, nullptr)) || (s = plan_call(st, c, &plan, &layout, sh)) ||
         (s = get_workspace(st, cs, layout, &ws, &wsp)))
       return s;
   }
-  return run_decode(c, st, plan, layout, ws, wsp, cs);
+  return run_decode(c, st, plan, layout, ws, wsp, cs, sh);
 }
 
 }  // namespace
@@ -979,6 +1077,40 @@ pa_status pa_decode(const pa_tensor* out, const pa_tensor* q, const pa_tensor* k
   return pa::abi_guard([&]() -> pa_status {
     return decode_entry(out, q, key_cache, value_cache, block_tables, seq_lens, num_kv_heads, scale,
                         block_size, window, kv_dtype, k_scale, v_scale, stream, false);
+  });
+}
+
+pa_status pa_decode_shared(const pa_tensor* out, const pa_tensor* q, const pa_tensor* key_cache,
+                           const pa_tensor* value_cache, const pa_tensor* block_tables,
+                           const pa_tensor* seq_lens, const pa_tensor* prefix_lens,
+                           const pa_tensor* group_starts, int32_t num_kv_heads, float scale,
+                           int32_t block_size, int32_t window, int32_t kv_dtype, float k_scale,
+                           float v_scale, pa_stream stream) {
+  return pa::abi_guard([&]() -> pa_status {
+    pa_status s;
+    if ((s = check_tensor(prefix_lens, "prefix_lens", 1)) ||
+        (s = check_tensor(group_starts, "group_starts", 1)) || (s = check_tensor(out, "out", 3)))
+      return s;
+    if (prefix_lens->dtype != PA_I32 || group_starts->dtype != PA_I32)
+      return fail(PA_ERR_INVALID_ARG, "prefix_lens and group_starts must be int32");
+    const int64_t NG = prefix_lens->shape[0];
+    if (group_starts->shape[0] != NG + 1)
+      return fail(PA_ERR_INVALID_ARG, "group_starts must have one element more than prefix_lens");
+    if (NG > kMaxBatch)
+      return fail(PA_ERR_UNSUPPORTED, "%lld groups > %lld", (long long)NG, (long long)kMaxBatch);
+    for (const pa_tensor* x : {prefix_lens, group_starts}) {
+      if (!is_contiguous(x)) return fail(PA_ERR_LAYOUT, "prefix_lens and group_starts must be contiguous");
+      if (reinterpret_cast<uintptr_t>(x->data) % 4)
+        return fail(PA_ERR_LAYOUT, "prefix_lens and group_starts must be aligned to their elements");
+      if (overlaps(out, x)) return fail(PA_ERR_INVALID_ARG, "out overlaps an input");
+    }
+    if (numel(out) > 0 && ((s = check_accessible(prefix_lens, "prefix_lens")) ||
+                           (s = check_accessible(group_starts, "group_starts"))))
+      return s;
+    const SharedCall sh = {group_starts, prefix_lens, NG};
+    return decode_entry(out, q, key_cache, value_cache, block_tables, seq_lens, num_kv_heads, scale,
+                        block_size, window, kv_dtype, k_scale, v_scale, stream, false,
+                        NG > 0 ? &sh : nullptr);
   });
 }
 

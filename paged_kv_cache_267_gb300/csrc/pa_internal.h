@@ -42,6 +42,8 @@ constexpr int kPlanScalars = 8;
 __host__ __device__ constexpr inline int plan_words(int B) { return kPlanScalars + B + 1; }
 constexpr int kMergeNarrow = 8;  // partials one merge warp folds in one round trip
 
+struct SharedRow;  // a sequence's part of a shared prefix (shared_plan.cuh)
+
 struct DecodeArgs {
   const void* q;                 // [B, T, Hq, D] ([B, Hq, D] when T = 1)
   const int32_t* block_tables;   // [B, MB]
@@ -62,6 +64,7 @@ struct DecodeArgs {
   int pool_permille;             // share of tiles handed out dynamically
   int piece_min;                 // least tiles per pool piece
   int np_max;                    // most pool pieces (bounds the slots)
+  const SharedRow* shared_rows;  // [B], shared-prefix steps only
 };
 
 struct MergeArgs {
@@ -71,6 +74,11 @@ struct MergeArgs {
   uint32_t* pool;                // reset to zero for the next step
   int B, Hq, Hkv, G, D, NW;
   int T, NCG, CG, Hv;            // as in DecodeArgs
+  // shared-prefix steps only (else null): each sequence's part of the prefix,
+  // the plan's header and the first slot of the prefix partials
+  const SharedRow* shared_rows;
+  const int32_t* shared_head;
+  int shared_part0;
 };
 
 // Bound on output columns (batch * q heads * queries) of one call.
@@ -132,64 +140,11 @@ PA_DECLARE_DECODE_FAMILY(mq_f16)
 PA_DECLARE_DECODE_FAMILY(mq_bf16)
 PA_DECLARE_DECODE_FAMILY(mq_fp8_f16)
 PA_DECLARE_DECODE_FAMILY(mq_fp8_bf16)
+PA_DECLARE_DECODE_FAMILY(sh_f16)
+PA_DECLARE_DECODE_FAMILY(sh_bf16)
+PA_DECLARE_DECODE_FAMILY(sh_fp8_f16)
+PA_DECLARE_DECODE_FAMILY(sh_fp8_bf16)
 #undef PA_DECLARE_DECODE_FAMILY
-
-// The block pool (pool_ops.cu). in_place: lens_out is lens, or state_out is
-// state; the last CTA to have read them then writes them.
-struct PoolExtendArgs {
-  int32_t* tables;               // [B, MB]
-  const int32_t* lens;           // [B] before the step
-  const int32_t* fresh;          // [B] new tokens
-  const int32_t* free_list;      // [NF]
-  int32_t* state;                // {free blocks, ticket}
-  int32_t* lens_out;             // [B]
-  int32_t* state_out;            // {free blocks, 0}
-  int32_t* query_start;          // [B + 1]
-  int64_t* slots;                // [T]
-  int32_t* positions;            // [T]
-  int32_t* err;                  // device error word
-  int B, MB, bs, NF, T;
-  bool in_place;
-  bool wide;                     // slots and positions are 16-byte aligned
-};
-struct PoolReleaseArgs {
-  const int32_t* tables;         // [B, MB]
-  const int32_t* lens;           // [B]
-  const int32_t* released;       // [B], nonzero: give the blocks back
-  const int32_t* shared;         // [B] tokens in blocks that stay, or null
-  int32_t* free_list;            // [NF]
-  int32_t* state;
-  int32_t* lens_out;
-  int32_t* state_out;
-  int32_t* err;
-  int B, MB, bs, NF;
-  bool in_place;
-};
-cudaError_t pool_extend_launch(const PoolExtendArgs& a, int num_sms, cudaStream_t s);
-cudaError_t pool_release_launch(const PoolReleaseArgs& a, int num_sms, cudaStream_t s);
-
-// Norm, rotation and cache write of a batch's projected rows (norm_cache.cu).
-struct NormCacheArgs {
-  const void* q;                 // [T, Hq, D], rows of q_stride elements
-  const void* k;                 // [T, Hkv, D]
-  const void* v;
-  void* q_out;                   // [T, Hq, D]
-  void* kc;                      // [NB, Hkv, bs, D]
-  void* vc;
-  const int64_t* slots;          // [T]
-  const int32_t* positions;      // [T]
-  const float* cos_sin;          // [NP, R]: R / 2 cosines, then R / 2 sines
-  const void* q_weight;          // [D] or null (no norm)
-  const void* k_weight;
-  int32_t* err;
-  int64_t q_stride, k_stride, v_stride, out_stride;  // elements a row
-  int64_t NB;
-  int T, Hq, Hkv, D, R, NP, bs;
-  float eps, k_scale, v_scale;
-  bool interleaved;
-};
-cudaError_t norm_cache_launch(int type, bool fp8, const NormCacheArgs& a, int num_sms,
-                              cudaStream_t s);
 
 // merge_reshape.cu
 cudaError_t merge_launch(int out_type, const MergeArgs& a, int grid, cudaStream_t s, bool pdl);

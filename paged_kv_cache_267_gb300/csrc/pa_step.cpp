@@ -11,6 +11,7 @@
 #include "pa.h"
 #include "pa_host.h"
 #include "pa_internal.h"
+#include "step_ops.h"
 
 namespace {
 

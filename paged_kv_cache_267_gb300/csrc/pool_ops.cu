@@ -21,6 +21,7 @@
 // state) writes them.
 #include "pa_internal.h"
 #include "ptx.cuh"
+#include "step_ops.h"
 
 namespace pa {
 namespace {

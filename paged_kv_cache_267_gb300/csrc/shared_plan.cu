@@ -1,0 +1,216 @@
+// Plan of a shared-prefix decode step (layout and meaning in shared_plan.cuh):
+// one CTA turns group starts, prefix lengths and sequence lengths into the
+// units, segments and partial slots of the step. A few thousand integers,
+// bound by its chain of block-wide scans (a few microseconds); it reads none
+// of what the write path writes, so it runs while that drains.
+#include "pa_internal.h"
+#include "ptx.cuh"
+#include "shared_plan.cuh"
+#include "step_ops.h"
+
+namespace pa {
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr unsigned kFull = 0xffffffffu;
+
+// Inclusive scan of x over the block with op (identity `zero`); *total
+// receives the whole block's value.
+template <typename Op>
+__device__ __forceinline__ int block_scan(int x, int zero, Op op, int* total) {
+  __shared__ int s_w[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kFull, x, o);
+    if (lane >= o) x = op(x, y);
+  }
+  if (lane == 31) s_w[warp] = x;
+  __syncthreads();
+  int v = s_w[lane];  // kWarps == 32
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kFull, v, o);
+    if (lane >= o) v = op(v, y);
+  }
+  *total = __shfl_sync(kFull, v, 31);
+  const int before = __shfl_sync(kFull, v, warp > 0 ? warp - 1 : 0);
+  __syncthreads();  // s_w is reused
+  return op(x, warp > 0 ? before : zero);
+}
+
+__global__ void __launch_bounds__(kThreads) shared_plan_kernel(const SharedPlanArgs a) {
+  extern __shared__ int s_dyn[];
+  int* s_r0 = s_dyn;             // [NG + 1] group starts, made non-decreasing in [0, B]
+  int* s_pre = s_r0 + a.NG + 1;  // [NG] prefix lengths, whole blocks
+  int* s_in = s_pre + a.NG;      // [NG] rows that take part, then first flat tile
+  int* s_first = s_in + a.NG;    // [NG] the first of them
+  int* s_base = s_first + a.NG;  // [NG] first slot
+  const int tid = threadIdx.x;
+  const int cap = a.MB * a.bs;
+  const auto add = [](int x, int y) { return x + y; };
+  const auto most = [](int x, int y) { return x > y ? x : y; };
+  griddep_launch_dependents();  // the prefix kernel sets itself up, then waits
+  // The inputs are not the write path's: planning overlaps it. The workspace
+  // it fills was last read by a kernel that an early-launching predecessor
+  // has already waited for.
+  int run = 0, total;
+  for (int g0 = 0; g0 <= a.NG; g0 += kThreads) {
+    const int g = g0 + tid;
+    int x = 0;
+    bool bad = false;
+    if (g <= a.NG) {
+      const int s = a.group_starts[g];
+      x = min(max(s, 0), a.B);
+      bad = s != x;
+      if (g < a.NG) {
+        const int p = a.prefix_lens[g];
+        const int q = min(max(p, 0), cap);
+        bad = bad || p != q;
+        s_pre[g] = q / a.bs * a.bs;
+        s_in[g] = 0;
+        s_first[g] = a.B;
+      }
+    }
+    const int y = most(block_scan(x, 0, most, &total), run);
+    if (g <= a.NG) {
+      s_r0[g] = y;
+      bad = bad || y != x;
+    }
+    if (bad) atomicOr(a.err, PA_DEVERR_GROUP);
+    run = most(run, total);
+  }
+  __syncthreads();
+  auto group_of = [&](int b) -> int {  // the group of row b, -1 for none
+    if (b < s_r0[0] || b >= s_r0[a.NG]) return -1;
+    int lo = 0, hi = a.NG;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_r0[mid] <= b) lo = mid; else hi = mid;
+    }
+    return lo;
+  };
+  auto takes_part = [&](int b, int g) -> bool {
+    const int L = min(max(a.seq_lens[b], 0), cap);
+    return g >= 0 && s_pre[g] > 0 && L >= s_pre[g] && (a.window == 0 || L <= a.window);
+  };
+  for (int b = tid; b < a.B; b += kThreads) {
+    const int g = group_of(b);
+    if (takes_part(b, g)) {
+      atomicAdd(&s_in[g], 1);
+      atomicMin(&s_first[g], b);
+    }
+  }
+  __syncthreads();
+
+  // units and flat tiles
+  const int up_max = a.unit_rows / a.G;
+  SharedGroup* groups = reinterpret_cast<SharedGroup*>(a.plan + kSharedHead);
+  auto units = [&](int g, int* nt, int* nut, int* up) {
+    const int n = s_r0[g + 1] - s_r0[g];
+    *nt = (s_pre[g] + a.kv - 1) / a.kv;
+    *nut = n > 0 ? (n + up_max - 1) / up_max : 0;
+    *up = n > 0 ? (n + *nut - 1) / *nut : 0;
+  };
+  run = 0;
+  for (int g0 = 0; g0 < a.NG; g0 += kThreads) {
+    const int g = g0 + tid;
+    int x = 0, nt, nut, up;
+    if (g < a.NG) {
+      if (s_in[g] < 2) s_pre[g] = 0;  // one sequence reads its prefix once anyway
+      units(g, &nt, &nut, &up);
+      x = a.Hkv * nut * nt;
+    }
+    const int y = block_scan(x, 0, add, &total);
+    if (g < a.NG) s_in[g] = run + y - x;
+    run += total;
+  }
+  const int tiles = run;
+  const int wsz = max((tiles + a.grid - 1) / a.grid, a.min_tiles);
+  // slots
+  run = 0;
+  for (int g0 = 0; g0 < a.NG; g0 += kThreads) {
+    const int g = g0 + tid;
+    int x = 0, nt = 0, nut = 0, up = 0, sub = 1;
+    if (g < a.NG) {
+      units(g, &nt, &nut, &up);
+      if (nt > 0) {
+        const int f0 = s_in[g], f1 = f0 + a.Hkv * nut * nt;
+        sub = a.halves && up * a.G <= a.unit_rows / 2 ? 2 : 1;
+        x = (a.Hkv * nut + (f1 - 1) / wsz - f0 / wsz) * up * sub;
+      }
+    }
+    const int y = block_scan(x, 0, add, &total);
+    if (g < a.NG) {
+      s_base[g] = run + y - x;
+      SharedGroup r;
+      r.r0 = s_r0[g];
+      r.n = s_r0[g + 1] - s_r0[g];
+      r.table_row = s_first[g];
+      r.prefix = s_pre[g];
+      r.f0 = s_in[g];
+      r.nt = nt;
+      r.nut = nut;
+      r.up = up;
+      r.base = run + y - x;
+      r.sub = sub;
+      r.wfirst = s_in[g] / wsz;
+      r.pad = 0;
+      groups[g] = r;
+    }
+    run += total;
+  }
+  if (tid == 0) {
+    a.plan[kShTotal] = tiles;
+    a.plan[kShWsz] = wsz;
+  }
+  __syncthreads();
+  SharedRow* rows = reinterpret_cast<SharedRow*>(a.plan + kSharedHead + 12 * a.NG);
+  for (int b = tid; b < a.B; b += kThreads) {
+    const int g = group_of(b);
+    const int L = min(max(a.seq_lens[b], 0), cap);
+    SharedRow r = {a.window > 0 && L > a.window ? L - a.window : 0, 0, 0, 0, 0, 0, 0, 0};
+    if (takes_part(b, g)) {
+      int nt, nut, up;
+      units(g, &nt, &nut, &up);
+      const int i = b - s_r0[g], ut = i / up;
+      const int sub = a.halves && up * a.G <= a.unit_rows / 2 ? 2 : 1;
+      r.start = s_pre[g];
+      r.nt = nt;
+      r.f0 = s_in[g] + ut * nt;
+      r.kv_step = nut * nt;
+      r.slot0 = s_base[g] + i - ut * up;
+      r.lid0 = ut - s_in[g] / wsz;
+      r.up_sub = up * sub;
+      r.nut_sub = nut << 2 | sub;
+    }
+    rows[b] = r;
+  }
+  griddep_wait();  // what follows this kernel follows its predecessors too
+}
+
+}  // namespace
+
+cudaError_t shared_plan_launch(const SharedPlanArgs& a, cudaStream_t s, bool pdl) {
+  const size_t smem = (5 * static_cast<size_t>(a.NG) + 1) * sizeof(int);
+  if (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(reinterpret_cast<const void*>(shared_plan_kernel),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, shared_plan_kernel, a);
+}
+
+}  // namespace pa

@@ -1,0 +1,66 @@
+// Layout of the plan of a shared-prefix decode step, written by the plan
+// kernel (shared_plan.cu) and read by the prefix, decode and merge kernels.
+//
+// Sequences of group g, rows [r0, r0 + n), share their first P tokens (P a
+// multiple of the block size, so of 16). A row takes part when it attends to all
+// of them: L >= P and no window cuts them. The prefix kernel computes the
+// partial softmax of all taking part over [0, P); the decode kernel covers
+// [P, L) of those, and the whole range of every other row.
+//
+// The (query, head) rows of one KV head of a group, n * G of them, are cut into
+// nut units of up pairs (sequences) each, at most 256 rows; a unit of at most
+// 128 rows is computed by both softmax groups of its CTA, each on every other
+// K/V tile (sub = 2 partials), a larger one by one group per 128 rows (sub = 1).
+// All K/V tiles of all units form one flat index space, group- then KV head-
+// then unit-major; CTA w of the prefix kernel takes tiles [w * wsz, (w + 1) *
+// wsz). A run of one CTA's tiles inside one unit is a segment; its partials go
+// to slots
+//   base_g + ((lid * sub + x) * up + i),  lid = unit + (w - wfirst),
+// for the unit's index among the group's (KV head, unit) list, the first CTA
+// that meets the group, parity x of the tile and pair i: unique because the
+// walk through the (unit, CTA) grid is a monotone staircase. Slots have the
+// decode partials' layout (one KV head's G columns of one sequence).
+#pragma once
+
+#include "pa_internal.h"
+
+namespace pa {
+
+constexpr int kSharedHead = 8;      // header words
+enum { kShTotal = 0, kShWsz = 1 };  // all tiles; tiles a CTA
+
+struct SharedGroup {  // 12 words a group
+  int r0, n;          // rows
+  int table_row;      // the row whose block table the prefix is read through
+  int prefix;         // P, 0 when the group does not share
+  int f0;             // first flat tile
+  int nt;             // K/V tiles of the prefix
+  int nut, up;        // units a KV head, pairs a unit
+  int base;           // first partial slot (counted from the prefix region)
+  int sub;            // partials a segment and pair: 1 or 2
+  int wfirst;         // first CTA that meets the group
+  int pad;
+};
+
+struct SharedRow {  // 8 words a sequence
+  int start;        // first position the decode kernel covers
+  int nt;           // K/V tiles of its prefix, 0: no part of it here
+  int f0;           // first flat tile of its unit at KV head 0
+  int kv_step;      // flat tiles between KV heads
+  int slot0;        // slot of lid 0, x 0 for this sequence's pair
+  int lid0;         // unit - wfirst at KV head 0 (added to the CTA)
+  int up_sub;       // up * sub
+  int nut_sub;      // nut << 2 | sub
+};
+
+__host__ __device__ constexpr inline size_t shared_plan_words(int64_t B, int64_t NG) {
+  return kSharedHead + 12 * static_cast<size_t>(NG) + 8 * static_cast<size_t>(B);
+}
+__device__ __forceinline__ const SharedGroup* shared_groups(const int32_t* plan) {
+  return reinterpret_cast<const SharedGroup*>(plan + kSharedHead);
+}
+__device__ __forceinline__ const SharedRow* shared_rows(const int32_t* plan, int NG) {
+  return reinterpret_cast<const SharedRow*>(plan + kSharedHead + 12 * NG);
+}
+
+}  // namespace pa

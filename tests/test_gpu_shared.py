@@ -1,0 +1,423 @@
+"""pa_decode_shared against the fp64 oracle's plain decode of the same batch.
+
+The pool holds NaN wherever no sequence has a token, so reading a table entry,
+a tail slot or a window's outside that nobody attends to shows in the result.
+
+Tolerance. With weights w_j (summing to 1) and A = sum_j w_j |v_j|, element by
+element (the oracle's decode over |V|):
+  - the output is rounded once: h |out|, h = 2^-8 (bf16) or 2^-11 (f16);
+  - the weights enter the second product in 16 bits, bf16 for bf16 caches and
+    f16 for the others: p A with p = 2^-8 or 2^-11, and, where f16 weights are
+    subnormal, 2^-25 each against a sum of at least 2^-8 (the lazy reference):
+    n 2^-17 mean |v|, which is below n 2^-17 max |v| over n tokens; weights that
+    small stay below 2^-6 A of the total for the sizes here, so 2^-11 A more;
+  - scores: fp32 sums of D products, off by D 2^-24 sum |q k| scale log2(e); with
+    sum |q k| scale below 64 here that is a relative error of each weight of at
+    most 256 * 2^-24 * 64 * 1.45 < 2^-9; the exponential adds 2^-21.
+Bound: h |ref| + (p + 2^-11 + 2^-9) A + 1e-6.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from conftest import have_gpu
+from pa_testutil import host_copy, out_f64
+from workloads.layout import shuffled_free_list
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not have_gpu(), reason="needs a GPU")]
+
+DT = {"bf16": torch.bfloat16, "f16": torch.float16}
+
+
+class Batch:
+    """Groups of (prefix tokens, tails) and rows of no group, over a shuffled
+    pool whose unused slots hold NaN."""
+
+    def __init__(self, groups, loose_before=(), loose_after=(), *, heads=(8, 2), D=128, bs=16,
+                 dt="bf16", fp8=False, idle=(), seed=0, extra_blocks=3, qmul=1.0, kmul=1.0):
+        rng = np.random.default_rng(seed)
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        Hq, Hkv = heads
+        self.heads, self.D, self.bs, self.dt, self.fp8 = heads, D, bs, dt, fp8
+        lens, starts, pre, owner = list(loose_before), [], [], [None] * len(loose_before)
+        for gi, (P, tails) in enumerate(groups):
+            starts.append(len(lens))
+            pre.append(P)
+            lens += [P + t if t is not None else 0 for t in tails]
+            owner += [gi] * len(tails)
+        starts.append(len(lens))
+        lens += list(loose_after)
+        owner += [None] * len(loose_after)
+        for b in idle:
+            lens[b] = 0
+        B = len(lens)
+        self.MB = max(1, max(-(-n // bs) for n in lens), *[-(-p // bs) for p in pre]) + 1
+        shared = [p // bs for p in pre]
+        need = sum(shared) + sum(-(-n // bs) for n in lens) + extra_blocks
+        ids = shuffled_free_list(need, seed + 1)
+        tables = np.full((B, self.MB), -1, np.int32)
+        blocks = [[ids.pop() for _ in range(n)] for n in shared]
+        used = np.zeros((need, bs), bool)
+        for b, n in enumerate(lens):
+            nb = -(-n // bs)
+            t = (blocks[owner[b]] if owner[b] is not None else [])[:nb]
+            t = t + [ids.pop() for _ in range(nb - len(t))]
+            tables[b, :nb] = t
+            for j, blk in enumerate(t):
+                used[blk, :min(bs, n - j * bs)] = True
+        self.lens = np.asarray(lens, np.int32)
+        self.tables, self.prefix, self.starts, self.B = tables, np.asarray(pre, np.int32), np.asarray(starts, np.int32), B
+        self.ks, self.vs = (0.031, 0.017) if fp8 else (1.0, 1.0)
+        u = torch.from_numpy(used).cuda()[:, None, :, None]
+        shape = (need, Hkv, bs, D)
+
+        def values(mul):
+            x = torch.randn(shape, generator=g, device="cuda") * mul
+            return torch.where(u, x, torch.nan)
+
+        k, v = values(kmul), values(1.0)
+        if fp8:
+            enc = lambda x, s: torch.where(u, (x / s).to(torch.float8_e4m3fn).view(torch.uint8), 0x7F)  # noqa: E731
+            self.kc, self.vc = enc(k, self.ks).to(torch.uint8), enc(v, self.vs).to(torch.uint8)
+            self.va = self.vc & 0x7F
+        else:
+            self.kc, self.vc = k.to(DT[dt]), v.to(DT[dt])
+            self.va = self.vc.abs()
+        self.q = (torch.randn(B, Hq, D, generator=g, device="cuda") * qmul).to(DT[dt])
+        self.scale = D ** -0.5
+
+    def args(self):
+        i = lambda x: torch.from_numpy(x).cuda()  # noqa: E731
+        return (self.q, self.kc, self.vc, i(self.tables), i(self.lens), i(self.prefix), i(self.starts))
+
+    def kw(self, window=0):
+        return dict(num_kv_heads=self.heads[1], scale=self.scale, block_size=self.bs, window=window,
+                    kv_dtype="fp8" if self.fp8 else "auto", k_scale=self.ks, v_scale=self.vs)
+
+    def reference(self, window=0):
+        kw = dict(num_kv_heads=self.heads[1], scale=self.scale, block_size=self.bs, window=window,
+                  q_dtype=self.dt, cache_dtype="fp8" if self.fp8 else self.dt, k_scale=self.ks, v_scale=self.vs)
+        q, kc = host_copy(self.q), host_copy(self.kc)
+        return [oracle.decode(q, kc, host_copy(v), self.tables, self.lens, **kw) for v in (self.vc, self.va)]
+
+    def check(self, out, window=0, what=""):
+        ref, A = self.reference(window)
+        got = out_f64(out)
+        assert np.isfinite(got).all(), f"{what}: non-finite outputs in rows {sorted(set(np.argwhere(~np.isfinite(got))[:, 0]))}"
+        h = 2.0 ** -8 if self.dt == "bf16" else 2.0 ** -11
+        p = 2.0 ** -8 if self.dt == "bf16" and not self.fp8 else 2.0 ** -11
+        bound = h * np.abs(ref) + (p + 2.0 ** -11 + 2.0 ** -9) * A + 1e-6
+        err = np.abs(got - ref)
+        over = (err - bound).max(axis=(1, 2))
+        assert over.max() <= 0, f"{what}: rows {np.argwhere(over > 0).ravel()[:8]} beyond the bound by {over.max():.3e}"
+        # a wrong or missing token would be far outside this
+        assert err.mean() <= 2e-3 * max(A.mean(), 1e-9), f"{what}: mean error {err.mean():.3e}"
+
+    def run(self, pa, window=0):
+        out = torch.full_like(self.q, float("nan"))
+        pa.decode_shared(*self.args(), out=out, **self.kw(window))
+        torch.cuda.synchronize()
+        return out
+
+
+CASES = {
+    # one small group, both halves on the same rows
+    "two_rows": dict(groups=[(128, [1, 5])]),
+    "one_tile": dict(groups=[(16, [1, 2, 40])]),
+    "odd_prefix": dict(groups=[(1040, [1, 17, 300, 2])]),
+    "no_tails": dict(groups=[(272, [0, 0, 0])]),
+    "partial_block": dict(groups=[(261, [3, 30, 9])]),     # 256 tokens are shared
+    "below_a_block": dict(groups=[(15, [3, 30])]),         # nothing is
+    "single_row_groups": dict(groups=[(256, [5]), (128, [7]), (64, [9])]),
+    "idle_rows": dict(groups=[(512, [4, 9, 1, 80, 2])], idle=(0, 3)),
+    "one_left": dict(groups=[(512, [4, 9, 1])], idle=(0, 2)),
+    "loose_rows": dict(groups=[(384, [1, 2, 3]), (640, [9, 8])], loose_before=(5, 700, 0), loose_after=(33, 1)),
+    "empty_groups": dict(groups=[(0, []), (300, [1, 2]), (128, []), (0, [9, 8]), (512, [3, 3, 3])]),
+    "many_groups": dict(groups=[(64 + 16 * i, [1 + i, 2]) for i in range(40)]),
+    "uneven": dict(groups=[(2048, [3] * 70), (48, [100, 2]), (1008, [1] * 9)], heads=(32, 8)),
+    # units of more than 128 rows, the last ones partly filled
+    "dual": dict(groups=[(640, [5] * 40)], heads=(8, 2)),
+    "dual_129": dict(groups=[(400, [1] * 129)], heads=(2, 2)),
+    "dual_units": dict(groups=[(656, [2] * 131)], heads=(8, 2)),
+    "group_of_3": dict(groups=[(528, [7] * 90)], heads=(6, 2)),
+    "group_of_7": dict(groups=[(528, [7] * 50)], heads=(7, 1)),
+    "group_of_16": dict(groups=[(304, [7] * 20)], heads=(32, 2)),
+    "group_of_12": dict(groups=[(304, [7] * 11)], heads=(24, 2)),
+    "f16": dict(groups=[(1200, [9, 200, 1, 44])], dt="f16", heads=(16, 4)),
+    "f16_dual": dict(groups=[(1200, [9] * 48)], dt="f16", heads=(16, 4)),
+    "d64": dict(groups=[(720, [9, 2, 130])], D=64, dt="f16"),
+    "d64_dual": dict(groups=[(720, [9] * 50)], D=64, heads=(8, 2)),
+    "d256": dict(groups=[(720, [9, 2, 130])], D=256),
+    "d256_units": dict(groups=[(336, [9] * 70)], D=256, dt="f16", heads=(4, 1)),
+    "fp8": dict(groups=[(848, [9, 2, 130])], fp8=True, heads=(8, 2)),
+    "fp8_dual": dict(groups=[(848, [3] * 45)], fp8=True, dt="f16", heads=(8, 2)),
+    "fp8_d256": dict(groups=[(336, [3] * 45)], fp8=True, D=256, heads=(4, 1)),
+    "fp8_d256_f16": dict(groups=[(1008, [3, 60])], fp8=True, dt="f16", D=256, heads=(8, 2)),
+    "blocks_of_32": dict(groups=[(992, [9, 2, 130])], bs=32),
+    "blocks_of_48": dict(groups=[(48 * 13, [9, 2, 130])], bs=48),
+    "blocks_of_1024": dict(groups=[(2048, [9, 1025])], bs=1024),
+    "long": dict(groups=[(20000, [50, 1, 700])], heads=(8, 1)),
+    "large_scores": dict(groups=[(1504, [9, 70, 300])], qmul=4.0, kmul=1.5),
+    "large_scores_dual": dict(groups=[(1504, [9] * 40)], qmul=4.0, kmul=1.5, dt="f16"),
+}
+
+
+@pytest.mark.parametrize("name", list(CASES))
+def test_against_the_oracle(name, pa_lib):
+    b = Batch(seed=len(name) * 7 + 1, **CASES[name])
+    out = b.run(pa_lib)
+    assert pa_lib.check_device_error() == 0
+    b.check(out, what=name)
+
+
+@pytest.mark.parametrize("window", [1, 100, 512, 530, 5000])
+def test_windows_that_cut_some_rows_off_the_prefix(window, pa_lib):
+    b = Batch([(512, [1, 18, 300, 2, 0]), (96, [4, 900])], loose_after=(700, 3), seed=5)
+    out = b.run(pa_lib, window)
+    assert pa_lib.check_device_error() == 0
+    b.check(out, window, f"window {window}")
+
+
+@pytest.mark.parametrize("dt,fp8", [("bf16", False), ("f16", True)])
+def test_negative_and_zero_scale(dt, fp8, pa_lib):
+    for scale in (-0.09, 0.0):
+        b = Batch([(400, [1, 18, 30]), (256, [4] * 40)], dt=dt, fp8=fp8, seed=6)
+        b.scale = scale
+        b.check(b.run(pa_lib), what=f"scale {scale}")
+    assert pa_lib.check_device_error() == 0
+
+
+@pytest.mark.parametrize("shape", ["climb", "jump", "fall"])
+def test_scores_that_grow_along_the_prefix(shape, pa_lib):
+    """The reference maximum moves in some tiles, by more and by less than 8."""
+    b = Batch([(1600, [40] * 3), (1600, [5] * 40)], dt="f16", seed=8)
+    n = 1600
+    t = torch.arange(n, device="cuda", dtype=torch.float32)
+    m = {"climb": 0.2 + t / 200, "jump": torch.where(t > 900, 6.0, 0.1), "fall": 8 - t / 250}[shape]
+    for gi, row in ((0, 0), (1, 3)):
+        blocks = torch.from_numpy(b.tables[row, :n // 16].astype(np.int64)).cuda()
+        # K along the mean query, so scores follow m
+        for h in range(2):
+            d = b.q[row:row + 3, 4 * h:4 * h + 4].float().mean((0, 1))
+            d = d / d.norm()
+            b.kc[blocks, h] = (m.view(-1, 16, 1) * d * 4).to(torch.float16)
+    b.check(b.run(pa_lib), what=shape)
+    assert pa_lib.check_device_error() == 0
+
+
+def test_agrees_with_decode_and_no_groups_is_decode(pa_lib):
+    b = Batch([(640, [9, 3, 100]), (128, [1, 1])], seed=11)
+    a = b.args()
+    out = b.run(pa_lib)
+    plain = pa_lib.decode(*a[:5], **b.kw())
+    assert (out.float() - plain.float()).abs().max() <= 2.0 ** -6
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pa_lib.set_decode_tuning(pool_permille=-1)  # bit-reproducible
+    try:
+        x = pa_lib.decode_shared(*a[:5], none, zero, **b.kw())
+        assert torch.equal(x, pa_lib.decode(*a[:5], **b.kw()))
+        y = [b.run(pa_lib) for _ in range(3)]
+        assert torch.equal(y[0], y[1]) and torch.equal(y[0], y[2])
+    finally:
+        pa_lib.set_decode_tuning()
+
+
+def test_empty_batch(pa_lib):
+    b = Batch([(640, [9, 3, 100])], seed=11)
+    a = list(b.args())
+    out = pa_lib.decode_shared(a[0][:0], a[1], a[2], a[3][:0], a[4][:0], a[5], a[6], **b.kw())
+    assert out.shape == (0, 8, 128)
+
+
+def test_data_errors_are_flagged_and_safe(pa_lib):
+    b = Batch([(512, [9, 3, 100]), (256, [4, 4])], seed=12)
+    a = list(b.args())
+    i = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    assert pa_lib.check_device_error() == 0
+    # group starts that leave the batch, or decrease: clamped; rows still right
+    for starts, pre in (([-4, 3, 5], [512, 256]), ([0, 3, 99], [512, 256]), ([3, 0, 5], [512, 256]),
+                        ([0, 3, 5], [512, -7])):
+        out = pa_lib.decode_shared(*a[:5], i(pre), i(starts), **b.kw())
+        assert pa_lib.check_device_error() == pa_lib.DEVERR_GROUP
+        if starts == [3, 0, 5]:
+            continue  # rows 3, 4 become one group with the first prefix
+        b.check(out, what=str(starts))
+    # beyond the tables: no row is that long
+    out = pa_lib.decode_shared(*a[:5], i([512, 2**31 - 1]), i([0, 3, 5]), **b.kw())
+    assert pa_lib.check_device_error() == pa_lib.DEVERR_GROUP
+    b.check(out, what="prefix")
+    # a bad block id in the prefix, a bad length
+    bad = a[3].clone()
+    bad[0, 7] = 10**6
+    pa_lib.decode_shared(*a[:3], bad, *a[4:], **b.kw())
+    assert pa_lib.check_device_error() & pa_lib.DEVERR_BLOCK_ID
+    lens = a[4].clone()
+    lens[1] = 10**7
+    pa_lib.decode_shared(*a[:4], lens, *a[5:], **b.kw())
+    assert pa_lib.check_device_error() & pa_lib.DEVERR_SEQ_LEN
+    b.check(b.run(pa_lib), what="after the errors")
+    assert pa_lib.check_device_error() == 0
+
+
+def test_own_workspace_of_the_stated_size(pa_lib):
+    b = Batch([(640, [9] * 40), (128, [1, 1])], seed=13)
+    n = pa_lib.decode_shared_workspace_size(b.B, 2, 8, 2, 128)
+    ws = torch.empty(n + 256, dtype=torch.uint8, device="cuda")
+    ws[n:] = 77
+    try:
+        pa_lib.set_workspace(ws[:n])
+        for _ in range(2):
+            b.check(b.run(pa_lib))
+        assert (ws[n:] == 77).all()
+        pa_lib.set_workspace(ws[:4096])
+        with pytest.raises(pa_lib.PAError):
+            b.run(pa_lib)
+    finally:
+        pa_lib.set_workspace(None)
+
+
+def test_other_streams_and_shapes_in_turn(pa_lib):
+    """Calls of several shapes on two streams at once, each with its own
+    library workspace, and plain decodes between them."""
+    bs = [Batch([(640, [9] * 40)], seed=14), Batch([(64, [2, 3]), (1600, [7, 8, 9])], seed=15)]
+    streams = [torch.cuda.Stream() for _ in bs]
+    torch.cuda.synchronize()
+    args = [b.args() for b in bs]
+    outs = [[], []]
+    torch.cuda.synchronize()
+    for rnd in range(6):
+        for k, (b, s) in enumerate(zip(bs, streams)):
+            with torch.cuda.stream(s):
+                if rnd % 3 == 2:
+                    outs[k].append(pa_lib.decode(*args[k][:5], **b.kw()))
+                else:
+                    outs[k].append(pa_lib.decode_shared(*args[k], **b.kw()))
+    torch.cuda.synchronize()
+    for k, b in enumerate(bs):
+        for o in outs[k]:
+            b.check(o)
+    assert pa_lib.check_device_error() == 0
+
+
+def test_captured_step_follows_new_lengths_and_groups(pa_lib):
+    b = Batch([(640, [9, 30, 1, 60]), (640, [200, 3, 4, 5])], seed=16)
+    args = b.args()
+    out = torch.empty_like(b.q)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        pa_lib.decode_shared(*args, out=out, **b.kw())  # workspace before the capture
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            pa_lib.decode_shared(*args, out=out, **b.kw())
+    full = b.lens.copy()
+    for lens, pre in ((full, b.prefix), (np.maximum(full - 1, 0), [320, 640]), (full * [1, 0, 1, 1, 0, 1, 1, 1], [640, 16]),
+                      (full, [0, 0])):
+        b.lens = np.asarray(lens, np.int32)
+        args[4].copy_(torch.from_numpy(b.lens))
+        args[5].copy_(torch.tensor(pre, dtype=torch.int32))
+        out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        b.check(out)
+    assert pa_lib.check_device_error() == 0
+
+
+def test_a_whole_step_from_lengths_to_attention(pa_lib):
+    """pool_extend, norm_rope_and_cache and decode_shared in one captured step,
+    replayed: a batch that forks one prompt grows by one token a step, its new
+    keys rotated at the positions the pool gave. The reference keeps its own
+    keys and values per sequence in 64 bits, from the same 16-bit inputs."""
+    B, P, Hq, Hkv, D, bs, steps = 6, 96, 8, 2, 128, 16, 20
+    dt = torch.float16
+    NB, MB = 64, 10
+    g = torch.Generator(device="cuda").manual_seed(3)
+    kc = torch.full((NB, Hkv, bs, D), float("nan"), dtype=dt, device="cuda")
+    vc = torch.full((NB, Hkv, bs, D), float("nan"), dtype=dt, device="cuda")
+    ids = shuffled_free_list(NB, 4)
+    pre = [ids.pop() for _ in range(P // bs)]
+    kp, vp = (torch.randn(P, Hkv, D, generator=g, device="cuda").to(dt) for _ in range(2))
+    slots = (torch.tensor(pre, device="cuda")[:, None] * bs + torch.arange(bs, device="cuda")).reshape(-1)
+    pa_lib.reshape_and_cache(kp, vp, kc, vc, slots)
+    tables = torch.full((B, MB), -1, dtype=torch.int32, device="cuda")
+    tables[:, :P // bs] = torch.tensor(pre, dtype=torch.int32, device="cuda")
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    free = torch.tensor(ids + pre, dtype=torch.int32, device="cuda")
+    state = i32(len(ids), 0)
+    lens, new = i32(*[P] * B), i32(*[1] * B)
+    new[4] = 0                                          # this one pauses
+    T = B + 2
+    slot, pos, start = (torch.zeros(n, dtype=d, device="cuda") for n, d in ((T, torch.int64), (T, torch.int32), (B + 1, torch.int32)))
+    qkv = torch.zeros(T, (Hq + 2 * Hkv) * D, dtype=dt, device="cuda")
+    q, k, v = qkv.view(T, Hq + 2 * Hkv, D).split([Hq, Hkv, Hkv], dim=1)
+    w = [(1 + 0.2 * torch.randn(D, generator=g, device="cuda")).to(dt) for _ in range(2)]
+    a = torch.arange(200, dtype=torch.float64)[:, None] * 10000.0 ** -(torch.arange(0, D, 2, dtype=torch.float64) / D)
+    cs = torch.cat([a.cos(), a.sin()], 1).float().cuda()
+    qr = torch.zeros(T, Hq, D, dtype=dt, device="cuda")
+    out = torch.zeros(B, Hq, D, dtype=dt, device="cuda")
+    prefix, groups = i32(P), i32(0, B)
+
+    def step():
+        pa_lib.pool_extend(tables, lens, new, free, state, block_size=bs, slot_mapping=slot, positions=pos, query_start=start)
+        pa_lib.norm_rope_and_cache(q, k, v, kc, vc, slot, pos, cs, q_weight=w[0], k_weight=w[1], out=qr)
+        # rows of the step to rows of the batch (a paused row keeps an older query)
+        qb.copy_(qr[torch.minimum(start[:B], last)])
+        pa_lib.decode_shared(qb, kc, vc, tables, lens, prefix, groups, num_kv_heads=Hkv, scale=D ** -0.5, block_size=bs, out=out)
+
+    qb = torch.zeros(B, Hq, D, dtype=dt, device="cuda")
+    last = torch.full((B,), T - 1, dtype=torch.int32, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    keep = [x.clone() for x in (tables, lens, state, kc, vc)]
+    with torch.cuda.stream(s):
+        step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            step()
+    for x, y in zip((tables, lens, state, kc, vc), keep):
+        x.copy_(y)
+    keys = [kp.double().cpu().numpy().copy() for _ in range(B)]
+    vals = [vp.double().cpu().numpy().copy() for _ in range(B)]
+    cs64 = cs.double().cpu().numpy()
+
+    def turned(x, wt, p):
+        x = x.double().cpu().numpy()
+        x = x / np.sqrt((x * x).mean(-1, keepdims=True) + 1e-6) * wt.double().cpu().numpy()
+        c, sn = cs64[p, :D // 2], cs64[p, D // 2:]
+        return np.concatenate([x[..., :D // 2] * c - x[..., D // 2:] * sn, x[..., D // 2:] * c + x[..., :D // 2] * sn], -1)
+
+    for n in range(steps):
+        qkv.copy_(torch.randn(qkv.shape, generator=g, device="cuda"))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out_f64(out)
+        row = 0
+        for b in range(B):
+            if b == 4:
+                assert lens[b].item() == P
+                continue
+            p = P + n
+            keys[b] = np.concatenate([keys[b], turned(k[row], w[1], p)[None]])
+            vals[b] = np.concatenate([vals[b], v[row].double().cpu().numpy()[None]])
+            qq = turned(q[row], w[0], p).reshape(Hkv, Hq // Hkv, D)
+            sc = np.einsum("kgd,tkd->kgt", qq, keys[b]) * D ** -0.5
+            e = np.exp(sc - sc.max(-1, keepdims=True))
+            e /= e.sum(-1, keepdims=True)
+            ref = np.einsum("kgt,tkd->kgd", e, vals[b]).reshape(Hq, D)
+            size = np.einsum("kgt,tkd->kgd", e, np.abs(vals[b])).reshape(Hq, D)
+            # besides the bound above: q and k are themselves rounded, 2^-11 of each
+            # element, so a score moves by at most 2^-10 sum |q k| scale (below 16
+            # here), a weight by 2^-10 * 16 of itself against the others'
+            bound = 2.0 ** -11 * np.abs(ref) + (2.0 ** -10 * 16 * 2 + 2.0 ** -8) * size + 1e-6
+            assert (np.abs(got[b] - ref) <= bound).all(), (n, b)
+            # and far closer on average
+            assert np.abs(got[b] - ref).mean() <= 2e-3 * size.mean(), (n, b)
+            row += 1
+        assert start.tolist() == [0, 1, 2, 3, 4, 4, 5]
+    assert pa_lib.check_device_error() == 0
