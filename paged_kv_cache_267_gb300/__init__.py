@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -50,7 +51,8 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(f"{LIB_PATH} is missing: build it with "
                                "`python -c 'import __graft_entry__ as g; g.build()'`")
         L = ctypes.CDLL(LIB_PATH)
-        P = ctypes.POINTER(PaTensor)
+        # descriptors are passed by address: a PaTensor by reference, or its bytes
+        P = ctypes.c_void_p
         i32, i64, f32, vp, st = (ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p,
                                  ctypes.c_int32)
         sig = {
@@ -133,8 +135,36 @@ def tensor_desc(t: torch.Tensor) -> PaTensor:
     return d
 
 
+# pa_tensor as bytes, by rank (the same layout as PaTensor): a descriptor built in
+# one call, a few times faster than filling a ctypes structure field by field.
+_PACK = [struct.Struct(f"Pii{n}q{8 * (_MAX_DIMS - n)}x{n}q{8 * (_MAX_DIMS - n)}x").pack
+         for n in range(_MAX_DIMS + 1)]
+
+
+def _desc(t):
+    """Descriptor argument of a tensor (as tensor_desc, in bytes); NULL for None."""
+    if t is None:
+        return None
+    shape = t.shape
+    try:
+        return _PACK[len(shape)](t.data_ptr(), _TORCH_TO_PA[t.dtype], len(shape), *shape,
+                                 *t.stride())
+    except KeyError:
+        raise TypeError(f"unsupported dtype {t.dtype}") from None
+    except IndexError:
+        raise ValueError("too many dims") from None
+
+
+# The current stream's handle straight from torch's C side where it offers it
+# (torch.cuda.current_stream() builds a Stream object every time).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
+        if _raw_stream is not None and _raw_device is not None and torch.cuda.is_initialized():
+            return _raw_stream(_raw_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -154,14 +184,9 @@ def _kv(kv_dtype) -> int:
 def reshape_and_cache(k, v, key_cache, value_cache, slot_mapping, kv_dtype="auto",
                       k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
     """Scatter k/v [T, Hkv, D] into the caches [NB, Hkv, bs, D] at slot_mapping [T]."""
-    descs = [tensor_desc(x) for x in (k, v, key_cache, value_cache, slot_mapping)]
-    _check(lib().pa_reshape_and_cache(*[ctypes.byref(d) for d in descs], _kv(kv_dtype),
+    descs = [_desc(x) for x in (k, v, key_cache, value_cache, slot_mapping)]
+    _check(lib().pa_reshape_and_cache(*descs, _kv(kv_dtype),
                                       float(k_scale), float(v_scale), _stream(stream)))
-
-
-def _ref(t):
-    """Descriptor argument of a tensor, or NULL for None."""
-    return None if t is None else ctypes.byref(tensor_desc(t))
 
 
 def norm_rope_and_cache(q, k, v, key_cache, value_cache, slot_mapping, positions, cos_sin, *,
@@ -176,7 +201,7 @@ def norm_rope_and_cache(q, k, v, key_cache, value_cache, slot_mapping, positions
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     _check(lib().pa_norm_rope_and_cache(
-        *[_ref(x) for x in (out, q, k, v, key_cache, value_cache, slot_mapping, positions,
+        *[_desc(x) for x in (out, q, k, v, key_cache, value_cache, slot_mapping, positions,
                             cos_sin, q_weight, k_weight)],
         float(eps), int(bool(interleaved)), _kv(kv_dtype), float(k_scale), float(v_scale),
         _stream(stream)))
@@ -193,7 +218,7 @@ def pool_extend(block_tables, seq_lens, new_tokens, free_list, pool_state, *, bl
     place unless outputs are given. A step that does not fit changes nothing
     and sets DEVERR_POOL, DEVERR_TOKENS or DEVERR_SEQ_LEN."""
     _check(lib().pa_pool_extend(
-        *[_ref(x) for x in (block_tables, seq_lens, new_tokens, free_list, pool_state,
+        *[_desc(x) for x in (block_tables, seq_lens, new_tokens, free_list, pool_state,
                             seq_lens if seq_lens_out is None else seq_lens_out,
                             pool_state if pool_state_out is None else pool_state_out,
                             query_start, slot_mapping, positions)],
@@ -207,7 +232,7 @@ def pool_release(block_tables, seq_lens, released, free_list, pool_state, *, blo
     list (all but the leading ones that hold shared_tokens[b] tokens) and set
     their lengths to 0, in place unless outputs are given."""
     _check(lib().pa_pool_release(
-        *[_ref(x) for x in (block_tables, seq_lens, released, shared_tokens, free_list,
+        *[_desc(x) for x in (block_tables, seq_lens, released, shared_tokens, free_list,
                             pool_state, seq_lens if seq_lens_out is None else seq_lens_out,
                             pool_state if pool_state_out is None else pool_state_out)],
         int(block_size), _stream(stream)))
@@ -219,8 +244,8 @@ def decode(q, key_cache, value_cache, block_tables, seq_lens, *, num_kv_heads: i
     """One paged decode step; returns out [B, Hq, D] (allocated if not given)."""
     if out is None:
         out = torch.empty_like(q)
-    descs = [tensor_desc(x) for x in (out, q, key_cache, value_cache, block_tables, seq_lens)]
-    _check(lib().pa_decode(*[ctypes.byref(d) for d in descs], int(num_kv_heads), float(scale),
+    descs = [_desc(x) for x in (out, q, key_cache, value_cache, block_tables, seq_lens)]
+    _check(lib().pa_decode(*descs, int(num_kv_heads), float(scale),
                            int(block_size), int(window), _kv(kv_dtype), float(k_scale),
                            float(v_scale), _stream(stream)))
     return out
@@ -237,7 +262,7 @@ def decode_shared(q, key_cache, value_cache, block_tables, seq_lens, prefix_lens
     if out is None:
         out = torch.empty_like(q)
     _check(lib().pa_decode_shared(
-        *[_ref(x) for x in (out, q, key_cache, value_cache, block_tables, seq_lens, prefix_lens,
+        *[_desc(x) for x in (out, q, key_cache, value_cache, block_tables, seq_lens, prefix_lens,
                             group_starts)],
         int(num_kv_heads), float(scale), int(block_size), int(window), _kv(kv_dtype),
         float(k_scale), float(v_scale), _stream(stream)))
@@ -252,8 +277,8 @@ def prefill_chunk(q, key_cache, value_cache, block_tables, seq_lens, *, num_kv_h
     [B, T, Hq, D] (allocated if not given)."""
     if out is None:
         out = torch.empty_like(q)
-    descs = [tensor_desc(x) for x in (out, q, key_cache, value_cache, block_tables, seq_lens)]
-    _check(lib().pa_prefill_chunk(*[ctypes.byref(d) for d in descs], int(num_kv_heads),
+    descs = [_desc(x) for x in (out, q, key_cache, value_cache, block_tables, seq_lens)]
+    _check(lib().pa_prefill_chunk(*descs, int(num_kv_heads),
                                   float(scale), int(block_size), int(window), _kv(kv_dtype),
                                   float(k_scale), float(v_scale), _stream(stream)))
     return out
@@ -265,8 +290,8 @@ def decode_noalloc(q, key_cache, value_cache, block_tables, seq_lens, *, num_kv_
     """pa_decode_noalloc: the decode step with the library's built-in scratch
     array instead of a workspace, for callers that cannot allocate device
     memory at decode time. `out` must be given (nothing is allocated)."""
-    descs = [tensor_desc(x) for x in (out, q, key_cache, value_cache, block_tables, seq_lens)]
-    _check(lib().pa_decode_noalloc(*[ctypes.byref(d) for d in descs], int(num_kv_heads),
+    descs = [_desc(x) for x in (out, q, key_cache, value_cache, block_tables, seq_lens)]
+    _check(lib().pa_decode_noalloc(*descs, int(num_kv_heads),
                                    float(scale), int(block_size), int(window), _kv(kv_dtype),
                                    float(k_scale), float(v_scale), _stream(stream)))
     return out

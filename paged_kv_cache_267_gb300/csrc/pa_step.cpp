@@ -143,6 +143,7 @@ pa_status pa_pool_extend(const pa_tensor* block_tables, const pa_tensor* seq_len
     a.B = static_cast<int>(B);
     a.MB = static_cast<int>(block_tables->shape[1]);
     a.bs = block_size;
+    a.div = fast_div(static_cast<uint32_t>(block_size));
     a.NF = static_cast<int>(free_list->shape[0]);
     a.T = static_cast<int>(T);
     a.in_place = a.lens_out == a.lens || a.state_out == a.state;
@@ -192,6 +193,7 @@ pa_status pa_pool_release(const pa_tensor* block_tables, const pa_tensor* seq_le
     a.B = static_cast<int>(B);
     a.MB = static_cast<int>(block_tables->shape[1]);
     a.bs = block_size;
+    a.div = fast_div(static_cast<uint32_t>(block_size));
     a.NF = static_cast<int>(free_list->shape[0]);
     a.in_place = a.lens_out == a.lens || a.state_out == a.state;
     const cudaError_t e = pool_release_launch(a, dev.num_sms, static_cast<cudaStream_t>(stream));

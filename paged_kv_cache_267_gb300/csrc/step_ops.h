@@ -10,6 +10,15 @@ namespace pa {
 
 // The block pool (pool_ops.cu). in_place: lens_out is lens, or state_out is
 // state; the last CTA to have read them then writes them.
+// Division of 31-bit integers by a fixed d > 1 as a multiplication.
+struct FastDiv {
+  uint32_t mul, shift;
+};
+inline FastDiv fast_div(uint32_t d) {
+  uint32_t l = 1;
+  while ((1ull << l) < d) ++l;
+  return FastDiv{static_cast<uint32_t>(((1ull << (31 + l)) + d - 1) / d), l - 1};
+}
 struct PoolExtendArgs {
   int32_t* tables;               // [B, MB]
   const int32_t* lens;           // [B] before the step
@@ -23,6 +32,7 @@ struct PoolExtendArgs {
   int32_t* positions;            // [T]
   int32_t* err;                  // device error word
   int B, MB, bs, NF, T;
+  FastDiv div;                   // by bs
   bool in_place;
   bool wide;                     // slots and positions are 16-byte aligned
 };
@@ -37,6 +47,7 @@ struct PoolReleaseArgs {
   int32_t* state_out;
   int32_t* err;
   int B, MB, bs, NF;
+  FastDiv div;                   // by bs
   bool in_place;
 };
 cudaError_t pool_extend_launch(const PoolExtendArgs& a, int num_sms, cudaStream_t s);
