@@ -22,7 +22,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CU_SOURCES = ["decode_bf16.cu", "decode_f16.cu", "decode_fp8.cu", "decode_mq_bf16.cu",
               "decode_mq_f16.cu", "decode_mq_fp8.cu", "chunk_tc.cu", "merge_reshape.cu",
               "decode_noalloc.cu", "selftest.cu", "pool_ops.cu", "norm_cache.cu",
-              "shared_plan.cu", "prefix_tc.cu", "decode_sh_bf16.cu", "decode_sh_f16.cu",
+              "shared_plan.cu", "prefix_tc.cu", "shared_merge.cu", "decode_sh_bf16.cu", "decode_sh_f16.cu",
               "decode_sh_fp8.cu"]
 CPP_SOURCES = ["pa_api.cpp", "pa_step.cpp", "pa_alloc.cpp"]
 

@@ -6,7 +6,6 @@
 #include "pa_internal.h"
 #include "plan.cuh"
 #include "ptx.cuh"
-#include "shared_plan.cuh"
 
 namespace pa {
 
@@ -221,23 +220,10 @@ struct MergeCol {
   int s;        // pair index
   Cands cd;
   int ncand;
-  // SH: partials of the shared prefix, the last nshared of ncand
-  int nshared, up, slot0;
 };
 
-// Slot of candidate k of column c: static segments, pool pieces, then (SH) the
-// prefix segments' partials.
-template <bool SH>
-__device__ __forceinline__ int slot_of(const MergeArgs& a, const MergeCol& c, int k) {
-  if (k < c.cd.na) return c.s + c.cd.w0 + k;
-  k -= c.cd.na;
-  if (!SH || k < c.cd.np) return a.B * a.Hv + a.NW + c.s + c.cd.i0 + k;
-  return c.slot0 + (k - c.cd.np) * c.up;  // (CTA, half), up slots apart
-}
-
-template <bool SH>
 __device__ __forceinline__ MergeCol merge_col(const MergeArgs& a, const StepPlan& pl,
-                                              const int* s_pref, int b, int col, int wsz) {
+                                              const int* s_pref, int b, int col) {
   MergeCol c;
   const int vh = col / a.CG;
   c.h = col - vh * a.CG;  // pair and column within it
@@ -250,19 +236,6 @@ __device__ __forceinline__ MergeCol merge_col(const MergeArgs& a, const StepPlan
   const int F = a.Hv * s_pref[b] + vh * nt;
   c.cd = pair_cands(F, nt, pl);
   c.ncand = c.cd.na + c.cd.np;
-  if constexpr (SH) {
-    const SharedRow r = a.shared_rows[b];
-    c.nshared = 0;
-    if (r.nt > 0) {
-      const int f0 = r.f0 + kvh * r.kv_step;
-      const int w0 = f0 / wsz, nut = r.nut_sub >> 2;
-      const int sub = r.nut_sub & 3;
-      c.up = r.up_sub / sub;
-      c.nshared = ((f0 + r.nt - 1) / wsz - w0 + 1) * sub;
-      c.slot0 = a.shared_part0 + r.slot0 + (kvh * nut + r.lid0 + w0) * r.up_sub;
-      c.ncand += c.nshared;
-    }
-  }
   c.orow = ((static_cast<size_t>(b) * a.T + tq) * a.Hq + kvh * a.G + (gc - tq * a.G)) * a.D;
   return c;
 }
@@ -300,7 +273,7 @@ __device__ __forceinline__ void combine_groups(const MergeArgs& a, const float* 
   store_head<OT, VPL>(a, orow, r, ngrp == 0);
 }
 
-template <int OT, int VPL, bool SH>
+template <int OT, int VPL>
 __global__ void __launch_bounds__(kMergeThreads, 3) merge_kernel(const MergeArgs a) {
   constexpr int ROW = VPL * 128 + 4;  // floats per group result in shared memory
   extern __shared__ __align__(16) float s_dyn[];
@@ -344,8 +317,7 @@ __global__ void __launch_bounds__(kMergeThreads, 3) merge_kernel(const MergeArgs
   __syncthreads();
   const StepPlan pl = plan_load(s_plan);
   const int HC = a.Hv * a.CG;  // columns per sequence
-  int wsz = 1;  // SH: K/V tiles a CTA of the prefix kernel
-  if constexpr (SH) wsz = a.shared_head[kShWsz];
+  const int S = a.B * a.Hv;
 
   // Wide columns, counted in half-CTA units: a column whose pairs may have
   // more than 4 * kMergeNarrow partials takes a whole CTA (two units; its
@@ -362,11 +334,7 @@ __global__ void __launch_bounds__(kMergeThreads, 3) merge_kernel(const MergeArgs
       int cls = 0, x = 0;
       if (b < a.B) {
         const int nt = s_pref[b + 1] - s_pref[b];
-        int ub = pair_cand_bound(nt, a.Hv * s_pref[b], a.Hv * s_pref[b + 1], pl);
-        if constexpr (SH) {
-          const SharedRow r = a.shared_rows[b];
-          if (r.nt > 0) ub += min(r.nt, r.nt / wsz + 2) * (r.nut_sub & 3);
-        }
+        const int ub = pair_cand_bound(nt, a.Hv * s_pref[b], a.Hv * s_pref[b + 1], pl);
         cls = ub > 4 * kMergeNarrow ? 2 : (ub > kMergeNarrow ? 1 : 0);
         x = cls == 2 ? 2 * HC : (cls == 1 ? HC + (HC & 1) : 0);
       }
@@ -408,12 +376,14 @@ __global__ void __launch_bounds__(kMergeThreads, 3) merge_kernel(const MergeArgs
     bool active = col < HC;  // an odd HC pads a half-column sequence by one unit
     MergeCol c;
     if (active) {
-      c = merge_col<SH>(a, pl, s_pref, lo, col, wsz);
+      c = merge_col(a, pl, s_pref, lo, col);
       active = !c.pad;
     }
     int ngrp = 0;
     if (active) {
-      auto slot = [&](int k) -> int { return slot_of<SH>(a, c, k); };
+      auto slot = [&](int k) -> int {
+        return k < c.cd.na ? c.s + c.cd.w0 + k : S + a.NW + c.s + c.cd.i0 + (k - c.cd.na);
+      };
       const int gsz = c.ncand > 0 ? (c.ncand + nwg - 1) / nwg : 1;
       ngrp = c.ncand > 0 ? (c.ncand + gsz - 1) / gsz : 0;
       const int wi = warp - w0;
@@ -455,10 +425,12 @@ __global__ void __launch_bounds__(kMergeThreads, 3) merge_kernel(const MergeArgs
       act = act && (s_wide[b] & 3) == 0;  // wide columns are taken by the wide phase
       MergeCol c = {};
       if (act) {
-        c = merge_col<SH>(a, pl, s_pref, b, u - b * HC, wsz);
+        c = merge_col(a, pl, s_pref, b, u - b * HC);
         act = !c.pad;
       }
-      auto slot = [&](int k) -> int { return slot_of<SH>(a, c, k); };
+      auto slot = [&](int k) -> int {
+        return k < c.cd.na ? c.s + c.cd.w0 + k : S + a.NW + c.s + c.cd.i0 + (k - c.cd.na);
+      };
       HalfAcc r;
       griddep_wait();  // the partials are complete and visible
       merge_fold_half(a, slot, act ? c.ncand : 0, act ? c.h : 0, r);
@@ -468,9 +440,11 @@ __global__ void __launch_bounds__(kMergeThreads, 3) merge_kernel(const MergeArgs
     for (int u = rot * kMergeWarps + warp; u < a.B * HC; u += nwarps) {
       const int b = u / HC;
       if (s_wide[b] & 3) continue;  // taken by the wide phase
-      const MergeCol c = merge_col<SH>(a, pl, s_pref, b, u - b * HC, wsz);
+      const MergeCol c = merge_col(a, pl, s_pref, b, u - b * HC);
       if (c.pad) continue;
-      auto slot = [&](int k) -> int { return slot_of<SH>(a, c, k); };
+      auto slot = [&](int k) -> int {
+        return k < c.cd.na ? c.s + c.cd.w0 + k : S + a.NW + c.s + c.cd.i0 + (k - c.cd.na);
+      };
       HeadAcc<VPL> r;
       griddep_wait();  // the partials are complete and visible
       merge_fold(a, slot, 0, c.ncand, c.h, r);
@@ -502,13 +476,8 @@ cudaError_t merge_launch(int out_type, const MergeArgs& a, int grid, cudaStream_
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   void (*fn)(const MergeArgs);
-  if (a.shared_rows) {
-    if (a.D > 128) fn = out_type == kBF16 ? merge_kernel<kBF16, 2, true> : merge_kernel<kF16, 2, true>;
-    else fn = out_type == kBF16 ? merge_kernel<kBF16, 1, true> : merge_kernel<kF16, 1, true>;
-  } else {
-    if (a.D > 128) fn = out_type == kBF16 ? merge_kernel<kBF16, 2, false> : merge_kernel<kF16, 2, false>;
-    else fn = out_type == kBF16 ? merge_kernel<kBF16, 1, false> : merge_kernel<kF16, 1, false>;
-  }
+  if (a.D > 128) fn = out_type == kBF16 ? merge_kernel<kBF16, 2> : merge_kernel<kF16, 2>;
+  else fn = out_type == kBF16 ? merge_kernel<kBF16, 1> : merge_kernel<kF16, 1>;
   if (cfg.dynamicSmemBytes > 48 * 1024) {  // large batches: the per-sequence prefixes
     const cudaError_t e = cudaFuncSetAttribute(
         reinterpret_cast<const void*>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize,

@@ -31,11 +31,7 @@ namespace pa {
 namespace {
 
 constexpr int kThreads = 256;
-#ifndef MH
-#define MH 4
-#define MB_ 4
-#endif
-constexpr int kManyHeads = MH;
+constexpr int kManyHeads = 4;  // heads a thread in large batches
 constexpr unsigned kFull = 0xffffffffu;
 
 // Two 8-byte chunks of a head: four words of two elements.
@@ -94,7 +90,7 @@ __device__ __forceinline__ void pairs_of(const Raw& r, float2 (&lo)[2], float2 (
 
 // LANES lanes a head (D <= 8 * LANES), kHeads heads of one kind a thread.
 template <int ST, bool FP8, bool INTER, int LANES, int kHeads>
-__global__ void __launch_bounds__(kThreads, kHeads > 1 ? MB_ : 4) norm_cache_kernel(const NormCacheArgs a) {
+__global__ void __launch_bounds__(kThreads, kHeads > 1 ? 5 : 4) norm_cache_kernel(const NormCacheArgs a) {
   constexpr int kGroups = kThreads / LANES;
   // rows may come from the previous kernel, and the caches may still be read
   // by it. The next kernel may start its launch: of what is written here it
@@ -278,7 +274,7 @@ cudaError_t launch(NormCacheArgs a, cudaStream_t s) {
 
 template <int ST, bool FP8, bool INTER, int LANES>
 cudaError_t launch_heads(const NormCacheArgs& a, int num_sms, cudaStream_t s) {
-  // eight heads a thread once that still fills every SM twice over
+  // four heads a thread once that still fills every SM twice over
   const long long groups = static_cast<long long>(a.T) * (a.Hq + 2 * a.Hkv);
   const long long ctas = groups / kManyHeads / (kThreads / LANES);
   return ctas >= 2ll * num_sms ? launch<ST, FP8, INTER, LANES, kManyHeads>(a, s)

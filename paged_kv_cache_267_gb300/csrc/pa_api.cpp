@@ -247,7 +247,7 @@ struct WsLayout {
 // Hv pairs per sequence with CG columns each (Hkv and G for single-query decode).
 // NG groups and shared_slots prefix partials: shared-prefix steps (else 0).
 WsLayout ws_layout(int64_t B, int Hv, int CG, int D, int64_t workers, int64_t NG = 0,
-                   size_t shared_slots = 0) {
+                   size_t shared_slots = 0, int ctas = 0) {
   const size_t S = static_cast<size_t>(B) * Hv;
   const size_t nslot = 2 * S + workers + static_cast<size_t>(workers) * kPiecesPerWorker;
   WsLayout L;
@@ -257,7 +257,7 @@ WsLayout ws_layout(int64_t B, int Hv, int CG, int D, int64_t workers, int64_t NG
   L.pool = o;  o += 256;
   L.plan = o;  o += round_up(static_cast<size_t>(pa::plan_words(static_cast<int>(B))) * 4, 256);
   L.shared = o;
-  if (shared_slots) o += round_up(pa::shared_plan_words(B, NG) * 4, 256);
+  if (shared_slots) o += round_up(pa::shared_plan_words(B, NG, ctas) * 4, 256);
   L.shared_slot0 = nslot;
   L.part = o;  o += (nslot + shared_slots) * static_cast<size_t>(pa::part_stride(CG, D)) * sizeof(float);
   L.total = o;
@@ -546,7 +546,8 @@ pa_status workspace_size(int64_t batch, int64_t num_queries, int32_t num_q_heads
                      num_groups > 0 ? most_shared_slots(batch, num_kv_heads,
                                                         num_q_heads / num_kv_heads, head_dim,
                                                         st->num_sms)
-                                    : 0)
+                                    : 0,
+                     num_groups > 0 ? st->num_sms : 0)
                .total;
   return ok();
 }
@@ -835,7 +836,8 @@ pa_status plan_call(DeviceState* st, const DecodeCall& c, DecodePlan* plan, WsLa
     plan->workers = plan->grid * plan->var.warps;
   }
   *layout = ws_layout(c.B, c.Hv, c.CG, static_cast<int>(c.D), plan->workers, sh ? sh->NG : 0,
-                      sh ? most_shared_slots(c.B, c.Hkv, c.G, static_cast<int>(c.D), st->num_sms) : 0);
+                      sh ? most_shared_slots(c.B, c.Hkv, c.G, static_cast<int>(c.D), st->num_sms) : 0,
+                      sh ? st->num_sms : 0);
   return PA_OK;
 }
 
@@ -913,7 +915,7 @@ pa_status run_decode(const DecodeCall& c, DeviceState* st, const DecodePlan& pla
     p.kv = shape.kv;
     p.unit_rows = shape.unit_rows;
     p.halves = shape.halves;
-    p.grid = grid;
+    p.ctas = grid;
     p.min_tiles = kPrefixMinTiles;
     e = pa::shared_plan_launch(p, cs, !prof);
     if (e != cudaSuccess) return cuda_fail(e, "shared plan launch");
@@ -923,6 +925,7 @@ pa_status run_decode(const DecodeCall& c, DeviceState* st, const DecodePlan& pla
     x.plan = p.plan;
     x.part = a.part + layout.shared_slot0 * pa::part_stride(a.CG, D);
     x.err = a.err;
+    x.ctas = grid;
     x.NG = p.NG;
     x.Hq = a.Hq;
     x.Hkv = a.Hkv;
@@ -935,7 +938,7 @@ pa_status run_decode(const DecodeCall& c, DeviceState* st, const DecodePlan& pla
     e = pa::prefix_launch(c.qt, c.fp8, D, tk, tv, x, grid, cs, !prof);
     if (e != cudaSuccess) return cuda_fail(e, "prefix kernel launch");
     g_launches += 2;
-    a.shared_rows = reinterpret_cast<const pa::SharedRow*>(p.plan + pa::kSharedHead + 12 * p.NG);
+    a.shared_rows = pa::shared_rows(p.plan, grid, p.NG);
   }
   if (prof && (e = cudaEventRecord(static_cast<cudaEvent_t>(g_prof_before), cs)) != cudaSuccess)
     return cuda_fail(e, "profile event");
@@ -958,15 +961,30 @@ pa_status run_decode(const DecodeCall& c, DeviceState* st, const DecodePlan& pla
   m.NCG = a.NCG;
   m.CG = a.CG;
   m.Hv = a.Hv;
-  m.shared_rows = a.shared_rows;
-  m.shared_head = sh ? reinterpret_cast<const int32_t*>(wsb + layout.shared) : nullptr;
-  m.shared_part0 = static_cast<int>(layout.shared_slot0);
   // three CTAs per SM, and no more than output columns (a wide column takes
   // one CTA, a narrow one a warp)
   const int64_t cols = static_cast<int64_t>(m.B) * m.Hv * m.CG;
   const int merge_grid =
       static_cast<int>(std::min<int64_t>(int64_t(st->num_sms) * 3, std::max<int64_t>(cols, 1)));
-  e = pa::merge_launch(c.qt, m, merge_grid, cs, !prof);
+  if (sh) {
+    pa::SharedMergeArgs sm;
+    sm.out = m.out;
+    sm.part = m.part;
+    sm.plan = m.plan;
+    sm.shared = reinterpret_cast<const int32_t*>(wsb + layout.shared);
+    sm.pool = m.pool;
+    sm.B = m.B;
+    sm.Hkv = m.Hkv;
+    sm.G = m.G;
+    sm.D = m.D;
+    sm.NW = m.NW;
+    sm.NG = static_cast<int>(sh->NG);
+    sm.ctas = st->num_sms;
+    sm.part0 = static_cast<int>(layout.shared_slot0);
+    e = pa::shared_merge_launch(c.qt, sm, cs, !prof);
+  } else {
+    e = pa::merge_launch(c.qt, m, merge_grid, cs, !prof);
+  }
   if (e != cudaSuccess) {
     if (wsp) {
       std::lock_guard<std::mutex> lk(g_mu);

@@ -74,11 +74,6 @@ struct MergeArgs {
   uint32_t* pool;                // reset to zero for the next step
   int B, Hq, Hkv, G, D, NW;
   int T, NCG, CG, Hv;            // as in DecodeArgs
-  // shared-prefix steps only (else null): each sequence's part of the prefix,
-  // the plan's header and the first slot of the prefix partials
-  const SharedRow* shared_rows;
-  const int32_t* shared_head;
-  int shared_part0;
 };
 
 // Bound on output columns (batch * q heads * queries) of one call.

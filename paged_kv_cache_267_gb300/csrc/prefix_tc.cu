@@ -10,27 +10,36 @@
 //
 // Read once for all rows, the prefix costs 4 n G D operations a token and KV
 // head for 4 D bytes (16-bit): memory-bound below about n G = 280 rows, tensor
-// and exponential above. The flat space of K/V tiles is split evenly over one
-// CTA per SM (shared_plan.cuh), whatever the groups' sizes.
+// and exponential above. The flat space of K/V tiles is split evenly over the
+// CTAs (shared_plan.cuh), whatever the groups' sizes.
 //
-// Roles as in the chunk kernel: a producer warp streams K and V tiles of kKv
-// tokens through two-stage rings (TMA through the block table of one of the
-// group's sequences), an MMA warp issues every product, and groups of four
-// softmax warps serve one 128-row tile each (one row a thread). With two
-// groups, a unit of more than 128 rows gives each group half of the rows on
-// every tile; a smaller one gives both groups the same rows on every other
-// tile, so that the tensor core always works for one group while the other
-// is in its softmax. Per tile and group x:
+// Roles as in the chunk kernel: producers stream K and V tiles of kKv tokens
+// through rings (TMA through the block table of one of the group's sequences;
+// the next tile's block ids are looked up while the last one's copies are
+// awaited), one thread issues every product, and groups of four softmax warps
+// serve one 128-row tile each (one row a thread). With two groups, a unit of
+// more than 128 rows gives each group half of the rows on every tile; a smaller
+// one gives both groups the same rows on every other tile, so that the tensor
+// core always works for one group while the other is in its softmax. Per tile
+// and group x:
 //   S_x = Q_x K^T -> TMEM; P_x (16-bit, packed in pairs) over the first half of
 //   each 64 columns of S_x; O_x += P_x V from TMEM
-// as in the chunk kernel, with its lazy reference max. K/V rows behind the
-// prefix in its last tile are not loaded; their scores are masked and their V
-// rows zeroed in shared memory. head_dim 256 takes one group and 64-token
-// tiles (its O fills half of the tensor memory, its Q 64 KB).
+// with a lazy reference max. K/V rows behind the prefix in its last tile are not
+// loaded; their scores are masked and their V rows zeroed in shared memory.
+// head_dim 256 takes one group and 64-token tiles (its O fills half of the
+// tensor memory, its Q 64 KB).
 //
-// FP8 caches: two converter warps turn each raw e4m3 tile into the f16 tile the
-// products read (exact); Q is rescaled per row by a power of two to f16's
-// range, which the row's score scale undoes.
+// A CTA's tiles are few (its share of one prefix), so what it does once a
+// segment counts as much as the loop: Q is loaded, and the partials stored, by
+// whole warps along the rows (through the Q buffer, which is free once the
+// last S is done), 128 bytes and more a row at once. One thread a row, 16
+// bytes each, had cost about 6,000 and 5,000-9,700 cycles a segment of at most
+// 100,000.
+//
+// FP8 caches: two converter warps, half of the rows each, turn each raw e4m3
+// tile into the f16 tile the products read (exact), K first: the next S waits
+// for it; Q is rescaled per row by a power of two to f16's range, which
+// the row's score scale undoes.
 #include "attn_tc.cuh"
 #include "pa_internal.h"
 #include "ptx.cuh"
@@ -43,19 +52,34 @@ namespace {
 
 constexpr int kRows = 128;
 constexpr int kGroupThreads = 128;
-constexpr int kConvWarps = 2;
+constexpr int kConv = 2;  // FP8 converter warps
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;  // bound of every wait (2 s)
 constexpr float kFloor = -1e30f;             // reference-max start
 constexpr float kRescaleAbove = 8.f;         // log2 units
 constexpr unsigned kFull = 0xffffffffu;
 
-// barriers: K and V rings (full, empty; two stages each); per group x: S_x
+// barriers: K and V rings (full, empty; up to kMaxStages each); per group x: S_x
 // computed, P_x written, O_x product complete, Q_x staged; FP8: converted K
 // written / read, converted V (two buffers) written / read
-constexpr int kBarKFull = 0, kBarKEmpty = 2, kBarVFull = 4, kBarVEmpty = 6, kBarS = 8, kBarP = 10,
-              kBarO = 12, kBarQ = 14, kBarCKFull = 16, kBarCKFree = 17, kBarCVFull = 18,
-              kBarCVFree = 20, kNumBars = 22;
+constexpr int kMaxStages = 4;
+constexpr int kBarKFull = 0, kBarKEmpty = kBarKFull + kMaxStages, kBarVFull = kBarKEmpty + kMaxStages,
+              kBarVEmpty = kBarVFull + kMaxStages, kBarS = kBarVEmpty + kMaxStages,
+              kBarP = kBarS + 2, kBarO = kBarP + 2, kBarQ = kBarO + 2, kBarCKFull = kBarQ + 2,
+              kBarCKFree = kBarCKFull + 1, kBarCVFull = kBarCKFree + 1, kBarCVFree = kBarCVFull + 2,
+              kNumBars = kBarCVFree + 2;
+
+// Stage and phase of a ring position.
+struct Ring {
+  int stage = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+};
 
 template <int D, bool FP8>
 struct Cfg {
@@ -63,14 +87,20 @@ struct Cfg {
   static constexpr int kKv = D == 256 ? 64 : 128;   // tokens a tile
   static constexpr int kSlices = kKv / 16;
   static constexpr int kBoxes = D / 64;  // 64-dim boxes of a 16-bit tile
-  static constexpr int kMmaWarp = 4 * kGroups, kLoadWarp = kMmaWarp + 1, kConvWarp0 = kLoadWarp + 1;
-  static constexpr int kThreads = (kConvWarp0 + (FP8 ? kConvWarps : 0)) * 32;
+  // 16-bit tiles are loaded by one warp for K and one for V: a V stage is held
+  // through a softmax, a K stage only through its product, and in one warp K
+  // loads would wait behind V's
+  static constexpr int kLoadWarps = FP8 ? 1 : 2;
+  static constexpr int kKStages = FP8 ? 2 : (D == 64 ? 4 : 2), kVStages = FP8 ? 2 : (D == 64 ? 4 : 3);
+  static constexpr int kMmaWarp = 4 * kGroups, kLoadWarp = kMmaWarp + 1,
+                       kConvWarp0 = kLoadWarp + kLoadWarps;
+  static constexpr int kThreads = (kConvWarp0 + (FP8 ? kConv : 0)) * 32;
   static constexpr uint32_t kQBox = kRows * 128, kQBytes = kBoxes * kQBox;  // one group's Q
   static constexpr uint32_t kBox = kKv * 128, kTile = kBoxes * kBox;        // 16-bit K or V tile
   static constexpr uint32_t kRawBoxes = FP8 ? D / 128 : kBoxes;             // 128-byte boxes
   static constexpr uint32_t kRing = kRawBoxes * kBox;                       // ring tile
-  static constexpr uint32_t kQ = 0, kK = kQ + kGroups * kQBytes, kV = kK + 2 * kRing;
-  static constexpr uint32_t kKc = kV + 2 * kRing, kVc = kKc + (FP8 ? kTile : 0);
+  static constexpr uint32_t kQ = 0, kK = kQ + kGroups * kQBytes, kV = kK + kKStages * kRing;
+  static constexpr uint32_t kKc = kV + kVStages * kRing, kVc = kKc + (FP8 ? kTile : 0);
   static constexpr uint32_t kBar = kVc + (FP8 ? 2 * kTile : 0);
   static constexpr uint32_t kSlot = kBar + 8 * kNumBars;
   static constexpr uint32_t kBytes = kSlot + 16 + 1024;  // + room to align the base to 1 KB
@@ -93,20 +123,11 @@ struct Segment {
   int slot0;   // slot of x 0, pair 0
 };
 
-// The segment that starts at flat tile f (gi: the group found last, or -1).
+// The segment that starts at flat tile f, in the group of s->g or one behind.
 __device__ __forceinline__ void segment_at(const PrefixArgs& a, int f, int f_end, int* gi,
                                            Segment* s) {
-  const SharedGroup* groups = shared_groups(a.plan);
-  if (*gi < 0) {  // the last group with f0 <= f (those without tiles come before)
-    int lo = 0, hi = a.NG;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (groups[mid].f0 <= f) lo = mid; else hi = mid;
-    }
-    *gi = lo;
-    s->g = groups[lo];
-  }
-  while (f >= s->g.f0 + a.Hkv * s->g.nut * s->g.nt && *gi + 1 < a.NG) s->g = groups[++*gi];
+  while (f >= s->g.f0 + a.Hkv * s->g.nut * s->g.nt && *gi + 1 < a.NG)
+    s->g = shared_groups(a.plan, a.ctas)[++*gi];
   const int rem = f - s->g.f0, unit = rem / s->g.nt;
   s->t0 = rem - unit * s->g.nt;
   s->nt = min(s->g.nt - s->t0, f_end - f);
@@ -116,6 +137,13 @@ __device__ __forceinline__ void segment_at(const PrefixArgs& a, int f, int f_end
   s->np = min(s->g.up, s->g.n - s->ut * s->g.up);
   s->dual = s->g.sub == 1;
   s->slot0 = s->g.base + (unit + static_cast<int>(blockIdx.x) - s->g.wfirst) * s->g.sub * s->g.up;
+}
+
+template <int QT>
+__device__ __forceinline__ float f32_of(uint32_t w, int hi) {
+  const uint16_t v = static_cast<uint16_t>(hi ? w >> 16 : w & 0xffffu);
+  return QT == kBF16 ? __uint_as_float(static_cast<uint32_t>(v) << 16)
+                     : __half2float(__ushort_as_half(v));
 }
 
 template <int QT, int D, bool FP8>
@@ -132,32 +160,26 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
   const uint32_t sKc = base + C::kKc, sVc = base + C::kVc;
   auto bar = [&](int i) -> uint32_t { return base + C::kBar + 8u * i; };
   const uint32_t* tslot = reinterpret_cast<const uint32_t*>(smem_raw + (base - raw) + C::kSlot);
-  // the 16-bit K and V tiles the products read for this CTA's c-th tile, and
-  // the barrier (with parity) that says they are ready
-  auto tile_k = [&](int c) -> uint32_t { return FP8 ? sKc : sK + (c & 1) * C::kTile; };
-  auto tile_v = [&](int c) -> uint32_t { return (FP8 ? sVc : sV) + (c & 1) * C::kTile; };
-  auto k_ready = [&](int c) -> uint32_t { return FP8 ? bar(kBarCKFull) : bar(kBarKFull + (c & 1)); };
-  auto v_ready = [&](int c) -> uint32_t { return bar((FP8 ? kBarCVFull : kBarVFull) + (c & 1)); };
-  auto k_par = [&](int c) -> uint32_t { return FP8 ? c & 1 : (c >> 1) & 1; };
-  auto v_par = [&](int c) -> uint32_t { return (c >> 1) & 1; };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(bar(kBarKFull + i), 1);
-      mbar_init(bar(kBarKEmpty + i), FP8 ? kConvWarps * 32 : 1);
+      mbar_init(bar(kBarKEmpty + i), FP8 ? kConv * 32 : 1);
       mbar_init(bar(kBarVFull + i), 1);
-      mbar_init(bar(kBarVEmpty + i), FP8 ? kConvWarps * 32 : 1);
+      mbar_init(bar(kBarVEmpty + i), FP8 ? kConv * 32 : 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kBarS + i), 1);
       mbar_init(bar(kBarP + i), kGroupThreads);
       mbar_init(bar(kBarO + i), 1);
       mbar_init(bar(kBarQ + i), kGroupThreads);
-      mbar_init(bar(kBarCVFull + i), kConvWarps * 32);
+      mbar_init(bar(kBarCVFull + i), kConv * 32);
       mbar_init(bar(kBarCVFree + i), 1);
     }
-    mbar_init(bar(kBarCKFull), kConvWarps * 32);
+    mbar_init(bar(kBarCKFull), kConv * 32);
     mbar_init(bar(kBarCKFree), 1);
     fence_mbar_init();
   }
@@ -169,251 +191,295 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
   griddep_wait();  // the plan, and behind it the caches and queries, are written
   griddep_launch_dependents();
 
-  const int total = a.plan[kShTotal], wsz = a.plan[kShWsz];
-  const int f0 = static_cast<int>(min(static_cast<long long>(blockIdx.x) * wsz, static_cast<long long>(total)));
-  const int f1 = min(f0 + wsz, total);
-  const int ntiles = f1 - f0;  // of this CTA, over all its segments
-  int gi = -1;
   Segment sg;
+  const SharedCta mine = shared_ctas(a.plan)[blockIdx.x];
+  sg.g = mine.g;
+  const int f0 = mine.f0, f1 = mine.f1;
+  const int ntiles = f1 - f0;  // of this CTA, over all its segments
+  int gi = mine.group;
 
-  if (warp == C::kLoadWarp) {
-    // ------------------------------------------------------------ producer
-    // K (or V) tile: lanes 0..kSlices-1 each look up one 16-token slice in the
-    // block table and copy its 128-byte boxes; slices behind the prefix are
-    // not loaded
-    auto load = [&](int c, int t, bool is_v) {
-      const uint32_t full = bar((is_v ? kBarVFull : kBarKFull) + (c & 1));
+  if (warp >= C::kLoadWarp && warp < C::kConvWarp0) {
+    // ------------------------------------------------------------ producers
+    // Lanes 0..kSlices-1 each look up one 16-token slice of a tile in the block
+    // table and copy its 128-byte boxes; slices behind the prefix (row < 0)
+    // are not loaded.
+    auto row_of = [&](int t) -> int {
       const int pos0 = t * C::kKv + 16 * lane;
-      int row = -1;
-      if (lane < C::kSlices && pos0 < sg.g.prefix) {
-        int blk = __ldg(a.block_tables + static_cast<size_t>(sg.g.table_row) * a.MB + pos0 / a.bs);
-        if (static_cast<unsigned>(blk) >= static_cast<unsigned>(a.NB)) {
-          atomicOr(a.err, PA_DEVERR_BLOCK_ID);
-          blk = 0;
-        }
-        row = (blk * a.Hkv + sg.kvh) * a.bs + pos0 % a.bs;
+      if (lane >= C::kSlices || pos0 >= sg.g.prefix) return -1;
+      int blk = __ldg(a.block_tables + static_cast<size_t>(sg.g.table_row) * a.MB + pos0 / a.bs);
+      if (static_cast<unsigned>(blk) >= static_cast<unsigned>(a.NB)) {
+        atomicOr(a.err, PA_DEVERR_BLOCK_ID);
+        blk = 0;
       }
+      return (blk * a.Hkv + sg.kvh) * a.bs + pos0 % a.bs;
+    };
+    auto load = [&](int stage, int row, bool is_v) {
+      const uint32_t full = bar((is_v ? kBarVFull : kBarKFull) + stage);
       const int nslices = __popc(__ballot_sync(kFull, row >= 0));
       if (lane == 0) mbar_arrive_expect_tx(full, nslices * C::kRawBoxes * 2048);
       __syncwarp();
       if (row >= 0) {
-        const uint32_t dst = (is_v ? sV : sK) + (c & 1) * C::kRing + lane * 2048;
+        const uint32_t dst = (is_v ? sV : sK) + stage * C::kRing + lane * 2048;
 #pragma unroll
         for (int box = 0; box < static_cast<int>(C::kRawBoxes); ++box)
           tma_load_2d(dst + box * C::kBox, is_v ? &tmV : &tmK, box * (FP8 ? 128 : 64), row, full);
       }
       __syncwarp();
     };
+    const bool do_k = C::kLoadWarps == 1 || warp == C::kLoadWarp;
+    const bool do_v = C::kLoadWarps == 1 || warp != C::kLoadWarp;
     bool ok = true;
+    Ring kr, vr;
     int c = 0;
     for (int f = f0; ok && f < f1; f += sg.nt) {
       segment_at(a, f, f1, &gi, &sg);
+      int row = row_of(sg.t0);
       for (int n = 0; ok && n < sg.nt; ++n, ++c) {
-        const uint32_t par = ((c - 2) >> 1) & 1;  // release of the stage's last tile
-        if (c >= 2 && !(ok = wait_all(bar(kBarKEmpty + (c & 1)), par))) break;
-        load(c, sg.t0 + n, false);
-        if (c >= 2 && !(ok = wait_all(bar(kBarVEmpty + (c & 1)), par))) break;
-        load(c, sg.t0 + n, true);
+        // looked up while the waits below run
+        const int next = n + 1 < sg.nt ? row_of(sg.t0 + n + 1) : -1;
+        if (do_k) {  // the release of the stage's last tile: the phase before
+          if (c >= C::kKStages && !(ok = wait_all(bar(kBarKEmpty + kr.stage), kr.phase ^ 1))) break;
+          load(kr.stage, row, false);
+          kr.next(C::kKStages);
+        }
+        if (do_v) {
+          if (c >= C::kVStages && !(ok = wait_all(bar(kBarVEmpty + vr.stage), vr.phase ^ 1))) break;
+          load(vr.stage, row, true);
+          vr.next(C::kVStages);
+        }
+        row = next;
       }
     }
     if (!ok && lane == 0) atomicOr(a.err, PA_DEVERR_TIMEOUT);
   } else if (warp == C::kMmaWarp) {
     // ------------------------------------------------------------ MMA issue
-    constexpr uint32_t idS = tc::idesc_f16(kRows, C::kKv, kBf16, false);
-    constexpr uint32_t idO = tc::idesc_f16(kRows, D, kBf16, true);
-    auto issue_s = [&](int x, int c) {
-      if (lane == 0) {
+    // One thread does all of it: its own instructions are on the critical
+    // path of every tile, and waits and votes of a whole warp cost about 150
+    // cycles each even when there is nothing to wait for.
+    if (lane == 0) {
+      constexpr uint32_t idS = tc::idesc_f16(kRows, C::kKv, kBf16, false);
+      constexpr uint32_t idO = tc::idesc_f16(kRows, D, kBf16, true);
+      // Positions of the K and V tiles in use, and the barriers that say they
+      // are ready: the ring's, or the converted buffers' (one of K, two of V).
+      constexpr int KB = FP8 ? 1 : C::kKStages, VB = FP8 ? 2 : C::kVStages;
+      Ring kr, vr;
+      int kc = 0, vc = 0;  // tiles of K, V the products are done with
+      auto wait = [&](uint32_t b, uint32_t parity) { return mbar_wait_bounded(b, parity, kWaitNs); };
+      auto issue_s = [&](int x) {
         const uint64_t dQ = tc::sdesc_sw128(sQ + x * C::kQBytes, 16, 1024);
-        const uint64_t dK = tc::sdesc_sw128(tile_k(c), 16, 1024);
+        const uint64_t dK = tc::sdesc_sw128((FP8 ? sKc : sK) + kr.stage * C::kTile, 16, 1024);
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          tc::mma_f16(tmem + C::kColS + C::kKv * x,
-                      dQ + (((ks >> 2) * C::kQBox + (ks & 3) * 32) >> 4),
-                      dK + (((ks >> 2) * C::kBox + (ks & 3) * 32) >> 4), idS, ks > 0);
+        for (int box = 0; box < C::kBoxes; ++box)
+          mma4_ss(tmem + C::kColS + C::kKv * x, dQ + box * (C::kQBox >> 4),
+                  dK + box * (C::kBox >> 4), idS, box > 0);
         tc::commit(bar(kBarS + x));
-      }
-      __syncwarp();
-    };
-    // O_x (+)= P_x V: 16 tokens a step, P in 8 columns each from 64 h on
-    auto issue_o = [&](int x, int c, bool first) {
-      if (lane == 0) {
-        const uint64_t dV = tc::sdesc_sw128(tile_v(c), C::kBox, 1024);
+      };
+      // O_x (+)= P_x V: 16 tokens a step, P in 8 columns each from 64 h on
+      auto issue_o = [&](int x, bool first) {
+        const uint64_t dV = tc::sdesc_sw128((FP8 ? sVc : sV) + vr.stage * C::kTile, C::kBox, 1024);
 #pragma unroll
-        for (int k = 0; k < C::kKv / 16; ++k)
-          tc::mma_f16_ta(tmem + C::kColO + D * x,
-                         tmem + C::kColS + C::kKv * x + 64 * (k >> 2) + 8 * (k & 3),
-                         dV + 128 * k, idO, !first || k > 0);
+        for (int h = 0; h < C::kKv / 64; ++h)
+          mma4_ts(tmem + C::kColO + D * x, tmem + C::kColS + C::kKv * x + 64 * h, dV + 512 * h, idO,
+                  !first || h > 0);
         tc::commit(bar(kBarO + x));
-      }
-      __syncwarp();
-    };
-    // A release is committed only when something will wait for it, so no
-    // arrive outlives the CTA.
-    auto release_k = [&](int c) {
-      if (lane == 0) {
-        if (FP8 && c + 1 < ntiles) tc::commit(bar(kBarCKFree));
-        if (!FP8 && c + 2 < ntiles) tc::commit(bar(kBarKEmpty + (c & 1)));
-      }
-      __syncwarp();
-    };
-    auto release_v = [&](int c) {
-      if (lane == 0 && c + 2 < ntiles) tc::commit(bar((FP8 ? kBarCVFree : kBarVEmpty) + (c & 1)));
-      __syncwarp();
-    };
-    bool ok = true;
-    int c0 = 0;
-    int ops[2] = {0, 0};   // products O_x issued so far
-    int segs[2] = {0, 0};  // segments of each group so far (those it has tiles of)
-    for (int f = f0; ok && f < f1; f += sg.nt, c0 += sg.nt) {
-      segment_at(a, f, f1, &gi, &sg);
-      // the i-th S (and O) product of the segment: group i % NX, tile i / NX
-      // (its own rows) or i (its own tiles)
-      const bool dual = NX == 2 && sg.dual;
-      const int nops = dual ? 2 * sg.nt : sg.nt;
-      auto x_of = [&](int i) -> int { return NX == 2 ? i & 1 : 0; };
-      auto c_of = [&](int i) -> int { return c0 + (dual ? i >> 1 : i); };
-      auto first_use = [&](int i) -> bool { return !dual || !(i & 1); };
-      auto last_use = [&](int i) -> bool { return !dual || (i & 1); };
-      for (int i = 0; i < NX && i < nops; ++i) {
-        if (!(ok = wait_all(bar(kBarQ + i), segs[i]++ & 1))) break;
-        if (first_use(i) && !(ok = wait_all(k_ready(c_of(i)), k_par(c_of(i))))) break;
-        tc::fence_after_sync();
-        issue_s(x_of(i), c_of(i));
-        if (last_use(i)) release_k(c_of(i));
-      }
-      for (int i = 0; ok && i < nops; ++i) {
-        const int x = x_of(i), c = c_of(i);
-        const uint32_t par = ops[x] & 1;
-        if (!(ok = wait_all(bar(kBarP + x), par))) break;  // P_x (and clean V rows) written
-        if (first_use(i) && !(ok = wait_all(v_ready(c), v_par(c)))) break;
-        tc::fence_after_sync();
-        issue_o(x, c, i < NX);
-        ++ops[x];
-        if (last_use(i)) release_v(c);
-        if (i + NX < nops) {
-          const int cn = c_of(i + NX);
-          if (first_use(i + NX) && !(ok = wait_all(k_ready(cn), k_par(cn)))) break;
-          if (!(ok = wait_all(bar(kBarO + x), par))) break;  // P_x consumed
+      };
+      // A release is committed only when something will wait for it, so no
+      // arrive outlives the CTA.
+      auto release_k = [&]() {
+        if (kc + KB < ntiles) tc::commit(bar(FP8 ? kBarCKFree : kBarKEmpty + kr.stage));
+        ++kc;
+        kr.next(KB);
+      };
+      auto release_v = [&]() {
+        if (vc + VB < ntiles) tc::commit(bar((FP8 ? kBarCVFree : kBarVEmpty) + vr.stage));
+        ++vc;
+        vr.next(VB);
+      };
+      auto wait_k = [&]() { return wait(bar(FP8 ? kBarCKFull : kBarKFull + kr.stage), kr.phase); };
+      auto wait_v = [&]() { return wait(bar((FP8 ? kBarCVFull : kBarVFull) + vr.stage), vr.phase); };
+      bool ok = true;
+      int ops[2] = {0, 0};   // products O_x issued so far
+      int segs[2] = {0, 0};  // segments of each group so far (those it has tiles of)
+      for (int f = f0; ok && f < f1; f += sg.nt) {
+        segment_at(a, f, f1, &gi, &sg);
+        // the i-th S (and O) product of the segment: group i % NX, tile i / NX
+        // (its own rows) or i (its own tiles)
+        const bool dual = NX == 2 && sg.dual;
+        const int nops = dual ? 2 * sg.nt : sg.nt;
+        auto x_of = [&](int i) -> int { return NX == 2 ? i & 1 : 0; };
+        auto first_use = [&](int i) -> bool { return !dual || !(i & 1); };
+        auto last_use = [&](int i) -> bool { return !dual || (i & 1); };
+        for (int i = 0; i < NX && i < nops; ++i) {
+          if (!(ok = wait(bar(kBarQ + i), segs[i]++ & 1))) break;
+          if (first_use(i) && !(ok = wait_k())) break;
           tc::fence_after_sync();
-          issue_s(x, cn);
-          if (last_use(i + NX)) release_k(cn);
+          issue_s(x_of(i));
+          if (last_use(i)) release_k();
+        }
+        for (int i = 0; ok && i < nops; ++i) {
+          const int x = x_of(i);
+          const uint32_t par = ops[x] & 1;
+          if (first_use(i) && !(ok = wait_v())) break;
+          if (!(ok = wait(bar(kBarP + x), par))) break;  // P_x (and clean V rows) written
+          tc::fence_after_sync();
+          issue_o(x, i < NX);
+          ++ops[x];
+          if (last_use(i)) release_v();
+          if (i + NX < nops) {
+            if (first_use(i + NX) && !(ok = wait_k())) break;
+            if (!(ok = wait(bar(kBarO + x), par))) break;  // P_x consumed
+            tc::fence_after_sync();
+            issue_s(x);
+            if (last_use(i + NX)) release_k();
+          }
         }
       }
+      if (!ok) atomicOr(a.err, PA_DEVERR_TIMEOUT);
     }
-    if (!ok && lane == 0) atomicOr(a.err, PA_DEVERR_TIMEOUT);
+    __syncwarp();
   } else if (warp >= C::kConvWarp0) {
     // ------------------------------------------------------------ FP8 converters
-    // e4m3 tile c, ring stage c & 1 -> the f16 buffer: a 16-byte chunk of 16
-    // codes becomes two 16-byte chunks of f16 in the 64-dim box that holds
-    // them; V rows behind the prefix are written as zeros.
+    // e4m3 tile -> the f16 buffer: a 16-byte chunk of 16 codes becomes two
+    // 16-byte chunks of f16 in the 64-dim box that holds them; V rows behind the
+    // prefix are zeroed. (The conversions bind a warp: about 2,000 cycles for
+    // the 16 KB of a tile.)
     if constexpr (FP8) {
-      constexpr int kChunks = D / 16, kPer = kConvWarps * 32 / kChunks;
-      const int ct = tid - C::kConvWarp0 * 32;
-      const int ch = ct % kChunks, q0 = ct / kChunks;
+      constexpr int kChunks = D / 16, kPer = 32 / kChunks;  // chunks a row, rows a pass
+      constexpr int kOctets = C::kKv / 8 / kConv;           // row octets of a warp
+      const int row0 = (warp - C::kConvWarp0) * kOctets * 8;
+      const int ch = lane % kChunks, q0 = lane / kChunks;
+      const int c16 = 2 * (ch & 3);
+      auto convert = [&](uint32_t src, uint32_t dst) {
+        src += (ch >> 3) * C::kBox;
+        dst += (ch >> 2) * C::kBox;
+        // rows r, r + 8, ... share one swizzle
+        static_assert(8 % kPer == 0, "passes of a row octet");
+#pragma unroll 1
+        for (int p = 0; p < 8 / kPer; ++p) {
+          const int r0 = row0 + q0 + kPer * p;
+          const uint32_t from = src + r0 * 128 + (((ch & 7) ^ (r0 & 7)) << 4);
+          const uint32_t lo = dst + r0 * 128 + ((c16 ^ (r0 & 7)) << 4);
+          const uint32_t hi = dst + r0 * 128 + (((c16 + 1) ^ (r0 & 7)) << 4);
+#pragma unroll
+          for (int k = 0; k < kOctets; ++k) {
+            uint32_t w[4], h[8];
+            lds_v4(from + 1024 * k, w[0], w[1], w[2], w[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              h[2 * i] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] & 0xffffu));
+              h[2 * i + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] >> 16));
+            }
+            sts_v4(lo + 1024 * k, make_uint4(h[0], h[1], h[2], h[3]));
+            sts_v4(hi + 1024 * k, make_uint4(h[4], h[5], h[6], h[7]));
+          }
+        }
+      };
       bool ok = true;
       int c = 0;
+      Ring in;
       for (int f = f0; ok && f < f1; f += sg.nt) {
         segment_at(a, f, f1, &gi, &sg);
         for (int n = 0; ok && n < sg.nt; ++n, ++c) {
           const int lim = sg.g.prefix - (sg.t0 + n) * C::kKv;  // rows of the tile inside the prefix
-          for (int is_v = 0; is_v < 2; ++is_v) {
-            if (!(ok = wait_all(bar((is_v ? kBarVFull : kBarKFull) + (c & 1)), (c >> 1) & 1))) break;
-            if (!is_v && c > 0 && !(ok = wait_all(bar(kBarCKFree), (c - 1) & 1))) break;
-            if (is_v && c > 1 && !(ok = wait_all(bar(kBarCVFree + (c & 1)), ((c - 2) >> 1) & 1))) break;
-            const uint32_t src = (is_v ? sV : sK) + (c & 1) * C::kRing + (ch >> 3) * C::kBox;
-            const uint32_t dst = (is_v ? sVc + (c & 1) * C::kTile : sKc) + (ch >> 2) * C::kBox;
-            const int c16 = 2 * (ch & 3);
-#pragma unroll 8
-            for (int k = 0; k < C::kKv / kPer; ++k) {
-              const int r = q0 + kPer * k;
-              uint32_t w[4];
-              lds_v4(src + r * 128 + (((ch & 7) ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
-              uint32_t h[8];
+          // K, once the products of the tile before have read its buffer
+          if (!(ok = wait_all(bar(kBarKFull + in.stage), in.phase))) break;
+          if (c > 0 && !(ok = wait_all(bar(kBarCKFree), (c - 1) & 1))) break;
+          convert(sK + in.stage * C::kRing, sKc);
+          fence_proxy_async();  // the f16 tile, visible to the tensor core
+          mbar_arrive(bar(kBarCKFull));
+          mbar_arrive(bar(kBarKEmpty + in.stage));  // reload the stage
+          // V, into the buffer of two tiles before
+          const uint32_t vt = sVc + (c & 1) * C::kTile;
+          if (!(ok = wait_all(bar(kBarVFull + in.stage), in.phase))) break;
+          if (c > 1 && !(ok = wait_all(bar(kBarCVFree + (c & 1)), ((c - 2) >> 1) & 1))) break;
+          convert(sV + in.stage * C::kRing, vt);
+          if (lim < C::kKv) {
+            __syncwarp();
+            for (int i = max(lim, row0) * 8 + lane; i < (row0 + kOctets * 8) * 8; i += 32)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                h[2 * i] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] & 0xffffu));
-                h[2 * i + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] >> 16));
-              }
-              const bool zero = is_v && r >= lim;
-              sts_v4(dst + r * 128 + ((c16 ^ (r & 7)) << 4),
-                     zero ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(h[0], h[1], h[2], h[3]));
-              sts_v4(dst + r * 128 + (((c16 + 1) ^ (r & 7)) << 4),
-                     zero ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(h[4], h[5], h[6], h[7]));
-            }
-            fence_proxy_async();  // the f16 tile, visible to the tensor core
-            mbar_arrive(bar(is_v ? kBarCVFull + (c & 1) : kBarCKFull));
-            // reload the stage (where something will wait for it)
-            mbar_arrive(bar((is_v ? kBarVEmpty : kBarKEmpty) + (c & 1)));
+              for (int box = 0; box < C::kBoxes; ++box)
+                sts_v4(vt + box * C::kBox + i * 16, make_uint4(0u, 0u, 0u, 0u));
           }
+          fence_proxy_async();
+          mbar_arrive(bar(kBarCVFull + (c & 1)));
+          mbar_arrive(bar(kBarVEmpty + in.stage));
+          in.next(2);
         }
       }
       if (!ok && lane == 0) atomicOr(a.err, PA_DEVERR_TIMEOUT);
     }
   } else {
     // ------------------------------------------------------------ softmax
-    const int x = warp >> 2;           // group
-    const int r = tid - x * kRows;     // row of the tile = tensor-memory lane
+    const int x = warp >> 2;        // group
+    const int r = tid - x * kRows;  // row of the tile = tensor-memory lane
     const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t tS = trow + C::kColS + C::kKv * x, tO = trow + C::kColO + D * x;
-    const SharedRow* rows = shared_rows(a.plan, a.NG);
+    const SharedRow* rows = shared_rows(a.plan, a.ctas, a.NG);
+    // Whole-warp row access: kPer rows at once, kCh lanes of 16 bytes each. A row
+    // of Q (D 16-bit values) and half a row of O (D / 2 floats) have 2 D bytes.
+    constexpr int kCh = D / 8, kPer = 32 / kCh;
+    const int wr0 = (warp & 3) * 32;  // first row of this warp
+    const int sub_r = lane / kCh, ch = lane % kCh;
+    const uint32_t pair_mul = (65536u + a.G - 1) / a.G;  // row / G = row * mul >> 16, rows < 256
     bool ok = true;
     int c0 = 0, op = 0;  // products of this group so far
     for (int f = f0; ok && f < f1; f += sg.nt, c0 += sg.nt) {
       segment_at(a, f, f1, &gi, &sg);
       const bool dual = NX == 2 && sg.dual;
       const int nj = dual || NX == 1 ? sg.nt : (sg.nt - x + 1) >> 1;  // this group's tiles
-      const int row = r + (dual ? x * kRows : 0);  // row of the unit: pair * G + head
-      const int pair = row / a.G, h = row - pair * a.G;
-      const int b = sg.b0 + pair;
-      // rows of the last pairs, and of sequences that take no part, stay zero
-      const bool valid = pair < sg.np && rows[b].nt > 0;
+      const int u0 = dual ? x * kRows : 0;  // row of the unit (pair * G + head) at row 0 here
       float sc = fabsf(a.score_scale);
       // A group without tiles in a segment (the second half of a single tile)
       // stages no Q: with nothing to wait for it would run ahead of the barrier.
-      if (nj > 0) {  // Q row -> shared memory (K-major, 128-byte swizzle)
+      if (nj > 0) {  // Q rows -> shared memory (K-major, 128-byte swizzle)
         const uint32_t flip = a.score_scale < 0.f ? 0x80008000u : 0u;
-        const size_t qrow =
-            (static_cast<size_t>(valid ? b : 0) * a.Hq + static_cast<size_t>(sg.kvh) * a.G + h) * D;
-        const uint4* src =
-            reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) + qrow);
-        const uint32_t dst = sQ + x * C::kQBytes + r * 128;
-        auto f32 = [&](uint32_t w, int hi) -> float {
-          const uint16_t v = static_cast<uint16_t>(hi ? w >> 16 : w & 0xffffu);
-          return QT == kBF16 ? __uint_as_float(static_cast<uint32_t>(v) << 16)
-                             : __half2float(__ushort_as_half(v));
-        };
-        int sh = 0;
-        if constexpr (FP8) {
-          // f16 after a power-of-two rescale: largest magnitude in [2^14, 2^15)
-          float amax = 0.f;
+        const uint32_t q_tile = sQ + x * C::kQBytes + (ch >> 3) * C::kQBox;
+        int sh_mine = 0;
+        constexpr int kBatch = 8;  // loads in flight
+#pragma unroll 1
+        for (int i0 = 0; i0 < kCh; i0 += kBatch) {
+          uint4 v[kBatch];
 #pragma unroll
-          for (int ch = 0; ch < D / 8; ++ch) {
-            const uint4 v = valid ? src[ch] : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+          for (int i = 0; i < kBatch; ++i) {
+            // rows behind the unit's, and sequences that take no part, compute
+            // on some row and are not stored
+            const int ur = u0 + wr0 + (i0 + i) * kPer + sub_r;
+            const int p = static_cast<int>((ur * pair_mul) >> 16), h = ur - p * a.G;
+            const size_t row = static_cast<size_t>(sg.b0 + min(p, sg.np - 1)) * a.Hq +
+                               static_cast<size_t>(sg.kvh) * a.G + h;
+            v[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + row * D) + ch);
+          }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f32(w4[i >> 1], i & 1)));
+          for (int i = 0; i < kBatch; ++i) {
+            const int rr = wr0 + (i0 + i) * kPer + sub_r;
+            if constexpr (FP8) {
+              // f16 after a power-of-two rescale: largest magnitude in [2^14, 2^15)
+              const uint32_t w4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+              float amax = 0.f;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f32_of<QT>(w4[e >> 1], e & 1)));
+#pragma unroll
+              for (int o = kCh / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+              int sh = 0;
+              if (amax > 0.f && amax < INFINITY) {
+                int e;
+                frexpf(amax, &e);
+                sh = e - 15;
+              }
+              uint32_t o4[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                o4[e] = pack16x2<false>(ldexpf(f32_of<QT>(w4[e], 0), -sh), ldexpf(f32_of<QT>(w4[e], 1), -sh));
+              v[i] = make_uint4(o4[0], o4[1], o4[2], o4[3]);
+              // to the lane that owns the row
+              const int theirs = __shfl_sync(kFull, sh, (lane % kPer) * kCh);
+              if (lane / kPer == i0 + i) sh_mine = theirs;
+            }
+            v[i].x ^= flip, v[i].y ^= flip, v[i].z ^= flip, v[i].w ^= flip;
+            sts_v4(q_tile + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4), v[i]);
           }
-          if (amax > 0.f && amax < INFINITY) {
-            int e;
-            frexpf(amax, &e);
-            sh = e - 15;
-          }
-          sc = ldexpf(sc, sh);
         }
-#pragma unroll
-        for (int ch = 0; ch < D / 8; ++ch) {
-          uint4 v = valid ? src[ch] : make_uint4(0u, 0u, 0u, 0u);
-          if constexpr (FP8) {
-            const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
-            uint32_t o4[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              o4[i] = pack16x2<false>(ldexpf(f32(w4[i], 0), -sh), ldexpf(f32(w4[i], 1), -sh));
-            v = make_uint4(o4[0], o4[1], o4[2], o4[3]);
-          }
-          v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
-          sts_v4(dst + (ch >> 3) * C::kQBox + (((ch & 7) ^ (r & 7)) << 4), v);
-        }
+        if constexpr (FP8) sc = ldexpf(sc, sh_mine);
         fence_proxy_async();
         tc::fence_before_sync();  // the last segment's O has been read
         mbar_arrive(bar(kBarQ + x));
@@ -489,13 +555,23 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             tc::wait_ld(sv[0], sv[1]);
           }
           uint32_t pk[32];
+          if (all_in) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float2 t = __ffma2_rn(score_pair(sv[i >> 4], (2 * i) & 31), sc2, nms2);
-            float p0 = ex2(t.x), p1 = ex2(t.y);
-            if (!all_in && 64 * hf + 2 * i >= lim) p0 = p1 = 0.f;
-            sp[i & 3] = __fadd2_rn(sp[i & 3], make_float2(p0, p1));
-            pk[i] = pack16x2<kBf16>(p0, p1);
+            for (int i = 0; i < 32; ++i) {
+              const float2 t = __ffma2_rn(score_pair(sv[i >> 4], (2 * i) & 31), sc2, nms2);
+              const float p0 = ex2(t.x), p1 = ex2(t.y);
+              sp[i & 3] = __fadd2_rn(sp[i & 3], make_float2(p0, p1));
+              pk[i] = pack16x2<kBf16>(p0, p1);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float2 t = __ffma2_rn(score_pair(sv[i >> 4], (2 * i) & 31), sc2, nms2);
+              const bool in = 64 * hf + 2 * i < lim;
+              const float p0 = in ? ex2(t.x) : 0.f, p1 = in ? ex2(t.y) : 0.f;
+              sp[i & 3] = __fadd2_rn(sp[i & 3], make_float2(p0, p1));
+              pk[i] = pack16x2<kBf16>(p0, p1);
+            }
           }
           tc::st32(tS + 64 * hf, pk);
         }
@@ -505,9 +581,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         if (!FP8 && !all_in && !(dual && x == 1)) {
           // the prefix ends inside this tile: zero its V rows behind it once
           // the others have landed
-          const int c = c0 + n;
-          if (!(ok = wait_all(bar(kBarVFull + (c & 1)), (c >> 1) & 1))) break;
-          const uint32_t vt = sV + (c & 1) * C::kTile;
+          const int c = c0 + n, stage = c % C::kVStages;
+          if (!(ok = wait_all(bar(kBarVFull + stage), (c / C::kVStages) & 1))) break;
+          const uint32_t vt = sV + stage * C::kTile;
           for (int i = lim * 8 + r; i < C::kKv * 8; i += kRows)
 #pragma unroll
             for (int box = 0; box < C::kBoxes; ++box)
@@ -518,34 +594,62 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         tc::fence_before_sync();
         mbar_arrive(bar(kBarP + x));
       }
-      // the partial of this row: O as it is, its reference max and sum
+      // The partials of these rows: O as it is, its reference max and sum. O goes
+      // through the Q buffer in two halves of the head dim.
+      const int ur_mine = u0 + r, p_mine = static_cast<int>((ur_mine * pair_mul) >> 16);
+      const bool valid = p_mine < sg.np && rows[sg.b0 + min(p_mine, sg.np - 1)].nt > 0;
+      const unsigned valid_rows = __ballot_sync(kFull, valid);
       if (ok && nj > 0) ok = wait_all(bar(kBarO + x), (op - 1) & 1);
       tc::fence_after_sync();
       const bool some = ok && nj > 0;
-      const int slot = sg.slot0 + (dual || NX == 1 ? 0 : x * sg.g.up) + pair;
-      float* P = a.part + static_cast<size_t>(slot) * part_stride(a.G, D);
+      float* const P0 =
+          a.part + static_cast<size_t>(sg.slot0 + (dual || NX == 1 ? 0 : x * sg.g.up)) * part_stride(a.G, D);
       const uint64_t keep = l2_evict_last();  // the merge reads them soon
+      // 16-byte chunk c of row r, where the row's own Q was: no warp touches
+      // another's rows
+      auto staged = [&](int row, int c) -> uint32_t {
+        return sQ + x * C::kQBytes + (c >> 3) * C::kQBox + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+      };
+      const float vs = some ? a.v_scale : 0.f;
 #pragma unroll 1
-      for (int d0 = 0; d0 < D; d0 += 32) {
-        uint32_t ov[32];
-        if (nj > 0) {
-          tc::ld32_async(tO + d0, ov);
-          tc::wait_ld(ov);
-        }
-        if (valid) {
-          const float vs = some ? a.v_scale : 0.f;
+      for (int half = 0; half < 2; ++half) {
+#pragma unroll 1
+        for (int d0 = 0; d0 < D / 2; d0 += 32) {
+          uint32_t ov[32];
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float* o = reinterpret_cast<const float*>(ov) + i;
-            const float4 v = some ? make_float4(o[0] * vs, o[1] * vs, o[2] * vs, o[3] * vs)
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
-            st_f32x4_hint(P + h * D + d0 + i, v, keep);
+          for (int i = 0; i < 32; ++i) ov[i] = 0u;
+          if (some) {
+            tc::ld32_async(tO + half * (D / 2) + d0, ov);
+            tc::wait_ld(ov);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float* o = reinterpret_cast<const float*>(ov) + 4 * i;
+            const uint4 v = make_uint4(__float_as_uint(o[0] * vs), __float_as_uint(o[1] * vs),
+                                       __float_as_uint(o[2] * vs), __float_as_uint(o[3] * vs));
+            sts_v4(staged(r, d0 / 4 + i), v);
           }
         }
+        __syncwarp();
+#pragma unroll 4
+        for (int i = 0; i < kCh; ++i) {
+          const int lr = i * kPer + sub_r, rr = wr0 + lr;
+          const int ur = u0 + rr;
+          const int p = static_cast<int>((ur * pair_mul) >> 16), h = ur - p * a.G;
+          uint32_t w[4];
+          lds_v4(staged(rr, ch), w[0], w[1], w[2], w[3]);
+          if ((valid_rows >> lr) & 1u)
+            st_f32x4_hint(P0 + static_cast<size_t>(p) * part_stride(a.G, D) + h * D + half * (D / 2) + 4 * ch,
+                          make_float4(__uint_as_float(w[0]), __uint_as_float(w[1]),
+                                      __uint_as_float(w[2]), __uint_as_float(w[3])),
+                          keep);
+        }
+        __syncwarp();
       }
       if (valid) {
-        st_f32_hint(P + a.G * D + h, some ? ms : kFloor, keep);
-        st_f32_hint(P + a.G * D + a.G + h, some ? l : 0.f, keep);
+        float* P = P0 + static_cast<size_t>(p_mine) * part_stride(a.G, D) + a.G * D + (ur_mine - p_mine * a.G);
+        st_f32_hint(P, some ? ms : kFloor, keep);
+        st_f32_hint(P + a.G, some ? l : 0.f, keep);
       }
     }
     if (!ok && lane == 0) atomicOr(a.err, PA_DEVERR_TIMEOUT);

@@ -16,15 +16,20 @@ constexpr int kWarps = kThreads / 32;
 constexpr unsigned kFull = 0xffffffffu;
 
 // Inclusive scan of x over the block with op (identity `zero`); *total
-// receives the whole block's value.
+// receives the whole block's value. one: only the first warp has values, and
+// only it calls.
 template <typename Op>
-__device__ __forceinline__ int block_scan(int x, int zero, Op op, int* total) {
+__device__ __forceinline__ int scan(bool one, int x, int zero, Op op, int* total) {
   __shared__ int s_w[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(kFull, x, o);
     if (lane >= o) x = op(x, y);
+  }
+  if (one) {
+    *total = __shfl_sync(kFull, x, 31);
+    return x;
   }
   if (lane == 31) s_w[warp] = x;
   __syncthreads();
@@ -47,39 +52,51 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const SharedPlanA
   int* s_in = s_pre + a.NG;      // [NG] rows that take part, then first flat tile
   int* s_first = s_in + a.NG;    // [NG] the first of them
   int* s_base = s_first + a.NG;  // [NG] first slot
+  __shared__ int s_wsz, s_tiles;
   const int tid = threadIdx.x;
   const int cap = a.MB * a.bs;
   const auto add = [](int x, int y) { return x + y; };
   const auto most = [](int x, int y) { return x > y ? x : y; };
+  // up to 31 groups: the scans below are the first warp's alone
+  const bool one = a.NG < 32;
+  const bool mine = !one || tid < 32;
+  const int step = one ? 32 : kThreads;
   griddep_launch_dependents();  // the prefix kernel sets itself up, then waits
   // The inputs are not the write path's: planning overlaps it. The workspace
   // it fills was last read by a kernel that an early-launching predecessor
   // has already waited for.
-  int run = 0, total;
-  for (int g0 = 0; g0 <= a.NG; g0 += kThreads) {
-    const int g = g0 + tid;
-    int x = 0;
-    bool bad = false;
-    if (g <= a.NG) {
-      const int s = a.group_starts[g];
-      x = min(max(s, 0), a.B);
-      bad = s != x;
-      if (g < a.NG) {
-        const int p = a.prefix_lens[g];
-        const int q = min(max(p, 0), cap);
-        bad = bad || p != q;
-        s_pre[g] = q / a.bs * a.bs;
-        s_in[g] = 0;
-        s_first[g] = a.B;
+  int len[4];  // this thread's first rows, in flight while the groups are set up
+#pragma unroll
+  for (int j = 0; j < 4; ++j) len[j] = tid + j * kThreads < a.B ? a.seq_lens[tid + j * kThreads] : 0;
+  auto length = [&](int b, int j) -> int { return min(max(j < 4 ? len[j] : a.seq_lens[b], 0), cap); };
+  int total;
+  if (mine) {
+    int run = 0;
+    for (int g0 = 0; g0 <= a.NG; g0 += step) {
+      const int g = g0 + tid;
+      int x = 0;
+      bool bad = false;
+      if (g <= a.NG) {
+        const int s = a.group_starts[g];
+        const int p = g < a.NG ? a.prefix_lens[g] : 0;
+        x = min(max(s, 0), a.B);
+        bad = s != x;
+        if (g < a.NG) {
+          const int q = min(max(p, 0), cap);
+          bad = bad || p != q;
+          s_pre[g] = q / a.bs * a.bs;
+          s_in[g] = 0;
+          s_first[g] = a.B;
+        }
       }
+      const int y = most(scan(one, x, 0, most, &total), run);
+      if (g <= a.NG) {
+        s_r0[g] = y;
+        bad = bad || y != x;
+      }
+      if (bad) atomicOr(a.err, PA_DEVERR_GROUP);
+      run = most(run, total);
     }
-    const int y = most(block_scan(x, 0, most, &total), run);
-    if (g <= a.NG) {
-      s_r0[g] = y;
-      bad = bad || y != x;
-    }
-    if (bad) atomicOr(a.err, PA_DEVERR_GROUP);
-    run = most(run, total);
   }
   __syncthreads();
   auto group_of = [&](int b) -> int {  // the group of row b, -1 for none
@@ -91,13 +108,12 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const SharedPlanA
     }
     return lo;
   };
-  auto takes_part = [&](int b, int g) -> bool {
-    const int L = min(max(a.seq_lens[b], 0), cap);
+  auto takes_part = [&](int L, int g) -> bool {
     return g >= 0 && s_pre[g] > 0 && L >= s_pre[g] && (a.window == 0 || L <= a.window);
   };
-  for (int b = tid; b < a.B; b += kThreads) {
+  for (int b = tid, j = 0; b < a.B; b += kThreads, ++j) {
     const int g = group_of(b);
-    if (takes_part(b, g)) {
+    if (takes_part(length(b, j), g)) {
       atomicAdd(&s_in[g], 1);
       atomicMin(&s_first[g], b);
     }
@@ -106,76 +122,96 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const SharedPlanA
 
   // units and flat tiles
   const int up_max = a.unit_rows / a.G;
-  SharedGroup* groups = reinterpret_cast<SharedGroup*>(a.plan + kSharedHead);
   auto units = [&](int g, int* nt, int* nut, int* up) {
     const int n = s_r0[g + 1] - s_r0[g];
     *nt = (s_pre[g] + a.kv - 1) / a.kv;
     *nut = n > 0 ? (n + up_max - 1) / up_max : 0;
     *up = n > 0 ? (n + *nut - 1) / *nut : 0;
   };
-  run = 0;
-  for (int g0 = 0; g0 < a.NG; g0 += kThreads) {
-    const int g = g0 + tid;
-    int x = 0, nt, nut, up;
-    if (g < a.NG) {
-      if (s_in[g] < 2) s_pre[g] = 0;  // one sequence reads its prefix once anyway
-      units(g, &nt, &nut, &up);
-      x = a.Hkv * nut * nt;
-    }
-    const int y = block_scan(x, 0, add, &total);
-    if (g < a.NG) s_in[g] = run + y - x;
-    run += total;
-  }
-  const int tiles = run;
-  const int wsz = max((tiles + a.grid - 1) / a.grid, a.min_tiles);
-  // slots
-  run = 0;
-  for (int g0 = 0; g0 < a.NG; g0 += kThreads) {
-    const int g = g0 + tid;
-    int x = 0, nt = 0, nut = 0, up = 0, sub = 1;
-    if (g < a.NG) {
-      units(g, &nt, &nut, &up);
-      if (nt > 0) {
-        const int f0 = s_in[g], f1 = f0 + a.Hkv * nut * nt;
-        sub = a.halves && up * a.G <= a.unit_rows / 2 ? 2 : 1;
-        x = (a.Hkv * nut + (f1 - 1) / wsz - f0 / wsz) * up * sub;
+  auto sub_of = [&](int up) -> int { return a.halves && up * a.G <= a.unit_rows / 2 ? 2 : 1; };
+  if (mine) {
+    int run = 0;
+    for (int g0 = 0; g0 < a.NG; g0 += step) {
+      const int g = g0 + tid;
+      int x = 0, nt, nut, up;
+      if (g < a.NG) {
+        if (s_in[g] < 2) s_pre[g] = 0;  // one sequence reads its prefix once anyway
+        units(g, &nt, &nut, &up);
+        x = a.Hkv * nut * nt;
       }
+      const int y = scan(one, x, 0, add, &total);
+      if (g < a.NG) s_in[g] = run + y - x;
+      run += total;
     }
-    const int y = block_scan(x, 0, add, &total);
-    if (g < a.NG) {
-      s_base[g] = run + y - x;
-      SharedGroup r;
-      r.r0 = s_r0[g];
-      r.n = s_r0[g + 1] - s_r0[g];
-      r.table_row = s_first[g];
-      r.prefix = s_pre[g];
-      r.f0 = s_in[g];
-      r.nt = nt;
-      r.nut = nut;
-      r.up = up;
-      r.base = run + y - x;
-      r.sub = sub;
-      r.wfirst = s_in[g] / wsz;
-      r.pad = 0;
-      groups[g] = r;
+    const int tiles = run;
+    const int wsz = max((tiles + a.ctas - 1) / a.ctas, a.min_tiles);
+    if (tid == 0) {
+      s_tiles = tiles;
+      s_wsz = wsz;
+      a.plan[kShTotal] = tiles;
+      a.plan[kShWsz] = wsz;
     }
-    run += total;
-  }
-  if (tid == 0) {
-    a.plan[kShTotal] = tiles;
-    a.plan[kShWsz] = wsz;
+    // slots
+    run = 0;
+    for (int g0 = 0; g0 < a.NG; g0 += step) {
+      const int g = g0 + tid;
+      int x = 0, nt = 0, nut = 0, up = 0;
+      if (g < a.NG) {
+        units(g, &nt, &nut, &up);
+        if (nt > 0) {
+          const int first = s_in[g], last = first + a.Hkv * nut * nt - 1;
+          x = (a.Hkv * nut + last / wsz - first / wsz) * up * sub_of(up);
+        }
+      }
+      const int y = scan(one, x, 0, add, &total);
+      if (g < a.NG) s_base[g] = run + y - x;
+      run += total;
+    }
   }
   __syncthreads();
-  SharedRow* rows = reinterpret_cast<SharedRow*>(a.plan + kSharedHead + 12 * a.NG);
-  for (int b = tid; b < a.B; b += kThreads) {
+  const int wsz = s_wsz, tiles = s_tiles;
+  auto record = [&](int g) -> SharedGroup {
+    SharedGroup r = {};
+    if (g >= a.NG) return r;
+    units(g, &r.nt, &r.nut, &r.up);
+    r.r0 = s_r0[g];
+    r.n = s_r0[g + 1] - s_r0[g];
+    r.table_row = s_first[g];
+    r.prefix = s_pre[g];
+    r.f0 = s_in[g];
+    r.base = s_base[g];
+    r.sub = sub_of(r.up);
+    r.wfirst = s_in[g] / wsz;
+    return r;
+  };
+  SharedGroup* groups = const_cast<SharedGroup*>(shared_groups(a.plan, a.ctas));
+  for (int g = tid; g < a.NG; g += kThreads) groups[g] = record(g);
+  SharedCta* ctas = const_cast<SharedCta*>(shared_ctas(a.plan));
+  for (int w = tid; w < a.ctas; w += kThreads) {
+    SharedCta c;
+    c.f0 = static_cast<int>(min(static_cast<long long>(w) * wsz, static_cast<long long>(tiles)));
+    c.f1 = min(c.f0 + wsz, tiles);
+    // the last group that starts at or before f0: those without tiles share
+    // their start with the next one
+    int lo = 0, hi = a.NG;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_in[mid] <= c.f0) lo = mid; else hi = mid;
+    }
+    c.group = lo;
+    c.pad = 0;
+    c.g = record(lo);
+    ctas[w] = c;
+  }
+  SharedRow* rows = const_cast<SharedRow*>(shared_rows(a.plan, a.ctas, a.NG));
+  for (int b = tid, j = 0; b < a.B; b += kThreads, ++j) {
     const int g = group_of(b);
-    const int L = min(max(a.seq_lens[b], 0), cap);
+    const int L = length(b, j);
     SharedRow r = {a.window > 0 && L > a.window ? L - a.window : 0, 0, 0, 0, 0, 0, 0, 0};
-    if (takes_part(b, g)) {
+    if (takes_part(L, g)) {
       int nt, nut, up;
       units(g, &nt, &nut, &up);
-      const int i = b - s_r0[g], ut = i / up;
-      const int sub = a.halves && up * a.G <= a.unit_rows / 2 ? 2 : 1;
+      const int i = b - s_r0[g], ut = i / up, sub = sub_of(up);
       r.start = s_pre[g];
       r.nt = nt;
       r.f0 = s_in[g] + ut * nt;

@@ -42,6 +42,13 @@ struct SharedGroup {  // 12 words a group
   int pad;
 };
 
+struct SharedCta {  // 16 words a CTA of the prefix kernel
+  int f0, f1;   // its flat tiles
+  int group;    // the group of f0
+  int pad;
+  SharedGroup g;  // that group, so that a CTA starts on one load
+};
+
 struct SharedRow {  // 8 words a sequence
   int start;        // first position the decode kernel covers
   int nt;           // K/V tiles of its prefix, 0: no part of it here
@@ -53,14 +60,20 @@ struct SharedRow {  // 8 words a sequence
   int nut_sub;      // nut << 2 | sub
 };
 
-__host__ __device__ constexpr inline size_t shared_plan_words(int64_t B, int64_t NG) {
-  return kSharedHead + 12 * static_cast<size_t>(NG) + 8 * static_cast<size_t>(B);
+// Words of the plan: header, CTAs, groups, rows.
+__host__ __device__ constexpr inline size_t shared_plan_words(int64_t B, int64_t NG, int ctas) {
+  return kSharedHead + 16 * static_cast<size_t>(ctas) + 12 * static_cast<size_t>(NG) +
+         8 * static_cast<size_t>(B);
 }
-__device__ __forceinline__ const SharedGroup* shared_groups(const int32_t* plan) {
-  return reinterpret_cast<const SharedGroup*>(plan + kSharedHead);
+__host__ __device__ __forceinline__ const SharedCta* shared_ctas(const int32_t* plan) {
+  return reinterpret_cast<const SharedCta*>(plan + kSharedHead);
 }
-__device__ __forceinline__ const SharedRow* shared_rows(const int32_t* plan, int NG) {
-  return reinterpret_cast<const SharedRow*>(plan + kSharedHead + 12 * NG);
+__host__ __device__ __forceinline__ const SharedGroup* shared_groups(const int32_t* plan, int ctas) {
+  return reinterpret_cast<const SharedGroup*>(plan + kSharedHead + 16 * ctas);
+}
+__host__ __device__ __forceinline__ const SharedRow* shared_rows(const int32_t* plan, int ctas,
+                                                                 int NG) {
+  return reinterpret_cast<const SharedRow*>(plan + kSharedHead + 16 * ctas + 12 * NG);
 }
 
 }  // namespace pa

@@ -87,7 +87,7 @@ struct SharedPlanArgs {
   int B, NG, MB, bs, Hkv, G, window;
   int kv, unit_rows;             // tokens a K/V tile, rows a unit
   bool halves;                   // small units are computed in two halves
-  int grid;                      // CTAs of the prefix kernel
+  int ctas;                      // of the prefix kernel
   int min_tiles;                 // least K/V tiles a CTA
 };
 cudaError_t shared_plan_launch(const SharedPlanArgs& a, cudaStream_t s, bool pdl);
@@ -98,6 +98,7 @@ struct PrefixArgs {
   const int32_t* plan;           // written by the plan kernel
   float* part;                   // first prefix partial
   int32_t* err;
+  int ctas;                      // the grid, which the plan's layout depends on
   int NG, Hq, Hkv, G, bs, MB, NB;
   float score_scale;             // scale * log2(e) (* k_scale for FP8)
   float v_scale;                 // FP8: applied to the partial outputs
@@ -111,5 +112,17 @@ struct PrefixShape {
 PrefixShape prefix_shape(int D);
 cudaError_t prefix_launch(int qt, bool fp8, int D, const CUtensorMap& tk, const CUtensorMap& tv,
                           const PrefixArgs& a, int grid, cudaStream_t s, bool pdl);
+
+// Joins the decode kernel's partials and the prefix kernel's (shared_merge.cu).
+struct SharedMergeArgs {
+  void* out;                     // [B, Hq, D]
+  const float* part;             // all partials, the decode kernel's first
+  const int32_t* plan;           // the decode kernel's plan
+  const int32_t* shared;         // the shared plan
+  uint32_t* pool;                // zero again for the next step
+  int B, Hkv, G, D, NW, NG, ctas;
+  int part0;                     // first slot of the prefix partials
+};
+cudaError_t shared_merge_launch(int out_type, const SharedMergeArgs& a, cudaStream_t s, bool pdl);
 
 }  // namespace pa
