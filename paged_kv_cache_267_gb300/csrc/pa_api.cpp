@@ -12,6 +12,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <cstdlib>
 #include <initializer_list>
 #include <map>
 #include <mutex>
@@ -916,6 +917,7 @@ pa_status run_decode(const DecodeCall& c, DeviceState* st, const DecodePlan& pla
     p.unit_rows = shape.unit_rows;
     p.halves = shape.halves;
     p.ctas = grid;
+    p.active = getenv("PA_X1") ? atoi(getenv("PA_X1")) : grid;
     p.min_tiles = kPrefixMinTiles;
     e = pa::shared_plan_launch(p, cs, !prof);
     if (e != cudaSuccess) return cuda_fail(e, "shared plan launch");

@@ -37,8 +37,8 @@
 // 100,000.
 //
 // FP8 caches: two converter warps, half of the rows each, turn each raw e4m3
-// tile into the f16 tile the products read (exact), K first: the next S waits
-// for it; Q is rescaled per row by a power of two to f16's range, which
+// tile into the f16 tile the products read (exact), in two buffers each for K
+// and V, so that a tile is converted while the one before is multiplied; Q is rescaled per row by a power of two to f16's range, which
 // the row's score scale undoes.
 #include "attn_tc.cuh"
 #include "pa_internal.h"
@@ -60,13 +60,13 @@ constexpr float kRescaleAbove = 8.f;         // log2 units
 constexpr unsigned kFull = 0xffffffffu;
 
 // barriers: K and V rings (full, empty; up to kMaxStages each); per group x: S_x
-// computed, P_x written, O_x product complete, Q_x staged; FP8: converted K
-// written / read, converted V (two buffers) written / read
+// computed, P_x written, O_x product complete; all rows' Q staged; both groups at
+// a segment's end; FP8: converted K and V (two buffers each) written / read
 constexpr int kMaxStages = 4;
 constexpr int kBarKFull = 0, kBarKEmpty = kBarKFull + kMaxStages, kBarVFull = kBarKEmpty + kMaxStages,
               kBarVEmpty = kBarVFull + kMaxStages, kBarS = kBarVEmpty + kMaxStages,
-              kBarP = kBarS + 2, kBarO = kBarP + 2, kBarQ = kBarO + 2, kBarCKFull = kBarQ + 2,
-              kBarCKFree = kBarCKFull + 1, kBarCVFull = kBarCKFree + 1, kBarCVFree = kBarCVFull + 2,
+              kBarP = kBarS + 2, kBarO = kBarP + 2, kBarQ = kBarO + 2, kBarEnd = kBarQ + 1, kBarCKFull = kBarEnd + 1,
+              kBarCKFree = kBarCKFull + 2, kBarCVFull = kBarCKFree + 2, kBarCVFree = kBarCVFull + 2,
               kNumBars = kBarCVFree + 2;
 
 // Stage and phase of a ring position.
@@ -91,7 +91,7 @@ struct Cfg {
   // through a softmax, a K stage only through its product, and in one warp K
   // loads would wait behind V's
   static constexpr int kLoadWarps = FP8 ? 1 : 2;
-  static constexpr int kKStages = FP8 ? 2 : (D == 64 ? 4 : 2), kVStages = FP8 ? 2 : (D == 64 ? 4 : 3);
+  static constexpr int kKStages = FP8 ? 1 : (D == 64 ? 4 : 2), kVStages = FP8 ? 1 : (D == 64 ? 4 : 3);
   static constexpr int kMmaWarp = 4 * kGroups, kLoadWarp = kMmaWarp + 1,
                        kConvWarp0 = kLoadWarp + kLoadWarps;
   static constexpr int kThreads = (kConvWarp0 + (FP8 ? kConv : 0)) * 32;
@@ -100,7 +100,7 @@ struct Cfg {
   static constexpr uint32_t kRawBoxes = FP8 ? D / 128 : kBoxes;             // 128-byte boxes
   static constexpr uint32_t kRing = kRawBoxes * kBox;                       // ring tile
   static constexpr uint32_t kQ = 0, kK = kQ + kGroups * kQBytes, kV = kK + kKStages * kRing;
-  static constexpr uint32_t kKc = kV + kVStages * kRing, kVc = kKc + (FP8 ? kTile : 0);
+  static constexpr uint32_t kKc = kV + kVStages * kRing, kVc = kKc + (FP8 ? 2 * kTile : 0);
   static constexpr uint32_t kBar = kVc + (FP8 ? 2 * kTile : 0);
   static constexpr uint32_t kSlot = kBar + 8 * kNumBars;
   static constexpr uint32_t kBytes = kSlot + 16 + 1024;  // + room to align the base to 1 KB
@@ -128,15 +128,31 @@ __device__ __forceinline__ void segment_at(const PrefixArgs& a, int f, int f_end
                                            Segment* s) {
   while (f >= s->g.f0 + a.Hkv * s->g.nut * s->g.nt && *gi + 1 < a.NG)
     s->g = shared_groups(a.plan, a.ctas)[++*gi];
-  const int rem = f - s->g.f0, unit = rem / s->g.nt;
+  const int rem = f - s->g.f0, unit = rem < s->g.nt ? 0 : rem / s->g.nt;
   s->t0 = rem - unit * s->g.nt;
   s->nt = min(s->g.nt - s->t0, f_end - f);
-  s->kvh = unit / s->g.nut;
+  s->kvh = s->g.nut == 1 ? unit : unit / s->g.nut;
   s->ut = unit - s->kvh * s->g.nut;
   s->b0 = s->g.r0 + s->ut * s->g.up;
   s->np = min(s->g.up, s->g.n - s->ut * s->g.up);
-  s->dual = s->g.sub == 1;
-  s->slot0 = s->g.base + (unit + static_cast<int>(blockIdx.x) - s->g.wfirst) * s->g.sub * s->g.up;
+  s->dual = s->g.dual != 0;
+  s->slot0 = s->g.base + (unit + static_cast<int>(blockIdx.x) - s->g.wfirst) * s->g.up;
+}
+
+// Two 32-bit columns of this thread's tensor-memory lane.
+__device__ __forceinline__ void st2(uint32_t taddr, float a, float b) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(taddr), "f"(a), "f"(b)
+               : "memory");
+}
+__device__ __forceinline__ float2 ld2(uint32_t taddr) {
+  float a, b;
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(a), "=f"(b)
+      : "r"(taddr)
+      : "memory");
+  return make_float2(a, b);
 }
 
 template <int QT>
@@ -175,12 +191,13 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       mbar_init(bar(kBarS + i), 1);
       mbar_init(bar(kBarP + i), kGroupThreads);
       mbar_init(bar(kBarO + i), 1);
-      mbar_init(bar(kBarQ + i), kGroupThreads);
+      mbar_init(bar(kBarCKFull + i), kConv * 32);
+      mbar_init(bar(kBarCKFree + i), 1);
       mbar_init(bar(kBarCVFull + i), kConv * 32);
       mbar_init(bar(kBarCVFree + i), 1);
     }
-    mbar_init(bar(kBarCKFull), kConv * 32);
-    mbar_init(bar(kBarCKFree), 1);
+    mbar_init(bar(kBarQ), NX * kGroupThreads);
+    mbar_init(bar(kBarEnd), NX * kGroupThreads);
     fence_mbar_init();
   }
   if (warp == 0) tc::tmem_alloc(base + C::kSlot, kTmemCols);
@@ -253,85 +270,98 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     if (!ok && lane == 0) atomicOr(a.err, PA_DEVERR_TIMEOUT);
   } else if (warp == C::kMmaWarp) {
     // ------------------------------------------------------------ MMA issue
-    // One thread does all of it: its own instructions are on the critical
-    // path of every tile, and waits and votes of a whole warp cost about 150
-    // cycles each even when there is nothing to wait for.
+    // One thread does all of it, and little besides: its own instructions are
+    // on the critical path of every tile (a wait by the whole warp costs about
+    // 150 cycles even when there is nothing to wait for, the products of one
+    // tile and group about 1,200).
     if (lane == 0) {
       constexpr uint32_t idS = tc::idesc_f16(kRows, C::kKv, kBf16, false);
       constexpr uint32_t idO = tc::idesc_f16(kRows, D, kBf16, true);
       // Positions of the K and V tiles in use, and the barriers that say they
-      // are ready: the ring's, or the converted buffers' (one of K, two of V).
-      constexpr int KB = FP8 ? 1 : C::kKStages, VB = FP8 ? 2 : C::kVStages;
+      // are ready: the ring's, or the converted buffers' (two of each).
+      constexpr int KB = FP8 ? 2 : C::kKStages, VB = FP8 ? 2 : C::kVStages;
+      constexpr int kKReady = FP8 ? kBarCKFull : kBarKFull, kKFree = FP8 ? kBarCKFree : kBarKEmpty;
+      constexpr int kVReady = FP8 ? kBarCVFull : kBarVFull, kVFree = FP8 ? kBarCVFree : kBarVEmpty;
+      const uint64_t dQ = tc::sdesc_sw128(sQ, 16, 1024);
+      const uint64_t dK = tc::sdesc_sw128(FP8 ? sKc : sK, 16, 1024);
+      const uint64_t dV = tc::sdesc_sw128(FP8 ? sVc : sV, C::kBox, 1024);
       Ring kr, vr;
-      int kc = 0, vc = 0;  // tiles of K, V the products are done with
+      // releases still to come: one is committed only when something will wait
+      // for it, so that no arrive outlives the CTA
+      int k_free = ntiles - KB, v_free = ntiles - VB;
       auto wait = [&](uint32_t b, uint32_t parity) { return mbar_wait_bounded(b, parity, kWaitNs); };
-      auto issue_s = [&](int x) {
-        const uint64_t dQ = tc::sdesc_sw128(sQ + x * C::kQBytes, 16, 1024);
-        const uint64_t dK = tc::sdesc_sw128((FP8 ? sKc : sK) + kr.stage * C::kTile, 16, 1024);
+      auto issue_s = [&](int x, bool last) {
 #pragma unroll
         for (int box = 0; box < C::kBoxes; ++box)
-          mma4_ss(tmem + C::kColS + C::kKv * x, dQ + box * (C::kQBox >> 4),
-                  dK + box * (C::kBox >> 4), idS, box > 0);
+          mma4_ss(tmem + C::kColS + C::kKv * x, dQ + ((x * C::kQBytes + box * C::kQBox) >> 4),
+                  dK + ((kr.stage * C::kTile + box * C::kBox) >> 4), idS, box > 0);
         tc::commit(bar(kBarS + x));
+        if (last) {
+          if (k_free-- > 0) tc::commit(bar(kKFree + kr.stage));
+          kr.next(KB);
+        }
       };
       // O_x (+)= P_x V: 16 tokens a step, P in 8 columns each from 64 h on
-      auto issue_o = [&](int x, bool first) {
-        const uint64_t dV = tc::sdesc_sw128((FP8 ? sVc : sV) + vr.stage * C::kTile, C::kBox, 1024);
+      auto issue_o = [&](int x, bool first, bool last) {
 #pragma unroll
         for (int h = 0; h < C::kKv / 64; ++h)
-          mma4_ts(tmem + C::kColO + D * x, tmem + C::kColS + C::kKv * x + 64 * h, dV + 512 * h, idO,
-                  !first || h > 0);
+          mma4_ts(tmem + C::kColO + D * x, tmem + C::kColS + C::kKv * x + 64 * h,
+                  dV + ((vr.stage * C::kTile) >> 4) + 512 * h, idO, !first || h > 0);
         tc::commit(bar(kBarO + x));
-      };
-      // A release is committed only when something will wait for it, so no
-      // arrive outlives the CTA.
-      auto release_k = [&]() {
-        if (kc + KB < ntiles) tc::commit(bar(FP8 ? kBarCKFree : kBarKEmpty + kr.stage));
-        ++kc;
-        kr.next(KB);
-      };
-      auto release_v = [&]() {
-        if (vc + VB < ntiles) tc::commit(bar((FP8 ? kBarCVFree : kBarVEmpty) + vr.stage));
-        ++vc;
-        vr.next(VB);
-      };
-      auto wait_k = [&]() { return wait(bar(FP8 ? kBarCKFull : kBarKFull + kr.stage), kr.phase); };
-      auto wait_v = [&]() { return wait(bar((FP8 ? kBarCVFull : kBarVFull) + vr.stage), vr.phase); };
-      bool ok = true;
-      int ops[2] = {0, 0};   // products O_x issued so far
-      int segs[2] = {0, 0};  // segments of each group so far (those it has tiles of)
-      for (int f = f0; ok && f < f1; f += sg.nt) {
-        segment_at(a, f, f1, &gi, &sg);
-        // the i-th S (and O) product of the segment: group i % NX, tile i / NX
-        // (its own rows) or i (its own tiles)
-        const bool dual = NX == 2 && sg.dual;
-        const int nops = dual ? 2 * sg.nt : sg.nt;
-        auto x_of = [&](int i) -> int { return NX == 2 ? i & 1 : 0; };
-        auto first_use = [&](int i) -> bool { return !dual || !(i & 1); };
-        auto last_use = [&](int i) -> bool { return !dual || (i & 1); };
-        for (int i = 0; i < NX && i < nops; ++i) {
-          if (!(ok = wait(bar(kBarQ + i), segs[i]++ & 1))) break;
-          if (first_use(i) && !(ok = wait_k())) break;
-          tc::fence_after_sync();
-          issue_s(x_of(i));
-          if (last_use(i)) release_k();
+        if (last) {
+          if (v_free-- > 0) tc::commit(bar(kVFree + vr.stage));
+          vr.next(VB);
         }
-        for (int i = 0; ok && i < nops; ++i) {
-          const int x = x_of(i);
-          const uint32_t par = ops[x] & 1;
-          if (first_use(i) && !(ok = wait_v())) break;
-          if (!(ok = wait(bar(kBarP + x), par))) break;  // P_x (and clean V rows) written
+      };
+      bool ok = true;
+      uint32_t par[2] = {0, 0};  // phase of each group's next product
+      // Group x's products on one tile: O, and S of its next tile if there is
+      // one. first_use, last_use: of the tile's V (and the next one's K).
+      auto step = [&](int x, bool first, bool more, bool first_use, bool last_use) {
+        // P_x (and clean V rows) written, V there; both tested before either is
+        // waited for
+        const bool v_in = !first_use || mbar_try_wait(bar(kVReady + vr.stage), vr.phase);
+        const bool p_in = mbar_try_wait(bar(kBarP + x), par[x]);
+        if (!p_in && !(ok = wait(bar(kBarP + x), par[x]))) return;
+        if (!v_in && !(ok = wait(bar(kVReady + vr.stage), vr.phase))) return;
+        tc::fence_after_sync();
+        issue_o(x, first, last_use);
+        if (more) {
+          const bool k_in = !first_use || mbar_try_wait(bar(kKReady + kr.stage), kr.phase);
+          if (!(ok = wait(bar(kBarO + x), par[x]))) return;  // P_x consumed
+          if (!k_in && !(ok = wait(bar(kKReady + kr.stage), kr.phase))) return;
           tc::fence_after_sync();
-          issue_o(x, i < NX);
-          ++ops[x];
-          if (last_use(i)) release_v();
-          if (i + NX < nops) {
-            if (first_use(i + NX) && !(ok = wait_k())) break;
-            if (!(ok = wait(bar(kBarO + x), par))) break;  // P_x consumed
-            tc::fence_after_sync();
-            issue_s(x);
-            if (last_use(i + NX)) release_k();
+          issue_s(x, last_use);
+        }
+        par[x] ^= 1;
+      };
+      uint32_t seg = 0;
+      for (int f = f0; ok && f < f1; f += sg.nt, seg ^= 1) {
+        segment_at(a, f, f1, &gi, &sg);
+        if (!(ok = wait(bar(kBarQ), seg))) break;
+        if (!(ok = wait(bar(kKReady + kr.stage), kr.phase))) break;
+        tc::fence_after_sync();
+        if (NX == 2 && sg.dual) {  // both groups on every tile
+          issue_s(0, false);
+          issue_s(1, true);
+          for (int n = 0; ok && n < sg.nt; ++n) {
+            step(0, n == 0, n + 1 < sg.nt, true, false);
+            if (ok) step(1, n == 0, n + 1 < sg.nt, false, true);
           }
+        } else if (NX == 2) {  // the groups on alternate tiles
+          issue_s(0, true);
+          if (sg.nt > 1) {
+            if (!(ok = wait(bar(kKReady + kr.stage), kr.phase))) break;
+            tc::fence_after_sync();
+            issue_s(1, true);
+          }
+          for (int n = 0; ok && n < sg.nt; n += 2) {
+            step(0, n == 0, n + 2 < sg.nt, true, true);
+            if (ok && n + 1 < sg.nt) step(1, n == 0, n + 3 < sg.nt, true, true);
+          }
+        } else {
+          issue_s(0, true);
+          for (int n = 0; ok && n < sg.nt; ++n) step(0, n == 0, n + 1 < sg.nt, true, true);
         }
       }
       if (!ok) atomicOr(a.err, PA_DEVERR_TIMEOUT);
@@ -376,23 +406,21 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       };
       bool ok = true;
       int c = 0;
-      Ring in;
       for (int f = f0; ok && f < f1; f += sg.nt) {
         segment_at(a, f, f1, &gi, &sg);
         for (int n = 0; ok && n < sg.nt; ++n, ++c) {
           const int lim = sg.g.prefix - (sg.t0 + n) * C::kKv;  // rows of the tile inside the prefix
-          // K, once the products of the tile before have read its buffer
-          if (!(ok = wait_all(bar(kBarKFull + in.stage), in.phase))) break;
-          if (c > 0 && !(ok = wait_all(bar(kBarCKFree), (c - 1) & 1))) break;
-          convert(sK + in.stage * C::kRing, sKc);
+          const uint32_t free_par = ((c - 2) >> 1) & 1;  // of the buffers' last tile
+          if (!(ok = wait_all(bar(kBarKFull), c & 1))) break;
+          if (c > 1 && !(ok = wait_all(bar(kBarCKFree + (c & 1)), free_par))) break;
+          convert(sK, sKc + (c & 1) * C::kTile);
           fence_proxy_async();  // the f16 tile, visible to the tensor core
-          mbar_arrive(bar(kBarCKFull));
-          mbar_arrive(bar(kBarKEmpty + in.stage));  // reload the stage
-          // V, into the buffer of two tiles before
+          mbar_arrive(bar(kBarCKFull + (c & 1)));
+          mbar_arrive(bar(kBarKEmpty));  // reload the stage
           const uint32_t vt = sVc + (c & 1) * C::kTile;
-          if (!(ok = wait_all(bar(kBarVFull + in.stage), in.phase))) break;
-          if (c > 1 && !(ok = wait_all(bar(kBarCVFree + (c & 1)), ((c - 2) >> 1) & 1))) break;
-          convert(sV + in.stage * C::kRing, vt);
+          if (!(ok = wait_all(bar(kBarVFull), c & 1))) break;
+          if (c > 1 && !(ok = wait_all(bar(kBarCVFree + (c & 1)), free_par))) break;
+          convert(sV, vt);
           if (lim < C::kKv) {
             __syncwarp();
             for (int i = max(lim, row0) * 8 + lane; i < (row0 + kOctets * 8) * 8; i += 32)
@@ -402,8 +430,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           }
           fence_proxy_async();
           mbar_arrive(bar(kBarCVFull + (c & 1)));
-          mbar_arrive(bar(kBarVEmpty + in.stage));
-          in.next(2);
+          mbar_arrive(bar(kBarVEmpty));
         }
       }
       if (!ok && lane == 0) atomicOr(a.err, PA_DEVERR_TIMEOUT);
@@ -423,15 +450,14 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     const uint32_t pair_mul = (65536u + a.G - 1) / a.G;  // row / G = row * mul >> 16, rows < 256
     bool ok = true;
     int c0 = 0, op = 0;  // products of this group so far
-    for (int f = f0; ok && f < f1; f += sg.nt, c0 += sg.nt) {
+    uint32_t seg = 0;    // phase of the segment
+    for (int f = f0; ok && f < f1; f += sg.nt, c0 += sg.nt, seg ^= 1) {
       segment_at(a, f, f1, &gi, &sg);
       const bool dual = NX == 2 && sg.dual;
       const int nj = dual || NX == 1 ? sg.nt : (sg.nt - x + 1) >> 1;  // this group's tiles
       const int u0 = dual ? x * kRows : 0;  // row of the unit (pair * G + head) at row 0 here
       float sc = fabsf(a.score_scale);
-      // A group without tiles in a segment (the second half of a single tile)
-      // stages no Q: with nothing to wait for it would run ahead of the barrier.
-      if (nj > 0) {  // Q rows -> shared memory (K-major, 128-byte swizzle)
+      {  // Q rows -> shared memory (K-major, 128-byte swizzle)
         const uint32_t flip = a.score_scale < 0.f ? 0x80008000u : 0u;
         const uint32_t q_tile = sQ + x * C::kQBytes + (ch >> 3) * C::kQBox;
         int sh_mine = 0;
@@ -466,10 +492,17 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                 frexpf(amax, &e);
                 sh = e - 15;
               }
+              // 2^-sh in two factors, each a normal number: sh is in [-163, 113]
+              const int s1 = sh / 2, s2 = sh - s1;
+              const float2 m1 = make_float2(__int_as_float((127 - s1) << 23), __int_as_float((127 - s1) << 23));
+              const float2 m2 = make_float2(__int_as_float((127 - s2) << 23), __int_as_float((127 - s2) << 23));
               uint32_t o4[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                o4[e] = pack16x2<false>(ldexpf(f32_of<QT>(w4[e], 0), -sh), ldexpf(f32_of<QT>(w4[e], 1), -sh));
+              for (int e = 0; e < 4; ++e) {
+                const float2 t = __fmul2_rn(
+                    __fmul2_rn(make_float2(f32_of<QT>(w4[e], 0), f32_of<QT>(w4[e], 1)), m1), m2);
+                o4[e] = pack16x2<false>(t.x, t.y);
+              }
               v[i] = make_uint4(o4[0], o4[1], o4[2], o4[3]);
               // to the lane that owns the row
               const int theirs = __shfl_sync(kFull, sh, (lane % kPer) * kCh);
@@ -482,7 +515,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         if constexpr (FP8) sc = ldexpf(sc, sh_mine);
         fence_proxy_async();
         tc::fence_before_sync();  // the last segment's O has been read
-        mbar_arrive(bar(kBarQ + x));
+        mbar_arrive(bar(kBarQ));
       }
       float ms = kFloor, l = 0.f;  // reference max (scaled, log2 units) and running sum
       for (int j = 0; j < nj; ++j, ++op) {
@@ -594,41 +627,73 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         tc::fence_before_sync();
         mbar_arrive(bar(kBarP + x));
       }
-      // The partials of these rows: O as it is, its reference max and sum. O goes
-      // through the Q buffer in two halves of the head dim.
+      // The partials of these rows: O, its reference max and sum. They go out
+      // through the Q buffer in two halves of the head dim: with its own rows, a
+      // group stores both; where both groups have the same rows, each joins one
+      // half of the two O (m = max(m0, m1), O = sum of 2^(mx - m) Ox, l alike)
+      // and stores it.
+      if (ok && nj > 0) ok = wait_all(bar(kBarO + x), (op - 1) & 1);
+      const bool join = NX == 2 && !dual;
+      float f_own = 1.f, f_other = 0.f;
+      if (join) {
+        // the same row is the same tensor-memory lane in both groups: m and l
+        // change hands in columns of S, which is done with
+        st2(tS, ok ? ms : kFloor, ok ? l : 0.f);
+        tc::wait_st();
+        tc::fence_before_sync();
+        mbar_arrive(bar(kBarEnd));
+        ok = wait_all(bar(kBarEnd), seg) && ok;
+        tc::fence_after_sync();
+        const float2 o = ld2(trow + C::kColS + C::kKv * (1 - x));
+        const float m = fmaxf(ms, o.x);
+        f_own = nj > 0 ? ex2(ms - m) : 0.f;
+        f_other = x == 1 || sg.nt > 1 ? ex2(o.x - m) : 0.f;  // a lone tile is group 0's
+        l = l * f_own + o.y * f_other;
+        ms = m;
+      } else if (NX == 2) {
+        mbar_arrive(bar(kBarEnd));  // keeps the phases of both kinds of segment in step
+        ok = wait_all(bar(kBarEnd), seg) && ok;
+      }
+      tc::fence_after_sync();
       const int ur_mine = u0 + r, p_mine = static_cast<int>((ur_mine * pair_mul) >> 16);
       const bool valid = p_mine < sg.np && rows[sg.b0 + min(p_mine, sg.np - 1)].nt > 0;
       const unsigned valid_rows = __ballot_sync(kFull, valid);
-      if (ok && nj > 0) ok = wait_all(bar(kBarO + x), (op - 1) & 1);
-      tc::fence_after_sync();
-      const bool some = ok && nj > 0;
-      float* const P0 =
-          a.part + static_cast<size_t>(sg.slot0 + (dual || NX == 1 ? 0 : x * sg.g.up)) * part_stride(a.G, D);
+      const int stride = part_stride(a.G, D);
+      float* const P0 = a.part + static_cast<size_t>(sg.slot0) * stride;
       const uint64_t keep = l2_evict_last();  // the merge reads them soon
       // 16-byte chunk c of row r, where the row's own Q was: no warp touches
       // another's rows
       auto staged = [&](int row, int c) -> uint32_t {
         return sQ + x * C::kQBytes + (c >> 3) * C::kQBox + row * 128 + (((c & 7) ^ (row & 7)) << 4);
       };
-      const float vs = some ? a.v_scale : 0.f;
+      if (!ok) f_own = f_other = 0.f;
+      f_own *= a.v_scale;
+      f_other *= a.v_scale;
 #pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
+      for (int half = join ? x : 0; half < (join ? x + 1 : 2); ++half) {
 #pragma unroll 1
         for (int d0 = 0; d0 < D / 2; d0 += 32) {
           uint32_t ov[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) ov[i] = 0u;
-          if (some) {
+          if (f_own != 0.f || __any_sync(kFull, f_own != 0.f)) {
             tc::ld32_async(tO + half * (D / 2) + d0, ov);
             tc::wait_ld(ov);
           }
+          float* o = reinterpret_cast<float*>(ov);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float* o = reinterpret_cast<const float*>(ov) + 4 * i;
-            const uint4 v = make_uint4(__float_as_uint(o[0] * vs), __float_as_uint(o[1] * vs),
-                                       __float_as_uint(o[2] * vs), __float_as_uint(o[3] * vs));
-            sts_v4(staged(r, d0 / 4 + i), v);
+          for (int i = 0; i < 32; ++i) o[i] = f_own != 0.f ? o[i] * f_own : 0.f;
+          if (join && __any_sync(kFull, f_other != 0.f)) {
+            uint32_t ow[32];
+            tc::ld32_async(trow + C::kColO + D * (1 - x) + half * (D / 2) + d0, ow);
+            tc::wait_ld(ow);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              o[i] = f_other != 0.f ? fmaf(__uint_as_float(ow[i]), f_other, o[i]) : o[i];
           }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            sts_v4(staged(r, d0 / 4 + i), make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]));
         }
         __syncwarp();
 #pragma unroll 4
@@ -639,17 +704,17 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           uint32_t w[4];
           lds_v4(staged(rr, ch), w[0], w[1], w[2], w[3]);
           if ((valid_rows >> lr) & 1u)
-            st_f32x4_hint(P0 + static_cast<size_t>(p) * part_stride(a.G, D) + h * D + half * (D / 2) + 4 * ch,
+            st_f32x4_hint(P0 + (p * stride + h * D + half * (D / 2) + 4 * ch),
                           make_float4(__uint_as_float(w[0]), __uint_as_float(w[1]),
                                       __uint_as_float(w[2]), __uint_as_float(w[3])),
                           keep);
         }
         __syncwarp();
       }
-      if (valid) {
-        float* P = P0 + static_cast<size_t>(p_mine) * part_stride(a.G, D) + a.G * D + (ur_mine - p_mine * a.G);
-        st_f32_hint(P, some ? ms : kFloor, keep);
-        st_f32_hint(P + a.G, some ? l : 0.f, keep);
+      if (valid && !(join && x == 1)) {
+        float* P = P0 + p_mine * stride + a.G * D + (ur_mine - p_mine * a.G);
+        st_f32_hint(P, ok ? ms : kFloor, keep);
+        st_f32_hint(P + a.G, ok ? l : 0.f, keep);
       }
     }
     if (!ok && lane == 0) atomicOr(a.err, PA_DEVERR_TIMEOUT);

@@ -58,10 +58,9 @@ __global__ void __launch_bounds__(kThreads) shared_merge_kernel(const SharedMerg
   int n = tail, slot0 = 0, up = 0;
   if (row.nt > 0) {
     const int f0 = row.f0 + kvh * row.kv_step, w0 = f0 / wsz;
-    const int sub = row.nut_sub & 3;
-    up = row.up_sub / sub;
-    slot0 = a.part0 + row.slot0 + (kvh * (row.nut_sub >> 2) + row.lid0 + w0) * row.up_sub;
-    n += ((f0 + row.nt - 1) / wsz - w0 + 1) * sub;
+    up = row.up;
+    slot0 = a.part0 + row.slot0 + (kvh * row.nut + row.lid0 + w0) * up;
+    n += (f0 + row.nt - 1) / wsz - w0 + 1;
   }
   const int S = a.B * a.Hkv;
   auto slot_of = [&](int k) -> int {

@@ -11,8 +11,7 @@
 namespace pa {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMaxThreads = 1024;
 constexpr unsigned kFull = 0xffffffffu;
 
 // Inclusive scan of x over the block with op (identity `zero`); *total
@@ -20,7 +19,7 @@ constexpr unsigned kFull = 0xffffffffu;
 // only it calls.
 template <typename Op>
 __device__ __forceinline__ int scan(bool one, int x, int zero, Op op, int* total) {
-  __shared__ int s_w[kWarps];
+  __shared__ int s_w[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -33,7 +32,7 @@ __device__ __forceinline__ int scan(bool one, int x, int zero, Op op, int* total
   }
   if (lane == 31) s_w[warp] = x;
   __syncthreads();
-  int v = s_w[lane];  // kWarps == 32
+  int v = lane < static_cast<int>(blockDim.x >> 5) ? s_w[lane] : zero;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(kFull, v, o);
@@ -45,29 +44,38 @@ __device__ __forceinline__ int scan(bool one, int x, int zero, Op op, int* total
   return op(x, warp > 0 ? before : zero);
 }
 
-__global__ void __launch_bounds__(kThreads) shared_plan_kernel(const SharedPlanArgs a) {
+// A group's units, worked out once (every division of a chain of them costs
+// about 200 cycles here).
+struct Units {
+  int nt, nut, up;
+  uint32_t up_mul;  // i / up = umulhi(i, up_mul) for i <= 4096; 0: up is 1
+};
+
+__global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPlanArgs a) {
   extern __shared__ int s_dyn[];
-  int* s_r0 = s_dyn;             // [NG + 1] group starts, made non-decreasing in [0, B]
+  Units* s_units = reinterpret_cast<Units*>(s_dyn);                // [NG]
+  int* s_r0 = s_dyn + 4 * a.NG;  // [NG + 1] group starts, made non-decreasing in [0, B]
   int* s_pre = s_r0 + a.NG + 1;  // [NG] prefix lengths, whole blocks
   int* s_in = s_pre + a.NG;      // [NG] rows that take part, then first flat tile
   int* s_first = s_in + a.NG;    // [NG] the first of them
   int* s_base = s_first + a.NG;  // [NG] first slot
+  int* s_w0 = s_base + a.NG;     // [NG] first CTA that meets the group
   __shared__ int s_wsz, s_tiles;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, nthreads = blockDim.x;
   const int cap = a.MB * a.bs;
   const auto add = [](int x, int y) { return x + y; };
   const auto most = [](int x, int y) { return x > y ? x : y; };
   // up to 31 groups: the scans below are the first warp's alone
   const bool one = a.NG < 32;
   const bool mine = !one || tid < 32;
-  const int step = one ? 32 : kThreads;
+  const int step = one ? 32 : nthreads;
   griddep_launch_dependents();  // the prefix kernel sets itself up, then waits
   // The inputs are not the write path's: planning overlaps it. The workspace
   // it fills was last read by a kernel that an early-launching predecessor
   // has already waited for.
   int len[4];  // this thread's first rows, in flight while the groups are set up
 #pragma unroll
-  for (int j = 0; j < 4; ++j) len[j] = tid + j * kThreads < a.B ? a.seq_lens[tid + j * kThreads] : 0;
+  for (int j = 0; j < 4; ++j) len[j] = tid + j * nthreads < a.B ? a.seq_lens[tid + j * nthreads] : 0;
   auto length = [&](int b, int j) -> int { return min(max(j < 4 ? len[j] : a.seq_lens[b], 0), cap); };
   int total;
   if (mine) {
@@ -111,57 +119,66 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const SharedPlanA
   auto takes_part = [&](int L, int g) -> bool {
     return g >= 0 && s_pre[g] > 0 && L >= s_pre[g] && (a.window == 0 || L <= a.window);
   };
-  for (int b = tid, j = 0; b < a.B; b += kThreads, ++j) {
-    const int g = group_of(b);
-    if (takes_part(length(b, j), g)) {
+  // Rows that take part, by group: a warp's rows are mostly of one group, and
+  // are then counted by one lane.
+  for (int b0 = tid & ~31, j = 0; b0 < a.B; b0 += nthreads, ++j) {
+    const int b = b0 + (tid & 31);
+    const int g = b < a.B ? group_of(b) : -1;
+    const bool in = b < a.B && takes_part(length(b, j), g);
+    const unsigned votes = __ballot_sync(kFull, in);
+    const int g_first = __shfl_sync(kFull, g, votes ? __ffs(votes) - 1 : 0);
+    if (__all_sync(kFull, !in || g == g_first)) {
+      if (in && (tid & 31) == __ffs(votes) - 1) {
+        atomicAdd(&s_in[g], __popc(votes));
+        atomicMin(&s_first[g], b);
+      }
+    } else if (in) {
       atomicAdd(&s_in[g], 1);
       atomicMin(&s_first[g], b);
     }
   }
   __syncthreads();
 
-  // units and flat tiles
+  // units, flat tiles, slots
   const int up_max = a.unit_rows / a.G;
-  auto units = [&](int g, int* nt, int* nut, int* up) {
-    const int n = s_r0[g + 1] - s_r0[g];
-    *nt = (s_pre[g] + a.kv - 1) / a.kv;
-    *nut = n > 0 ? (n + up_max - 1) / up_max : 0;
-    *up = n > 0 ? (n + *nut - 1) / *nut : 0;
-  };
-  auto sub_of = [&](int up) -> int { return a.halves && up * a.G <= a.unit_rows / 2 ? 2 : 1; };
   if (mine) {
     int run = 0;
     for (int g0 = 0; g0 < a.NG; g0 += step) {
       const int g = g0 + tid;
-      int x = 0, nt, nut, up;
+      int x = 0;
       if (g < a.NG) {
         if (s_in[g] < 2) s_pre[g] = 0;  // one sequence reads its prefix once anyway
-        units(g, &nt, &nut, &up);
-        x = a.Hkv * nut * nt;
+        const int n = s_r0[g + 1] - s_r0[g];
+        Units u;
+        u.nt = (s_pre[g] + a.kv - 1) / a.kv;
+        u.nut = n <= up_max ? (n > 0) : (n + up_max - 1) / up_max;
+        u.up = u.nut <= 1 ? n : (n + u.nut - 1) / u.nut;
+        u.up_mul = u.nut <= 1 ? 0u : 0xffffffffu / static_cast<uint32_t>(max(u.up, 1)) + 1u;
+        s_units[g] = u;
+        x = a.Hkv * u.nut * u.nt;
       }
       const int y = scan(one, x, 0, add, &total);
       if (g < a.NG) s_in[g] = run + y - x;
       run += total;
     }
     const int tiles = run;
-    const int wsz = max((tiles + a.ctas - 1) / a.ctas, a.min_tiles);
+    const int wsz = max((tiles + a.active - 1) / a.active, a.min_tiles);
     if (tid == 0) {
       s_tiles = tiles;
       s_wsz = wsz;
       a.plan[kShTotal] = tiles;
       a.plan[kShWsz] = wsz;
     }
-    // slots
     run = 0;
     for (int g0 = 0; g0 < a.NG; g0 += step) {
       const int g = g0 + tid;
-      int x = 0, nt = 0, nut = 0, up = 0;
+      int x = 0;
       if (g < a.NG) {
-        units(g, &nt, &nut, &up);
-        if (nt > 0) {
-          const int first = s_in[g], last = first + a.Hkv * nut * nt - 1;
-          x = (a.Hkv * nut + last / wsz - first / wsz) * up * sub_of(up);
-        }
+        const Units u = s_units[g];
+        const int first = s_in[g], last = first + a.Hkv * u.nut * u.nt - 1;
+        const int w0 = first / wsz;
+        s_w0[g] = w0;
+        if (u.nt > 0) x = (a.Hkv * u.nut + last / wsz - w0) * u.up;
       }
       const int y = scan(one, x, 0, add, &total);
       if (g < a.NG) s_base[g] = run + y - x;
@@ -173,21 +190,24 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const SharedPlanA
   auto record = [&](int g) -> SharedGroup {
     SharedGroup r = {};
     if (g >= a.NG) return r;
-    units(g, &r.nt, &r.nut, &r.up);
+    const Units u = s_units[g];
     r.r0 = s_r0[g];
     r.n = s_r0[g + 1] - s_r0[g];
     r.table_row = s_first[g];
     r.prefix = s_pre[g];
     r.f0 = s_in[g];
+    r.nt = u.nt;
+    r.nut = u.nut;
+    r.up = u.up;
     r.base = s_base[g];
-    r.sub = sub_of(r.up);
-    r.wfirst = s_in[g] / wsz;
+    r.dual = a.halves && u.up * a.G > a.unit_rows / 2;
+    r.wfirst = s_w0[g];
     return r;
   };
   SharedGroup* groups = const_cast<SharedGroup*>(shared_groups(a.plan, a.ctas));
-  for (int g = tid; g < a.NG; g += kThreads) groups[g] = record(g);
+  for (int g = tid; g < a.NG; g += nthreads) groups[g] = record(g);
   SharedCta* ctas = const_cast<SharedCta*>(shared_ctas(a.plan));
-  for (int w = tid; w < a.ctas; w += kThreads) {
+  for (int w = tid; w < a.ctas; w += nthreads) {
     SharedCta c;
     c.f0 = static_cast<int>(min(static_cast<long long>(w) * wsz, static_cast<long long>(tiles)));
     c.f1 = min(c.f0 + wsz, tiles);
@@ -204,22 +224,22 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const SharedPlanA
     ctas[w] = c;
   }
   SharedRow* rows = const_cast<SharedRow*>(shared_rows(a.plan, a.ctas, a.NG));
-  for (int b = tid, j = 0; b < a.B; b += kThreads, ++j) {
+  for (int b = tid, j = 0; b < a.B; b += nthreads, ++j) {
     const int g = group_of(b);
     const int L = length(b, j);
     SharedRow r = {a.window > 0 && L > a.window ? L - a.window : 0, 0, 0, 0, 0, 0, 0, 0};
     if (takes_part(L, g)) {
-      int nt, nut, up;
-      units(g, &nt, &nut, &up);
-      const int i = b - s_r0[g], ut = i / up, sub = sub_of(up);
+      const Units u = s_units[g];
+      const int i = b - s_r0[g];
+      const int ut = u.up_mul ? (u.up == 1 ? i : static_cast<int>(__umulhi(static_cast<uint32_t>(i), u.up_mul))) : 0;
       r.start = s_pre[g];
-      r.nt = nt;
-      r.f0 = s_in[g] + ut * nt;
-      r.kv_step = nut * nt;
-      r.slot0 = s_base[g] + i - ut * up;
-      r.lid0 = ut - s_in[g] / wsz;
-      r.up_sub = up * sub;
-      r.nut_sub = nut << 2 | sub;
+      r.nt = u.nt;
+      r.f0 = s_in[g] + ut * u.nt;
+      r.kv_step = u.nut * u.nt;
+      r.slot0 = s_base[g] + i - ut * u.up;
+      r.lid0 = ut - s_w0[g];
+      r.up = u.up;
+      r.nut = u.nut;
     }
     rows[b] = r;
   }
@@ -229,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const SharedPlanA
 }  // namespace
 
 cudaError_t shared_plan_launch(const SharedPlanArgs& a, cudaStream_t s, bool pdl) {
-  const size_t smem = (5 * static_cast<size_t>(a.NG) + 1) * sizeof(int);
+  const size_t smem = (10 * static_cast<size_t>(a.NG) + 1) * sizeof(int);
   if (smem > 48 * 1024) {
     const cudaError_t e =
         cudaFuncSetAttribute(reinterpret_cast<const void*>(shared_plan_kernel),
@@ -238,7 +258,7 @@ cudaError_t shared_plan_launch(const SharedPlanArgs& a, cudaStream_t s, bool pdl
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(a.B <= 512 && a.NG < 32 ? 256 : kMaxThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];

@@ -10,14 +10,14 @@
 // The (query, head) rows of one KV head of a group, n * G of them, are cut into
 // nut units of up pairs (sequences) each, at most 256 rows; a unit of at most
 // 128 rows is computed by both softmax groups of its CTA, each on every other
-// K/V tile (sub = 2 partials), a larger one by one group per 128 rows (sub = 1).
+// K/V tile, a larger one (dual) by one group per 128 rows.
 // All K/V tiles of all units form one flat index space, group- then KV head-
 // then unit-major; CTA w of the prefix kernel takes tiles [w * wsz, (w + 1) *
 // wsz). A run of one CTA's tiles inside one unit is a segment; its partials go
 // to slots
-//   base_g + ((lid * sub + x) * up + i),  lid = unit + (w - wfirst),
+//   base_g + lid * up + i,  lid = unit + (w - wfirst),
 // for the unit's index among the group's (KV head, unit) list, the first CTA
-// that meets the group, parity x of the tile and pair i: unique because the
+// that meets the group and pair i: unique because the
 // walk through the (unit, CTA) grid is a monotone staircase. Slots have the
 // decode partials' layout (one KV head's G columns of one sequence).
 #pragma once
@@ -37,7 +37,7 @@ struct SharedGroup {  // 12 words a group
   int nt;             // K/V tiles of the prefix
   int nut, up;        // units a KV head, pairs a unit
   int base;           // first partial slot (counted from the prefix region)
-  int sub;            // partials a segment and pair: 1 or 2
+  int dual;           // its units have rows for both softmax groups
   int wfirst;         // first CTA that meets the group
   int pad;
 };
@@ -54,10 +54,9 @@ struct SharedRow {  // 8 words a sequence
   int nt;           // K/V tiles of its prefix, 0: no part of it here
   int f0;           // first flat tile of its unit at KV head 0
   int kv_step;      // flat tiles between KV heads
-  int slot0;        // slot of lid 0, x 0 for this sequence's pair
+  int slot0;        // slot of lid 0 for this sequence's pair
   int lid0;         // unit - wfirst at KV head 0 (added to the CTA)
-  int up_sub;       // up * sub
-  int nut_sub;      // nut << 2 | sub
+  int up, nut;      // slots between lids, lids between KV heads
 };
 
 // Words of the plan: header, CTAs, groups, rows.

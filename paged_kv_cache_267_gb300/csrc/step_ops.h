@@ -88,6 +88,7 @@ struct SharedPlanArgs {
   int kv, unit_rows;             // tokens a K/V tile, rows a unit
   bool halves;                   // small units are computed in two halves
   int ctas;                      // of the prefix kernel
+  int active;                    // CTAs that get work
   int min_tiles;                 // least K/V tiles a CTA
 };
 cudaError_t shared_plan_launch(const SharedPlanArgs& a, cudaStream_t s, bool pdl);
