@@ -332,6 +332,9 @@ pa_status pa_decode_noalloc(const pa_tensor* out, const pa_tensor* q,
  * an idle row of length 0 among them, is decoded by itself, as is a group with
  * fewer than two that do. The prefix is read through the table of the
  * group's first row that takes part.
+ * A step whose tables could not name more than 72 MB of K/V in all (B * MB *
+ * Hkv * bs * D keys and values) is decoded plainly, whatever its groups: there
+ * is too little to save (pa_set_shared_path changes that).
  * Data errors: a prefix length outside [0, MB * bs] or group starts that
  * decrease or leave [0, B] are clamped and flagged (PA_DEVERR_GROUP).
  * Like pa_decode, the call reads group_starts, prefix_lens, seq_lens and
@@ -346,6 +349,11 @@ pa_status pa_decode_shared(const pa_tensor* out, const pa_tensor* q, const pa_te
                            const pa_tensor* group_starts, int32_t num_kv_heads, float scale,
                            int32_t block_size, int32_t window, int32_t kv_dtype, float k_scale,
                            float v_scale, pa_stream stream);
+
+/* Kernel choice for pa_decode_shared, process-wide: 0 (default) picks per call by
+ * the size of the tables (above); 1 always decodes plainly; 2 takes the shared
+ * path wherever there are groups. */
+pa_status pa_set_shared_path(int32_t path);
 
 /* Workspace bytes pa_decode_shared needs on the current device. */
 pa_status pa_decode_shared_workspace_size(int64_t batch, int64_t num_groups, int32_t num_q_heads,

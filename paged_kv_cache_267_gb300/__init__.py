@@ -72,6 +72,7 @@ def lib() -> ctypes.CDLL:
             "pa_set_workspace": (st, [vp, ctypes.c_size_t]),
             "pa_set_decode_tuning": (st, [i32, i32, i32, i32]),
             "pa_set_prefill_path": (st, [i32]),
+            "pa_set_shared_path": (st, [i32]),
             "pa_profile_events": (st, [vp, vp]),
             "pa_check_device_error": (st, [ctypes.POINTER(i32), vp]),
             "pa_selftest_bounded_wait": (st, [ctypes.c_uint32, vp, vp]),
@@ -331,6 +332,12 @@ def set_prefill_path(path: int = 0) -> None:
     """pa_prefill_chunk's kernel: 0 auto, 1 persistent split-KV kernel,
     2 tensor-memory kernel wherever it applies."""
     _check(lib().pa_set_prefill_path(path))
+
+
+def set_shared_path(path: int = 0) -> None:
+    """pa_decode_shared's kernels: 0 auto, 1 plain decode, 2 the shared path
+    wherever there are groups."""
+    _check(lib().pa_set_shared_path(path))
 
 
 def set_decode_tuning(max_ctas: int = 0, min_tiles: int = 0, pool_permille: int = 0,

@@ -212,6 +212,9 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
   pin.span = a.span;
   pin.Hv = a.Hv;
   pin.nw = gridDim.x * WARPS;
+  // SH: the static ranges go to the CTAs that find an SM free of the prefix
+  // kernel (the first ones); the others come when it ends and join the pool.
+  if constexpr (SH) pin.nw = a.shared_head[kShEarly] * WARPS;
   pin.pool_permille = a.pool_permille;
   pin.min_tiles = a.min_tiles;
   pin.np_max = a.np_max;
@@ -226,7 +229,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
   };
   const StepPlan pl = plan_step<SH>(pin, s_len, s_pref, s_first);
   const int total = pl.total, ws = pl.ws, ts = pl.ts;
-  const int nw = pin.nw;
+  const int nw = gridDim.x * WARPS;
   const int pool_tiles = total - ts;
   if (blockIdx.x == 0) {
     // the plan, for the merge kernel (kept in L2: every merge CTA reads it)

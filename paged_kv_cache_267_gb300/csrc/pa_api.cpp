@@ -12,7 +12,6 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
-#include <cstdlib>
 #include <initializer_list>
 #include <map>
 #include <mutex>
@@ -42,6 +41,7 @@ std::atomic<int32_t> g_tune_max_ctas{0};
 std::atomic<int32_t> g_tune_min_tiles{0};
 std::atomic<int32_t> g_tune_pool{0};
 std::atomic<int32_t> g_tune_piece{0};
+std::atomic<int32_t> g_shared_path{0};  // 0 auto, 1 plain decode, 2 shared wherever there are groups
 std::atomic<int32_t> g_chunk_path{0};  // 0 auto, 1 persistent kernel, 2 tensor-memory kernel
 thread_local void* g_prof_before = nullptr;
 thread_local void* g_prof_after = nullptr;
@@ -54,6 +54,11 @@ constexpr int kDefaultPiece = 4;           // least tiles per pool piece
 constexpr int kDefaultPieceFp8 = 8;
 // least K/V tiles a CTA of the prefix kernel takes
 constexpr int kPrefixMinTiles = 2;
+// Shared-prefix steps that could not read more K/V than this, sequence by
+// sequence, are decoded plainly: the plan, the prefix kernel's start and the join
+// cost about 9 us, in which the decode kernel reads shared blocks (from L2) at
+// about 8.6 TB/s (four requests of 272 tokens: 16.4 us shared, 7.2 us plain).
+constexpr double kSharedMinBytes = 72e6;
 constexpr int kPiecesPerWorker = 4;        // pool pieces per worker warp, at most
 constexpr int kMaxCtasPerSm = 2;
 constexpr int kWarpsPerCta = 8;  // most worker warps of any decode variant
@@ -346,7 +351,7 @@ Family family_of(int ct, int qt, int kind) {
 struct DecodePlan {
   Family fam;
   int nt;
-  int smem, grid, workers, min_tiles, pool_permille, piece;
+  int smem, grid, per_sm, workers, min_tiles, pool_permille, piece;
   pa::DecodeVariant var;
 };
 
@@ -391,6 +396,7 @@ pa_status plan_decode(DeviceState* st, int ct, int qt, int kind, int64_t B, int 
   }
   if (ctas < 1) return fail(PA_ERR_UNSUPPORTED, "decode kernel does not fit on an SM (smem %d)", p->smem);
   if (ctas > kMaxCtasPerSm) ctas = kMaxCtasPerSm;
+  p->per_sm = ctas;
   p->grid = st->num_sms * ctas;
   const int cap = g_tune_max_ctas.load();
   if (cap > 0 && p->grid > cap) p->grid = cap;
@@ -484,6 +490,12 @@ pa_status pa_set_decode_tuning(int32_t max_ctas, int32_t min_tiles, int32_t pool
 pa_status pa_set_prefill_path(int32_t path) {
   if (path < 0 || path > 2) return fail(PA_ERR_INVALID_ARG, "path must be 0, 1 or 2");
   g_chunk_path = path;
+  return ok();
+}
+
+pa_status pa_set_shared_path(int32_t path) {
+  if (path < 0 || path > 2) return fail(PA_ERR_INVALID_ARG, "path must be 0, 1 or 2");
+  g_shared_path = path;
   return ok();
 }
 
@@ -842,6 +854,20 @@ pa_status plan_call(DeviceState* st, const DecodeCall& c, DecodePlan* plan, WsLa
   return PA_OK;
 }
 
+// Times of a shared-prefix step's tiles (see SharedCost): the prefix kernel's
+// measured on a step with both kernels running, the tails' from the decode
+// kernel's rate, about 6.5 TB/s (e4m3: 4.4 TB/s, bound by its instructions).
+pa::SharedCost shared_cost(int D, bool fp8) {
+  pa::SharedCost c;
+  const float d = static_cast<float>(D) / 128.f;
+  c.dual_ns = D == 64 ? 2600.f : 3500.f;
+  c.single_ns = D == 64 ? 2200.f : 3000.f;
+  c.tail_ns = (fp8 ? 140.f : 190.f) * d;
+  c.prefix_ns = 10000.f;
+  c.decode_ns = 5000.f;
+  return c;
+}
+
 // Encodes the cache maps and launches the decode and merge kernels with the
 // scratch at `ws`. `wsp` (if given) is marked dirty when the merge launch
 // fails after the decode kernel ran, so that its pool counter is cleared
@@ -895,6 +921,7 @@ pa_status run_decode(const DecodeCall& c, DeviceState* st, const DecodePlan& pla
   const bool prof = g_prof_before && g_prof_after;
   cudaError_t e;
   a.shared_rows = nullptr;
+  a.shared_head = nullptr;
   if (sh) {
     // the plan, then the shared positions; the decode kernel below covers the
     // tails, and the merge joins both
@@ -917,7 +944,10 @@ pa_status run_decode(const DecodeCall& c, DeviceState* st, const DecodePlan& pla
     p.unit_rows = shape.unit_rows;
     p.halves = shape.halves;
     p.ctas = grid;
-    p.active = getenv("PA_X1") ? atoi(getenv("PA_X1")) : grid;
+    p.whole = grid * 7 / 10;
+    p.decode_ctas = plan.grid;
+    p.decode_per_sm = plan.per_sm;
+    p.cost = shared_cost(D, c.fp8);
     p.min_tiles = kPrefixMinTiles;
     e = pa::shared_plan_launch(p, cs, !prof);
     if (e != cudaSuccess) return cuda_fail(e, "shared plan launch");
@@ -941,6 +971,7 @@ pa_status run_decode(const DecodeCall& c, DeviceState* st, const DecodePlan& pla
     if (e != cudaSuccess) return cuda_fail(e, "prefix kernel launch");
     g_launches += 2;
     a.shared_rows = pa::shared_rows(p.plan, grid, p.NG);
+    a.shared_head = p.plan;
   }
   if (prof && (e = cudaEventRecord(static_cast<cudaEvent_t>(g_prof_before), cs)) != cudaSuccess)
     return cuda_fail(e, "profile event");
@@ -1085,6 +1116,21 @@ pa_status decode_entry(const pa_tensor* out, const pa_tensor* q, const pa_tensor
   return run_decode(c, st, plan, layout, ws, wsp, cs, sh);
 }
 
+// Whether a step with NG groups takes the shared path: its tables have to name
+// enough K/V. Tensors that check_decode() will refuse may get any answer.
+bool use_shared(int64_t NG, const pa_tensor* q, const pa_tensor* key_cache,
+                const pa_tensor* block_tables) {
+  const int path = g_shared_path.load();
+  if (NG == 0 || path == 1) return false;
+  if (path == 2) return true;
+  if (!q || !key_cache || !block_tables || q->ndim != 3 || key_cache->ndim != 4 ||
+      block_tables->ndim != 2)
+    return false;
+  return dprod({double(q->shape[0]), double(block_tables->shape[1]), double(key_cache->shape[1]),
+                double(key_cache->shape[2]), double(key_cache->shape[3]), 2.0,
+                double(elem_size(key_cache->dtype))}) >= kSharedMinBytes;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1130,7 +1176,7 @@ pa_status pa_decode_shared(const pa_tensor* out, const pa_tensor* q, const pa_te
     const SharedCall sh = {group_starts, prefix_lens, NG};
     return decode_entry(out, q, key_cache, value_cache, block_tables, seq_lens, num_kv_heads, scale,
                         block_size, window, kv_dtype, k_scale, v_scale, stream, false,
-                        NG > 0 ? &sh : nullptr);
+                        use_shared(NG, q, key_cache, block_tables) ? &sh : nullptr);
   });
 }
 

@@ -65,6 +65,7 @@ struct DecodeArgs {
   int piece_min;                 // least tiles per pool piece
   int np_max;                    // most pool pieces (bounds the slots)
   const SharedRow* shared_rows;  // [B], shared-prefix steps only
+  const int32_t* shared_head;    // the shared plan's header
 };
 
 struct MergeArgs {

@@ -486,21 +486,16 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
               for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f32_of<QT>(w4[e >> 1], e & 1)));
 #pragma unroll
               for (int o = kCh / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
-              int sh = 0;
-              if (amax > 0.f && amax < INFINITY) {
-                int e;
-                frexpf(amax, &e);
-                sh = e - 15;
-              }
-              // 2^-sh in two factors, each a normal number: sh is in [-163, 113]
-              const int s1 = sh / 2, s2 = sh - s1;
-              const float2 m1 = make_float2(__int_as_float((127 - s1) << 23), __int_as_float((127 - s1) << 23));
-              const float2 m2 = make_float2(__int_as_float((127 - s2) << 23), __int_as_float((127 - s2) << 23));
+              // 2^-sh from its exponent bits; below 2^-111 (scores that are zero
+              // for any weight) the largest stays under 2^14, as does zero
+              const int ex = static_cast<int>(__float_as_uint(amax) >> 23);  // 255: inf
+              const int sh = ex == 255 ? 0 : max(ex - 141, -126);
+              const float m = __int_as_float((127 - sh) << 23);
+              const float2 m2 = make_float2(m, m);
               uint32_t o4[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const float2 t = __fmul2_rn(
-                    __fmul2_rn(make_float2(f32_of<QT>(w4[e], 0), f32_of<QT>(w4[e], 1)), m1), m2);
+                const float2 t = __fmul2_rn(make_float2(f32_of<QT>(w4[e], 0), f32_of<QT>(w4[e], 1)), m2);
                 o4[e] = pack16x2<false>(t.x, t.y);
               }
               v[i] = make_uint4(o4[0], o4[1], o4[2], o4[3]);

@@ -5,14 +5,17 @@
 //   out = sum_k w_k o_k / sum_k w_k l_k,  w_k = 2^(m_k - max m).
 //
 // The heads of one KV head of a sequence (a pair) have the same list of
-// partials, and their outputs are contiguous in each, so a CTA takes 512
-// floats of a pair (four heads of 128): its warps first turn the list's maxima
-// and sums into weights in shared memory, a warp a head, then each warp adds up
-// its share of the partials, four of them with their sixteen loads in flight,
-// and the four sums are added through shared memory. The step is bound by the
-// partials' bytes through L2 and three dependent round trips (plan, maxima,
-// outputs). The plain merge's half warp a column, which works out its list for
-// every column, took 33 us for 8192 columns of about 8 partials.
+// partials, and their outputs are contiguous in each, so a warp takes 512 floats
+// of a pair (four heads of 128), sixteen a lane: it works out the list once,
+// reads the maxima and sums of 32 partials a lane each, and adds up the
+// outputs, four partials (sixteen 16-byte loads a lane) in flight, the first
+// four of them while the maxima are still on their way. Two dependent round
+// trips (plan, partials) and the partials' bytes through L2 bound it. Steps with
+// few pairs give each task four warps, which share its list and are joined
+// through shared memory. The list is worked out before the dependency wait,
+// from plans that are complete by then. (A half warp a column, which works out the list for
+// every column, took 33 us for 8192 columns of about 8 partials; a CTA a pair
+// with the weights in shared memory first, 17 us.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -27,190 +30,227 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kChunk = 512;     // floats of a pair a CTA joins
-constexpr int kList = 128;      // partials a round
-constexpr int kMaxHeads = 16;   // of a pair that a chunk can meet (head_dim 64: 8)
+constexpr int kChunk = 512;   // floats of a pair a task joins
+constexpr int kFlight = 4;    // partials in flight
 constexpr unsigned kFull = 0xffffffffu;
+constexpr int kPlanPolls = 64;     // polls of the plan flag before the wait, at most
+constexpr int kPlanPollNs = 500;   // pause between polls
 
-template <int OT>
-__global__ void __launch_bounds__(kThreads) shared_merge_kernel(const SharedMergeArgs a) {
-  __shared__ float s_w[kMaxHeads][kList];
-  __shared__ float s_scale[kMaxHeads];  // of what was added up before this round
-  __shared__ int s_slot[kList];
-  __shared__ __align__(16) float s_acc[kWarps - 1][kChunk];
+template <int OT, int D, int WPT>
+__global__ void __launch_bounds__(kThreads, 4) shared_merge_kernel(const SharedMergeArgs a) {
+  constexpr int NH = kChunk / D;  // heads a chunk
+  constexpr int C = 32 / NH;      // lanes a head, where maxima and sums are read
+  constexpr int kLog2D = D == 64 ? 6 : (D == 128 ? 7 : 8);
+  __shared__ __align__(16) float s_acc[WPT > 1 ? kWarps - 1 : 1][kChunk];
+  __shared__ float s_m[kWarps][NH], s_l[kWarps][NH];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int GD = a.G * a.D;
-  const int chunks = (GD + kChunk - 1) / kChunk;
-  const int pair = blockIdx.x / chunks, e0 = (blockIdx.x - pair * chunks) * kChunk;
-  const int b = pair / a.Hkv, kvh = pair - b * a.Hkv;
-  griddep_wait();  // the partials (the prefix kernel's too) are complete and visible
-  if (blockIdx.x == 0 && tid == 0) {  // the decode kernel's counters, for the next step
-    a.pool[0] = 0u;
-    a.pool[1] = 0u;
+  // Before the dependency wait: the shared plan is complete (the decode kernel
+  // started after it), and the decode kernel's is once its flag is set, usually
+  // long before that kernel ends; a CTA that does not see the flag waits first.
+  // The last CTA to have read the flag clears it, and the count, after the wait.
+  int32_t* const flag = reinterpret_cast<int32_t*>(a.pool) + 1;
+  int early = 0;
+  bool last = false;
+  if (tid == 0) {
+    for (int i = 0; i < kPlanPolls; ++i) {
+      early = ld_acquire_gpu(flag) == 1;
+      if (early) break;
+      __nanosleep(kPlanPollNs);
+    }
+    last = atomicAdd(a.pool + 2, 1u) == gridDim.x - 1;
   }
-  const StepPlan pl = plan_load(a.plan);
-  const int pref = a.plan[kPlanScalars + b], nt = a.plan[kPlanScalars + b + 1] - pref;
+  early = __syncthreads_or(early);
+  if (!early) griddep_wait();
+  const int GD = a.G * D;
+  const int chunks = (GD + kChunk - 1) / kChunk;
+  int task = WPT > 1 ? static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x) * kWarps + warp;
+  const bool idle = task >= a.B * a.Hkv * chunks;  // whole warps, and WPT == 1
+  if (idle) task = 0;
+  const int pair = chunks == 1 ? task : task / chunks, e0 = (task - pair * chunks) * kChunk;
+  const int b = pair / a.Hkv, kvh = pair - b * a.Hkv;
+  StepPlan pl;
+  pl.total = 0;
+  pl.ws = ld_relaxed_gpu(a.plan + 1);
+  pl.ts = ld_relaxed_gpu(a.plan + 2);
+  pl.piece = ld_relaxed_gpu(a.plan + 3);
+  pl.n_pool = 0;
+  const int pref = ld_relaxed_gpu(a.plan + kPlanScalars + b);
+  const int nt = ld_relaxed_gpu(a.plan + kPlanScalars + b + 1) - pref;
   const SharedRow row = shared_rows(a.shared, a.ctas, a.NG)[b];
   const int wsz = a.shared[kShWsz];
 
   const Cands cd = pair_cands(a.Hkv * pref + kvh * nt, nt, pl);
   const int tail = cd.na + cd.np;
-  int n = tail, slot0 = 0, up = 0;
+  int n = tail, slot0 = 0;
   if (row.nt > 0) {
     const int f0 = row.f0 + kvh * row.kv_step, w0 = f0 / wsz;
-    up = row.up;
-    slot0 = a.part0 + row.slot0 + (kvh * row.nut + row.lid0 + w0) * up;
+    slot0 = a.part0 + row.slot0 + (kvh * row.nut + row.lid0 + w0) * row.up;
     n += (f0 + row.nt - 1) / wsz - w0 + 1;
   }
   const int S = a.B * a.Hkv;
-  auto slot_of = [&](int k) -> int {
-    if (k < cd.na) return pair + cd.w0 + k;
-    if (k < tail) return S + a.NW + pair + cd.i0 + (k - cd.na);
-    return slot0 + (k - tail) * up;
+  const size_t stride = static_cast<size_t>(part_stride(a.G, D));
+  auto partial = [&](int k) -> const float* {
+    const int slot = k < cd.na ? pair + cd.w0 + k
+                     : k < tail ? S + a.NW + pair + cd.i0 + (k - cd.na)
+                                : slot0 + (k - tail) * row.up;
+    return a.part + static_cast<size_t>(slot) * stride;
   };
-  const size_t stride = static_cast<size_t>(part_stride(a.G, a.D));
-  const int h0 = e0 / a.D;                                        // heads of this chunk
-  const int nh = min(a.G, (e0 + kChunk + a.D - 1) / a.D) - h0;
+  const int h0 = e0 >> kLog2D;  // heads of this chunk
+  const int nh = min(a.G - h0, NH);
+  const int k_lo = WPT > 1 ? n * warp / WPT : 0, k_hi = WPT > 1 ? n * (warp + 1) / WPT : n;
 
-  // this lane's four groups of four floats, and their heads
+  // this lane's four groups of four floats
   float4 acc[4];
-  int head[4];
   bool on[4];
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
     acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int e = e0 + 128 * v + 4 * lane;
-    on[v] = e < GD;
-    head[v] = on[v] ? e / a.D - h0 : 0;
+    on[v] = e0 + 128 * v + 4 * lane < GD && !idle;
   }
-  // running maximum and sum of the heads this warp weighs (lane 0 of each)
-  constexpr int kOwn = kMaxHeads / kWarps;
-  float M[kOwn], den[kOwn];
-#pragma unroll
-  for (int i = 0; i < kOwn; ++i) M[i] = -INFINITY, den[i] = 0.f;
+  // value x of this lane's head in group v, from the lanes that hold x by head
+  auto of_head = [&](float x, int v) -> float {
+    return __shfl_sync(kFull, x, ((128 * v + 4 * lane) >> kLog2D) * C);
+  };
+  const int hl = lane / C, cl = lane % C;  // head and partial this lane reads
+  float M = -INFINITY, den = 0.f;          // running maximum and sum of head hl
   const uint64_t once = l2_evict_first();  // each partial is read once
+  griddep_wait();  // the partials (the prefix kernel's too) are complete and visible
+  if (last) {
+    st_relaxed_gpu(flag, 0);
+    a.pool[2] = 0u;
+  }
+  if (blockIdx.x == 0 && tid == 0) a.pool[0] = 0u;
 
-  for (int k0 = 0; k0 < n; k0 += kList) {
-    const int nk = min(kList, n - k0);
-    if (k0 > 0) __syncthreads();  // the last round's weights have been used
-    if (tid < nk) s_slot[tid] = slot_of(k0 + tid);
+  for (int k0 = k_lo; k0 < k_hi; k0 += 32) {
+    const int k1 = min(k0 + 32, k_hi);
+    float m[NH], w[NH];  // of partials cl, cl + C, ...
 #pragma unroll
-    for (int i = 0; i < kOwn; ++i) {
-      const int h = warp + kWarps * i;
-      if (h >= nh) break;
-      float m[kList / 32], l[kList / 32];
-      float top = M[i];
-#pragma unroll
-      for (int q = 0; q < kList / 32; ++q) {
-        const int k = 32 * q + lane;
-        m[q] = -INFINITY;
-        l[q] = 0.f;
-        if (k < nk) {
-          const float* P = a.part + static_cast<size_t>(slot_of(k0 + k)) * stride + GD + h0 + h;
-          m[q] = ld_f32_hint(P, once);
-          l[q] = ld_f32_hint(P + a.G, once);
-        }
-      }
-#pragma unroll
-      for (int q = 0; q < kList / 32; ++q) top = fmaxf(top, m[q]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-      float sum = 0.f;
-#pragma unroll
-      for (int q = 0; q < kList / 32; ++q) {
-        const float w = m[q] > -INFINITY ? fast_exp2(m[q] - top) : 0.f;
-        s_w[h][32 * q + lane] = w;
-        sum += w * l[q];
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-      const float old = M[i] > -INFINITY ? fast_exp2(M[i] - top) : 0.f;
-      den[i] = den[i] * old + sum;
-      M[i] = top;
-      if (lane == 0) s_scale[h] = old;
-    }
-    __syncthreads();
-    if (k0 > 0) {
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const float f = s_scale[head[v]];
-        acc[v].x *= f, acc[v].y *= f, acc[v].z *= f, acc[v].w *= f;
+    for (int q = 0; q < NH; ++q) {
+      const int k = k0 + cl + C * q;
+      m[q] = -INFINITY;
+      w[q] = 0.f;
+      if (k < k1 && hl < nh) {
+        const float* P = partial(k) + GD + h0 + hl;
+        m[q] = ld_f32_hint(P, once);
+        w[q] = ld_f32_hint(P + a.G, once);
       }
     }
-    // partials warp, warp + 4, ...: four in flight
-    for (int k = warp; k < nk; k += 4 * kWarps) {
-      float4 o[4][4];
+    float4 o[kFlight][4];
+    auto fetch = [&](int k) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int kk = k + j * kWarps;
-        const float* P = a.part + static_cast<size_t>(s_slot[kk < nk ? kk : k]) * stride + e0 + 4 * lane;
+      for (int j = 0; j < kFlight; ++j) {
+        const bool in = k + j < k1;
+        const float* P = partial(in ? k + j : k0) + e0 + 4 * lane;
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           o[j][v] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (kk < nk && on[v]) o[j][v] = ld_f32x4_hint(P + 128 * v, once);
+          if (in && on[v]) o[j][v] = ld_f32x4_hint(P + 128 * v, once);
         }
       }
+    };
+    fetch(k0);  // while the maxima are on their way
+    float top = M;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int kk = k + j * kWarps;
-        if (kk >= nk) break;
+    for (int q = 0; q < NH; ++q) top = fmaxf(top, m[q]);
+#pragma unroll
+    for (int s = C / 2; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, s));
+    float sum = 0.f;
+#pragma unroll
+    for (int q = 0; q < NH; ++q) {
+      const float e = m[q] > -INFINITY ? fast_exp2(m[q] - top) : 0.f;
+      sum += e * w[q];
+      w[q] = e;
+    }
+#pragma unroll
+    for (int s = C / 2; s > 0; s >>= 1) sum += __shfl_xor_sync(kFull, sum, s);
+    const float scale = M > -INFINITY ? fast_exp2(M - top) : 0.f;  // of what was added up before
+    den = den * scale + sum;
+    M = top;
+    if (k0 > k_lo) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const float f = of_head(scale, v);
+        acc[v].x *= f, acc[v].y *= f, acc[v].z *= f, acc[v].w *= f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 32; i += kFlight) {  // partials k0 + i ..., weights in w[i / C]
+      if (k0 + i >= k1) break;
+      if (i > 0) fetch(k0 + i);
+#pragma unroll
+      for (int j = 0; j < kFlight; ++j) {
+        const float wq = w[(i + j) / C];
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-          const float w = s_w[head[v]][kk];
-          acc[v].x += w * o[j][v].x;
-          acc[v].y += w * o[j][v].y;
-          acc[v].z += w * o[j][v].z;
-          acc[v].w += w * o[j][v].w;
+          // (0 behind the list: its lane has none)
+          const float f = __shfl_sync(kFull, wq, ((128 * v + 4 * lane) >> kLog2D) * C + (i + j) % C);
+          acc[v].x += f * o[j][v].x;
+          acc[v].y += f * o[j][v].y;
+          acc[v].z += f * o[j][v].z;
+          acc[v].w += f * o[j][v].w;
         }
       }
     }
   }
 
-  // the warps' sums, and the heads' denominators
-  __syncthreads();
+  if constexpr (WPT > 1) {
+    if (cl == 0) s_m[warp][hl] = M, s_l[warp][hl] = den;
+    if (warp > 0) {
 #pragma unroll
-  for (int i = 0; i < kOwn; ++i) {
-    const int h = warp + kWarps * i;
-    if (h < nh && lane == 0) s_scale[h] = den[i] > 0.f ? 1.f / den[i] : 0.f;  // empty range: zeros
-  }
-  if (warp > 0) {
+      for (int v = 0; v < 4; ++v)
+        *reinterpret_cast<float4*>(&s_acc[warp - 1][128 * v + 4 * lane]) = acc[v];
+    }
+    __syncthreads();
+    if (warp > 0) return;
+    float top = s_m[0][hl], f[kWarps];
 #pragma unroll
-    for (int v = 0; v < 4; ++v)
-      *reinterpret_cast<float4*>(&s_acc[warp - 1][128 * v + 4 * lane]) = acc[v];
-  }
-  __syncthreads();
-  if (warp == 0) {
-    uint16_t* out = static_cast<uint16_t*>(a.out) + static_cast<size_t>(pair) * GD + e0;
+    for (int q = 1; q < kWarps; ++q) top = fmaxf(top, s_m[q][hl]);
+    den = 0.f;
+#pragma unroll
+    for (int q = 0; q < kWarps; ++q) {
+      f[q] = s_m[q][hl] > -INFINITY ? fast_exp2(s_m[q][hl] - top) : 0.f;
+      den += f[q] * s_l[q][hl];
+    }
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      float4 x = acc[v];
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kWarps - 1; ++w) {
-        const float4 y = *reinterpret_cast<const float4*>(&s_acc[w][128 * v + 4 * lane]);
-        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+      for (int q = 0; q < kWarps; ++q) {
+        const float4 y = q == 0 ? acc[v] : *reinterpret_cast<const float4*>(&s_acc[q - 1][128 * v + 4 * lane]);
+        const float g = of_head(f[q], v);
+        x.x += g * y.x, x.y += g * y.y, x.z += g * y.z, x.w += g * y.w;
       }
-      if (!on[v]) continue;
-      const float f = s_scale[head[v]];
-      uint2 u;
-      if constexpr (OT == kBF16) {
-        const __nv_bfloat162 p = __floats2bfloat162_rn(x.x * f, x.y * f);
-        const __nv_bfloat162 q = __floats2bfloat162_rn(x.z * f, x.w * f);
-        u = make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
-      } else {
-        const __half2 p = __floats2half2_rn(x.x * f, x.y * f);
-        const __half2 q = __floats2half2_rn(x.z * f, x.w * f);
-        u = make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
-      }
-      *reinterpret_cast<uint2*>(out + 128 * v + 4 * lane) = u;
+      acc[v] = x;
     }
+  }
+  const float inv = den > 0.f ? 1.f / den : 0.f;  // empty range: zeros
+  uint16_t* out = static_cast<uint16_t*>(a.out) + static_cast<size_t>(pair) * GD + e0;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const float f = of_head(inv, v);
+    if (!on[v]) continue;
+    const float4 x = acc[v];
+    uint2 u;
+    if constexpr (OT == kBF16) {
+      const __nv_bfloat162 p = __floats2bfloat162_rn(x.x * f, x.y * f);
+      const __nv_bfloat162 q = __floats2bfloat162_rn(x.z * f, x.w * f);
+      u = make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
+    } else {
+      const __half2 p = __floats2half2_rn(x.x * f, x.y * f);
+      const __half2 q = __floats2half2_rn(x.z * f, x.w * f);
+      u = make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
+    }
+    *reinterpret_cast<uint2*>(out + 128 * v + 4 * lane) = u;
   }
 }
 
-}  // namespace
-
-cudaError_t shared_merge_launch(int out_type, const SharedMergeArgs& a, cudaStream_t s, bool pdl) {
-  const long long grid = static_cast<long long>(a.B) * a.Hkv * ((a.G * a.D + kChunk - 1) / kChunk);
-  if (grid <= 0) return cudaSuccess;
+template <int OT, int D>
+cudaError_t launch(const SharedMergeArgs& a, int num_sms, cudaStream_t s, bool pdl) {
+  const long long tasks = static_cast<long long>(a.B) * a.Hkv * ((a.G * D + kChunk - 1) / kChunk);
+  if (tasks <= 0) return cudaSuccess;
+  // one warp a task once that gives every SM five of them
+  const bool single = tasks >= 5ll * num_sms;
+  const long long grid = single ? (tasks + kWarps - 1) / kWarps : tasks;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
@@ -221,8 +261,22 @@ cudaError_t shared_merge_launch(int out_type, const SharedMergeArgs& a, cudaStre
   attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return out_type == kBF16 ? cudaLaunchKernelEx(&cfg, shared_merge_kernel<kBF16>, a)
-                           : cudaLaunchKernelEx(&cfg, shared_merge_kernel<kF16>, a);
+  return single ? cudaLaunchKernelEx(&cfg, shared_merge_kernel<OT, D, 1>, a)
+                : cudaLaunchKernelEx(&cfg, shared_merge_kernel<OT, D, kWarps>, a);
+}
+
+template <int OT>
+cudaError_t launch_dim(const SharedMergeArgs& a, int num_sms, cudaStream_t s, bool pdl) {
+  if (a.D == 64) return launch<OT, 64>(a, num_sms, s, pdl);
+  if (a.D == 128) return launch<OT, 128>(a, num_sms, s, pdl);
+  if (a.D == 256) return launch<OT, 256>(a, num_sms, s, pdl);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t shared_merge_launch(int out_type, const SharedMergeArgs& a, cudaStream_t s, bool pdl) {
+  return out_type == kBF16 ? launch_dim<kBF16>(a, a.ctas, s, pdl) : launch_dim<kF16>(a, a.ctas, s, pdl);
 }
 
 }  // namespace pa

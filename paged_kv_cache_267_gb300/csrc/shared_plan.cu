@@ -51,6 +51,28 @@ struct Units {
   uint32_t up_mul;  // i / up = umulhi(i, up_mul) for i <= 4096; 0: up is 1
 };
 
+// How many CTAs (SMs) the prefix kernel's tiles go to. The decode kernel needs
+// none of its results and takes the SMs it leaves free, so the step lasts as
+// long as the longer of the two:
+//   max(a + Tp / n, b + Td / (N - n)),
+// with the tiles' times on one SM (measured with both kernels running, in
+// step_ops.h) and what a CTA of each costs once. Near all SMs, the kernels run
+// better one after the other. Called by one warp.
+__device__ __forceinline__ int share_sms(const SharedPlanArgs& a, int tiles, int dual, int tails) {
+  const float tp = a.cost.dual_ns * dual + a.cost.single_ns * (tiles - dual);
+  const float td = a.cost.tail_ns * tails;
+  const int N = a.ctas;
+  unsigned best = 0xffffffffu;
+  for (int n0 = 1; n0 < N; n0 += 32) {
+    const int n = min(n0 + static_cast<int>(threadIdx.x & 31), N - 1);
+    const float t = fmaxf(a.cost.prefix_ns + tp / n, a.cost.decode_ns + td / (N - n));
+    // time in the upper bits (a positive float's bits order as the float), n below
+    best = min(best, (__float_as_uint(t) & 0xfffffe00u) | static_cast<unsigned>(n & 511));
+  }
+  const int n = static_cast<int>(__reduce_min_sync(kFull, best) & 511u);
+  return n > a.whole ? N : n;
+}
+
 __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPlanArgs a) {
   extern __shared__ int s_dyn[];
   Units* s_units = reinterpret_cast<Units*>(s_dyn);                // [NG]
@@ -60,7 +82,7 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
   int* s_first = s_in + a.NG;    // [NG] the first of them
   int* s_base = s_first + a.NG;  // [NG] first slot
   int* s_w0 = s_base + a.NG;     // [NG] first CTA that meets the group
-  __shared__ int s_wsz, s_tiles;
+  __shared__ int s_wsz, s_tiles, s_tails, s_dual;
   const int tid = threadIdx.x, nthreads = blockDim.x;
   const int cap = a.MB * a.bs;
   const auto add = [](int x, int y) { return x + y; };
@@ -77,6 +99,7 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
 #pragma unroll
   for (int j = 0; j < 4; ++j) len[j] = tid + j * nthreads < a.B ? a.seq_lens[tid + j * nthreads] : 0;
   auto length = [&](int b, int j) -> int { return min(max(j < 4 ? len[j] : a.seq_lens[b], 0), cap); };
+  if (tid == 0) s_tails = s_dual = 0;
   int total;
   if (mine) {
     int run = 0;
@@ -121,10 +144,14 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
   };
   // Rows that take part, by group: a warp's rows are mostly of one group, and
   // are then counted by one lane.
+  int tails = 0;  // 16-token tiles of the decode kernel, of one KV head
   for (int b0 = tid & ~31, j = 0; b0 < a.B; b0 += nthreads, ++j) {
     const int b = b0 + (tid & 31);
     const int g = b < a.B ? group_of(b) : -1;
-    const bool in = b < a.B && takes_part(length(b, j), g);
+    const int L = b < a.B ? length(b, j) : 0;
+    const bool in = takes_part(L, g) && b < a.B;
+    const int first = in ? s_pre[g] : (a.window > 0 ? max(L - a.window, 0) : 0);
+    tails += (L + kTile - 1) / kTile - first / kTile;
     const unsigned votes = __ballot_sync(kFull, in);
     const int g_first = __shfl_sync(kFull, g, votes ? __ffs(votes) - 1 : 0);
     if (__all_sync(kFull, !in || g == g_first)) {
@@ -137,6 +164,8 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
       atomicMin(&s_first[g], b);
     }
   }
+  tails = __reduce_add_sync(kFull, tails);
+  if ((tid & 31) == 0) atomicAdd(&s_tails, tails);
   __syncthreads();
 
   // units, flat tiles, slots
@@ -156,18 +185,33 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
         u.up_mul = u.nut <= 1 ? 0u : 0xffffffffu / static_cast<uint32_t>(max(u.up, 1)) + 1u;
         s_units[g] = u;
         x = a.Hkv * u.nut * u.nt;
+        if (a.halves && u.up * a.G > a.unit_rows / 2) atomicAdd(&s_dual, x);
       }
       const int y = scan(one, x, 0, add, &total);
       if (g < a.NG) s_in[g] = run + y - x;
       run += total;
     }
+    if (one) __syncwarp(); else __syncthreads();
+    const int dual = s_dual;
     const int tiles = run;
-    const int wsz = max((tiles + a.active - 1) / a.active, a.min_tiles);
+    int ctas = a.ctas;
+    if (tid < 32) ctas = share_sms(a, tiles, dual, s_tails * a.Hkv);
+    if (!one) {  // the first warp's answer, for all
+      if (tid == 0) s_wsz = ctas;
+      __syncthreads();
+      ctas = s_wsz;
+      __syncthreads();
+    }
+    const int wsz = max((tiles + ctas - 1) / ctas, a.min_tiles);
     if (tid == 0) {
       s_tiles = tiles;
       s_wsz = wsz;
       a.plan[kShTotal] = tiles;
       a.plan[kShWsz] = wsz;
+      // the prefix kernel's CTAs with work; the others leave their SMs at once
+      const int busy = (tiles + wsz - 1) / wsz;
+      a.plan[kShEarly] = busy > a.whole ? a.decode_ctas
+                                        : max(1, min(a.decode_ctas, (a.ctas - busy) * a.decode_per_sm));
     }
     run = 0;
     for (int g0 = 0; g0 < a.NG; g0 += step) {

@@ -27,7 +27,8 @@
 namespace pa {
 
 constexpr int kSharedHead = 8;      // header words
-enum { kShTotal = 0, kShWsz = 1 };  // all tiles; tiles a CTA
+// all tiles; tiles a CTA; decode CTAs that find an SM free of the prefix kernel
+enum { kShTotal = 0, kShWsz = 1, kShEarly = 2 };
 
 struct SharedGroup {  // 12 words a group
   int r0, n;          // rows

@@ -78,6 +78,13 @@ cudaError_t norm_cache_launch(int type, bool fp8, const NormCacheArgs& a, int nu
 
 // Shared-prefix decode: the plan (shared_plan.cu) and the attention over the
 // shared positions (prefix_tc.cu).
+// Times that share the SMs between the prefix kernel and the decode kernel of a
+// step, in nanoseconds of one SM while both run: a K/V tile of the prefix for
+// two row tiles or one, a 16-token tile of a tail (one KV head), and what a CTA
+// of each kernel costs besides.
+struct SharedCost {
+  float dual_ns, single_ns, tail_ns, prefix_ns, decode_ns;
+};
 struct SharedPlanArgs {
   const int32_t* group_starts;   // [NG + 1]
   const int32_t* prefix_lens;    // [NG]
@@ -88,7 +95,9 @@ struct SharedPlanArgs {
   int kv, unit_rows;             // tokens a K/V tile, rows a unit
   bool halves;                   // small units are computed in two halves
   int ctas;                      // of the prefix kernel
-  int active;                    // CTAs that get work
+  int whole;                     // more busy CTAs than this: take all SMs
+  int decode_ctas, decode_per_sm;  // of the decode kernel
+  SharedCost cost;
   int min_tiles;                 // least K/V tiles a CTA
 };
 cudaError_t shared_plan_launch(const SharedPlanArgs& a, cudaStream_t s, bool pdl);

@@ -30,6 +30,14 @@ pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not have_gpu(), reason="needs 
 DT = {"bf16": torch.bfloat16, "f16": torch.float16}
 
 
+@pytest.fixture(autouse=True)
+def shared_path(pa_lib):
+    """These batches are small: by default they would be decoded plainly."""
+    pa_lib.set_shared_path(2)
+    yield
+    pa_lib.set_shared_path(0)
+
+
 class Batch:
     """Groups of (prefix tokens, tails) and rows of no group, over a shuffled
     pool whose unused slots hold NaN."""
@@ -222,6 +230,20 @@ def test_agrees_with_decode_and_no_groups_is_decode(pa_lib):
         assert torch.equal(y[0], y[1]) and torch.equal(y[0], y[2])
     finally:
         pa_lib.set_decode_tuning()
+
+
+def test_small_steps_are_decoded_plainly_by_default(pa_lib):
+    b = Batch([(640, [9, 3, 100]), (128, [1, 1])], seed=21)
+    big = Batch([(8192, [9] * 70)], seed=22)  # 70 rows of 8200 tokens: 590 MB
+    for path, small_kernels, big_kernels in ((0, 2, 4), (1, 2, 2), (2, 4, 4)):
+        pa_lib.set_shared_path(path)
+        for x, kernels in ((b, small_kernels), (big, big_kernels)):
+            n = pa_lib.launch_count()
+            out = x.run(pa_lib)
+            assert pa_lib.launch_count() - n == kernels
+            x.check(out)
+    with pytest.raises(pa_lib.PAError):
+        pa_lib.set_shared_path(3)
 
 
 def test_empty_batch(pa_lib):
