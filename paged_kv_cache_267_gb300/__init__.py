@@ -103,6 +103,36 @@ def lib() -> ctypes.CDLL:
     return _lib_handle
 
 
+class _CtypesCalls:
+    """The hot entry points through ctypes, called as the compiled binding is:
+    with tensors, numbers, and a stream handle or None."""
+
+    def __getattr__(self, name):
+        fn = getattr(lib(), name)
+
+        def call(*args):
+            return fn(*[_desc(x) if isinstance(x, torch.Tensor) else x for x in args[:-1]],
+                      _stream(args[-1]))
+        setattr(self, name, call)
+        return call
+
+
+_calls = None
+
+
+def _native():
+    """The hot entry points: the compiled binding (built with the library, for
+    this torch), else ctypes. Both run the same library."""
+    global _calls
+    if _calls is None:
+        lib()
+        try:
+            from . import _pa_torch as _calls
+        except ImportError:  # built for another torch or Python
+            _calls = _CtypesCalls()
+    return _calls
+
+
 def last_error() -> str:
     return lib().pa_last_error().decode()
 
@@ -172,6 +202,11 @@ def _stream(stream) -> int | None:
     return int(stream)
 
 
+def _handle(stream) -> int | None:
+    """Stream argument of the hot calls: None stays None (the current stream)."""
+    return None if stream is None else _stream(stream)
+
+
 def _kv(kv_dtype) -> int:
     if kv_dtype in ("auto", None, PA_KV_AUTO):
         return PA_KV_AUTO
@@ -185,9 +220,9 @@ def _kv(kv_dtype) -> int:
 def reshape_and_cache(k, v, key_cache, value_cache, slot_mapping, kv_dtype="auto",
                       k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
     """Scatter k/v [T, Hkv, D] into the caches [NB, Hkv, bs, D] at slot_mapping [T]."""
-    descs = [_desc(x) for x in (k, v, key_cache, value_cache, slot_mapping)]
-    _check(lib().pa_reshape_and_cache(*descs, _kv(kv_dtype),
-                                      float(k_scale), float(v_scale), _stream(stream)))
+    _check(_native().pa_reshape_and_cache(k, v, key_cache, value_cache, slot_mapping,
+                                          _kv(kv_dtype), float(k_scale), float(v_scale),
+                                          _handle(stream)))
 
 
 def norm_rope_and_cache(q, k, v, key_cache, value_cache, slot_mapping, positions, cos_sin, *,
@@ -201,11 +236,10 @@ def norm_rope_and_cache(q, k, v, key_cache, value_cache, slot_mapping, positions
     [T, Hq, D] (allocated if `out` is not given; `out=q` updates in place)."""
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    _check(lib().pa_norm_rope_and_cache(
-        *[_desc(x) for x in (out, q, k, v, key_cache, value_cache, slot_mapping, positions,
-                            cos_sin, q_weight, k_weight)],
-        float(eps), int(bool(interleaved)), _kv(kv_dtype), float(k_scale), float(v_scale),
-        _stream(stream)))
+    _check(_native().pa_norm_rope_and_cache(
+        out, q, k, v, key_cache, value_cache, slot_mapping, positions, cos_sin, q_weight, k_weight,
+        float(eps), 1 if interleaved else 0, _kv(kv_dtype), float(k_scale), float(v_scale),
+        _handle(stream)))
     return out
 
 
@@ -218,12 +252,11 @@ def pool_extend(block_tables, seq_lens, new_tokens, free_list, pool_state, *, bl
     tokens (slot -1 behind the last). Lengths and pool state are updated in
     place unless outputs are given. A step that does not fit changes nothing
     and sets DEVERR_POOL, DEVERR_TOKENS or DEVERR_SEQ_LEN."""
-    _check(lib().pa_pool_extend(
-        *[_desc(x) for x in (block_tables, seq_lens, new_tokens, free_list, pool_state,
-                            seq_lens if seq_lens_out is None else seq_lens_out,
-                            pool_state if pool_state_out is None else pool_state_out,
-                            query_start, slot_mapping, positions)],
-        int(block_size), _stream(stream)))
+    _check(_native().pa_pool_extend(
+        block_tables, seq_lens, new_tokens, free_list, pool_state,
+        seq_lens if seq_lens_out is None else seq_lens_out,
+        pool_state if pool_state_out is None else pool_state_out, query_start, slot_mapping,
+        positions, int(block_size), _handle(stream)))
 
 
 def pool_release(block_tables, seq_lens, released, free_list, pool_state, *, block_size: int,
@@ -232,11 +265,11 @@ def pool_release(block_tables, seq_lens, released, free_list, pool_state, *, blo
     """Give the blocks of the sequences with released[b] != 0 back to the free
     list (all but the leading ones that hold shared_tokens[b] tokens) and set
     their lengths to 0, in place unless outputs are given."""
-    _check(lib().pa_pool_release(
-        *[_desc(x) for x in (block_tables, seq_lens, released, shared_tokens, free_list,
-                            pool_state, seq_lens if seq_lens_out is None else seq_lens_out,
-                            pool_state if pool_state_out is None else pool_state_out)],
-        int(block_size), _stream(stream)))
+    _check(_native().pa_pool_release(
+        block_tables, seq_lens, released, shared_tokens, free_list, pool_state,
+        seq_lens if seq_lens_out is None else seq_lens_out,
+        pool_state if pool_state_out is None else pool_state_out, int(block_size),
+        _handle(stream)))
 
 
 def decode(q, key_cache, value_cache, block_tables, seq_lens, *, num_kv_heads: int,
@@ -245,10 +278,10 @@ def decode(q, key_cache, value_cache, block_tables, seq_lens, *, num_kv_heads: i
     """One paged decode step; returns out [B, Hq, D] (allocated if not given)."""
     if out is None:
         out = torch.empty_like(q)
-    descs = [_desc(x) for x in (out, q, key_cache, value_cache, block_tables, seq_lens)]
-    _check(lib().pa_decode(*descs, int(num_kv_heads), float(scale),
-                           int(block_size), int(window), _kv(kv_dtype), float(k_scale),
-                           float(v_scale), _stream(stream)))
+    _check(_native().pa_decode(
+        out, q, key_cache, value_cache, block_tables, seq_lens, int(num_kv_heads), float(scale),
+        int(block_size), int(window), _kv(kv_dtype), float(k_scale), float(v_scale),
+        _handle(stream)))
     return out
 
 
@@ -262,11 +295,10 @@ def decode_shared(q, key_cache, value_cache, block_tables, seq_lens, prefix_lens
     the whole group. Returns what decode returns."""
     if out is None:
         out = torch.empty_like(q)
-    _check(lib().pa_decode_shared(
-        *[_desc(x) for x in (out, q, key_cache, value_cache, block_tables, seq_lens, prefix_lens,
-                            group_starts)],
+    _check(_native().pa_decode_shared(
+        out, q, key_cache, value_cache, block_tables, seq_lens, prefix_lens, group_starts,
         int(num_kv_heads), float(scale), int(block_size), int(window), _kv(kv_dtype),
-        float(k_scale), float(v_scale), _stream(stream)))
+        float(k_scale), float(v_scale), _handle(stream)))
     return out
 
 
@@ -278,10 +310,10 @@ def prefill_chunk(q, key_cache, value_cache, block_tables, seq_lens, *, num_kv_h
     [B, T, Hq, D] (allocated if not given)."""
     if out is None:
         out = torch.empty_like(q)
-    descs = [_desc(x) for x in (out, q, key_cache, value_cache, block_tables, seq_lens)]
-    _check(lib().pa_prefill_chunk(*descs, int(num_kv_heads),
-                                  float(scale), int(block_size), int(window), _kv(kv_dtype),
-                                  float(k_scale), float(v_scale), _stream(stream)))
+    _check(_native().pa_prefill_chunk(
+        out, q, key_cache, value_cache, block_tables, seq_lens, int(num_kv_heads), float(scale),
+        int(block_size), int(window), _kv(kv_dtype), float(k_scale), float(v_scale),
+        _handle(stream)))
     return out
 
 
@@ -291,10 +323,10 @@ def decode_noalloc(q, key_cache, value_cache, block_tables, seq_lens, *, num_kv_
     """pa_decode_noalloc: the decode step with the library's built-in scratch
     array instead of a workspace, for callers that cannot allocate device
     memory at decode time. `out` must be given (nothing is allocated)."""
-    descs = [_desc(x) for x in (out, q, key_cache, value_cache, block_tables, seq_lens)]
-    _check(lib().pa_decode_noalloc(*descs, int(num_kv_heads),
-                                   float(scale), int(block_size), int(window), _kv(kv_dtype),
-                                   float(k_scale), float(v_scale), _stream(stream)))
+    _check(_native().pa_decode_noalloc(
+        out, q, key_cache, value_cache, block_tables, seq_lens, int(num_kv_heads), float(scale),
+        int(block_size), int(window), _kv(kv_dtype), float(k_scale), float(v_scale),
+        _handle(stream)))
     return out
 
 
