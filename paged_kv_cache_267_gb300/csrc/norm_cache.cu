@@ -11,15 +11,21 @@
 // between the load and the store is fp32 and is rounded once.
 //
 // The pass moves each row once in and once out. At 16 bits an element the
-// memory allows about ten instructions an element, so the layout keeps the
-// arithmetic short: a lane holds eight elements of a head as two 8-byte chunks,
-// in the rotated part four pairs (elements 4 i .. 4 i + 3 and R / 2 further on; or
-// eight neighbours when interleaved), so a rotation needs no exchange between
-// lanes; and a thread takes kHeads heads of the same row and kind, for which it
-// folds weights and angles into four coefficients a pair once,
+// memory allows about ten instructions an element, so the layout keeps them few: a
+// lane holds sixteen elements of a head as two 16-byte chunks, in the rotated
+// part eight pairs (elements 8 i .. 8 i + 7 and R / 2 further on; or sixteen
+// neighbours when interleaved), so a rotation needs no exchange between lanes;
+// and a thread takes kHeads heads of the same row and kind, for which it folds
+// weights and angles into four coefficients a pair once,
 //   lo' = r (lo A - hi B),  hi' = r (hi C + lo E),
 // A = w_lo c, B = w_hi s, C = w_hi c, E = w_lo s (behind R: c = 1, s = 0). The
-// loads of all its heads are in flight together.
+// loads of all its heads are in flight together; neighbouring groups of lanes
+// take neighbouring heads, so that a CTA reads and writes one piece of the rows.
+// 16384 rows of 32 + 2 x 8 heads of 128: 68.7 us (5.93 TB/s) into a 16-bit cache,
+// 71.2 us into an e4m3 one. Half the elements a lane, 78.6 and 74 us; two heads a
+// thread, 78 us; eight or more (one batch after the other), 93-130 us; a CTA
+// that stays with its heads over many rows, 165 us (registers for it leave a
+// quarter of the threads).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -34,19 +40,25 @@ constexpr int kThreads = 256;
 constexpr int kManyHeads = 4;  // heads a thread in large batches
 constexpr unsigned kFull = 0xffffffffu;
 
-// Two 8-byte chunks of a head: four words of two elements.
+// x / d for x < 2^31 by the host's multiplication (see FastDiv).
+__device__ __forceinline__ unsigned quot31(unsigned x, const FastDiv& f) {
+  return f.mul ? __umulhi(x, f.mul) >> f.shift : x;
+}
+
+// Two 16-byte chunks of a head: eight words of two elements.
 struct Raw {
-  uint32_t w[4];
+  uint4 a, b;
 };
 
 __device__ __forceinline__ Raw load_raw(const uint16_t* head, int ea, int eb) {
-  const uint2 x = *reinterpret_cast<const uint2*>(head + ea);
-  const uint2 y = *reinterpret_cast<const uint2*>(head + eb);
-  return Raw{{x.x, x.y, y.x, y.y}};
+  return Raw{*reinterpret_cast<const uint4*>(head + ea), *reinterpret_cast<const uint4*>(head + eb)};
 }
 __device__ __forceinline__ void store_raw(uint16_t* head, int ea, int eb, const Raw& r) {
-  *reinterpret_cast<uint2*>(head + ea) = make_uint2(r.w[0], r.w[1]);
-  *reinterpret_cast<uint2*>(head + eb) = make_uint2(r.w[2], r.w[3]);
+  *reinterpret_cast<uint4*>(head + ea) = r.a;
+  *reinterpret_cast<uint4*>(head + eb) = r.b;
+}
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
 template <int ST>
@@ -74,23 +86,56 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) 
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
-// Pairs of a lane's elements: pair i is (lo[i], hi[i]). Interleaved, the two of
-// a word; else element i of the first chunk and of the second.
+// x / scale, correctly rounded, from the correctly rounded reciprocal: the product
+// is within an ulp of the quotient, its remainder x - q scale is exact in one fma,
+// and a second one rounds q + remainder / scale correctly (Markstein, "Computation
+// of elementary functions on the IBM RISC System/6000 processor", 1990). Where
+// the product overflows, or x is not finite, it is the result. Holds for scales
+// in [2^-60, 2^60]: what underflows is then far below the least code. Six
+// instructions; the compiler's quotient made the e4m3 write of v cost as much as
+// the norm and rotation of q.
+__device__ __forceinline__ float quotient(float x, float scale, float inv) {
+  const float q = x * inv;
+  const float y = fmaf(fmaf(-q, scale, x), inv, q);
+  return fabsf(q) < INFINITY ? copysignf(y, q) : q;  // (a remainder of zero is +0)
+}
+
+// Pairs of a lane's elements, as float2 of two pairs: pair i is (lo_i, hi_i).
+// Interleaved, the two of a word; else element i of the first chunk and of the
+// second. Words (2 q, 2 q + 1) of the order below make lo[q], hi[q] when
+// interleaved, word q of each chunk otherwise.
 template <int ST, bool INTER>
-__device__ __forceinline__ void pairs_of(const Raw& r, float2 (&lo)[2], float2 (&hi)[2]) {
-  const float2 a = unpack2<ST>(r.w[0]), b = unpack2<ST>(r.w[1]);
-  const float2 c = unpack2<ST>(r.w[2]), d = unpack2<ST>(r.w[3]);
-  if constexpr (INTER) {
-    lo[0] = make_float2(a.x, b.x), hi[0] = make_float2(a.y, b.y);
-    lo[1] = make_float2(c.x, d.x), hi[1] = make_float2(c.y, d.y);
-  } else {
-    lo[0] = a, lo[1] = b, hi[0] = c, hi[1] = d;
+__device__ __forceinline__ void pairs_of(const Raw& r, float2 (&lo)[4], float2 (&hi)[4]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if constexpr (INTER) {
+      const uint4& v = q < 2 ? r.a : r.b;
+      const float2 x = unpack2<ST>(word(v, 2 * (q & 1))), y = unpack2<ST>(word(v, 2 * (q & 1) + 1));
+      lo[q] = make_float2(x.x, y.x), hi[q] = make_float2(x.y, y.y);
+    } else {
+      lo[q] = unpack2<ST>(word(r.a, q));
+      hi[q] = unpack2<ST>(word(r.b, q));
+    }
+  }
+}
+// Back to element order: the eight pairs of values of the two chunks.
+template <bool INTER>
+__device__ __forceinline__ void order_of(const float2 (&lo)[4], const float2 (&hi)[4], float2 (&e)[8]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if constexpr (INTER) {
+      e[2 * q] = make_float2(lo[q].x, hi[q].x);
+      e[2 * q + 1] = make_float2(lo[q].y, hi[q].y);
+    } else {
+      e[q] = lo[q];
+      e[4 + q] = hi[q];
+    }
   }
 }
 
-// LANES lanes a head (D <= 8 * LANES), kHeads heads of one kind a thread.
+// LANES lanes a head (D <= 16 * LANES), kHeads heads of one kind a thread.
 template <int ST, bool FP8, bool INTER, int LANES, int kHeads>
-__global__ void __launch_bounds__(kThreads, kHeads > 1 ? 5 : 4) norm_cache_kernel(const NormCacheArgs a) {
+__global__ void __launch_bounds__(kThreads, kHeads > 1 ? 3 : 4) norm_cache_kernel(const NormCacheArgs a) {
   constexpr int kGroups = kThreads / LANES;
   // rows may come from the previous kernel, and the caches may still be read
   // by it. The next kernel may start its launch: of what is written here it
@@ -100,17 +145,17 @@ __global__ void __launch_bounds__(kThreads, kHeads > 1 ? 5 : 4) norm_cache_kerne
   const int lane = threadIdx.x % LANES;
   const int uq = (a.Hq + kHeads - 1) / kHeads, uk = (a.Hkv + kHeads - 1) / kHeads;
   const unsigned per_row = uq + 2 * uk;
-  const unsigned unit = blockIdx.x * kGroups + threadIdx.x / LANES;  // the host keeps it in 32 bits
-  const unsigned row = unit / per_row;
+  const unsigned unit = blockIdx.x * kGroups + threadIdx.x / LANES;  // the host keeps it in 31 bits
+  const unsigned row = quot31(unit, a.per_row_div);
   if (row >= static_cast<unsigned>(a.T)) return;  // whole groups: the shuffles below are per group
   const int t = static_cast<int>(row);
   const int u = static_cast<int>(unit - row * per_row);
   const int kind = u < uq ? 0 : (u < uq + uk ? 1 : 2);  // q, k, v
   const int h0 = (u - (kind == 0 ? 0 : (kind == 1 ? uq : uq + uk))) * kHeads;
   const int nh = min(kHeads, (kind == 0 ? a.Hq : a.Hkv) - h0);
-  const bool on = 8 * lane < a.D, rotated = 8 * lane < a.R;
-  const int ea = rotated && !INTER ? 4 * lane : 8 * lane;
-  const int eb = rotated && !INTER ? (a.R >> 1) + 4 * lane : 8 * lane + 4;
+  const bool on = 16 * lane < a.D, rotated = 16 * lane < a.R;
+  const int ea = rotated && !INTER ? 8 * lane : 16 * lane;
+  const int eb = rotated && !INTER ? (a.R >> 1) + 8 * lane : 16 * lane + 8;
 
   const uint16_t* src = static_cast<const uint16_t*>(kind == 0 ? a.q : (kind == 1 ? a.k : a.v)) +
                         t * (kind == 0 ? a.q_stride : (kind == 1 ? a.k_stride : a.v_stride)) +
@@ -118,125 +163,150 @@ __global__ void __launch_bounds__(kThreads, kHeads > 1 ? 5 : 4) norm_cache_kerne
   Raw x[kHeads];
 #pragma unroll
   for (int j = 0; j < kHeads; ++j) {
-    x[j] = Raw{{0u, 0u, 0u, 0u}};
+    x[j].a = x[j].b = make_uint4(0u, 0u, 0u, 0u);
     if (on && j < nh) x[j] = load_raw(src + j * a.D, ea, eb);
   }
 
-  // where k and v go
-  size_t dst = 0;  // element of head h0 in the cache
-  bool stored = kind == 0;
-  if (kind != 0) {
-    const long long slot = a.slots[t];
+  // where the results go: of head h0, and from head to head
+  constexpr int elt = FP8 ? 1 : 2;
+  char* dst;
+  size_t step;
+  bool stored = on;
+  if (kind == 0) {
+    dst = reinterpret_cast<char*>(static_cast<uint16_t*>(a.q_out) + t * a.out_stride + h0 * a.D);
+    step = a.D * sizeof(uint16_t);
+  } else {
+    long long slot = a.slots[t];
     if (slot >= a.NB * a.bs) {
       if (lane == 0) atomicOr(a.err, PA_DEVERR_SLOT);
-    } else if (slot >= 0) {
-      stored = true;
-      // pools below 2^32 slots divide in 32 bits
-      const long long blk = slot >> 32 ? slot / a.bs
-                                       : static_cast<unsigned>(slot) / static_cast<unsigned>(a.bs);
-      dst = ((static_cast<size_t>(blk) * a.Hkv + h0) * a.bs + (slot - blk * a.bs)) * a.D;
+      slot = -1;
     }
+    stored = stored && slot >= 0;
+    if (slot < 0) slot = 0;
+    const long long blk = slot >> 31 ? slot / a.bs : quot31(static_cast<unsigned>(slot), a.bs_div);
+    step = static_cast<size_t>(a.bs) * a.D * elt;
+    dst = static_cast<char*>(kind == 1 ? a.kc : a.vc) +
+          ((static_cast<size_t>(blk) * a.Hkv + h0) * a.bs + (slot - blk * a.bs)) * (a.D * elt);
   }
-  const size_t head_step = static_cast<size_t>(a.bs) * a.D;
+  // e4m3 codes of a lane's values
+  auto store_codes = [&](char* at, const float2 (&e)[8]) {
+    *reinterpret_cast<uint2*>(at + ea) = make_uint2(encode4(e[0].x, e[0].y, e[1].x, e[1].y),
+                                                    encode4(e[2].x, e[2].y, e[3].x, e[3].y));
+    *reinterpret_cast<uint2*>(at + eb) = make_uint2(encode4(e[4].x, e[4].y, e[5].x, e[5].y),
+                                                    encode4(e[6].x, e[6].y, e[7].x, e[7].y));
+  };
 
   if (kind == 2) {
-    if (!stored || !on) return;
+    if (!stored) return;
 #pragma unroll
     for (int j = 0; j < kHeads; ++j) {
       if (j >= nh) break;
-      const size_t at = dst + j * head_step;
       if constexpr (FP8) {
-        uint8_t* c = static_cast<uint8_t*>(a.vc) + at;
-        const float2 p = unpack2<ST>(x[j].w[0]), q = unpack2<ST>(x[j].w[1]);
-        const float2 r = unpack2<ST>(x[j].w[2]), s = unpack2<ST>(x[j].w[3]);
         // the IEEE quotient, as the plain write path stores it
-        *reinterpret_cast<uint32_t*>(c + ea) =
-            encode4(p.x / a.v_scale, p.y / a.v_scale, q.x / a.v_scale, q.y / a.v_scale);
-        *reinterpret_cast<uint32_t*>(c + eb) =
-            encode4(r.x / a.v_scale, r.y / a.v_scale, s.x / a.v_scale, s.y / a.v_scale);
+        float2 e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = unpack2<ST>(word(i < 4 ? x[j].a : x[j].b, i & 3));
+        if (a.v_scale >= 0x1p-60f && a.v_scale <= 0x1p60f) {
+          const float inv = 1.f / a.v_scale;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            e[i] = make_float2(quotient(e[i].x, a.v_scale, inv), quotient(e[i].y, a.v_scale, inv));
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i) e[i] = make_float2(e[i].x / a.v_scale, e[i].y / a.v_scale);
+        }
+        store_codes(dst, e);
       } else {
-        store_raw(static_cast<uint16_t*>(a.vc) + at, ea, eb, x[j]);
+        store_raw(reinterpret_cast<uint16_t*>(dst), ea, eb, x[j]);
       }
+      dst += step;
     }
     return;
   }
 
   // coefficients of this lane's pairs
   const void* weight = kind == 0 ? a.q_weight : a.k_weight;
-  float2 A[2], B[2], C[2], E[2];
-  A[0] = A[1] = C[0] = C[1] = make_float2(1.f, 1.f);  // the weights first
+  float2 A[4], B[4], C[4], E[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    A[q] = C[q] = make_float2(1.f, 1.f);  // the weights first
+    B[q] = E[q] = make_float2(0.f, 0.f);
+  }
   if (weight && on) pairs_of<ST, INTER>(load_raw(static_cast<const uint16_t*>(weight), ea, eb), A, C);
-  B[0] = B[1] = E[0] = E[1] = make_float2(0.f, 0.f);
   if (rotated) {
     int pos = a.positions[t];
     if (pos < 0 || pos >= a.NP) {
       if (lane == 0) atomicOr(a.err, PA_DEVERR_POSITION);
       pos = pos < 0 ? 0 : a.NP - 1;
     }
-    const float* angle = a.cos_sin + static_cast<size_t>(pos) * a.R + 4 * lane;
-    const float4 c = __ldg(reinterpret_cast<const float4*>(angle));
-    const float4 s = __ldg(reinterpret_cast<const float4*>(angle + (a.R >> 1)));
-    const float2 c2[2] = {make_float2(c.x, c.y), make_float2(c.z, c.w)};
-    const float2 s2[2] = {make_float2(s.x, s.y), make_float2(s.z, s.w)};
+    const float* angle = a.cos_sin + static_cast<size_t>(pos) * a.R + 8 * lane;
+    const float4 c0 = __ldg(reinterpret_cast<const float4*>(angle));
+    const float4 c1 = __ldg(reinterpret_cast<const float4*>(angle) + 1);
+    const float4 s0 = __ldg(reinterpret_cast<const float4*>(angle + (a.R >> 1)));
+    const float4 s1 = __ldg(reinterpret_cast<const float4*>(angle + (a.R >> 1)) + 1);
+    const float2 c2[4] = {make_float2(c0.x, c0.y), make_float2(c0.z, c0.w), make_float2(c1.x, c1.y),
+                          make_float2(c1.z, c1.w)};
+    const float2 s2[4] = {make_float2(s0.x, s0.y), make_float2(s0.z, s0.w), make_float2(s1.x, s1.y),
+                          make_float2(s1.z, s1.w)};
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      B[i] = __fmul2_rn(C[i], make_float2(-s2[i].x, -s2[i].y));
-      E[i] = __fmul2_rn(A[i], s2[i]);
-      A[i] = __fmul2_rn(A[i], c2[i]);
-      C[i] = __fmul2_rn(C[i], c2[i]);
+    for (int q = 0; q < 4; ++q) {
+      B[q] = __fmul2_rn(C[q], make_float2(-s2[q].x, -s2[q].y));
+      E[q] = __fmul2_rn(A[q], s2[q]);
+      A[q] = __fmul2_rn(A[q], c2[q]);
+      C[q] = __fmul2_rn(C[q], c2[q]);
     }
   }
-  // lanes of this group within its warp
-  const unsigned members = LANES == 32 ? kFull : ((1u << LANES) - 1u) << (threadIdx.x & 31 & ~(LANES - 1));
+  // the heads' norms, interleaved: a head behind nh is zeros and goes nowhere
   const float inv_d = 1.f / static_cast<float>(a.D);
   const float inv_scale = kind == 1 && FP8 ? 1.f / a.k_scale : 1.f;
-  // the heads' norms, interleaved: a head behind nh is zeros and goes nowhere
   float rn[kHeads];
-#pragma unroll
-  for (int j = 0; j < kHeads; ++j) rn[j] = 0.f;
   if (weight) {
+    const unsigned members =
+        LANES == 32 ? kFull : ((1u << LANES) - 1u) << (threadIdx.x & 31 & ~(LANES - 1));
 #pragma unroll
     for (int j = 0; j < kHeads; ++j) {
+      float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 p = unpack2<ST>(x[j].w[i]);
-        rn[j] = fmaf(p.x, p.x, fmaf(p.y, p.y, rn[j]));
+      for (int i = 0; i < 8; ++i) {
+        const float2 p = unpack2<ST>(word(i < 4 ? x[j].a : x[j].b, i & 3));
+        ss = __ffma2_rn(p, p, ss);
       }
+      rn[j] = ss.x + ss.y;
     }
 #pragma unroll
     for (int o = LANES / 2; o > 0; o >>= 1)
 #pragma unroll
       for (int j = 0; j < kHeads; ++j) rn[j] += __shfl_xor_sync(members, rn[j], o);
+#pragma unroll
+    for (int j = 0; j < kHeads; ++j) rn[j] = rsqrtf(fmaf(rn[j], inv_d, a.eps)) * inv_scale;
+  } else {
+#pragma unroll
+    for (int j = 0; j < kHeads; ++j) rn[j] = inv_scale;
   }
 #pragma unroll
   for (int j = 0; j < kHeads; ++j) {
-    float2 lo[2], hi[2];
+    float2 lo[4], hi[4], yl[4], yh[4], e[8];
     pairs_of<ST, INTER>(x[j], lo, hi);
-    const float r = weight ? rsqrtf(fmaf(rn[j], inv_d, a.eps)) * inv_scale : inv_scale;
-    const float2 r2 = make_float2(r, r);
-    float2 yl[2], yh[2];
+    const float2 r2 = make_float2(rn[j], rn[j]);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      yl[i] = __fmul2_rn(__ffma2_rn(hi[i], B[i], __fmul2_rn(lo[i], A[i])), r2);
-      yh[i] = __fmul2_rn(__ffma2_rn(lo[i], E[i], __fmul2_rn(hi[i], C[i])), r2);
+    for (int q = 0; q < 4; ++q) {
+      yl[q] = __fmul2_rn(__ffma2_rn(hi[q], B[q], __fmul2_rn(lo[q], A[q])), r2);
+      yh[q] = __fmul2_rn(__ffma2_rn(lo[q], E[q], __fmul2_rn(hi[q], C[q])), r2);
     }
-    if (!on || !stored || j >= nh) continue;
-    // back to element order: words of the two chunks
-    const float2 w0 = INTER ? make_float2(yl[0].x, yh[0].x) : yl[0];
-    const float2 w1 = INTER ? make_float2(yl[0].y, yh[0].y) : yl[1];
-    const float2 w2 = INTER ? make_float2(yl[1].x, yh[1].x) : yh[0];
-    const float2 w3 = INTER ? make_float2(yl[1].y, yh[1].y) : yh[1];
-    if (FP8 && kind == 1) {
-      uint8_t* c = static_cast<uint8_t*>(a.kc) + dst + j * head_step;
-      *reinterpret_cast<uint32_t*>(c + ea) = encode4(w0.x, w0.y, w1.x, w1.y);
-      *reinterpret_cast<uint32_t*>(c + eb) = encode4(w2.x, w2.y, w3.x, w3.y);
-    } else {
-      uint16_t* c = kind == 0 ? static_cast<uint16_t*>(a.q_out) + t * a.out_stride + (h0 + j) * a.D
-                              : static_cast<uint16_t*>(a.kc) + dst + j * head_step;
-      const Raw y = {{pack2<ST>(w0.x, w0.y), pack2<ST>(w1.x, w1.y), pack2<ST>(w2.x, w2.y),
-                      pack2<ST>(w3.x, w3.y)}};
-      store_raw(c, ea, eb, y);
+    order_of<INTER>(yl, yh, e);
+    if (stored && j < nh) {
+      if (FP8 && kind == 1) {
+        store_codes(dst, e);
+      } else {
+        Raw y;
+        y.a = make_uint4(pack2<ST>(e[0].x, e[0].y), pack2<ST>(e[1].x, e[1].y), pack2<ST>(e[2].x, e[2].y),
+                         pack2<ST>(e[3].x, e[3].y));
+        y.b = make_uint4(pack2<ST>(e[4].x, e[4].y), pack2<ST>(e[5].x, e[5].y), pack2<ST>(e[6].x, e[6].y),
+                         pack2<ST>(e[7].x, e[7].y));
+        store_raw(reinterpret_cast<uint16_t*>(dst), ea, eb, y);
+      }
     }
+    dst += step;
   }
 }
 
@@ -244,20 +314,21 @@ template <int ST, bool FP8, bool INTER, int LANES, int kHeads>
 cudaError_t launch(NormCacheArgs a, cudaStream_t s) {
   constexpr int kGroups = kThreads / LANES;
   const long long per_row = (a.Hq + kHeads - 1) / kHeads + 2ll * ((a.Hkv + kHeads - 1) / kHeads);
-  // the kernel counts units in 32 bits: at most 2^31 - 2^16 a launch
-  const long long most_rows = (0x7fff0000ll) / per_row;
-  for (int t0 = 0, n = 0; t0 < a.T || n == 0; ++n) {
+  // the kernel counts units in 31 bits
+  const long long most_rows = 0x7fff0000ll / per_row;
+  for (long long t0 = 0; t0 < a.T; t0 += most_rows) {
     NormCacheArgs b = a;
     b.T = static_cast<int>(a.T - t0 < most_rows ? a.T - t0 : most_rows);
-    const long long grid = (b.T * per_row + kGroups - 1) / kGroups;
     b.q = static_cast<const uint16_t*>(a.q) + t0 * a.q_stride;
     b.k = static_cast<const uint16_t*>(a.k) + t0 * a.k_stride;
     b.v = static_cast<const uint16_t*>(a.v) + t0 * a.v_stride;
     b.q_out = static_cast<uint16_t*>(a.q_out) + t0 * a.out_stride;
     b.slots = a.slots + t0;
     b.positions = a.positions + t0;
+    b.per_row_div = fast_div(static_cast<uint32_t>(per_row));
+    b.bs_div = fast_div(static_cast<uint32_t>(a.bs));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.gridDim = dim3(static_cast<unsigned>((b.T * per_row + kGroups - 1) / kGroups));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -267,14 +338,13 @@ cudaError_t launch(NormCacheArgs a, cudaStream_t s) {
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, norm_cache_kernel<ST, FP8, INTER, LANES, kHeads>, b);
     if (e != cudaSuccess) return e;
-    t0 += b.T;
   }
   return cudaSuccess;
 }
 
 template <int ST, bool FP8, bool INTER, int LANES>
 cudaError_t launch_heads(const NormCacheArgs& a, int num_sms, cudaStream_t s) {
-  // four heads a thread once that still fills every SM twice over
+  // several heads a thread once that still fills every SM twice over
   const long long groups = static_cast<long long>(a.T) * (a.Hq + 2 * a.Hkv);
   const long long ctas = groups / kManyHeads / (kThreads / LANES);
   return ctas >= 2ll * num_sms ? launch<ST, FP8, INTER, LANES, kManyHeads>(a, s)
@@ -283,18 +353,16 @@ cudaError_t launch_heads(const NormCacheArgs& a, int num_sms, cudaStream_t s) {
 
 template <int ST, bool FP8, bool INTER>
 cudaError_t launch_lanes(const NormCacheArgs& a, int num_sms, cudaStream_t s) {
-  if (a.D <= 64) return launch_heads<ST, FP8, INTER, 8>(a, num_sms, s);
-  if (a.D <= 128) return launch_heads<ST, FP8, INTER, 16>(a, num_sms, s);
-  return launch_heads<ST, FP8, INTER, 32>(a, num_sms, s);
+  if (a.D <= 64) return launch_heads<ST, FP8, INTER, 4>(a, num_sms, s);
+  if (a.D <= 128) return launch_heads<ST, FP8, INTER, 8>(a, num_sms, s);
+  return launch_heads<ST, FP8, INTER, 16>(a, num_sms, s);
 }
 
 template <int ST>
 cudaError_t launch_type(bool fp8, const NormCacheArgs& a, int num_sms, cudaStream_t s) {
   if (a.interleaved)
-    return fp8 ? launch_lanes<ST, true, true>(a, num_sms, s)
-               : launch_lanes<ST, false, true>(a, num_sms, s);
-  return fp8 ? launch_lanes<ST, true, false>(a, num_sms, s)
-             : launch_lanes<ST, false, false>(a, num_sms, s);
+    return fp8 ? launch_lanes<ST, true, true>(a, num_sms, s) : launch_lanes<ST, false, true>(a, num_sms, s);
+  return fp8 ? launch_lanes<ST, true, false>(a, num_sms, s) : launch_lanes<ST, false, false>(a, num_sms, s);
 }
 
 }  // namespace

@@ -124,10 +124,10 @@ __device__ __forceinline__ Sums scan_rows(int* s_tok, int* s_blk, int B, int bad
   return all;
 }
 
-// The index b in [0, B) with s[b] <= x < s[b + 1], for s[0] <= x < s[B]
+// The index b in [lo, B) with s[b] <= x < s[b + 1], for s[lo] <= x < s[B]
 // (sequences with nothing are skipped).
-__device__ __forceinline__ int row_of(const int* s, int B, int x) {
-  int lo = 0, hi = B;
+__device__ __forceinline__ int row_of(const int* s, int B, int x, int lo = 0) {
+  int hi = B;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (s[mid] <= x) lo = mid; else hi = mid;
@@ -176,8 +176,10 @@ struct Step {
 };
 
 // Slots and positions of rows [t0, t0 + N): one search, then along the rows.
+// The rows belong to sequences [b_lo, b_hi).
 template <int N>
-__device__ __forceinline__ void write_rows(const PoolExtendArgs& a, const Step& s, int t0) {
+__device__ __forceinline__ void write_rows(const PoolExtendArgs& a, const Step& s, int t0, int b_lo,
+                                           int b_hi) {
   long long slot[N];
   int pos[N];
   int b = -1, end = 0, base = 0, had = 0, cur = -1;
@@ -189,7 +191,7 @@ __device__ __forceinline__ void write_rows(const PoolExtendArgs& a, const Step& 
     pos[j] = 0;
     if (t >= s.ntok) continue;
     if (b < 0 || t >= end) {
-      b = row_of(s.tok, a.B, t);
+      b = row_of(s.tok, b_hi, t, b_lo);
       end = s.tok[b + 1];
       base = s.len[b] - s.tok[b];
       had = quot(s.len[b] + a.bs - 1, a.div);
@@ -284,10 +286,14 @@ __global__ void __launch_bounds__(kThreads) pool_extend_kernel(const PoolExtendA
   const Step step = {s_tok, s_blk, s_len, count, ntok};
   if (a.T <= static_cast<int>(gridDim.x) * kThreads) {
     const int t = blockIdx.x * kThreads + tid;
-    if (t < a.T) write_rows<1>(a, step, t);
+    if (t < a.T) write_rows<1>(a, step, t, 0, a.B);
   } else {
     const Share st = share_of(a.T, 4 * 32);
-    for (int t0 = st.lo + 4 * tid; t0 < st.hi; t0 += 4 * kThreads) write_rows<4>(a, step, t0);
+    const int last = min(st.hi, ntok) - 1;  // the share meets few sequences
+    const int b_lo = st.lo <= last ? row_of(s_tok, a.B, st.lo) : 0;
+    const int b_hi = st.lo <= last ? row_of(s_tok, a.B, last, b_lo) + 1 : 0;
+    for (int t0 = st.lo + 4 * tid; t0 < st.hi; t0 += 4 * kThreads)
+      write_rows<4>(a, step, t0, b_lo, b_hi);
   }
 
   if (!commit_turn(a.in_place, a.state + 1)) return;
@@ -422,7 +428,7 @@ cudaError_t launch(void (*fn)(const Args), const Args& a, int grid, size_t smem,
 
 cudaError_t pool_extend_launch(const PoolExtendArgs& a, int num_sms, cudaStream_t s) {
   const size_t smem = (3 * static_cast<size_t>(a.B) + 2) * sizeof(int);
-  return launch(pool_extend_kernel, a, grid_for(a.T, 4 * kThreads, num_sms), smem, s);
+  return launch(pool_extend_kernel, a, grid_for(a.T, 4 * kThreads, 2 * num_sms), smem, s);
 }
 
 cudaError_t pool_release_launch(const PoolReleaseArgs& a, int num_sms, cudaStream_t s) {

@@ -10,11 +10,13 @@ namespace pa {
 
 // The block pool (pool_ops.cu). in_place: lens_out is lens, or state_out is
 // state; the last CTA to have read them then writes them.
-// Division of 31-bit integers by a fixed d > 1 as a multiplication.
+// Division of 31-bit integers by a fixed d as a multiplication.
 struct FastDiv {
   uint32_t mul, shift;
 };
+// (d = 1: mul 0, which stands for no division; d = 0 never divides)
 inline FastDiv fast_div(uint32_t d) {
+  if (d <= 1) return FastDiv{0, 0};
   uint32_t l = 1;
   while ((1ull << l) < d) ++l;
   return FastDiv{static_cast<uint32_t>(((1ull << (31 + l)) + d - 1) / d), l - 1};
@@ -70,6 +72,7 @@ struct NormCacheArgs {
   int64_t q_stride, k_stride, v_stride, out_stride;  // elements a row
   int64_t NB;
   int T, Hq, Hkv, D, R, NP, bs;
+  FastDiv per_row_div, bs_div;   // set by the launcher: by the units of a row, by bs
   float eps, k_scale, v_scale;
   bool interleaved;
 };

@@ -135,6 +135,27 @@ def test_against_the_formulas(T, Hq, Hkv, D, R, dt, fp8, inter, norm, pa_lib):
     assert torch.equal(vc, vp)
 
 
+@pytest.mark.parametrize("src", ["bf16", "f16"])
+@pytest.mark.parametrize("scale", [1.0, 0.0123, 3.7, 1e-3, 300.0, 0.7499999, 2.0 ** -60, 1.1e-19, 1e-30, 1e30, 3e38])
+def test_v_codes_equal_the_plain_write_paths_for_every_pattern(src, scale, pa_lib):
+    """All 65,536 16-bit inputs, infinities and NaNs among them."""
+    bits = torch.from_numpy(np.arange(65536, dtype=np.uint32).astype(np.uint16).view(np.int16).copy())
+    for H, D in ((2, 128), (4, 64)):
+        T = 65536 // (H * D)
+        v = bits.view(DT[src]).reshape(T, H, D).cuda()
+        k = torch.zeros_like(v)
+        NB = -(-T // 16)
+        a = [torch.zeros(NB, H, 16, D, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        slots = torch.arange(T, device="cuda")
+        pos = torch.zeros(T, dtype=torch.int32, device="cuda")
+        pa_lib.norm_rope_and_cache(k, k, v, a[0], a[1], slots, pos, angles(1, D), kv_dtype="fp8", v_scale=scale)
+        pa_lib.reshape_and_cache(k, v, a[2], a[3], slots, "fp8", 1.0, scale)
+        nan = torch.isnan(v.float()).reshape(-1, H, D).cpu()
+        x, y = (c.transpose(1, 2).reshape(NB * 16, H, D)[:T].cpu() for c in (a[1], a[3]))
+        assert torch.equal(x[~nan], y[~nan])
+        assert ((x[nan] & 0x7F) == 0x7F).all()
+
+
 @pytest.mark.parametrize("T", [3, 3000])
 def test_in_place_and_strided_outputs(T, pa_lib):
     packed, q, k, v, kc, vc, slots, pos, cs, (wq, wk) = make(T, 8, 2, 128, "bf16", False, extra_cols=24)
