@@ -337,6 +337,7 @@ pa_status pa_decode_noalloc(const pa_tensor* out, const pa_tensor* q,
  * is too little to save (pa_set_shared_path changes that).
  * Data errors: a prefix length outside [0, MB * bs] or group starts that
  * decrease or leave [0, B] are clamped and flagged (PA_DEVERR_GROUP).
+ * A step that is decoded plainly does not look at either.
  * Like pa_decode, the call reads group_starts, prefix_lens, seq_lens and
  * block_tables before it waits for the previous kernel of the stream, and q
  * and the caches after.
@@ -427,8 +428,9 @@ pa_status pa_set_workspace(void* ptr, size_t bytes);
  *   pool_permille  share of the tiles handed out dynamically in small pieces
  *                  after the static ranges (default 100; the pool only
  *                  covers the trailing run of sequences no longer than 4x the
- *                  mean length); negative turns the pool off, which makes
- *                  results bit-reproducible;
+ *                  mean length; none in a shared step of pa_decode_shared);
+ *                  negative turns the pool off, which makes results
+ *                  bit-reproducible;
  *   piece_tiles    least tiles per pool piece (default 4; 8 for single-query
  *                  decode on e4m3 caches). */
 pa_status pa_set_decode_tuning(int32_t max_ctas, int32_t min_tiles, int32_t pool_permille,

@@ -213,7 +213,8 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
   pin.Hv = a.Hv;
   pin.nw = gridDim.x * WARPS;
   // SH: the static ranges go to the CTAs that find an SM free of the prefix
-  // kernel (the first ones); the others come when it ends and join the pool.
+  // kernel (the first ones); the others come when it ends, too late for a
+  // share (they have one only where a pool is asked for).
   if constexpr (SH) pin.nw = a.shared_head[kShEarly] * WARPS;
   pin.pool_permille = a.pool_permille;
   pin.min_tiles = a.min_tiles;

@@ -278,9 +278,14 @@ size_t most_shared_slots(int64_t B, int64_t Hkv, int G, int D, int grid) {
   return static_cast<size_t>(2 * Hkv * B + grid * std::max<int64_t>(unit, 1));
 }
 
-int tuned_pool_permille() {
+// The tails of a shared-prefix step take no pool: their CTAs start at different
+// times, which the split of the SMs allows for, and the pool's many small
+// partials cost the merge more than its balance gains (e4m3 batch of 256 98.0 us
+// with it, 95.2 without; 65536-token document 75.5 and 70.7; 4 groups of 32 103.7
+// and 104.8).
+int tuned_pool_permille(bool tails) {
   const int v = g_tune_pool.load();
-  return v == 0 ? kDefaultPoolPermille : (v < 0 ? 0 : v);
+  return v == 0 ? (tails ? 0 : kDefaultPoolPermille) : (v < 0 ? 0 : v);
 }
 
 int tuned_piece(bool fp8_decode) {
@@ -403,7 +408,7 @@ pa_status plan_decode(DeviceState* st, int ct, int qt, int kind, int64_t B, int 
   p->workers = p->grid * p->var.warps;
   const int mt = g_tune_min_tiles.load();
   p->min_tiles = mt > 0 ? mt : kDefaultMinTiles;
-  p->pool_permille = tuned_pool_permille();
+  p->pool_permille = tuned_pool_permille(kind == kTails);
   p->piece = tuned_piece(ct == pa::kE4M3 && kind != kChunked);
   return PA_OK;
 }
@@ -861,7 +866,7 @@ pa::SharedCost shared_cost(int D, bool fp8) {
   pa::SharedCost c;
   const float d = static_cast<float>(D) / 128.f;
   c.dual_ns = D == 64 ? 2600.f : 3500.f;
-  c.single_ns = D == 64 ? 2200.f : 3000.f;
+  c.single_ns = D == 64 ? 2200.f : (fp8 ? 3000.f : 4000.f);
   c.tail_ns = (fp8 ? 140.f : 190.f) * d;
   c.prefix_ns = 10000.f;
   c.decode_ns = 5000.f;
@@ -1086,6 +1091,15 @@ pa_status run_chunk_tc(const DecodeCall& c, cudaStream_t cs) {
   return ok();
 }
 
+// Whether a step with NG groups takes the shared path: its tables have to name
+// enough K/V.
+bool use_shared(const DecodeCall& c, int64_t NG) {
+  const int path = g_shared_path.load();
+  if (NG == 0 || path == 1) return false;
+  return path == 2 || dprod({double(c.B), double(c.MB), double(c.Hkv), double(c.bs), double(c.D), 2.0,
+                             c.fp8 ? 1.0 : 2.0}) >= kSharedMinBytes;
+}
+
 // Validation, planning and launch with the library's (or the caller's set)
 // workspace.
 pa_status decode_entry(const pa_tensor* out, const pa_tensor* q, const pa_tensor* key_cache,
@@ -1100,6 +1114,10 @@ pa_status decode_entry(const pa_tensor* out, const pa_tensor* q, const pa_tensor
                              chunked, &c);
   if (s) return s;
   if (c.B == 0) return ok();
+  if (sh && ((s = check_accessible(sh->prefix_lens, "prefix_lens")) ||
+             (s = check_accessible(sh->group_starts, "group_starts"))))
+    return s;
+  if (sh && !use_shared(c, sh->NG)) sh = nullptr;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (chunked && use_chunk_tc(c)) return run_chunk_tc(c, cs);
   DeviceState* st;
@@ -1114,21 +1132,6 @@ pa_status decode_entry(const pa_tensor* out, const pa_tensor* q, const pa_tensor
       return s;
   }
   return run_decode(c, st, plan, layout, ws, wsp, cs, sh);
-}
-
-// Whether a step with NG groups takes the shared path: its tables have to name
-// enough K/V. Tensors that check_decode() will refuse may get any answer.
-bool use_shared(int64_t NG, const pa_tensor* q, const pa_tensor* key_cache,
-                const pa_tensor* block_tables) {
-  const int path = g_shared_path.load();
-  if (NG == 0 || path == 1) return false;
-  if (path == 2) return true;
-  if (!q || !key_cache || !block_tables || q->ndim != 3 || key_cache->ndim != 4 ||
-      block_tables->ndim != 2)
-    return false;
-  return dprod({double(q->shape[0]), double(block_tables->shape[1]), double(key_cache->shape[1]),
-                double(key_cache->shape[2]), double(key_cache->shape[3]), 2.0,
-                double(elem_size(key_cache->dtype))}) >= kSharedMinBytes;
 }
 
 }  // namespace
@@ -1170,13 +1173,9 @@ pa_status pa_decode_shared(const pa_tensor* out, const pa_tensor* q, const pa_te
         return fail(PA_ERR_LAYOUT, "prefix_lens and group_starts must be aligned to their elements");
       if (overlaps(out, x)) return fail(PA_ERR_INVALID_ARG, "out overlaps an input");
     }
-    if (numel(out) > 0 && ((s = check_accessible(prefix_lens, "prefix_lens")) ||
-                           (s = check_accessible(group_starts, "group_starts"))))
-      return s;
     const SharedCall sh = {group_starts, prefix_lens, NG};
     return decode_entry(out, q, key_cache, value_cache, block_tables, seq_lens, num_kv_heads, scale,
-                        block_size, window, kv_dtype, k_scale, v_scale, stream, false,
-                        use_shared(NG, q, key_cache, block_tables) ? &sh : nullptr);
+                        block_size, window, kv_dtype, k_scale, v_scale, stream, false, &sh);
   });
 }
 

@@ -15,10 +15,10 @@ constexpr int kMaxThreads = 1024;
 constexpr unsigned kFull = 0xffffffffu;
 
 // Inclusive scan of x over the block with op (identity `zero`); *total
-// receives the whole block's value. one: only the first warp has values, and
+// receives the whole block's value. ONE: only the first warp has values, and
 // only it calls.
-template <typename Op>
-__device__ __forceinline__ int scan(bool one, int x, int zero, Op op, int* total) {
+template <bool ONE, typename Op>
+__device__ __forceinline__ int scan(int x, int zero, Op op, int* total) {
   __shared__ int s_w[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -26,7 +26,7 @@ __device__ __forceinline__ int scan(bool one, int x, int zero, Op op, int* total
     const int y = __shfl_up_sync(kFull, x, o);
     if (lane >= o) x = op(x, y);
   }
-  if (one) {
+  if constexpr (ONE) {
     *total = __shfl_sync(kFull, x, 31);
     return x;
   }
@@ -63,9 +63,10 @@ __device__ __forceinline__ int share_sms(const SharedPlanArgs& a, int tiles, int
   const float td = a.cost.tail_ns * tails;
   const int N = a.ctas;
   unsigned best = 0xffffffffu;
+#pragma unroll 1
   for (int n0 = 1; n0 < N; n0 += 32) {
     const int n = min(n0 + static_cast<int>(threadIdx.x & 31), N - 1);
-    const float t = fmaxf(a.cost.prefix_ns + tp / n, a.cost.decode_ns + td / (N - n));
+    const float t = fmaxf(a.cost.prefix_ns + __fdividef(tp, n), a.cost.decode_ns + __fdividef(td, N - n));
     // time in the upper bits (a positive float's bits order as the float), n below
     best = min(best, (__float_as_uint(t) & 0xfffffe00u) | static_cast<unsigned>(n & 511));
   }
@@ -73,6 +74,9 @@ __device__ __forceinline__ int share_sms(const SharedPlanArgs& a, int tiles, int
   return n > a.whole ? N : n;
 }
 
+// ONE: up to 31 groups, whose scans are the first warp's alone (a much shorter
+// program: most of the time goes by in its one pass through the instructions).
+template <bool ONE>
 __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPlanArgs a) {
   extern __shared__ int s_dyn[];
   Units* s_units = reinterpret_cast<Units*>(s_dyn);                // [NG]
@@ -87,10 +91,8 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
   const int cap = a.MB * a.bs;
   const auto add = [](int x, int y) { return x + y; };
   const auto most = [](int x, int y) { return x > y ? x : y; };
-  // up to 31 groups: the scans below are the first warp's alone
-  const bool one = a.NG < 32;
-  const bool mine = !one || tid < 32;
-  const int step = one ? 32 : nthreads;
+  const bool mine = !ONE || tid < 32;
+  const int step = ONE ? 32 : nthreads;
   griddep_launch_dependents();  // the prefix kernel sets itself up, then waits
   // The inputs are not the write path's: planning overlaps it. The workspace
   // it fills was last read by a kernel that an early-launching predecessor
@@ -120,7 +122,7 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
           s_first[g] = a.B;
         }
       }
-      const int y = most(scan(one, x, 0, most, &total), run);
+      const int y = most(scan<ONE>(x, 0, most, &total), run);
       if (g <= a.NG) {
         s_r0[g] = y;
         bad = bad || y != x;
@@ -187,16 +189,16 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
         x = a.Hkv * u.nut * u.nt;
         if (a.halves && u.up * a.G > a.unit_rows / 2) atomicAdd(&s_dual, x);
       }
-      const int y = scan(one, x, 0, add, &total);
+      const int y = scan<ONE>(x, 0, add, &total);
       if (g < a.NG) s_in[g] = run + y - x;
       run += total;
     }
-    if (one) __syncwarp(); else __syncthreads();
+    if constexpr (ONE) __syncwarp(); else __syncthreads();
     const int dual = s_dual;
     const int tiles = run;
     int ctas = a.ctas;
     if (tid < 32) ctas = share_sms(a, tiles, dual, s_tails * a.Hkv);
-    if (!one) {  // the first warp's answer, for all
+    if constexpr (!ONE) {  // the first warp's answer, for all
       if (tid == 0) s_wsz = ctas;
       __syncthreads();
       ctas = s_wsz;
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
         s_w0[g] = w0;
         if (u.nt > 0) x = (a.Hkv * u.nut + last / wsz - w0) * u.up;
       }
-      const int y = scan(one, x, 0, add, &total);
+      const int y = scan<ONE>(x, 0, add, &total);
       if (g < a.NG) s_base[g] = run + y - x;
       run += total;
     }
@@ -296,13 +298,14 @@ cudaError_t shared_plan_launch(const SharedPlanArgs& a, cudaStream_t s, bool pdl
   const size_t smem = (10 * static_cast<size_t>(a.NG) + 1) * sizeof(int);
   if (smem > 48 * 1024) {
     const cudaError_t e =
-        cudaFuncSetAttribute(reinterpret_cast<const void*>(shared_plan_kernel),
+        cudaFuncSetAttribute(reinterpret_cast<const void*>(shared_plan_kernel<false>),
                              cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(a.B <= 512 && a.NG < 32 ? 256 : kMaxThreads);
+  const bool one = a.NG < 32;
+  cfg.blockDim = dim3(a.B <= 1024 && one ? 256 : kMaxThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -310,7 +313,8 @@ cudaError_t shared_plan_launch(const SharedPlanArgs& a, cudaStream_t s, bool pdl
   attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, shared_plan_kernel, a);
+  return one ? cudaLaunchKernelEx(&cfg, shared_plan_kernel<true>, a)
+             : cudaLaunchKernelEx(&cfg, shared_plan_kernel<false>, a);
 }
 
 }  // namespace pa

@@ -1,0 +1,63 @@
+"""The compiled binding of the hot calls and the ctypes route reach the same
+library: same statuses and messages for the same arguments, on the host."""
+import pytest
+import torch
+
+import paged_kv_cache_267_gb300 as pa
+
+pytestmark = pytest.mark.skipif(torch.cuda.is_available(), reason="host tensors, stopped by the missing device")
+
+
+@pytest.fixture(scope="module")
+def routes(pa_lib):
+    binding = pytest.importorskip("paged_kv_cache_267_gb300._pa_torch")
+    return binding, pa._CtypesCalls()
+
+
+def call_args():
+    B, Hq, Hkv, D, NB, bs, MB, T = 3, 8, 2, 128, 10, 16, 4, 5
+    bf, i32 = torch.bfloat16, torch.int32
+    cache = lambda: torch.zeros(NB, Hkv, bs, D, dtype=bf)  # noqa: E731
+    q = torch.zeros(B, Hq, D, dtype=bf)
+    tables, lens = torch.zeros(B, MB, dtype=i32), torch.zeros(B, dtype=i32)
+    row = torch.zeros(T, (Hq + 2 * Hkv) * D, dtype=bf)
+    qkv = [t.view(T, -1, D) for t in row.split([Hq * D, Hkv * D, Hkv * D], 1)]
+    slots, pos = torch.zeros(T, dtype=torch.int64), torch.zeros(T, dtype=i32)
+    free, state = torch.zeros(NB, dtype=i32), torch.zeros(2, dtype=i32)
+    attend = [torch.empty_like(q), q, cache(), cache(), tables, lens]
+    return dict(
+        pa_decode=attend + [Hkv, 0.1, bs, 0, 0, 1.0, 1.0],
+        pa_decode_shared=attend + [torch.zeros(1, dtype=i32), torch.zeros(2, dtype=i32), Hkv, 0.1, bs, 0, 0, 1.0, 1.0],
+        pa_prefill_chunk=[t.unsqueeze(1) for t in attend[:2]] + attend[2:] + [Hkv, 0.1, bs, 0, 0, 1.0, 1.0],
+        pa_reshape_and_cache=[qkv[1], qkv[2], cache(), cache(), slots, 0, 1.0, 1.0],
+        pa_norm_rope_and_cache=[torch.empty(T, Hq, D, dtype=bf), *qkv, cache(), cache(), slots, pos,
+                                torch.zeros(9, 64), None, torch.zeros(D, dtype=bf), 1e-6, 1, 0, 1.0, 1.0],
+        pa_pool_extend=[tables, lens, lens.clone(), free, state, lens.clone(), state.clone(),
+                        torch.zeros(B + 1, dtype=i32), slots, pos, bs],
+        pa_pool_release=[tables, lens, lens.clone(), None, free, state, lens.clone(), state.clone(), bs])
+
+
+@pytest.mark.parametrize("name", list(call_args()))
+def test_routes_agree(routes, name):
+    args = call_args()[name]
+    seen = {}
+    for i, x in enumerate(args):
+        for other in ([None, x.to(torch.float64) if x.dtype != torch.float64 else x, x.flatten()[1:], x.unsqueeze(0)]
+                      if isinstance(x, torch.Tensor) else [x]):
+            if isinstance(other, torch.Tensor) and other.dtype not in pa._TORCH_TO_PA:
+                continue
+            got = []
+            for route in routes:
+                status = getattr(route, name)(*args[:i], other, *args[i + 1:], 0)
+                got.append((status, pa.last_error()))
+            assert got[0] == got[1], (name, i, got)
+            seen[got[0][0]] = seen.get(got[0][0], 0) + 1
+    assert -1 in seen and -4 in seen, seen      # refusals, and fine calls stopped by the missing device
+
+
+def test_unknown_type(routes):
+    args = call_args()["pa_decode"]
+    args[1] = args[1].to(torch.float64)
+    for route in routes:
+        with pytest.raises((TypeError, KeyError)):
+            getattr(route, "pa_decode")(*args, 0)

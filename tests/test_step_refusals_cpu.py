@@ -182,3 +182,77 @@ def test_pool_refusals(pool):
     assert release(lens_out=i((3,), 0x1000), state_out=i((2,), 0x4000)) == -4
     too_many = dict(tables=i((4097, 4), 1 << 30), lens=i((4097,), 1 << 31), lens_out=i((4097,), 1 << 32))
     assert extend(new=i((4097,), 1 << 33), start=i((4098,), 1 << 34), **too_many) == UNSUP
+
+
+@pytest.fixture
+def shared(pa_lib):
+    pa = pa_lib
+    B, Hq, Hkv, D, NB, bs, MB, NG = 6, 8, 2, 128, 20, 16, 9, 2
+
+    def call(heads=Hkv, scale=0.1, bs=bs, window=0, kv=0, ks=1.0, vs=1.0, **over):
+        d = lambda dt, shape, at: _desc(pa, dt, shape, BASE + at)  # noqa: E731
+        a = dict(out=d(pa.PA_BF16, (B, Hq, D), 0x100000), q=d(pa.PA_BF16, (B, Hq, D), 0),
+                 kc=d(pa.PA_BF16, (NB, Hkv, bs, D), 0x200000), vc=d(pa.PA_BF16, (NB, Hkv, bs, D), 0x400000),
+                 tables=d(pa.PA_I32, (B, MB), 0x600000), lens=d(pa.PA_I32, (B,), 0x610000),
+                 prefix=d(pa.PA_I32, (NG,), 0x620000), starts=d(pa.PA_I32, (NG + 1,), 0x630000))
+        a.update(over)
+        return pa.lib().pa_decode_shared(*refs(a.values()), heads, scale, bs, window, kv, ks, vs, None)
+
+    return pa, call
+
+
+@pytest.mark.parametrize("path", [0, 1, 2])
+def test_shared_refusals(shared, path):
+    """The same answers whichever kernels the call would take."""
+    pa, call = shared
+    d = lambda dt, shape, at: _desc(pa, dt, shape, BASE + at)  # noqa: E731
+    bf, f16, i32, i64, e4 = pa.PA_BF16, pa.PA_F16, pa.PA_I32, pa.PA_I64, pa.PA_FP8_E4M3
+    pa.set_shared_path(path)
+    try:
+        assert call() == -4, pa.last_error()       # fine: stopped by the missing device only
+        none = dict(prefix=d(i32, (0,), 0x620000), starts=d(i32, (1,), 0x630000))
+        assert call(**none) == -4
+        for want, over in [
+            (ARG, {n: None}) if isinstance(n, str) else n for n in [
+                "out", "q", "kc", "vc", "tables", "lens", "prefix", "starts",
+                (ARG, dict(prefix=d(i64, (2,), 0x620000))), (ARG, dict(starts=d(i64, (3,), 0x630000))),
+                (ARG, dict(starts=d(i32, (2,), 0x630000))), (ARG, dict(prefix=d(i32, (3,), 0x620000))),
+                (ARG, dict(prefix=d(i32, (2, 1), 0x620000))),
+                (LAYOUT, dict(prefix=strided(pa, i32, (2,), (2,), BASE + 0x620000))),
+                (LAYOUT, dict(starts=strided(pa, i32, (3,), (0,), BASE + 0x630000))),
+                (LAYOUT, dict(starts=d(i32, (3,), 0x630002))),
+                (UNSUP, dict(prefix=d(i32, (4097,), 0x1000000), starts=d(i32, (4098,), 0x2000000))),
+                (ARG, dict(prefix=d(i32, (2,), 0x100000 + 8))),           # under out
+                (ARG, dict(starts=d(i32, (3,), 0x100000 - 8))),
+                (ARG, dict(out=d(bf, (6, 8, 128), 0x610000 - 16))),       # over the lengths
+                (ARG, dict(out=d(bf, (6, 8, 128), 0x200000))),
+                (ARG, dict(out=d(f16, (6, 8, 128), 0x100000))), (ARG, dict(out=d(bf, (6, 7, 128), 0x100000))),
+                (ARG, dict(heads=4)), (ARG, dict(scale=float("nan"))), (ARG, dict(kv=1)),
+                (ARG, dict(tables=d(i32, (5, 9), 0x600000))), (ARG, dict(lens=d(i64, (6,), 0x610000))),
+                (ARG, dict(tables=d(i32, (6, 0), 0x600000))),
+                (LAYOUT, dict(q=d(bf, (6, 8, 128), 4))),
+                (LAYOUT, dict(tables=strided(pa, i32, (6, 9), (12, 1), BASE + 0x600000))),
+                (ARG, dict(kv=2)),                                        # e4m3 asked, bf16 caches
+                (ARG, dict(kv=2, vs=0.0, kc=d(e4, (20, 2, 16, 128), 0x200000),
+                           vc=d(e4, (20, 2, 16, 128), 0x400000))),
+                (UNSUP, dict(q=d(bf, (6, 8, 96), 0), out=d(bf, (6, 8, 96), 0x100000),
+                             kc=d(bf, (20, 2, 16, 96), 0x200000), vc=d(bf, (20, 2, 16, 96), 0x400000))),
+            ]]:
+            got = call(**over)
+            assert got == want, (got, want, sorted(over), pa.last_error())
+        # no sequences: nothing to do, before any device
+        assert call(q=d(bf, (0, 8, 128), 0), out=d(bf, (0, 8, 128), 0x100000), tables=d(i32, (0, 9), 0x600000),
+                    lens=d(i32, (0,), 0x610000)) == 0
+    finally:
+        pa.set_shared_path(0)
+
+
+def test_shared_settings(shared):
+    pa, _ = shared
+    for bad in (-1, 3):
+        with pytest.raises(pa.PAError):
+            pa.set_shared_path(bad)
+    for bad in (dict(num_groups=-1), dict(num_groups=4097), dict(batch=4097), dict(head_dim=96), dict(num_kv_heads=3)):
+        with pytest.raises(pa.PAError):
+            pa.decode_shared_workspace_size(**{**dict(batch=4, num_groups=1, num_q_heads=8, num_kv_heads=2, head_dim=128),
+                                               **bad})
