@@ -142,7 +142,8 @@ __device__ __forceinline__ bool commit_turn(bool in_place, int32_t* ticket) {
   __shared__ int s_last;
   if (threadIdx.x == 0) {
     __threadfence();
-    s_last = atomicAdd(ticket, 1) == static_cast<int>(gridDim.x) - 1;
+    // (wraps to zero for the next call, whichever of the two is in place)
+    s_last = atomicInc(reinterpret_cast<unsigned*>(ticket), gridDim.x - 1) == gridDim.x - 1;
   }
   __syncthreads();
   return s_last != 0;

@@ -8,8 +8,6 @@
 
 namespace pa {
 
-// The block pool (pool_ops.cu). in_place: lens_out is lens, or state_out is
-// state; the last CTA to have read them then writes them.
 // Division of 31-bit integers by a fixed d as a multiplication.
 struct FastDiv {
   uint32_t mul, shift;
@@ -21,6 +19,8 @@ inline FastDiv fast_div(uint32_t d) {
   while ((1ull << l) < d) ++l;
   return FastDiv{static_cast<uint32_t>(((1ull << (31 + l)) + d - 1) / d), l - 1};
 }
+// The block pool (pool_ops.cu). in_place: lens_out is lens, or state_out is
+// state; the last CTA to have read them then writes them.
 struct PoolExtendArgs {
   int32_t* tables;               // [B, MB]
   const int32_t* lens;           // [B] before the step

@@ -204,6 +204,40 @@ def test_a_step_that_does_not_fit_changes_nothing(B, new, T, bit, in_place, pa_l
     assert pa_lib.check_device_error() == 0
 
 
+@pytest.mark.parametrize("which", ["seq_lens_out", "pool_state_out"])
+@pytest.mark.parametrize("B", [5, 700])
+def test_only_one_of_lengths_and_state_in_place(B, which, pa_lib):
+    """The other one's input stays as it was, so it can be used again."""
+    bs, MB, T = 16, 4, 64 * B
+    new = [(7 * b) % 30 for b in range(B)]
+    gone = [b % 3 == 0 for b in range(B)]
+    g = Gpu(pa_lib, Pool(B, MB, bs, 4 * B, seed=5))
+    for _ in range(3):
+        m = Pool(B, MB, bs, 4 * B, seed=5)
+        g.tables.fill_(-1)
+        g.lens.copy_(torch.from_numpy(m.lens)), g.free.copy_(torch.from_numpy(m.free)), g.state.copy_(i32([m.count, 0]))
+        for step in range(2):
+            for call in ("extend", "release"):
+                out = torch.full_like(g.lens if which == "seq_lens_out" else g.state, -9)
+                before = g.lens.clone(), g.state.clone()
+                g.step(T)
+                if call == "extend":
+                    pa_lib.pool_extend(g.tables, g.lens, i32(new), g.free, g.state, block_size=bs, slot_mapping=g.slots,
+                                       positions=g.pos, query_start=g.start, **{which: out})
+                    g.same_step(m.extend(new, T))
+                else:
+                    pa_lib.pool_release(g.tables, g.lens, i32(gone), g.free, g.state, block_size=bs, **{which: out})
+                    m.release(gone)
+                if which == "seq_lens_out":
+                    assert torch.equal(g.lens, before[0])
+                    g.lens = out
+                else:
+                    assert torch.equal(g.state, before[1])
+                    g.state = out
+                g.same_state(m)
+    assert pa_lib.check_device_error() == 0
+
+
 def test_release_beyond_the_free_list_and_bad_lengths_change_nothing(pa_lib):
     m = Pool(2, 4, 16, 8, seed=3)
     m.extend([40, 40], 80)
