@@ -258,7 +258,10 @@ __global__ void __launch_bounds__(kThreads, kHeads > 1 ? 3 : 4) norm_cache_kerne
   }
   // the heads' norms, interleaved: a head behind nh is zeros and goes nowhere
   const float inv_d = 1.f / static_cast<float>(a.D);
-  const float inv_scale = kind == 1 && FP8 ? 1.f / a.k_scale : 1.f;
+  // (a scale whose reciprocal, times a norm, could leave fp32's range divides
+  // the values instead)
+  const bool scaled = kind == 1 && FP8, wild = scaled && !(a.k_scale >= 0x1p-60f && a.k_scale <= 0x1p60f);
+  const float inv_scale = scaled && !wild ? 1.f / a.k_scale : 1.f;
   float rn[kHeads];
   if (weight) {
     const unsigned members =
@@ -295,7 +298,11 @@ __global__ void __launch_bounds__(kThreads, kHeads > 1 ? 3 : 4) norm_cache_kerne
     }
     order_of<INTER>(yl, yh, e);
     if (stored && j < nh) {
-      if (FP8 && kind == 1) {
+      if (scaled) {
+        if (wild) {
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i) e[i] = make_float2(e[i].x / a.k_scale, e[i].y / a.k_scale);
+        }
         store_codes(dst, e);
       } else {
         Raw y;

@@ -282,12 +282,21 @@ pa_status pa_norm_rope_and_cache(const pa_tensor* q_out, const pa_tensor* q, con
     if (numel(key_cache) > 0 && overlaps(key_cache, value_cache))
       return fail(PA_ERR_INVALID_ARG, "key and value caches overlap");
     const bool in_place = q_out->data == q->data && q_out->strides[0] == q->strides[0];
+    // Rows of x between rows of q_out: of one row stride, and in every row
+    // behind q_out's heads and before its next row.
+    auto between_rows = [&](const pa_tensor* x) {
+      const int64_t row = q_out->strides[0] * 2;  // bytes
+      if (T < 2 || x->strides[0] != q_out->strides[0]) return false;
+      int64_t at = (static_cast<const char*>(x->data) - static_cast<const char*>(q_out->data)) % row;
+      if (at < 0) at += row;
+      return at >= Hq * D * 2 && at + Hkv * D * 2 <= row;
+    };
     for (const pa_tensor* x : {q, k, v, slot_mapping, positions, cos_sin, q_weight, k_weight}) {
       if (!x) continue;
       if (overlaps(key_cache, x) || overlaps(value_cache, x))
         return fail(PA_ERR_INVALID_ARG, "a cache overlaps an input");
-      // q_out in q's place: the packed rows of k and v lie between its rows
-      if (!(in_place && (x == q || x == k || x == v)) && overlaps(q_out, x))
+      // q_out in q's place: packed rows of k and v lie between its rows
+      if (!(in_place && (x == q || ((x == k || x == v) && between_rows(x)))) && overlaps(q_out, x))
         return fail(PA_ERR_INVALID_ARG, "q_out overlaps an input");
     }
     if (overlaps(q_out, key_cache) || overlaps(q_out, value_cache))

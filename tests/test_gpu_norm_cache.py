@@ -156,6 +156,29 @@ def test_v_codes_equal_the_plain_write_paths_for_every_pattern(src, scale, pa_li
         assert ((x[nan] & 0x7F) == 0x7F).all()
 
 
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("T", [5, 2100])
+@pytest.mark.parametrize("scale", [1e-40, 1e-25, 0.02, 1e25, 3e38])
+def test_keys_at_any_scale(scale, T, norm, pa_lib):
+    """Keys of up to about 448 times the scale, inside fp32's range with a
+    factor of 30 for the products and sums on the way."""
+    D = 128
+    packed, q, k, v, kc, vc, slots, pos, cs, (_, wk) = make(T, 8, 2, D, "bf16", True, skipped=0, seed=3)
+    sc = float(np.float32(scale))
+    size = min(100 * sc, 1e37)
+    if norm:
+        wk = (wk.double() * size).to(torch.bfloat16)
+    else:
+        wk = None
+        k.copy_(k.double() * size / 5)
+    k[0].zero_()
+    k0 = kc.clone()
+    pa_lib.norm_rope_and_cache(q, k, v, kc, vc, slots, pos, cs, k_weight=wk, eps=1e-5, kv_dtype="fp8", k_scale=sc)
+    ref, slack = reference(k, wk, cs, pos, D, False, float(np.float32(1e-5)))
+    # a product below fp32's least normal number is off by 2^-149, four of them a pair
+    check_cache(kc, k0, ref, slack + 2.0 ** -146, slots, "e4m3", sc, f"k at {scale}")
+
+
 @pytest.mark.parametrize("T", [3, 3000])
 def test_in_place_and_strided_outputs(T, pa_lib):
     packed, q, k, v, kc, vc, slots, pos, cs, (wq, wk) = make(T, 8, 2, 128, "bf16", False, extra_cols=24)

@@ -99,8 +99,15 @@ def test_norm_refusals(norm):
     ]:
         got = norm(**over)
         assert got == want, (got, want, sorted(over), pa.last_error())
-    # q's own place is fine
-    assert norm(out=norm.rows(4, 128, W, 0)) == -4
+    # q's own place is fine, but not where k or v are rows of q themselves
+    own = norm.rows(4, 128, W, 0)
+    assert norm(out=own) == -4
+    assert norm(out=own, k=norm.rows(2, 128, W, 768), v=norm.rows(2, 128, W, 512)) == -4
+    assert norm(out=own, k=norm.rows(2, 128, W, 256)) == ARG
+    assert norm(out=own, v=norm.rows(2, 128, W, 2 * W + 128)) == ARG
+    assert norm(out=own, v=norm.rows(2, 128, W, W - 128)) == ARG      # ends in the next row's q
+    assert norm(out=own, v=norm.rows(2, 128, 2 * W, 768)) == ARG      # another stride
+    assert norm(out=own, v=norm.rows(2, 128, W, 9 * W + 384)) == -4   # beyond the last row
     for D in (8, 264, 272):
         assert norm(q=norm.rows(4, D, 8 * D, 0), out=d(bf, (5, 4, D), 0x100000), k=norm.rows(2, D, 8 * D, 4 * D),
                     v=norm.rows(2, D, 8 * D, 6 * D), kc=d(bf, (6, 2, 16, D), 0x200000), vc=d(bf, (6, 2, 16, D), 0x400000),
