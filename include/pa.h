@@ -251,20 +251,22 @@ pa_status pa_pool_release(const pa_tensor* block_tables, const pa_tensor* seq_le
  * run to run (pa_set_decode_tuning can turn the dynamic share off).
  *
  * Ordering: the kernels use programmatic dependent launch. The decode kernel
- * reads q, block_tables and seq_lens (and plans the step) before it waits for
- * the previous kernel of the stream, and reads the caches only after. A
+ * reads block_tables and seq_lens (and plans the step) before it waits for
+ * the previous kernel of the stream, and reads q and the caches only after. A
  * predecessor that lets its dependents start early (as pa_reshape_and_cache
- * does) must therefore have written q, block_tables and seq_lens before doing
- * so; ordinary kernels and copies are waited for in full.
+ * and pa_norm_rope_and_cache do) must therefore have written block_tables and
+ * seq_lens before doing so; ordinary kernels and copies are waited for in full.
  *
  * Workspace: the step writes per-segment partial results (running max, sum
  * and unnormalised output), its plan and three counter words (zero again
  * when the step ends) to a device workspace of pa_decode_workspace_size()
  * bytes. It is the buffer
  * given to pa_set_workspace() for the current device, or else a buffer the
- * library allocates (and zeroes) once per (device, stream) outside stream
- * capture and keeps. Calls that overlap on the GPU must not share a
- * workspace.
+ * library allocates (and zeroes) per (device, stream) outside stream
+ * capture and keeps, with any larger one that a later step needs: a captured
+ * graph goes on using the one that it was captured with. Calls that overlap on
+ * the GPU must not share a workspace. Host threads may call at once: the
+ * launches of one step are not torn apart.
  */
 pa_status pa_decode(const pa_tensor* out, const pa_tensor* q, const pa_tensor* key_cache,
                     const pa_tensor* value_cache, const pa_tensor* block_tables,

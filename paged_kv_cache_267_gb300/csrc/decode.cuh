@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
   // seq_lens) overlaps the previous kernel of the stream.
   // A kernel of this library that lets dependents start early (the write
   // path) does so only once its own predecessors have finished, and it
-  // writes none of q, seq_lens, block_tables or this workspace, only the
+  // writes none of seq_lens, block_tables or this workspace, only q and the
   // caches, which are first read after the wait.
   griddep_launch_dependents();
 

@@ -318,10 +318,20 @@ pa_status make_cache_map(CUtensorMap* map, const void* base, int64_t rows, int D
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(D) * elt};
   cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elt), static_cast<cuuint32_t>(pa::kTile)};
   cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(map, elt == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
-                  2, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  auto encode = [&] {
+    return fn(map, elt == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
+              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = encode();
+  if (r == CUDA_ERROR_INVALID_CONTEXT) {  // a host thread's first call: bind the device's context
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaSetDevice(dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
+    r = encode();
+  }
   if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return PA_OK;
 }
@@ -439,23 +449,22 @@ pa_status get_workspace(DeviceState* st, cudaStream_t stream, const WsLayout& la
                     "decode workspace must grow to %zu bytes during stream capture; run one "
                     "step before capturing or call pa_set_workspace",
                     need);
-      if (w->ptr) {
-        e = cudaStreamSynchronize(stream);
-        if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
-        cudaFree(w->ptr);
-        *w = Workspace{};
-      }
-      const size_t bytes = round_up(need + need / 4, 1 << 20);
+      // The old buffer stays: a captured graph may replay steps in it. Each is at
+      // least twice the last, so all that stay are smaller than the one in use.
+      size_t bytes = round_up(std::max(need + need / 4, 2 * w->bytes), 1 << 20);
       void* p = nullptr;
       e = cudaMalloc(&p, bytes);
+      if (e == cudaErrorMemoryAllocation && bytes > need) {  // without the room to grow, then
+        cudaGetLastError();
+        e = cudaMalloc(&p, bytes = need);
+      }
       if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(workspace)");
       e = cudaMemsetAsync(p, 0, bytes, stream);
       if (e != cudaSuccess) {
         cudaFree(p);
         return cuda_fail(e, "cudaMemsetAsync(workspace)");
       }
-      w->ptr = p;
-      w->bytes = bytes;
+      *w = Workspace{p, bytes, false};
     }
   }
   if (w->dirty) {
@@ -1120,6 +1129,10 @@ pa_status decode_entry(const pa_tensor* out, const pa_tensor* q, const pa_tensor
   if (sh && !use_shared(c, sh->NG)) sh = nullptr;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (chunked && use_chunk_tc(c)) return run_chunk_tc(c, cs);
+  // a step's launches follow one another on their stream, whichever host
+  // threads call: the next step in the same workspace comes behind them
+  static std::mutex in_order;
+  std::lock_guard<std::mutex> launches(in_order);
   DeviceState* st;
   DecodePlan plan;
   WsLayout layout;

@@ -570,7 +570,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           if (grow) ms = mx;
         }
         // P = 2^(s * sc - ms), packed in pairs over the columns of the scores
-        // just used; the last half is still in registers
+        // just used; the last half is still in registers. It is rounded to the
+        // products' 16-bit type, which the tensor core needs beside V's: at most
+        // half a step of each weight (2^-8 bf16, 2^-11 f16), against sums in fp32 of
+        // the unrounded ones.
         const float2 sc2 = make_float2(sc, sc), nms2 = make_float2(-ms, -ms);
         float2 sp[4];
 #pragma unroll
@@ -641,8 +644,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         tc::fence_after_sync();
         const float2 o = ld2(trow + C::kColS + C::kKv * (1 - x));
         const float m = fmaxf(ms, o.x);
-        f_own = nj > 0 ? ex2(ms - m) : 0.f;
-        f_other = x == 1 || sg.nt > 1 ? ex2(o.x - m) : 0.f;  // a lone tile is group 0's
+        f_own = ex2(ms - m);
+        f_other = ex2(o.x - m);
         l = l * f_own + o.y * f_other;
         ms = m;
       } else if (NX == 2) {
@@ -661,7 +664,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       auto staged = [&](int row, int c) -> uint32_t {
         return sQ + x * C::kQBytes + (c >> 3) * C::kQBox + row * 128 + (((c & 7) ^ (row & 7)) << 4);
       };
-      if (!ok) f_own = f_other = 0.f;
+      // Whether there is an O to take: uniform over the warp, and whatever it weighs
+      // (a NaN in it stays one). A lone tile is group 0's.
+      const bool take_own = ok && nj > 0, take_other = ok && join && (x == 1 || sg.nt > 1);
       f_own *= a.v_scale;
       f_other *= a.v_scale;
 #pragma unroll 1
@@ -671,20 +676,19 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           uint32_t ov[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) ov[i] = 0u;
-          if (f_own != 0.f || __any_sync(kFull, f_own != 0.f)) {
+          if (take_own) {
             tc::ld32_async(tO + half * (D / 2) + d0, ov);
             tc::wait_ld(ov);
           }
           float* o = reinterpret_cast<float*>(ov);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = f_own != 0.f ? o[i] * f_own : 0.f;
-          if (join && __any_sync(kFull, f_other != 0.f)) {
+          for (int i = 0; i < 32; ++i) o[i] *= f_own;
+          if (take_other) {
             uint32_t ow[32];
             tc::ld32_async(trow + C::kColO + D * (1 - x) + half * (D / 2) + d0, ow);
             tc::wait_ld(ow);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              o[i] = f_other != 0.f ? fmaf(__uint_as_float(ow[i]), f_other, o[i]) : o[i];
+            for (int i = 0; i < 32; ++i) o[i] = fmaf(__uint_as_float(ow[i]), f_other, o[i]);
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i)

@@ -214,6 +214,49 @@ def test_scores_that_grow_along_the_prefix(shape, pa_lib):
     assert pa_lib.check_device_error() == 0
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("heavy", [0, 1])
+def test_halves_of_a_unit_whose_weights_vanish_for_some_rows(heavy, fp8, pa_lib):
+    """K along one query on every other tile of 128: for its row one half of the
+    unit outweighs the other by more than fp32's range, for the other rows not.
+    |score| <= 120 with D = 128 keeps the bound on the scores' error above."""
+    b = Batch([(1200, [4, 30, 1])], dt="f16", fp8=fp8, seed=9)
+    blocks = torch.from_numpy(b.tables[0, :75].astype(np.int64)).cuda()
+    on = blocks[(torch.arange(75, device="cuda") // 8) % 2 == heavy]
+    for h in range(2):
+        d = b.q[1, 4 * h + 2].float()
+        d = d * (119 / b.scale / d.square().sum())
+        row = d.to(torch.float16)
+        if fp8:
+            row = (d / b.ks).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        b.kc[on, h] = row
+    b.check(b.run(pa_lib), what=f"heavy {heavy}")
+    assert pa_lib.check_device_error() == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("where", ["k", "v"])
+@pytest.mark.parametrize("tile", [0, 1, 9])
+@pytest.mark.parametrize("rows", [3, 40])
+def test_a_nan_that_is_attended_to_shows(rows, tile, where, fp8, pa_lib):
+    """One NaN among the shared keys or values of KV head 1: its heads' outputs
+    are NaN (one element of them, for a value), the other heads' are as ever."""
+    b = Batch([(1200, [4] * rows)], loose_after=(50,), dt="f16", fp8=fp8, seed=9)
+    block = int(b.tables[0, tile * 8 + 2])
+    cache = b.kc if where == "k" else b.vc
+    cache[block, 1, 5, 77] = 0x7F if fp8 else float("nan")
+    out = b.run(pa_lib)
+    bad = torch.zeros(out.shape, dtype=torch.bool, device="cuda")
+    bad[:rows, 4:, slice(None) if where == "k" else slice(77, 78)] = True
+    assert torch.equal(out.isnan(), bad)
+    cache[block, 1, 5, 77] = 0          # and the rest is what it is without it
+    clean = b.run(pa_lib)
+    b.check(clean)
+    heads = ~bad.any(-1)
+    assert (out[heads].float() - clean[heads].float()).abs().max() <= 2.0 ** -6
+    assert pa_lib.check_device_error() == 0
+
+
 def test_agrees_with_decode_and_no_groups_is_decode(pa_lib):
     b = Batch([(640, [9, 3, 100]), (128, [1, 1])], seed=11)
     a = b.args()
@@ -320,6 +363,66 @@ def test_other_streams_and_shapes_in_turn(pa_lib):
     for k, b in enumerate(bs):
         for o in outs[k]:
             b.check(o)
+    assert pa_lib.check_device_error() == 0
+
+
+def test_threads_calling_on_one_stream(pa_lib):
+    """Steps of different shapes from two host threads on the same stream: their
+    launches must not mix in the stream's one workspace."""
+    import threading
+    bs = [Batch([(640, [9] * 40)], seed=14), Batch([(64, [2, 3]), (1600, [7, 8, 9])], seed=15)]
+    args = [b.args() for b in bs]
+    s = torch.cuda.Stream()
+    outs = [[torch.empty_like(b.q) for _ in range(60)] for b in bs]
+    torch.cuda.synchronize()
+    for b, a, o in zip(bs, args, outs):  # the workspace grows here
+        pa_lib.decode_shared(*a, out=o[0], stream=s, **b.kw())
+    errors = []
+
+    def calls(k):
+        try:
+            for i, o in enumerate(outs[k]):
+                if (i + k) % 5 == 4:
+                    pa_lib.decode(*args[k][:5], out=o, stream=s, **bs[k].kw())
+                else:
+                    pa_lib.decode_shared(*args[k], out=o, stream=s, **bs[k].kw())
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=calls, args=(k,)) for k in range(2)]
+    pa_lib.set_shared_path(2)
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    assert pa_lib.check_device_error() == 0
+    for k, b in enumerate(bs):
+        ref = torch.stack(outs[k]).float()
+        b.check(outs[k][0])
+        # the same values up to the order of summation
+        assert (ref - ref[0]).abs().max() <= 2.0 ** -6
+
+
+def test_a_graph_outlives_a_larger_step_on_its_stream(pa_lib):
+    small, large = Batch([(640, [9, 30, 1, 60])], seed=16), Batch([(512, [9] * 200)], heads=(16, 8), seed=17)
+    args = small.args()
+    out = torch.empty_like(small.q)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        pa_lib.decode_shared(*args, out=out, **small.kw())
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            pa_lib.decode_shared(*args, out=out, **small.kw())
+        for _ in range(3):
+            large.check(large.run(pa_lib))      # the stream's workspace grows
+            out.fill_(float("nan"))
+            graph.replay()
+            torch.cuda.synchronize()
+            small.check(out)
     assert pa_lib.check_device_error() == 0
 
 
