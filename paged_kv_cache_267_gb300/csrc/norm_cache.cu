@@ -29,6 +29,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "pa_internal.h"
 #include "ptx.cuh"
 #include "step_ops.h"
@@ -258,10 +260,12 @@ __global__ void __launch_bounds__(kThreads, kHeads > 1 ? 3 : 4) norm_cache_kerne
   }
   // the heads' norms, interleaved: a head behind nh is zeros and goes nowhere
   const float inv_d = 1.f / static_cast<float>(a.D);
-  // (a scale whose reciprocal, times a norm, could leave fp32's range divides
-  // the values instead)
+  // (a scale whose reciprocal, times a norm, could leave fp32's range: the values
+  // go through a power of two instead, which brings the scale nearer to 1 and
+  // loses nothing that has a code other than zero or the largest)
   const bool scaled = kind == 1 && FP8, wild = scaled && !(a.k_scale >= 0x1p-60f && a.k_scale <= 0x1p60f);
   const float inv_scale = scaled && !wild ? 1.f / a.k_scale : 1.f;
+  const float near = a.k_scale < 1.f ? 0x1p100f : 0x1p-100f;
   float rn[kHeads];
   if (weight) {
     const unsigned members =
@@ -286,35 +290,46 @@ __global__ void __launch_bounds__(kThreads, kHeads > 1 ? 3 : 4) norm_cache_kerne
 #pragma unroll
     for (int j = 0; j < kHeads; ++j) rn[j] = inv_scale;
   }
+  auto finish = [&](auto is_wild) {  // (apart: in one loop the branch costs 4 us of 71)
 #pragma unroll
-  for (int j = 0; j < kHeads; ++j) {
-    float2 lo[4], hi[4], yl[4], yh[4], e[8];
-    pairs_of<ST, INTER>(x[j], lo, hi);
-    const float2 r2 = make_float2(rn[j], rn[j]);
+    for (int j = 0; j < kHeads; ++j) {
+      float2 lo[4], hi[4], yl[4], yh[4], e[8];
+      pairs_of<ST, INTER>(x[j], lo, hi);
+      const float2 r2 = make_float2(rn[j], rn[j]);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      yl[q] = __fmul2_rn(__ffma2_rn(hi[q], B[q], __fmul2_rn(lo[q], A[q])), r2);
-      yh[q] = __fmul2_rn(__ffma2_rn(lo[q], E[q], __fmul2_rn(hi[q], C[q])), r2);
-    }
-    order_of<INTER>(yl, yh, e);
-    if (stored && j < nh) {
-      if (scaled) {
-        if (wild) {
-#pragma unroll 1
-          for (int i = 0; i < 8; ++i) e[i] = make_float2(e[i].x / a.k_scale, e[i].y / a.k_scale);
-        }
-        store_codes(dst, e);
-      } else {
-        Raw y;
-        y.a = make_uint4(pack2<ST>(e[0].x, e[0].y), pack2<ST>(e[1].x, e[1].y), pack2<ST>(e[2].x, e[2].y),
-                         pack2<ST>(e[3].x, e[3].y));
-        y.b = make_uint4(pack2<ST>(e[4].x, e[4].y), pack2<ST>(e[5].x, e[5].y), pack2<ST>(e[6].x, e[6].y),
-                         pack2<ST>(e[7].x, e[7].y));
-        store_raw(reinterpret_cast<uint16_t*>(dst), ea, eb, y);
+      for (int q = 0; q < 4; ++q) {
+        yl[q] = __fmul2_rn(__ffma2_rn(hi[q], B[q], __fmul2_rn(lo[q], A[q])), r2);
+        yh[q] = __fmul2_rn(__ffma2_rn(lo[q], E[q], __fmul2_rn(hi[q], C[q])), r2);
       }
+      order_of<INTER>(yl, yh, e);
+      if (stored && j < nh) {
+        if (scaled) {
+          if constexpr (is_wild.value) {
+            const float inv = 1.f / (a.k_scale * near);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              e[i] = __fmul2_rn(__fmul2_rn(e[i], make_float2(near, near)), make_float2(inv, inv));
+          }
+          store_codes(dst, e);
+        } else {
+          Raw y;
+          y.a = make_uint4(pack2<ST>(e[0].x, e[0].y), pack2<ST>(e[1].x, e[1].y), pack2<ST>(e[2].x, e[2].y),
+                           pack2<ST>(e[3].x, e[3].y));
+          y.b = make_uint4(pack2<ST>(e[4].x, e[4].y), pack2<ST>(e[5].x, e[5].y), pack2<ST>(e[6].x, e[6].y),
+                           pack2<ST>(e[7].x, e[7].y));
+          store_raw(reinterpret_cast<uint16_t*>(dst), ea, eb, y);
+        }
+      }
+      dst += step;
     }
-    dst += step;
+  };
+  if constexpr (FP8) {
+    if (wild) {
+      finish(std::true_type{});
+      return;
+    }
   }
+  finish(std::false_type{});
 }
 
 template <int ST, bool FP8, bool INTER, int LANES, int kHeads>
