@@ -329,11 +329,13 @@ pa_status pa_decode_noalloc(const pa_tensor* out, const pa_tensor* q,
  *                 and pa_alloc_add_cached leave them). Tokens of a last, partial
  *                 block count to the tails.
  *   every other argument as for pa_decode. NG <= 4096; NG = 0 is pa_decode.
- * A sequence takes part in its group's shared pass if it attends to all of
- * the prefix (it is at least that long and no window cuts it); any other one,
- * an idle row of length 0 among them, is decoded by itself, as is a group with
- * fewer than two that do. The prefix is read through the table of the
- * group's first row that takes part.
+ * A sequence takes part in its group's shared pass if it is at least as long
+ * as the prefix and attends to all of it, or if its window reaches back over at
+ * least half of its length into the prefix; the pass covers the positions that
+ * all of these attend to. Any other sequence, an idle row of length 0 among
+ * them, is decoded by itself, as is a group with fewer than two that take part.
+ * The pass reads the prefix through the table of the group's first row that
+ * takes part, and no entry of a block that this row does not attend to.
  * A step whose tables could not name more than 72 MB of K/V in all (B * MB *
  * Hkv * bs * D keys and values) is decoded plainly, whatever its groups: there
  * is too little to save (pa_set_shared_path changes that).

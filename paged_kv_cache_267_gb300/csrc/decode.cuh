@@ -52,9 +52,9 @@
 // a segment yields m = floor, l = 0 and a zero output.
 //
 // Shared prefixes (SH = true, single queries). Part of the batch has its leading
-// positions covered by the prefix kernel: every sequence's range starts at the
-// position the step's shared plan gives (shared_plan.cuh) instead of the
-// window's start, and is empty where the prefix is all there is.
+// positions covered by the prefix kernel: the step's shared plan
+// (shared_plan.cuh) gives every sequence's tiles, with a gap where those are,
+// and none where they are all there is.
 //
 // FP8 e4m3 caches: codes are converted to f16 in registers (exact), Q is
 // converted once per segment to f16 after a power-of-two rescale so its
@@ -182,7 +182,8 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
   int* s_meta = reinterpret_cast<int*>(gbase + WARPS * Gm::RING_BYTES + WARPS * STAGES * 8);
   int* s_len = s_meta + 2 * WARPS * STAGES;
   int* s_pref = s_len + a.B;
-  int* s_first = s_pref + a.B + 1;  // SH: first position of each sequence's range
+  int* s_first = s_pref + a.B + 1;  // SH: first position of each sequence's range,
+  int* s_head = s_first + a.B;      // and its tiles before the gap
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t4 = lane & 3;
@@ -221,14 +222,26 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
   pin.np_max = a.np_max;
   pin.piece_min = a.piece_min;
   if constexpr (SH) {
-    for (int b = tid; b < a.B; b += blockDim.x) s_first[b] = a.shared_rows[b].start;
+    for (int b = tid; b < a.B; b += blockDim.x) {
+      const SharedRow r = a.shared_rows[b];
+      s_first[b] = r.start;
+      s_head[b] = r.head;
+      s_pref[b + 1] = r.tiles;
+    }
   }
   // first position of sequence b's range
   auto start_of = [&](int b) -> int {
     if constexpr (SH) return s_first[b];
     else return win_start(s_len[b], a.span);
   };
-  const StepPlan pl = plan_step<SH>(pin, s_len, s_pref, s_first);
+  // tile t of sequence b's nt, in position space
+  auto tile_of = [&](int b, int t, int nt) -> int {
+    if constexpr (SH) {
+      if (t >= s_head[b]) return (s_len[b] + kTile - 1) / kTile - nt + t;
+    }
+    return start_of(b) / kTile + t;
+  };
+  const StepPlan pl = plan_step<SH>(pin, s_len, s_pref);
   const int total = pl.total, ws = pl.ws, ts = pl.ts;
   const int nw = gridDim.x * WARPS;
   const int pool_tiles = total - ts;
@@ -336,7 +349,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
       // static range about to end: claim the first pool piece now
       if (phase == 0 && pool_tiles > 0 && !claim_issued) issue_claim();
     }
-    const int pt = start_of(pc.b) / kTile + pc.t;  // tile index in position space
+    const int pt = tile_of(pc.b, pc.t, pc.nt);
     const int lb = (pt * kTile) / a.bs;
     refresh_window(pc.b, lb);
     int phys = __shfl_sync(FULL, id_val, lb - id_lb0);
@@ -372,7 +385,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
   if (f0 < f1) {
     Cursor c0;
     cursor_locate(c0, f0, s_pref, a.B, a.Hv);
-    const int pt0 = start_of(c0.b) / kTile + c0.t;
+    const int pt0 = tile_of(c0.b, c0.t, c0.nt);
     refresh_window(c0.b, (pt0 * kTile) / a.bs);
   }
   // The caches may have been written by the previous kernel. SH: that is the
@@ -527,7 +540,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
     // tile position and edge masks
     const int L = s_len[cc.b];
     const int st = start_of(cc.b);
-    const int p0 = (st / kTile + cc.t) * kTile;
+    const int p0 = tile_of(cc.b, cc.t, cc.nt) * kTile;
     const bool edge = (p0 < st) || (p0 + kTile > L);  // outside the pair's union range
     auto valid = [&](int r) { return !edge || (p0 + r >= st && p0 + r < L); };
 
@@ -777,8 +790,12 @@ struct DecodeKernel {
   }
   static DecodeVariant variant() { return DecodeVariant{WARPS, STAGES, WARPS * Gm::RING_BYTES}; }
   static cudaError_t prepare(int smem, int* ctas_per_sm) {
-    cudaError_t e =
-        cudaFuncSetAttribute(fn(), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // only ever raised: a size that has been prepared is launched again later,
+    // behind smaller ones
+    cudaFuncAttributes now;
+    cudaError_t e = cudaFuncGetAttributes(&now, fn());
+    if (e == cudaSuccess && now.maxDynamicSharedSizeBytes < smem)
+      e = cudaFuncSetAttribute(fn(), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas_per_sm, fn(), WARPS * 32, smem);
   }

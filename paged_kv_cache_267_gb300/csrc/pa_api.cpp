@@ -393,7 +393,7 @@ pa_status plan_decode(DeviceState* st, int ct, int qt, int kind, int64_t B, int 
   cudaError_t e = p->fam.variant(D, p->nt, &p->var);
   if (e != cudaSuccess) return fail(PA_ERR_UNSUPPORTED, "no decode kernel for this dtype/head_dim");
   const size_t smem = 1024 + p->var.ring_bytes + p->var.warps * p->var.stages * (8 + 8) +
-                      static_cast<size_t>((kind == kTails ? 3 : 2) * B + 1) * sizeof(int32_t);
+                      static_cast<size_t>((kind == kTails ? 4 : 2) * B + 1) * sizeof(int32_t);
   p->smem = static_cast<int>(round_up(smem, 1024));
   auto key = std::make_tuple(ct, qt, D, p->nt, p->smem, kind);
   auto it = st->occupancy.find(key);

@@ -24,10 +24,6 @@ __device__ __forceinline__ int tiles_of(int L, int W) {
   return L > 0 ? (L + kTile - 1) / kTile - win_start(L, W) / kTile : 0;
 }
 
-__device__ __forceinline__ int tiles_from(int L, int first) {
-  return L > first ? (L + kTile - 1) / kTile - first / kTile : 0;
-}
-
 struct PlanIn {
   const int32_t* seq_lens;  // [B]
   int32_t* err;             // device error word (null: do not report)
@@ -63,11 +59,10 @@ __device__ __forceinline__ void piece_range(int i, const StepPlan& pl, int* f0, 
 // outside is reported through `err`) and s_pref[0 .. B] with the exclusive
 // prefix of tiles per pair over the sequences. The host bounds B * Hv * tiles
 // per pair below 2^31, so the tile counts fit 32-bit integers.
-// FROM: sequence b's range starts at s_first[b] (filled by the caller before)
-// instead of its window's start.
-template <bool FROM>
-__device__ inline StepPlan plan_step(const PlanIn& p, int* s_len, int* s_pref,
-                                     const int* s_first) {
+// GIVEN: sequence b has s_pref[b + 1] tiles per pair (filled by the caller
+// before) instead of those of its window.
+template <bool GIVEN>
+__device__ inline StepPlan plan_step(const PlanIn& p, int* s_len, int* s_pref) {
   constexpr unsigned FULL = 0xffffffffu;
   __shared__ int s_last_long;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -86,7 +81,7 @@ __device__ inline StepPlan plan_step(const PlanIn& p, int* s_len, int* s_pref,
     for (int b0 = 0; b0 < p.B; b0 += 32) {
       const int b = b0 + lane;
       int x = 0;
-      if (b < p.B) x = FROM ? tiles_from(s_len[b], s_first[b]) : tiles_of(s_len[b], p.span);
+      if (b < p.B) x = GIVEN ? s_pref[b + 1] : tiles_of(s_len[b], p.span);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(FULL, x, o);

@@ -29,6 +29,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxRows = 4096 / kThreads;  // of the batch, a thread
+constexpr int kMostShared = (3 * kThreads * kMaxRows + 2) * 4;  // bytes, at the largest batch
 constexpr unsigned kFull = 0xffffffffu;
 // Token sums saturate here: more than any call accepts, and the sum of two
 // such values still fits 32 bits.
@@ -406,10 +407,9 @@ int grid_for(long long items, long long per, int num_sms) {
 
 template <typename Args>
 cudaError_t launch(void (*fn)(const Args), const Args& a, int grid, size_t smem, cudaStream_t s) {
-  if (smem > 48 * 1024) {  // large batches: the per-sequence prefixes
-    const cudaError_t e =
-        cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (smem > 48 * 1024) {  // large batches: the per-sequence prefixes (one value, whichever thread sets it)
+    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};

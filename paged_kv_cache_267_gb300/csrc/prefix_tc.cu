@@ -2,7 +2,8 @@
 // 5th-generation tensor cores: one pass over the prefix's K/V for all of them.
 //
 // The queries of the n sequences of a group, G heads of one KV head each, are
-// the rows of one matrix Q [n G x D]; every row attends to all of [0, P), so
+// the rows of one matrix Q [n G x D]; every row attends to all of the positions
+// that the kernel covers (shared_plan.cuh), so
 //   S = Q K^T,  P = 2^(S c - m),  O += P V,  l += sum P
 // with a running reference m per row, and no mask but the end of the last
 // tile. Partials (O, m, l) go to workspace slots in the decode partials'
@@ -221,8 +222,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     // table and copy its 128-byte boxes; slices behind the prefix (row < 0)
     // are not loaded.
     auto row_of = [&](int t) -> int {
-      const int pos0 = t * C::kKv + 16 * lane;
-      if (lane >= C::kSlices || pos0 >= sg.g.prefix) return -1;
+      const int at = t * C::kKv + 16 * lane, pos0 = sg.g.first + at;
+      if (lane >= C::kSlices || at >= sg.g.prefix) return -1;
       int blk = __ldg(a.block_tables + static_cast<size_t>(sg.g.table_row) * a.MB + pos0 / a.bs);
       if (static_cast<unsigned>(blk) >= static_cast<unsigned>(a.NB)) {
         atomicOr(a.err, PA_DEVERR_BLOCK_ID);

@@ -12,6 +12,7 @@ namespace pa {
 namespace {
 
 constexpr int kMaxThreads = 1024;
+constexpr int kMostGroups = 4096;  // as the host checks
 constexpr unsigned kFull = 0xffffffffu;
 
 // Inclusive scan of x over the block with op (identity `zero`); *total
@@ -86,6 +87,7 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
   int* s_first = s_in + a.NG;    // [NG] the first of them
   int* s_base = s_first + a.NG;  // [NG] first slot
   int* s_w0 = s_base + a.NG;     // [NG] first CTA that meets the group
+  int* s_lo = s_w0 + a.NG;       // [NG] first position that all taking part attend to
   __shared__ int s_wsz, s_tiles, s_tails, s_dual;
   const int tid = threadIdx.x, nthreads = blockDim.x;
   const int cap = a.MB * a.bs;
@@ -120,6 +122,7 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
           s_pre[g] = q / a.bs * a.bs;
           s_in[g] = 0;
           s_first[g] = a.B;
+          s_lo[g] = 0;
         }
       }
       const int y = most(scan<ONE>(x, 0, most, &total), run);
@@ -142,18 +145,21 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
     return lo;
   };
   auto takes_part = [&](int L, int g) -> bool {
-    return g >= 0 && s_pre[g] > 0 && L >= s_pre[g] && (a.window == 0 || L <= a.window);
+    return g >= 0 && s_pre[g] > 0 && L >= s_pre[g] &&
+           (a.window == 0 || L <= a.window || L - s_pre[g] <= a.window / 2);
   };
+  auto start_of = [&](int L) -> int { return a.window > 0 ? max(L - a.window, 0) : 0; };
   // Rows that take part, by group: a warp's rows are mostly of one group, and
   // are then counted by one lane.
-  int tails = 0;  // 16-token tiles of the decode kernel, of one KV head
+  int tails = 0;  // 16-token tiles of all ranges, of one KV head
   for (int b0 = tid & ~31, j = 0; b0 < a.B; b0 += nthreads, ++j) {
     const int b = b0 + (tid & 31);
     const int g = b < a.B ? group_of(b) : -1;
     const int L = b < a.B ? length(b, j) : 0;
     const bool in = takes_part(L, g) && b < a.B;
-    const int first = in ? s_pre[g] : (a.window > 0 ? max(L - a.window, 0) : 0);
-    tails += (L + kTile - 1) / kTile - first / kTile;
+    const int start = start_of(L);
+    tails += (L + kTile - 1) / kTile - start / kTile;
+    if (in && start > 0) atomicMax(&s_lo[g], (start + kTile - 1) / kTile * kTile);
     const unsigned votes = __ballot_sync(kFull, in);
     const int g_first = __shfl_sync(kFull, g, votes ? __ffs(votes) - 1 : 0);
     if (__all_sync(kFull, !in || g == g_first)) {
@@ -178,10 +184,12 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
       const int g = g0 + tid;
       int x = 0;
       if (g < a.NG) {
-        if (s_in[g] < 2) s_pre[g] = 0;  // one sequence reads its prefix once anyway
-        const int n = s_r0[g + 1] - s_r0[g];
+        // one sequence reads its prefix once anyway
+        if (s_in[g] < 2 || s_lo[g] >= s_pre[g]) s_pre[g] = s_lo[g] = 0;
+        const int n = s_r0[g + 1] - s_r0[g], span = s_pre[g] - s_lo[g];
+        if (span > 0) atomicSub(&s_tails, s_in[g] * (span / kTile));
         Units u;
-        u.nt = (s_pre[g] + a.kv - 1) / a.kv;
+        u.nt = (span + a.kv - 1) / a.kv;
         u.nut = n <= up_max ? (n > 0) : (n + up_max - 1) / up_max;
         u.up = u.nut <= 1 ? n : (n + u.nut - 1) / u.nut;
         u.up_mul = u.nut <= 1 ? 0u : 0xffffffffu / static_cast<uint32_t>(max(u.up, 1)) + 1u;
@@ -240,7 +248,8 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
     r.r0 = s_r0[g];
     r.n = s_r0[g + 1] - s_r0[g];
     r.table_row = s_first[g];
-    r.prefix = s_pre[g];
+    r.prefix = s_pre[g] - s_lo[g];
+    r.first = s_lo[g];
     r.f0 = s_in[g];
     r.nt = u.nt;
     r.nut = u.nut;
@@ -273,12 +282,15 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
   for (int b = tid, j = 0; b < a.B; b += nthreads, ++j) {
     const int g = group_of(b);
     const int L = length(b, j);
-    SharedRow r = {a.window > 0 && L > a.window ? L - a.window : 0, 0, 0, 0, 0, 0, 0, 0};
+    SharedRow r = {};
+    r.start = start_of(L);
+    r.tiles = (L + kTile - 1) / kTile - r.start / kTile;
     if (takes_part(L, g)) {
       const Units u = s_units[g];
       const int i = b - s_r0[g];
       const int ut = u.up_mul ? (u.up == 1 ? i : static_cast<int>(__umulhi(static_cast<uint32_t>(i), u.up_mul))) : 0;
-      r.start = s_pre[g];
+      r.head = s_lo[g] / kTile - r.start / kTile;
+      r.tiles -= (s_pre[g] - s_lo[g]) / kTile;
       r.nt = u.nt;
       r.f0 = s_in[g] + ut * u.nt;
       r.kv_step = u.nut * u.nt;
@@ -295,11 +307,12 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
 }  // namespace
 
 cudaError_t shared_plan_launch(const SharedPlanArgs& a, cudaStream_t s, bool pdl) {
-  const size_t smem = (10 * static_cast<size_t>(a.NG) + 1) * sizeof(int);
+  const size_t smem = (11 * static_cast<size_t>(a.NG) + 1) * sizeof(int);
   if (smem > 48 * 1024) {
+    // one value, whichever thread sets it
     const cudaError_t e =
         cudaFuncSetAttribute(reinterpret_cast<const void*>(shared_plan_kernel<false>),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, (11 * kMostGroups + 1) * 4);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};

@@ -2,10 +2,12 @@
 // kernel (shared_plan.cu) and read by the prefix, decode and merge kernels.
 //
 // Sequences of group g, rows [r0, r0 + n), share their first P tokens (P a
-// multiple of the block size, so of 16). A row takes part when it attends to all
-// of them: L >= P and no window cuts them. The prefix kernel computes the
-// partial softmax of all taking part over [0, P); the decode kernel covers
-// [P, L) of those, and the whole range of every other row.
+// multiple of the block size, so of 16). A row takes part when it is at least
+// that long and no window cuts it, or one that reaches back over at least half
+// of its length into them. With S the largest window start of those that take
+// part, rounded up to 16 (0 without windows), the prefix kernel computes the
+// partial softmax of all of them over [S, P); the decode kernel covers the rest
+// of their ranges, [start, S) and [P, L), and the whole range of every other row.
 //
 // The (query, head) rows of one KV head of a group, n * G of them, are cut into
 // nut units of up pairs (sequences) each, at most 256 rows; a unit of at most
@@ -33,14 +35,14 @@ enum { kShTotal = 0, kShWsz = 1, kShEarly = 2 };
 struct SharedGroup {  // 12 words a group
   int r0, n;          // rows
   int table_row;      // the row whose block table the prefix is read through
-  int prefix;         // P, 0 when the group does not share
+  int prefix;         // P - S, 0 when the group does not share
   int f0;             // first flat tile
   int nt;             // K/V tiles of the prefix
   int nut, up;        // units a KV head, pairs a unit
   int base;           // first partial slot (counted from the prefix region)
   int dual;           // its units have rows for both softmax groups
   int wfirst;         // first CTA that meets the group
-  int pad;
+  int first;          // S
 };
 
 struct SharedCta {  // 16 words a CTA of the prefix kernel
@@ -50,20 +52,22 @@ struct SharedCta {  // 16 words a CTA of the prefix kernel
   SharedGroup g;  // that group, so that a CTA starts on one load
 };
 
-struct SharedRow {  // 8 words a sequence
-  int start;        // first position the decode kernel covers
+struct SharedRow {  // 12 words a sequence
+  int start;        // first position of its range
+  int head, tiles;  // 16-token tiles the decode kernel covers: before S, and in all
   int nt;           // K/V tiles of its prefix, 0: no part of it here
   int f0;           // first flat tile of its unit at KV head 0
   int kv_step;      // flat tiles between KV heads
   int slot0;        // slot of lid 0 for this sequence's pair
   int lid0;         // unit - wfirst at KV head 0 (added to the CTA)
   int up, nut;      // slots between lids, lids between KV heads
+  int pad[2];
 };
 
 // Words of the plan: header, CTAs, groups, rows.
 __host__ __device__ constexpr inline size_t shared_plan_words(int64_t B, int64_t NG, int ctas) {
   return kSharedHead + 16 * static_cast<size_t>(ctas) + 12 * static_cast<size_t>(NG) +
-         8 * static_cast<size_t>(B);
+         12 * static_cast<size_t>(B);
 }
 __host__ __device__ __forceinline__ const SharedCta* shared_ctas(const int32_t* plan) {
   return reinterpret_cast<const SharedCta*>(plan + kSharedHead);

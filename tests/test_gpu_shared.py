@@ -187,6 +187,59 @@ def test_windows_that_cut_some_rows_off_the_prefix(window, pa_lib):
     b.check(out, window, f"window {window}")
 
 
+def poison_outside_windows(b, window):
+    """NaN at every position that no sequence attends to, and no table entry of a
+    block wholly before a sequence's window."""
+    bs = b.bs
+    seen = np.zeros((b.kc.shape[0], bs), bool)
+    for r, L in enumerate(b.lens):
+        p = np.arange(max(0, L - window), L)
+        seen[b.tables[r, p // bs], p % bs] = True
+        b.tables[r, :max(0, L - window) // bs] = -1
+    out = torch.from_numpy(~seen).cuda()[:, None, :, None]
+    for x in (b.kc, b.vc):
+        x.copy_(torch.where(out, torch.full_like(x, 0x7F if b.fp8 else float("nan")), x))
+    b.va = b.vc & 0x7F if b.fp8 else b.vc.abs()
+
+
+WINDOWED = [
+    # groups, windows: prefixes that the windows cut at many places
+    (dict(groups=[(1600, [1, 18, 300, 2, 0])], loose_after=(900, 3)), (17, 40, 599, 601, 800, 1599, 1600, 1601, 1700)),
+    (dict(groups=[(640, [9] * 40), (2048, [1, 700, 3])], heads=(8, 2)), (330, 1000, 1409)),
+    (dict(groups=[(1040, [5, 5, 6])], bs=80, dt="f16"), (250, 1039)),
+    (dict(groups=[(848, [9, 2, 130])], fp8=True), (300, 777)),
+    (dict(groups=[(720, [9, 2, 130])], D=256, dt="f16"), (288,)),
+    (dict(groups=[(720, [9, 2, 30])], D=64), (333,)),
+    (dict(groups=[(512, [1, 2]), (256, [1, 1]), (64, [4, 4])] * 12), (200, 511)),
+    (dict(groups=[(2048, [9, 1025, 5, 6])], bs=1024, loose_before=(1500,)), (1500, 2049)),
+]
+
+
+@pytest.mark.parametrize("kw,window", [(k, w) for k, ws in WINDOWED for w in ws])
+def test_windows_that_end_inside_the_prefix(kw, window, pa_lib):
+    b = Batch(seed=window, **kw)
+    poison_outside_windows(b, window)
+    out = b.run(pa_lib, window)
+    assert pa_lib.check_device_error() == 0
+    b.check(out, window, f"window {window}")
+
+
+def test_a_nan_in_one_sequences_window_stays_its_own(pa_lib):
+    """The shortest sequence of a group attends to positions that no other one's
+    window reaches."""
+    b = Batch([(1600, [40, 1, 60, 33])], dt="f16", seed=3)
+    window = 900                    # from 701 on for the shortest (1601 - 900), from 733 for the others
+    out0 = b.run(pa_lib, window)
+    b.check(out0, window)
+    b.vc[int(b.tables[1, 732 // 16]), :, 732 % 16] = float("nan")
+    b.kc[int(b.tables[1, 705 // 16]), :, 705 % 16] = float("nan")
+    out = b.run(pa_lib, window)
+    assert out[1].isnan().all()
+    rest = [0, 2, 3]
+    assert torch.equal(out[rest], out0[rest])
+    assert pa_lib.check_device_error() == 0
+
+
 @pytest.mark.parametrize("dt,fp8", [("bf16", False), ("f16", True)])
 def test_negative_and_zero_scale(dt, fp8, pa_lib):
     for scale in (-0.09, 0.0):
@@ -341,6 +394,30 @@ def test_own_workspace_of_the_stated_size(pa_lib):
             b.run(pa_lib)
     finally:
         pa_lib.set_workspace(None)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_large_batches_after_small_ones(fp8, pa_lib):
+    """The shared memory that a large batch needs stays granted."""
+    kw = dict(dt="f16", fp8=fp8, heads=(2, 1))
+    big, mid, small = (Batch([(64, [3] * n)], seed=n, **kw) for n in (1500, 300, 2))
+    for b in (big, small, mid, big, small, big):
+        b.check(b.run(pa_lib))
+        a = b.args()
+        b.check(pa_lib.decode(*a[:5], **b.kw()))
+    assert pa_lib.check_device_error() == 0
+
+
+def test_many_groups_of_many_rows(pa_lib):
+    """More groups than one warp scans, up to the limits of the call."""
+    b = Batch([(16, [1])] * 4000 + [(32, [2] * 96)], dt="f16", heads=(1, 1), D=64, seed=5)
+    assert b.B == 4096
+    out = b.run(pa_lib)
+    assert pa_lib.check_device_error() == 0
+    b.check(out)
+    few = Batch([(16, [1, 1])] * 40, dt="f16", heads=(1, 1), D=64, seed=6)
+    few.check(few.run(pa_lib))
+    b.check(b.run(pa_lib))
 
 
 def test_other_streams_and_shapes_in_turn(pa_lib):
