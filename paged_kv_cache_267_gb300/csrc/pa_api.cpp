@@ -868,17 +868,22 @@ pa_status plan_call(DeviceState* st, const DecodeCall& c, DecodePlan* plan, WsLa
   return PA_OK;
 }
 
-// Times of a shared-prefix step's tiles (see SharedCost): the prefix kernel's
-// measured on a step with both kernels running, the tails' from the decode
-// kernel's rate, about 6.5 TB/s (e4m3: 4.4 TB/s, bound by its instructions).
+// Times of a shared-prefix step's tiles (see SharedCost), by head dim and cache
+// type: what made the slowest sum over 7 to 14 steps of each kind shortest, with
+// batches of 20 to 256, prefixes of 1024 to 14496 tokens and tails of up to 1024.
+// They are two to three times a tile's time in a kernel that runs alone (1750 ns
+// for the two row tiles of head_dim 128): both kernels wait for the same memory. A
+// ratio of prefix to tail that is off by a quarter costs 5 to 15%.
 pa::SharedCost shared_cost(int D, bool fp8) {
   pa::SharedCost c;
-  const float d = static_cast<float>(D) / 128.f;
-  c.dual_ns = D == 64 ? 2600.f : 3500.f;
-  c.single_ns = D == 64 ? 2200.f : (fp8 ? 3000.f : 4000.f);
-  c.tail_ns = (fp8 ? 140.f : 190.f) * d;
-  c.prefix_ns = 10000.f;
-  c.decode_ns = 5000.f;
+  if (D == 64)
+    c = {2000.f, 1600.f, 150.f, 10000.f, 8000.f};
+  else if (D == 128)
+    c = fp8 ? pa::SharedCost{3000.f, 3000.f, 140.f, 10000.f, 5000.f}
+            : pa::SharedCost{3200.f, 3500.f, 190.f, 10000.f, 5000.f};
+  else  // (one row tile only)
+    c = fp8 ? pa::SharedCost{2600.f, 2600.f, 280.f, 10000.f, 5000.f}
+            : pa::SharedCost{2700.f, 2700.f, 500.f, 10000.f, 5000.f};
   return c;
 }
 
@@ -958,7 +963,7 @@ pa_status run_decode(const DecodeCall& c, DeviceState* st, const DecodePlan& pla
     p.unit_rows = shape.unit_rows;
     p.halves = shape.halves;
     p.ctas = grid;
-    p.whole = grid * 7 / 10;
+    p.whole = grid * 17 / 20;
     p.decode_ctas = plan.grid;
     p.decode_per_sm = plan.per_sm;
     p.cost = shared_cost(D, c.fp8);

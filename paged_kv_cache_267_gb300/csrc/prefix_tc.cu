@@ -37,10 +37,12 @@
 // bytes each, had cost about 6,000 and 5,000-9,700 cycles a segment of at most
 // 100,000.
 //
-// FP8 caches: two converter warps, half of the rows each, turn each raw e4m3
+// FP8 caches: six converter warps, every sixth eight rows each, turn each raw e4m3
 // tile into the f16 tile the products read (exact), in two buffers each for K
-// and V, so that a tile is converted while the one before is multiplied; Q is rescaled per row by a power of two to f16's range, which
-// the row's score scale undoes.
+// and V, so that a tile is converted while the one before is multiplied; Q is
+// rescaled per row by a power of two to f16's range, which the row's score scale
+// undoes. With two converter warps they bound the loop (2.19 us a tile of 128
+// tokens and two row tiles; now 1.89, bf16 1.71).
 #include "attn_tc.cuh"
 #include "pa_internal.h"
 #include "ptx.cuh"
@@ -53,7 +55,9 @@ namespace {
 
 constexpr int kRows = 128;
 constexpr int kGroupThreads = 128;
-constexpr int kConv = 2;  // FP8 converter warps
+constexpr int kConv = 6;  // FP8 converter warps
+// Registers a thread where 16 warps share the SM's: softmax warps, all others.
+constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;  // bound of every wait (2 s)
 constexpr float kFloor = -1e30f;             // reference-max start
@@ -96,6 +100,11 @@ struct Cfg {
   static constexpr int kMmaWarp = 4 * kGroups, kLoadWarp = kMmaWarp + 1,
                        kConvWarp0 = kLoadWarp + kLoadWarps;
   static constexpr int kThreads = (kConvWarp0 + (FP8 ? kConv : 0)) * 32;
+  // more than 12 warps leave each thread 128 registers, too few for the softmax:
+  // its warps get what the others hand back
+  static constexpr bool kSplitRegs = kThreads > 384;
+  static_assert(!kSplitRegs || (kThreads == 512 && kGroups == 2 &&
+                                kSoftmaxRegs + kOtherRegs == 2 * 128), "registers of the block");
   static constexpr uint32_t kQBox = kRows * 128, kQBytes = kBoxes * kQBox;  // one group's Q
   static constexpr uint32_t kBox = kKv * 128, kTile = kBoxes * kBox;        // 16-bit K or V tile
   static constexpr uint32_t kRawBoxes = FP8 ? D / 128 : kBoxes;             // 128-byte boxes
@@ -216,228 +225,228 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
   const int ntiles = f1 - f0;  // of this CTA, over all its segments
   int gi = mine.group;
 
-  if (warp >= C::kLoadWarp && warp < C::kConvWarp0) {
-    // ------------------------------------------------------------ producers
-    // Lanes 0..kSlices-1 each look up one 16-token slice of a tile in the block
-    // table and copy its 128-byte boxes; slices behind the prefix (row < 0)
-    // are not loaded.
-    auto row_of = [&](int t) -> int {
-      const int at = t * C::kKv + 16 * lane, pos0 = sg.g.first + at;
-      if (lane >= C::kSlices || at >= sg.g.prefix) return -1;
-      int blk = __ldg(a.block_tables + static_cast<size_t>(sg.g.table_row) * a.MB + pos0 / a.bs);
-      if (static_cast<unsigned>(blk) >= static_cast<unsigned>(a.NB)) {
-        atomicOr(a.err, PA_DEVERR_BLOCK_ID);
-        blk = 0;
-      }
-      return (blk * a.Hkv + sg.kvh) * a.bs + pos0 % a.bs;
-    };
-    auto load = [&](int stage, int row, bool is_v) {
-      const uint32_t full = bar((is_v ? kBarVFull : kBarKFull) + stage);
-      const int nslices = __popc(__ballot_sync(kFull, row >= 0));
-      if (lane == 0) mbar_arrive_expect_tx(full, nslices * C::kRawBoxes * 2048);
-      __syncwarp();
-      if (row >= 0) {
-        const uint32_t dst = (is_v ? sV : sK) + stage * C::kRing + lane * 2048;
+  if (warp >= C::kMmaWarp) {
+    if constexpr (C::kSplitRegs)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp >= C::kLoadWarp && warp < C::kConvWarp0) {
+      // ------------------------------------------------------------ producers
+      // Lanes 0..kSlices-1 each look up one 16-token slice of a tile in the block
+      // table and copy its 128-byte boxes; slices behind the prefix (row < 0)
+      // are not loaded.
+      auto row_of = [&](int t) -> int {
+        const int at = t * C::kKv + 16 * lane, pos0 = sg.g.first + at;
+        if (lane >= C::kSlices || at >= sg.g.prefix) return -1;
+        int blk = __ldg(a.block_tables + static_cast<size_t>(sg.g.table_row) * a.MB + pos0 / a.bs);
+        if (static_cast<unsigned>(blk) >= static_cast<unsigned>(a.NB)) {
+          atomicOr(a.err, PA_DEVERR_BLOCK_ID);
+          blk = 0;
+        }
+        return (blk * a.Hkv + sg.kvh) * a.bs + pos0 % a.bs;
+      };
+      auto load = [&](int stage, int row, bool is_v) {
+        const uint32_t full = bar((is_v ? kBarVFull : kBarKFull) + stage);
+        const int nslices = __popc(__ballot_sync(kFull, row >= 0));
+        if (lane == 0) mbar_arrive_expect_tx(full, nslices * C::kRawBoxes * 2048);
+        __syncwarp();
+        if (row >= 0) {
+          const uint32_t dst = (is_v ? sV : sK) + stage * C::kRing + lane * 2048;
 #pragma unroll
-        for (int box = 0; box < static_cast<int>(C::kRawBoxes); ++box)
-          tma_load_2d(dst + box * C::kBox, is_v ? &tmV : &tmK, box * (FP8 ? 128 : 64), row, full);
-      }
-      __syncwarp();
-    };
-    const bool do_k = C::kLoadWarps == 1 || warp == C::kLoadWarp;
-    const bool do_v = C::kLoadWarps == 1 || warp != C::kLoadWarp;
-    bool ok = true;
-    Ring kr, vr;
-    int c = 0;
-    for (int f = f0; ok && f < f1; f += sg.nt) {
-      segment_at(a, f, f1, &gi, &sg);
-      int row = row_of(sg.t0);
-      for (int n = 0; ok && n < sg.nt; ++n, ++c) {
-        // looked up while the waits below run
-        const int next = n + 1 < sg.nt ? row_of(sg.t0 + n + 1) : -1;
-        if (do_k) {  // the release of the stage's last tile: the phase before
-          if (c >= C::kKStages && !(ok = wait_all(bar(kBarKEmpty + kr.stage), kr.phase ^ 1))) break;
-          load(kr.stage, row, false);
-          kr.next(C::kKStages);
+          for (int box = 0; box < static_cast<int>(C::kRawBoxes); ++box)
+            tma_load_2d(dst + box * C::kBox, is_v ? &tmV : &tmK, box * (FP8 ? 128 : 64), row, full);
         }
-        if (do_v) {
-          if (c >= C::kVStages && !(ok = wait_all(bar(kBarVEmpty + vr.stage), vr.phase ^ 1))) break;
-          load(vr.stage, row, true);
-          vr.next(C::kVStages);
-        }
-        row = next;
-      }
-    }
-    if (!ok && lane == 0) atomicOr(a.err, PA_DEVERR_TIMEOUT);
-  } else if (warp == C::kMmaWarp) {
-    // ------------------------------------------------------------ MMA issue
-    // One thread does all of it, and little besides: its own instructions are
-    // on the critical path of every tile (a wait by the whole warp costs about
-    // 150 cycles even when there is nothing to wait for, the products of one
-    // tile and group about 1,200).
-    if (lane == 0) {
-      constexpr uint32_t idS = tc::idesc_f16(kRows, C::kKv, kBf16, false);
-      constexpr uint32_t idO = tc::idesc_f16(kRows, D, kBf16, true);
-      // Positions of the K and V tiles in use, and the barriers that say they
-      // are ready: the ring's, or the converted buffers' (two of each).
-      constexpr int KB = FP8 ? 2 : C::kKStages, VB = FP8 ? 2 : C::kVStages;
-      constexpr int kKReady = FP8 ? kBarCKFull : kBarKFull, kKFree = FP8 ? kBarCKFree : kBarKEmpty;
-      constexpr int kVReady = FP8 ? kBarCVFull : kBarVFull, kVFree = FP8 ? kBarCVFree : kBarVEmpty;
-      const uint64_t dQ = tc::sdesc_sw128(sQ, 16, 1024);
-      const uint64_t dK = tc::sdesc_sw128(FP8 ? sKc : sK, 16, 1024);
-      const uint64_t dV = tc::sdesc_sw128(FP8 ? sVc : sV, C::kBox, 1024);
+        __syncwarp();
+      };
+      const bool do_k = C::kLoadWarps == 1 || warp == C::kLoadWarp;
+      const bool do_v = C::kLoadWarps == 1 || warp != C::kLoadWarp;
+      bool ok = true;
       Ring kr, vr;
-      // releases still to come: one is committed only when something will wait
-      // for it, so that no arrive outlives the CTA
-      int k_free = ntiles - KB, v_free = ntiles - VB;
-      auto wait = [&](uint32_t b, uint32_t parity) { return mbar_wait_bounded(b, parity, kWaitNs); };
-      auto issue_s = [&](int x, bool last) {
-#pragma unroll
-        for (int box = 0; box < C::kBoxes; ++box)
-          mma4_ss(tmem + C::kColS + C::kKv * x, dQ + ((x * C::kQBytes + box * C::kQBox) >> 4),
-                  dK + ((kr.stage * C::kTile + box * C::kBox) >> 4), idS, box > 0);
-        tc::commit(bar(kBarS + x));
-        if (last) {
-          if (k_free-- > 0) tc::commit(bar(kKFree + kr.stage));
-          kr.next(KB);
-        }
-      };
-      // O_x (+)= P_x V: 16 tokens a step, P in 8 columns each from 64 h on
-      auto issue_o = [&](int x, bool first, bool last) {
-#pragma unroll
-        for (int h = 0; h < C::kKv / 64; ++h)
-          mma4_ts(tmem + C::kColO + D * x, tmem + C::kColS + C::kKv * x + 64 * h,
-                  dV + ((vr.stage * C::kTile) >> 4) + 512 * h, idO, !first || h > 0);
-        tc::commit(bar(kBarO + x));
-        if (last) {
-          if (v_free-- > 0) tc::commit(bar(kVFree + vr.stage));
-          vr.next(VB);
-        }
-      };
-      bool ok = true;
-      uint32_t par[2] = {0, 0};  // phase of each group's next product
-      // Group x's products on one tile: O, and S of its next tile if there is
-      // one. first_use, last_use: of the tile's V (and the next one's K).
-      auto step = [&](int x, bool first, bool more, bool first_use, bool last_use) {
-        // P_x (and clean V rows) written, V there; both tested before either is
-        // waited for
-        const bool v_in = !first_use || mbar_try_wait(bar(kVReady + vr.stage), vr.phase);
-        const bool p_in = mbar_try_wait(bar(kBarP + x), par[x]);
-        if (!p_in && !(ok = wait(bar(kBarP + x), par[x]))) return;
-        if (!v_in && !(ok = wait(bar(kVReady + vr.stage), vr.phase))) return;
-        tc::fence_after_sync();
-        issue_o(x, first, last_use);
-        if (more) {
-          const bool k_in = !first_use || mbar_try_wait(bar(kKReady + kr.stage), kr.phase);
-          if (!(ok = wait(bar(kBarO + x), par[x]))) return;  // P_x consumed
-          if (!k_in && !(ok = wait(bar(kKReady + kr.stage), kr.phase))) return;
-          tc::fence_after_sync();
-          issue_s(x, last_use);
-        }
-        par[x] ^= 1;
-      };
-      uint32_t seg = 0;
-      for (int f = f0; ok && f < f1; f += sg.nt, seg ^= 1) {
-        segment_at(a, f, f1, &gi, &sg);
-        if (!(ok = wait(bar(kBarQ), seg))) break;
-        if (!(ok = wait(bar(kKReady + kr.stage), kr.phase))) break;
-        tc::fence_after_sync();
-        if (NX == 2 && sg.dual) {  // both groups on every tile
-          issue_s(0, false);
-          issue_s(1, true);
-          for (int n = 0; ok && n < sg.nt; ++n) {
-            step(0, n == 0, n + 1 < sg.nt, true, false);
-            if (ok) step(1, n == 0, n + 1 < sg.nt, false, true);
-          }
-        } else if (NX == 2) {  // the groups on alternate tiles
-          issue_s(0, true);
-          if (sg.nt > 1) {
-            if (!(ok = wait(bar(kKReady + kr.stage), kr.phase))) break;
-            tc::fence_after_sync();
-            issue_s(1, true);
-          }
-          for (int n = 0; ok && n < sg.nt; n += 2) {
-            step(0, n == 0, n + 2 < sg.nt, true, true);
-            if (ok && n + 1 < sg.nt) step(1, n == 0, n + 3 < sg.nt, true, true);
-          }
-        } else {
-          issue_s(0, true);
-          for (int n = 0; ok && n < sg.nt; ++n) step(0, n == 0, n + 1 < sg.nt, true, true);
-        }
-      }
-      if (!ok) atomicOr(a.err, PA_DEVERR_TIMEOUT);
-    }
-    __syncwarp();
-  } else if (warp >= C::kConvWarp0) {
-    // ------------------------------------------------------------ FP8 converters
-    // e4m3 tile -> the f16 buffer: a 16-byte chunk of 16 codes becomes two
-    // 16-byte chunks of f16 in the 64-dim box that holds them; V rows behind the
-    // prefix are zeroed. (The conversions bind a warp: about 2,000 cycles for
-    // the 16 KB of a tile.)
-    if constexpr (FP8) {
-      constexpr int kChunks = D / 16, kPer = 32 / kChunks;  // chunks a row, rows a pass
-      constexpr int kOctets = C::kKv / 8 / kConv;           // row octets of a warp
-      const int row0 = (warp - C::kConvWarp0) * kOctets * 8;
-      const int ch = lane % kChunks, q0 = lane / kChunks;
-      const int c16 = 2 * (ch & 3);
-      auto convert = [&](uint32_t src, uint32_t dst) {
-        src += (ch >> 3) * C::kBox;
-        dst += (ch >> 2) * C::kBox;
-        // rows r, r + 8, ... share one swizzle
-        static_assert(8 % kPer == 0, "passes of a row octet");
-#pragma unroll 1
-        for (int p = 0; p < 8 / kPer; ++p) {
-          const int r0 = row0 + q0 + kPer * p;
-          const uint32_t from = src + r0 * 128 + (((ch & 7) ^ (r0 & 7)) << 4);
-          const uint32_t lo = dst + r0 * 128 + ((c16 ^ (r0 & 7)) << 4);
-          const uint32_t hi = dst + r0 * 128 + (((c16 + 1) ^ (r0 & 7)) << 4);
-#pragma unroll
-          for (int k = 0; k < kOctets; ++k) {
-            uint32_t w[4], h[8];
-            lds_v4(from + 1024 * k, w[0], w[1], w[2], w[3]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              h[2 * i] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] & 0xffffu));
-              h[2 * i + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] >> 16));
-            }
-            sts_v4(lo + 1024 * k, make_uint4(h[0], h[1], h[2], h[3]));
-            sts_v4(hi + 1024 * k, make_uint4(h[4], h[5], h[6], h[7]));
-          }
-        }
-      };
-      bool ok = true;
       int c = 0;
       for (int f = f0; ok && f < f1; f += sg.nt) {
         segment_at(a, f, f1, &gi, &sg);
+        int row = row_of(sg.t0);
         for (int n = 0; ok && n < sg.nt; ++n, ++c) {
-          const int lim = sg.g.prefix - (sg.t0 + n) * C::kKv;  // rows of the tile inside the prefix
-          const uint32_t free_par = ((c - 2) >> 1) & 1;  // of the buffers' last tile
-          if (!(ok = wait_all(bar(kBarKFull), c & 1))) break;
-          if (c > 1 && !(ok = wait_all(bar(kBarCKFree + (c & 1)), free_par))) break;
-          convert(sK, sKc + (c & 1) * C::kTile);
-          fence_proxy_async();  // the f16 tile, visible to the tensor core
-          mbar_arrive(bar(kBarCKFull + (c & 1)));
-          mbar_arrive(bar(kBarKEmpty));  // reload the stage
-          const uint32_t vt = sVc + (c & 1) * C::kTile;
-          if (!(ok = wait_all(bar(kBarVFull), c & 1))) break;
-          if (c > 1 && !(ok = wait_all(bar(kBarCVFree + (c & 1)), free_par))) break;
-          convert(sV, vt);
-          if (lim < C::kKv) {
-            __syncwarp();
-            for (int i = max(lim, row0) * 8 + lane; i < (row0 + kOctets * 8) * 8; i += 32)
-#pragma unroll
-              for (int box = 0; box < C::kBoxes; ++box)
-                sts_v4(vt + box * C::kBox + i * 16, make_uint4(0u, 0u, 0u, 0u));
+          // looked up while the waits below run
+          const int next = n + 1 < sg.nt ? row_of(sg.t0 + n + 1) : -1;
+          if (do_k) {  // the release of the stage's last tile: the phase before
+            if (c >= C::kKStages && !(ok = wait_all(bar(kBarKEmpty + kr.stage), kr.phase ^ 1))) break;
+            load(kr.stage, row, false);
+            kr.next(C::kKStages);
           }
-          fence_proxy_async();
-          mbar_arrive(bar(kBarCVFull + (c & 1)));
-          mbar_arrive(bar(kBarVEmpty));
+          if (do_v) {
+            if (c >= C::kVStages && !(ok = wait_all(bar(kBarVEmpty + vr.stage), vr.phase ^ 1))) break;
+            load(vr.stage, row, true);
+            vr.next(C::kVStages);
+          }
+          row = next;
         }
       }
       if (!ok && lane == 0) atomicOr(a.err, PA_DEVERR_TIMEOUT);
+    } else if (warp == C::kMmaWarp) {
+      // ------------------------------------------------------------ MMA issue
+      // One thread does all of it, and little besides: its own instructions are
+      // on the critical path of every tile (a wait by the whole warp costs about
+      // 150 cycles even when there is nothing to wait for, the products of one
+      // tile and group about 1,200).
+      if (lane == 0) {
+        constexpr uint32_t idS = tc::idesc_f16(kRows, C::kKv, kBf16, false);
+        constexpr uint32_t idO = tc::idesc_f16(kRows, D, kBf16, true);
+        // Positions of the K and V tiles in use, and the barriers that say they
+        // are ready: the ring's, or the converted buffers' (two of each).
+        constexpr int KB = FP8 ? 2 : C::kKStages, VB = FP8 ? 2 : C::kVStages;
+        constexpr int kKReady = FP8 ? kBarCKFull : kBarKFull, kKFree = FP8 ? kBarCKFree : kBarKEmpty;
+        constexpr int kVReady = FP8 ? kBarCVFull : kBarVFull, kVFree = FP8 ? kBarCVFree : kBarVEmpty;
+        const uint64_t dQ = tc::sdesc_sw128(sQ, 16, 1024);
+        const uint64_t dK = tc::sdesc_sw128(FP8 ? sKc : sK, 16, 1024);
+        const uint64_t dV = tc::sdesc_sw128(FP8 ? sVc : sV, C::kBox, 1024);
+        Ring kr, vr;
+        // releases still to come: one is committed only when something will wait
+        // for it, so that no arrive outlives the CTA
+        int k_free = ntiles - KB, v_free = ntiles - VB;
+        auto wait = [&](uint32_t b, uint32_t parity) { return mbar_wait_bounded(b, parity, kWaitNs); };
+        auto issue_s = [&](int x, bool last) {
+#pragma unroll
+          for (int box = 0; box < C::kBoxes; ++box)
+            mma4_ss(tmem + C::kColS + C::kKv * x, dQ + ((x * C::kQBytes + box * C::kQBox) >> 4),
+                    dK + ((kr.stage * C::kTile + box * C::kBox) >> 4), idS, box > 0);
+          tc::commit(bar(kBarS + x));
+          if (last) {
+            if (k_free-- > 0) tc::commit(bar(kKFree + kr.stage));
+            kr.next(KB);
+          }
+        };
+        // O_x (+)= P_x V: 16 tokens a step, P in 8 columns each from 64 h on
+        auto issue_o = [&](int x, bool first, bool last) {
+#pragma unroll
+          for (int h = 0; h < C::kKv / 64; ++h)
+            mma4_ts(tmem + C::kColO + D * x, tmem + C::kColS + C::kKv * x + 64 * h,
+                    dV + ((vr.stage * C::kTile) >> 4) + 512 * h, idO, !first || h > 0);
+          tc::commit(bar(kBarO + x));
+          if (last) {
+            if (v_free-- > 0) tc::commit(bar(kVFree + vr.stage));
+            vr.next(VB);
+          }
+        };
+        bool ok = true;
+        uint32_t par[2] = {0, 0};  // phase of each group's next product
+        // Group x's products on one tile: O, and S of its next tile if there is
+        // one. first_use, last_use: of the tile's V (and the next one's K).
+        auto step = [&](int x, bool first, bool more, bool first_use, bool last_use) {
+          // P_x (and clean V rows) written, V there; both tested before either is
+          // waited for
+          const bool v_in = !first_use || mbar_try_wait(bar(kVReady + vr.stage), vr.phase);
+          const bool p_in = mbar_try_wait(bar(kBarP + x), par[x]);
+          if (!p_in && !(ok = wait(bar(kBarP + x), par[x]))) return;
+          if (!v_in && !(ok = wait(bar(kVReady + vr.stage), vr.phase))) return;
+          tc::fence_after_sync();
+          issue_o(x, first, last_use);
+          if (more) {
+            const bool k_in = !first_use || mbar_try_wait(bar(kKReady + kr.stage), kr.phase);
+            if (!(ok = wait(bar(kBarO + x), par[x]))) return;  // P_x consumed
+            if (!k_in && !(ok = wait(bar(kKReady + kr.stage), kr.phase))) return;
+            tc::fence_after_sync();
+            issue_s(x, last_use);
+          }
+          par[x] ^= 1;
+        };
+        uint32_t seg = 0;
+        for (int f = f0; ok && f < f1; f += sg.nt, seg ^= 1) {
+          segment_at(a, f, f1, &gi, &sg);
+          if (!(ok = wait(bar(kBarQ), seg))) break;
+          if (!(ok = wait(bar(kKReady + kr.stage), kr.phase))) break;
+          tc::fence_after_sync();
+          if (NX == 2 && sg.dual) {  // both groups on every tile
+            issue_s(0, false);
+            issue_s(1, true);
+            for (int n = 0; ok && n < sg.nt; ++n) {
+              step(0, n == 0, n + 1 < sg.nt, true, false);
+              if (ok) step(1, n == 0, n + 1 < sg.nt, false, true);
+            }
+          } else if (NX == 2) {  // the groups on alternate tiles
+            issue_s(0, true);
+            if (sg.nt > 1) {
+              if (!(ok = wait(bar(kKReady + kr.stage), kr.phase))) break;
+              tc::fence_after_sync();
+              issue_s(1, true);
+            }
+            for (int n = 0; ok && n < sg.nt; n += 2) {
+              step(0, n == 0, n + 2 < sg.nt, true, true);
+              if (ok && n + 1 < sg.nt) step(1, n == 0, n + 3 < sg.nt, true, true);
+            }
+          } else {
+            issue_s(0, true);
+            for (int n = 0; ok && n < sg.nt; ++n) step(0, n == 0, n + 1 < sg.nt, true, true);
+          }
+        }
+        if (!ok) atomicOr(a.err, PA_DEVERR_TIMEOUT);
+      }
+      __syncwarp();
+    } else {
+      // ------------------------------------------------------------ FP8 converters
+      // e4m3 tile -> the f16 buffer: a 16-byte chunk of 16 codes becomes two
+      // 16-byte chunks of f16 in the 64-dim box that holds them; V rows behind the
+      // prefix become zeros. (The conversions bind a warp: about 2,000 cycles for
+      // 8 KB.)
+      if constexpr (FP8) {
+        constexpr int kChunks = D / 16, kPer = 32 / kChunks;  // chunks a row, rows a pass
+        constexpr int kOctets = C::kKv / 8;  // of rows: a warp takes every kConv-th
+        const int o0 = warp - C::kConvWarp0;
+        const int ch = lane % kChunks, q0 = lane / kChunks;
+        const int c16 = 2 * (ch & 3);
+        auto convert = [&](uint32_t src, uint32_t dst, int lim) {
+          src += (ch >> 3) * C::kBox;
+          dst += (ch >> 2) * C::kBox;
+          // rows r, r + 8, ... share one swizzle
+          static_assert(8 % kPer == 0, "passes of a row octet");
+#pragma unroll 1
+          for (int p = 0; p < 8 / kPer; ++p) {
+            const int r0 = 8 * o0 + q0 + kPer * p;
+            const uint32_t from = src + r0 * 128 + (((ch & 7) ^ (r0 & 7)) << 4);
+            const uint32_t lo = dst + r0 * 128 + ((c16 ^ (r0 & 7)) << 4);
+            const uint32_t hi = dst + r0 * 128 + (((c16 + 1) ^ (r0 & 7)) << 4);
+#pragma unroll
+            for (int k = 0; k < kOctets; k += kConv) {
+              if (o0 + k >= kOctets) break;
+              uint32_t w[4] = {0u, 0u, 0u, 0u}, h[8];
+              if (8 * (o0 + k) < lim) lds_v4(from + 1024 * k, w[0], w[1], w[2], w[3]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                h[2 * i] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] & 0xffffu));
+                h[2 * i + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] >> 16));
+              }
+              sts_v4(lo + 1024 * k, make_uint4(h[0], h[1], h[2], h[3]));
+              sts_v4(hi + 1024 * k, make_uint4(h[4], h[5], h[6], h[7]));
+            }
+          }
+        };
+        bool ok = true;
+        int c = 0;
+        for (int f = f0; ok && f < f1; f += sg.nt) {
+          segment_at(a, f, f1, &gi, &sg);
+          for (int n = 0; ok && n < sg.nt; ++n, ++c) {
+            const int lim = sg.g.prefix - (sg.t0 + n) * C::kKv;  // rows of the tile inside the prefix
+            const uint32_t free_par = ((c - 2) >> 1) & 1;  // of the buffers' last tile
+            if (!(ok = wait_all(bar(kBarKFull), c & 1))) break;
+            if (c > 1 && !(ok = wait_all(bar(kBarCKFree + (c & 1)), free_par))) break;
+            convert(sK, sKc + (c & 1) * C::kTile, C::kKv);
+            fence_proxy_async();  // the f16 tile, visible to the tensor core
+            mbar_arrive(bar(kBarCKFull + (c & 1)));
+            mbar_arrive(bar(kBarKEmpty));  // reload the stage
+            const uint32_t vt = sVc + (c & 1) * C::kTile;
+            if (!(ok = wait_all(bar(kBarVFull), c & 1))) break;
+            if (c > 1 && !(ok = wait_all(bar(kBarCVFree + (c & 1)), free_par))) break;
+            convert(sV, vt, lim);
+            fence_proxy_async();
+            mbar_arrive(bar(kBarCVFull + (c & 1)));
+            mbar_arrive(bar(kBarVEmpty));
+          }
+        }
+        if (!ok && lane == 0) atomicOr(a.err, PA_DEVERR_TIMEOUT);
+      }
     }
   } else {
     // ------------------------------------------------------------ softmax
+    if constexpr (C::kSplitRegs)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int x = warp >> 2;        // group
     const int r = tid - x * kRows;  // row of the tile = tensor-memory lane
     const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -738,6 +747,14 @@ cudaError_t launch_typed(const CUtensorMap& tk, const CUtensorMap& tv, const Pre
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        Cfg<D, FP8>::kBytes);
   if (e != cudaSuccess) return e;
+  if constexpr (Cfg<D, FP8>::kSplitRegs) {
+    // the softmax warps wait for registers that the block must have been given
+    static const int regs = [] {
+      cudaFuncAttributes f;
+      return cudaFuncGetAttributes(&f, prefix_attn_tc_kernel<QT, D, FP8>) == cudaSuccess ? f.numRegs : 0;
+    }();
+    if (2 * regs < kSoftmaxRegs + kOtherRegs) return cudaErrorLaunchOutOfResources;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(Cfg<D, FP8>::kThreads);
