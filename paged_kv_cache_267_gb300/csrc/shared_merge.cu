@@ -12,7 +12,8 @@
 // four of them while the maxima are still on their way. Two dependent round
 // trips (plan, partials) and the partials' bytes through L2 bound it. Steps with
 // few pairs give each task four warps, which share its list and are joined
-// through shared memory. The list is worked out before the dependency wait,
+// through shared memory. From the end of the wait: 3.3 us for 512 pairs of about
+// 7 partials, 4.2 us for 2048 pairs of about 5. The list is worked out before the dependency wait,
 // from plans that are complete by then. (A half warp a column, which works out the list for
 // every column, took 33 us for 8192 columns of about 8 partials; a CTA a pair
 // with the weights in shared memory first, 17 us.)
