@@ -344,7 +344,9 @@ pa_status pa_decode_noalloc(const pa_tensor* out, const pa_tensor* q,
  * A step that is decoded plainly does not look at either.
  * Like pa_decode, the call reads group_starts, prefix_lens, seq_lens and
  * block_tables before it waits for the previous kernel of the stream, and q
- * and the caches after.
+ * and the caches after. Its last kernel lets its dependents start before out is
+ * complete: a kernel launched as one waits for it before it reads out, and the
+ * library's own do.
  * Workspace: pa_decode_shared_workspace_size() bytes, from the same source as
  * pa_decode's and under the same rules. Errors as for pa_decode.
  */

@@ -252,7 +252,7 @@ struct WsLayout {
 
 // Hv pairs per sequence with CG columns each (Hkv and G for single-query decode).
 // NG groups and shared_slots prefix partials: shared-prefix steps (else 0).
-WsLayout ws_layout(int64_t B, int Hv, int CG, int D, int64_t workers, int64_t NG = 0,
+WsLayout ws_layout(int64_t B, int Hv, int CG, int D, int64_t workers,
                    size_t shared_slots = 0, int ctas = 0) {
   const size_t S = static_cast<size_t>(B) * Hv;
   const size_t nslot = 2 * S + workers + static_cast<size_t>(workers) * kPiecesPerWorker;
@@ -261,9 +261,13 @@ WsLayout ws_layout(int64_t B, int Hv, int CG, int D, int64_t workers, int64_t NG
   // The pool counter sits at a fixed offset: it must stay zero between calls
   // whatever their shapes, and each step's merge only resets its own copy.
   L.pool = o;  o += 256;
-  L.plan = o;  o += round_up(static_cast<size_t>(pa::plan_words(static_cast<int>(B))) * 4, 256);
+  // While the merge of a shared-prefix step still reads its partials, the next
+  // step's plan is written, of whatever shape: there, plans have the room of the
+  // largest (0.4 MB).
+  const int64_t rows = shared_slots ? kMaxBatch : B;
+  L.plan = o;  o += round_up(static_cast<size_t>(pa::plan_words(static_cast<int>(rows))) * 4, 256);
   L.shared = o;
-  if (shared_slots) o += round_up(pa::shared_plan_words(B, NG, ctas) * 4, 256);
+  if (shared_slots) o += round_up(pa::shared_plan_words(rows, kMaxBatch, ctas) * 4, 256);
   L.shared_slot0 = nslot;
   L.part = o;  o += (nslot + shared_slots) * static_cast<size_t>(pa::part_stride(CG, D)) * sizeof(float);
   L.total = o;
@@ -569,7 +573,7 @@ pa_status workspace_size(int64_t batch, int64_t num_queries, int32_t num_q_heads
   int64_t workers = static_cast<int64_t>(st->num_sms) * kMaxCtasPerSm * kWarpsPerCta;
   const int cap = g_tune_max_ctas.load();
   if (cap > 0 && cap * kWarpsPerCta < workers) workers = static_cast<int64_t>(cap) * kWarpsPerCta;
-  *bytes = ws_layout(batch, static_cast<int>(Hv), CG, head_dim, workers, num_groups,
+  *bytes = ws_layout(batch, static_cast<int>(Hv), CG, head_dim, workers,
                      num_groups > 0 ? most_shared_slots(batch, num_kv_heads,
                                                         num_q_heads / num_kv_heads, head_dim,
                                                         st->num_sms)
@@ -862,7 +866,7 @@ pa_status plan_call(DeviceState* st, const DecodeCall& c, DecodePlan* plan, WsLa
     plan->grid = static_cast<int>(std::max<int64_t>(ctas, 1));
     plan->workers = plan->grid * plan->var.warps;
   }
-  *layout = ws_layout(c.B, c.Hv, c.CG, static_cast<int>(c.D), plan->workers, sh ? sh->NG : 0,
+  *layout = ws_layout(c.B, c.Hv, c.CG, static_cast<int>(c.D), plan->workers,
                       sh ? most_shared_slots(c.B, c.Hkv, c.G, static_cast<int>(c.D), st->num_sms) : 0,
                       sh ? st->num_sms : 0);
   return PA_OK;

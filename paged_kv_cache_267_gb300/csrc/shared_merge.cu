@@ -12,11 +12,11 @@
 // four of them while the maxima are still on their way. Two dependent round
 // trips (plan, partials) and the partials' bytes through L2 bound it. Steps with
 // few pairs give each task four warps, which share its list and are joined
-// through shared memory. From the end of the wait: 3.3 us for 512 pairs of about
-// 7 partials, 4.2 us for 2048 pairs of about 5. The list is worked out before the dependency wait,
-// from plans that are complete by then. (A half warp a column, which works out the list for
-// every column, took 33 us for 8192 columns of about 8 partials; a CTA a pair
-// with the weights in shared memory first, 17 us.)
+// through shared memory. The list is worked out before the dependency wait, from
+// plans that are complete by then. From the end of the wait: 3.3 us for 512 pairs
+// of about 7 partials, 4.2 us for 2048 pairs of about 5. (A half warp a column,
+// which works out the list for every column, took 33 us for 8192 columns of about
+// 8 partials; a CTA a pair with the weights in shared memory first, 17 us.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -115,12 +115,21 @@ __global__ void __launch_bounds__(kThreads, 4) shared_merge_kernel(const SharedM
   const int hl = lane / C, cl = lane % C;  // head and partial this lane reads
   float M = -INFINITY, den = 0.f;          // running maximum and sum of head hl
   const uint64_t once = l2_evict_first();  // each partial is read once
+  // the list is worked out: this CTA has read all that it wants of the plans
+  __syncthreads_or((n | slot0) < 0);
   griddep_wait();  // the partials (the prefix kernel's too) are complete and visible
-  if (last) {
-    st_relaxed_gpu(flag, 0);
-    a.pool[2] = 0u;
+  if (tid == 0) {
+    if (last) {
+      st_relaxed_gpu(flag, 0);
+      a.pool[2] = 0u;
+    }
+    if (blockIdx.x == 0) a.pool[0] = 0u;
+    // The next kernel may start: what it writes before it waits for this one, a
+    // plan and its flag, is not read here any more and is reset. (Steps one after
+    // the other then plan during the merge.)
+    __threadfence();
+    griddep_launch_dependents();
   }
-  if (blockIdx.x == 0 && tid == 0) a.pool[0] = 0u;
 
   for (int k0 = k_lo; k0 < k_hi; k0 += 32) {
     const int k1 = min(k0 + 32, k_hi);

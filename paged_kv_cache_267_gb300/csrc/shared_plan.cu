@@ -55,26 +55,20 @@ struct Units {
 
 // How many CTAs (SMs) the prefix kernel's tiles go to. The decode kernel needs
 // none of its results and takes the SMs it leaves free, so the step lasts as
-// long as the longer of the two:
+// long as the longer of the two,
 //   max(a + Tp / n, b + Td / (N - n)),
 // with the tiles' times on one SM (measured with both kernels running) and what
-// a CTA of each costs once. Near all SMs, the kernels run better one after the
-// other: with 95% of the SMs for a 65536-token document its step took 93 us, with
-// all of them first 71. Called by one warp.
+// a CTA of each costs once. They are equal where, with c = a - b and
+// S = Tp + Td - c N,  c n^2 + S n - Tp N = 0, which is solved without a difference
+// of large numbers. Near all SMs, the kernels run better one after the other: with
+// 95% of the SMs for a 65536-token document its step took 93 us, with all of them
+// first 71. (Every n tried, 32 at once: 1,000 cycles, a tenth of the plan.)
 __device__ __forceinline__ int share_sms(const SharedPlanArgs& a, int tiles, int dual, int tails) {
   const float tp = a.cost.dual_ns * dual + a.cost.single_ns * (tiles - dual);
-  const float td = a.cost.tail_ns * tails;
-  const int N = a.ctas;
-  unsigned best = 0xffffffffu;
-#pragma unroll 1
-  for (int n0 = 1; n0 < N; n0 += 32) {
-    const int n = min(n0 + static_cast<int>(threadIdx.x & 31), N - 1);
-    const float t = fmaxf(a.cost.prefix_ns + __fdividef(tp, n), a.cost.decode_ns + __fdividef(td, N - n));
-    // time in the upper bits (a positive float's bits order as the float), n below
-    best = min(best, (__float_as_uint(t) & 0xfffffe00u) | static_cast<unsigned>(n & 511));
-  }
-  const int n = static_cast<int>(__reduce_min_sync(kFull, best) & 511u);
-  return n > a.whole ? N : n;
+  const float td = a.cost.tail_ns * tails, N = a.ctas, c = a.cost.prefix_ns - a.cost.decode_ns;
+  const float s = tp + td - c * N, root = sqrtf(fmaxf(s * s + 4.f * c * tp * N, 0.f));
+  const int n = static_cast<int>(__fdividef(2.f * tp * N, fmaxf(s + root, 1.f)) + 0.5f);
+  return n > a.whole ? a.ctas : max(n, 1);
 }
 
 // ONE: up to 31 groups, whose scans are the first warp's alone (a much shorter
@@ -206,14 +200,7 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
     if constexpr (ONE) __syncwarp(); else __syncthreads();
     const int dual = s_dual;
     const int tiles = run;
-    int ctas = a.ctas;
-    if (tid < 32) ctas = share_sms(a, tiles, dual, s_tails * a.Hkv);
-    if constexpr (!ONE) {  // the first warp's answer, for all
-      if (tid == 0) s_wsz = ctas;
-      __syncthreads();
-      ctas = s_wsz;
-      __syncthreads();
-    }
+    const int ctas = share_sms(a, tiles, dual, s_tails * a.Hkv);
     const int wsz = max((tiles + ctas - 1) / ctas, a.min_tiles);
     if (tid == 0) {
       s_tiles = tiles;

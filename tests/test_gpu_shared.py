@@ -443,6 +443,47 @@ def test_other_streams_and_shapes_in_turn(pa_lib):
     assert pa_lib.check_device_error() == 0
 
 
+def test_steps_that_follow_one_another_without_a_gap(pa_lib):
+    """A step may plan while the one before is still being joined: steps of very
+    different shapes in one workspace, enqueued back to back, shared and plain."""
+    bs = [Batch([(640, [9] * 40), (1600, [7, 8, 9])], seed=31), Batch([(16, [1])] * 2000 + [(32, [2] * 96)], heads=(2, 1), seed=32),
+          Batch([(64, [2, 3])] * 30, dt="f16", seed=33), Batch([(2048, [5, 9, 300])], heads=(32, 8), seed=34)]
+    args = [b.args() for b in bs]
+    want = [b.run(pa_lib) for b in bs]
+    for b, w in zip(bs, want):
+        b.check(w)
+    order = [0, 1, 0, 2, 3, 1, 3, 2, 0, 3, 1, 2] * 4
+    outs = [torch.empty_like(bs[k].q) for k in order]
+    plain = [torch.empty_like(bs[k].q) for k in order]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for rep in range(2):
+        with torch.cuda.stream(s):
+            for i, k in enumerate(order):
+                pa_lib.decode_shared(*args[k], out=outs[i], stream=s, **bs[k].kw())
+                if i % 3 == rep:
+                    pa_lib.decode(*args[k][:5], out=plain[i], stream=s, **bs[k].kw())
+        torch.cuda.synchronize()
+        for i, k in enumerate(order):
+            assert torch.equal(outs[i], want[k]), (rep, i, k)
+            if i % 3 == rep:
+                bs[k].check(plain[i])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        for i, k in enumerate(order):
+            pa_lib.decode_shared(*args[k], out=outs[i], stream=s, **bs[k].kw())
+    for _ in range(3):
+        for o in outs:
+            o.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, k in enumerate(order):
+            assert torch.equal(outs[i], want[k]), (i, k)
+    assert pa_lib.check_device_error() == 0
+
+
 def test_threads_calling_on_one_stream(pa_lib):
     """Steps of different shapes from two host threads on the same stream: their
     launches must not mix in the stream's one workspace."""
