@@ -255,7 +255,9 @@ struct WsLayout {
 WsLayout ws_layout(int64_t B, int Hv, int CG, int D, int64_t workers,
                    size_t shared_slots = 0, int ctas = 0) {
   const size_t S = static_cast<size_t>(B) * Hv;
-  const size_t nslot = 2 * S + workers + static_cast<size_t>(workers) * kPiecesPerWorker;
+  // (a shared-prefix step has no pool pieces)
+  const size_t nslot =
+      shared_slots ? S + workers : 2 * S + workers + static_cast<size_t>(workers) * kPiecesPerWorker;
   WsLayout L;
   size_t o = 0;
   // The pool counter sits at a fixed offset: it must stay zero between calls
@@ -282,14 +284,9 @@ size_t most_shared_slots(int64_t B, int64_t Hkv, int G, int D, int grid) {
   return static_cast<size_t>(2 * Hkv * B + grid * std::max<int64_t>(unit, 1));
 }
 
-// The tails of a shared-prefix step take no pool: their CTAs start at different
-// times, which the split of the SMs allows for, and the pool's many small
-// partials cost the merge more than its balance gains (e4m3 batch of 256 98.0 us
-// with it, 95.2 without; 65536-token document 75.5 and 70.7; 4 groups of 32 103.7
-// and 104.8).
-int tuned_pool_permille(bool tails) {
+int tuned_pool_permille() {
   const int v = g_tune_pool.load();
-  return v == 0 ? (tails ? 0 : kDefaultPoolPermille) : (v < 0 ? 0 : v);
+  return v == 0 ? kDefaultPoolPermille : (v < 0 ? 0 : v);
 }
 
 int tuned_piece(bool fp8_decode) {
@@ -422,7 +419,7 @@ pa_status plan_decode(DeviceState* st, int ct, int qt, int kind, int64_t B, int 
   p->workers = p->grid * p->var.warps;
   const int mt = g_tune_min_tiles.load();
   p->min_tiles = mt > 0 ? mt : kDefaultMinTiles;
-  p->pool_permille = tuned_pool_permille(kind == kTails);
+  p->pool_permille = tuned_pool_permille();
   p->piece = tuned_piece(ct == pa::kE4M3 && kind != kChunked);
   return PA_OK;
 }
@@ -970,6 +967,8 @@ pa_status run_decode(const DecodeCall& c, DeviceState* st, const DecodePlan& pla
     p.whole = grid * 17 / 20;
     p.decode_ctas = plan.grid;
     p.decode_per_sm = plan.per_sm;
+    p.decode_warps = plan.var.warps;
+    p.decode_min_tiles = plan.min_tiles;
     p.cost = shared_cost(D, c.fp8);
     p.min_tiles = kPrefixMinTiles;
     e = pa::shared_plan_launch(p, cs, !prof);
@@ -1026,14 +1025,11 @@ pa_status run_decode(const DecodeCall& c, DeviceState* st, const DecodePlan& pla
     pa::SharedMergeArgs sm;
     sm.out = m.out;
     sm.part = m.part;
-    sm.plan = m.plan;
-    sm.shared = reinterpret_cast<const int32_t*>(wsb + layout.shared);
-    sm.pool = m.pool;
+    sm.plan = reinterpret_cast<const int32_t*>(wsb + layout.shared);
     sm.B = m.B;
     sm.Hkv = m.Hkv;
     sm.G = m.G;
     sm.D = m.D;
-    sm.NW = m.NW;
     sm.NG = static_cast<int>(sh->NG);
     sm.ctas = st->num_sms;
     sm.part0 = static_cast<int>(layout.shared_slot0);

@@ -59,9 +59,6 @@ __device__ __forceinline__ void piece_range(int i, const StepPlan& pl, int* f0, 
 // outside is reported through `err`) and s_pref[0 .. B] with the exclusive
 // prefix of tiles per pair over the sequences. The host bounds B * Hv * tiles
 // per pair below 2^31, so the tile counts fit 32-bit integers.
-// GIVEN: sequence b has s_pref[b + 1] tiles per pair (filled by the caller
-// before) instead of those of its window.
-template <bool GIVEN>
 __device__ inline StepPlan plan_step(const PlanIn& p, int* s_len, int* s_pref) {
   constexpr unsigned FULL = 0xffffffffu;
   __shared__ int s_last_long;
@@ -80,8 +77,7 @@ __device__ inline StepPlan plan_step(const PlanIn& p, int* s_len, int* s_pref) {
     int run = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
       const int b = b0 + lane;
-      int x = 0;
-      if (b < p.B) x = GIVEN ? s_pref[b + 1] : tiles_of(s_len[b], p.span);
+      int x = (b < p.B) ? tiles_of(s_len[b], p.span) : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(FULL, x, o);

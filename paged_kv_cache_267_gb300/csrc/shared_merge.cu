@@ -13,7 +13,7 @@
 // trips (plan, partials) and the partials' bytes through L2 bound it. Steps with
 // few pairs give each task four warps, which share its list and are joined
 // through shared memory. The list is worked out before the dependency wait, from
-// plans that are complete by then. From the end of the wait: 3.3 us for 512 pairs
+// the plan, which is complete by then. From the end of the wait: 3.3 us for 512 pairs
 // of about 7 partials, 4.2 us for 2048 pairs of about 5. (A half warp a column,
 // which works out the list for every column, took 33 us for 8192 columns of about
 // 8 partials; a CTA a pair with the weights in shared memory first, 17 us.)
@@ -21,7 +21,6 @@
 #include <cuda_fp16.h>
 
 #include "pa_internal.h"
-#include "plan.cuh"
 #include "ptx.cuh"
 #include "shared_plan.cuh"
 #include "step_ops.h"
@@ -34,8 +33,6 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kChunk = 512;   // floats of a pair a task joins
 constexpr int kFlight = 4;    // partials in flight
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kPlanPolls = 64;     // polls of the plan flag before the wait, at most
-constexpr int kPlanPollNs = 500;   // pause between polls
 
 template <int OT, int D, int WPT>
 __global__ void __launch_bounds__(kThreads, 4) shared_merge_kernel(const SharedMergeArgs a) {
@@ -45,23 +42,6 @@ __global__ void __launch_bounds__(kThreads, 4) shared_merge_kernel(const SharedM
   __shared__ __align__(16) float s_acc[WPT > 1 ? kWarps - 1 : 1][kChunk];
   __shared__ float s_m[kWarps][NH], s_l[kWarps][NH];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // Before the dependency wait: the shared plan is complete (the decode kernel
-  // started after it), and the decode kernel's is once its flag is set, usually
-  // long before that kernel ends; a CTA that does not see the flag waits first.
-  // The last CTA to have read the flag clears it, and the count, after the wait.
-  int32_t* const flag = reinterpret_cast<int32_t*>(a.pool) + 1;
-  int early = 0;
-  bool last = false;
-  if (tid == 0) {
-    for (int i = 0; i < kPlanPolls; ++i) {
-      early = ld_acquire_gpu(flag) == 1;
-      if (early) break;
-      __nanosleep(kPlanPollNs);
-    }
-    last = atomicAdd(a.pool + 2, 1u) == gridDim.x - 1;
-  }
-  early = __syncthreads_or(early);
-  if (!early) griddep_wait();
   const int GD = a.G * D;
   const int chunks = (GD + kChunk - 1) / kChunk;
   int task = WPT > 1 ? static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x) * kWarps + warp;
@@ -69,31 +49,27 @@ __global__ void __launch_bounds__(kThreads, 4) shared_merge_kernel(const SharedM
   if (idle) task = 0;
   const int pair = chunks == 1 ? task : task / chunks, e0 = (task - pair * chunks) * kChunk;
   const int b = pair / a.Hkv, kvh = pair - b * a.Hkv;
-  StepPlan pl;
-  pl.total = 0;
-  pl.ws = ld_relaxed_gpu(a.plan + 1);
-  pl.ts = ld_relaxed_gpu(a.plan + 2);
-  pl.piece = ld_relaxed_gpu(a.plan + 3);
-  pl.n_pool = 0;
-  const int pref = ld_relaxed_gpu(a.plan + kPlanScalars + b);
-  const int nt = ld_relaxed_gpu(a.plan + kPlanScalars + b + 1) - pref;
-  const SharedRow row = shared_rows(a.shared, a.ctas, a.NG)[b];
-  const int wsz = a.shared[kShWsz];
+  // Before the dependency wait: the plan is complete (the decode kernel started
+  // after it).
+  const SharedRow row = shared_rows(a.plan, a.ctas, a.NG)[b];
+  const int wsz = a.plan[kShWsz], tail_ws = a.plan[kShTailsWs];
 
-  const Cands cd = pair_cands(a.Hkv * pref + kvh * nt, nt, pl);
-  const int tail = cd.na + cd.np;
+  // the decode kernel's partials: of the warps whose tiles meet the pair's
+  int tail = 0, tail0 = 0;
+  if (row.tiles > 0) {
+    const int f0 = a.Hkv * row.pref + kvh * row.tiles, w0 = f0 / tail_ws;
+    tail0 = pair + w0;
+    tail = (f0 + row.tiles - 1) / tail_ws - w0 + 1;
+  }
   int n = tail, slot0 = 0;
   if (row.nt > 0) {
     const int f0 = row.f0 + kvh * row.kv_step, w0 = f0 / wsz;
     slot0 = a.part0 + row.slot0 + (kvh * row.nut + row.lid0 + w0) * row.up;
     n += (f0 + row.nt - 1) / wsz - w0 + 1;
   }
-  const int S = a.B * a.Hkv;
   const size_t stride = static_cast<size_t>(part_stride(a.G, D));
   auto partial = [&](int k) -> const float* {
-    const int slot = k < cd.na ? pair + cd.w0 + k
-                     : k < tail ? S + a.NW + pair + cd.i0 + (k - cd.na)
-                                : slot0 + (k - tail) * row.up;
+    const int slot = k < tail ? tail0 + k : slot0 + (k - tail) * row.up;
     return a.part + static_cast<size_t>(slot) * stride;
   };
   const int h0 = e0 >> kLog2D;  // heads of this chunk
@@ -115,21 +91,13 @@ __global__ void __launch_bounds__(kThreads, 4) shared_merge_kernel(const SharedM
   const int hl = lane / C, cl = lane % C;  // head and partial this lane reads
   float M = -INFINITY, den = 0.f;          // running maximum and sum of head hl
   const uint64_t once = l2_evict_first();  // each partial is read once
-  // the list is worked out: this CTA has read all that it wants of the plans
-  __syncthreads_or((n | slot0) < 0);
+  // the list is worked out: this CTA has read all that it wants of the plan
+  __syncthreads_or((n | slot0 | tail0) < 0);
   griddep_wait();  // the partials (the prefix kernel's too) are complete and visible
-  if (tid == 0) {
-    if (last) {
-      st_relaxed_gpu(flag, 0);
-      a.pool[2] = 0u;
-    }
-    if (blockIdx.x == 0) a.pool[0] = 0u;
-    // The next kernel may start: what it writes before it waits for this one, a
-    // plan and its flag, is not read here any more and is reset. (Steps one after
-    // the other then plan during the merge.)
-    __threadfence();
-    griddep_launch_dependents();
-  }
+  // The next kernel may start: what it writes before it waits for this one, a
+  // plan, is not read here any more. (Steps one after the other then plan during
+  // the merge.)
+  griddep_launch_dependents();
 
   for (int k0 = k_lo; k0 < k_hi; k0 += 32) {
     const int k1 = min(k0 + 32, k_hi);

@@ -98,7 +98,11 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
   int len[4];  // this thread's first rows, in flight while the groups are set up
 #pragma unroll
   for (int j = 0; j < 4; ++j) len[j] = tid + j * nthreads < a.B ? a.seq_lens[tid + j * nthreads] : 0;
-  auto length = [&](int b, int j) -> int { return min(max(j < 4 ? len[j] : a.seq_lens[b], 0), cap); };
+  auto length = [&](int b, int j, bool report = false) -> int {
+    const int L = j < 4 ? len[j] : a.seq_lens[b], x = min(max(L, 0), cap);
+    if (report && x != L) atomicOr(a.err, PA_DEVERR_SEQ_LEN);
+    return x;
+  };
   if (tid == 0) s_tails = s_dual = 0;
   int total;
   if (mine) {
@@ -151,7 +155,7 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
   for (int b0 = tid & ~31, j = 0; b0 < a.B; b0 += nthreads, ++j) {
     const int b = b0 + (tid & 31);
     const int g = b < a.B ? group_of(b) : -1;
-    const int L = b < a.B ? length(b, j) : 0;
+    const int L = b < a.B ? length(b, j, true) : 0;
     const bool in = takes_part(L, g) && b < a.B;
     const int start = start_of(L);
     tails += (L + kTile - 1) / kTile - start / kTile;
@@ -205,12 +209,16 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
     if (tid == 0) {
       s_tiles = tiles;
       s_wsz = wsz;
-      a.plan[kShTotal] = tiles;
       a.plan[kShWsz] = wsz;
-      // the prefix kernel's CTAs with work; the others leave their SMs at once
+      // the prefix kernel's CTAs with work; the others leave their SMs at once, to
+      // the first CTAs of the decode kernel
       const int busy = (tiles + wsz - 1) / wsz;
-      a.plan[kShEarly] = busy > a.whole ? a.decode_ctas
-                                        : max(1, min(a.decode_ctas, (a.ctas - busy) * a.decode_per_sm));
+      const int early = busy > a.whole ? a.decode_ctas
+                                       : max(1, min(a.decode_ctas, (a.ctas - busy) * a.decode_per_sm));
+      const unsigned warps = static_cast<unsigned>(early) * a.decode_warps;
+      a.plan[kShTails] = s_tails;
+      a.plan[kShTailsWs] = max(static_cast<int>((static_cast<unsigned>(s_tails * a.Hkv) + warps - 1u) / warps),
+                               a.decode_min_tiles);
     }
     run = 0;
     for (int g0 = 0; g0 < a.NG; g0 += step) {
@@ -268,11 +276,14 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
     ctas[w] = c;
   }
   SharedRow* rows = const_cast<SharedRow*>(shared_rows(a.plan, a.ctas, a.NG));
-  for (int b = tid, j = 0; b < a.B; b += nthreads, ++j) {
-    const int g = group_of(b);
-    const int L = length(b, j);
+  int before = 0;  // tiles of the rows of earlier rounds
+  for (int b0 = 0, j = 0; b0 < a.B; b0 += nthreads, ++j) {
+    const int b = b0 + tid;
+    const int g = b < a.B ? group_of(b) : -1;
+    const int L = b < a.B ? length(b, j) : 0;
     SharedRow r = {};
     r.start = start_of(L);
+    r.len = L;
     r.tiles = (L + kTile - 1) / kTile - r.start / kTile;
     if (takes_part(L, g)) {
       const Units u = s_units[g];
@@ -288,7 +299,10 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
       r.up = u.up;
       r.nut = u.nut;
     }
-    rows[b] = r;
+    int all;
+    r.pref = before + scan<false>(r.tiles, 0, add, &all) - r.tiles;
+    before += all;
+    if (b < a.B) rows[b] = r;
   }
   griddep_wait();  // what follows this kernel follows its predecessors too
 }

@@ -29,8 +29,9 @@
 namespace pa {
 
 constexpr int kSharedHead = 8;      // header words
-// all tiles; tiles a CTA; decode CTAs that find an SM free of the prefix kernel
-enum { kShTotal = 0, kShWsz = 1, kShEarly = 2 };
+// tiles a CTA of the prefix kernel; 16-token tiles that the decode kernel covers,
+// of one KV head; and tiles a warp of it
+enum { kShWsz = 0, kShTails = 1, kShTailsWs = 2 };
 
 struct SharedGroup {  // 12 words a group
   int r0, n;          // rows
@@ -54,14 +55,16 @@ struct SharedCta {  // 16 words a CTA of the prefix kernel
 
 struct SharedRow {  // 12 words a sequence
   int start;        // first position of its range
-  int head, tiles;  // 16-token tiles the decode kernel covers: before S, and in all
+  int head;         // 16-token tiles of it before S
+  int len;          // its length, inside the tables
+  int pref;         // tiles the decode kernel covers of the sequences before
+  int tiles;        // and of this one
   int nt;           // K/V tiles of its prefix, 0: no part of it here
   int f0;           // first flat tile of its unit at KV head 0
   int kv_step;      // flat tiles between KV heads
   int slot0;        // slot of lid 0 for this sequence's pair
   int lid0;         // unit - wfirst at KV head 0 (added to the CTA)
   int up, nut;      // slots between lids, lids between KV heads
-  int pad[2];
 };
 
 // Words of the plan: header, CTAs, groups, rows.

@@ -100,6 +100,7 @@ struct SharedPlanArgs {
   int ctas;                      // of the prefix kernel
   int whole;                     // more busy CTAs than this: take all SMs
   int decode_ctas, decode_per_sm;  // of the decode kernel
+  int decode_warps, decode_min_tiles;  // a CTA; least tiles a warp
   SharedCost cost;
   int min_tiles;                 // least K/V tiles a CTA
 };
@@ -130,10 +131,8 @@ cudaError_t prefix_launch(int qt, bool fp8, int D, const CUtensorMap& tk, const 
 struct SharedMergeArgs {
   void* out;                     // [B, Hq, D]
   const float* part;             // all partials, the decode kernel's first
-  const int32_t* plan;           // the decode kernel's plan
-  const int32_t* shared;         // the shared plan
-  uint32_t* pool;                // zero again for the next step
-  int B, Hkv, G, D, NW, NG, ctas;
+  const int32_t* plan;           // the step's
+  int B, Hkv, G, D, NG, ctas;
   int part0;                     // first slot of the prefix partials
 };
 cudaError_t shared_merge_launch(int out_type, const SharedMergeArgs& a, cudaStream_t s, bool pdl);
