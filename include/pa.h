@@ -337,8 +337,9 @@ pa_status pa_decode_noalloc(const pa_tensor* out, const pa_tensor* q,
  * The pass reads the prefix through the table of the group's first row that
  * takes part, and no entry of a block that this row does not attend to.
  * A step whose tables could not name more than 72 MB of K/V in all (B * MB *
- * Hkv * bs * D keys and values) is decoded plainly, whatever its groups: there
- * is too little to save (pa_set_shared_path changes that).
+ * Hkv * bs * D keys and values; a window that is shorter counts instead of MB *
+ * bs) is decoded plainly, whatever its groups: there is too little to save
+ * (pa_set_shared_path changes that).
  * Data errors: a prefix length outside [0, MB * bs] or group starts that
  * decrease or leave [0, B] are clamped and flagged (PA_DEVERR_GROUP).
  * A step that is decoded plainly does not look at either.

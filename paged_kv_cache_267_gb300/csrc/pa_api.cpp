@@ -57,7 +57,9 @@ constexpr int kPrefixMinTiles = 2;
 // Shared-prefix steps that could not read more K/V than this, sequence by
 // sequence, are decoded plainly: the plan, the prefix kernel's start and the join
 // cost about 9 us, in which the decode kernel reads shared blocks (from L2) at
-// about 8.6 TB/s (four requests of 272 tokens: 16.4 us shared, 7.2 us plain).
+// about 8.6 TB/s. Of 90 steps of all kinds, 38 of 25 to 72 MB took 9-26 us
+// plainly and 14-26 shared (8 of them less), 36 of 150 to 700 MB 17-113 us
+// plainly and 16-67 shared (30 of them less).
 constexpr double kSharedMinBytes = 72e6;
 constexpr int kPiecesPerWorker = 4;        // pool pieces per worker warp, at most
 constexpr int kMaxCtasPerSm = 2;
@@ -878,13 +880,13 @@ pa_status plan_call(DeviceState* st, const DecodeCall& c, DecodePlan* plan, WsLa
 pa::SharedCost shared_cost(int D, bool fp8) {
   pa::SharedCost c;
   if (D == 64)
-    c = {2000.f, 1600.f, 150.f, 10000.f, 8000.f};
+    c = {2000.f, 1600.f, 6000.f, 150.f, 10000.f, 8000.f};
   else if (D == 128)
-    c = fp8 ? pa::SharedCost{3000.f, 3000.f, 140.f, 10000.f, 5000.f}
-            : pa::SharedCost{3200.f, 3500.f, 190.f, 10000.f, 5000.f};
+    c = fp8 ? pa::SharedCost{3000.f, 3000.f, 6000.f, 140.f, 10000.f, 5000.f}
+            : pa::SharedCost{3200.f, 3500.f, 6000.f, 190.f, 10000.f, 5000.f};
   else  // (one row tile only)
-    c = fp8 ? pa::SharedCost{2600.f, 2600.f, 280.f, 10000.f, 5000.f}
-            : pa::SharedCost{2700.f, 2700.f, 500.f, 10000.f, 5000.f};
+    c = fp8 ? pa::SharedCost{2600.f, 2600.f, 6000.f, 280.f, 10000.f, 5000.f}
+            : pa::SharedCost{2700.f, 2700.f, 6000.f, 500.f, 10000.f, 5000.f};
   return c;
 }
 
@@ -1105,12 +1107,13 @@ pa_status run_chunk_tc(const DecodeCall& c, cudaStream_t cs) {
   return ok();
 }
 
-// Whether a step with NG groups takes the shared path: its tables have to name
-// enough K/V.
+// Whether a step with NG groups takes the shared path: its tables (its windows,
+// where they are shorter) have to name enough K/V.
 bool use_shared(const DecodeCall& c, int64_t NG) {
   const int path = g_shared_path.load();
   if (NG == 0 || path == 1) return false;
-  return path == 2 || dprod({double(c.B), double(c.MB), double(c.Hkv), double(c.bs), double(c.D), 2.0,
+  const int64_t span = c.window > 0 ? std::min<int64_t>(c.MB * c.bs, c.window) : c.MB * c.bs;
+  return path == 2 || dprod({double(c.B), double(span), double(c.Hkv), double(c.D), 2.0,
                              c.fp8 ? 1.0 : 2.0}) >= kSharedMinBytes;
 }
 

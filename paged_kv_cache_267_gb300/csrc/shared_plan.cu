@@ -63,8 +63,8 @@ struct Units {
 // of large numbers. Near all SMs, the kernels run better one after the other: with
 // 95% of the SMs for a 65536-token document its step took 93 us, with all of them
 // first 71. (Every n tried, 32 at once: 1,000 cycles, a tenth of the plan.)
-__device__ __forceinline__ int share_sms(const SharedPlanArgs& a, int tiles, int dual, int tails) {
-  const float tp = a.cost.dual_ns * dual + a.cost.single_ns * (tiles - dual);
+__device__ __forceinline__ int share_sms(const SharedPlanArgs& a, int tiles, int dual, int units, int tails) {
+  const float tp = a.cost.dual_ns * dual + a.cost.single_ns * (tiles - dual) + a.cost.unit_ns * units;
   const float td = a.cost.tail_ns * tails, N = a.ctas, c = a.cost.prefix_ns - a.cost.decode_ns;
   const float s = tp + td - c * N, root = sqrtf(fmaxf(s * s + 4.f * c * tp * N, 0.f));
   const int n = static_cast<int>(__fdividef(2.f * tp * N, fmaxf(s + root, 1.f)) + 0.5f);
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
   int* s_base = s_first + a.NG;  // [NG] first slot
   int* s_w0 = s_base + a.NG;     // [NG] first CTA that meets the group
   int* s_lo = s_w0 + a.NG;       // [NG] first position that all taking part attend to
-  __shared__ int s_wsz, s_tiles, s_tails, s_dual;
+  __shared__ int s_wsz, s_tiles, s_tails, s_dual, s_nunits;
   const int tid = threadIdx.x, nthreads = blockDim.x;
   const int cap = a.MB * a.bs;
   const auto add = [](int x, int y) { return x + y; };
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
     if (report && x != L) atomicOr(a.err, PA_DEVERR_SEQ_LEN);
     return x;
   };
-  if (tid == 0) s_tails = s_dual = 0;
+  if (tid == 0) s_tails = s_dual = s_nunits = 0;
   int total;
   if (mine) {
     int run = 0;
@@ -195,6 +195,7 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
         u.up_mul = u.nut <= 1 ? 0u : 0xffffffffu / static_cast<uint32_t>(max(u.up, 1)) + 1u;
         s_units[g] = u;
         x = a.Hkv * u.nut * u.nt;
+        if (x > 0) atomicAdd(&s_nunits, a.Hkv * u.nut);
         if (a.halves && u.up * a.G > a.unit_rows / 2) atomicAdd(&s_dual, x);
       }
       const int y = scan<ONE>(x, 0, add, &total);
@@ -202,9 +203,8 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
       run += total;
     }
     if constexpr (ONE) __syncwarp(); else __syncthreads();
-    const int dual = s_dual;
     const int tiles = run;
-    const int ctas = share_sms(a, tiles, dual, s_tails * a.Hkv);
+    const int ctas = share_sms(a, tiles, s_dual, s_nunits, s_tails * a.Hkv);
     const int wsz = max((tiles + ctas - 1) / ctas, a.min_tiles);
     if (tid == 0) {
       s_tiles = tiles;

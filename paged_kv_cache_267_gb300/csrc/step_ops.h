@@ -83,10 +83,11 @@ cudaError_t norm_cache_launch(int type, bool fp8, const NormCacheArgs& a, int nu
 // shared positions (prefix_tc.cu).
 // Times that share the SMs between the prefix kernel and the decode kernel of a
 // step, in nanoseconds of one SM while both run: a K/V tile of the prefix for
-// two row tiles or one, a 16-token tile of a tail (one KV head), and what a CTA
-// of each kernel costs besides.
+// two row tiles or one, a unit's way in and out (its queries and partials), a
+// 16-token tile of a tail (one KV head), and what a CTA of each kernel costs
+// besides.
 struct SharedCost {
-  float dual_ns, single_ns, tail_ns, prefix_ns, decode_ns;
+  float dual_ns, single_ns, unit_ns, tail_ns, prefix_ns, decode_ns;
 };
 struct SharedPlanArgs {
   const int32_t* group_starts;   // [NG + 1]
