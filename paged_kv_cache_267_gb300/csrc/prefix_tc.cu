@@ -47,8 +47,8 @@
 // bf16, 256 queries of 4 heads a KV head on 65536 tokens: 1.71 us a tile of one
 // SM for 16.8 MFLOP, 1.49 PFLOP/s over the chip, 0.78 of the measured peak; bound
 // by the softmax's exponentials and the products in turn. Shares of one prefix
-// are short: of a 4096-token prompt a CTA has six tiles, and of its 14 us about
-// five are the queries' way in, the first tiles' latency and the partials' way
+// are short: of a 4096-token prompt a CTA has four tiles, and of its 14 us about
+// seven are the queries' way in, the first tiles' latency and the partials' way
 // out.
 #include "attn_tc.cuh"
 #include "pa_internal.h"
