@@ -246,10 +246,12 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
     if constexpr (SH) return s_first[b];
     else return win_start(s_len[b], a.span);
   };
-  // tile t of sequence b's nt, in position space
+  // Tile t of sequence b's nt, in position space. SH: a pair's first unit is not a
+  // tile (shared_plan.cuh), and its tiles have a gap.
   auto tile_of = [&](int b, int t, int nt) -> int {
     if constexpr (SH) {
-      if (t >= s_head[b]) return (s_len[b] + kTile - 1) / kTile - nt + t;
+      if (t > s_head[b]) return (s_len[b] + kTile - 1) / kTile - nt + t;
+      return start_of(b) / kTile + t - 1;
     }
     return start_of(b) / kTile + t;
   };
@@ -346,7 +348,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
       run_first = true;
       issue_claim();  // the next piece, one piece ahead
     }
-    const int f = np++;
+    int f = np++;
     unsigned flags = (phase == 1) ? kFlagPool : 0u;
     if (run_first) {
       flags |= kFlagStart;
@@ -354,6 +356,16 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
       run_first = false;
     } else {
       cursor_next(pc, s_pref, a.B, a.Hv);
+    }
+    if constexpr (SH) {
+      if (pc.t == 0) {  // the pair's way in and out
+        if (np >= run_end) {
+          phase = 2;
+          return false;
+        }
+        f = np++;
+        pc.t = 1;
+      }
     }
     if (np == run_end) {
       flags |= kFlagEnd;
@@ -396,7 +408,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
   if (f0 < f1) {
     Cursor c0;
     cursor_locate(c0, f0, s_pref, a.B, a.Hv);
-    const int pt0 = tile_of(c0.b, c0.t, c0.nt);
+    const int pt0 = tile_of(c0.b, SH ? max(c0.t, 1) : c0.t, c0.nt);
     refresh_window(c0.b, (pt0 * kTile) / a.bs);
   }
   // The caches may have been written by the previous kernel. SH: that is the
@@ -429,7 +441,8 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
     const int piece_id = mf >> 3;
     if (flags & kFlagStart) cursor_locate(cc, f, s_pref, a.B, a.Hv);
     else cursor_next(cc, s_pref, a.B, a.Hv);
-    const bool seg_start = (flags & kFlagStart) || (cc.t == 0);
+    if constexpr (SH) cc.t = max(cc.t, 1);
+    const bool seg_start = (flags & kFlagStart) || (cc.t == (SH ? 1 : 0));
     if (seg_start) {
       // Query fragments of this pair's columns (B operand, k = head dim).
       // Column c is q head kvh * G + c (T = 1), or, chunked, column

@@ -971,6 +971,7 @@ pa_status run_decode(const DecodeCall& c, DeviceState* st, const DecodePlan& pla
     p.decode_per_sm = plan.per_sm;
     p.decode_warps = plan.var.warps;
     p.decode_min_tiles = plan.min_tiles;
+    p.wide_partials = c.G * D >= 2048;
     p.cost = shared_cost(D, c.fp8);
     p.min_tiles = kPrefixMinTiles;
     e = pa::shared_plan_launch(p, cs, !prof);

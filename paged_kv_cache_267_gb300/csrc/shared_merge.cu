@@ -54,10 +54,10 @@ __global__ void __launch_bounds__(kThreads, 4) shared_merge_kernel(const SharedM
   const SharedRow row = shared_rows(a.plan, a.ctas, a.NG)[b];
   const int wsz = a.plan[kShWsz], tail_ws = a.plan[kShTailsWs];
 
-  // the decode kernel's partials: of the warps whose tiles meet the pair's
+  // the decode kernel's partials: of the warps whose units meet the pair's tiles
   int tail = 0, tail0 = 0;
   if (row.tiles > 0) {
-    const int f0 = a.Hkv * row.pref + kvh * row.tiles, w0 = f0 / tail_ws;
+    const int f0 = a.Hkv * row.pref + kvh * (row.tiles + 1) + 1, w0 = f0 / tail_ws;
     tail0 = pair + w0;
     tail = (f0 + row.tiles - 1) / tail_ws - w0 + 1;
   }

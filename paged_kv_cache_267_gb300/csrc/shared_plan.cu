@@ -176,6 +176,7 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
   if ((tid & 31) == 0) atomicAdd(&s_tails, tails);
   __syncthreads();
 
+  int early = 0;  // thread 0: CTAs of the decode kernel that find an SM free
   // units, flat tiles, slots
   const int up_max = a.unit_rows / a.G;
   if (mine) {
@@ -213,12 +214,8 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
       // the prefix kernel's CTAs with work; the others leave their SMs at once, to
       // the first CTAs of the decode kernel
       const int busy = (tiles + wsz - 1) / wsz;
-      const int early = busy > a.whole ? a.decode_ctas
-                                       : max(1, min(a.decode_ctas, (a.ctas - busy) * a.decode_per_sm));
-      const unsigned warps = static_cast<unsigned>(early) * a.decode_warps;
-      a.plan[kShTails] = s_tails;
-      a.plan[kShTailsWs] = max(static_cast<int>((static_cast<unsigned>(s_tails * a.Hkv) + warps - 1u) / warps),
-                               a.decode_min_tiles);
+      early = busy > a.whole ? a.decode_ctas
+                             : max(1, min(a.decode_ctas, (a.ctas - busy) * a.decode_per_sm));
     }
     run = 0;
     for (int g0 = 0; g0 < a.NG; g0 += step) {
@@ -276,7 +273,7 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
     ctas[w] = c;
   }
   SharedRow* rows = const_cast<SharedRow*>(shared_rows(a.plan, a.ctas, a.NG));
-  int before = 0;  // tiles of the rows of earlier rounds
+  int before = 0, some = 0;  // units of the rows of earlier rounds, rows with any
   for (int b0 = 0, j = 0; b0 < a.B; b0 += nthreads, ++j) {
     const int b = b0 + tid;
     const int g = b < a.B ? group_of(b) : -1;
@@ -300,9 +297,22 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
       r.nut = u.nut;
     }
     int all;
-    r.pref = before + scan<false>(r.tiles, 0, add, &all) - r.tiles;
+    const int units = r.tiles > 0 ? r.tiles + 1 : 0;
+    r.pref = before + scan<false>(units, 0, add, &all) - units;
     before += all;
+    some += __syncthreads_count(units > 0);
     if (b < a.B) rows[b] = r;
+  }
+  if (tid == 0) {
+    const unsigned warps = static_cast<unsigned>(early) * a.decode_warps;
+    a.plan[kShTails] = before;
+    // (A unit alone may be no tile. Pairs of two tiles whose partials are large, 8 KB
+    // and more, are better left whole than joined from two warps: 95 rows of 64/8
+    // heads of 256, 64.2 against 68.9 us. Smaller ones are not: 26 rows of 64/8 heads
+    // of 128 with tails of up to 95 tokens 42.1 whole, 39.8 cut.)
+    const int pair = a.wide_partials ? min((before + max(some, 1) - 1) / max(some, 1), 3) : 2;
+    a.plan[kShTailsWs] = max(static_cast<int>((static_cast<unsigned>(before * a.Hkv) + warps - 1u) / warps),
+                             max(a.decode_min_tiles, max(pair, 2)));
   }
   griddep_wait();  // what follows this kernel follows its predecessors too
 }

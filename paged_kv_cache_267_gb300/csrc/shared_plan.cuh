@@ -29,8 +29,12 @@
 namespace pa {
 
 constexpr int kSharedHead = 8;      // header words
-// tiles a CTA of the prefix kernel; 16-token tiles that the decode kernel covers,
-// of one KV head; and tiles a warp of it
+// tiles a CTA of the prefix kernel; units of the decode kernel of one KV head; and
+// units a warp of it. A (sequence, KV head) pair has a unit for each of the
+// 16-token tiles that the decode kernel covers, and one before them for its way
+// in and out (its queries, its partial: 0.8 us of a warp, where a tile takes 0.9;
+// warps with a dozen pairs of a tile or two each otherwise end 8 us after the
+// others' 24).
 enum { kShWsz = 0, kShTails = 1, kShTailsWs = 2 };
 
 struct SharedGroup {  // 12 words a group
@@ -57,8 +61,8 @@ struct SharedRow {  // 12 words a sequence
   int start;        // first position of its range
   int head;         // 16-token tiles of it before S
   int len;          // its length, inside the tables
-  int pref;         // tiles the decode kernel covers of the sequences before
-  int tiles;        // and of this one
+  int pref;         // units of the decode kernel of the sequences before
+  int tiles;        // 16-token tiles that it covers of this one
   int nt;           // K/V tiles of its prefix, 0: no part of it here
   int f0;           // first flat tile of its unit at KV head 0
   int kv_step;      // flat tiles between KV heads

@@ -102,6 +102,7 @@ struct SharedPlanArgs {
   int whole;                     // more busy CTAs than this: take all SMs
   int decode_ctas, decode_per_sm;  // of the decode kernel
   int decode_warps, decode_min_tiles;  // a CTA; least tiles a warp
+  bool wide_partials;            // a partial has 8 KB and more
   SharedCost cost;
   int min_tiles;                 // least K/V tiles a CTA
 };
