@@ -572,13 +572,14 @@ pa_status workspace_size(int64_t batch, int64_t num_queries, int32_t num_q_heads
   int64_t workers = static_cast<int64_t>(st->num_sms) * kMaxCtasPerSm * kWarpsPerCta;
   const int cap = g_tune_max_ctas.load();
   if (cap > 0 && cap * kWarpsPerCta < workers) workers = static_cast<int64_t>(cap) * kWarpsPerCta;
-  *bytes = ws_layout(batch, static_cast<int>(Hv), CG, head_dim, workers,
-                     num_groups > 0 ? most_shared_slots(batch, num_kv_heads,
-                                                        num_q_heads / num_kv_heads, head_dim,
-                                                        st->num_sms)
-                                    : 0,
-                     num_groups > 0 ? st->num_sms : 0)
-               .total;
+  *bytes = ws_layout(batch, static_cast<int>(Hv), CG, head_dim, workers).total;
+  if (num_groups > 0)  // for either path
+    *bytes = std::max(*bytes, ws_layout(batch, static_cast<int>(Hv), CG, head_dim, workers,
+                                        most_shared_slots(batch, num_kv_heads,
+                                                          num_q_heads / num_kv_heads, head_dim,
+                                                          st->num_sms),
+                                        st->num_sms)
+                                  .total);
   return ok();
 }
 

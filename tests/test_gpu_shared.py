@@ -420,6 +420,37 @@ def test_many_groups_of_many_rows(pa_lib):
     b.check(b.run(pa_lib))
 
 
+@pytest.mark.parametrize("B,heads,D", [(2, (8, 2), 128), (300, (2, 1), 64), (40, (16, 1), 256)])
+def test_the_stated_workspace_serves_both_paths(B, heads, D, pa_lib):
+    b = Batch([(320, [3 + i % 40 for i in range(B)])], dt="f16", heads=heads, D=D, seed=B)
+    n = pa_lib.decode_shared_workspace_size(b.B, 1, *heads, D)
+    ws = torch.empty(n + 256, dtype=torch.uint8, device="cuda")
+    ws[n:] = 77
+    try:
+        pa_lib.set_workspace(ws[:n])
+        for path in (1, 2, 0, 2, 1):
+            pa_lib.set_shared_path(path)
+            b.check(b.run(pa_lib), what=f"path {path}")
+        assert (ws[n:] == 77).all()
+    finally:
+        pa_lib.set_workspace(None)
+
+
+@pytest.mark.parametrize("tuning", [dict(max_ctas=1), dict(max_ctas=7, min_tiles=5), dict(min_tiles=1 << 20),
+                                    dict(pool_permille=900, piece_tiles=1)])
+def test_any_split_of_the_tails(tuning, pa_lib):
+    bs = [Batch([(640, [9, 1, 70, 300, 1, 16, 17])], loose_after=(0, 33), seed=41),
+          Batch([(1600, [40, 1, 60, 33]), (64, [1] * 30)], dt="f16", fp8=True, seed=42)]
+    try:
+        pa_lib.set_decode_tuning(**tuning)
+        for b in bs:
+            for window in (0, 700):
+                b.check(b.run(pa_lib, window), window, f"{tuning} window {window}")
+    finally:
+        pa_lib.set_decode_tuning()
+    assert pa_lib.check_device_error() == 0
+
+
 def test_other_streams_and_shapes_in_turn(pa_lib):
     """Calls of several shapes on two streams at once, each with its own
     library workspace, and plain decodes between them."""
