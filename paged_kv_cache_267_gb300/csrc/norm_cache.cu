@@ -25,10 +25,10 @@
 // 71.2 us into an e4m3 one. Half the elements a lane, 78.6 and 74 us; two heads a
 // thread, 78 us; eight or more (one batch after the other), 93-130 us; a CTA
 // that stays with its heads over many rows, 165 us (registers for it leave a
-// quarter of the threads). What is left is the loads in flight of 24 warps an SM
-// between their arithmetic: 15% more instructions (no paired fp32 operations) cost
-// 1% (72.3 us), a fourth CTA an SM spills (89 us), and persistent CTAs that copy
-// a unit or two ahead into shared memory take 75-78 us.
+// quarter of the threads). No one thing bounds what is left, with 24 warps an SM and
+// issue slots at 57%: 15% more instructions (no paired fp32 operations) cost 1%
+// (72.3 us), a fourth CTA an SM spills (89 us), and persistent CTAs that copy the
+// next unit, with its angles or without, into shared memory take 75-78 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
