@@ -67,6 +67,7 @@ constexpr int kConv = 6;  // FP8 converter warps
 constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;  // bound of every wait (2 s)
+constexpr uint64_t kDrainNs = 200000000ull;  // and of those after one ran out
 constexpr float kFloor = -1e30f;             // reference-max start
 constexpr float kRescaleAbove = 8.f;         // log2 units
 constexpr unsigned kFull = 0xffffffffu;
@@ -79,7 +80,7 @@ constexpr int kBarKFull = 0, kBarKEmpty = kBarKFull + kMaxStages, kBarVFull = kB
               kBarVEmpty = kBarVFull + kMaxStages, kBarS = kBarVEmpty + kMaxStages,
               kBarP = kBarS + 2, kBarO = kBarP + 2, kBarQ = kBarO + 2, kBarEnd = kBarQ + 1, kBarCKFull = kBarEnd + 1,
               kBarCKFree = kBarCKFull + 2, kBarCVFull = kBarCKFree + 2, kBarCVFree = kBarCVFull + 2,
-              kNumBars = kBarCVFree + 2;
+              kBarDrain = kBarCVFree + 2, kNumBars = kBarDrain + 1;
 
 // Stage and phase of a ring position.
 struct Ring {
@@ -215,6 +216,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     }
     mbar_init(bar(kBarQ), NX * kGroupThreads);
     mbar_init(bar(kBarEnd), NX * kGroupThreads);
+    mbar_init(bar(kBarDrain), 1);
     fence_mbar_init();
   }
   if (warp == 0) tc::tmem_alloc(base + C::kSlot, kTmemCols);
@@ -267,7 +269,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       const bool do_v = C::kLoadWarps == 1 || warp != C::kLoadWarp;
       bool ok = true;
       Ring kr, vr;
-      int c = 0;
+      int c = 0, nk = 0, nv = 0;  // tiles so far; K and V loads
       for (int f = f0; ok && f < f1; f += sg.nt) {
         segment_at(a, f, f1, &gi, &sg);
         int row = row_of(sg.t0);
@@ -278,16 +280,25 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             if (c >= C::kKStages && !(ok = wait_all(bar(kBarKEmpty + kr.stage), kr.phase ^ 1))) break;
             load(kr.stage, row, false);
             kr.next(C::kKStages);
+            ++nk;
           }
           if (do_v) {
             if (c >= C::kVStages && !(ok = wait_all(bar(kBarVEmpty + vr.stage), vr.phase ^ 1))) break;
             load(vr.stage, row, true);
             vr.next(C::kVStages);
+            ++nv;
           }
           row = next;
         }
       }
-      if (!ok && lane == 0) atomicOr(a.err, PA_DEVERR_TIMEOUT);
+      if (!ok) {
+        if (lane == 0) atomicOr(a.err, PA_DEVERR_TIMEOUT);
+        // no copy outlives the CTA
+        for (int i = max(nk - C::kKStages, 0); i < nk; ++i)
+          (void)mbar_wait_bounded(bar(kBarKFull + i % C::kKStages), (i / C::kKStages) & 1, kDrainNs);
+        for (int i = max(nv - C::kVStages, 0); i < nv; ++i)
+          (void)mbar_wait_bounded(bar(kBarVFull + i % C::kVStages), (i / C::kVStages) & 1, kDrainNs);
+      }
     } else if (warp == C::kMmaWarp) {
       // ------------------------------------------------------------ MMA issue
       // One thread does all of it, and little besides: its own instructions are
@@ -384,7 +395,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             for (int n = 0; ok && n < sg.nt; ++n) step(0, n == 0, n + 1 < sg.nt, true, true);
           }
         }
-        if (!ok) atomicOr(a.err, PA_DEVERR_TIMEOUT);
+        if (!ok) {
+          atomicOr(a.err, PA_DEVERR_TIMEOUT);
+          tc::commit(bar(kBarDrain));  // nor a product
+          (void)mbar_wait_bounded(bar(kBarDrain), 0, kDrainNs);
+        }
       }
       __syncwarp();
     } else {
@@ -736,7 +751,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     if (!ok && lane == 0) atomicOr(a.err, PA_DEVERR_TIMEOUT);
   }
 
-  // every MMA has completed (each group waited for its last product)
+  // every MMA has completed (each group waited for its last product, or the
+  // issuing thread did)
   tc::fence_before_sync();
   __syncthreads();
   if (warp == 0) {
