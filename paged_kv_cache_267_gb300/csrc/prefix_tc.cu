@@ -70,6 +70,10 @@ constexpr uint64_t kWaitNs = 2000000000ull;  // bound of every wait (2 s)
 constexpr uint64_t kDrainNs = 200000000ull;  // and of those after one ran out
 constexpr float kFloor = -1e30f;             // reference-max start
 constexpr float kRescaleAbove = 8.f;         // log2 units
+// f16 weights are 2^7 times as large against their reference: at most 2^15, and
+// subnormal below 2^-21 of it instead of 2^-14. (55,000 tokens of weight 2^-19.5
+// behind one of weight 1: 0.1% off without it, nothing with it.)
+constexpr float kF16Lift = 7.f;              // log2 units
 constexpr unsigned kFull = 0xffffffffu;
 
 // barriers: K and V rings (full, empty; up to kMaxStages each); per group x: S_x
@@ -186,6 +190,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                           const __grid_constant__ CUtensorMap tmV, const PrefixArgs a) {
   using C = Cfg<D, FP8>;
   constexpr bool kBf16 = !FP8 && QT == kBF16;  // operand type of the products
+  constexpr float kLift = kBf16 ? 0.f : kF16Lift;
   constexpr int NX = C::kGroups;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
@@ -603,10 +608,14 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         }
         // P = 2^(s * sc - ms), packed in pairs over the columns of the scores
         // just used; the last half is still in registers. It is rounded to the
-        // products' 16-bit type, which the tensor core needs beside V's: at most
-        // half a step of each weight (2^-8 bf16, 2^-11 f16), against sums in fp32 of
-        // the unrounded ones.
-        const float2 sc2 = make_float2(sc, sc), nms2 = make_float2(-ms, -ms);
+        // products' 16-bit type, which the tensor core needs beside V's, against sums
+        // in fp32 of the unrounded ones: at most 2^-8 of each weight (bf16), or 2^-11
+        // of it and, where it is subnormal, 2^-32 of the reference's weight, which
+        // the segment's largest is not below (f16, with its lift). The products are
+        // added in fp32 by the tensor core, 16 tokens at a time: weights below 2^-24
+        // of a sum that is already there are lost from it (55,000 tokens of weight
+        // 2^-25 behind one of weight 1: 0.1%).
+        const float2 sc2 = make_float2(sc, sc), nms2 = make_float2(kLift - ms, kLift - ms);
         float2 sp[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) sp[i] = make_float2(0.f, 0.f);
@@ -744,7 +753,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       }
       if (valid && !(join && x == 1)) {
         float* P = P0 + p_mine * stride + a.G * D + (ur_mine - p_mine * a.G);
-        st_f32_hint(P, ok ? ms : kFloor, keep);
+        st_f32_hint(P, ok ? ms - kLift : kFloor, keep);
         st_f32_hint(P + a.G, ok ? l : 0.f, keep);
       }
     }

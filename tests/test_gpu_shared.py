@@ -287,6 +287,33 @@ def test_halves_of_a_unit_whose_weights_vanish_for_some_rows(heavy, fp8, pa_lib)
     assert pa_lib.check_device_error() == 0
 
 
+@pytest.mark.parametrize("fp8,D", [(False, 64), (True, 128)])
+@pytest.mark.parametrize("log2,bound", [(25.05, 55296 * 2.0 ** -25.05 + 2.0 ** -12), (19.5, 2.0 ** -11)])
+def test_many_small_weights_behind_one_large_one(log2, bound, fp8, D, pa_lib):
+    """The first of 131072 shared keys outweighs each of the others by 2^log2; every
+    value is 1, and so is the output. A segment has at most 64 * 1024 tiles / 152
+    = 432, 55296 tokens. The second product adds 16 weights at a time to an fp32
+    sum, which starts with the large one (2^7 with the lift): it drops what is
+    below 2^-16, its last place there.
+    2^-25.05 each: 16 of them are 2^-14.05, and each alone below the last place, so
+    all may go: 55296 2^-25.05, and half a step of f16, 2^-12.
+    2^-19.5: 16 are 2^-8.5, off by 2^-7.5 of themselves at most, as is their part
+    of the whole, 55296 2^-19.5 = 0.0744: 2^-11.2; their f16 rounding adds 2^-11 of
+    that part, the output's 2^-12: below 0.0008, so at most one step from 1."""
+    P, Hkv, B, bs = 131072, 64, 2, 16
+    k, v = torch.zeros(3, Hkv, bs, D, device="cuda"), torch.ones(3, Hkv, bs, D, device="cuda")
+    k[0, :, 0] = 1.0
+    k, v = (x.to(torch.float8_e4m3fn).view(torch.uint8) if fp8 else x.to(torch.float16) for x in (k, v))
+    tables = torch.ones(B, P // bs + 1, dtype=torch.int32, device="cuda")
+    tables[:, 0], tables[:, -1] = 0, 2
+    i = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    out = pa_lib.decode_shared(torch.ones(B, Hkv, D, dtype=torch.float16, device="cuda"), k, v, tables, i(P + 3, P + 5),
+                               i(P), i(0, B), num_kv_heads=Hkv, scale=log2 * np.log(2.0) / D, block_size=bs,
+                               kv_dtype="fp8" if fp8 else "auto")
+    assert pa_lib.check_device_error() == 0
+    assert (out.double() - 1).abs().max() <= bound, (out.min(), out.max())
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("where", ["k", "v"])
 @pytest.mark.parametrize("tile", [0, 1, 9])
