@@ -18,7 +18,8 @@
 // and a thread takes kHeads heads of the same row and kind, for which it folds
 // weights and angles into four coefficients a pair once,
 //   lo' = r (lo A - hi B),  hi' = r (hi C + lo E),
-// A = w_lo c, B = w_hi s, C = w_hi c, E = w_lo s (behind R: c = 1, s = 0). The
+// A = w_lo c, B = w_hi s, C = w_hi c, E = w_lo s (behind R: c = 1, s = 0, and the
+// other element does not enter, which may be infinite). The
 // loads of all its heads are in flight together; neighbouring groups of lanes
 // take neighbouring heads, so that a CTA reads and writes one piece of the rows.
 // 16384 rows of 32 + 2 x 8 heads of 128: 68.7 us (5.93 TB/s) into a 16-bit cache,
@@ -138,8 +139,9 @@ __device__ __forceinline__ void order_of(const float2 (&lo)[4], const float2 (&h
   }
 }
 
-// LANES lanes a head (D <= 16 * LANES), kHeads heads of one kind a thread.
-template <int ST, bool FP8, bool INTER, int LANES, int kHeads>
+// LANES lanes a head (D <= 16 * LANES), kHeads heads of one kind a thread; PART:
+// some lanes are behind R.
+template <int ST, bool FP8, bool INTER, bool PART, int LANES, int kHeads>
 __global__ void __launch_bounds__(kThreads, kHeads > 1 ? 3 : 4) norm_cache_kernel(const NormCacheArgs a) {
   constexpr int kGroups = kThreads / LANES;
   // rows may come from the previous kernel, and the caches may still be read
@@ -229,13 +231,13 @@ __global__ void __launch_bounds__(kThreads, kHeads > 1 ? 3 : 4) norm_cache_kerne
     return;
   }
 
-  // coefficients of this lane's pairs
+  // coefficients of this lane's pairs (behind R, x + -0 is x whatever its sign)
   const void* weight = kind == 0 ? a.q_weight : a.k_weight;
   float2 A[4], B[4], C[4], E[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     A[q] = C[q] = make_float2(1.f, 1.f);  // the weights first
-    B[q] = E[q] = make_float2(0.f, 0.f);
+    B[q] = E[q] = make_float2(-0.f, -0.f);
   }
   if (weight && on) pairs_of<ST, INTER>(load_raw(static_cast<const uint16_t*>(weight), ea, eb), A, C);
   if (rotated) {
@@ -301,8 +303,10 @@ __global__ void __launch_bounds__(kThreads, kHeads > 1 ? 3 : 4) norm_cache_kerne
       const float2 r2 = make_float2(rn[j], rn[j]);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        yl[q] = __fmul2_rn(__ffma2_rn(hi[q], B[q], __fmul2_rn(lo[q], A[q])), r2);
-        yh[q] = __fmul2_rn(__ffma2_rn(lo[q], E[q], __fmul2_rn(hi[q], C[q])), r2);
+        const bool cross = !PART || rotated;
+        const float2 h = cross ? hi[q] : make_float2(0.f, 0.f), l = cross ? lo[q] : make_float2(0.f, 0.f);
+        yl[q] = __fmul2_rn(__ffma2_rn(h, B[q], __fmul2_rn(lo[q], A[q])), r2);
+        yh[q] = __fmul2_rn(__ffma2_rn(l, E[q], __fmul2_rn(hi[q], C[q])), r2);
       }
       order_of<INTER>(yl, yh, e);
       if (stored && j < nh) {
@@ -335,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, kHeads > 1 ? 3 : 4) norm_cache_kerne
   finish(std::false_type{});
 }
 
-template <int ST, bool FP8, bool INTER, int LANES, int kHeads>
+template <int ST, bool FP8, bool INTER, bool PART, int LANES, int kHeads>
 cudaError_t launch(NormCacheArgs a, cudaStream_t s) {
   constexpr int kGroups = kThreads / LANES;
   const long long per_row = (a.Hq + kHeads - 1) / kHeads + 2ll * ((a.Hkv + kHeads - 1) / kHeads);
@@ -361,33 +365,39 @@ cudaError_t launch(NormCacheArgs a, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, norm_cache_kernel<ST, FP8, INTER, LANES, kHeads>, b);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, norm_cache_kernel<ST, FP8, INTER, PART, LANES, kHeads>, b);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
 
-template <int ST, bool FP8, bool INTER, int LANES>
+template <int ST, bool FP8, bool INTER, bool PART, int LANES>
 cudaError_t launch_heads(const NormCacheArgs& a, int num_sms, cudaStream_t s) {
   // several heads a thread once that still fills every SM twice over
   const long long groups = static_cast<long long>(a.T) * (a.Hq + 2 * a.Hkv);
   const long long ctas = groups / kManyHeads / (kThreads / LANES);
-  return ctas >= 2ll * num_sms ? launch<ST, FP8, INTER, LANES, kManyHeads>(a, s)
-                               : launch<ST, FP8, INTER, LANES, 1>(a, s);
+  return ctas >= 2ll * num_sms ? launch<ST, FP8, INTER, PART, LANES, kManyHeads>(a, s)
+                               : launch<ST, FP8, INTER, PART, LANES, 1>(a, s);
+}
+
+template <int ST, bool FP8, bool INTER, bool PART>
+cudaError_t launch_lanes(const NormCacheArgs& a, int num_sms, cudaStream_t s) {
+  if (a.D <= 64) return launch_heads<ST, FP8, INTER, PART, 4>(a, num_sms, s);
+  if (a.D <= 128) return launch_heads<ST, FP8, INTER, PART, 8>(a, num_sms, s);
+  return launch_heads<ST, FP8, INTER, PART, 16>(a, num_sms, s);
 }
 
 template <int ST, bool FP8, bool INTER>
-cudaError_t launch_lanes(const NormCacheArgs& a, int num_sms, cudaStream_t s) {
-  if (a.D <= 64) return launch_heads<ST, FP8, INTER, 4>(a, num_sms, s);
-  if (a.D <= 128) return launch_heads<ST, FP8, INTER, 8>(a, num_sms, s);
-  return launch_heads<ST, FP8, INTER, 16>(a, num_sms, s);
+cudaError_t launch_part(const NormCacheArgs& a, int num_sms, cudaStream_t s) {
+  return a.R < a.D ? launch_lanes<ST, FP8, INTER, true>(a, num_sms, s)
+                   : launch_lanes<ST, FP8, INTER, false>(a, num_sms, s);
 }
 
 template <int ST>
 cudaError_t launch_type(bool fp8, const NormCacheArgs& a, int num_sms, cudaStream_t s) {
   if (a.interleaved)
-    return fp8 ? launch_lanes<ST, true, true>(a, num_sms, s) : launch_lanes<ST, false, true>(a, num_sms, s);
-  return fp8 ? launch_lanes<ST, true, false>(a, num_sms, s) : launch_lanes<ST, false, false>(a, num_sms, s);
+    return fp8 ? launch_part<ST, true, true>(a, num_sms, s) : launch_part<ST, false, true>(a, num_sms, s);
+  return fp8 ? launch_part<ST, true, false>(a, num_sms, s) : launch_part<ST, false, false>(a, num_sms, s);
 }
 
 }  // namespace

@@ -211,6 +211,38 @@ def test_one_weight_only_and_zero_rows(pa_lib):
     assert got.shape == (0, 4, 64)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("R", [0, 32])
+@pytest.mark.parametrize("T", [9, 2100])
+def test_an_infinity_behind_the_rotation_stays_its_own(T, R, inter, norm, fp8, pa_lib):
+    """One infinite element a head, where nothing is rotated: without a weight the
+    others pass as they are (as the plain write path stores them), with one they
+    are zeros, x / sqrt(inf)."""
+    H, D = 4, 96
+    packed, q, k, v, kc, vc, slots, pos, cs, (wq, wk) = make(T, 8, H, D, "f16", fp8, skipped=0, R=R, seed=R + T)
+    at = torch.randint(R, D, (T, 8 + H), generator=torch.Generator(device="cuda").manual_seed(T), device="cuda")
+    for h, x in enumerate([*q.unbind(1), *k.unbind(1)]):
+        x.scatter_(1, at[:, h:h + 1], float("inf") if h % 2 else float("-inf"))
+    hit = torch.zeros(T, 8 + H, D, dtype=torch.bool, device="cuda").scatter_(2, at[:, :, None], True)
+    kw = dict(kv_dtype="fp8", k_scale=0.25) if fp8 else {}
+    kp, vp = kc.clone(), vc.clone()
+    out = pa_lib.norm_rope_and_cache(q, k, v, kc, vc, slots, pos, cs, interleaved=inter,
+                                     **(dict(q_weight=wq, k_weight=wk) if norm else {}), **kw)
+    stored = lambda c: c.transpose(1, 2).reshape(-1, H, D)[slots]  # noqa: E731
+    keys = stored(kc)
+    if fp8:
+        keys = keys.view(torch.float8_e4m3fn).float()
+    if norm:
+        assert (out[~hit[:, :8]] == 0).all() and (keys[~hit[:, 8:]] == 0).all()
+        return
+    pa_lib.reshape_and_cache(k.contiguous(), v.contiguous(), kp, vp, slots, kw.get("kv_dtype", "auto"),
+                             kw.get("k_scale", 1.0), 1.0)
+    assert torch.equal(out[..., R:], q[..., R:]) and torch.equal(stored(kc)[..., R:], stored(kp)[..., R:])
+    assert torch.isfinite(out[..., :R]).all() and torch.isfinite(keys[..., :R].float()).all()
+
+
 @pytest.mark.parametrize("dt,spread", [("bf16", 1e18), ("bf16", 1e-18), ("f16", 1e4), ("f16", 1e-6)])
 def test_large_and_small_rows(dt, spread, pa_lib):
     """Sums of squares that leave 16 bits (1e36 D is inside fp32's range)."""
