@@ -23,7 +23,7 @@
 // loads of all its heads are in flight together; neighbouring groups of lanes
 // take neighbouring heads, so that a CTA reads and writes one piece of the rows.
 // 16384 rows of 32 + 2 x 8 heads of 128: 68.7 us (5.93 TB/s) into a 16-bit cache,
-// 71.2 us into an e4m3 one. Half the elements a lane, 78.6 and 74 us; two heads a
+// 71.4 us into an e4m3 one. Half the elements a lane, 78.6 and 74 us; two heads a
 // thread, 78 us; eight or more (one batch after the other), 93-130 us; a CTA
 // that stays with its heads over many rows, 165 us (registers for it leave a
 // quarter of the threads). No one thing bounds what is left, with 24 warps an SM and
@@ -92,18 +92,53 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) 
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
-// x / scale, correctly rounded, from the correctly rounded reciprocal: the product
-// is within an ulp of the quotient, its remainder x - q scale is exact in one fma,
-// and a second one rounds q + remainder / scale correctly (Markstein, "Computation
-// of elementary functions on the IBM RISC System/6000 processor", 1990). Where
-// the product overflows, or x is not finite, it is the result. Holds for scales
-// in [2^-60, 2^60]: what underflows is then far below the least code. Six
-// instructions; the compiler's quotient made the e4m3 write of v cost as much as
-// the norm and rotation of q.
-__device__ __forceinline__ float quotient(float x, float scale, float inv) {
-  const float q = x * inv;
-  const float y = fmaf(fmaf(-q, scale, x), inv, q);
-  return fabsf(q) < INFINITY ? copysignf(y, q) : q;  // (a remainder of zero is +0)
+// e4m3 codes of x / scale, the quotient as the plain write path takes it. From the
+// correctly rounded reciprocal: the product q is within 1.5 ulp of the quotient, one
+// fma gives its remainder (exact, or rounded in its 25th bit), and a second one
+// rounds q - remainder / scale (after Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor", 1990). What is rounded is off
+// by less than 2^-22 ulp, so the result is the correctly rounded quotient unless
+// that lies as near to the middle of two floats. The remainder is taken as q scale
+// - x, and x is given negated: an exact one, +0, then leaves a zero q its sign. Holds for
+// scales in [2^-60, 2^60] (what underflows is then far below the least code) and
+// finite q; other scales are brought there with x by a power of two, which loses
+// nothing that has a code other than zero or the largest, and x is cut to 512
+// scale where any of a lane's is beyond. (The compiler's quotient made the e4m3
+// write of v cost as much as the norm and rotation of q.)
+struct CodeScale {
+  float scale, ninv, shift;
+  __device__ __forceinline__ explicit CodeScale(float s) {
+    shift = s < 0x1p-60f ? 0x1p100f : (s > 0x1p60f ? 0x1p-100f : 1.f);
+    scale = s * shift;
+    ninv = -1.f / scale;
+  }
+};
+__device__ __forceinline__ float clamp_nan(float x, float lim) {  // a NaN stays one
+  float y;
+  asm("{\n.reg .f32 t;\nmin.NaN.f32 t, %1, %2;\nmax.NaN.f32 %0, t, %3;\n}" : "=f"(y) : "f"(x), "f"(lim), "f"(-lim));
+  return y;
+}
+// Eight codes, in order, of the negated values nx.
+__device__ __forceinline__ uint2 encode8(float2 (&nx)[4], const CodeScale& s) {
+  const float2 shift = make_float2(s.shift, s.shift);
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    nx[i] = __fmul2_rn(nx[i], shift);
+    top = fmaxf(fmaxf(fabsf(nx[i].x), fabsf(nx[i].y)), top);
+  }
+  if (top > 512.f * s.scale) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      nx[i] = make_float2(clamp_nan(nx[i].x, 512.f * s.scale), clamp_nan(nx[i].y, 512.f * s.scale));
+  }
+  const float2 sc = make_float2(s.scale, s.scale), ninv = make_float2(s.ninv, s.ninv);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 q = __fmul2_rn(nx[i], ninv);
+    nx[i] = __ffma2_rn(__ffma2_rn(q, sc, nx[i]), ninv, q);
+  }
+  return make_uint2(encode4(nx[0].x, nx[0].y, nx[1].x, nx[1].y), encode4(nx[2].x, nx[2].y, nx[3].x, nx[3].y));
 }
 
 // Pairs of a lane's elements, as float2 of two pairs: pair i is (lo_i, hi_i).
@@ -195,44 +230,27 @@ __global__ void __launch_bounds__(kThreads, kHeads > 1 ? 3 : 4) norm_cache_kerne
     dst = static_cast<char*>(kind == 1 ? a.kc : a.vc) +
           ((static_cast<size_t>(blk) * a.Hkv + h0) * a.bs + (slot - blk * a.bs)) * (a.D * elt);
   }
-  // e4m3 codes of a lane's values
-  auto store_codes = [&](char* at, const float2 (&e)[8]) {
-    *reinterpret_cast<uint2*>(at + ea) = make_uint2(encode4(e[0].x, e[0].y, e[1].x, e[1].y),
-                                                    encode4(e[2].x, e[2].y, e[3].x, e[3].y));
-    *reinterpret_cast<uint2*>(at + eb) = make_uint2(encode4(e[4].x, e[4].y, e[5].x, e[5].y),
-                                                    encode4(e[6].x, e[6].y, e[7].x, e[7].y));
+  auto store_codes = [&](char* at, const float2 (&nx)[8], const CodeScale& scale) {
+    float2 lo[4] = {nx[0], nx[1], nx[2], nx[3]}, hi[4] = {nx[4], nx[5], nx[6], nx[7]};
+    *reinterpret_cast<uint2*>(at + ea) = encode8(lo, scale);
+    *reinterpret_cast<uint2*>(at + eb) = encode8(hi, scale);
   };
 
-  if (kind == 2) {
+  if (!FP8 && kind == 2) {  // a bit copy
     if (!stored) return;
 #pragma unroll
     for (int j = 0; j < kHeads; ++j) {
       if (j >= nh) break;
-      if constexpr (FP8) {
-        // the IEEE quotient, as the plain write path stores it
-        float2 e[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = unpack2<ST>(word(i < 4 ? x[j].a : x[j].b, i & 3));
-        if (a.v_scale >= 0x1p-60f && a.v_scale <= 0x1p60f) {
-          const float inv = 1.f / a.v_scale;
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            e[i] = make_float2(quotient(e[i].x, a.v_scale, inv), quotient(e[i].y, a.v_scale, inv));
-        } else {
-#pragma unroll 1
-          for (int i = 0; i < 8; ++i) e[i] = make_float2(e[i].x / a.v_scale, e[i].y / a.v_scale);
-        }
-        store_codes(dst, e);
-      } else {
-        store_raw(reinterpret_cast<uint16_t*>(dst), ea, eb, x[j]);
-      }
+      store_raw(reinterpret_cast<uint16_t*>(dst), ea, eb, x[j]);
       dst += step;
     }
     return;
   }
 
-  // coefficients of this lane's pairs (behind R, x + -0 is x whatever its sign)
-  const void* weight = kind == 0 ? a.q_weight : a.k_weight;
+  // coefficients of this lane's pairs (behind R, x + -0 is x whatever its sign); v on
+  // its way to codes has none
+  const void* weight = kind == 0 ? a.q_weight : (kind == 1 ? a.k_weight : nullptr);
+  const bool turned = rotated && kind != 2;
   float2 A[4], B[4], C[4], E[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -240,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, kHeads > 1 ? 3 : 4) norm_cache_kerne
     B[q] = E[q] = make_float2(-0.f, -0.f);
   }
   if (weight && on) pairs_of<ST, INTER>(load_raw(static_cast<const uint16_t*>(weight), ea, eb), A, C);
-  if (rotated) {
+  if (turned) {
     int pos = a.positions[t];
     if (pos < 0 || pos >= a.NP) {
       if (lane == 0) atomicOr(a.err, PA_DEVERR_POSITION);
@@ -265,12 +283,6 @@ __global__ void __launch_bounds__(kThreads, kHeads > 1 ? 3 : 4) norm_cache_kerne
   }
   // the heads' norms, interleaved: a head behind nh is zeros and goes nowhere
   const float inv_d = 1.f / static_cast<float>(a.D);
-  // (a scale whose reciprocal, times a norm, could leave fp32's range: the values
-  // go through a power of two instead, which brings the scale nearer to 1 and
-  // loses nothing that has a code other than zero or the largest)
-  const bool scaled = kind == 1 && FP8, wild = scaled && !(a.k_scale >= 0x1p-60f && a.k_scale <= 0x1p60f);
-  const float inv_scale = scaled && !wild ? 1.f / a.k_scale : 1.f;
-  const float near = a.k_scale < 1.f ? 0x1p100f : 0x1p-100f;
   float rn[kHeads];
   if (weight) {
     const unsigned members =
@@ -290,34 +302,33 @@ __global__ void __launch_bounds__(kThreads, kHeads > 1 ? 3 : 4) norm_cache_kerne
 #pragma unroll
       for (int j = 0; j < kHeads; ++j) rn[j] += __shfl_xor_sync(members, rn[j], o);
 #pragma unroll
-    for (int j = 0; j < kHeads; ++j) rn[j] = rsqrtf(fmaf(rn[j], inv_d, a.eps)) * inv_scale;
+    for (int j = 0; j < kHeads; ++j) rn[j] = rsqrtf(fmaf(rn[j], inv_d, a.eps));
   } else {
 #pragma unroll
-    for (int j = 0; j < kHeads; ++j) rn[j] = inv_scale;
+    for (int j = 0; j < kHeads; ++j) rn[j] = 1.f;
   }
-  auto finish = [&](auto is_wild) {  // (apart: in one loop the branch costs 4 us of 71)
+  // The codes apart from q's 16 bits (in one loop with a branch 74 us, not 71), but
+  // those of k and v together: heads of both are in one warp, and v with codes of
+  // its own beside k's took 75.
+  auto finish = [&](auto is_code) {
+    const CodeScale scale(!is_code.value ? 1.f : (kind == 1 ? a.k_scale : a.v_scale));
 #pragma unroll
     for (int j = 0; j < kHeads; ++j) {
       float2 lo[4], hi[4], yl[4], yh[4], e[8];
       pairs_of<ST, INTER>(x[j], lo, hi);
-      const float2 r2 = make_float2(rn[j], rn[j]);
+      // (codes are made of the negated values)
+      const float2 r2 = is_code.value ? make_float2(-rn[j], -rn[j]) : make_float2(rn[j], rn[j]);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const bool cross = !PART || rotated;
+        const bool cross = (!PART && !is_code.value) || turned;
         const float2 h = cross ? hi[q] : make_float2(0.f, 0.f), l = cross ? lo[q] : make_float2(0.f, 0.f);
         yl[q] = __fmul2_rn(__ffma2_rn(h, B[q], __fmul2_rn(lo[q], A[q])), r2);
         yh[q] = __fmul2_rn(__ffma2_rn(l, E[q], __fmul2_rn(hi[q], C[q])), r2);
       }
       order_of<INTER>(yl, yh, e);
       if (stored && j < nh) {
-        if (scaled) {
-          if constexpr (is_wild.value) {
-            const float inv = 1.f / (a.k_scale * near);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              e[i] = __fmul2_rn(__fmul2_rn(e[i], make_float2(near, near)), make_float2(inv, inv));
-          }
-          store_codes(dst, e);
+        if constexpr (is_code.value) {
+          store_codes(dst, e, scale);
         } else {
           Raw y;
           y.a = make_uint4(pack2<ST>(e[0].x, e[0].y), pack2<ST>(e[1].x, e[1].y), pack2<ST>(e[2].x, e[2].y),
@@ -331,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, kHeads > 1 ? 3 : 4) norm_cache_kerne
     }
   };
   if constexpr (FP8) {
-    if (wild) {
+    if (kind > 0) {
       finish(std::true_type{});
       return;
     }

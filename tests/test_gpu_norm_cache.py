@@ -156,6 +156,30 @@ def test_v_codes_equal_the_plain_write_paths_for_every_pattern(src, scale, pa_li
         assert ((x[nan] & 0x7F) == 0x7F).all()
 
 
+@pytest.mark.parametrize("src", ["bf16", "f16"])
+@pytest.mark.parametrize("scale", [1.0, 0.0123, 3.7, 7.0, 1e-3, 300.0, 0.7499999, 2.0 ** -60, 1.1e-19, 1e-30, 1e30, 3e38])
+def test_key_codes_equal_the_plain_write_paths_for_every_pattern(src, scale, pa_lib):
+    """All 65,536 16-bit keys, without a weight or a rotation: nothing comes between
+    the key and its code, so ties of the quotient fall alike."""
+    bits = torch.from_numpy(np.arange(65536, dtype=np.uint32).astype(np.uint16).view(np.int16).copy())
+    for H, D in ((2, 128), (4, 64)):
+        for many in (1, 20):            # 20: four heads a thread
+            T = 65536 // (H * D)
+            k = bits.view(DT[src]).reshape(T, H, D).cuda().repeat(many, 1, 1)
+            T *= many
+            v = torch.zeros_like(k)
+            NB = -(-T // 16)
+            a = [torch.zeros(NB, H, 16, D, dtype=torch.uint8, device="cuda") for _ in range(4)]
+            slots = torch.arange(T, device="cuda")
+            pos = torch.zeros(T, dtype=torch.int32, device="cuda")
+            pa_lib.norm_rope_and_cache(v, k, v, a[0], a[1], slots, pos, angles(1, 0), kv_dtype="fp8", k_scale=scale)
+            pa_lib.reshape_and_cache(k, v, a[2], a[3], slots, "fp8", scale, 1.0)
+            nan = torch.isnan(k.float()).cpu()
+            x, y = (c.transpose(1, 2).reshape(NB * 16, H, D)[:T].cpu() for c in (a[0], a[2]))
+            assert torch.equal(x[~nan], y[~nan])
+            assert ((x[nan] & 0x7F) == 0x7F).all()
+
+
 @pytest.mark.parametrize("norm", [True, False])
 @pytest.mark.parametrize("T", [5, 2100])
 @pytest.mark.parametrize("scale", [1e-40, 1e-25, 0.02, 1e25, 3e38])
