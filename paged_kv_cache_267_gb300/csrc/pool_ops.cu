@@ -401,15 +401,18 @@ __global__ void __launch_bounds__(kThreads) pool_release_kernel(const PoolReleas
 }
 
 // CTAs for `items` outputs of `per` each: one where they fit one CTA (no
-// ticket, no repeated scan), at most one an SM (every CTA scans the batch).
-int grid_for(long long items, long long per, int num_sms) {
+// ticket, no repeated scan), at most `most`, which is as many as the SMs hold at
+// once or fewer (every CTA scans the batch).
+int grid_for(long long items, long long per, int most) {
   const long long g = (items + per - 1) / per;
-  return static_cast<int>(g < 1 ? 1 : (g > num_sms ? num_sms : g));
+  return static_cast<int>(g < 1 ? 1 : (g > most ? most : g));
 }
 
 template <typename Args>
 cudaError_t launch(void (*fn)(const Args), const Args& a, int grid, size_t smem, cudaStream_t s) {
-  if (smem > 48 * 1024) {  // large batches: the per-sequence prefixes (one value, whichever thread sets it)
+  // Large batches: the per-sequence prefixes. Without asking, a CTA has 48 KB, its
+  // static arrays (0.2 KB) among them. (One value, whichever thread sets it.)
+  if (smem > 40 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
     if (e != cudaSuccess) return e;

@@ -3,11 +3,14 @@ model of it, entry for entry: lengths from zero up, odd requests, sequences
 that want nothing, padded rows, one CTA and many, in place and not, refused
 steps, captured steps, and the host allocator's tables for the same requests.
 """
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
 
-from conftest import have_gpu
+from conftest import ROOT, have_gpu
 from workloads.layout import shuffled_free_list
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not have_gpu(), reason="needs a GPU")]
@@ -309,3 +312,33 @@ def test_captured_steps_replay_in_place(pa_lib):
         g.same_step(m.extend([1] * B, B + 3))
         g.same_state(m)
     assert pa_lib.check_device_error() == 0
+
+
+FRESH = """
+import sys
+sys.path[:0] = [{root!r}, {root!r} + "/tests"]
+import numpy as np
+import paged_kv_cache_267_gb300 as pa
+from test_gpu_pool import Gpu, Pool, i32
+for B in {sizes}:
+    m = Pool(B, 2, 16, 2 * B, seed=B)
+    g = Gpu(pa, m)
+    new = np.arange(B) % 19
+    g.step(int(new.sum()) + 3)
+    g.extend(i32(new))
+    g.same_step(m.extend(new, int(new.sum()) + 3))
+    g.same_state(m)
+    gone = np.arange(B) % 3 == 0
+    g.release(i32(gone))
+    m.release(gone)
+    g.same_state(m)
+assert pa.check_device_error() == 0
+"""
+
+
+@pytest.mark.parametrize("sizes", [[3400], [4077, 4078], [4079, 4095], [4096, 3413, 4079]])
+def test_batches_whose_prefixes_just_fit_the_shared_memory(sizes, pa_lib):
+    """In a process of their own: a larger batch before them would raise the limit."""
+    r = subprocess.run([sys.executable, "-c", FRESH.format(root=ROOT, sizes=sizes)], capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
