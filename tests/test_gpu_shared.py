@@ -16,12 +16,15 @@ element (the oracle's decode over |V|):
     most 256 * 2^-24 * 64 * 1.45 < 2^-9; the exponential adds 2^-21.
 Bound: h |ref| + (p + 2^-11 + 2^-9) A + 1e-6.
 """
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
 
 import oracle
-from conftest import have_gpu
+from conftest import ROOT, have_gpu
 from pa_testutil import host_copy, out_f64
 from workloads.layout import shuffled_free_list
 
@@ -722,3 +725,24 @@ def test_a_whole_step_from_lengths_to_attention(pa_lib):
             row += 1
         assert start.tolist() == [0, 1, 2, 3, 4, 4, 5]
     assert pa_lib.check_device_error() == 0
+
+
+FRESH = """
+import sys
+sys.path[:0] = [{root!r}, {root!r} + "/tests"]
+import paged_kv_cache_267_gb300 as pa
+from test_gpu_shared import Batch
+pa.set_shared_path(2)
+for n in {sizes}:
+    b = Batch([(16, [1])] * (n - 1) + [(32, [2, 5, 1])], dt="f16", heads=(1, 1), D=64, seed=n)
+    b.check(b.run(pa), what=str(n))
+assert pa.check_device_error() == 0
+"""
+
+
+@pytest.mark.parametrize("sizes", [[853, 930, 931], [1023, 1024, 1025], [1109, 1110, 1111], [1117, 1118], [4000, 1111]])
+def test_group_counts_whose_plan_just_fits_the_shared_memory(sizes, pa_lib):
+    """In a process of their own: more groups before them would raise the limit."""
+    r = subprocess.run([sys.executable, "-c", FRESH.format(root=ROOT, sizes=sizes)], capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
