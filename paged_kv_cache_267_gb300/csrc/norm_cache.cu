@@ -264,11 +264,9 @@ __global__ void __launch_bounds__(kThreads, kHeads > 1 ? 3 : 4) norm_cache_kerne
       if (lane == 0) atomicOr(a.err, PA_DEVERR_POSITION);
       pos = pos < 0 ? 0 : a.NP - 1;
     }
-    const float* angle = a.cos_sin + static_cast<size_t>(pos) * a.R + 8 * lane;
-    const float4 c0 = __ldg(reinterpret_cast<const float4*>(angle));
-    const float4 c1 = __ldg(reinterpret_cast<const float4*>(angle) + 1);
-    const float4 s0 = __ldg(reinterpret_cast<const float4*>(angle + (a.R >> 1)));
-    const float4 s1 = __ldg(reinterpret_cast<const float4*>(angle + (a.R >> 1)) + 1);
+    // (no read-only loads: this kernel may have started before they were written)
+    const float4* angle = reinterpret_cast<const float4*>(a.cos_sin + static_cast<size_t>(pos) * a.R + 8 * lane);
+    const float4 c0 = angle[0], c1 = angle[1], s0 = angle[a.R >> 3], s1 = angle[(a.R >> 3) + 1];
     const float2 c2[4] = {make_float2(c0.x, c0.y), make_float2(c0.z, c0.w), make_float2(c1.x, c1.y),
                           make_float2(c1.z, c1.w)};
     const float2 s2[4] = {make_float2(s0.x, s0.y), make_float2(s0.z, s0.w), make_float2(s1.x, s1.y),

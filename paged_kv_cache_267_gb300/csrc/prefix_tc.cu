@@ -510,7 +510,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             const int p = static_cast<int>((ur * pair_mul) >> 16), h = ur - p * a.G;
             const size_t row = static_cast<size_t>(sg.b0 + min(p, sg.np - 1)) * a.Hq +
                                static_cast<size_t>(sg.kvh) * a.G + h;
-            v[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + row * D) + ch);
+            // (no read-only load: this kernel may have started before q was written)
+            v[i] = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + row * D)[ch];
           }
 #pragma unroll
           for (int i = 0; i < kBatch; ++i) {

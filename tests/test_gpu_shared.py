@@ -631,6 +631,61 @@ def test_captured_step_follows_new_lengths_and_groups(pa_lib):
     assert pa_lib.check_device_error() == 0
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_queries_written_by_the_call_just_before(fp8, pa_lib):
+    """norm_rope_and_cache lets the shared step start before it has written q and the
+    caches: steps in a row, in place in one buffer, without anything between them and
+    in a graph, give what they give one by one."""
+    b = Batch([(640, [9] * 40), (1600, [7, 8, 9])], dt="f16", fp8=fp8, seed=51)
+    Hq, Hkv = b.heads
+    D, n, steps = b.D, b.B, 8
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rows = torch.randn(steps, n, Hq + 2 * Hkv, D, generator=g, device="cuda").to(torch.float16)
+    last = torch.from_numpy(b.lens.astype(np.int64) - 1).cuda()
+    _, kc, vc, tables, lens, prefix, starts = b.args()
+    slots = tables.gather(1, (last // b.bs)[:, None])[:, 0].long() * b.bs + last % b.bs
+    a = torch.arange(2000, dtype=torch.float64)[:, None] * 10000.0 ** -(torch.arange(0, D, 2, dtype=torch.float64) / D)
+    cs = torch.cat([a.cos(), a.sin()], 1).float().cuda()
+    position = last.int()
+    w = torch.ones(D, dtype=torch.float16, device="cuda")
+    kv = dict(kv_dtype="fp8" if fp8 else "auto", k_scale=b.ks, v_scale=b.vs)
+    kw = dict(b.kw(), **kv)
+    q = torch.empty(n, Hq, D, dtype=torch.float16, device="cuda")
+    outs = torch.empty(steps, n, Hq, D, dtype=torch.float16, device="cuda")
+
+    def run(between=lambda: None):
+        for i in range(steps):
+            x = rows[i]
+            pa_lib.norm_rope_and_cache(*x.split([Hq, Hkv, Hkv], 1), kc, vc, slots, position, cs, q_weight=w, k_weight=w,
+                                       out=q, **kv)
+            between()
+            pa_lib.decode_shared(q, kc, vc, tables, lens, prefix, starts, out=outs[i], **kw)
+            between()
+
+    run(torch.cuda.synchronize)
+    want = outs.clone()
+    for _ in range(5):
+        outs.fill_(float("nan"))
+        run()
+        assert torch.equal(outs, want)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        run()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            run()
+    for _ in range(5):
+        outs.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs, want)
+    assert pa_lib.check_device_error() == 0
+
+
 def test_a_whole_step_from_lengths_to_attention(pa_lib):
     """pool_extend, norm_rope_and_cache and decode_shared in one captured step,
     replayed: a batch that forks one prompt grows by one token a step, its new
