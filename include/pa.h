@@ -263,8 +263,10 @@ pa_status pa_pool_release(const pa_tensor* block_tables, const pa_tensor* seq_le
  * bytes. It is the buffer
  * given to pa_set_workspace() for the current device, or else a buffer the
  * library allocates (and zeroes) per (device, stream) outside stream
- * capture and keeps, with any larger one that a later step needs: a captured
- * graph goes on using the one that it was captured with. Calls that overlap on
+ * capture and keeps. Where a later step needs a larger one, the call waits for
+ * the stream and frees the old one first, unless a step was captured in it: a
+ * graph goes on using the one that it was captured with, which then stays
+ * allocated for as long as the process runs. Calls that overlap on
  * the GPU must not share a workspace. Host threads may call at once: the
  * launches of one step are not torn apart.
  */

@@ -206,6 +206,7 @@ struct Workspace {
   void* ptr = nullptr;
   size_t bytes = 0;
   bool dirty = false;  // the pool counter may be nonzero (a merge launch failed)
+  bool captured = false;  // a graph may replay steps in it
 };
 
 struct DeviceState {
@@ -443,18 +444,28 @@ pa_status get_workspace(DeviceState* st, cudaStream_t stream, const WsLayout& la
     } catch (const std::bad_alloc&) {
       return fail(PA_ERR_HOST_MEMORY, "host memory exhausted");
     }
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(stream, &cap);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
+    const bool capturing = cap != cudaStreamCaptureStatusNone;
     if (w->bytes < need) {
-      cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-      cudaError_t e = cudaStreamIsCapturing(stream, &cap);
-      if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
-      if (cap != cudaStreamCaptureStatusNone)
+      if (capturing)
         return fail(PA_ERR_WORKSPACE,
                     "decode workspace must grow to %zu bytes during stream capture; run one "
                     "step before capturing or call pa_set_workspace",
                     need);
-      // The old buffer stays: a captured graph may replay steps in it. Each is at
-      // least twice the last, so all that stay are smaller than the one in use.
-      size_t bytes = round_up(std::max(need + need / 4, 2 * w->bytes), 1 << 20);
+      size_t bytes = need + need / 4;
+      if (w->captured) {
+        // The old buffer stays with the graph. Each is at least twice the last (where
+        // there is room), so all that stay are smaller than the one in use.
+        bytes = std::max(bytes, 2 * w->bytes);
+      } else if (w->ptr) {  // freed first: the new one may need its room
+        e = cudaStreamSynchronize(stream);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
+        cudaFree(w->ptr);
+        *w = Workspace{};
+      }
+      bytes = round_up(bytes, 1 << 20);
       void* p = nullptr;
       e = cudaMalloc(&p, bytes);
       if (e == cudaErrorMemoryAllocation && bytes > need) {  // without the room to grow, then
@@ -467,8 +478,9 @@ pa_status get_workspace(DeviceState* st, cudaStream_t stream, const WsLayout& la
         cudaFree(p);
         return cuda_fail(e, "cudaMemsetAsync(workspace)");
       }
-      *w = Workspace{p, bytes, false};
+      *w = Workspace{p, bytes, false, false};
     }
+    if (capturing) w->captured = true;
   }
   if (w->dirty) {
     cudaError_t e = cudaMemsetAsync(static_cast<char*>(w->ptr) + lay.pool, 0,

@@ -605,6 +605,52 @@ def test_a_graph_outlives_a_larger_step_on_its_stream(pa_lib):
     assert pa_lib.check_device_error() == 0
 
 
+def test_a_workspace_that_grows_is_not_kept_twice(pa_lib):
+    """A stream whose steps get larger holds what one with the large step alone holds;
+    only one that a graph was captured with stays beside the larger one."""
+    D, Hq, Hkv = 256, 16, 8
+    kc = torch.zeros(4, Hkv, 16, D, dtype=torch.bfloat16, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    steps = []
+    for B in (1024, 4096):
+        q = torch.ones(B, Hq, D, dtype=torch.bfloat16, device="cuda")
+        steps.append((q, kc, kc.clone(), torch.zeros(B, 2, **i32), torch.ones(B, **i32), torch.empty_like(q)))
+
+    def call(k, s):
+        *args, out = steps[k]
+        pa_lib.decode(*args, num_kv_heads=Hkv, scale=1.0, block_size=16, out=out, stream=s)
+
+    def held(ks, capture=False):
+        s = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        before = torch.cuda.mem_get_info()[0]
+        for n, k in enumerate(ks):
+            call(k, s)
+            if capture and n == 0:
+                torch.cuda.synchronize()
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph, stream=s):
+                    call(k, s)
+                graphs.append(graph)
+        torch.cuda.synchronize()
+        return before - torch.cuda.mem_get_info()[0]
+
+    graphs = []
+    held([0, 1], capture=True)                  # whatever a first call sets up
+    small, large = held([0]), held([1])
+    slack = 4 << 20
+    assert small > 2 * slack
+    assert held([0, 1, 0, 1]) <= large + slack
+    assert held([0, 1], capture=True) >= small + large - slack
+    want = [o.clone() for *_, o in steps]
+    for *_, o in steps:
+        o.fill_(float("nan"))
+    for g in graphs:
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(steps[0][-1], want[0])
+
+
 def test_captured_step_follows_new_lengths_and_groups(pa_lib):
     b = Batch([(640, [9, 30, 1, 60]), (640, [200, 3, 4, 5])], seed=16)
     args = b.args()
