@@ -268,7 +268,8 @@ pa_status pa_pool_release(const pa_tensor* block_tables, const pa_tensor* seq_le
  * graph goes on using the one that it was captured with, which then stays
  * allocated for as long as the process runs. Calls that overlap on
  * the GPU must not share a workspace. Host threads may call at once: the
- * launches of one step are not torn apart.
+ * launches of one step are not torn apart, and calls in different workspaces do
+ * not wait for one another's launches.
  */
 pa_status pa_decode(const pa_tensor* out, const pa_tensor* q, const pa_tensor* key_cache,
                     const pa_tensor* value_cache, const pa_tensor* block_tables,

@@ -202,11 +202,21 @@ using namespace pa;  // the checking helpers (pa_host.h)
 
 // ------------------------------------------------------------ device state
 
+// A step's launches must follow one another on their stream, whichever host
+// threads call: the next step in the same workspace comes behind them. `order` is
+// held from the choice of the buffer to the last launch, and guards the rest; it
+// is taken before g_mu.
 struct Workspace {
+  std::mutex order;
   void* ptr = nullptr;
   size_t bytes = 0;
   bool dirty = false;  // the pool counter may be nonzero (a merge launch failed)
   bool captured = false;  // a graph may replay steps in it
+  void set(void* p, size_t n) {
+    ptr = p;
+    bytes = n;
+    dirty = captured = false;
+  }
 };
 
 struct DeviceState {
@@ -427,23 +437,28 @@ pa_status plan_decode(DeviceState* st, int ct, int qt, int kind, int64_t B, int 
   return PA_OK;
 }
 
-// Picks the workspace for this call (zeroed on allocation: the pool counter
-// starts at zero, and each step's merge kernel leaves it at zero).
-pa_status get_workspace(DeviceState* st, cudaStream_t stream, const WsLayout& lay, void** ws,
-                        Workspace** wsp) {
-  Workspace* w;
-  const size_t need = lay.total;
+// Picks the workspace for this call (g_mu held): the caller's, or the stream's.
+pa_status pick_workspace(DeviceState* st, cudaStream_t stream, Workspace** wsp) {
   if (st->user_ws.ptr) {
-    if (st->user_ws.bytes < need)
-      return fail(PA_ERR_WORKSPACE, "workspace too small: %zu bytes set, %zu needed",
-                  st->user_ws.bytes, need);
-    w = &st->user_ws;
+    *wsp = &st->user_ws;
+    return PA_OK;
+  }
+  try {
+    *wsp = &st->lib_ws[reinterpret_cast<uintptr_t>(stream)];
+  } catch (const std::bad_alloc&) {
+    return fail(PA_ERR_HOST_MEMORY, "host memory exhausted");
+  }
+  return PA_OK;
+}
+
+// Makes the picked workspace (its order held) large enough: zeroed on allocation
+// (the pool counter starts at zero, and each step's merge kernel leaves it at zero).
+pa_status ready_workspace(DeviceState* st, cudaStream_t stream, const WsLayout& lay, Workspace* w) {
+  const size_t need = lay.total;
+  if (w == &st->user_ws) {
+    if (w->bytes < need)
+      return fail(PA_ERR_WORKSPACE, "workspace too small: %zu bytes set, %zu needed", w->bytes, need);
   } else {
-    try {
-      w = &st->lib_ws[reinterpret_cast<uintptr_t>(stream)];
-    } catch (const std::bad_alloc&) {
-      return fail(PA_ERR_HOST_MEMORY, "host memory exhausted");
-    }
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
     cudaError_t e = cudaStreamIsCapturing(stream, &cap);
     if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
@@ -463,7 +478,7 @@ pa_status get_workspace(DeviceState* st, cudaStream_t stream, const WsLayout& la
         e = cudaStreamSynchronize(stream);
         if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
         cudaFree(w->ptr);
-        *w = Workspace{};
+        w->set(nullptr, 0);
       }
       bytes = round_up(bytes, 1 << 20);
       void* p = nullptr;
@@ -478,7 +493,7 @@ pa_status get_workspace(DeviceState* st, cudaStream_t stream, const WsLayout& la
         cudaFree(p);
         return cuda_fail(e, "cudaMemsetAsync(workspace)");
       }
-      *w = Workspace{p, bytes, false, false};
+      w->set(p, bytes);
     }
     if (capturing) w->captured = true;
   }
@@ -488,8 +503,6 @@ pa_status get_workspace(DeviceState* st, cudaStream_t stream, const WsLayout& la
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(pool counter)");
     w->dirty = false;
   }
-  *ws = w->ptr;
-  *wsp = w;
   return PA_OK;
 }
 
@@ -540,21 +553,21 @@ pa_status pa_set_workspace(void* ptr, size_t bytes) {
   return pa::abi_guard([&]() -> pa_status {
     if (ptr && (reinterpret_cast<uintptr_t>(ptr) % 256))
       return fail(PA_ERR_LAYOUT, "workspace must be 256-byte aligned");
-    std::lock_guard<std::mutex> lk(g_mu);
     DeviceState* st;
-    pa_status s = device_state(&st, nullptr);
-    if (s) return s;
+    {
+      std::lock_guard<std::mutex> lk(g_mu);
+      const pa_status s = device_state(&st, nullptr);
+      if (s) return s;
+    }
+    std::lock_guard<std::mutex> order(st->user_ws.order);
     if (ptr && bytes) {
       // The pool counter must start at zero; zero the whole buffer.
       cudaError_t e = cudaMemset(ptr, 0, bytes);
       if (e == cudaSuccess) e = cudaDeviceSynchronize();
       if (e != cudaSuccess) return cuda_fail(e, "zeroing the workspace");
     }
-    st->user_ws = Workspace{};
-    if (ptr) {
-      st->user_ws.ptr = ptr;
-      st->user_ws.bytes = bytes;
-    }
+    std::lock_guard<std::mutex> lk(g_mu);  // pick_workspace reads it under this one
+    st->user_ws.set(ptr, ptr ? bytes : 0);
     return ok();
   });
 }
@@ -1054,10 +1067,7 @@ pa_status run_decode(const DecodeCall& c, DeviceState* st, const DecodePlan& pla
     e = pa::merge_launch(c.qt, m, merge_grid, cs, !prof);
   }
   if (e != cudaSuccess) {
-    if (wsp) {
-      std::lock_guard<std::mutex> lk(g_mu);
-      wsp->dirty = true;  // the decode kernel ran; its pool counter was not reset
-    }
+    if (wsp) wsp->dirty = true;  // the decode kernel ran; its pool counter was not reset
     return cuda_fail(e, "merge kernel launch");
   }
   g_launches += 2;
@@ -1151,22 +1161,23 @@ pa_status decode_entry(const pa_tensor* out, const pa_tensor* q, const pa_tensor
   if (sh && !use_shared(c, sh->NG)) sh = nullptr;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (chunked && use_chunk_tc(c)) return run_chunk_tc(c, cs);
-  // a step's launches follow one another on their stream, whichever host
-  // threads call: the next step in the same workspace comes behind them
-  static std::mutex in_order;
-  std::lock_guard<std::mutex> launches(in_order);
   DeviceState* st;
   DecodePlan plan;
   WsLayout layout;
-  void* ws = nullptr;
-  Workspace* wsp = nullptr;
-  {
+  Workspace *w = nullptr, *again = nullptr;
+  std::unique_lock<std::mutex> order;
+  do {  // (pa_set_workspace may come between the choice and the hold)
+    if (order.owns_lock()) order.unlock();
+    {
+      std::lock_guard<std::mutex> lk(g_mu);
+      if ((s = device_state(&st, nullptr)) || (s = pick_workspace(st, cs, &w))) return s;
+    }
+    order = std::unique_lock<std::mutex>(w->order);
     std::lock_guard<std::mutex> lk(g_mu);
-    if ((s = device_state(&st, nullptr)) || (s = plan_call(st, c, &plan, &layout, sh)) ||
-        (s = get_workspace(st, cs, layout, &ws, &wsp)))
-      return s;
-  }
-  return run_decode(c, st, plan, layout, ws, wsp, cs, sh);
+    if ((s = plan_call(st, c, &plan, &layout, sh)) || (s = pick_workspace(st, cs, &again))) return s;
+  } while (w != again);
+  if ((s = ready_workspace(st, cs, layout, w))) return s;
+  return run_decode(c, st, plan, layout, w->ptr, w, cs, sh);
 }
 
 }  // namespace

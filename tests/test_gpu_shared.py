@@ -584,6 +584,49 @@ def test_threads_calling_on_one_stream(pa_lib):
         assert (ref - ref[0]).abs().max() <= 2.0 ** -6
 
 
+def test_a_thread_that_waits_on_its_stream_holds_up_no_other(pa_lib):
+    """A host function keeps one stream from going on (for at most 20 s), a thread
+    fills it with steps until its launches wait; a step on another stream, from
+    another thread, is enqueued all the same, and releases the first."""
+    import ctypes
+    import threading
+    import time
+    cu = ctypes.CDLL("libcuda.so.1")
+    b = Batch([(64, [3, 4])], seed=1)
+    args = b.args()[:5]
+    outs = [torch.empty_like(b.q) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for o, s in zip(outs, streams):
+        pa_lib.decode(*args, out=o, stream=s, **b.kw())
+    torch.cuda.synchronize()
+    went_on, freed, count = threading.Event(), [], [0]
+    hold = ctypes.CFUNCTYPE(None, ctypes.c_void_p)(lambda _: freed.append(went_on.wait(20)))
+    assert cu.cuLaunchHostFunc(ctypes.c_void_p(streams[0].cuda_stream), hold, None) == 0
+
+    def many():
+        for _ in range(3000):
+            pa_lib.decode(*args, out=outs[0], stream=streams[0], **b.kw())
+            count[0] += 1
+
+    def other():
+        pa_lib.decode(*args, out=outs[1], stream=streams[1], **b.kw())
+        went_on.set()
+
+    threads = [threading.Thread(target=f) for f in (many, other)]
+    threads[0].start()
+    last = -1
+    while count[0] != last and not freed:       # until it no longer gets on
+        last = count[0]
+        time.sleep(1)
+    threads[1].start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert freed == [True]
+    b.check(outs[0])
+    b.check(outs[1])
+
+
 def test_a_graph_outlives_a_larger_step_on_its_stream(pa_lib):
     small, large = Batch([(640, [9, 30, 1, 60])], seed=16), Batch([(512, [9] * 200)], heads=(16, 8), seed=17)
     args = small.args()
