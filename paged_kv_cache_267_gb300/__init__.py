@@ -12,6 +12,7 @@ import struct
 
 import torch
 
+from . import build
 from .build import LIB_PATH
 
 PA_F16, PA_BF16, PA_FP8_E4M3, PA_I32, PA_I64, PA_F32 = 0, 1, 2, 3, 4, 5
@@ -121,15 +122,19 @@ _calls = None
 
 
 def _native():
-    """The hot entry points: the compiled binding (built with the library, for
-    this torch), else ctypes. Both run the same library."""
+    """The hot entry points: the compiled binding, where it was built for this
+    torch and Python (it reads torch's tensors by their layout), else ctypes. Both
+    run the same library."""
     global _calls
     if _calls is None:
         lib()
-        try:
-            from . import _pa_torch as _calls
-        except ImportError:  # built for another torch or Python
-            _calls = _CtypesCalls()
+        calls = _CtypesCalls()
+        if build.binding_fits():
+            try:
+                from . import _pa_torch as calls
+            except ImportError:  # a library that it needs is missing
+                pass
+        _calls = calls
     return _calls
 
 

@@ -51,7 +51,7 @@ def _binding_stamp() -> str:
     return f"{torch.__version__} {sysconfig.get_config_var('SOABI')}"
 
 
-def _binding_fits() -> bool:
+def binding_fits() -> bool:
     """Whether _pa_torch.so was built for this torch and Python."""
     try:
         with open(BINDING_STAMP, encoding="utf-8") as f:
@@ -61,7 +61,7 @@ def _binding_fits() -> bool:
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB_PATH) or not _binding_fits():
+    if not os.path.exists(LIB_PATH) or not binding_fits():
         return True
     t = os.path.getmtime(LIB_PATH)
     return any(os.path.getmtime(p) > t for p in _deps())

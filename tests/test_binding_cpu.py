@@ -61,3 +61,17 @@ def test_unknown_type(routes):
     for route in routes:
         with pytest.raises((TypeError, KeyError)):
             getattr(route, "pa_decode")(*args, 0)
+
+
+@pytest.mark.parametrize("stamp", [None, "2.1.0 cpython-312-x86_64-linux-gnu", ""])
+def test_a_binding_of_another_torch_is_not_loaded(pa_lib, monkeypatch, tmp_path, stamp):
+    """Its symbols may resolve and the layout of tensors differ all the same."""
+    from paged_kv_cache_267_gb300 import build
+    monkeypatch.setattr(pa, "_calls", None)
+    assert not isinstance(pa._native(), pa._CtypesCalls)
+    path = tmp_path / "stamp"
+    if stamp is not None:
+        path.write_text(stamp)
+    monkeypatch.setattr(build, "BINDING_STAMP", str(path))
+    monkeypatch.setattr(pa, "_calls", None)
+    assert isinstance(pa._native(), pa._CtypesCalls)
