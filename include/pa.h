@@ -337,6 +337,10 @@ pa_status pa_decode_noalloc(const pa_tensor* out, const pa_tensor* q,
  * least half of its length into the prefix; the pass covers the positions that
  * all of these attend to. Any other sequence, an idle row of length 0 among
  * them, is decoded by itself, as is a group with fewer than two that take part.
+ * The pass works on the group's rows from the first that takes part to the last, in
+ * units of at most 256 (query, head) rows of a KV head (128 with head_dim 256),
+ * each of which reads the shared positions: a group with no more rows that take
+ * part than units is decoded row by row as well.
  * The pass reads the prefix through the table of the group's first row that
  * takes part, and no entry of a block that this row does not attend to.
  * A step whose tables could not name more than 72 MB of K/V in all (B * MB *

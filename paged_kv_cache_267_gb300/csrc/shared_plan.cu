@@ -81,7 +81,8 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
   int* s_pre = s_r0 + a.NG + 1;  // [NG] prefix lengths, whole blocks
   int* s_in = s_pre + a.NG;      // [NG] rows that take part, then first flat tile
   int* s_first = s_in + a.NG;    // [NG] the first of them
-  int* s_base = s_first + a.NG;  // [NG] first slot
+  int* s_last = s_first + a.NG;  // [NG] and the last
+  int* s_base = s_last + a.NG;   // [NG] first slot
   int* s_w0 = s_base + a.NG;     // [NG] first CTA that meets the group
   int* s_lo = s_w0 + a.NG;       // [NG] first position that all taking part attend to
   __shared__ int s_wsz, s_tiles, s_tails, s_dual, s_nunits;
@@ -122,6 +123,7 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
           s_pre[g] = q / a.bs * a.bs;
           s_in[g] = 0;
           s_first[g] = a.B;
+          s_last[g] = -1;
           s_lo[g] = 0;
         }
       }
@@ -166,10 +168,12 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
       if (in && (tid & 31) == __ffs(votes) - 1) {
         atomicAdd(&s_in[g], __popc(votes));
         atomicMin(&s_first[g], b);
+        atomicMax(&s_last[g], b0 + 31 - __clz(votes));
       }
     } else if (in) {
       atomicAdd(&s_in[g], 1);
       atomicMin(&s_first[g], b);
+      atomicMax(&s_last[g], b);
     }
   }
   tails = __reduce_add_sync(kFull, tails);
@@ -185,13 +189,17 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
       const int g = g0 + tid;
       int x = 0;
       if (g < a.NG) {
-        // one sequence reads its prefix once anyway
-        if (s_in[g] < 2 || s_lo[g] >= s_pre[g]) s_pre[g] = s_lo[g] = 0;
-        const int n = s_r0[g + 1] - s_r0[g], span = s_pre[g] - s_lo[g];
-        if (span > 0) atomicSub(&s_tails, s_in[g] * (span / kTile));
+        // Units are cut over the rows from the first that takes part to the last
+        // (idle rows are mostly the end of a padded batch). Each reads the prefix
+        // once, as a sequence by itself does, so there must be fewer of them than
+        // rows that take part.
+        const int n = max(s_last[g] - s_first[g] + 1, 0);
         Units u;
-        u.nt = (span + a.kv - 1) / a.kv;
         u.nut = n <= up_max ? (n > 0) : (n + up_max - 1) / up_max;
+        if (s_in[g] <= u.nut || s_lo[g] >= s_pre[g]) s_pre[g] = s_lo[g] = 0;
+        const int span = s_pre[g] - s_lo[g];
+        if (span > 0) atomicSub(&s_tails, s_in[g] * (span / kTile));
+        u.nt = (span + a.kv - 1) / a.kv;
         u.up = u.nut <= 1 ? n : (n + u.nut - 1) / u.nut;
         u.up_mul = u.nut <= 1 ? 0u : 0xffffffffu / static_cast<uint32_t>(max(u.up, 1)) + 1u;
         s_units[g] = u;
@@ -239,9 +247,8 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
     SharedGroup r = {};
     if (g >= a.NG) return r;
     const Units u = s_units[g];
-    r.r0 = s_r0[g];
-    r.n = s_r0[g + 1] - s_r0[g];
-    r.table_row = s_first[g];
+    r.r0 = r.table_row = s_first[g];
+    r.n = max(s_last[g] - s_first[g] + 1, 0);
     r.prefix = s_pre[g] - s_lo[g];
     r.first = s_lo[g];
     r.f0 = s_in[g];
@@ -284,7 +291,7 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
     r.tiles = (L + kTile - 1) / kTile - r.start / kTile;
     if (takes_part(L, g)) {
       const Units u = s_units[g];
-      const int i = b - s_r0[g];
+      const int i = b - s_first[g];
       const int ut = u.up_mul ? (u.up == 1 ? i : static_cast<int>(__umulhi(static_cast<uint32_t>(i), u.up_mul))) : 0;
       r.head = s_lo[g] / kTile - r.start / kTile;
       r.tiles -= (s_pre[g] - s_lo[g]) / kTile;
@@ -320,13 +327,13 @@ __global__ void __launch_bounds__(kMaxThreads) shared_plan_kernel(const SharedPl
 }  // namespace
 
 cudaError_t shared_plan_launch(const SharedPlanArgs& a, cudaStream_t s, bool pdl) {
-  const size_t smem = (11 * static_cast<size_t>(a.NG) + 1) * sizeof(int);
+  const size_t smem = (12 * static_cast<size_t>(a.NG) + 1) * sizeof(int);
   if (smem > 40 * 1024) {
     // Without asking, a CTA has 48 KB, its static arrays (0.3 KB) among them. (One
     // value, whichever thread sets it.)
     const cudaError_t e =
         cudaFuncSetAttribute(reinterpret_cast<const void*>(shared_plan_kernel<false>),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, (11 * kMostGroups + 1) * 4);
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, (12 * kMostGroups + 1) * 4);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};

@@ -1,13 +1,14 @@
 // Layout of the plan of a shared-prefix decode step, written by the plan
 // kernel (shared_plan.cu) and read by the prefix, decode and merge kernels.
 //
-// Sequences of group g, rows [r0, r0 + n), share their first P tokens (P a
-// multiple of the block size, so of 16). A row takes part when it is at least
-// that long and no window cuts it, or one that reaches back over at least half
-// of its length into them. With S the largest window start of those that take
-// part, rounded up to 16 (0 without windows), the prefix kernel computes the
-// partial softmax of all of them over [S, P); the decode kernel covers the rest
-// of their ranges, [start, S) and [P, L), and the whole range of every other row.
+// Sequences of group g share their first P tokens (P a multiple of the block
+// size, so of 16). A row takes part when it is at least that long and no window
+// cuts it, or one that reaches back over at least half of its length into them;
+// rows [r0, r0 + n) are those from the first that does to the last. With S the
+// largest window start of those that take part, rounded up to 16 (0 without
+// windows), the prefix kernel computes the partial softmax of all of them over
+// [S, P); the decode kernel covers the rest of their ranges, [start, S) and
+// [P, L), and the whole range of every other row.
 //
 // The (query, head) rows of one KV head of a group, n * G of them, are cut into
 // nut units of up pairs (sequences) each, at most 256 rows; a unit of at most
@@ -39,7 +40,7 @@ enum { kShWsz = 0, kShTails = 1, kShTailsWs = 2 };
 
 struct SharedGroup {  // 12 words a group
   int r0, n;          // rows
-  int table_row;      // the row whose block table the prefix is read through
+  int table_row;      // r0, whose block table the prefix is read through
   int prefix;         // P - S, 0 when the group does not share
   int f0;             // first flat tile
   int nt;             // K/V tiles of the prefix

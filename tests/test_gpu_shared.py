@@ -450,6 +450,45 @@ def test_many_groups_of_many_rows(pa_lib):
     b.check(b.run(pa_lib))
 
 
+def group_plan(ws, g):
+    """Group g's record in the plan of the last shared step in the workspace ws."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    at = (256 + -(-(8 + 4097) * 4 // 256) * 256) // 4 + 8 + 16 * sms + 12 * g
+    names = "r0 n table_row prefix f0 nt nut up base dual wfirst first".split()
+    return dict(zip(names, ws.view(torch.int32)[at:at + 12].tolist()))
+
+
+@pytest.mark.parametrize("rows,live,units,kw", [
+    (256, [100, 103], 1, {}),                        # 4 units for all rows of the group
+    (256, range(10), 1, {}),                         # a padded batch
+    (256, range(200, 256), 1, {}),
+    (256, range(100, 190), 2, {}),
+    (256, [0, 255], 0, {}),                          # two rows would read the prefix four times
+    (256, [0, 100, 180, 255], 0, {}),
+    (256, [0, 100, 180, 200, 255], 4, {}),
+    (130, [7, 9, 128], 0, dict(D=256)),              # 4 units of at most 32 rows
+    (130, [1, 33, 34], 2, dict(D=256)),
+    (200, [0, 70, 199], 0, dict(fp8=True)),
+    (200, range(150, 199), 1, dict(fp8=True)),
+])
+def test_idle_rows_make_no_units(rows, live, units, kw, pa_lib):
+    """Every unit reads the prefix: a batch that is mostly idle has no more of them
+    than its live rows need."""
+    b = Batch([(640, [5 + i % 7 for i in range(rows)])], heads=(8, 2), seed=rows,
+              idle=[i for i in range(rows) if i not in live], **kw)
+    ws = torch.zeros(pa_lib.decode_shared_workspace_size(b.B, 1, 8, 2, b.D), dtype=torch.uint8, device="cuda")
+    try:
+        pa_lib.set_workspace(ws)
+        b.check(b.run(pa_lib))
+    finally:
+        pa_lib.set_workspace(None)
+    p = group_plan(ws, 0)
+    assert (p["nut"] if p["nt"] else 0) == units, p
+    if units:
+        assert (p["r0"], p["n"], p["table_row"]) == (min(live), max(live) - min(live) + 1, min(live))
+    assert pa_lib.check_device_error() == 0
+
+
 @pytest.mark.parametrize("B,heads,D", [(2, (8, 2), 128), (300, (2, 1), 64), (40, (16, 1), 256)])
 def test_the_stated_workspace_serves_both_paths(B, heads, D, pa_lib):
     b = Batch([(320, [3 + i % 40 for i in range(B)])], dt="f16", heads=heads, D=D, seed=B)
