@@ -41,6 +41,17 @@ class PaTensor(ctypes.Structure):
                 ("shape", ctypes.c_int64 * _MAX_DIMS), ("strides", ctypes.c_int64 * _MAX_DIMS)]
 
 
+class _TensorArg:
+    """A `const pa_tensor*` argument: a PaTensor, a pointer to one, its bytes, or
+    None. (Not a bare number, which would be taken for an address.)"""
+
+    @classmethod
+    def from_param(cls, x):
+        if x is None or isinstance(x, bytes):
+            return ctypes.c_char_p.from_param(x)
+        return ctypes.POINTER(PaTensor).from_param(x)
+
+
 _lib_handle = None
 
 
@@ -52,8 +63,7 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(f"{LIB_PATH} is missing: build it with "
                                "`python -c 'import __graft_entry__ as g; g.build()'`")
         L = ctypes.CDLL(LIB_PATH)
-        # descriptors are passed by address: a PaTensor by reference, or its bytes
-        P = ctypes.c_void_p
+        P = _TensorArg
         i32, i64, f32, vp, st = (ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p,
                                  ctypes.c_int32)
         sig = {

@@ -75,3 +75,18 @@ def test_a_binding_of_another_torch_is_not_loaded(pa_lib, monkeypatch, tmp_path,
     monkeypatch.setattr(build, "BINDING_STAMP", str(path))
     monkeypatch.setattr(pa, "_calls", None)
     assert isinstance(pa._native(), pa._CtypesCalls)
+
+
+def test_descriptors_for_the_library_itself(pa_lib):
+    """As a PaTensor, by reference, as a pointer or as bytes; nothing else."""
+    import ctypes
+    t = call_args()["pa_decode"][:6]
+    forms = [pa.tensor_desc, lambda x: ctypes.byref(pa.tensor_desc(x)), lambda x: ctypes.pointer(pa.tensor_desc(x)), pa._desc]
+    seen = set()
+    for form in forms:
+        seen.add((pa.lib().pa_decode(*[form(x) for x in t], 2, 0.1, 16, 0, 0, 1.0, 1.0, None), pa.last_error()))
+        assert pa.lib().pa_decode(None, *[form(x) for x in t[1:]], 2, 0.1, 16, 0, 0, 1.0, 1.0, None) == -1
+    assert len(seen) == 1
+    for bad in (t[0].data_ptr(), 0, "x", t[0], 1.5):
+        with pytest.raises(ctypes.ArgumentError):
+            pa.lib().pa_decode(bad, *[pa.tensor_desc(x) for x in t[1:]], 2, 0.1, 16, 0, 0, 1.0, 1.0, None)
