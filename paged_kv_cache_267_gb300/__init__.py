@@ -230,6 +230,12 @@ def _kv(kv_dtype) -> int:
     raise ValueError(f"bad kv_dtype {kv_dtype!r}")
 
 
+def _window(window) -> int:
+    """Window argument in 32 bits: one that is larger cuts nothing off, one below
+    zero is none."""
+    return max(-1, min(int(window), 2**31 - 1))
+
+
 # ---------------------------------------------------------------- hot path
 
 def reshape_and_cache(k, v, key_cache, value_cache, slot_mapping, kv_dtype="auto",
@@ -295,7 +301,7 @@ def decode(q, key_cache, value_cache, block_tables, seq_lens, *, num_kv_heads: i
         out = torch.empty_like(q)
     _check(_native().pa_decode(
         out, q, key_cache, value_cache, block_tables, seq_lens, int(num_kv_heads), float(scale),
-        int(block_size), int(window), _kv(kv_dtype), float(k_scale), float(v_scale),
+        int(block_size), _window(window), _kv(kv_dtype), float(k_scale), float(v_scale),
         _handle(stream)))
     return out
 
@@ -312,7 +318,7 @@ def decode_shared(q, key_cache, value_cache, block_tables, seq_lens, prefix_lens
         out = torch.empty_like(q)
     _check(_native().pa_decode_shared(
         out, q, key_cache, value_cache, block_tables, seq_lens, prefix_lens, group_starts,
-        int(num_kv_heads), float(scale), int(block_size), int(window), _kv(kv_dtype),
+        int(num_kv_heads), float(scale), int(block_size), _window(window), _kv(kv_dtype),
         float(k_scale), float(v_scale), _handle(stream)))
     return out
 
@@ -327,7 +333,7 @@ def prefill_chunk(q, key_cache, value_cache, block_tables, seq_lens, *, num_kv_h
         out = torch.empty_like(q)
     _check(_native().pa_prefill_chunk(
         out, q, key_cache, value_cache, block_tables, seq_lens, int(num_kv_heads), float(scale),
-        int(block_size), int(window), _kv(kv_dtype), float(k_scale), float(v_scale),
+        int(block_size), _window(window), _kv(kv_dtype), float(k_scale), float(v_scale),
         _handle(stream)))
     return out
 
@@ -340,7 +346,7 @@ def decode_noalloc(q, key_cache, value_cache, block_tables, seq_lens, *, num_kv_
     memory at decode time. `out` must be given (nothing is allocated)."""
     _check(_native().pa_decode_noalloc(
         out, q, key_cache, value_cache, block_tables, seq_lens, int(num_kv_heads), float(scale),
-        int(block_size), int(window), _kv(kv_dtype), float(k_scale), float(v_scale),
+        int(block_size), _window(window), _kv(kv_dtype), float(k_scale), float(v_scale),
         _handle(stream)))
     return out
 

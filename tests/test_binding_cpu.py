@@ -90,3 +90,27 @@ def test_descriptors_for_the_library_itself(pa_lib):
     for bad in (t[0].data_ptr(), 0, "x", t[0], 1.5):
         with pytest.raises(ctypes.ArgumentError):
             pa.lib().pa_decode(bad, *[pa.tensor_desc(x) for x in t[1:]], 2, 0.1, 16, 0, 0, 1.0, 1.0, None)
+
+
+@pytest.mark.parametrize("window", [2**31 - 1, 2**31, 2**32 + 5, 2**63 - 1, -1, -2**31 - 1])
+def test_windows_beyond_32_bits(routes, window, monkeypatch):
+    """They reach the library (and are stopped by the missing device only), as the
+    largest window or none."""
+    args = call_args()
+    kw = dict(num_kv_heads=2, scale=0.1, block_size=16, window=window, stream=0)
+    for route in routes:
+        sent = []
+
+        class Spy:
+            def __getattr__(self, name):
+                return lambda *a: (sent.append(a), getattr(route, name)(*a))[1]
+
+        monkeypatch.setattr(pa, "_calls", Spy())
+        for name in ("decode", "decode_shared", "prefill_chunk", "decode_noalloc"):
+            out, *rest = args["pa_" + name if name != "decode_noalloc" else "pa_decode"]
+            rest = [x for x in rest if isinstance(x, torch.Tensor)]
+            with pytest.raises(pa.PAError) as e:
+                getattr(pa, name)(*rest, out=out, **kw)
+            assert e.value.status == -4
+        windows = [[x for x in a if isinstance(x, int)][2] for a in sent]  # kv heads, block size, window
+        assert windows == [2**31 - 1 if window > 0 else -1] * 4

@@ -358,6 +358,24 @@ def test_agrees_with_decode_and_no_groups_is_decode(pa_lib):
         pa_lib.set_decode_tuning()
 
 
+def test_windows_longer_than_any_sequence(pa_lib):
+    """2^31 - 1 and all that is beyond 32 bits cut nothing off."""
+    b = Batch([(640, [9, 3, 100]), (128, [1, 1])], seed=11)
+    args, kw = b.args(), {k: v for k, v in b.kw().items() if k != "window"}
+    q4 = torch.stack([b.q, b.q], 1)
+    calls = [lambda w: pa_lib.decode_shared(*args, window=w, **kw), lambda w: pa_lib.decode(*args[:5], window=w, **kw),
+             lambda w: pa_lib.prefill_chunk(q4, *args[1:5], window=w, **kw)]
+    pa_lib.set_decode_tuning(pool_permille=-1)  # bit-reproducible
+    try:
+        for call in calls:
+            want = call(0)
+            for w in (2**31 - 1, 2**31, 2**32 + 5, 2**63 - 1, -1, -2**40):
+                assert torch.equal(call(w), want), w
+    finally:
+        pa_lib.set_decode_tuning()
+    assert pa_lib.check_device_error() == 0
+
+
 def test_small_steps_are_decoded_plainly_by_default(pa_lib):
     b = Batch([(640, [9, 3, 100]), (128, [1, 1])], seed=21)
     big = Batch([(8192, [9] * 70)], seed=22)  # 70 rows of 8200 tokens: 590 MB
