@@ -266,10 +266,11 @@ pa_status pa_pool_release(const pa_tensor* block_tables, const pa_tensor* seq_le
  * capture and keeps. Where a later step needs a larger one, the call waits for
  * the stream and frees the old one first, unless a step was captured in it: a
  * graph goes on using the one that it was captured with, which then stays
- * allocated for as long as the process runs. Calls that overlap on
- * the GPU must not share a workspace. Host threads may call at once: the
- * launches of one step are not torn apart, and calls in different workspaces do
- * not wait for one another's launches.
+ * allocated for as long as the process runs. Calls that overlap on the GPU must
+ * not share a workspace, and no more must replays of graphs that were captured
+ * on one stream. Host threads may call at once: the launches of one step are not
+ * torn apart, and calls in different workspaces do not wait for one another's
+ * launches.
  */
 pa_status pa_decode(const pa_tensor* out, const pa_tensor* q, const pa_tensor* key_cache,
                     const pa_tensor* value_cache, const pa_tensor* block_tables,
@@ -322,8 +323,12 @@ pa_status pa_decode_noalloc(const pa_tensor* out, const pa_tensor* q,
 /*
  * pa_decode_shared — pa_decode for a batch whose sequences share prefixes: the
  * shared positions of a group are read and multiplied once for all of its
- * sequences instead of once for each. The result is pa_decode's (up to the
- * order of summation).
+ * sequences instead of once for each. The result is pa_decode's up to the
+ * order of summation and, over the shared positions, the rounding of the softmax
+ * weights: they enter the product with V in 16 bits, bf16 for bf16 caches (at most
+ * 2^-8 of each weight; pa_decode holds about 16 bits of them) and f16 for the
+ * others (2^-11, as in pa_decode). The sum that they are divided by is of the
+ * unrounded ones. A step that is decoded plainly (below) has pa_decode's weights.
  *   group_starts  [NG + 1] int32, non-decreasing: group g is the rows
  *                 [group_starts[g], group_starts[g + 1]) of the batch. Rows in
  *                 no group are decoded by themselves.

@@ -313,7 +313,8 @@ def decode_shared(q, key_cache, value_cache, block_tables, seq_lens, prefix_lens
     """One paged decode step of a batch whose rows [group_starts[g],
     group_starts[g + 1]) share their first prefix_lens[g] tokens (the same
     blocks in their tables): the shared positions are attended to once for
-    the whole group. Returns what decode returns."""
+    the whole group. Returns what decode returns, up to the order of summation and,
+    with bf16 caches, softmax weights of the shared positions in bf16."""
     if out is None:
         out = torch.empty_like(q)
     _check(_native().pa_decode_shared(

@@ -27,7 +27,7 @@
 // thread, 78 us; eight or more (one batch after the other), 93-130 us; a CTA
 // that stays with its heads over many rows, 165 us (registers for it leave a
 // quarter of the threads). No one thing bounds what is left, with 24 warps an SM and
-// issue slots at 57%: 15% more instructions (no paired fp32 operations) cost 1%
+// issue slots at 51%: 15% more instructions (no paired fp32 operations) cost 1%
 // (72.3 us), a fourth CTA an SM spills (89 us), and persistent CTAs that copy the
 // next unit, with its angles or without, into shared memory take 75-78 us.
 #include <cuda_bf16.h>

@@ -42,14 +42,16 @@
 // and V, so that a tile is converted while the one before is multiplied; Q is
 // rescaled per row by a power of two to f16's range, which the row's score scale
 // undoes. With two converter warps they bound the loop (2.19 us a tile of 128
-// tokens and two row tiles; now 1.89, bf16 1.71).
+// tokens and two row tiles; now 1.89, bf16 1.73).
 //
-// bf16, 256 queries of 4 heads a KV head on 65536 tokens: 1.71 us a tile of one
-// SM for 16.8 MFLOP, 1.49 PFLOP/s over the chip, 0.78 of the measured peak; bound
-// by the softmax's exponentials and the products in turn. Shares of one prefix
-// are short: of a 4096-token prompt a CTA has four tiles, and of its 14 us about
-// seven are the queries' way in, the first tiles' latency and the partials' way
-// out.
+// bf16, 256 queries of 4 heads on 8 KV heads, between prefixes of 16384 and 65536
+// tokens (75.8 and 216.1 us): 1.73 us a tile of one SM for 16.8 MFLOP, 1.47 PFLOP/s
+// over the chip, 0.77 of the measured peak; bound by the softmax's exponentials
+// and the products in turn. Shares of one prefix are short: of a 4096-token prompt
+// a CTA has four tiles, and of its 14 us about seven are the queries' way in, the
+// first tiles' latency and the partials' way out. head_dim 64 has half the bytes
+// and products a tile for the same exponentials; head_dim 256, with one group and
+// one S, runs S, softmax and O of a tile one after the other.
 #include "attn_tc.cuh"
 #include "pa_internal.h"
 #include "ptx.cuh"
@@ -607,15 +609,16 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           l *= alpha;
           if (grow) ms = mx;
         }
-        // P = 2^(s * sc - ms), packed in pairs over the columns of the scores
-        // just used; the last half is still in registers. It is rounded to the
+        // P = 2^(s * sc - ms + kLift), packed in pairs over the columns of the
+        // scores just used; the last half is still in registers. It is rounded to the
         // products' 16-bit type, which the tensor core needs beside V's, against sums
-        // in fp32 of the unrounded ones: at most 2^-8 of each weight (bf16), or 2^-11
-        // of it and, where it is subnormal, 2^-32 of the reference's weight, which
-        // the segment's largest is not below (f16, with its lift). The products are
-        // added in fp32 by the tensor core, 16 tokens at a time: weights below 2^-24
-        // of a sum that is already there are lost from it (55,000 tokens of weight
-        // 2^-25 behind one of weight 1: 0.1%).
+        // in fp32 of the unrounded ones: at most 2^-8 of each weight for bf16 (a
+        // second product for the remainders costs 15% of a 4096-token prompt's step
+        // and 38% where the prefix is all), for f16 2^-11 of it and, where it is
+        // subnormal, 2^-32 of the reference's weight, which the segment's largest is
+        // not below. The products are added in fp32 by the tensor core, 16 tokens at
+        // a time: weights below 2^-24 of a sum that is already there are lost from it
+        // (55,000 tokens of weight 2^-25 behind one of weight 1: 0.1%).
         const float2 sc2 = make_float2(sc, sc), nms2 = make_float2(kLift - ms, kLift - ms);
         float2 sp[4];
 #pragma unroll
