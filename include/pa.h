@@ -85,8 +85,11 @@ enum {
   PA_DEVERR_TOKENS = 32,   /* pa_pool_extend: a negative request, or more new tokens
                               than slot_mapping has rows */
   PA_DEVERR_POSITION = 64, /* a position outside the rows of cos_sin */
-  PA_DEVERR_GROUP = 128    /* group_starts that decrease or leave [0, B], or a prefix
+  PA_DEVERR_GROUP = 128,   /* group_starts that decrease or leave [0, B], or a prefix
                               that its group's tables cannot hold */
+  PA_DEVERR_QUERY = 256    /* query_start that decreases or leaves [0, T], more than 64
+                              drafted tokens of a sequence, or kept tokens that are not
+                              ascending drafted ones */
 };
 
 #define PA_MAX_DIMS 6
@@ -430,6 +433,109 @@ pa_status pa_set_prefill_path(int32_t path);
 pa_status pa_prefill_chunk_workspace_size(int64_t batch, int32_t num_queries,
                                           int32_t num_q_heads, int32_t num_kv_heads,
                                           int32_t head_dim, size_t* bytes);
+
+/* ------------------------------------------------------------ ragged steps */
+
+/*
+ * pa_prefill_packed — causal attention of a ragged step over the paged cache: whole
+ * prompts, chunks of prompts and single tokens of different sequences, packed one after
+ * the other as pa_pool_extend lays them out. Sequence b's n = query_start[b + 1] -
+ * query_start[b] new tokens (any n >= 0) are rows query_start[b] + t of q and sit at its
+ * last n positions p = seq_lens[b] - n + t; their K/V rows are in the cache already. With
+ * start = (window > 0 && p + 1 > window) ? p + 1 - window : 0,
+ *   out[row, h, :] = sum_{j in [start, p]} softmax_j(scale * q[row,h,:] . K_j) V_j
+ * with K_j, V_j as in pa_decode. A token with p < 0 (seq_lens[b] < n) gives zeros. What
+ * a token does not attend to does not reach its row, infinities and NaN included.
+ *
+ *   out, q        [T, Hq, D]; dims 1 and 2 contiguous, dim 0 any stride (of out: rows
+ *                 that do not overlap); rows 16-byte aligned. Rows of out outside of
+ *                 [query_start[0], query_start[B]) are not written.
+ *   query_start   [B + 1] int32, non-decreasing in [0, T]. A start that decreases or
+ *                 leaves the range is raised to the one before it or clamped, and
+ *                 flagged (PA_DEVERR_QUERY).
+ *   every other argument as for pa_decode; T <= 2^30.
+ * Softmax weights enter the product with V in 16 bits (bf16 for bf16 caches: at most
+ * 2^-8 of each weight, else f16: 2^-11), against sums of the unrounded ones. The order of
+ * summation depends on the lengths and the GPU's SM count only: results are
+ * bit-reproducible.
+ * All inputs are read behind the dependency wait: any kernel may have written them just
+ * before. Workspace: pa_packed_workspace_size() bytes, from the same source as
+ * pa_decode's and under the same rules. Errors as for pa_decode.
+ */
+pa_status pa_prefill_packed(const pa_tensor* out, const pa_tensor* q, const pa_tensor* key_cache,
+                            const pa_tensor* value_cache, const pa_tensor* block_tables,
+                            const pa_tensor* seq_lens, const pa_tensor* query_start,
+                            int32_t num_kv_heads, float scale, int32_t block_size, int32_t window,
+                            int32_t kv_dtype, float k_scale, float v_scale, pa_stream stream);
+
+/*
+ * pa_decode_tree — attention of drafted tokens that form a tree, over the paged cache
+ * (a step that verifies several continuations of a sequence at once). As
+ * pa_prefill_packed, but of its sequence's n <= 64 drafted tokens a row attends to those
+ * whose bit is set in its mask, in place of all those before it:
+ *   positions [start, L - n)  and  L - n + j for every bit j < n of tree_mask[row],
+ * L = seq_lens[b]; a tree sets the bits of a token's ancestors and its own. The window
+ * counts from the row's place in its own continuation: p = L - n + (its bits) - 1, start
+ * as above. A row with no bit attends to the tokens before the drafted ones; where there
+ * are none it is zeros. Of more than 64 drafted tokens the rows are computed against the
+ * first 64 (flagged PA_DEVERR_QUERY). Drafted tokens at negative positions are not there.
+ *
+ *   tree_mask     [T] int64, bit j: drafted token j of the row's sequence.
+ *   window        <= 0: none, else at least 64 (it never cuts through the tree).
+ */
+pa_status pa_decode_tree(const pa_tensor* out, const pa_tensor* q, const pa_tensor* key_cache,
+                         const pa_tensor* value_cache, const pa_tensor* block_tables,
+                         const pa_tensor* seq_lens, const pa_tensor* query_start,
+                         const pa_tensor* tree_mask, int32_t num_kv_heads, float scale,
+                         int32_t block_size, int32_t window, int32_t kv_dtype, float k_scale,
+                         float v_scale, pa_stream stream);
+
+/* Workspace bytes pa_prefill_packed and pa_decode_tree need on the current device for
+ * num_rows rows of q and `batch` sequences, whatever their lengths. */
+pa_status pa_packed_workspace_size(int64_t num_rows, int64_t batch, int32_t num_q_heads,
+                                   int32_t num_kv_heads, int32_t head_dim, size_t* bytes);
+
+/* --------------------------------------------------------- moves of cached rows */
+
+/*
+ * pa_copy_blocks — copies whole blocks of K and V bit for bit: block_pairs[i] =
+ * (source, target). The copies that pa_alloc_append asks its caller for (cow_src,
+ * cow_dst), for instance; a pair with a negative entry is skipped, one with an entry
+ * beyond the pool is skipped and flagged (PA_DEVERR_BLOCK_ID). A block that is the target
+ * of two pairs, or of one and the source of another, is a caller error (which contents
+ * it gets is unspecified).
+ *   key_cache,    [NB, Hkv, bs, D] contiguous, or [layers, NB, Hkv, bs, D] whose layers
+ *   value_cache   are contiguous and any stride apart (the pairs hold for all layers);
+ *                 f16, bf16 or e4m3, rows a multiple of 16 bytes, 16-byte aligned.
+ *   block_pairs   [n, 2] int32 contiguous, 8-byte aligned.
+ */
+pa_status pa_copy_blocks(const pa_tensor* key_cache, const pa_tensor* value_cache,
+                         const pa_tensor* block_pairs, pa_stream stream);
+
+/*
+ * pa_compact_cache — keeps the accepted ones of a step's tokens (of a drafted tree, the
+ * path that was verified): with n = query_start[b + 1] - query_start[b] and base =
+ * seq_lens[b] - n, the K and V rows at position base + kept[b, i] move to base + i for
+ * i < num_kept[b], and
+ *   seq_lens_out[b] = base + num_kept[b];
+ * kept_tokens[b], if given, is that rounded up to whole blocks: pa_pool_release with
+ * released = 1 and shared_tokens = kept_tokens gives the blocks behind it back (its own
+ * lengths then go to a buffer that is not used). Positions behind the kept ones keep
+ * their rows. A list that is not strictly ascending in [0, n), a count that is negative
+ * or beyond n or the list, or a negative base leaves the sequence as it is
+ * (PA_DEVERR_QUERY); a table entry outside of the pool moves nothing
+ * (PA_DEVERR_BLOCK_ID). Sequences that share the blocks that rows are moved in are a
+ * caller error.
+ *   caches        as for pa_copy_blocks; block_tables, seq_lens as for pa_decode.
+ *   query_start   [B + 1] int32; kept [B, M] int32 contiguous; num_kept, seq_lens_out,
+ *                 kept_tokens [B] int32 (kept_tokens may be NULL). Outputs overlap
+ *                 nothing else.
+ */
+pa_status pa_compact_cache(const pa_tensor* key_cache, const pa_tensor* value_cache,
+                           const pa_tensor* block_tables, const pa_tensor* seq_lens,
+                           const pa_tensor* query_start, const pa_tensor* kept,
+                           const pa_tensor* num_kept, const pa_tensor* seq_lens_out,
+                           const pa_tensor* kept_tokens, int32_t block_size, pa_stream stream);
 
 /* Use caller-owned device memory [ptr, ptr + bytes) as the decode workspace on
  * the current device (ptr 256-byte aligned). The call zeroes the buffer and

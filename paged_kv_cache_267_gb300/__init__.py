@@ -19,6 +19,7 @@ PA_F16, PA_BF16, PA_FP8_E4M3, PA_I32, PA_I64, PA_F32 = 0, 1, 2, 3, 4, 5
 PA_KV_AUTO, PA_KV_FP8_E4M3 = 0, 2
 DEVERR_BLOCK_ID, DEVERR_SEQ_LEN, DEVERR_SLOT, DEVERR_TIMEOUT = 1, 2, 4, 8
 DEVERR_POOL, DEVERR_TOKENS, DEVERR_POSITION, DEVERR_GROUP = 16, 32, 64, 128
+DEVERR_QUERY = 256
 _MAX_DIMS = 6
 
 _STATUS = {0: "PA_OK", -1: "PA_ERR_INVALID_ARG", -2: "PA_ERR_UNSUPPORTED", -3: "PA_ERR_LAYOUT",
@@ -78,6 +79,12 @@ def lib() -> ctypes.CDLL:
                                                      ctypes.POINTER(ctypes.c_size_t)]),
             "pa_decode_workspace_size": (st, [i64, i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)]),
             "pa_prefill_chunk": (st, [P, P, P, P, P, P, i32, f32, i32, i32, i32, f32, f32, vp]),
+            "pa_prefill_packed": (st, [P] * 7 + [i32, f32, i32, i32, i32, f32, f32, vp]),
+            "pa_decode_tree": (st, [P] * 8 + [i32, f32, i32, i32, i32, f32, f32, vp]),
+            "pa_packed_workspace_size": (st, [i64, i64, i32, i32, i32,
+                                              ctypes.POINTER(ctypes.c_size_t)]),
+            "pa_copy_blocks": (st, [P, P, P, vp]),
+            "pa_compact_cache": (st, [P] * 9 + [i32, vp]),
             "pa_prefill_chunk_workspace_size": (st, [i64, i32, i32, i32, i32,
                                                      ctypes.POINTER(ctypes.c_size_t)]),
             "pa_set_workspace": (st, [vp, ctypes.c_size_t]),
@@ -339,6 +346,66 @@ def prefill_chunk(q, key_cache, value_cache, block_tables, seq_lens, *, num_kv_h
     return out
 
 
+def prefill_packed(q, key_cache, value_cache, block_tables, seq_lens, query_start, *,
+                   num_kv_heads: int, scale: float, block_size: int, window: int = 0,
+                   kv_dtype="auto", k_scale: float = 1.0, v_scale: float = 1.0, out=None,
+                   stream=None):
+    """Causal attention of packed rows over the paged cache: rows
+    [query_start[b], query_start[b + 1]) of q [T, Hq, D] are the last tokens of
+    sequence b (whole prompts, chunks, or single tokens, as pool_extend lays
+    them out). Returns out [T, Hq, D] (allocated if not given); rows outside
+    of every sequence are not written."""
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    _check(_native().pa_prefill_packed(
+        out, q, key_cache, value_cache, block_tables, seq_lens, query_start, int(num_kv_heads),
+        float(scale), int(block_size), _window(window), _kv(kv_dtype), float(k_scale),
+        float(v_scale), _handle(stream)))
+    return out
+
+
+def decode_tree(q, key_cache, value_cache, block_tables, seq_lens, query_start, tree_mask, *,
+                num_kv_heads: int, scale: float, block_size: int, window: int = 0,
+                kv_dtype="auto", k_scale: float = 1.0, v_scale: float = 1.0, out=None,
+                stream=None):
+    """Attention of drafted tokens that form trees: rows [query_start[b],
+    query_start[b + 1]) of q [T, Hq, D] are the last (at most 64) tokens of
+    sequence b; each attends to the tokens before them and to drafted token j of
+    its sequence where bit j of tree_mask [T] (int64) is set (itself included).
+    Returns out [T, Hq, D] (allocated if not given); rows outside of every
+    sequence are not written."""
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    _check(_native().pa_decode_tree(
+        out, q, key_cache, value_cache, block_tables, seq_lens, query_start, tree_mask,
+        int(num_kv_heads), float(scale), int(block_size), _window(window), _kv(kv_dtype),
+        float(k_scale), float(v_scale), _handle(stream)))
+    return out
+
+
+def copy_blocks(key_cache, value_cache, block_pairs, stream=None) -> None:
+    """Copy whole blocks, keys and values, bit for bit: block_pairs [n, 2]
+    (source, target; a negative one skips the pair), as BlockAllocator.append
+    asks for. Caches [NB, Hkv, bs, D], or all layers' [layers, NB, Hkv, bs, D]."""
+    _check(_native().pa_copy_blocks(key_cache, value_cache, block_pairs, _handle(stream)))
+
+
+def compact_cache(key_cache, value_cache, block_tables, seq_lens, query_start, kept, num_kept, *,
+                  block_size: int, seq_lens_out=None, kept_tokens=None, stream=None):
+    """Move the accepted ones of a step's tokens together: sequence b's last
+    query_start[b + 1] - query_start[b] tokens are cut down to its num_kept[b]
+    tokens kept[b, :] (ascending, counted from the first of them). Caches as for
+    copy_blocks. Returns the lengths after it (seq_lens_out, allocated if not
+    given); kept_tokens [B], if given, receives them rounded up to whole blocks, as
+    pool_release's shared_tokens wants them to give the blocks behind them back."""
+    if seq_lens_out is None:
+        seq_lens_out = torch.empty_like(seq_lens)
+    _check(_native().pa_compact_cache(key_cache, value_cache, block_tables, seq_lens, query_start,
+                                      kept, num_kept, seq_lens_out, kept_tokens, int(block_size),
+                                      _handle(stream)))
+    return seq_lens_out
+
+
 def decode_noalloc(q, key_cache, value_cache, block_tables, seq_lens, *, num_kv_heads: int,
                    scale: float, block_size: int, out, window: int = 0, kv_dtype="auto",
                    k_scale: float = 1.0, v_scale: float = 1.0, stream=None):
@@ -372,6 +439,15 @@ def prefill_chunk_workspace_size(batch: int, num_queries: int, num_q_heads: int,
     n = ctypes.c_size_t(0)
     _check(lib().pa_prefill_chunk_workspace_size(batch, num_queries, num_q_heads, num_kv_heads,
                                                  head_dim, ctypes.byref(n)))
+    return n.value
+
+
+def packed_workspace_size(num_rows: int, batch: int, num_q_heads: int, num_kv_heads: int,
+                          head_dim: int) -> int:
+    """Workspace bytes of prefill_packed and decode_tree."""
+    n = ctypes.c_size_t(0)
+    _check(lib().pa_packed_workspace_size(num_rows, batch, num_q_heads, num_kv_heads, head_dim,
+                                          ctypes.byref(n)))
     return n.value
 
 

@@ -12,6 +12,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <functional>
 #include <initializer_list>
 #include <map>
 #include <mutex>
@@ -323,6 +324,9 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
+}  // namespace
+
+namespace pa {
 // 2-D view of a cache [NB * Hkv * bs rows, D]: box of 16 rows x 128 bytes,
 // 128-byte swizzle.
 pa_status make_cache_map(CUtensorMap* map, const void* base, int64_t rows, int D, int elt) {
@@ -349,6 +353,9 @@ pa_status make_cache_map(CUtensorMap* map, const void* base, int64_t rows, int D
   if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return PA_OK;
 }
+}  // namespace pa
+
+namespace {
 
 // ------------------------------------------------------------ dispatch glue
 
@@ -1281,6 +1288,27 @@ pa_status set_cuda_error(cudaError_t e, const char* what) { return cuda_fail(e, 
 }  // namespace pa
 
 namespace pa {
+pa_status with_workspace(cudaStream_t stream, size_t bytes, const std::function<pa_status(char*)>& body) {
+  DeviceState* st;
+  Workspace *w = nullptr, *again = nullptr;
+  std::unique_lock<std::mutex> order;
+  pa_status s;
+  do {  // (pa_set_workspace may come between the choice and the hold)
+    if (order.owns_lock()) order.unlock();
+    {
+      std::lock_guard<std::mutex> lk(g_mu);
+      if ((s = device_state(&st, nullptr)) || (s = pick_workspace(st, stream, &w))) return s;
+    }
+    order = std::unique_lock<std::mutex>(w->order);
+    std::lock_guard<std::mutex> lk(g_mu);
+    if ((s = pick_workspace(st, stream, &again))) return s;
+  } while (w != again);
+  WsLayout lay = {};
+  lay.plan = 256;
+  lay.total = bytes;
+  if ((s = ready_workspace(st, stream, lay, w))) return s;
+  return body(static_cast<char*>(w->ptr));
+}
 pa_status device_info(DeviceInfo* out) {
   std::lock_guard<std::mutex> lk(g_mu);
   DeviceState* st;

@@ -3,9 +3,12 @@
 // throws; none touches the device except check_accessible and device_info.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
+#include <functional>
 #include <initializer_list>
 
 #include "pa.h"
@@ -35,5 +38,13 @@ struct DeviceInfo {
 };
 pa_status device_info(DeviceInfo* out);
 void count_launches(int n);
+
+// 2-D view of a cache for TMA: [rows, D], boxes of 16 rows x 128 bytes, 128-byte
+// swizzle.
+pa_status make_cache_map(CUtensorMap* map, const void* base, int64_t rows, int D, int elt);
+// Calls body with the workspace of the stream's steps (the caller's, or the stream's
+// own, made large enough), which no other host thread's step gets before body returns.
+// Its first 256 bytes are the decode kernels' counters and stay as they are.
+pa_status with_workspace(cudaStream_t stream, size_t bytes, const std::function<pa_status(char*)>& body);
 
 }  // namespace pa

@@ -145,6 +145,10 @@ PyMethodDef kMethods[] = {PA_WRAP(pa_reshape_and_cache),
                           PA_WRAP(pa_decode_noalloc),
                           PA_WRAP(pa_decode_shared),
                           PA_WRAP(pa_prefill_chunk),
+                          PA_WRAP(pa_prefill_packed),
+                          PA_WRAP(pa_decode_tree),
+                          PA_WRAP(pa_copy_blocks),
+                          PA_WRAP(pa_compact_cache),
                           {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_pa_torch", nullptr, -1, kMethods,

@@ -1,0 +1,1045 @@
+// Attention of a ragged step over the paged cache, on the 5th-generation tensor
+// cores: packed prompts and chunks (causal), and drafted trees (each row attends to
+// the cache before the drafted tokens and to its ancestors among them).
+//
+// The rows of an item (packed_plan.cuh) are the (token, head) pairs of a unit of one
+// sequence and one KV head, as matrix Q [rows x D]; with K/V tiles of kKv tokens,
+//   S = Q K^T,  P = 2^(S c - m),  O += P V,  l += sum P
+// with a running reference m per row, which moves only when a score exceeds it by
+// more than 2^8, and out = O / l.
+//
+// Roles: one warp streams K tiles and one V tiles through rings (TMA through the
+// block table), one thread issues every product, groups of four softmax warps serve a
+// 128-row tile each (one row a thread), and four warps stage Q and store the results,
+// so that a group goes on with its next item while the last one's output is written.
+// A job is the product of a row tile and a K/V tile; jobs alternate between the two
+// groups (a unit of more than 128 rows: each group has its rows and every tile; one of
+// at most 128: both groups have the same rows, each every other tile, joined by the
+// storing warps). The products run two jobs ahead of the softmax in S and follow it
+// in O, across items. head_dim 256 has one group, whose S has two buffers (its O fills
+// half of the tensor memory).
+//
+// Masks: a row's attended positions in a tile are a bit word per 32 tokens (a range,
+// and for a tree the ancestor bits moved to the tile); tiles that every row of a
+// warp attends to in full take no mask. V rows outside of the unit's range are zeroed,
+// as they may hold anything; where a tile is masked for some row, its V is looked
+// through for infinities and NaN, which a weight of zero would not keep out of the
+// other rows, and such a tile is added up without the tensor cores.
+//
+// FP8 caches: four warps turn each raw e4m3 tile into the f16 tile that the products
+// read (exact), in two buffers each for K and V; Q is rescaled per row by a power of
+// two to f16's range, which the row's score scale undoes.
+#include "attn_tc.cuh"
+#include "packed_ops.h"
+#include "pa_internal.h"
+#include "ptx.cuh"
+#include "tc.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kRows = 128;
+constexpr int kGroupThreads = 128;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint64_t kWaitNs = 2000000000ull;  // bound of every wait (2 s)
+constexpr uint64_t kDrainNs = 200000000ull;  // and of those after one ran out
+constexpr float kFloor = -3e38f;             // reference-max start
+constexpr float kRescaleAbove = 8.f;         // log2 units
+// f16 weights are 2^7 times as large against their reference: at most 2^15, and
+// subnormal below 2^-21 of it instead of 2^-14.
+constexpr float kF16Lift = 7.f;              // log2 units
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kMaxStages = 4;
+
+// Barriers: K and V rings (full, empty); per S buffer: computed, P written, product
+// with V complete; Q staged (items in turn) and done with; per group: last product of an item complete,
+// O and statistics read, statistics written; FP8: converted K and V (two buffers each)
+// written and read; per group: a tile's V looked through; the end.
+enum {
+  kBarKFull = 0,
+  kBarKEmpty = kBarKFull + kMaxStages,
+  kBarVFull = kBarKEmpty + kMaxStages,
+  kBarVEmpty = kBarVFull + kMaxStages,
+  kBarS = kBarVEmpty + kMaxStages,
+  kBarP = kBarS + 2,
+  kBarO = kBarP + 2,
+  kBarQFull = kBarO + 2,
+  kBarQFree = kBarQFull + 2,
+  kBarOFull = kBarQFree + 1,
+  kBarOFree = kBarOFull + 2,
+  kBarStat = kBarOFree + 2,
+  kBarCKFull = kBarStat + 2,
+  kBarCKFree = kBarCKFull + 2,
+  kBarCVFull = kBarCKFree + 2,
+  kBarCVFree = kBarCVFull + 2,
+  kBarLook = kBarCVFree + 2,
+  kBarDrain = kBarLook + 2,
+  kNumBars
+};
+
+template <int D, bool FP8>
+struct Cfg {
+  static constexpr int kGroups = packed_shape(D).rows;  // softmax groups
+  static constexpr int kKv = packed_shape(D).kv;        // tokens a tile
+  static constexpr int kSlices = kKv / 16;
+  static constexpr int kBoxes = D / 64;  // 64-dim boxes of a 16-bit tile
+  static constexpr int kKStages = FP8 ? 1 : (D == 64 ? 4 : 2), kVStages = FP8 ? 1 : (D == 64 ? 4 : 3);
+  static constexpr int kEpiWarp = 4 * kGroups, kConvWarp = kEpiWarp + 4,
+                       kMmaWarp = kConvWarp + (FP8 ? 4 : 0), kLoadK = kMmaWarp + 1, kLoadV = kMmaWarp + 2;
+  static constexpr int kThreads = (kMmaWarp + 4) * 32;  // (one warp idle: registers move by fours)
+  // Registers: what the block is launched with, and the shares of the softmax warps and
+  // of all others where each thread's part is too little for the softmax.
+  static constexpr int kGroupsAll = kThreads / 128;
+  static constexpr int kLaunchRegs = kThreads == 384 ? 168 : (kThreads == 512 ? 128 : 96);
+  static constexpr bool kSplitRegs = kThreads > 384;
+  static constexpr int kOtherRegs = kThreads == 640 ? 56 : 88;
+  static constexpr int kSoftmaxRegs = kThreads == 640 ? 152 : 168;
+  static_assert(!kSplitRegs || kGroups * kSoftmaxRegs + (kGroupsAll - kGroups) * kOtherRegs <=
+                                   kGroupsAll * kLaunchRegs, "registers of the block");
+  static constexpr uint32_t kQBox = kRows * 128, kQBytes = kBoxes * kQBox;  // one row tile's Q
+  static constexpr uint32_t kBox = kKv * 128, kTile = kBoxes * kBox;        // 16-bit K or V tile
+  static constexpr uint32_t kRawBoxes = FP8 ? D / 128 : kBoxes;             // 128-byte boxes
+  static constexpr uint32_t kRing = kRawBoxes * kBox;                       // ring tile
+  // small things first, then the tiles, which start on 1 KB
+  static constexpr uint32_t kBar = 0, kSlot = 8 * kNumBars, kSkip = kSlot + 8, kLook = kSkip + 8,
+                            kShift = kLook + 32,
+                            kStat = kShift + (FP8 ? 2 * kGroups * kRows : 0),
+                            kSmall = kStat + kGroups * 2 * kRows * 4;
+  static constexpr uint32_t kQ = (kSmall + 1023) / 1024 * 1024, kK = kQ + kGroups * kQBytes,
+                            kV = kK + kKStages * kRing, kKc = kV + kVStages * kRing,
+                            kVc = kKc + (FP8 ? 2 * kTile : 0), kBytes = kVc + (FP8 ? 2 * kTile : 0);
+  static constexpr uint32_t kColS = 0, kColO = 2 * kKv;
+  static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
+  static_assert(kColO + kGroups * D <= kTmemCols, "tensor memory");
+};
+
+__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity) {
+  return mbar_wait_bounded(bar, parity & 1, kWaitNs);
+}
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity) {
+  return __all_sync(kFull, wait_one(bar, parity));
+}
+
+// Stage and phase of a ring position.
+struct Ring {
+  int stage = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// The items of this CTA, in order.
+struct Items {
+  const PackedItem* at;
+  int count, whole, ctas;
+  __device__ __forceinline__ Items(const int32_t* plan, int n) {
+    const PackedItem* items = reinterpret_cast<const PackedItem*>(plan + packed_items_at(n));
+    ctas = n;
+    whole = plan[kPkWhole];
+    const int w = blockIdx.x;
+    if (whole) {  // dealt out there and back
+      const int total = plan[kPkItems], rounds = total / n, left = total - rounds * n;
+      at = items;
+      count = rounds + (((rounds & 1) ? n - 1 - w : w) < left ? 1 : 0);
+    } else {
+      const int2 c = reinterpret_cast<const int2*>(plan + packed_ctas_at())[w];
+      at = items + c.x;
+      count = c.y - c.x;
+    }
+  }
+  __device__ __forceinline__ PackedItem get(int k) const {
+    const int w = blockIdx.x;
+    const int4* p = reinterpret_cast<const int4*>(at + (whole ? k * ctas + ((k & 1) ? ctas - 1 - w : w) : k));
+    const int4 x = p[0], y = p[1], z = p[2];
+    return PackedItem{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
+  }
+};
+
+template <int QT>
+__device__ __forceinline__ float f32_of(uint32_t w, int hi) {
+  const uint16_t v = static_cast<uint16_t>(hi ? w >> 16 : w & 0xffffu);
+  return QT == kBF16 ? __uint_as_float(static_cast<uint32_t>(v) << 16)
+                     : __half2float(__ushort_as_half(v));
+}
+// Element `hi` of a pair of 16-bit values of the products' type.
+template <bool BF16>
+__device__ __forceinline__ float op_f32(uint32_t w, int hi) {
+  return f32_of<BF16 ? kBF16 : kF16>(w, hi);
+}
+// Whether one of a pair's exponents is all ones (an infinity or NaN), in bits 15, 31.
+template <bool BF16>
+__device__ __forceinline__ uint32_t nonfinite(uint32_t w) {
+  constexpr uint32_t m = BF16 ? 0x7f807f80u : 0x7c007c00u, one = BF16 ? 0x00800080u : 0x04000400u;
+  return ((w & m) + one) & 0x80008000u;
+}
+__device__ __forceinline__ void lds_f32x2(uint32_t addr, float& a, float& b) {
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(a), "=f"(b) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void sts_f32x2(uint32_t addr, float a, float b) {
+  asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
+}
+__device__ __forceinline__ void sts_b32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void sts_s8(uint32_t addr, int v) {
+  asm volatile("st.shared.s8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ int lds_s8(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared.s8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+// Low k bits (none for k <= 0, all for k >= 32).
+__device__ __forceinline__ uint32_t below(int k) {
+  return k <= 0 ? 0u : (k >= 32 ? 0xffffffffu : (1u << k) - 1u);
+}
+
+template <int QT, int D, bool FP8>
+__global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
+    packed_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK,
+                          const __grid_constant__ CUtensorMap tmV, const PackedArgs a) {
+  using C = Cfg<D, FP8>;
+  constexpr bool kBf16 = !FP8 && QT == kBF16;  // operand type of the products
+  constexpr float kLift = kBf16 ? 0.f : kF16Lift;
+  constexpr int NX = C::kGroups, KV = C::kKv;
+  // Positions of the K and V tiles in use, and the barriers that say they are ready:
+  // the ring's, or the converted buffers' (two of each).
+  constexpr int KB = FP8 ? 2 : C::kKStages, VB = FP8 ? 2 : C::kVStages;
+  constexpr int kKReady = FP8 ? kBarCKFull : kBarKFull, kKFree = FP8 ? kBarCKFree : kBarKEmpty;
+  constexpr int kVReady = FP8 ? kBarCVFull : kBarVFull, kVFree = FP8 ? kBarCVFree : kBarVEmpty;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t base = smem_addr(smem_raw);
+  const uint32_t sQ = base + C::kQ, sK = base + C::kK, sV = base + C::kV;
+  const uint32_t sKc = base + C::kKc, sVc = base + C::kVc;
+  const uint32_t sVt = FP8 ? sVc : sV;  // 16-bit V tiles
+  auto bar = [&](int i) -> uint32_t { return base + C::kBar + 8u * i; };
+  const uint32_t* tslot = reinterpret_cast<const uint32_t*>(smem_raw + C::kSlot);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (base & 1023u) {  // the tiles would be misplaced (not so without static shared memory)
+    if (tid == 0) atomicOr(a.err, PA_DEVERR_TIMEOUT);
+    return;
+  }
+  if (tid == 0) {
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+    for (int i = 0; i < kMaxStages; ++i) {
+      mbar_init(bar(kBarKFull + i), 1);
+      mbar_init(bar(kBarKEmpty + i), FP8 ? 128 : 1);
+      mbar_init(bar(kBarVFull + i), 1);
+      mbar_init(bar(kBarVEmpty + i), FP8 ? 128 : 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kBarS + i), 1);
+      mbar_init(bar(kBarP + i), kGroupThreads);
+      mbar_init(bar(kBarO + i), 1);
+      mbar_init(bar(kBarOFull + i), 1);
+      mbar_init(bar(kBarOFree + i), 128);
+      mbar_init(bar(kBarStat + i), kGroupThreads);
+      mbar_init(bar(kBarCKFull + i), 128);
+      mbar_init(bar(kBarCKFree + i), 1);
+      mbar_init(bar(kBarCVFull + i), 128);
+      mbar_init(bar(kBarCVFree + i), 1);
+      mbar_init(bar(kBarLook + i), 4);
+    }
+    mbar_init(bar(kBarQFull), 128);
+    mbar_init(bar(kBarQFull + 1), 128);
+    mbar_init(bar(kBarQFree), 1);
+    mbar_init(bar(kBarDrain), 1);
+    sts_b32(base + C::kSkip, 0);
+    sts_b32(base + C::kSkip + 4, 0);
+    fence_mbar_init();
+  }
+  if (warp == 0) tc::tmem_alloc(base + C::kSlot, kTmemCols);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tslot;
+  griddep_wait();  // the plan, and behind it the caches and queries, are written
+  griddep_launch_dependents();
+  const Items items(a.plan, a.ctas);
+
+  // An item with more tokens than a row tile has rows for both groups.
+  auto is_dual = [&](const PackedItem& it) { return NX == 2 && it.ntok > a.tpg; };
+  auto jobs_of = [&](const PackedItem& it) { return is_dual(it) ? 2 * it.nt : it.nt; };
+
+  if (warp >= C::kMmaWarp) {
+    if constexpr (C::kSplitRegs)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+    if (warp == C::kLoadK || warp == C::kLoadV) {
+      // ------------------------------------------------------------ producers
+      // Lanes 0..kSlices-1 each look up one 16-token slice of a tile in the block
+      // table and copy its 128-byte boxes; slices behind the range are not loaded.
+      const bool is_v = warp == C::kLoadV;
+      const CUtensorMap* map = is_v ? &tmV : &tmK;
+      const int stages = is_v ? C::kVStages : C::kKStages;
+      const uint32_t dst0 = (is_v ? sV : sK) + lane * 2048;
+      const int full0 = is_v ? kBarVFull : kBarKFull, empty0 = is_v ? kBarVEmpty : kBarKEmpty;
+      bool ok = true;
+      Ring r;
+      int c = 0;  // tiles so far
+      for (int k = 0; ok && k < items.count; ++k) {
+        const PackedItem it = items.get(k);
+        const int32_t* table = a.block_tables + static_cast<size_t>(it.b) * a.MB;
+        auto row_of = [&](int n) -> int {
+          const int pos0 = (it.lo & ~15) + (it.tile0 + n) * KV + 16 * lane;
+          if (lane >= C::kSlices || pos0 > it.hi || n >= it.nt) return -1;
+          const int lb = pos0 / a.bs;
+          int blk = table[lb];
+          if (static_cast<unsigned>(blk) >= static_cast<unsigned>(a.NB)) {
+            atomicOr(a.err, PA_DEVERR_BLOCK_ID);
+            blk = 0;
+          }
+          return (blk * a.Hkv + it.kvh) * a.bs + (pos0 - lb * a.bs);
+        };
+        int row = row_of(0);
+        for (int n = 0; n < it.nt; ++n, ++c) {
+          const int next = row_of(n + 1);  // looked up while the wait below runs
+          if (c >= stages && !(ok = wait_all(bar(empty0 + r.stage), r.phase ^ 1))) break;
+          const uint32_t full = bar(full0 + r.stage);
+          const int nslices = __popc(__ballot_sync(kFull, row >= 0));
+          if (lane == 0) mbar_arrive_expect_tx(full, nslices * C::kRawBoxes * 2048);
+          __syncwarp();
+          if (row >= 0) {
+            const uint32_t dst = dst0 + r.stage * C::kRing;
+#pragma unroll
+            for (int box = 0; box < static_cast<int>(C::kRawBoxes); ++box)
+              tma_load_2d(dst + box * C::kBox, map, box * (FP8 ? 128 : 64), row, full);
+          }
+          __syncwarp();
+          r.next(stages);
+          row = next;
+        }
+      }
+      if (!ok) {
+        if (lane == 0) atomicOr(a.err, PA_DEVERR_TIMEOUT);
+        for (int i = max(c - stages, 0); i < c; ++i)  // no copy outlives the CTA
+          (void)mbar_wait_bounded(bar(full0 + i % stages), (i / stages) & 1, kDrainNs);
+      }
+    } else if (warp == C::kMmaWarp) {
+      // ------------------------------------------------------------ MMA issue
+      // One thread does all of it: its own instructions are on the critical path.
+      if (lane == 0) {
+        constexpr uint32_t idS = tc::idesc_f16(kRows, KV, kBf16, false);
+        constexpr uint32_t idO = tc::idesc_f16(kRows, D, kBf16, true);
+        const uint64_t dQ = tc::sdesc_sw128(sQ, 16, 1024);
+        const uint64_t dK = tc::sdesc_sw128(FP8 ? sKc : sK, 16, 1024);
+        const uint64_t dV = tc::sdesc_sw128(sVt, C::kBox, 1024);
+        // A place in the sequence of jobs of all items.
+        struct Cursor {
+          int k = -1, j = 0, jobs = 0;  // item, job of it, its jobs
+          bool dual = false;
+        };
+        auto settle = [&](Cursor& c) {  // the next job, skipping items without any
+          while (c.j == c.jobs && c.k < items.count) {
+            if (++c.k < items.count) {
+              const PackedItem it = items.get(c.k);
+              c.dual = is_dual(it);
+              c.jobs = jobs_of(it);
+              c.j = 0;
+            }
+          }
+          return c.k < items.count;
+        };
+        bool ok = true;
+        Cursor sc, oc;
+        Ring kr, vr;
+        uint32_t sjobs = 0, ojobs = 0, sitems = 0;
+        uint32_t o_items[2] = {0, 0};  // items begun in each group's O
+        int k_done = 0, v_done = 0;    // releases committed
+        // S of the next job, where there is one.
+        auto step_s = [&]() {
+          if (!settle(sc)) return;
+          const int x = sjobs & 1;
+          if (sc.j == 0 && !(ok = wait_one(bar(kBarQFull + (sitems & 1)), sitems >> 1))) return;
+          const bool first_use = !sc.dual || !(sc.j & 1), last_use = !sc.dual || (sc.j & 1);
+          if (first_use && !(ok = wait_one(bar(kKReady + kr.stage), kr.phase))) return;
+          // the buffer's last P has been used
+          if (sjobs >= 2 && !(ok = wait_one(bar(kBarO + x), (sjobs - 2) >> 1))) return;
+          tc::fence_after_sync();
+          const uint64_t q = dQ + (sc.dual && x ? C::kQBytes >> 4 : 0);
+#pragma unroll
+          for (int box = 0; box < C::kBoxes; ++box)
+            mma4_ss(tmem + C::kColS + KV * x, q + ((box * C::kQBox) >> 4),
+                    dK + ((kr.stage * C::kTile + box * C::kBox) >> 4), idS, box > 0);
+          tc::commit(bar(kBarS + x));
+          if (last_use) {
+            tc::commit(bar(kKFree + kr.stage));
+            kr.next(KB);
+            ++k_done;
+          }
+          ++sjobs;
+          if (++sc.j == sc.jobs) {
+            tc::commit(bar(kBarQFree));
+            ++sitems;
+          }
+        };
+        // O of the next job.
+        bool begun[2] = {false, false};  // O of each group holds something of this item
+        auto step_o = [&]() {
+          const int x = ojobs & 1, g = NX == 2 ? x : 0;
+          const bool first_use = !oc.dual || !(oc.j & 1), last_use = !oc.dual || (oc.j & 1);
+          if (!(ok = wait_one(bar(kBarP + x), ojobs >> 1))) return;
+          if (first_use && !(ok = wait_one(bar(kVReady + vr.stage), vr.phase))) return;
+          if (!begun[g]) {  // the last item's result has been read
+            if (o_items[g] > 0 && !(ok = wait_one(bar(kBarOFree + g), o_items[g] - 1))) return;
+            ++o_items[g];
+          }
+          tc::fence_after_sync();
+          volatile uint32_t* skip = reinterpret_cast<volatile uint32_t*>(smem_raw + C::kSkip) + x;
+          if (*skip) {  // the group has added this tile itself
+            *skip = 0;
+          } else {
+#pragma unroll
+            for (int h = 0; h < KV / 64; ++h)
+              mma4_ts(tmem + C::kColO + D * g, tmem + C::kColS + KV * x + 64 * h,
+                      dV + ((vr.stage * C::kTile) >> 4) + 512 * h, idO, begun[g] || h > 0);
+          }
+          begun[g] = true;
+          tc::commit(bar(kBarO + x));
+          if (last_use) {
+            tc::commit(bar(kVFree + vr.stage));
+            vr.next(VB);
+            ++v_done;
+          }
+          ++ojobs;
+          ++oc.j;
+          // the last job of a group in this item: the last two jobs, or the last one
+          if (oc.j == oc.jobs) {
+            if (NX == 2 && oc.jobs > 1) tc::commit(bar(kBarOFull + (x ^ 1)));
+            tc::commit(bar(kBarOFull + g));
+            begun[0] = begun[1] = false;
+          }
+        };
+        step_s();
+        if (ok) step_s();
+        while (ok && settle(oc)) {
+          step_o();
+          if (ok) step_s();
+        }
+        // no product and no arrival outlives the CTA
+        if (!ok) atomicOr(a.err, PA_DEVERR_TIMEOUT);
+        const uint64_t limit = ok ? kWaitNs : kDrainNs;
+        tc::commit(bar(kBarDrain));
+        (void)mbar_wait_bounded(bar(kBarDrain), 0, limit);
+        for (int i = 0; i < KB && i < k_done; ++i)
+          (void)mbar_wait_bounded(bar(kKFree + i), ((k_done - 1 - i) / KB) & 1, limit);
+        for (int i = 0; i < VB && i < v_done; ++i)
+          (void)mbar_wait_bounded(bar(kVFree + i), ((v_done - 1 - i) / VB) & 1, limit);
+      }
+      __syncwarp();
+    }
+  } else if (FP8 && warp >= C::kConvWarp) {
+    if constexpr (C::kSplitRegs)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+    // -------------------------------------------------------------- FP8 converters
+    // e4m3 tile -> the f16 buffer: a 16-byte chunk of 16 codes becomes two 16-byte
+    // chunks of f16 in the 64-dim box that holds them; V rows outside of the unit's
+    // range become zeros.
+    if constexpr (FP8) {
+      constexpr int kChunks = D / 16, kPer = 32 / kChunks;  // chunks a row, rows a pass
+      constexpr int kOctets = KV / 8;                       // of rows: a warp takes every fourth
+      const int o0 = warp - C::kConvWarp;
+      const int ch = lane % kChunks, q0 = lane / kChunks;
+      const int c16 = 2 * (ch & 3);
+      // rows [r_lo, r_hi) are converted, the others become zeros
+      auto convert = [&](uint32_t src, uint32_t dst, int r_lo, int r_hi) {
+        src += (ch >> 3) * C::kBox;
+        dst += (ch >> 2) * C::kBox;
+        static_assert(8 % kPer == 0, "passes of a row octet");
+#pragma unroll 1
+        for (int p = 0; p < 8 / kPer; ++p) {
+          const int r0 = 8 * o0 + q0 + kPer * p;  // rows r0, r0 + 32, ... share one swizzle
+          const uint32_t from = src + r0 * 128 + (((ch & 7) ^ (r0 & 7)) << 4);
+          const uint32_t lo = dst + r0 * 128 + ((c16 ^ (r0 & 7)) << 4);
+          const uint32_t hi = dst + r0 * 128 + (((c16 + 1) ^ (r0 & 7)) << 4);
+#pragma unroll
+          for (int k = 0; k < kOctets; k += 4) {
+            uint32_t w[4] = {0u, 0u, 0u, 0u}, h[8];
+            if (r0 + 8 * k >= r_lo && r0 + 8 * k < r_hi) lds_v4(from + 1024 * k, w[0], w[1], w[2], w[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              h[2 * i] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] & 0xffffu));
+              h[2 * i + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] >> 16));
+            }
+            sts_v4(lo + 1024 * k, make_uint4(h[0], h[1], h[2], h[3]));
+            sts_v4(hi + 1024 * k, make_uint4(h[4], h[5], h[6], h[7]));
+          }
+        }
+      };
+      bool ok = true;
+      int c = 0;
+      for (int k = 0; ok && k < items.count; ++k) {
+        const PackedItem it = items.get(k);
+        for (int n = 0; ok && n < it.nt; ++n, ++c) {
+          const int t0 = (it.lo & ~15) + (it.tile0 + n) * KV;
+          const uint32_t free_par = (c - 2) >> 1;  // of the buffers' last tile
+          if (!(ok = wait_all(bar(kBarKFull), c))) break;
+          if (c > 1 && !(ok = wait_all(bar(kBarCKFree + (c & 1)), free_par))) break;
+          convert(sK, sKc + (c & 1) * C::kTile, 0, KV);
+          fence_proxy_async();  // the f16 tile, visible to the tensor core
+          mbar_arrive(bar(kBarCKFull + (c & 1)));
+          mbar_arrive(bar(kBarKEmpty));  // reload the stage
+          if (!(ok = wait_all(bar(kBarVFull), c))) break;
+          if (c > 1 && !(ok = wait_all(bar(kBarCVFree + (c & 1)), free_par))) break;
+          convert(sV, sVc + (c & 1) * C::kTile, it.lo - t0, it.hi + 1 - t0);
+          fence_proxy_async();
+          mbar_arrive(bar(kBarCVFull + (c & 1)));
+          mbar_arrive(bar(kBarVEmpty));
+        }
+      }
+      if (!ok && lane == 0) atomicOr(a.err, PA_DEVERR_TIMEOUT);
+    }
+  } else if (warp >= C::kEpiWarp) {
+    if constexpr (C::kSplitRegs)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+    // ---------------------------------------------------- queries in, results out
+    const int wr0 = (warp - C::kEpiWarp) * 32;  // first row of this warp
+    const int r = wr0 + lane;                   // row = tensor-memory lane
+    const uint32_t trow = tmem + (static_cast<uint32_t>(wr0) << 16);
+    constexpr int kCh = D / 8, kPer = 32 / kCh;  // 16-byte chunks a row, rows at once
+    const int sub_r = lane / kCh, ch = lane % kCh;
+    const uint32_t mul = (65536u + a.G - 1) / a.G;  // row / G = row * mul >> 16, rows < 256
+    const int tok_r = static_cast<int>((r * mul) >> 16), head_r = r - tok_r * a.G;
+    // Q rows of an item -> shared memory (K-major, 128-byte swizzle); rows beside the
+    // unit's are zeros, up to whole warps.
+    const uint32_t flip = a.score_scale < 0.f ? 0x80008000u : 0u;
+    auto stage_q = [&](const PackedItem& it, uint32_t which) {
+      const int tiles = is_dual(it) ? 2 : 1;
+      for (int xt = 0; xt < tiles; ++xt) {
+        const int rows = min(it.ntok - xt * a.tpg, a.tpg) * a.G;
+        if (wr0 >= rows) continue;
+        const uint32_t q_tile = sQ + xt * C::kQBytes + (ch >> 3) * C::kQBox;
+        const uint16_t* q0 = static_cast<const uint16_t*>(a.q) +
+                             static_cast<size_t>(it.row0 + xt * a.tpg) * a.q_stride +
+                             static_cast<size_t>(it.kvh) * a.G * D;
+        constexpr int kBatch = kCh < 8 ? kCh : 8;  // loads in flight
+#pragma unroll 1
+        for (int i0 = 0; i0 < kCh; i0 += kBatch) {
+          uint4 v[kBatch];
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int rr = wr0 + (i0 + i) * kPer + sub_r;
+            const int t = static_cast<int>((rr * mul) >> 16), h = rr - t * a.G;
+            v[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (rr < rows)
+              v[i] = reinterpret_cast<const uint4*>(q0 + t * a.q_stride + h * D)[ch];
+          }
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int rr = wr0 + (i0 + i) * kPer + sub_r;
+            if constexpr (FP8) {
+              // f16 after a power-of-two rescale: largest magnitude in [2^14, 2^15)
+              const uint32_t w4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+              float amax = 0.f;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f32_of<QT>(w4[e >> 1], e & 1)));
+#pragma unroll
+              for (int o = kCh / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+              // 2^-sh from its exponent bits; below 2^-111 (scores that are zero for any
+              // weight) the largest stays under 2^14, as does zero
+              const int ex = static_cast<int>(__float_as_uint(amax) >> 23);  // 255: inf
+              const int sh = ex == 255 ? 0 : max(ex - 141, -126);
+              const float m = __int_as_float((127 - sh) << 23);
+              const float2 m2 = make_float2(m, m);
+              uint32_t o4[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 t = __fmul2_rn(make_float2(f32_of<QT>(w4[e], 0), f32_of<QT>(w4[e], 1)), m2);
+                o4[e] = pack16x2<false>(t.x, t.y);
+              }
+              v[i] = make_uint4(o4[0], o4[1], o4[2], o4[3]);
+              if (ch == 0) sts_s8(base + C::kShift + (which & 1) * NX * kRows + xt * kRows + rr, sh);
+            }
+            v[i].x ^= flip, v[i].y ^= flip, v[i].z ^= flip, v[i].w ^= flip;
+            sts_v4(q_tile + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4), v[i]);
+          }
+        }
+      }
+      fence_proxy_async();
+      mbar_arrive(bar(kBarQFull + (which & 1)));
+    };
+    bool ok = true;
+    uint32_t staged = 0, stored = 0;  // items with tiles so far
+    uint32_t o_items[2] = {0, 0};
+    uint32_t jobs = 0;
+    int kq = 0;  // next item whose Q is not staged
+    auto stage_next = [&]() {
+      while (kq < items.count) {
+        const PackedItem it = items.get(kq++);
+        if (it.nt == 0) continue;
+        if (staged > 0 && !(ok = wait_all(bar(kBarQFree), staged - 1))) return;
+        stage_q(it, staged);
+        ++staged;
+        return;
+      }
+    };
+    stage_next();
+    for (int k = 0; ok && k < items.count; ++k) {
+      const PackedItem it = items.get(k);
+      const bool dual = is_dual(it);
+      const int nj = jobs_of(it);
+      const uint32_t s = jobs & 1;  // group of the item's first job
+      jobs += nj;
+      if (nj > 0) {
+        stage_next();
+        if (!ok) break;
+        ++stored;
+      }
+      const int tiles = dual ? 2 : 1;
+      float* const part = a.part + static_cast<size_t>(max(it.slot, 0)) * packed_slot_floats(a.slot_rows, D);
+      const int g0 = NX == 2 ? static_cast<int>(s) : 0;  // the group with the first job
+      const bool both = NX == 2 && nj > 1;
+      // both groups' results of this item are complete
+      if (nj > 0) {
+        for (int q = 0; q < (both ? 2 : 1); ++q) {
+          const int g = g0 ^ q;
+          if (!(ok = wait_all(bar(kBarOFull + g), o_items[g]))) break;
+          if (!(ok = wait_all(bar(kBarStat + g), o_items[g]))) break;
+          ++o_items[g];
+        }
+        if (!ok) break;
+        tc::fence_after_sync();
+      }
+      for (int xt = 0; xt < tiles; ++xt) {
+        const int rows = min(it.ntok - xt * a.tpg, a.tpg) * a.G;
+        if (wr0 >= rows) continue;
+        const bool valid = r < rows;
+        const int ga = dual ? xt : g0;       // the group whose O holds these rows
+        const bool join = both && !dual;     // and the other one
+        float m = kFloor, l = 0.f, f_own = 0.f, f_other = 0.f;
+        if (nj > 0) {
+          lds_f32x2(base + C::kStat + (ga * kRows + r) * 8, m, l);
+          f_own = 1.f;
+          if (join) {
+            float m1, l1;
+            lds_f32x2(base + C::kStat + ((ga ^ 1) * kRows + r) * 8, m1, l1);
+            const float top = fmaxf(m, m1);
+            f_own = ex2(m - top);
+            f_other = ex2(m1 - top);
+            l = l * f_own + l1 * f_other;
+            m = top;
+          }
+        }
+        const bool direct = it.slot < 0;
+        // an empty row is zeros; a NaN in the sum stays one
+        const float inv = direct ? (l == 0.f ? 0.f : a.v_scale / l) : a.v_scale;
+        f_own *= inv;
+        f_other *= inv;
+        uint16_t* const out = static_cast<uint16_t*>(a.out) +
+                              static_cast<size_t>(it.row0 + xt * a.tpg + tok_r) * a.out_stride +
+                              static_cast<size_t>(it.kvh * a.G + head_r) * D;
+        const int slot_row = xt * kRows + r;
+        float* const prow = part + static_cast<size_t>(slot_row) * D;
+#pragma unroll 1
+        for (int d0 = 0; d0 < D; d0 += 16) {
+          uint32_t ov[16];
+          float o[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = 0.f;
+          if (nj > 0) {
+            tc::ld16(trow + C::kColO + D * ga + d0, ov);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(ov[i]) * f_own;
+            if (join) {
+              tc::ld16(trow + C::kColO + D * (ga ^ 1) + d0, ov);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = fmaf(__uint_as_float(ov[i]), f_other, o[i]);
+            }
+          }
+          if (direct) {
+            // (a row that attends to nothing: whatever O holds)
+            if (l == 0.f)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = 0.f;
+            if (valid) {
+              uint4* dst = reinterpret_cast<uint4*>(out + d0);
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                dst[c] = make_uint4(pack16x2<QT == kBF16>(o[8 * c], o[8 * c + 1]),
+                                    pack16x2<QT == kBF16>(o[8 * c + 2], o[8 * c + 3]),
+                                    pack16x2<QT == kBF16>(o[8 * c + 4], o[8 * c + 5]),
+                                    pack16x2<QT == kBF16>(o[8 * c + 6], o[8 * c + 7]));
+            }
+          } else if (valid) {
+            float4* dst = reinterpret_cast<float4*>(prow + d0);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) dst[c] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+          }
+        }
+        if (!direct && valid) {
+          float* stat = part + static_cast<size_t>(a.slot_rows) * D + slot_row;
+          stat[0] = m - kLift;
+          stat[a.slot_rows] = l;
+        }
+      }
+      if (nj > 0) {
+        tc::fence_before_sync();
+        mbar_arrive(bar(kBarOFree + g0));
+        if (both) mbar_arrive(bar(kBarOFree + (g0 ^ 1)));
+      }
+    }
+    if (!ok && lane == 0) atomicOr(a.err, PA_DEVERR_TIMEOUT);
+  } else {
+    // ---------------------------------------------------------------- softmax
+    if constexpr (C::kSplitRegs)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
+    const int x = warp >> 2;        // group
+    const int r = tid - x * kRows;  // row of the tile = tensor-memory lane
+    const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t tO = trow + C::kColO + D * x;
+    const int tok_r = r / a.G;
+    bool ok = true;
+    uint32_t jobs = 0;   // of all items before
+    uint32_t mine = 0;   // of this group
+    uint32_t done = 0;   // items of this group
+    uint32_t live = 0;   // items with tiles
+    uint32_t tiles = 0;  // K/V tiles of the items before
+    uint32_t looks = 0;  // tiles whose V was looked through
+    for (int k = 0; ok && k < items.count; ++k) {
+      const PackedItem it = items.get(k);
+      const bool dual = is_dual(it);
+      const int nj = jobs_of(it);
+      if (nj == 0) continue;
+      const int s = jobs & 1;  // S buffer (and group) of the item's first job
+      jobs += nj;
+      // this group's jobs: every one (one group), or those of its parity
+      const int j0 = NX == 2 ? (s ^ x) : 0, step = NX == 2 ? 2 : 1;
+      const uint32_t which = live++;
+      if (j0 >= nj) {
+        tiles += it.nt;
+        continue;
+      }
+      // this row
+      const int xt = dual ? x : 0;
+      const int tok = xt * a.tpg + tok_r;
+      const bool valid = tok_r < a.tpg && tok < it.ntok;
+      const bool alive = __any_sync(kFull, valid);
+      uint64_t bits = 0;
+      int hi_r, lo_r;  // the range that it attends to (a tree: before the drafted tokens)
+      if (a.tree) {
+        const int nb = it.hi + 1 - it.first;  // drafted tokens that have a bit
+        if (valid) bits = static_cast<uint64_t>(a.tree[it.row0 + tok]) & (nb >= 64 ? ~0ull : (1ull << nb) - 1);
+        const int p1 = it.first + __popcll(bits);  // its position + 1
+        hi_r = it.first - 1;
+        lo_r = a.window > 0 && p1 > a.window ? p1 - a.window : 0;
+      } else {
+        hi_r = it.pos0 + tok;
+        lo_r = a.window > 0 && hi_r + 1 > a.window ? hi_r + 1 - a.window : 0;
+      }
+      if (!valid) bits = 0, hi_r = -1, lo_r = 0;
+      // What all rows of the group attend to for sure, uniform over it: a tile inside
+      // takes no look through V.
+      const int last_tok = min(it.ntok, (xt + 1) * a.tpg) - 1;
+      const int sure_hi = a.tree ? it.first - 1 : it.pos0 + xt * a.tpg;
+      const int top = a.tree ? it.hi + 1 : it.pos0 + last_tok + 1;
+      const int sure_lo = a.window > 0 && top > a.window ? top - a.window : 0;
+      float sc = fabsf(a.score_scale);
+      if constexpr (FP8) {
+        if (!(ok = wait_all(bar(kBarQFull + (which & 1)), which >> 1))) break;
+        if (alive) sc = ldexpf(sc, lds_s8(base + C::kShift + (which & 1) * NX * kRows + xt * kRows + r));
+      }
+      float ms = kFloor, l = 0.f;  // reference max (scaled, log2 units) and running sum
+      for (int j = j0; j < nj; j += step, ++mine) {
+        const int n = dual ? j >> 1 : j;
+        const int t0 = (it.lo & ~15) + (it.tile0 + n) * KV;
+        const int buf = NX == 2 ? x : ((s + j) & 1);
+        const uint32_t phase = NX == 2 ? mine : mine >> 1;
+        // with one group, jobs alternate between the buffers from the very first one on
+        const uint32_t tS = trow + C::kColS + KV * buf;
+        if (!(ok = wait_all(bar(kBarS + buf), phase))) break;
+        tc::fence_after_sync();
+        const bool all_in = __all_sync(kFull, !valid || (t0 >= lo_r && t0 + KV - 1 <= hi_r));
+        uint32_t mask[KV / 32];
+#pragma unroll
+        for (int w = 0; w < KV / 32; ++w) {
+          mask[w] = below(hi_r + 1 - t0 - 32 * w) & ~below(lo_r - t0 - 32 * w);
+          const int sh = 32 * w + t0 - it.first;  // bit of this word's first token
+          if (sh > -32 && sh < 64)
+            mask[w] |= sh >= 0 ? static_cast<uint32_t>(bits >> sh) : static_cast<uint32_t>(bits << -sh);
+        }
+        auto word = [&](int hf, int i) -> uint32_t {  // bits of scores 64 hf + 32 i ...
+          if constexpr (KV == 64) return mask[i];
+          return hf ? mask[2 + i] : mask[i];
+        };
+        bool skip = false;
+        // A tile that some row does not attend to in full.
+        if (t0 < sure_lo || t0 + KV - 1 > sure_hi) {
+          const uint32_t c = tiles + n, stage = c % VB;
+          if (!(ok = wait_all(bar(kVReady + stage), c / VB))) break;
+          const uint32_t vt = sVt + stage * C::kTile;
+          uint32_t bad = 0;
+          if (r < KV) {
+            const int pos = t0 + r;
+            if (pos >= it.lo && pos <= it.hi) {
+#pragma unroll
+              for (int box = 0; box < C::kBoxes; ++box)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  uint32_t w[4];
+                  lds_v4(vt + box * C::kBox + r * 128 + ((i ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
+                  bad |= nonfinite<kBf16>(w[0]) | nonfinite<kBf16>(w[1]) | nonfinite<kBf16>(w[2]) |
+                         nonfinite<kBf16>(w[3]);
+                }
+            } else if (!FP8 && (!dual || !(j & 1))) {
+              // outside of the range: zeros, before the tile's first product
+#pragma unroll
+              for (int box = 0; box < C::kBoxes; ++box)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  sts_v4(vt + box * C::kBox + r * 128 + i * 16, make_uint4(0u, 0u, 0u, 0u));
+            }
+          }
+          fence_proxy_async();
+          // what any warp of the group has found
+          const uint32_t look = base + C::kLook + 16 * x;
+          const bool any_bad = __any_sync(kFull, bad != 0);
+          if (lane == 0) {
+            sts_b32(look + 4 * (warp & 3), any_bad ? 1u : 0u);
+            mbar_arrive(bar(kBarLook + x));
+          }
+          if (!(ok = wait_all(bar(kBarLook + x), looks++))) break;
+          uint32_t w[4];
+          lds_v4(look, w[0], w[1], w[2], w[3]);
+          skip = (w[0] | w[1] | w[2] | w[3]) != 0;
+        }
+        if (alive) {
+          uint32_t sv[2][32];
+          float mxp[8];  // eight independent partial maxima (raw scores)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) mxp[i] = -INFINITY;
+#pragma unroll 1
+          for (int hf = 0; hf < KV / 64; ++hf) {
+            tc::ld32_async(tS + 64 * hf, sv[0]);
+            tc::ld32_async(tS + 64 * hf + 32, sv[1]);
+            tc::wait_ld(sv[0], sv[1]);
+            if (all_in) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                mxp[i & 7] = fmax3(mxp[i & 7], __uint_as_float(sv[i >> 4][(2 * i) & 31]),
+                                   __uint_as_float(sv[i >> 4][(2 * i + 1) & 31]));
+            } else {
+              const uint32_t w0 = word(hf, 0), w1 = word(hf, 1);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const uint32_t w = i < 16 ? w0 : w1;
+                mxp[i & 7] = fmax3(mxp[i & 7],
+                                   (w >> ((2 * i) & 31)) & 1 ? __uint_as_float(sv[i >> 4][(2 * i) & 31]) : -INFINITY,
+                                   (w >> ((2 * i + 1) & 31)) & 1 ? __uint_as_float(sv[i >> 4][(2 * i + 1) & 31])
+                                                                 : -INFINITY);
+              }
+            }
+          }
+          const float mxr = fmaxf(fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])),
+                                  fmaxf(fmaxf(mxp[4], mxp[5]), fmaxf(mxp[6], mxp[7])));
+          const float mx = fmaxf(mxr * sc, kFloor);  // NaN (all masked, sc = 0) -> floor
+          const bool grow = mx > ms + kRescaleAbove;
+          const bool old = j != j0;  // O holds something
+          if (!old) {
+            ms = mx;
+          } else if (__any_sync(kFull, grow)) {
+            // O is complete up to the group's last job: with two groups S was issued
+            // after its product; one group has to wait for it
+            if (NX == 1) ok = wait_all(bar(kBarO + (buf ^ 1)), (mine - 1) >> 1);
+            tc::fence_after_sync();
+            const float alpha = grow ? ex2(ms - mx) : 1.f;
+#pragma unroll 1
+            for (int d0 = 0; d0 < D; d0 += 32) {
+              uint32_t ov[32];
+              tc::ld32_async(tO + d0, ov);
+              tc::wait_ld(ov);
+              const float2 a2 = make_float2(alpha, alpha);
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float2 o = __fmul2_rn(score_pair(ov, i), a2);
+                ov[i] = __float_as_uint(o.x);
+                ov[i + 1] = __float_as_uint(o.y);
+              }
+              tc::st32(tO + d0, ov);
+            }
+            l *= alpha;
+            if (grow) ms = mx;
+          }
+          if (skip) {
+            // Infinities or NaN in V: weights times rows on the CUDA cores, attended
+            // positions only.
+            const uint32_t vt = sVt + ((tiles + n) % VB) * C::kTile;
+            if (NX == 1 && old) ok = wait_all(bar(kBarO + (buf ^ 1)), (mine - 1) >> 1);
+            // (the item's first job: the storing warps have read the last item's O)
+            if (!old && done > 0) ok = wait_all(bar(kBarOFree + x), done - 1) && ok;
+            tc::fence_after_sync();
+#pragma unroll 1
+            for (int e0 = 0; e0 < KV; e0 += 32) {
+              tc::ld32_async(tS + e0, sv[0]);
+              tc::wait_ld(sv[0]);
+              uint32_t w = 0;
+#pragma unroll
+              for (int i = 0; i < KV / 32; ++i) w = e0 == 32 * i ? mask[i] : w;
+              float sum = 0.f;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float p = (w >> i) & 1 ? ex2(fmaf(__uint_as_float(sv[0][i]), sc, kLift - ms)) : 0.f;
+                sv[0][i] = __float_as_uint(p);
+                sum += p;
+              }
+              l += sum;
+#pragma unroll 1
+              for (int d0 = 0; d0 < D; d0 += 16) {
+                uint32_t ov[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) ov[i] = 0u;
+                if (old || e0 > 0) tc::ld16(tO + d0, ov);
+#pragma unroll 4
+                for (int e = 0; e < 32; ++e) {
+                  const bool on = (w >> e) & 1;
+                  if (!__any_sync(kFull, on)) continue;
+                  // (the weights sit in registers: a chain of selects picks one)
+                  float p = 0.f;
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) p = i == e ? __uint_as_float(sv[0][i]) : p;
+                  const int row = e0 + e;
+#pragma unroll
+                  for (int q = 0; q < 2; ++q) {
+                    uint32_t v[4];
+                    const int c = (d0 & 63) / 8 + q;
+                    lds_v4(vt + (d0 >> 6) * C::kBox + row * 128 + ((c ^ (row & 7)) << 4), v[0], v[1], v[2], v[3]);
+                    if (on) {
+#pragma unroll
+                      for (int i = 0; i < 8; ++i)
+                        ov[8 * q + i] = __float_as_uint(fmaf(p, op_f32<kBf16>(v[i >> 1], i & 1),
+                                                             __uint_as_float(ov[8 * q + i])));
+                    }
+                  }
+                }
+                tc::st16(tO + d0, ov);
+                tc::wait_st();
+              }
+            }
+            if (r == 0) sts_b32(base + C::kSkip + 4 * buf, 1u);
+          } else {
+            // P = 2^(s * sc - ms + kLift), packed in pairs over the columns of the scores
+            // just used; the last half is still in registers. It is rounded to the
+            // products' 16-bit type, which the tensor core needs beside V's, against sums
+            // in fp32 of the unrounded ones: at most 2^-8 of each weight for bf16, for f16
+            // 2^-11 of it and, where it is subnormal, 2^-32 of the reference's weight.
+            const float2 sc2 = make_float2(sc, sc), nms2 = make_float2(kLift - ms, kLift - ms);
+            float2 sp[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sp[i] = make_float2(0.f, 0.f);
+#pragma unroll 1
+            for (int hf = KV / 64 - 1; hf >= 0; --hf) {
+              if (hf != KV / 64 - 1) {
+                tc::ld32_async(tS + 64 * hf, sv[0]);
+                tc::ld32_async(tS + 64 * hf + 32, sv[1]);
+                tc::wait_ld(sv[0], sv[1]);
+              }
+              uint32_t pk[32];
+              if (all_in) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  const float2 t = __ffma2_rn(score_pair(sv[i >> 4], (2 * i) & 31), sc2, nms2);
+                  const float p0 = ex2(t.x), p1 = ex2(t.y);
+                  sp[i & 3] = __fadd2_rn(sp[i & 3], make_float2(p0, p1));
+                  pk[i] = pack16x2<kBf16>(p0, p1);
+                }
+              } else {  // masked scores give exactly 0
+                const uint32_t w0 = word(hf, 0), w1 = word(hf, 1);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  const uint32_t w = i < 16 ? w0 : w1;
+                  const float2 t = __ffma2_rn(score_pair(sv[i >> 4], (2 * i) & 31), sc2, nms2);
+                  const float p0 = (w >> ((2 * i) & 31)) & 1 ? ex2(t.x) : 0.f;
+                  const float p1 = (w >> ((2 * i + 1) & 31)) & 1 ? ex2(t.y) : 0.f;
+                  sp[i & 3] = __fadd2_rn(sp[i & 3], make_float2(p0, p1));
+                  pk[i] = pack16x2<kBf16>(p0, p1);
+                }
+              }
+              tc::st32(tS + 64 * hf, pk);
+            }
+            const float2 s01 = __fadd2_rn(sp[0], sp[1]), s23 = __fadd2_rn(sp[2], sp[3]);
+            const float2 st = __fadd2_rn(s01, s23);
+            l += st.x + st.y;
+          }
+        }
+        if (!ok) break;
+        tc::wait_st();
+        tc::fence_before_sync();
+        mbar_arrive(bar(kBarP + buf));
+      }
+      tiles += it.nt;
+      if (!ok) break;
+      // the statistics, once the last ones have been read
+      if (done > 0 && !(ok = wait_all(bar(kBarOFree + x), done - 1))) break;
+      sts_f32x2(base + C::kStat + (x * kRows + r) * 8, ms, l);
+      mbar_arrive(bar(kBarStat + x));
+      ++done;
+    }
+    if (!ok && lane == 0) atomicOr(a.err, PA_DEVERR_TIMEOUT);
+  }
+
+  // every product has completed (the issuing thread waited for them)
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 0) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int QT, int D, bool FP8>
+cudaError_t launch_typed(const CUtensorMap& tk, const CUtensorMap& tv, const PackedArgs& a,
+                         cudaStream_t s, bool pdl) {
+  using C = Cfg<D, FP8>;
+  // a function attribute of the current device's context: set every time, a host-side
+  // store
+  cudaError_t e = cudaFuncSetAttribute(packed_attn_tc_kernel<QT, D, FP8>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
+  if (e != cudaSuccess) return e;
+  if constexpr (C::kSplitRegs) {
+    // the softmax warps wait for registers that the block must have been given
+    static const int regs = [] {
+      cudaFuncAttributes f;
+      return cudaFuncGetAttributes(&f, packed_attn_tc_kernel<QT, D, FP8>) == cudaSuccess ? f.numRegs : 0;
+    }();
+    if (regs < C::kLaunchRegs) return cudaErrorLaunchOutOfResources;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.ctas);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, packed_attn_tc_kernel<QT, D, FP8>, tk, tv, a);
+}
+
+template <int QT>
+cudaError_t launch_dim(bool fp8, int D, const CUtensorMap& tk, const CUtensorMap& tv,
+                       const PackedArgs& a, cudaStream_t s, bool pdl) {
+  if (fp8) {
+    if (D == 128) return launch_typed<QT, 128, true>(tk, tv, a, s, pdl);
+    if (D == 256) return launch_typed<QT, 256, true>(tk, tv, a, s, pdl);
+    return cudaErrorInvalidValue;
+  }
+  if (D == 64) return launch_typed<QT, 64, false>(tk, tv, a, s, pdl);
+  if (D == 128) return launch_typed<QT, 128, false>(tk, tv, a, s, pdl);
+  if (D == 256) return launch_typed<QT, 256, false>(tk, tv, a, s, pdl);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t packed_launch(int qt, bool fp8, int D, const CUtensorMap& tk, const CUtensorMap& tv,
+                          const PackedArgs& a, cudaStream_t s, bool pdl) {
+  return qt == kBF16 ? launch_dim<kBF16>(fp8, D, tk, tv, a, s, pdl)
+                     : launch_dim<kF16>(fp8, D, tk, tv, a, s, pdl);
+}
+
+}  // namespace pa
