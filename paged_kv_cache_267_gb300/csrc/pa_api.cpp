@@ -326,21 +326,18 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 }  // namespace
 
-namespace pa {
-// 2-D view of a cache [NB * Hkv * bs rows, D]: box of 16 rows x 128 bytes,
-// 128-byte swizzle.
-pa_status make_cache_map(CUtensorMap* map, const void* base, int64_t rows, int D, int elt) {
+namespace {
+// Encodes a tiled map of 16-bit or byte elements with 128-byte swizzle.
+pa_status encode_map(CUtensorMap* map, int elt, int rank, const void* base, const cuuint64_t* dims,
+                     const cuuint64_t* strides, const cuuint32_t* box) {
   auto fn = encode_fn();
   if (!fn) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(D) * elt};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elt), static_cast<cuuint32_t>(pa::kTile)};
-  cuuint32_t estr[2] = {1, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
   auto encode = [&] {
-    return fn(map, elt == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
-              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return fn(map, elt == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
+              static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   };
   CUresult r = encode();
   if (r == CUDA_ERROR_INVALID_CONTEXT) {  // a host thread's first call: bind the device's context
@@ -352,6 +349,26 @@ pa_status make_cache_map(CUtensorMap* map, const void* base, int64_t rows, int D
   }
   if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return PA_OK;
+}
+}  // namespace
+
+namespace pa {
+// 2-D view of a cache [NB * Hkv * bs rows, D]: box of 16 rows x 128 bytes,
+// 128-byte swizzle.
+pa_status make_cache_map(CUtensorMap* map, const void* base, int64_t rows, int D, int elt) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(D) * elt};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elt), static_cast<cuuint32_t>(pa::kTile)};
+  return encode_map(map, elt, 2, base, dims, strides, box);
+}
+
+pa_status make_query_map(CUtensorMap* map, const void* base, int64_t T, int64_t Hq, int D,
+                         int64_t stride, int G, int tokens) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hq),
+                              static_cast<cuuint64_t>(T)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(tokens)};
+  return encode_map(map, 2, 3, base, dims, strides, box);
 }
 }  // namespace pa
 

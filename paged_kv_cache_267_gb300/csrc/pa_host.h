@@ -42,6 +42,10 @@ void count_launches(int n);
 // 2-D view of a cache for TMA: [rows, D], boxes of 16 rows x 128 bytes, 128-byte
 // swizzle.
 pa_status make_cache_map(CUtensorMap* map, const void* base, int64_t rows, int D, int elt);
+// 3-D view of packed query rows [T, Hq, D], rows `stride` elements apart: boxes of 64
+// head dims x G heads x `tokens` rows, 128-byte swizzle.
+pa_status make_query_map(CUtensorMap* map, const void* base, int64_t T, int64_t Hq, int D,
+                         int64_t stride, int G, int tokens);
 // Calls body with the workspace of the stream's steps (the caller's, or the stream's
 // own, made large enough), which no other host thread's step gets before body returns.
 // Its first 256 bytes are the decode kernels' counters and stay as they are.

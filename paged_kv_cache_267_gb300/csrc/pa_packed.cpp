@@ -20,9 +20,10 @@ using namespace pa;
 
 constexpr double k2p31 = 2147483648.0;
 constexpr int64_t kMaxRows = int64_t(1) << 30;
-// Split mode of a step (packed_plan.cuh): least tiles a CTA, and what the partial results
-// and their join cost in tiles of one CTA.
+// Costs of a step (packed_plan.cuh) in tiles of one CTA: least tiles a CTA in split mode,
+// an item's way in and out, the partial results of a split and their join.
 constexpr int kMinTiles = 2;
+constexpr int kUnitTiles = 1;
 constexpr int kSplitTiles = 4;
 
 bool misaligned(const pa_tensor* t, uintptr_t n) {
@@ -143,8 +144,9 @@ pa_status packed_attention(const pa_tensor* out, const pa_tensor* q, const pa_te
   if (misaligned(key_cache, 16) || misaligned(value_cache, 16))
     return fail(PA_ERR_LAYOUT, "caches must be 16-byte aligned");
   if ((s = check_rows(q, "q")) || (s = check_rows(out, "out"))) return s;
-  if (T > 1 && numel(out) > 0 && out->strides[0] < Hq * D)
-    return fail(PA_ERR_LAYOUT, "out: rows overlap");
+  for (const pa_tensor* x : {q, out})
+    if (T > 1 && numel(x) > 0 && x->strides[0] < Hq * D)
+      return fail(PA_ERR_LAYOUT, "rows of q or out overlap");
   if (!std::isfinite(scale)) return fail(PA_ERR_INVALID_ARG, "scale must be finite");
   if (fp8 && !(std::isfinite(k_scale) && std::isfinite(v_scale) && k_scale > 0 && v_scale > 0))
     return fail(PA_ERR_INVALID_ARG, "fp8 scales must be finite and positive");
@@ -159,7 +161,7 @@ pa_status packed_attention(const pa_tensor* out, const pa_tensor* q, const pa_te
   // of a unit: a window's reach and its own tokens (drafted ones: 64)
   const int64_t span = window > 0 ? std::min<int64_t>(MB * block_size, int64_t(window) + std::max<int64_t>(tpu, 64))
                                   : MB * block_size;
-  if (dprod({double(T / tpu + std::min(B, T)), double(Hkv), double(span / shape.kv + 2)}) >= k2p31 - 4096)
+  if (dprod({double(T / tpu + std::min(B, T)), double(Hkv), double(span / shape.kv + 8)}) >= k2p31 - 4096)
     return fail(PA_ERR_UNSUPPORTED, "rows times table width exceed 32-bit indexing");
   for (const pa_tensor* x : {q, key_cache, value_cache, block_tables, seq_lens, query_start, tree ? tree_mask : q})
     if (overlaps(out, x)) return fail(PA_ERR_INVALID_ARG, "out overlaps an input");
@@ -173,12 +175,14 @@ pa_status packed_attention(const pa_tensor* out, const pa_tensor* q, const pa_te
     if ((s = check_accessible(t, name))) return s;
   DeviceInfo dev;
   if ((s = device_info(&dev))) return s;
-  CUtensorMap tk, tv;
+  CUtensorMap tk, tv, tq;
   const int elt = fp8 ? 1 : 2;
   if ((s = make_cache_map(&tk, key_cache->data, NB * Hkv * block_size, static_cast<int>(D), elt)) ||
       (s = make_cache_map(&tv, value_cache->data, NB * Hkv * block_size, static_cast<int>(D), elt)))
     return s;
   const PackedSizes z = packed_sizes(T, B, span, G, Hkv, static_cast<int>(D), dev.num_sms);
+  if ((s = make_query_map(&tq, q->data, T, Hq, static_cast<int>(D), T > 1 ? q->strides[0] : Hq * D, G, z.tpg)))
+    return s;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   return with_workspace(cs, z.bytes, [&](char* ws) -> pa_status {
     PackedPlanArgs p;
@@ -196,6 +200,7 @@ pa_status packed_attention(const pa_tensor* out, const pa_tensor* q, const pa_te
     p.kv = z.kv;
     p.ctas = z.ctas;
     p.min_tiles = kMinTiles;
+    p.unit_tiles = kUnitTiles;
     p.split_tiles = kSplitTiles;
     p.tree = tree;
     cudaError_t e = packed_plan_launch(p, cs, true);
@@ -223,7 +228,7 @@ pa_status packed_attention(const pa_tensor* out, const pa_tensor* q, const pa_te
     a.score_scale = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634 *
                                        (fp8 ? static_cast<double>(k_scale) : 1.0));
     a.v_scale = fp8 ? v_scale : 1.f;
-    e = packed_launch(q->dtype, fp8, static_cast<int>(D), tk, tv, a, cs, true);
+    e = packed_launch(q->dtype, fp8, static_cast<int>(D), tk, tv, tq, a, cs, true);
     if (e != cudaSuccess) return cuda_fail(e, "packed attention launch");
     PackedMergeArgs m;
     m.out = out->data;

@@ -23,6 +23,7 @@ struct PackedPlanArgs {
   int kv;                       // tokens a K/V tile
   int ctas;                     // of the attention
   int min_tiles;                // least tiles a CTA in split mode
+  int unit_tiles;               // an item's way in and out, in tiles
   int split_tiles;              // what a split costs, in tiles of one CTA
   bool tree;
 };
@@ -44,7 +45,7 @@ struct PackedArgs {
   float v_scale;                // FP8: applied to the output
 };
 cudaError_t packed_launch(int qt, bool fp8, int D, const CUtensorMap& tk, const CUtensorMap& tv,
-                          const PackedArgs& a, cudaStream_t s, bool pdl);
+                          const CUtensorMap& tq, const PackedArgs& a, cudaStream_t s, bool pdl);
 
 struct PackedMergeArgs {
   void* out;

@@ -121,36 +121,36 @@ __global__ void __launch_bounds__(kThreads, 1) packed_plan_kernel(const PackedPl
     ctas[w] = make_int2(0, 0);
     joins[w].n = 0;
   }
-  int tiles = 0;  // of all units of one KV head
+  const int out = a.unit_tiles;
+  int places = 0;  // of all units of one KV head
   for (int u0 = 0; u0 < units; u0 += kThreads) {
     const int u = u0 + tid;
-    const int c = u < units ? max(unit(u).nt, 1) : 0;
+    const int c = u < units ? out + max(unit(u).nt, 1) : 0;
     scan(c, 0, add, &total);
-    tiles += total;
+    places += total;
     if (c > 0) atomicMax(&s_max, c);
   }
   __syncthreads();
   const int longest = s_max;
-  const long long all = static_cast<long long>(tiles) * a.Hkv;
+  const long long all = static_cast<long long>(places) * a.Hkv;
   const int nitems = units * a.Hkv;
-  // Whole units, or tiles split evenly? In tiles of one CTA: dealing out whole units
-  // takes the mean and about half of the longest unit, and not less than that; a
-  // split takes the mean and what the partial results and their join cost.
+  // Whole units, or tiles split evenly? A split takes every CTA the mean, and besides
+  // what the partial results and their join cost; whole units take as long as the
+  // CTA with the most, which is looked up once they are dealt out.
   const long long mean = (all + a.ctas - 1) / a.ctas;
-  const long long whole_cost = nitems <= a.ctas ? longest : max(static_cast<long long>(longest), mean + longest / 2);
-  const bool whole = whole_cost <= mean + a.split_tiles;
-  if (tid == 0) {
-    plan[kPkWhole] = whole;
-    plan[kPkItems] = nitems;
-  }
+  const long long split_cost = mean + a.split_tiles;
+  bool whole = longest <= split_cost;
   if (whole) {
     // sorted by tiles in kBins steps, most first
-    auto bin_of = [&](int nt) { return kBins - 1 - static_cast<int>(static_cast<long long>(nt) * (kBins - 1) / longest); };
+    auto bin_of = [&](int nt) {
+      return kBins - 1 - static_cast<int>(static_cast<long long>(nt) * (kBins - 1) / longest);
+    };
     for (int u = tid; u < units; u += kThreads) atomicAdd(&s_bin[bin_of(unit(u).nt)], 1);
     __syncthreads();
     const int n = tid < kBins ? s_bin[tid] : 0;
     const int y = scan(n, 0, add, &total);
     if (tid < kBins) s_bin[tid] = y - n;
+    if (tid == 0) s_max = 0;
     __syncthreads();
     for (int u = tid; u < units; u += kThreads) {
       PackedItem it = unit(u);
@@ -160,14 +160,29 @@ __global__ void __launch_bounds__(kThreads, 1) packed_plan_kernel(const PackedPl
         items[at * a.Hkv + h] = it;
       }
     }
-    return;
+    if (nitems > a.ctas) {
+      __syncthreads();
+      for (int w = tid; w < a.ctas; w += kThreads) {
+        int cost = 0;
+        for (int k = 0, i = w; i < nitems; ++k, i = k * a.ctas + ((k & 1) ? a.ctas - 1 - w : w))
+          cost += out + max(items[i].nt, 1);
+        atomicMax(&s_max, cost);
+      }
+      __syncthreads();
+      whole = s_max <= split_cost;
+      __syncthreads();  // before the items are written over
+    }
   }
+  if (tid == 0) {
+    plan[kPkWhole] = whole;
+    plan[kPkItems] = nitems;
+  }
+  if (whole) return;
   const int wsz = static_cast<int>(max(mean, static_cast<long long>(a.min_tiles)));
-  int before = 0;  // tiles of the passes before
-  __syncthreads();
+  int before = 0;  // places of the passes before
   for (int u0 = 0; u0 < units; u0 += kThreads) {
     const int nu = min(units - u0, kThreads);
-    const int c = tid < nu ? max(unit(u0 + tid).nt, 1) : 0;
+    const int c = tid < nu ? out + max(unit(u0 + tid).nt, 1) : 0;
     s_f[tid] = before + scan(c, 0, add, &total) - c;
     before += total;
     __syncthreads();
@@ -175,19 +190,21 @@ __global__ void __launch_bounds__(kThreads, 1) packed_plan_kernel(const PackedPl
       const int v = p / a.Hkv, h = p - v * a.Hkv;
       PackedItem it = unit(u0 + v);
       it.kvh = h;
-      const int cost = max(it.nt, 1), nt = it.nt;
-      const int f0 = s_f[v] * a.Hkv + h * cost, f1 = f0 + cost;  // (below 2^31: the host checks)
-      const int w0 = f0 / wsz, w1 = (f1 - 1) / wsz;
+      const int nt = it.nt, tiles = max(nt, 1);
+      const int f0 = s_f[v] * a.Hkv + h * (out + tiles);  // (below 2^31: the host checks)
+      const int g0 = f0 + out, f1 = g0 + tiles;           // its tiles, its end
+      const int w0 = g0 / wsz, w1 = (f1 - 1) / wsz;
       const int id = (u0 + v) * a.Hkv + h;
       for (int w = w0; w <= w1; ++w) {
-        const int from = max(f0, w * wsz), to = w == w1 ? f1 : (w + 1) * wsz;
-        it.tile0 = from - f0;
+        const int from = max(g0, w * wsz), to = w == w1 ? f1 : (w + 1) * wsz;
+        it.tile0 = from - g0;
         it.nt = nt == 0 ? 0 : to - from;
-        const bool opens = from == w * wsz;
+        const bool opens = f0 <= w * wsz;  // the CTA's first: nothing of it lies before
         it.slot = w0 == w1 ? -1 : 2 * w + (opens ? 0 : 1);
         items[id + w] = it;
         if (opens) ctas[w].x = id + w;
-        if (to == (w + 1) * wsz || to == all) ctas[w].y = id + w + 1;
+        // its last: the next unit's tiles begin behind its end
+        if (f1 + out >= (w + 1) * wsz || f1 == all) ctas[w].y = id + w + 1;
       }
       if (w0 != w1) {
         PackedJoin j;
@@ -195,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_plan_kernel(const PackedPl
         j.ntok = it.ntok;
         j.kvh = h;
         j.n = w1 - w0 + 1;
-        j.slot0 = 2 * w0 + (f0 == w0 * wsz ? 0 : 1);
+        j.slot0 = 2 * w0 + (f0 <= w0 * wsz ? 0 : 1);
         j.slot1 = 2 * (w0 + 1);
         j.pad[0] = j.pad[1] = 0;
         joins[w0] = j;

@@ -10,9 +10,10 @@
 //   - whole mode: every unit is one item; items are sorted by their tiles, most
 //     first, and dealt out to the CTAs there and back (0 .. C-1, C-1 .. 0, ...).
 //   - split mode: the tiles of all units form one flat index space, unit- then KV
-//     head-major, and CTA w takes [w * wsz, (w + 1) * wsz) of it. Item u + w is
-//     what CTA w has of unit u (counted over KV heads): unique, because the walk
-//     through the (unit, CTA) grid is a monotone staircase. A unit cut between CTAs
+//     head-major, with a few places before each unit's for its way in and out, and
+//     CTA w takes [w * wsz, (w + 1) * wsz) of it. Item u + w is what CTA w has of the
+//     tiles of unit u (counted over KV heads): unique, because the walk through the
+//     (unit, CTA) grid is a monotone staircase. A unit cut between CTAs
 //     leaves a partial result with each, in slot 2 w if it is CTA w's first item,
 //     else 2 w + 1 (its last); the merge joins them.
 // A unit that attends to nothing counts as one tile (its rows are zeros).

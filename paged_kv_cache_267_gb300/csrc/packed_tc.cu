@@ -8,15 +8,16 @@
 // with a running reference m per row, which moves only when a score exceeds it by
 // more than 2^8, and out = O / l.
 //
-// Roles: one warp streams K tiles and one V tiles through rings (TMA through the
-// block table), one thread issues every product, groups of four softmax warps serve a
-// 128-row tile each (one row a thread), and four warps stage Q and store the results,
+// Roles: one warp streams K tiles and one V tiles through rings (TMA through the block
+// table), one loads Q and issues the products S, one issues the products O, groups of four softmax
+// warps serve a 128-row tile each (one row a thread), and four warps store the results,
 // so that a group goes on with its next item while the last one's output is written.
+// (With one warp for all products, its own waits and instruction fetches, 700 cycles a job
+// beside 1,050 of tensor work, came in the way of both.)
 // A job is the product of a row tile and a K/V tile; jobs alternate between the two
 // groups (a unit of more than 128 rows: each group has its rows and every tile; one of
 // at most 128: both groups have the same rows, each every other tile, joined by the
-// storing warps). The products run two jobs ahead of the softmax in S and follow it
-// in O, across items. head_dim 256 has one group, whose S has two buffers (its O fills
+// storing warps). S runs two jobs ahead of the softmax, across items. head_dim 256 has one group, whose S has two buffers (its O fills
 // half of the tensor memory).
 //
 // Masks: a row's attended positions in a tile are a bit word per 32 tokens (a range,
@@ -27,8 +28,13 @@
 // other rows, and such a tile is added up without the tensor cores.
 //
 // FP8 caches: four warps turn each raw e4m3 tile into the f16 tile that the products
-// read (exact), in two buffers each for K and V; Q is rescaled per row by a power of
-// two to f16's range, which the row's score scale undoes.
+// read (exact), in two buffers each for K and V; Q goes through the storing warps, which
+// rescale it per row by a power of two to f16's range, which the row's score scale
+// undoes.
+#include <float.h>
+
+#include <type_traits>
+
 #include "attn_tc.cuh"
 #include "packed_ops.h"
 #include "pa_internal.h"
@@ -51,8 +57,8 @@ constexpr float kF16Lift = 7.f;              // log2 units
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kMaxStages = 4;
 
-// Barriers: K and V rings (full, empty); per S buffer: computed, P written, product
-// with V complete; Q staged (items in turn) and done with; per group: last product of an item complete,
+// Barriers: K and V rings (full, empty); per S buffer: computed, half of P written, the
+// other half, product with V complete; Q staged (items in turn) and done with; per group: last product of an item complete,
 // O and statistics read, statistics written; FP8: converted K and V (two buffers each)
 // written and read; per group: a tile's V looked through; the end.
 enum {
@@ -62,7 +68,8 @@ enum {
   kBarVEmpty = kBarVFull + kMaxStages,
   kBarS = kBarVEmpty + kMaxStages,
   kBarP = kBarS + 2,
-  kBarO = kBarP + 2,
+  kBarP2 = kBarP + 2,
+  kBarO = kBarP2 + 2,
   kBarQFull = kBarO + 2,
   kBarQFree = kBarQFull + 2,
   kBarOFull = kBarQFree + 1,
@@ -74,7 +81,7 @@ enum {
   kBarCVFree = kBarCVFull + 2,
   kBarLook = kBarCVFree + 2,
   kBarDrain = kBarLook + 2,
-  kNumBars
+  kNumBars = kBarDrain + 2
 };
 
 template <int D, bool FP8>
@@ -85,15 +92,19 @@ struct Cfg {
   static constexpr int kBoxes = D / 64;  // 64-dim boxes of a 16-bit tile
   static constexpr int kKStages = FP8 ? 1 : (D == 64 ? 4 : 2), kVStages = FP8 ? 1 : (D == 64 ? 4 : 3);
   static constexpr int kEpiWarp = 4 * kGroups, kConvWarp = kEpiWarp + 4,
-                       kMmaWarp = kConvWarp + (FP8 ? 4 : 0), kLoadK = kMmaWarp + 1, kLoadV = kMmaWarp + 2;
-  static constexpr int kThreads = (kMmaWarp + 4) * 32;  // (one warp idle: registers move by fours)
+                       kMmaS = kConvWarp + (FP8 ? 4 : 0), kLoadK = kMmaS + 2,  // (and O behind S)
+                       kLoadV = kMmaS + 3;
+  static constexpr int kThreads = (kMmaS + 4) * 32;
   // Registers: what the block is launched with, and the shares of the softmax warps and
   // of all others where each thread's part is too little for the softmax.
   static constexpr int kGroupsAll = kThreads / 128;
   static constexpr int kLaunchRegs = kThreads == 384 ? 168 : (kThreads == 512 ? 128 : 96);
   static constexpr bool kSplitRegs = kThreads > 384;
-  static constexpr int kOtherRegs = kThreads == 640 ? 56 : 88;
-  static constexpr int kSoftmaxRegs = kThreads == 640 ? 152 : 168;
+  static constexpr int kOtherRegs = kThreads == 640 ? 56 : (kGroups == 2 ? 64 : 104);
+  static constexpr int kSoftmaxRegs = kThreads == 640 ? 152 : 192;
+  // A row's scores of a tile stay in registers from the maximum to the weights; with
+  // fewer registers they are read from tensor memory 64 at a time, twice.
+  static constexpr bool kHeld = kKv == 64 || kThreads != 640;
   static_assert(!kSplitRegs || kGroups * kSoftmaxRegs + (kGroupsAll - kGroups) * kOtherRegs <=
                                    kGroupsAll * kLaunchRegs, "registers of the block");
   static constexpr uint32_t kQBox = kRows * 128, kQBytes = kBoxes * kQBox;  // one row tile's Q
@@ -101,7 +112,7 @@ struct Cfg {
   static constexpr uint32_t kRawBoxes = FP8 ? D / 128 : kBoxes;             // 128-byte boxes
   static constexpr uint32_t kRing = kRawBoxes * kBox;                       // ring tile
   // small things first, then the tiles, which start on 1 KB
-  static constexpr uint32_t kBar = 0, kSlot = 8 * kNumBars, kSkip = kSlot + 8, kLook = kSkip + 8,
+  static constexpr uint32_t kBar = 0, kSlot = (8 * kNumBars + 15) & ~15, kSkip = kSlot + 8, kLook = kSkip + 8,
                             kShift = kLook + 32,
                             kStat = kShift + (FP8 ? 2 * kGroups * kRows : 0),
                             kSmall = kStat + kGroups * 2 * kRows * 4;
@@ -109,6 +120,7 @@ struct Cfg {
                             kV = kK + kKStages * kRing, kKc = kV + kVStages * kRing,
                             kVc = kKc + (FP8 ? 2 * kTile : 0), kBytes = kVc + (FP8 ? 2 * kTile : 0);
   static constexpr uint32_t kColS = 0, kColO = 2 * kKv;
+  static_assert(kLook % 16 == 0 && kStat % 8 == 0, "alignment of what is read at once");
   static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
   static_assert(kColO + kGroups * D <= kTmemCols, "tensor memory");
 };
@@ -118,6 +130,69 @@ __device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity) {
 }
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity) {
   return __all_sync(kFull, wait_one(bar, parity));
+}
+
+// Products issued by a whole warp in step: every lane comes here with the same values,
+// which then sit in uniform registers, and one elected lane issues. (Issued by one lane
+// of a diverged warp, each product took 60 to 90 cycles to move its descriptors, 1,300 a
+// job of 1,024 cycles of tensor work.) Four M128 K16 steps over one 64-element swizzled
+// box, A and B in shared memory; the first accumulates iff acc0 != 0.
+__device__ __forceinline__ void mma4_ss_all(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                            uint32_t acc0) {
+  asm volatile(
+      "{\n.reg .pred p0, p1, e;\n.reg .b64 ad, bd;\n"
+      "elect.sync _|e, 0xffffffff;\n"
+      "setp.ne.b32 p0, %4, 0;\nsetp.eq.b32 p1, 0, 0;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p0;\n"
+      "add.u64 ad, %1, 2;\nadd.u64 bd, %2, 2;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %3, p1;\n"
+      "add.u64 ad, %1, 4;\nadd.u64 bd, %2, 4;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %3, p1;\n"
+      "add.u64 ad, %1, 6;\nadd.u64 bd, %2, 6;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %3, p1;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc0)
+      : "memory");
+}
+// 2 or 4 M128 K16 steps with A in tensor memory: step k reads A 8 k columns on and B 16 k
+// rows (2048 k bytes) on.
+template <int STEPS>
+__device__ __forceinline__ void mma_ts_all(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t acc0) {
+  static_assert(STEPS == 2 || STEPS == 4, "steps");
+  if constexpr (STEPS == 4) {
+    asm volatile(
+        "{\n.reg .pred p0, p1, e;\n.reg .b32 ac;\n.reg .b64 bd;\n"
+        "elect.sync _|e, 0xffffffff;\n"
+        "setp.ne.b32 p0, %4, 0;\nsetp.eq.b32 p1, 0, 0;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p0;\n"
+        "add.u32 ac, %1, 8;\nadd.u64 bd, %2, 128;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ac], bd, %3, p1;\n"
+        "add.u32 ac, %1, 16;\nadd.u64 bd, %2, 256;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ac], bd, %3, p1;\n"
+        "add.u32 ac, %1, 24;\nadd.u64 bd, %2, 384;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ac], bd, %3, p1;\n}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc0)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n.reg .pred p0, p1, e;\n.reg .b32 ac;\n.reg .b64 bd;\n"
+        "elect.sync _|e, 0xffffffff;\n"
+        "setp.ne.b32 p0, %4, 0;\nsetp.eq.b32 p1, 0, 0;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p0;\n"
+        "add.u32 ac, %1, 8;\nadd.u64 bd, %2, 128;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ac], bd, %3, p1;\n}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc0)
+        : "memory");
+  }
+}
+// Column of S where half h of a tile's weights begins: 128 tokens' sit over columns 0-31
+// and 64-95, 64 tokens' over 0-15 and 16-31.
+__device__ __forceinline__ constexpr int half_col(int kv, int h) { return h * (kv == 128 ? 64 : 16); }
+__device__ __forceinline__ void commit_all(uint32_t bar) {
+  asm volatile(
+      "{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\n"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar)
+      : "memory");
 }
 
 // Stage and phase of a ring position.
@@ -151,8 +226,10 @@ struct Items {
       count = c.y - c.x;
     }
   }
+  // Item k, an empty one behind the last.
   __device__ __forceinline__ PackedItem get(int k) const {
     const int w = blockIdx.x;
+    if (k >= count) return PackedItem{};
     const int4* p = reinterpret_cast<const int4*>(at + (whole ? k * ctas + ((k & 1) ? ctas - 1 - w : w) : k));
     const int4 x = p[0], y = p[1], z = p[2];
     return PackedItem{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
@@ -201,7 +278,8 @@ __device__ __forceinline__ uint32_t below(int k) {
 template <int QT, int D, bool FP8>
 __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     packed_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK,
-                          const __grid_constant__ CUtensorMap tmV, const PackedArgs a) {
+                          const __grid_constant__ CUtensorMap tmV,
+                          const __grid_constant__ CUtensorMap tmQ, const PackedArgs a) {
   using C = Cfg<D, FP8>;
   constexpr bool kBf16 = !FP8 && QT == kBF16;  // operand type of the products
   constexpr float kLift = kBf16 ? 0.f : kF16Lift;
@@ -227,6 +305,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
   if (tid == 0) {
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
+    if (!FP8) tma_prefetch_desc(&tmQ);
     for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(bar(kBarKFull + i), 1);
       mbar_init(bar(kBarKEmpty + i), FP8 ? 128 : 1);
@@ -236,6 +315,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kBarS + i), 1);
       mbar_init(bar(kBarP + i), kGroupThreads);
+      mbar_init(bar(kBarP2 + i), kGroupThreads);
       mbar_init(bar(kBarO + i), 1);
       mbar_init(bar(kBarOFull + i), 1);
       mbar_init(bar(kBarOFree + i), 128);
@@ -246,10 +326,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       mbar_init(bar(kBarCVFree + i), 1);
       mbar_init(bar(kBarLook + i), 4);
     }
-    mbar_init(bar(kBarQFull), 128);
-    mbar_init(bar(kBarQFull + 1), 128);
+    mbar_init(bar(kBarQFull), FP8 ? 128 : 1);
+    mbar_init(bar(kBarQFull + 1), FP8 ? 128 : 1);
     mbar_init(bar(kBarQFree), 1);
     mbar_init(bar(kBarDrain), 1);
+    mbar_init(bar(kBarDrain + 1), 1);
     sts_b32(base + C::kSkip, 0);
     sts_b32(base + C::kSkip + 4, 0);
     fence_mbar_init();
@@ -267,7 +348,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
   auto is_dual = [&](const PackedItem& it) { return NX == 2 && it.ntok > a.tpg; };
   auto jobs_of = [&](const PackedItem& it) { return is_dual(it) ? 2 * it.nt : it.nt; };
 
-  if (warp >= C::kMmaWarp) {
+  if (warp >= C::kMmaS) {
     if constexpr (C::kSplitRegs)
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     if (warp == C::kLoadK || warp == C::kLoadV) {
@@ -282,23 +363,25 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       bool ok = true;
       Ring r;
       int c = 0;  // tiles so far
+      // first row of this lane's slice of tile n, -1 behind the range
+      auto row_of = [&](const PackedItem& it, int n) -> int {
+        const int pos0 = (it.lo & ~15) + (it.tile0 + n) * KV + 16 * lane;
+        if (lane >= C::kSlices || pos0 > it.hi || n >= it.nt) return -1;
+        const int lb = pos0 / a.bs;
+        int blk = a.block_tables[static_cast<size_t>(it.b) * a.MB + lb];
+        if (static_cast<unsigned>(blk) >= static_cast<unsigned>(a.NB)) {
+          atomicOr(a.err, PA_DEVERR_BLOCK_ID);
+          blk = 0;
+        }
+        return (blk * a.Hkv + it.kvh) * a.bs + (pos0 - lb * a.bs);
+      };
+      PackedItem it = items.get(0);
+      int row = row_of(it, 0);
       for (int k = 0; ok && k < items.count; ++k) {
-        const PackedItem it = items.get(k);
-        const int32_t* table = a.block_tables + static_cast<size_t>(it.b) * a.MB;
-        auto row_of = [&](int n) -> int {
-          const int pos0 = (it.lo & ~15) + (it.tile0 + n) * KV + 16 * lane;
-          if (lane >= C::kSlices || pos0 > it.hi || n >= it.nt) return -1;
-          const int lb = pos0 / a.bs;
-          int blk = table[lb];
-          if (static_cast<unsigned>(blk) >= static_cast<unsigned>(a.NB)) {
-            atomicOr(a.err, PA_DEVERR_BLOCK_ID);
-            blk = 0;
-          }
-          return (blk * a.Hkv + it.kvh) * a.bs + (pos0 - lb * a.bs);
-        };
-        int row = row_of(0);
+        const PackedItem ahead = items.get(k + 1);
         for (int n = 0; n < it.nt; ++n, ++c) {
-          const int next = row_of(n + 1);  // looked up while the wait below runs
+          // looked up while the wait below runs
+          const int next = n + 1 < it.nt ? row_of(it, n + 1) : row_of(ahead, 0);
           if (c >= stages && !(ok = wait_all(bar(empty0 + r.stage), r.phase ^ 1))) break;
           const uint32_t full = bar(full0 + r.stage);
           const int nslices = __popc(__ballot_sync(kFull, row >= 0));
@@ -314,123 +397,147 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           r.next(stages);
           row = next;
         }
+        if (it.nt == 0) row = row_of(ahead, 0);
+        it = ahead;
       }
       if (!ok) {
         if (lane == 0) atomicOr(a.err, PA_DEVERR_TIMEOUT);
         for (int i = max(c - stages, 0); i < c; ++i)  // no copy outlives the CTA
           (void)mbar_wait_bounded(bar(full0 + i % stages), (i / stages) & 1, kDrainNs);
       }
-    } else if (warp == C::kMmaWarp) {
-      // ------------------------------------------------------------ MMA issue
-      // One thread does all of it: its own instructions are on the critical path.
-      if (lane == 0) {
-        constexpr uint32_t idS = tc::idesc_f16(kRows, KV, kBf16, false);
-        constexpr uint32_t idO = tc::idesc_f16(kRows, D, kBf16, true);
+    } else {
+      // ------------------------------------------------------------ products
+      // The warps stay together, so that what they issue with is uniform; their own
+      // instructions are on the critical path.
+      const uint32_t tm = __shfl_sync(kFull, tmem, 0);
+      const int count = __shfl_sync(kFull, items.count, 0);
+      bool ok = true;
+      Ring ring;
+      uint32_t jobs = 0, live = 0;
+      int done = 0;  // releases of K or V committed
+      if (warp == C::kMmaS) {
+        // (a negative scale flips the sign of A, Q)
+        const uint32_t idS = tc::idesc_f16(kRows, KV, kBf16, false) | (a.score_scale < 0.f ? 1u << 13 : 0u);
         const uint64_t dQ = tc::sdesc_sw128(sQ, 16, 1024);
         const uint64_t dK = tc::sdesc_sw128(FP8 ? sKc : sK, 16, 1024);
-        const uint64_t dV = tc::sdesc_sw128(sVt, C::kBox, 1024);
-        // A place in the sequence of jobs of all items.
-        struct Cursor {
-          int k = -1, j = 0, jobs = 0;  // item, job of it, its jobs
-          bool dual = false;
-        };
-        auto settle = [&](Cursor& c) {  // the next job, skipping items without any
-          while (c.j == c.jobs && c.k < items.count) {
-            if (++c.k < items.count) {
-              const PackedItem it = items.get(c.k);
-              c.dual = is_dual(it);
-              c.jobs = jobs_of(it);
-              c.j = 0;
-            }
-          }
-          return c.k < items.count;
-        };
-        bool ok = true;
-        Cursor sc, oc;
-        Ring kr, vr;
-        uint32_t sjobs = 0, ojobs = 0, sitems = 0;
-        uint32_t o_items[2] = {0, 0};  // items begun in each group's O
-        int k_done = 0, v_done = 0;    // releases committed
-        // S of the next job, where there is one.
-        auto step_s = [&]() {
-          if (!settle(sc)) return;
-          const int x = sjobs & 1;
-          if (sc.j == 0 && !(ok = wait_one(bar(kBarQFull + (sitems & 1)), sitems >> 1))) return;
-          const bool first_use = !sc.dual || !(sc.j & 1), last_use = !sc.dual || (sc.j & 1);
-          if (first_use && !(ok = wait_one(bar(kKReady + kr.stage), kr.phase))) return;
+        auto job = [&](bool own_rows) {
+          const int x = jobs & 1;
           // the buffer's last P has been used
-          if (sjobs >= 2 && !(ok = wait_one(bar(kBarO + x), (sjobs - 2) >> 1))) return;
+          if (jobs >= 2 && !(ok = wait_all(bar(kBarO + x), (jobs - 2) >> 1))) return;
           tc::fence_after_sync();
-          const uint64_t q = dQ + (sc.dual && x ? C::kQBytes >> 4 : 0);
+          const uint64_t q = dQ + (own_rows && x ? C::kQBytes >> 4 : 0);
 #pragma unroll
           for (int box = 0; box < C::kBoxes; ++box)
-            mma4_ss(tmem + C::kColS + KV * x, q + ((box * C::kQBox) >> 4),
-                    dK + ((kr.stage * C::kTile + box * C::kBox) >> 4), idS, box > 0);
-          tc::commit(bar(kBarS + x));
-          if (last_use) {
-            tc::commit(bar(kKFree + kr.stage));
-            kr.next(KB);
-            ++k_done;
-          }
-          ++sjobs;
-          if (++sc.j == sc.jobs) {
-            tc::commit(bar(kBarQFree));
-            ++sitems;
-          }
+            mma4_ss_all(tm + C::kColS + KV * x, q + ((box * C::kQBox) >> 4),
+                        dK + ((ring.stage * C::kTile + box * C::kBox) >> 4), idS, box > 0);
+          commit_all(bar(kBarS + x));
+          ++jobs;
         };
-        // O of the next job.
+        PackedItem ahead = items.get(0);
+        for (int k = 0; ok && k < count; ++k) {
+          const PackedItem it = ahead;
+          ahead = items.get(k + 1);
+          const int nt = __shfl_sync(kFull, it.nt, 0);
+          const bool dual = __any_sync(kFull, is_dual(it));
+          if (nt == 0) continue;
+          if (!FP8) {
+            // Q, once the last item's products are done with it: a row tile's tokens times
+            // the group's heads are one box a 64 head dims. (Rows behind the unit's are
+            // other sequences', or zeros behind the last: not used.)
+            if (live > 0 && !(ok = wait_all(bar(kBarQFree), live - 1))) break;
+            if (lane == 0) {
+              const int row_tiles = dual ? 2 : 1;
+              const uint32_t full = bar(kBarQFull + (live & 1));
+              mbar_arrive_expect_tx(full, row_tiles * C::kBoxes * a.tpg * a.G * 128);
+              for (int xt = 0; xt < row_tiles; ++xt)
+#pragma unroll
+                for (int box = 0; box < C::kBoxes; ++box)
+                  tma_load_3d(sQ + xt * C::kQBytes + box * C::kQBox, &tmQ, box * 64, it.kvh * a.G,
+                              it.row0 + xt * a.tpg, full);
+            }
+            __syncwarp();
+          }
+          if (!(ok = wait_all(bar(kBarQFull + (live & 1)), live >> 1))) {
+            if (!FP8) (void)mbar_wait_bounded(bar(kBarQFull + (live & 1)), (live >> 1) & 1, kDrainNs);
+            break;  // (no copy outlives the CTA)
+          }
+          ++live;
+#pragma unroll 1
+          for (int n = 0; n < nt; ++n) {
+            if (!(ok = wait_all(bar(kKReady + ring.stage), ring.phase))) break;
+            job(dual);
+            if (dual && ok) job(true);
+            if (!ok) break;
+            commit_all(bar(kKFree + ring.stage));
+            ring.next(KB);
+            ++done;
+          }
+          commit_all(bar(kBarQFree));
+        }
+      } else {
+        constexpr uint32_t idO = tc::idesc_f16(kRows, D, kBf16, true);
+        const uint64_t dV = tc::sdesc_sw128(sVt, C::kBox, 1024);
+        uint32_t o_items[2] = {0, 0};    // items begun in each group's O
         bool begun[2] = {false, false};  // O of each group holds something of this item
-        auto step_o = [&]() {
-          const int x = ojobs & 1, g = NX == 2 ? x : 0;
-          const bool first_use = !oc.dual || !(oc.j & 1), last_use = !oc.dual || (oc.j & 1);
-          if (!(ok = wait_one(bar(kBarP + x), ojobs >> 1))) return;
-          if (first_use && !(ok = wait_one(bar(kVReady + vr.stage), vr.phase))) return;
+        auto job = [&]() {
+          const int x = jobs & 1, g = NX == 2 ? x : 0;
           if (!begun[g]) {  // the last item's result has been read
-            if (o_items[g] > 0 && !(ok = wait_one(bar(kBarOFree + g), o_items[g] - 1))) return;
+            if (o_items[g] > 0 && !(ok = wait_all(bar(kBarOFree + g), o_items[g] - 1))) return;
             ++o_items[g];
           }
+          if (!(ok = wait_all(bar(kBarP + x), jobs >> 1))) return;
           tc::fence_after_sync();
           volatile uint32_t* skip = reinterpret_cast<volatile uint32_t*>(smem_raw + C::kSkip) + x;
-          if (*skip) {  // the group has added this tile itself
-            *skip = 0;
+          if (__any_sync(kFull, *skip != 0)) {  // the group has added this tile itself
+            if (lane == 0) *skip = 0;
+            __syncwarp();
           } else {
-#pragma unroll
-            for (int h = 0; h < KV / 64; ++h)
-              mma4_ts(tmem + C::kColO + D * g, tmem + C::kColS + KV * x + 64 * h,
-                      dV + ((vr.stage * C::kTile) >> 4) + 512 * h, idO, begun[g] || h > 0);
+            // the half of the weights that is written first, then the other
+            constexpr int kSteps = KV / 32;  // of 16 tokens a half
+            constexpr int h0 = C::kHeld ? 0 : 1, h1 = 1 - h0;
+            const uint32_t o = tm + C::kColO + D * g, p = tm + C::kColS + KV * x;
+            const uint64_t v = dV + ((ring.stage * C::kTile) >> 4);
+            mma_ts_all<kSteps>(o, p + half_col(KV, h0), v + 128 * kSteps * h0, idO, begun[g]);
+            if (!(ok = wait_all(bar(kBarP2 + x), jobs >> 1))) return;
+            tc::fence_after_sync();
+            mma_ts_all<kSteps>(o, p + half_col(KV, h1), v + 128 * kSteps * h1, idO, 1u);
           }
+          commit_all(bar(kBarO + x));
           begun[g] = true;
-          tc::commit(bar(kBarO + x));
-          if (last_use) {
-            tc::commit(bar(kVFree + vr.stage));
-            vr.next(VB);
-            ++v_done;
-          }
-          ++ojobs;
-          ++oc.j;
-          // the last job of a group in this item: the last two jobs, or the last one
-          if (oc.j == oc.jobs) {
-            if (NX == 2 && oc.jobs > 1) tc::commit(bar(kBarOFull + (x ^ 1)));
-            tc::commit(bar(kBarOFull + g));
-            begun[0] = begun[1] = false;
-          }
+          ++jobs;
         };
-        step_s();
-        if (ok) step_s();
-        while (ok && settle(oc)) {
-          step_o();
-          if (ok) step_s();
+        PackedItem ahead = items.get(0);
+        for (int k = 0; ok && k < count; ++k) {
+          const PackedItem it = ahead;
+          ahead = items.get(k + 1);
+          const int nt = __shfl_sync(kFull, it.nt, 0);
+          const bool dual = __any_sync(kFull, is_dual(it));
+          if (nt == 0) continue;
+#pragma unroll 1
+          for (int n = 0; n < nt; ++n) {
+            if (!(ok = wait_all(bar(kVReady + ring.stage), ring.phase))) break;
+            job();
+            if (dual && ok) job();
+            if (!ok) break;
+            commit_all(bar(kVFree + ring.stage));
+            ring.next(VB);
+            ++done;
+          }
+          // each group's O is complete
+          if (begun[0]) commit_all(bar(kBarOFull));
+          if (begun[1]) commit_all(bar(kBarOFull + 1));
+          begun[0] = begun[1] = false;
         }
-        // no product and no arrival outlives the CTA
-        if (!ok) atomicOr(a.err, PA_DEVERR_TIMEOUT);
-        const uint64_t limit = ok ? kWaitNs : kDrainNs;
-        tc::commit(bar(kBarDrain));
-        (void)mbar_wait_bounded(bar(kBarDrain), 0, limit);
-        for (int i = 0; i < KB && i < k_done; ++i)
-          (void)mbar_wait_bounded(bar(kKFree + i), ((k_done - 1 - i) / KB) & 1, limit);
-        for (int i = 0; i < VB && i < v_done; ++i)
-          (void)mbar_wait_bounded(bar(kVFree + i), ((v_done - 1 - i) / VB) & 1, limit);
       }
+      // no product and no arrival outlives the CTA
+      if (!ok && lane == 0) atomicOr(a.err, PA_DEVERR_TIMEOUT);
+      const uint64_t limit = ok ? kWaitNs : kDrainNs;
+      const int drain = warp == C::kMmaS ? kBarDrain : kBarDrain + 1;
+      const int free0 = warp == C::kMmaS ? kKFree : kVFree, bufs = warp == C::kMmaS ? KB : VB;
+      commit_all(bar(drain));
+      (void)mbar_wait_bounded(bar(drain), 0, limit);
+      for (int i = 0; i < bufs && i < done; ++i)
+        (void)mbar_wait_bounded(bar(free0 + i), ((done - 1 - i) / bufs) & 1, limit);
       __syncwarp();
     }
   } else if (FP8 && warp >= C::kConvWarp) {
@@ -505,9 +612,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     const int sub_r = lane / kCh, ch = lane % kCh;
     const uint32_t mul = (65536u + a.G - 1) / a.G;  // row / G = row * mul >> 16, rows < 256
     const int tok_r = static_cast<int>((r * mul) >> 16), head_r = r - tok_r * a.G;
-    // Q rows of an item -> shared memory (K-major, 128-byte swizzle); rows beside the
-    // unit's are zeros, up to whole warps.
-    const uint32_t flip = a.score_scale < 0.f ? 0x80008000u : 0u;
+    // FP8: Q rows of an item -> shared memory (K-major, 128-byte swizzle); rows beside
+    // the unit's are zeros, up to whole warps.
     auto stage_q = [&](const PackedItem& it, uint32_t which) {
       const int tiles = is_dual(it) ? 2 : 1;
       for (int xt = 0; xt < tiles; ++xt) {
@@ -532,30 +638,27 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < kBatch; ++i) {
             const int rr = wr0 + (i0 + i) * kPer + sub_r;
-            if constexpr (FP8) {
-              // f16 after a power-of-two rescale: largest magnitude in [2^14, 2^15)
-              const uint32_t w4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-              float amax = 0.f;
+            // f16 after a power-of-two rescale: largest magnitude in [2^14, 2^15)
+            const uint32_t w4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            float amax = 0.f;
 #pragma unroll
-              for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f32_of<QT>(w4[e >> 1], e & 1)));
+            for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f32_of<QT>(w4[e >> 1], e & 1)));
 #pragma unroll
-              for (int o = kCh / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
-              // 2^-sh from its exponent bits; below 2^-111 (scores that are zero for any
-              // weight) the largest stays under 2^14, as does zero
-              const int ex = static_cast<int>(__float_as_uint(amax) >> 23);  // 255: inf
-              const int sh = ex == 255 ? 0 : max(ex - 141, -126);
-              const float m = __int_as_float((127 - sh) << 23);
-              const float2 m2 = make_float2(m, m);
-              uint32_t o4[4];
+            for (int o = kCh / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+            // 2^-sh from its exponent bits; below 2^-111 (scores that are zero for any
+            // weight) the largest stays under 2^14, as does zero
+            const int ex = static_cast<int>(__float_as_uint(amax) >> 23);  // 255: inf
+            const int sh = ex == 255 ? 0 : max(ex - 141, -126);
+            const float m = __int_as_float((127 - sh) << 23);
+            const float2 m2 = make_float2(m, m);
+            uint32_t o4[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 t = __fmul2_rn(make_float2(f32_of<QT>(w4[e], 0), f32_of<QT>(w4[e], 1)), m2);
-                o4[e] = pack16x2<false>(t.x, t.y);
-              }
-              v[i] = make_uint4(o4[0], o4[1], o4[2], o4[3]);
-              if (ch == 0) sts_s8(base + C::kShift + (which & 1) * NX * kRows + xt * kRows + rr, sh);
+            for (int e = 0; e < 4; ++e) {
+              const float2 t = __fmul2_rn(make_float2(f32_of<QT>(w4[e], 0), f32_of<QT>(w4[e], 1)), m2);
+              o4[e] = pack16x2<false>(t.x, t.y);
             }
-            v[i].x ^= flip, v[i].y ^= flip, v[i].z ^= flip, v[i].w ^= flip;
+            v[i] = make_uint4(o4[0], o4[1], o4[2], o4[3]);
+            if (ch == 0) sts_s8(base + C::kShift + (which & 1) * NX * kRows + xt * kRows + rr, sh);
             sts_v4(q_tile + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4), v[i]);
           }
         }
@@ -564,7 +667,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       mbar_arrive(bar(kBarQFull + (which & 1)));
     };
     bool ok = true;
-    uint32_t staged = 0, stored = 0;  // items with tiles so far
+    uint32_t staged = 0;  // items whose Q is staged
     uint32_t o_items[2] = {0, 0};
     uint32_t jobs = 0;
     int kq = 0;  // next item whose Q is not staged
@@ -578,17 +681,16 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         return;
       }
     };
-    stage_next();
+    if (FP8) stage_next();
     for (int k = 0; ok && k < items.count; ++k) {
       const PackedItem it = items.get(k);
       const bool dual = is_dual(it);
       const int nj = jobs_of(it);
       const uint32_t s = jobs & 1;  // group of the item's first job
       jobs += nj;
-      if (nj > 0) {
+      if (FP8 && nj > 0) {
         stage_next();
         if (!ok) break;
-        ++stored;
       }
       const int tiles = dual ? 2 : 1;
       float* const part = a.part + static_cast<size_t>(max(it.slot, 0)) * packed_slot_floats(a.slot_rows, D);
@@ -605,9 +707,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         if (!ok) break;
         tc::fence_after_sync();
       }
-      for (int xt = 0; xt < tiles; ++xt) {
-        const int rows = min(it.ntok - xt * a.tpg, a.tpg) * a.G;
-        if (wr0 >= rows) continue;
+      for (int q = 0; q < tiles; ++q) {
+        const int xt = dual ? g0 ^ q : 0;    // (the group of the first job first)
+        const int rows = wr0 < min(it.ntok - xt * a.tpg, a.tpg) * a.G ? min(it.ntok - xt * a.tpg, a.tpg) * a.G : 0;
         const bool valid = r < rows;
         const int ga = dual ? xt : g0;       // the group whose O holds these rows
         const bool join = both && !dual;     // and the other one
@@ -636,7 +738,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         const int slot_row = xt * kRows + r;
         float* const prow = part + static_cast<size_t>(slot_row) * D;
 #pragma unroll 1
-        for (int d0 = 0; d0 < D; d0 += 16) {
+        for (int d0 = 0; d0 < (rows > 0 ? D : 0); d0 += 16) {
           uint32_t ov[16];
           float o[16];
 #pragma unroll
@@ -676,11 +778,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           stat[0] = m - kLift;
           stat[a.slot_rows] = l;
         }
-      }
-      if (nj > 0) {
-        tc::fence_before_sync();
-        mbar_arrive(bar(kBarOFree + g0));
-        if (both) mbar_arrive(bar(kBarOFree + (g0 ^ 1)));
+        if (nj > 0) {
+          tc::fence_before_sync();
+          mbar_arrive(bar(kBarOFree + ga));
+          if (join) mbar_arrive(bar(kBarOFree + (ga ^ 1)));
+        }
       }
     }
     if (!ok && lane == 0) atomicOr(a.err, PA_DEVERR_TIMEOUT);
@@ -738,10 +840,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       const int sure_hi = a.tree ? it.first - 1 : it.pos0 + xt * a.tpg;
       const int top = a.tree ? it.hi + 1 : it.pos0 + last_tok + 1;
       const int sure_lo = a.window > 0 && top > a.window ? top - a.window : 0;
-      float sc = fabsf(a.score_scale);
+      // (never zero, so that a masked score stays -inf)
+      float sc = fmaxf(fabsf(a.score_scale), FLT_MIN);
       if constexpr (FP8) {
         if (!(ok = wait_all(bar(kBarQFull + (which & 1)), which >> 1))) break;
-        if (alive) sc = ldexpf(sc, lds_s8(base + C::kShift + (which & 1) * NX * kRows + xt * kRows + r));
+        if (alive) sc = fmaxf(FLT_MIN, ldexpf(sc, lds_s8(base + C::kShift + (which & 1) * NX * kRows + xt * kRows + r)));
       }
       float ms = kFloor, l = 0.f;  // reference max (scaled, log2 units) and running sum
       for (int j = j0; j < nj; j += step, ++mine) {
@@ -751,10 +854,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         const uint32_t phase = NX == 2 ? mine : mine >> 1;
         // with one group, jobs alternate between the buffers from the very first one on
         const uint32_t tS = trow + C::kColS + KV * buf;
-        if (!(ok = wait_all(bar(kBarS + buf), phase))) break;
-        tc::fence_after_sync();
         const bool all_in = __all_sync(kFull, !valid || (t0 >= lo_r && t0 + KV - 1 <= hi_r));
         uint32_t mask[KV / 32];
+#pragma unroll
+        for (int w = 0; w < KV / 32; ++w) mask[w] = 0xffffffffu;
+        if (!all_in)
 #pragma unroll
         for (int w = 0; w < KV / 32; ++w) {
           mask[w] = below(hi_r + 1 - t0 - 32 * w) & ~below(lo_r - t0 - 32 * w);
@@ -762,10 +866,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           if (sh > -32 && sh < 64)
             mask[w] |= sh >= 0 ? static_cast<uint32_t>(bits >> sh) : static_cast<uint32_t>(bits << -sh);
         }
-        auto word = [&](int hf, int i) -> uint32_t {  // bits of scores 64 hf + 32 i ...
-          if constexpr (KV == 64) return mask[i];
-          return hf ? mask[2 + i] : mask[i];
-        };
         bool skip = false;
         // A tile that some row does not attend to in full.
         if (t0 < sure_lo || t0 + KV - 1 > sure_hi) {
@@ -807,36 +907,61 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           lds_v4(look, w[0], w[1], w[2], w[3]);
           skip = (w[0] | w[1] | w[2] | w[3]) != 0;
         }
+        if (!(ok = wait_all(bar(kBarS + buf), phase))) break;
+        tc::fence_after_sync();
         if (alive) {
-          uint32_t sv[2][32];
+          constexpr int NS = C::kHeld ? KV / 32 : 2;
+          uint32_t sv[NS][32];
           float mxp[8];  // eight independent partial maxima (raw scores)
 #pragma unroll
           for (int i = 0; i < 8; ++i) mxp[i] = -INFINITY;
-#pragma unroll 1
-          for (int hf = 0; hf < KV / 64; ++hf) {
-            tc::ld32_async(tS + 64 * hf, sv[0]);
-            tc::ld32_async(tS + 64 * hf + 32, sv[1]);
-            tc::wait_ld(sv[0], sv[1]);
-            if (all_in) {
+          // scores 64 h ... into two rows of sv, masked ones as -inf
+          auto fetched = [&](int c, int h) {
+            if (!all_in) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                mxp[i & 7] = fmax3(mxp[i & 7], __uint_as_float(sv[i >> 4][(2 * i) & 31]),
-                                   __uint_as_float(sv[i >> 4][(2 * i + 1) & 31]));
-            } else {
-              const uint32_t w0 = word(hf, 0), w1 = word(hf, 1);
+              for (int q = 0; q < 2; ++q) {
+                const uint32_t w = KV == 64 || h == 0 ? mask[q] : mask[(2 + q) % (KV / 32)];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const uint32_t w = i < 16 ? w0 : w1;
-                mxp[i & 7] = fmax3(mxp[i & 7],
-                                   (w >> ((2 * i) & 31)) & 1 ? __uint_as_float(sv[i >> 4][(2 * i) & 31]) : -INFINITY,
-                                   (w >> ((2 * i + 1) & 31)) & 1 ? __uint_as_float(sv[i >> 4][(2 * i + 1) & 31])
-                                                                 : -INFINITY);
+                for (int i = 0; i < 32; ++i) sv[c + q][i] = (w >> i) & 1 ? sv[c + q][i] : 0xff800000u;
               }
+            }
+          };
+          auto add_max = [&](int c) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int i = 0; i < 32; i += 2)
+                mxp[(i >> 1) & 7] = fmax3(mxp[(i >> 1) & 7], __uint_as_float(sv[c + q][i]),
+                                          __uint_as_float(sv[c + q][i + 1]));
+          };
+          if constexpr (C::kHeld) {
+            tc::ld32_async(tS, sv[0]);
+            tc::ld32_async(tS + 32, sv[1]);
+            tc::wait_ld(sv[0], sv[1]);
+            if constexpr (KV == 128) {  // the second half on its way during the first's maximum
+              tc::ld32_async(tS + 64, sv[2]);
+              tc::ld32_async(tS + 96, sv[3]);
+            }
+            fetched(0, 0);
+            add_max(0);
+            if constexpr (KV == 128) {
+              tc::wait_ld(sv[2], sv[3]);
+              fetched(2, 1);
+              add_max(2);
+            }
+          } else {
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              tc::ld32_async(tS + 64 * h, sv[0]);
+              tc::ld32_async(tS + 64 * h + 32, sv[1]);
+              tc::wait_ld(sv[0], sv[1]);
+              fetched(0, h);
+              add_max(0);
             }
           }
           const float mxr = fmaxf(fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])),
                                   fmaxf(fmaxf(mxp[4], mxp[5]), fmaxf(mxp[6], mxp[7])));
-          const float mx = fmaxf(mxr * sc, kFloor);  // NaN (all masked, sc = 0) -> floor
+          const float mx = fmaxf(mxr * sc, kFloor);
           const bool grow = mx > ms + kRescaleAbove;
           const bool old = j != j0;  // O holds something
           if (!old) {
@@ -920,6 +1045,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
               }
             }
             if (r == 0) sts_b32(base + C::kSkip + 4 * buf, 1u);
+            tc::fence_before_sync();
+            mbar_arrive(bar(kBarP + buf));
           } else {
             // P = 2^(s * sc - ms + kLift), packed in pairs over the columns of the scores
             // just used; the last half is still in registers. It is rounded to the
@@ -930,45 +1057,51 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             float2 sp[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) sp[i] = make_float2(0.f, 0.f);
-#pragma unroll 1
-            for (int hf = KV / 64 - 1; hf >= 0; --hf) {
-              if (hf != KV / 64 - 1) {
-                tc::ld32_async(tS + 64 * hf, sv[0]);
-                tc::ld32_async(tS + 64 * hf + 32, sv[1]);
-                tc::wait_ld(sv[0], sv[1]);
-              }
-              uint32_t pk[32];
-              if (all_in) {
+            // N pairs of scores from sv rows c ..., to column col
+            auto weigh = [&](int c, int first, int col, auto n) {
+              constexpr int N = decltype(n)::value;
+              uint32_t pk[N];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  const float2 t = __ffma2_rn(score_pair(sv[i >> 4], (2 * i) & 31), sc2, nms2);
-                  const float p0 = ex2(t.x), p1 = ex2(t.y);
-                  sp[i & 3] = __fadd2_rn(sp[i & 3], make_float2(p0, p1));
-                  pk[i] = pack16x2<kBf16>(p0, p1);
-                }
-              } else {  // masked scores give exactly 0
-                const uint32_t w0 = word(hf, 0), w1 = word(hf, 1);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  const uint32_t w = i < 16 ? w0 : w1;
-                  const float2 t = __ffma2_rn(score_pair(sv[i >> 4], (2 * i) & 31), sc2, nms2);
-                  const float p0 = (w >> ((2 * i) & 31)) & 1 ? ex2(t.x) : 0.f;
-                  const float p1 = (w >> ((2 * i + 1) & 31)) & 1 ? ex2(t.y) : 0.f;
-                  sp[i & 3] = __fadd2_rn(sp[i & 3], make_float2(p0, p1));
-                  pk[i] = pack16x2<kBf16>(p0, p1);
-                }
+              for (int i = 0; i < N; ++i) {
+                const int e = first + 2 * i;
+                const float2 t = __ffma2_rn(score_pair(sv[c + (e >> 5)], e & 31), sc2, nms2);
+                const float p0 = ex2(t.x), p1 = ex2(t.y);
+                sp[i & 3] = __fadd2_rn(sp[i & 3], make_float2(p0, p1));
+                pk[i] = pack16x2<kBf16>(p0, p1);
               }
-              tc::st32(tS + 64 * hf, pk);
+              if constexpr (N == 32) tc::st32(tS + col, pk);
+              else tc::st16(tS + col, pk);
+            };
+            // half of the weights, which the products start on, then the other half
+            using Half = std::integral_constant<int, KV / 4>;
+            if constexpr (C::kHeld) {
+              weigh(0, 0, 0, Half());
+            } else {
+              weigh(0, 0, 64, Half());  // (the second half of the scores is in registers)
+            }
+            tc::wait_st();
+            tc::fence_before_sync();
+            mbar_arrive(bar(kBarP + buf));
+            if constexpr (C::kHeld) {
+              weigh(KV == 128 ? 2 : 0, KV == 128 ? 0 : 32, half_col(KV, 1), Half());
+            } else {
+              tc::ld32_async(tS, sv[0]);
+              tc::ld32_async(tS + 32, sv[1]);
+              tc::wait_ld(sv[0], sv[1]);
+              fetched(0, 0);
+              weigh(0, 0, 0, Half());
             }
             const float2 s01 = __fadd2_rn(sp[0], sp[1]), s23 = __fadd2_rn(sp[2], sp[3]);
             const float2 st = __fadd2_rn(s01, s23);
             l += st.x + st.y;
           }
+        } else {
+          mbar_arrive(bar(kBarP + buf));
         }
         if (!ok) break;
         tc::wait_st();
         tc::fence_before_sync();
-        mbar_arrive(bar(kBarP + buf));
+        mbar_arrive(bar(kBarP2 + buf));
       }
       tiles += it.nt;
       if (!ok) break;
@@ -981,7 +1114,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     if (!ok && lane == 0) atomicOr(a.err, PA_DEVERR_TIMEOUT);
   }
 
-  // every product has completed (the issuing thread waited for them)
+  // every product has completed (the issuing warps waited for them)
   tc::fence_before_sync();
   __syncthreads();
   if (warp == 0) {
@@ -991,8 +1124,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
 }
 
 template <int QT, int D, bool FP8>
-cudaError_t launch_typed(const CUtensorMap& tk, const CUtensorMap& tv, const PackedArgs& a,
-                         cudaStream_t s, bool pdl) {
+cudaError_t launch_typed(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
+                         const PackedArgs& a, cudaStream_t s, bool pdl) {
   using C = Cfg<D, FP8>;
   // a function attribute of the current device's context: set every time, a host-side
   // store
@@ -1017,29 +1150,29 @@ cudaError_t launch_typed(const CUtensorMap& tk, const CUtensorMap& tv, const Pac
   attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, packed_attn_tc_kernel<QT, D, FP8>, tk, tv, a);
+  return cudaLaunchKernelEx(&cfg, packed_attn_tc_kernel<QT, D, FP8>, tk, tv, tq, a);
 }
 
 template <int QT>
 cudaError_t launch_dim(bool fp8, int D, const CUtensorMap& tk, const CUtensorMap& tv,
-                       const PackedArgs& a, cudaStream_t s, bool pdl) {
+                       const CUtensorMap& tq, const PackedArgs& a, cudaStream_t s, bool pdl) {
   if (fp8) {
-    if (D == 128) return launch_typed<QT, 128, true>(tk, tv, a, s, pdl);
-    if (D == 256) return launch_typed<QT, 256, true>(tk, tv, a, s, pdl);
+    if (D == 128) return launch_typed<QT, 128, true>(tk, tv, tq, a, s, pdl);
+    if (D == 256) return launch_typed<QT, 256, true>(tk, tv, tq, a, s, pdl);
     return cudaErrorInvalidValue;
   }
-  if (D == 64) return launch_typed<QT, 64, false>(tk, tv, a, s, pdl);
-  if (D == 128) return launch_typed<QT, 128, false>(tk, tv, a, s, pdl);
-  if (D == 256) return launch_typed<QT, 256, false>(tk, tv, a, s, pdl);
+  if (D == 64) return launch_typed<QT, 64, false>(tk, tv, tq, a, s, pdl);
+  if (D == 128) return launch_typed<QT, 128, false>(tk, tv, tq, a, s, pdl);
+  if (D == 256) return launch_typed<QT, 256, false>(tk, tv, tq, a, s, pdl);
   return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
 cudaError_t packed_launch(int qt, bool fp8, int D, const CUtensorMap& tk, const CUtensorMap& tv,
-                          const PackedArgs& a, cudaStream_t s, bool pdl) {
-  return qt == kBF16 ? launch_dim<kBF16>(fp8, D, tk, tv, a, s, pdl)
-                     : launch_dim<kF16>(fp8, D, tk, tv, a, s, pdl);
+                          const CUtensorMap& tq, const PackedArgs& a, cudaStream_t s, bool pdl) {
+  return qt == kBF16 ? launch_dim<kBF16>(fp8, D, tk, tv, tq, a, s, pdl)
+                     : launch_dim<kF16>(fp8, D, tk, tv, tq, a, s, pdl);
 }
 
 }  // namespace pa
