@@ -20,6 +20,7 @@ using namespace pa;
 
 constexpr double k2p31 = 2147483648.0;
 constexpr int64_t kMaxRows = int64_t(1) << 30;
+constexpr int64_t kMaxRowStride = int64_t(1) << 23;
 // Costs of a step (packed_plan.cuh) in tiles of one CTA: least tiles a CTA in split mode,
 // an item's way in and out, the partial results of a split and their join.
 constexpr int kMinTiles = 2;
@@ -145,8 +146,11 @@ pa_status packed_attention(const pa_tensor* out, const pa_tensor* q, const pa_te
     return fail(PA_ERR_LAYOUT, "caches must be 16-byte aligned");
   if ((s = check_rows(q, "q")) || (s = check_rows(out, "out"))) return s;
   for (const pa_tensor* x : {q, out})
-    if (T > 1 && numel(x) > 0 && x->strides[0] < Hq * D)
-      return fail(PA_ERR_LAYOUT, "rows of q or out overlap");
+    if (T > 1 && numel(x) > 0) {
+      if (x->strides[0] < Hq * D) return fail(PA_ERR_LAYOUT, "rows of q or out overlap");
+      if (x->strides[0] >= kMaxRowStride)  // (a unit's rows are counted in 32 bits)
+        return fail(PA_ERR_UNSUPPORTED, "rows of q or out are 2^23 elements or more apart");
+    }
   if (!std::isfinite(scale)) return fail(PA_ERR_INVALID_ARG, "scale must be finite");
   if (fp8 && !(std::isfinite(k_scale) && std::isfinite(v_scale) && k_scale > 0 && v_scale > 0))
     return fail(PA_ERR_INVALID_ARG, "fp8 scales must be finite and positive");

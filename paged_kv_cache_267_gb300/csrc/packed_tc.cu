@@ -27,10 +27,10 @@
 // through for infinities and NaN, which a weight of zero would not keep out of the
 // other rows, and such a tile is added up without the tensor cores.
 //
-// FP8 caches: four warps turn each raw e4m3 tile into the f16 tile that the products
-// read (exact), in two buffers each for K and V; Q goes through the storing warps, which
-// rescale it per row by a power of two to f16's range, which the row's score scale
-// undoes.
+// FP8 caches: the storing warps turn each raw e4m3 tile into the f16 tile that the products
+// read (exact), in two buffers each for K and V, and store an item's results between the
+// next one's first tiles. Q goes through them as well: they rescale it per row by a power
+// of two to f16's range, which the row's score scale undoes.
 #include <float.h>
 
 #include <type_traits>
@@ -91,22 +91,20 @@ struct Cfg {
   static constexpr int kSlices = kKv / 16;
   static constexpr int kBoxes = D / 64;  // 64-dim boxes of a 16-bit tile
   static constexpr int kKStages = FP8 ? 1 : (D == 64 ? 4 : 2), kVStages = FP8 ? 1 : (D == 64 ? 4 : 3);
-  static constexpr int kEpiWarp = 4 * kGroups, kConvWarp = kEpiWarp + 4,
-                       kMmaS = kConvWarp + (FP8 ? 4 : 0), kLoadK = kMmaS + 2,  // (and O behind S)
-                       kLoadV = kMmaS + 3;
+  static constexpr int kStoreWarp = 4 * kGroups, kMmaS = kStoreWarp + 4,
+                       kLoadK = kMmaS + 2, kLoadV = kMmaS + 3;  // (the products O behind S)
   static constexpr int kThreads = (kMmaS + 4) * 32;
-  // Registers: what the block is launched with, and the shares of the softmax warps and
-  // of all others where each thread's part is too little for the softmax.
-  static constexpr int kGroupsAll = kThreads / 128;
-  static constexpr int kLaunchRegs = kThreads == 384 ? 168 : (kThreads == 512 ? 128 : 96);
-  static constexpr bool kSplitRegs = kThreads > 384;
-  static constexpr int kOtherRegs = kThreads == 640 ? 56 : (kGroups == 2 ? 64 : 104);
-  static constexpr int kSoftmaxRegs = kThreads == 640 ? 152 : 192;
-  // A row's scores of a tile stay in registers from the maximum to the weights; with
-  // fewer registers they are read from tensor memory 64 at a time, twice.
-  static constexpr bool kHeld = kKv == 64 || kThreads != 640;
-  static_assert(!kSplitRegs || kGroups * kSoftmaxRegs + (kGroupsAll - kGroups) * kOtherRegs <=
-                                   kGroupsAll * kLaunchRegs, "registers of the block");
+  // Registers a thread: what the block is launched with, and what the softmax warps, the
+  // storing warps and all others make of it where that is too little for the softmax.
+  // (A spill costs far more than its instruction here: beside 220 KB of shared memory
+  // the L1 cache holds little, and what the storing warps had spilt at 64 made them ten
+  // times slower.)
+  static constexpr bool kSplitRegs = kThreads == 512;
+  static constexpr int kLaunchRegs = kSplitRegs ? 128 : 168;
+  static constexpr int kSoftmaxRegs = 192, kStoreRegs = 88, kOtherRegs = 40;
+  static_assert(kThreads == 384 || (kThreads == 512 && kGroups == 2 && 2 * kSoftmaxRegs + kStoreRegs +
+                                                                           kOtherRegs == 4 * kLaunchRegs),
+                "registers of the block");
   static constexpr uint32_t kQBox = kRows * 128, kQBytes = kBoxes * kQBox;  // one row tile's Q
   static constexpr uint32_t kBox = kKv * 128, kTile = kBoxes * kBox;        // 16-bit K or V tile
   static constexpr uint32_t kRawBoxes = FP8 ? D / 128 : kBoxes;             // 128-byte boxes
@@ -269,6 +267,24 @@ __device__ __forceinline__ int lds_s8(uint32_t addr) {
   int v;
   asm volatile("ld.shared.s8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
+}
+// 16-byte pieces k = 0..3 of a row in each lane -> piece (lane & 3) of the four rows of
+// the lanes around: a store then covers 64 bytes of a row instead of 16 of each.
+__device__ __forceinline__ void transpose4(uint32_t (&v)[16], int lane) {
+#pragma unroll
+  for (int bit = 1; bit <= 2; bit <<= 1) {
+    const bool up = lane & bit;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const int lo = bit == 1 ? 2 * m : m, hi = lo + bit;  // pieces that change places
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t got = __shfl_xor_sync(kFull, up ? v[4 * lo + c] : v[4 * hi + c], bit);
+        if (up) v[4 * lo + c] = got;
+        else v[4 * hi + c] = got;
+      }
+    }
+  }
 }
 // Low k bits (none for k <= 0, all for k >= 32).
 __device__ __forceinline__ uint32_t below(int k) {
@@ -477,13 +493,15 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       } else {
         constexpr uint32_t idO = tc::idesc_f16(kRows, D, kBf16, true);
         const uint64_t dV = tc::sdesc_sw128(sVt, C::kBox, 1024);
-        uint32_t o_items[2] = {0, 0};    // items begun in each group's O
-        bool begun[2] = {false, false};  // O of each group holds something of this item
+        // of each group: items begun in its O (the parity is all that counts, a bit each),
+        // whether there was one, whether O holds something of this item
+        uint32_t o_items = 0, o_any = 0, begun = 0;
         auto job = [&]() {
           const int x = jobs & 1, g = NX == 2 ? x : 0;
-          if (!begun[g]) {  // the last item's result has been read
-            if (o_items[g] > 0 && !(ok = wait_all(bar(kBarOFree + g), o_items[g] - 1))) return;
-            ++o_items[g];
+          if (!(begun >> g & 1)) {  // the last item's result has been read
+            if ((o_any >> g & 1) && !(ok = wait_all(bar(kBarOFree + g), (o_items >> g) ^ 1))) return;
+            o_items ^= 1u << g;
+            o_any |= 1u << g;
           }
           if (!(ok = wait_all(bar(kBarP + x), jobs >> 1))) return;
           tc::fence_after_sync();
@@ -494,16 +512,16 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           } else {
             // the half of the weights that is written first, then the other
             constexpr int kSteps = KV / 32;  // of 16 tokens a half
-            constexpr int h0 = C::kHeld ? 0 : 1, h1 = 1 - h0;
+            constexpr int h0 = 0, h1 = 1;
             const uint32_t o = tm + C::kColO + D * g, p = tm + C::kColS + KV * x;
             const uint64_t v = dV + ((ring.stage * C::kTile) >> 4);
-            mma_ts_all<kSteps>(o, p + half_col(KV, h0), v + 128 * kSteps * h0, idO, begun[g]);
+            mma_ts_all<kSteps>(o, p + half_col(KV, h0), v + 128 * kSteps * h0, idO, begun >> g & 1);
             if (!(ok = wait_all(bar(kBarP2 + x), jobs >> 1))) return;
             tc::fence_after_sync();
             mma_ts_all<kSteps>(o, p + half_col(KV, h1), v + 128 * kSteps * h1, idO, 1u);
           }
           commit_all(bar(kBarO + x));
-          begun[g] = true;
+          begun |= 1u << g;
           ++jobs;
         };
         PackedItem ahead = items.get(0);
@@ -524,9 +542,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             ++done;
           }
           // each group's O is complete
-          if (begun[0]) commit_all(bar(kBarOFull));
-          if (begun[1]) commit_all(bar(kBarOFull + 1));
-          begun[0] = begun[1] = false;
+          if (begun & 1) commit_all(bar(kBarOFull));
+          if (begun & 2) commit_all(bar(kBarOFull + 1));
+          begun = 0;
         }
       }
       // no product and no arrival outlives the CTA
@@ -540,78 +558,16 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         (void)mbar_wait_bounded(bar(free0 + i), ((done - 1 - i) / bufs) & 1, limit);
       __syncwarp();
     }
-  } else if (FP8 && warp >= C::kConvWarp) {
+  } else if (warp >= C::kStoreWarp) {
     if constexpr (C::kSplitRegs)
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
-    // -------------------------------------------------------------- FP8 converters
-    // e4m3 tile -> the f16 buffer: a 16-byte chunk of 16 codes becomes two 16-byte
-    // chunks of f16 in the 64-dim box that holds them; V rows outside of the unit's
-    // range become zeros.
-    if constexpr (FP8) {
-      constexpr int kChunks = D / 16, kPer = 32 / kChunks;  // chunks a row, rows a pass
-      constexpr int kOctets = KV / 8;                       // of rows: a warp takes every fourth
-      const int o0 = warp - C::kConvWarp;
-      const int ch = lane % kChunks, q0 = lane / kChunks;
-      const int c16 = 2 * (ch & 3);
-      // rows [r_lo, r_hi) are converted, the others become zeros
-      auto convert = [&](uint32_t src, uint32_t dst, int r_lo, int r_hi) {
-        src += (ch >> 3) * C::kBox;
-        dst += (ch >> 2) * C::kBox;
-        static_assert(8 % kPer == 0, "passes of a row octet");
-#pragma unroll 1
-        for (int p = 0; p < 8 / kPer; ++p) {
-          const int r0 = 8 * o0 + q0 + kPer * p;  // rows r0, r0 + 32, ... share one swizzle
-          const uint32_t from = src + r0 * 128 + (((ch & 7) ^ (r0 & 7)) << 4);
-          const uint32_t lo = dst + r0 * 128 + ((c16 ^ (r0 & 7)) << 4);
-          const uint32_t hi = dst + r0 * 128 + (((c16 + 1) ^ (r0 & 7)) << 4);
-#pragma unroll
-          for (int k = 0; k < kOctets; k += 4) {
-            uint32_t w[4] = {0u, 0u, 0u, 0u}, h[8];
-            if (r0 + 8 * k >= r_lo && r0 + 8 * k < r_hi) lds_v4(from + 1024 * k, w[0], w[1], w[2], w[3]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              h[2 * i] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] & 0xffffu));
-              h[2 * i + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] >> 16));
-            }
-            sts_v4(lo + 1024 * k, make_uint4(h[0], h[1], h[2], h[3]));
-            sts_v4(hi + 1024 * k, make_uint4(h[4], h[5], h[6], h[7]));
-          }
-        }
-      };
-      bool ok = true;
-      int c = 0;
-      for (int k = 0; ok && k < items.count; ++k) {
-        const PackedItem it = items.get(k);
-        for (int n = 0; ok && n < it.nt; ++n, ++c) {
-          const int t0 = (it.lo & ~15) + (it.tile0 + n) * KV;
-          const uint32_t free_par = (c - 2) >> 1;  // of the buffers' last tile
-          if (!(ok = wait_all(bar(kBarKFull), c))) break;
-          if (c > 1 && !(ok = wait_all(bar(kBarCKFree + (c & 1)), free_par))) break;
-          convert(sK, sKc + (c & 1) * C::kTile, 0, KV);
-          fence_proxy_async();  // the f16 tile, visible to the tensor core
-          mbar_arrive(bar(kBarCKFull + (c & 1)));
-          mbar_arrive(bar(kBarKEmpty));  // reload the stage
-          if (!(ok = wait_all(bar(kBarVFull), c))) break;
-          if (c > 1 && !(ok = wait_all(bar(kBarCVFree + (c & 1)), free_par))) break;
-          convert(sV, sVc + (c & 1) * C::kTile, it.lo - t0, it.hi + 1 - t0);
-          fence_proxy_async();
-          mbar_arrive(bar(kBarCVFull + (c & 1)));
-          mbar_arrive(bar(kBarVEmpty));
-        }
-      }
-      if (!ok && lane == 0) atomicOr(a.err, PA_DEVERR_TIMEOUT);
-    }
-  } else if (warp >= C::kEpiWarp) {
-    if constexpr (C::kSplitRegs)
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kStoreRegs));
     // ---------------------------------------------------- queries in, results out
-    const int wr0 = (warp - C::kEpiWarp) * 32;  // first row of this warp
+    const int wr0 = (warp - C::kStoreWarp) * 32;  // first row of this warp
     const int r = wr0 + lane;                   // row = tensor-memory lane
     const uint32_t trow = tmem + (static_cast<uint32_t>(wr0) << 16);
     constexpr int kCh = D / 8, kPer = 32 / kCh;  // 16-byte chunks a row, rows at once
     const int sub_r = lane / kCh, ch = lane % kCh;
     const uint32_t mul = (65536u + a.G - 1) / a.G;  // row / G = row * mul >> 16, rows < 256
-    const int tok_r = static_cast<int>((r * mul) >> 16), head_r = r - tok_r * a.G;
     // FP8: Q rows of an item -> shared memory (K-major, 128-byte swizzle); rows beside
     // the unit's are zeros, up to whole warps.
     auto stage_q = [&](const PackedItem& it, uint32_t which) {
@@ -623,7 +579,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         const uint16_t* q0 = static_cast<const uint16_t*>(a.q) +
                              static_cast<size_t>(it.row0 + xt * a.tpg) * a.q_stride +
                              static_cast<size_t>(it.kvh) * a.G * D;
-        constexpr int kBatch = kCh < 8 ? kCh : 8;  // loads in flight
+        constexpr int kBatch = 4;  // loads in flight
 #pragma unroll 1
         for (int i0 = 0; i0 < kCh; i0 += kBatch) {
           uint4 v[kBatch];
@@ -667,122 +623,204 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       mbar_arrive(bar(kBarQFull + (which & 1)));
     };
     bool ok = true;
-    uint32_t staged = 0;  // items whose Q is staged
-    uint32_t o_items[2] = {0, 0};
+    uint32_t o_items = 0;  // items of each group so far (the parity, a bit each)
     uint32_t jobs = 0;
-    int kq = 0;  // next item whose Q is not staged
-    auto stage_next = [&]() {
-      while (kq < items.count) {
-        const PackedItem it = items.get(kq++);
-        if (it.nt == 0) continue;
-        if (staged > 0 && !(ok = wait_all(bar(kBarQFree), staged - 1))) return;
-        stage_q(it, staged);
-        ++staged;
-        return;
-      }
-    };
-    if (FP8) stage_next();
-    for (int k = 0; ok && k < items.count; ++k) {
-      const PackedItem it = items.get(k);
+    // the results of an item, items in order
+    auto store = [&](const PackedItem& it) {
       const bool dual = is_dual(it);
       const int nj = jobs_of(it);
       const uint32_t s = jobs & 1;  // group of the item's first job
       jobs += nj;
-      if (FP8 && nj > 0) {
-        stage_next();
-        if (!ok) break;
-      }
-      const int tiles = dual ? 2 : 1;
-      float* const part = a.part + static_cast<size_t>(max(it.slot, 0)) * packed_slot_floats(a.slot_rows, D);
       const int g0 = NX == 2 ? static_cast<int>(s) : 0;  // the group with the first job
       const bool both = NX == 2 && nj > 1;
-      // both groups' results of this item are complete
+      // the groups' results of this item are complete
       if (nj > 0) {
         for (int q = 0; q < (both ? 2 : 1); ++q) {
           const int g = g0 ^ q;
-          if (!(ok = wait_all(bar(kBarOFull + g), o_items[g]))) break;
-          if (!(ok = wait_all(bar(kBarStat + g), o_items[g]))) break;
-          ++o_items[g];
+          if (!(ok = wait_all(bar(kBarOFull + g), o_items >> g))) return;
+          if (!(ok = wait_all(bar(kBarStat + g), o_items >> g))) return;
+          o_items ^= 1u << g;
         }
-        if (!ok) break;
         tc::fence_after_sync();
       }
-      for (int q = 0; q < tiles; ++q) {
-        const int xt = dual ? g0 ^ q : 0;    // (the group of the first job first)
-        const int rows = wr0 < min(it.ntok - xt * a.tpg, a.tpg) * a.G ? min(it.ntok - xt * a.tpg, a.tpg) * a.G : 0;
-        const bool valid = r < rows;
-        const int ga = dual ? xt : g0;       // the group whose O holds these rows
-        const bool join = both && !dual;     // and the other one
-        float m = kFloor, l = 0.f, f_own = 0.f, f_other = 0.f;
-        if (nj > 0) {
-          lds_f32x2(base + C::kStat + (ga * kRows + r) * 8, m, l);
-          f_own = 1.f;
-          if (join) {
-            float m1, l1;
-            lds_f32x2(base + C::kStat + ((ga ^ 1) * kRows + r) * 8, m1, l1);
-            const float top = fmaxf(m, m1);
-            f_own = ex2(m - top);
-            f_other = ex2(m1 - top);
-            l = l * f_own + l1 * f_other;
-            m = top;
-          }
-        }
-        const bool direct = it.slot < 0;
-        // an empty row is zeros; a NaN in the sum stays one
-        const float inv = direct ? (l == 0.f ? 0.f : a.v_scale / l) : a.v_scale;
-        f_own *= inv;
-        f_other *= inv;
-        uint16_t* const out = static_cast<uint16_t*>(a.out) +
-                              static_cast<size_t>(it.row0 + xt * a.tpg + tok_r) * a.out_stride +
-                              static_cast<size_t>(it.kvh * a.G + head_r) * D;
-        const int slot_row = xt * kRows + r;
-        float* const prow = part + static_cast<size_t>(slot_row) * D;
+      const bool join = both && !dual;  // both groups' O are the same rows'
 #pragma unroll 1
-        for (int d0 = 0; d0 < (rows > 0 ? D : 0); d0 += 16) {
-          uint32_t ov[16];
-          float o[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = 0.f;
+      for (int q = 0; q < (dual ? 2 : 1); ++q) {
+        const int xt = dual ? g0 ^ q : 0;  // row tile (the group of the first job first)
+        const int ga = dual ? xt : g0;     // the group whose O holds its rows
+        const int rows = min(it.ntok - xt * a.tpg, a.tpg) * a.G;
+        if (wr0 < rows) {
+          float m = kFloor, l = 0.f, f_own = 0.f, f_other = 0.f;
           if (nj > 0) {
-            tc::ld16(trow + C::kColO + D * ga + d0, ov);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(ov[i]) * f_own;
+            lds_f32x2(base + C::kStat + (ga * kRows + r) * 8, m, l);
+            f_own = 1.f;
             if (join) {
-              tc::ld16(trow + C::kColO + D * (ga ^ 1) + d0, ov);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = fmaf(__uint_as_float(ov[i]), f_other, o[i]);
+              float m1, l1;
+              lds_f32x2(base + C::kStat + ((ga ^ 1) * kRows + r) * 8, m1, l1);
+              const float top = fmaxf(m, m1);
+              f_own = ex2(m - top);
+              f_other = ex2(m1 - top);
+              l = l * f_own + l1 * f_other;
+              m = top;
             }
           }
-          if (direct) {
-            // (a row that attends to nothing: whatever O holds)
-            if (l == 0.f)
+          // 16 columns of this row, joined and scaled
+          const uint32_t t_own = trow + C::kColO + D * ga, t_other = trow + C::kColO + D * (ga ^ 1);
+          auto take = [&](int d0, uint32_t (&v)[16]) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = 0.f;
-            if (valid) {
-              uint4* dst = reinterpret_cast<uint4*>(out + d0);
+            for (int i = 0; i < 16; ++i) v[i] = 0u;
+            if (nj > 0) tc::ld16(t_own + d0, v);
 #pragma unroll
-              for (int c = 0; c < 2; ++c)
-                dst[c] = make_uint4(pack16x2<QT == kBF16>(o[8 * c], o[8 * c + 1]),
-                                    pack16x2<QT == kBF16>(o[8 * c + 2], o[8 * c + 3]),
-                                    pack16x2<QT == kBF16>(o[8 * c + 4], o[8 * c + 5]),
-                                    pack16x2<QT == kBF16>(o[8 * c + 6], o[8 * c + 7]));
+            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f_own);
+            if (join) {
+              uint32_t w[16];
+              tc::ld16(t_other + d0, w);
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                v[i] = __float_as_uint(fmaf(__uint_as_float(w[i]), f_other, __uint_as_float(v[i])));
             }
-          } else if (valid) {
-            float4* dst = reinterpret_cast<float4*>(prow + d0);
+          };
+          const int r4 = wr0 + (lane & ~3);  // rows r4 .. r4 + 3 are this lane's to store
+          if (it.slot < 0) {
+            // an empty row is zeros; a NaN in the sum stays one
+            const float inv = l == 0.f ? 0.f : a.v_scale / l;
+            f_own *= inv;
+            f_other *= inv;
+            uint16_t* const out = static_cast<uint16_t*>(a.out) +
+                                  static_cast<size_t>(it.row0 + xt * a.tpg) * a.out_stride +
+                                  static_cast<size_t>(it.kvh) * a.G * D + 8 * (lane & 3);
+            int at[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) dst[c] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+            for (int i = 0; i < 4; ++i) {
+              const int t = static_cast<int>(((r4 + i) * mul) >> 16), h = r4 + i - t * a.G;
+              at[i] = r4 + i < rows ? t * static_cast<int>(a.out_stride) + h * D : -1;
+            }
+#pragma unroll 1
+            for (int d0 = 0; d0 < D; d0 += 32) {
+              uint32_t p[16];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                uint32_t v[16];
+                take(d0 + 16 * e, v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)  // (an empty row: whatever O holds)
+                  p[8 * e + i] = l == 0.f ? 0u : pack16x2<QT == kBF16>(__uint_as_float(v[2 * i]),
+                                                                       __uint_as_float(v[2 * i + 1]));
+              }
+              transpose4(p, lane);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (at[i] >= 0)
+                  *reinterpret_cast<uint4*>(out + at[i] + d0) =
+                      make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
+            }
+          } else {
+            f_own *= a.v_scale;
+            f_other *= a.v_scale;
+            float* const part = a.part + static_cast<size_t>(it.slot) * packed_slot_floats(a.slot_rows, D);
+            float* const to = part + static_cast<size_t>(xt * kRows + r4) * D + 4 * (lane & 3);
+#pragma unroll 1
+            for (int d0 = 0; d0 < D; d0 += 16) {
+              uint32_t v[16];
+              take(d0, v);
+              transpose4(v, lane);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (r4 + i < rows)
+                  *reinterpret_cast<uint4*>(to + i * D + d0) =
+                      make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            }
+            if (r < rows) {
+              float* stat = part + static_cast<size_t>(a.slot_rows) * D + xt * kRows + r;
+              stat[0] = m - kLift;
+              stat[a.slot_rows] = l;
+            }
           }
-        }
-        if (!direct && valid) {
-          float* stat = part + static_cast<size_t>(a.slot_rows) * D + slot_row;
-          stat[0] = m - kLift;
-          stat[a.slot_rows] = l;
         }
         if (nj > 0) {
           tc::fence_before_sync();
           mbar_arrive(bar(kBarOFree + ga));
           if (join) mbar_arrive(bar(kBarOFree + (ga ^ 1)));
         }
+      }
+    };
+    if constexpr (FP8) {
+      constexpr int kChunks = D / 16, kPer = 32 / kChunks;  // chunks a row, rows a pass
+      constexpr int kOctets = KV / 8;                       // of rows: a warp takes every fourth
+      const int o0 = warp - C::kStoreWarp;
+      const int ch = lane % kChunks, q0 = lane / kChunks;
+      const int c16 = 2 * (ch & 3);
+      // rows [r_lo, r_hi) are converted, the others become zeros
+      auto convert = [&](uint32_t src, uint32_t dst, int r_lo, int r_hi) {
+        src += (ch >> 3) * C::kBox;
+        dst += (ch >> 2) * C::kBox;
+        static_assert(8 % kPer == 0, "passes of a row octet");
+#pragma unroll 1
+        for (int p = 0; p < 8 / kPer; ++p) {
+          const int r0 = 8 * o0 + q0 + kPer * p;  // rows r0, r0 + 32, ... share one swizzle
+          const uint32_t from = src + r0 * 128 + (((ch & 7) ^ (r0 & 7)) << 4);
+          const uint32_t lo = dst + r0 * 128 + ((c16 ^ (r0 & 7)) << 4);
+          const uint32_t hi = dst + r0 * 128 + (((c16 + 1) ^ (r0 & 7)) << 4);
+#pragma unroll
+          for (int k = 0; k < kOctets; k += 4) {
+            uint32_t w[4] = {0u, 0u, 0u, 0u}, h[8];
+            if (r0 + 8 * k >= r_lo && r0 + 8 * k < r_hi) lds_v4(from + 1024 * k, w[0], w[1], w[2], w[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              h[2 * i] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] & 0xffffu));
+              h[2 * i + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] >> 16));
+            }
+            sts_v4(lo + 1024 * k, make_uint4(h[0], h[1], h[2], h[3]));
+            sts_v4(hi + 1024 * k, make_uint4(h[4], h[5], h[6], h[7]));
+          }
+        }
+      };
+      int c = 0;                  // tiles so far
+      uint32_t staged = 0;        // items whose Q is staged
+      int last = -1;              // the item whose results are to be stored
+#pragma unroll 1
+      for (int k = 0; ok && k < items.count; ++k) {
+        int nt, v_lo, v_hi;  // tiles, range of V rows from the first tile on
+        {
+          const PackedItem it = items.get(k);
+          const int start = (it.lo & ~15) + it.tile0 * KV;
+          nt = it.nt;
+          v_lo = it.lo - start;
+          v_hi = it.hi + 1 - start;
+        }
+        if (nt == 0) store(items.get(k));
+#pragma unroll 1
+        for (int n = 0; ok && n < nt; ++n, ++c) {
+          const uint32_t free_par = (c - 2) >> 1;  // of the buffers' last tile
+          if (!(ok = wait_all(bar(kBarKFull), c))) break;
+          if (c > 1 && !(ok = wait_all(bar(kBarCKFree + (c & 1)), free_par))) break;
+          convert(sK, sKc + (c & 1) * C::kTile, 0, KV);
+          fence_proxy_async();  // the f16 tile, visible to the tensor core
+          mbar_arrive(bar(kBarCKFull + (c & 1)));
+          mbar_arrive(bar(kBarKEmpty));  // reload the stage
+          if (n == 0) {
+            if (staged > 0 && !(ok = wait_all(bar(kBarQFree), staged - 1))) break;
+            stage_q(items.get(k), staged);
+            ++staged;
+          }
+          if (!(ok = wait_all(bar(kBarVFull), c))) break;
+          if (c > 1 && !(ok = wait_all(bar(kBarCVFree + (c & 1)), free_par))) break;
+          convert(sV, sVc + (c & 1) * C::kTile, v_lo - n * KV, v_hi - n * KV);
+          fence_proxy_async();
+          mbar_arrive(bar(kBarCVFull + (c & 1)));
+          mbar_arrive(bar(kBarVEmpty));
+          if (n == 0 && last >= 0) store(items.get(last));
+        }
+        if (nt > 0) last = k;
+      }
+      if (ok && last >= 0) store(items.get(last));
+    } else {
+      PackedItem it = items.get(0);
+#pragma unroll 1
+      for (int k = 0; ok && k < items.count; ++k) {
+        const PackedItem ahead = items.get(k + 1);
+        store(it);
+        it = ahead;
       }
     }
     if (!ok && lane == 0) atomicOr(a.err, PA_DEVERR_TIMEOUT);
@@ -802,10 +840,25 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     uint32_t live = 0;   // items with tiles
     uint32_t tiles = 0;  // K/V tiles of the items before
     uint32_t looks = 0;  // tiles whose V was looked through
-    for (int k = 0; ok && k < items.count; ++k) {
-      const PackedItem it = items.get(k);
-      const bool dual = is_dual(it);
-      const int nj = jobs_of(it);
+    const int count = __shfl_sync(kFull, items.count, 0);
+#pragma unroll 1
+    for (int k = 0; ok && k < count; ++k) {
+      // What is the same for the whole group, in uniform registers; positions from the
+      // first tile's first token on.
+      int nt, row0, ntok, first, u_lo, u_hi, pos0, start;
+      {
+        const PackedItem it = items.get(k);
+        start = __shfl_sync(kFull, (it.lo & ~15) + it.tile0 * KV, 0);
+        nt = __shfl_sync(kFull, it.nt, 0);
+        row0 = __shfl_sync(kFull, it.row0, 0);
+        ntok = __shfl_sync(kFull, it.ntok, 0);
+        first = __shfl_sync(kFull, it.first, 0) - start;
+        u_lo = __shfl_sync(kFull, it.lo, 0) - start;      // the unit's range
+        u_hi = __shfl_sync(kFull, it.hi, 0) + 1 - start;  // (its end)
+        pos0 = __shfl_sync(kFull, it.pos0, 0) - start;
+      }
+      const bool dual = NX == 2 && ntok > a.tpg;
+      const int nj = dual ? 2 * nt : nt;
       if (nj == 0) continue;
       const int s = jobs & 1;  // S buffer (and group) of the item's first job
       jobs += nj;
@@ -813,33 +866,31 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       const int j0 = NX == 2 ? (s ^ x) : 0, step = NX == 2 ? 2 : 1;
       const uint32_t which = live++;
       if (j0 >= nj) {
-        tiles += it.nt;
+        tiles += nt;
         continue;
       }
-      // this row
+      // this row: the range that it attends to (a tree: before the drafted tokens)
       const int xt = dual ? x : 0;
       const int tok = xt * a.tpg + tok_r;
-      const bool valid = tok_r < a.tpg && tok < it.ntok;
+      const bool valid = tok_r < a.tpg && tok < ntok;
       const bool alive = __any_sync(kFull, valid);
       uint64_t bits = 0;
-      int hi_r, lo_r;  // the range that it attends to (a tree: before the drafted tokens)
+      int r_lo, r_hi;
       if (a.tree) {
-        const int nb = it.hi + 1 - it.first;  // drafted tokens that have a bit
-        if (valid) bits = static_cast<uint64_t>(a.tree[it.row0 + tok]) & (nb >= 64 ? ~0ull : (1ull << nb) - 1);
-        const int p1 = it.first + __popcll(bits);  // its position + 1
-        hi_r = it.first - 1;
-        lo_r = a.window > 0 && p1 > a.window ? p1 - a.window : 0;
+        const int nb = u_hi - first;  // drafted tokens that have a bit
+        if (valid) bits = static_cast<uint64_t>(a.tree[row0 + tok]) & (nb >= 64 ? ~0ull : (1ull << nb) - 1);
+        r_hi = first;
+        r_lo = r_hi + __popcll(bits);  // its place + 1
       } else {
-        hi_r = it.pos0 + tok;
-        lo_r = a.window > 0 && hi_r + 1 > a.window ? hi_r + 1 - a.window : 0;
+        r_hi = r_lo = pos0 + tok + 1;
       }
-      if (!valid) bits = 0, hi_r = -1, lo_r = 0;
-      // What all rows of the group attend to for sure, uniform over it: a tile inside
-      // takes no look through V.
-      const int last_tok = min(it.ntok, (xt + 1) * a.tpg) - 1;
-      const int sure_hi = a.tree ? it.first - 1 : it.pos0 + xt * a.tpg;
-      const int top = a.tree ? it.hi + 1 : it.pos0 + last_tok + 1;
-      const int sure_lo = a.window > 0 && top > a.window ? top - a.window : 0;
+      r_lo = a.window > 0 ? max(r_lo - a.window, -start) : -start;
+      if (!valid) bits = 0, r_hi = -start, r_lo = 0x40000000;
+      // What all rows of the group attend to for sure: a tile inside takes no look
+      // through V.
+      const int sure_hi = a.tree ? first : pos0 + xt * a.tpg + 1;
+      const int last = a.tree ? u_hi : pos0 + min(ntok, (xt + 1) * a.tpg);
+      const int sure_lo = a.window > 0 ? last - a.window : -start;
       // (never zero, so that a masked score stays -inf)
       float sc = fmaxf(fabsf(a.score_scale), FLT_MIN);
       if constexpr (FP8) {
@@ -848,34 +899,33 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       }
       float ms = kFloor, l = 0.f;  // reference max (scaled, log2 units) and running sum
       for (int j = j0; j < nj; j += step, ++mine) {
-        const int n = dual ? j >> 1 : j;
-        const int t0 = (it.lo & ~15) + (it.tile0 + n) * KV;
+        const int n = dual ? j >> 1 : j, t0 = n * KV;
         const int buf = NX == 2 ? x : ((s + j) & 1);
         const uint32_t phase = NX == 2 ? mine : mine >> 1;
-        // with one group, jobs alternate between the buffers from the very first one on
         const uint32_t tS = trow + C::kColS + KV * buf;
-        const bool all_in = __all_sync(kFull, !valid || (t0 >= lo_r && t0 + KV - 1 <= hi_r));
+        const bool all_in = __all_sync(kFull, !valid || (t0 >= r_lo && t0 + KV <= r_hi));
         uint32_t mask[KV / 32];
 #pragma unroll
         for (int w = 0; w < KV / 32; ++w) mask[w] = 0xffffffffu;
-        if (!all_in)
+        if (!all_in) {
 #pragma unroll
-        for (int w = 0; w < KV / 32; ++w) {
-          mask[w] = below(hi_r + 1 - t0 - 32 * w) & ~below(lo_r - t0 - 32 * w);
-          const int sh = 32 * w + t0 - it.first;  // bit of this word's first token
-          if (sh > -32 && sh < 64)
-            mask[w] |= sh >= 0 ? static_cast<uint32_t>(bits >> sh) : static_cast<uint32_t>(bits << -sh);
+          for (int w = 0; w < KV / 32; ++w) {
+            mask[w] = below(r_hi - t0 - 32 * w) & ~below(r_lo - t0 - 32 * w);
+            const int sh = 32 * w + t0 - first;  // bit of this word's first token
+            if (sh > -32 && sh < 64)
+              mask[w] |= sh >= 0 ? static_cast<uint32_t>(bits >> sh) : static_cast<uint32_t>(bits << -sh);
+          }
         }
         bool skip = false;
         // A tile that some row does not attend to in full.
-        if (t0 < sure_lo || t0 + KV - 1 > sure_hi) {
+        if (t0 < sure_lo || t0 + KV > sure_hi) {
           const uint32_t c = tiles + n, stage = c % VB;
           if (!(ok = wait_all(bar(kVReady + stage), c / VB))) break;
           const uint32_t vt = sVt + stage * C::kTile;
           uint32_t bad = 0;
           if (r < KV) {
             const int pos = t0 + r;
-            if (pos >= it.lo && pos <= it.hi) {
+            if (pos >= u_lo && pos < u_hi) {
 #pragma unroll
               for (int box = 0; box < C::kBoxes; ++box)
 #pragma unroll
@@ -910,20 +960,17 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         if (!(ok = wait_all(bar(kBarS + buf), phase))) break;
         tc::fence_after_sync();
         if (alive) {
-          constexpr int NS = C::kHeld ? KV / 32 : 2;
-          uint32_t sv[NS][32];
+          uint32_t sv[KV / 32][32];
           float mxp[8];  // eight independent partial maxima (raw scores)
 #pragma unroll
           for (int i = 0; i < 8; ++i) mxp[i] = -INFINITY;
-          // scores 64 h ... into two rows of sv, masked ones as -inf
-          auto fetched = [&](int c, int h) {
+          // masked scores of two rows of sv as -inf
+          auto fetched = [&](int c) {
             if (!all_in) {
 #pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                const uint32_t w = KV == 64 || h == 0 ? mask[q] : mask[(2 + q) % (KV / 32)];
+              for (int q = 0; q < 2; ++q)
 #pragma unroll
-                for (int i = 0; i < 32; ++i) sv[c + q][i] = (w >> i) & 1 ? sv[c + q][i] : 0xff800000u;
-              }
+                for (int i = 0; i < 32; ++i) sv[c + q][i] = (mask[c + q] >> i) & 1 ? sv[c + q][i] : 0xff800000u;
             }
           };
           auto add_max = [&](int c) {
@@ -934,30 +981,19 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                 mxp[(i >> 1) & 7] = fmax3(mxp[(i >> 1) & 7], __uint_as_float(sv[c + q][i]),
                                           __uint_as_float(sv[c + q][i + 1]));
           };
-          if constexpr (C::kHeld) {
-            tc::ld32_async(tS, sv[0]);
-            tc::ld32_async(tS + 32, sv[1]);
-            tc::wait_ld(sv[0], sv[1]);
-            if constexpr (KV == 128) {  // the second half on its way during the first's maximum
-              tc::ld32_async(tS + 64, sv[2]);
-              tc::ld32_async(tS + 96, sv[3]);
-            }
-            fetched(0, 0);
-            add_max(0);
-            if constexpr (KV == 128) {
-              tc::wait_ld(sv[2], sv[3]);
-              fetched(2, 1);
-              add_max(2);
-            }
-          } else {
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-              tc::ld32_async(tS + 64 * h, sv[0]);
-              tc::ld32_async(tS + 64 * h + 32, sv[1]);
-              tc::wait_ld(sv[0], sv[1]);
-              fetched(0, h);
-              add_max(0);
-            }
+          tc::ld32_async(tS, sv[0]);
+          tc::ld32_async(tS + 32, sv[1]);
+          tc::wait_ld(sv[0], sv[1]);
+          if constexpr (KV == 128) {  // the second half on its way during the first's maximum
+            tc::ld32_async(tS + 64, sv[2]);
+            tc::ld32_async(tS + 96, sv[3]);
+          }
+          fetched(0);
+          add_max(0);
+          if constexpr (KV == 128) {
+            tc::wait_ld(sv[2], sv[3]);
+            fetched(2);
+            add_max(2);
           }
           const float mxr = fmaxf(fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])),
                                   fmaxf(fmaxf(mxp[4], mxp[5]), fmaxf(mxp[6], mxp[7])));
@@ -1048,8 +1084,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             tc::fence_before_sync();
             mbar_arrive(bar(kBarP + buf));
           } else {
-            // P = 2^(s * sc - ms + kLift), packed in pairs over the columns of the scores
-            // just used; the last half is still in registers. It is rounded to the
+            // P = 2^(s * sc - ms + kLift), packed in pairs over the scores' columns, which are
+            // all in registers by now. It is rounded to the
             // products' 16-bit type, which the tensor core needs beside V's, against sums
             // in fp32 of the unrounded ones: at most 2^-8 of each weight for bf16, for f16
             // 2^-11 of it and, where it is subnormal, 2^-32 of the reference's weight.
@@ -1074,23 +1110,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             };
             // half of the weights, which the products start on, then the other half
             using Half = std::integral_constant<int, KV / 4>;
-            if constexpr (C::kHeld) {
-              weigh(0, 0, 0, Half());
-            } else {
-              weigh(0, 0, 64, Half());  // (the second half of the scores is in registers)
-            }
+            weigh(0, 0, 0, Half());
             tc::wait_st();
             tc::fence_before_sync();
             mbar_arrive(bar(kBarP + buf));
-            if constexpr (C::kHeld) {
-              weigh(KV == 128 ? 2 : 0, KV == 128 ? 0 : 32, half_col(KV, 1), Half());
-            } else {
-              tc::ld32_async(tS, sv[0]);
-              tc::ld32_async(tS + 32, sv[1]);
-              tc::wait_ld(sv[0], sv[1]);
-              fetched(0, 0);
-              weigh(0, 0, 0, Half());
-            }
+            weigh(KV == 128 ? 2 : 0, KV == 128 ? 0 : 32, half_col(KV, 1), Half());
             const float2 s01 = __fadd2_rn(sp[0], sp[1]), s23 = __fadd2_rn(sp[2], sp[3]);
             const float2 st = __fadd2_rn(s01, s23);
             l += st.x + st.y;
@@ -1103,7 +1127,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         tc::fence_before_sync();
         mbar_arrive(bar(kBarP2 + buf));
       }
-      tiles += it.nt;
+      tiles += nt;
       if (!ok) break;
       // the statistics, once the last ones have been read
       if (done > 0 && !(ok = wait_all(bar(kBarOFree + x), done - 1))) break;
