@@ -33,8 +33,6 @@
 // of two to f16's range, which the row's score scale undoes.
 #include <float.h>
 
-#include <type_traits>
-
 #include "attn_tc.cuh"
 #include "packed_ops.h"
 #include "pa_internal.h"
@@ -60,7 +58,8 @@ constexpr int kMaxStages = 4;
 // Barriers: K and V rings (full, empty); per S buffer: computed, half of P written, the
 // other half, product with V complete; Q staged (items in turn) and done with; per group: last product of an item complete,
 // O and statistics read, statistics written; FP8: converted K and V (two buffers each)
-// written and read; per group: a tile's V looked through; the end.
+// written and read; per group: a tile's V looked through; per softmax warp:
+// its weights of a job taken; the end.
 enum {
   kBarKFull = 0,
   kBarKEmpty = kBarKFull + kMaxStages,
@@ -80,7 +79,8 @@ enum {
   kBarCVFull = kBarCKFree + 2,
   kBarCVFree = kBarCVFull + 2,
   kBarLook = kBarCVFree + 2,
-  kBarDrain = kBarLook + 2,
+  kBarTurn = kBarLook + 2,
+  kBarDrain = kBarTurn + 8,
   kNumBars = kBarDrain + 2
 };
 
@@ -101,7 +101,7 @@ struct Cfg {
   // times slower.)
   static constexpr bool kSplitRegs = kThreads == 512;
   static constexpr int kLaunchRegs = kSplitRegs ? 128 : 168;
-  static constexpr int kSoftmaxRegs = 192, kStoreRegs = 88, kOtherRegs = 40;
+  static constexpr int kSoftmaxRegs = FP8 ? 184 : 192, kStoreRegs = FP8 ? 104 : 88, kOtherRegs = 40;
   static_assert(kThreads == 384 || (kThreads == 512 && kGroups == 2 && 2 * kSoftmaxRegs + kStoreRegs +
                                                                            kOtherRegs == 4 * kLaunchRegs),
                 "registers of the block");
@@ -345,6 +345,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     mbar_init(bar(kBarQFull), FP8 ? 128 : 1);
     mbar_init(bar(kBarQFull + 1), FP8 ? 128 : 1);
     mbar_init(bar(kBarQFree), 1);
+    for (int i = 0; i < 8; ++i) mbar_init(bar(kBarTurn + i), 1);
     mbar_init(bar(kBarDrain), 1);
     mbar_init(bar(kBarDrain + 1), 1);
     sts_b32(base + C::kSkip, 0);
@@ -761,7 +762,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           const uint32_t from = src + r0 * 128 + (((ch & 7) ^ (r0 & 7)) << 4);
           const uint32_t lo = dst + r0 * 128 + ((c16 ^ (r0 & 7)) << 4);
           const uint32_t hi = dst + r0 * 128 + (((c16 + 1) ^ (r0 & 7)) << 4);
-#pragma unroll
+#pragma unroll 2
           for (int k = 0; k < kOctets; k += 4) {
             uint32_t w[4] = {0u, 0u, 0u, 0u}, h[8];
             if (r0 + 8 * k >= r_lo && r0 + 8 * k < r_hi) lds_v4(from + 1024 * k, w[0], w[1], w[2], w[3]);
@@ -815,13 +816,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       }
       if (ok && last >= 0) store(items.get(last));
     } else {
-      PackedItem it = items.get(0);
 #pragma unroll 1
-      for (int k = 0; ok && k < items.count; ++k) {
-        const PackedItem ahead = items.get(k + 1);
-        store(it);
-        it = ahead;
-      }
+      for (int k = 0; ok && k < items.count; ++k) store(items.get(k));
     }
     if (!ok && lane == 0) atomicOr(a.err, PA_DEVERR_TIMEOUT);
   } else {
@@ -959,13 +955,23 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         }
         if (!(ok = wait_all(bar(kBarS + buf), phase))) break;
         tc::fence_after_sync();
+        // the other group's warp has taken the weights of the job before
+        auto my_turn = [&]() {
+          if (NX == 2 && (mine > 0 || x == 1)) ok = wait_all(bar(kBarTurn + (warp ^ 4)), mine - (x ^ 1)) && ok;
+          return ok;
+        };
         if (alive) {
           uint32_t sv[KV / 32][32];
-          float mxp[8];  // eight independent partial maxima (raw scores)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) mxp[i] = -INFINITY;
+          const bool old = j != j0;  // O holds something
+          tc::ld32_async(tS, sv[0]);
+          tc::ld32_async(tS + 32, sv[1]);
+          tc::wait_ld(sv[0], sv[1]);
+          if constexpr (KV == 128) {  // the second half on its way during the first's maximum
+            tc::ld32_async(tS + 64, sv[2]);
+            tc::ld32_async(tS + 96, sv[3]);
+          }
           // masked scores of two rows of sv as -inf
-          auto fetched = [&](int c) {
+          auto mask_out = [&](int c) {
             if (!all_in) {
 #pragma unroll
               for (int q = 0; q < 2; ++q)
@@ -973,6 +979,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                 for (int i = 0; i < 32; ++i) sv[c + q][i] = (mask[c + q] >> i) & 1 ? sv[c + q][i] : 0xff800000u;
             }
           };
+          mask_out(0);
+          float mxp[8];  // eight independent partial maxima (raw scores)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) mxp[i] = -INFINITY;
           auto add_max = [&](int c) {
 #pragma unroll
             for (int q = 0; q < 2; ++q)
@@ -981,50 +991,68 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                 mxp[(i >> 1) & 7] = fmax3(mxp[(i >> 1) & 7], __uint_as_float(sv[c + q][i]),
                                           __uint_as_float(sv[c + q][i + 1]));
           };
-          tc::ld32_async(tS, sv[0]);
-          tc::ld32_async(tS + 32, sv[1]);
-          tc::wait_ld(sv[0], sv[1]);
-          if constexpr (KV == 128) {  // the second half on its way during the first's maximum
-            tc::ld32_async(tS + 64, sv[2]);
-            tc::ld32_async(tS + 96, sv[3]);
-          }
-          fetched(0);
           add_max(0);
           if constexpr (KV == 128) {
             tc::wait_ld(sv[2], sv[3]);
-            fetched(2);
+            mask_out(2);
             add_max(2);
           }
           const float mxr = fmaxf(fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])),
                                   fmaxf(fmaxf(mxp[4], mxp[5]), fmaxf(mxp[6], mxp[7])));
           const float mx = fmaxf(mxr * sc, kFloor);
           const bool grow = mx > ms + kRescaleAbove;
-          const bool old = j != j0;  // O holds something
           if (!old) {
-            ms = mx;
+            ms = mx;  // nothing accumulated yet
           } else if (__any_sync(kFull, grow)) {
-            // O is complete up to the group's last job: with two groups S was issued
-            // after its product; one group has to wait for it
+            // O is complete up to the group's last job: with two groups S was issued after
+            // its product; one group has to wait for it
             if (NX == 1) ok = wait_all(bar(kBarO + (buf ^ 1)), (mine - 1) >> 1);
             tc::fence_after_sync();
             const float alpha = grow ? ex2(ms - mx) : 1.f;
 #pragma unroll 1
-            for (int d0 = 0; d0 < D; d0 += 32) {
-              uint32_t ov[32];
-              tc::ld32_async(tO + d0, ov);
-              tc::wait_ld(ov);
+            for (int d0 = 0; d0 < D; d0 += 16) {
+              uint32_t ov[16];
+              tc::ld16(tO + d0, ov);
               const float2 a2 = make_float2(alpha, alpha);
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) {
+              for (int i = 0; i < 16; i += 2) {
                 const float2 o = __fmul2_rn(score_pair(ov, i), a2);
                 ov[i] = __float_as_uint(o.x);
                 ov[i + 1] = __float_as_uint(o.y);
               }
-              tc::st32(tO + d0, ov);
+              tc::st16(tO + d0, ov);
             }
             l *= alpha;
             if (grow) ms = mx;
           }
+          // P = 2^(s * sc - ms + kLift), packed in pairs over the scores' columns. It is
+          // rounded to the products' 16-bit type, which the tensor core needs beside V's,
+          // against sums in fp32 of the unrounded ones: at most 2^-8 of each weight for
+          // bf16, for f16 2^-11 of it and, where it is subnormal, 2^-32 of the reference's
+          // weight.
+          const float2 sc2 = make_float2(sc, sc);
+          float2 sp[4];
+          // half of the tile's weights, from score `first` of sv rows c ..., to column col
+          auto weigh = [&](int c, int first, int col) {
+            const float2 nms2 = make_float2(kLift - ms, kLift - ms);
+#pragma unroll
+            for (int q = 0; q < KV / 64; ++q) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const int e = first + 32 * q + 2 * i;
+                const float2 t = __ffma2_rn(score_pair(sv[c + (e >> 5)], e & 31), sc2, nms2);
+                const float p0 = ex2(t.x), p1 = ex2(t.y);
+                sp[i & 3] = __fadd2_rn(sp[i & 3], make_float2(p0, p1));
+                pk[i] = pack16x2<kBf16>(p0, p1);
+              }
+              tc::st16(tS + col + 16 * q, pk);
+            }
+          };
+          // The two warps of a processor share its exponential unit (1,024 cycles for both
+          // of 2,100 of products): they take turns, job by job, so that one group's weights
+          // are ready while the products of the other's run, and not both at once.
+          if (!my_turn()) break;
           if (skip) {
             // Infinities or NaN in V: weights times rows on the CUDA cores, attended
             // positions only.
@@ -1084,45 +1112,24 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             tc::fence_before_sync();
             mbar_arrive(bar(kBarP + buf));
           } else {
-            // P = 2^(s * sc - ms + kLift), packed in pairs over the scores' columns, which are
-            // all in registers by now. It is rounded to the
-            // products' 16-bit type, which the tensor core needs beside V's, against sums
-            // in fp32 of the unrounded ones: at most 2^-8 of each weight for bf16, for f16
-            // 2^-11 of it and, where it is subnormal, 2^-32 of the reference's weight.
-            const float2 sc2 = make_float2(sc, sc), nms2 = make_float2(kLift - ms, kLift - ms);
-            float2 sp[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) sp[i] = make_float2(0.f, 0.f);
-            // N pairs of scores from sv rows c ..., to column col
-            auto weigh = [&](int c, int first, int col, auto n) {
-              constexpr int N = decltype(n)::value;
-              uint32_t pk[N];
-#pragma unroll
-              for (int i = 0; i < N; ++i) {
-                const int e = first + 2 * i;
-                const float2 t = __ffma2_rn(score_pair(sv[c + (e >> 5)], e & 31), sc2, nms2);
-                const float p0 = ex2(t.x), p1 = ex2(t.y);
-                sp[i & 3] = __fadd2_rn(sp[i & 3], make_float2(p0, p1));
-                pk[i] = pack16x2<kBf16>(p0, p1);
-              }
-              if constexpr (N == 32) tc::st32(tS + col, pk);
-              else tc::st16(tS + col, pk);
-            };
             // half of the weights, which the products start on, then the other half
-            using Half = std::integral_constant<int, KV / 4>;
-            weigh(0, 0, 0, Half());
+            weigh(0, 0, 0);
             tc::wait_st();
             tc::fence_before_sync();
             mbar_arrive(bar(kBarP + buf));
-            weigh(KV == 128 ? 2 : 0, KV == 128 ? 0 : 32, half_col(KV, 1), Half());
+            weigh(KV == 128 ? 2 : 0, KV == 128 ? 0 : 32, half_col(KV, 1));
             const float2 s01 = __fadd2_rn(sp[0], sp[1]), s23 = __fadd2_rn(sp[2], sp[3]);
             const float2 st = __fadd2_rn(s01, s23);
             l += st.x + st.y;
           }
         } else {
+          if (!my_turn()) break;
           mbar_arrive(bar(kBarP + buf));
         }
         if (!ok) break;
+        if (NX == 2 && lane == 0) mbar_arrive(bar(kBarTurn + warp));
         tc::wait_st();
         tc::fence_before_sync();
         mbar_arrive(bar(kBarP2 + buf));
