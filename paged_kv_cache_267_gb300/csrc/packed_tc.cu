@@ -29,8 +29,9 @@
 //
 // FP8 caches: the storing warps turn each raw e4m3 tile into the f16 tile that the products
 // read (exact), in two buffers each for K and V, and store an item's results between the
-// next one's first tiles. Q goes through them as well: they rescale it per row by a power
-// of two to f16's range, which the row's score scale undoes.
+// next one's first tiles. A bf16 Q becomes f16 in its place, a thread a row, after a
+// rescale of the row by a power of two to f16's range, which its score scale undoes.
+// (Through registers, loaded by warps along the rows, it had taken 10 us an item.)
 #include <float.h>
 
 #include "attn_tc.cuh"
@@ -56,7 +57,8 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kMaxStages = 4;
 
 // Barriers: K and V rings (full, empty); per S buffer: computed, half of P written, the
-// other half, product with V complete; Q staged (items in turn) and done with; per group: last product of an item complete,
+// other half, product with V complete; Q loaded, ready (items in turn) and done with; per
+// group: last product of an item complete,
 // O and statistics read, statistics written; FP8: converted K and V (two buffers each)
 // written and read; per group: a tile's V looked through; per softmax warp:
 // its weights of a job taken; the end.
@@ -69,7 +71,8 @@ enum {
   kBarP = kBarS + 2,
   kBarP2 = kBarP + 2,
   kBarO = kBarP2 + 2,
-  kBarQFull = kBarO + 2,
+  kBarQRaw = kBarO + 2,
+  kBarQFull = kBarQRaw + 1,
   kBarQFree = kBarQFull + 2,
   kBarOFull = kBarQFree + 1,
   kBarOFree = kBarOFull + 2,
@@ -298,6 +301,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                           const __grid_constant__ CUtensorMap tmQ, const PackedArgs a) {
   using C = Cfg<D, FP8>;
   constexpr bool kBf16 = !FP8 && QT == kBF16;  // operand type of the products
+  constexpr bool kConvertQ = FP8 && QT == kBF16;
   constexpr float kLift = kBf16 ? 0.f : kF16Lift;
   constexpr int NX = C::kGroups, KV = C::kKv;
   // Positions of the K and V tiles in use, and the barriers that say they are ready:
@@ -321,7 +325,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
   if (tid == 0) {
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
-    if (!FP8) tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmQ);
     for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(bar(kBarKFull + i), 1);
       mbar_init(bar(kBarKEmpty + i), FP8 ? 128 : 1);
@@ -342,8 +346,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       mbar_init(bar(kBarCVFree + i), 1);
       mbar_init(bar(kBarLook + i), 4);
     }
-    mbar_init(bar(kBarQFull), FP8 ? 128 : 1);
-    mbar_init(bar(kBarQFull + 1), FP8 ? 128 : 1);
+    mbar_init(bar(kBarQRaw), 1);
+    mbar_init(bar(kBarQFull), kConvertQ ? 128 : 1);
+    mbar_init(bar(kBarQFull + 1), kConvertQ ? 128 : 1);
     mbar_init(bar(kBarQFree), 1);
     for (int i = 0; i < 8; ++i) mbar_init(bar(kBarTurn + i), 1);
     mbar_init(bar(kBarDrain), 1);
@@ -457,14 +462,14 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           const int nt = __shfl_sync(kFull, it.nt, 0);
           const bool dual = __any_sync(kFull, is_dual(it));
           if (nt == 0) continue;
-          if (!FP8) {
+          {
             // Q, once the last item's products are done with it: a row tile's tokens times
             // the group's heads are one box a 64 head dims. (Rows behind the unit's are
             // other sequences', or zeros behind the last: not used.)
             if (live > 0 && !(ok = wait_all(bar(kBarQFree), live - 1))) break;
             if (lane == 0) {
               const int row_tiles = dual ? 2 : 1;
-              const uint32_t full = bar(kBarQFull + (live & 1));
+              const uint32_t full = bar(kConvertQ ? kBarQRaw : kBarQFull + (live & 1));
               mbar_arrive_expect_tx(full, row_tiles * C::kBoxes * a.tpg * a.G * 128);
               for (int xt = 0; xt < row_tiles; ++xt)
 #pragma unroll
@@ -475,7 +480,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             __syncwarp();
           }
           if (!(ok = wait_all(bar(kBarQFull + (live & 1)), live >> 1))) {
-            if (!FP8) (void)mbar_wait_bounded(bar(kBarQFull + (live & 1)), (live >> 1) & 1, kDrainNs);
+            if (kConvertQ) (void)mbar_wait_bounded(bar(kBarQRaw), live & 1, kDrainNs);
+            else (void)mbar_wait_bounded(bar(kBarQFull + (live & 1)), (live >> 1) & 1, kDrainNs);
             break;  // (no copy outlives the CTA)
           }
           ++live;
@@ -494,6 +500,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       } else {
         constexpr uint32_t idO = tc::idesc_f16(kRows, D, kBf16, true);
         const uint64_t dV = tc::sdesc_sw128(sVt, C::kBox, 1024);
+        int left = 0;  // jobs of this item
         // of each group: items begun in its O (the parity is all that counts, a bit each),
         // whether there was one, whether O holds something of this item
         uint32_t o_items = 0, o_any = 0, begun = 0;
@@ -524,6 +531,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           commit_all(bar(kBarO + x));
           begun |= 1u << g;
           ++jobs;
+          // the group's last of this item: with two groups one of the last two
+          if (--left < NX) {
+            commit_all(bar(kBarOFull + g));
+            begun &= ~(1u << g);
+          }
         };
         PackedItem ahead = items.get(0);
         for (int k = 0; ok && k < count; ++k) {
@@ -532,6 +544,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           const int nt = __shfl_sync(kFull, it.nt, 0);
           const bool dual = __any_sync(kFull, is_dual(it));
           if (nt == 0) continue;
+          left = dual ? 2 * nt : nt;
 #pragma unroll 1
           for (int n = 0; n < nt; ++n) {
             if (!(ok = wait_all(bar(kVReady + ring.stage), ring.phase))) break;
@@ -542,10 +555,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             ring.next(VB);
             ++done;
           }
-          // each group's O is complete
-          if (begun & 1) commit_all(bar(kBarOFull));
-          if (begun & 2) commit_all(bar(kBarOFull + 1));
-          begun = 0;
         }
       }
       // no product and no arrival outlives the CTA
@@ -566,91 +575,46 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     const int wr0 = (warp - C::kStoreWarp) * 32;  // first row of this warp
     const int r = wr0 + lane;                   // row = tensor-memory lane
     const uint32_t trow = tmem + (static_cast<uint32_t>(wr0) << 16);
-    constexpr int kCh = D / 8, kPer = 32 / kCh;  // 16-byte chunks a row, rows at once
-    const int sub_r = lane / kCh, ch = lane % kCh;
     const uint32_t mul = (65536u + a.G - 1) / a.G;  // row / G = row * mul >> 16, rows < 256
-    // FP8: Q rows of an item -> shared memory (K-major, 128-byte swizzle); rows beside
-    // the unit's are zeros, up to whole warps.
-    auto stage_q = [&](const PackedItem& it, uint32_t which) {
-      const int tiles = is_dual(it) ? 2 : 1;
-      for (int xt = 0; xt < tiles; ++xt) {
-        const int rows = min(it.ntok - xt * a.tpg, a.tpg) * a.G;
-        if (wr0 >= rows) continue;
-        const uint32_t q_tile = sQ + xt * C::kQBytes + (ch >> 3) * C::kQBox;
-        const uint16_t* q0 = static_cast<const uint16_t*>(a.q) +
-                             static_cast<size_t>(it.row0 + xt * a.tpg) * a.q_stride +
-                             static_cast<size_t>(it.kvh) * a.G * D;
-        constexpr int kBatch = 4;  // loads in flight
-#pragma unroll 1
-        for (int i0 = 0; i0 < kCh; i0 += kBatch) {
-          uint4 v[kBatch];
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            const int rr = wr0 + (i0 + i) * kPer + sub_r;
-            const int t = static_cast<int>((rr * mul) >> 16), h = rr - t * a.G;
-            v[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (rr < rows)
-              v[i] = reinterpret_cast<const uint4*>(q0 + t * a.q_stride + h * D)[ch];
-          }
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            const int rr = wr0 + (i0 + i) * kPer + sub_r;
-            // f16 after a power-of-two rescale: largest magnitude in [2^14, 2^15)
-            const uint32_t w4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-            float amax = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f32_of<QT>(w4[e >> 1], e & 1)));
-#pragma unroll
-            for (int o = kCh / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
-            // 2^-sh from its exponent bits; below 2^-111 (scores that are zero for any
-            // weight) the largest stays under 2^14, as does zero
-            const int ex = static_cast<int>(__float_as_uint(amax) >> 23);  // 255: inf
-            const int sh = ex == 255 ? 0 : max(ex - 141, -126);
-            const float m = __int_as_float((127 - sh) << 23);
-            const float2 m2 = make_float2(m, m);
-            uint32_t o4[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 t = __fmul2_rn(make_float2(f32_of<QT>(w4[e], 0), f32_of<QT>(w4[e], 1)), m2);
-              o4[e] = pack16x2<false>(t.x, t.y);
-            }
-            v[i] = make_uint4(o4[0], o4[1], o4[2], o4[3]);
-            if (ch == 0) sts_s8(base + C::kShift + (which & 1) * NX * kRows + xt * kRows + rr, sh);
-            sts_v4(q_tile + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4), v[i]);
-          }
-        }
-      }
-      fence_proxy_async();
-      mbar_arrive(bar(kBarQFull + (which & 1)));
-    };
     bool ok = true;
     uint32_t o_items = 0;  // items of each group so far (the parity, a bit each)
     uint32_t jobs = 0;
     // the results of an item, items in order
-    auto store = [&](const PackedItem& it) {
-      const bool dual = is_dual(it);
-      const int nj = jobs_of(it);
+    auto store = [&](int k) {
+      const PackedItem item = items.get(k);  // (into uniform registers)
+      const int ntok = __shfl_sync(kFull, item.ntok, 0), nt = __shfl_sync(kFull, item.nt, 0);
+      const int row0 = __shfl_sync(kFull, item.row0, 0), kvh = __shfl_sync(kFull, item.kvh, 0);
+      const int slot = __shfl_sync(kFull, item.slot, 0);
+      const bool dual = NX == 2 && ntok > a.tpg;
+      const int nj = dual ? 2 * nt : nt;
       const uint32_t s = jobs & 1;  // group of the item's first job
       jobs += nj;
       const int g0 = NX == 2 ? static_cast<int>(s) : 0;  // the group with the first job
       const bool both = NX == 2 && nj > 1;
-      // the groups' results of this item are complete
-      if (nj > 0) {
-        for (int q = 0; q < (both ? 2 : 1); ++q) {
-          const int g = g0 ^ q;
-          if (!(ok = wait_all(bar(kBarOFull + g), o_items >> g))) return;
-          if (!(ok = wait_all(bar(kBarStat + g), o_items >> g))) return;
-          o_items ^= 1u << g;
-        }
+      // a group's result of this item is complete
+      auto complete = [&](int g) {
+        ok = ok && wait_all(bar(kBarOFull + g), o_items >> g) && wait_all(bar(kBarStat + g), o_items >> g);
+        o_items ^= 1u << g;
         tc::fence_after_sync();
-      }
+        return ok;
+      };
       const bool join = both && !dual;  // both groups' O are the same rows'
 #pragma unroll 1
       for (int q = 0; q < (dual ? 2 : 1); ++q) {
         const int xt = dual ? g0 ^ q : 0;  // row tile (the group of the first job first)
         const int ga = dual ? xt : g0;     // the group whose O holds its rows
-        const int rows = min(it.ntok - xt * a.tpg, a.tpg) * a.G;
-        if (wr0 < rows) {
+        const int rows = min(ntok - xt * a.tpg, a.tpg) * a.G;
+        if (nj > 0 && (!complete(ga) || (join && !complete(ga ^ 1)))) return;
+        auto release = [&]() {  // the groups may go on in O
+          if (nj > 0) {
+            tc::fence_before_sync();
+            mbar_arrive(bar(kBarOFree + ga));
+            if (join) mbar_arrive(bar(kBarOFree + (ga ^ 1)));
+          }
+        };
+        if (wr0 >= rows) {
+          release();
+        } else {
           float m = kFloor, l = 0.f, f_own = 0.f, f_other = 0.f;
           if (nj > 0) {
             lds_f32x2(base + C::kStat + (ga * kRows + r) * 8, m, l);
@@ -682,14 +646,14 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             }
           };
           const int r4 = wr0 + (lane & ~3);  // rows r4 .. r4 + 3 are this lane's to store
-          if (it.slot < 0) {
-            // an empty row is zeros; a NaN in the sum stays one
+          if (slot < 0) {
+            // an empty row is zeros (its O is, as its weights were); a NaN in the sum stays one
             const float inv = l == 0.f ? 0.f : a.v_scale / l;
             f_own *= inv;
             f_other *= inv;
             uint16_t* const out = static_cast<uint16_t*>(a.out) +
-                                  static_cast<size_t>(it.row0 + xt * a.tpg) * a.out_stride +
-                                  static_cast<size_t>(it.kvh) * a.G * D + 8 * (lane & 3);
+                                  static_cast<size_t>(row0 + xt * a.tpg) * a.out_stride +
+                                  static_cast<size_t>(kvh) * a.G * D + 8 * (lane & 3);
             int at[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -704,10 +668,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                 uint32_t v[16];
                 take(d0 + 16 * e, v);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)  // (an empty row: whatever O holds)
-                  p[8 * e + i] = l == 0.f ? 0u : pack16x2<QT == kBF16>(__uint_as_float(v[2 * i]),
-                                                                       __uint_as_float(v[2 * i + 1]));
+                for (int i = 0; i < 8; ++i)
+                  p[8 * e + i] = pack16x2<QT == kBF16>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
               }
+              if (d0 + 32 == D) release();  // before the last stores
               transpose4(p, lane);
 #pragma unroll
               for (int i = 0; i < 4; ++i)
@@ -718,7 +682,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           } else {
             f_own *= a.v_scale;
             f_other *= a.v_scale;
-            float* const part = a.part + static_cast<size_t>(it.slot) * packed_slot_floats(a.slot_rows, D);
+            float* const part = a.part + static_cast<size_t>(slot) * packed_slot_floats(a.slot_rows, D);
             float* const to = part + static_cast<size_t>(xt * kRows + r4) * D + 4 * (lane & 3);
 #pragma unroll 1
             for (int d0 = 0; d0 < D; d0 += 16) {
@@ -736,12 +700,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
               stat[0] = m - kLift;
               stat[a.slot_rows] = l;
             }
+            release();
           }
-        }
-        if (nj > 0) {
-          tc::fence_before_sync();
-          mbar_arrive(bar(kBarOFree + ga));
-          if (join) mbar_arrive(bar(kBarOFree + (ga ^ 1)));
         }
       }
     };
@@ -776,8 +736,46 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           }
         }
       };
+      // this thread's rows of Q, bf16 -> f16 in their place: largest magnitude in
+      // [2^14, 2^15); rows beside the unit's stay whatever they are
+      auto convert_q = [&](int ntok, uint32_t which) {
+#pragma unroll 1
+        for (int xt = 0; xt < (NX == 2 && ntok > a.tpg ? 2 : 1); ++xt) {
+          if (r >= min(ntok - xt * a.tpg, a.tpg) * a.G) continue;
+          const uint32_t row = sQ + xt * C::kQBytes + r * 128;
+          auto chunk = [&](int i) { return row + (i >> 3) * C::kQBox + (((i & 7) ^ (r & 7)) << 4); };
+          uint32_t top = 0;  // largest magnitudes of the even and the odd elements, as bits
+#pragma unroll 4
+          for (int i = 0; i < D / 8; ++i) {
+            uint32_t w[4];
+            lds_v4(chunk(i), w[0], w[1], w[2], w[3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = __vmaxu2(top, w[e] & 0x7fff7fffu);
+          }
+          // 2^-sh from its exponent bits; below 2^-111 (scores that are zero for any
+          // weight) the largest stays under 2^14, as does zero
+          const int ex = static_cast<int>(max(top >> 16, top & 0xffffu) >> 7);  // 255: inf
+          const int sh = ex == 255 ? 0 : max(ex - 141, -126);
+          const float m = __int_as_float((127 - sh) << 23);
+          const float2 m2 = make_float2(m, m);
+#pragma unroll 4
+          for (int i = 0; i < D / 8; ++i) {
+            uint32_t w[4];
+            lds_v4(chunk(i), w[0], w[1], w[2], w[3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 t = __fmul2_rn(make_float2(f32_of<QT>(w[e], 0), f32_of<QT>(w[e], 1)), m2);
+              w[e] = pack16x2<false>(t.x, t.y);
+            }
+            sts_v4(chunk(i), make_uint4(w[0], w[1], w[2], w[3]));
+          }
+          sts_s8(base + C::kShift + (which & 1) * NX * kRows + xt * kRows + r, sh);
+        }
+        fence_proxy_async();
+        mbar_arrive(bar(kBarQFull + (which & 1)));
+      };
       int c = 0;                  // tiles so far
-      uint32_t staged = 0;        // items whose Q is staged
+      uint32_t live = 0;          // items with tiles so far
       int last = -1;              // the item whose results are to be stored
 #pragma unroll 1
       for (int k = 0; ok && k < items.count; ++k) {
@@ -789,7 +787,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           v_lo = it.lo - start;
           v_hi = it.hi + 1 - start;
         }
-        if (nt == 0) store(items.get(k));
+        if (nt == 0) store(k);
 #pragma unroll 1
         for (int n = 0; ok && n < nt; ++n, ++c) {
           const uint32_t free_par = (c - 2) >> 1;  // of the buffers' last tile
@@ -800,9 +798,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           mbar_arrive(bar(kBarCKFull + (c & 1)));
           mbar_arrive(bar(kBarKEmpty));  // reload the stage
           if (n == 0) {
-            if (staged > 0 && !(ok = wait_all(bar(kBarQFree), staged - 1))) break;
-            stage_q(items.get(k), staged);
-            ++staged;
+            if (kConvertQ) {
+              if (!(ok = wait_all(bar(kBarQRaw), live))) break;
+              convert_q(items.get(k).ntok, live);
+            }
+            ++live;
           }
           if (!(ok = wait_all(bar(kBarVFull), c))) break;
           if (c > 1 && !(ok = wait_all(bar(kBarCVFree + (c & 1)), free_par))) break;
@@ -810,14 +810,14 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           fence_proxy_async();
           mbar_arrive(bar(kBarCVFull + (c & 1)));
           mbar_arrive(bar(kBarVEmpty));
-          if (n == 0 && last >= 0) store(items.get(last));
+          if (n == 0 && last >= 0) store(last);
         }
         if (nt > 0) last = k;
       }
-      if (ok && last >= 0) store(items.get(last));
+      if (ok && last >= 0) store(last);
     } else {
 #pragma unroll 1
-      for (int k = 0; ok && k < items.count; ++k) store(items.get(k));
+      for (int k = 0; ok && k < items.count; ++k) store(k);
     }
     if (!ok && lane == 0) atomicOr(a.err, PA_DEVERR_TIMEOUT);
   } else {
@@ -889,9 +889,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       const int sure_lo = a.window > 0 ? last - a.window : -start;
       // (never zero, so that a masked score stays -inf)
       float sc = fmaxf(fabsf(a.score_scale), FLT_MIN);
-      if constexpr (FP8) {
+      if constexpr (kConvertQ) {
         if (!(ok = wait_all(bar(kBarQFull + (which & 1)), which >> 1))) break;
-        if (alive) sc = fmaxf(FLT_MIN, ldexpf(sc, lds_s8(base + C::kShift + (which & 1) * NX * kRows + xt * kRows + r)));
+        if (valid) sc = fmaxf(FLT_MIN, ldexpf(sc, lds_s8(base + C::kShift + (which & 1) * NX * kRows + xt * kRows + r)));
       }
       float ms = kFloor, l = 0.f;  // reference max (scaled, log2 units) and running sum
       for (int j = j0; j < nj; j += step, ++mine) {
