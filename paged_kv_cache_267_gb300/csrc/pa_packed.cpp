@@ -21,11 +21,10 @@ using namespace pa;
 constexpr double k2p31 = 2147483648.0;
 constexpr int64_t kMaxRows = int64_t(1) << 30;
 constexpr int64_t kMaxRowStride = int64_t(1) << 23;
-// Costs of a step (packed_plan.cuh) in tiles of one CTA: least tiles a CTA in split mode,
-// an item's way in and out, the partial results of a split and their join.
-constexpr int kMinTiles = 2;
-constexpr int kUnitTiles = 1;
-constexpr int kSplitTiles = 4;
+// Costs of a step in places (packed_plan.cuh): least share of a CTA in split mode, the
+// partial results of a split and their join.
+constexpr int kMinPlaces = 8;
+constexpr int kSplitPlaces = 16;
 
 bool misaligned(const pa_tensor* t, uintptr_t n) {
   return numel(t) > 0 && reinterpret_cast<uintptr_t>(t->data) % n;
@@ -71,7 +70,7 @@ pa_status check_rows(const pa_tensor* t, const char* name) {
 // What a ragged step launches, from its host-known sizes.
 struct PackedSizes {
   int tpg, tpu, kv, slot_rows, ctas;
-  size_t items, plan_words, part_at, bytes;
+  size_t plan_words, part_at, bytes;
 };
 
 PackedSizes packed_sizes(int64_t T, int64_t B, int64_t span, int G, int64_t Hkv, int D, int num_sms) {
@@ -83,9 +82,8 @@ PackedSizes packed_sizes(int64_t T, int64_t B, int64_t span, int G, int64_t Hkv,
   z.slot_rows = shape.rows == 2 && T > z.tpg ? 256 : 128;
   const int64_t units = T / z.tpu + std::min(B, T);  // at most
   const double tiles = dprod({double(units), double(Hkv), double(span / z.kv + 2)});
-  z.ctas = static_cast<int>(std::min<double>(num_sms, std::max(1.0, std::ceil(tiles / kMinTiles))));
-  z.items = static_cast<size_t>(units) * static_cast<size_t>(Hkv) + static_cast<size_t>(z.ctas);
-  z.plan_words = packed_plan_words(z.ctas, z.items);
+  z.ctas = static_cast<int>(std::min<double>(num_sms, std::max(1.0, std::ceil(tiles * 4 / kMinPlaces))));
+  z.plan_words = packed_plan_words(z.ctas, static_cast<size_t>(units));
   // behind the decode workspace's counters, which stay zero
   z.part_at = (256 + z.plan_words * 4 + 255) / 256 * 256;
   z.bytes = z.part_at + 2 * static_cast<size_t>(z.ctas) * packed_slot_floats(z.slot_rows, D) * sizeof(float);
@@ -160,13 +158,8 @@ pa_status packed_attention(const pa_tensor* out, const pa_tensor* q, const pa_te
   if (T > kMaxRows || dprod({double(NB), double(Hkv), double(block_size)}) >= k2p31 || pos >= k2p31 - 4096)
     return fail(PA_ERR_UNSUPPORTED, "pool, tables or rows exceed 32-bit indexing");
   window = window > 0 ? window : 0;
-  const PackedShape shape = packed_shape(static_cast<int>(D));
-  const int64_t tpu = 128 / G * shape.rows;
-  // of a unit: a window's reach and its own tokens (drafted ones: 64)
-  const int64_t span = window > 0 ? std::min<int64_t>(MB * block_size, int64_t(window) + std::max<int64_t>(tpu, 64))
-                                  : MB * block_size;
-  if (dprod({double(T / tpu + std::min(B, T)), double(Hkv), double(span / shape.kv + 8)}) >= k2p31 - 4096)
-    return fail(PA_ERR_UNSUPPORTED, "rows times table width exceed 32-bit indexing");
+  // of a unit: a window's reach and its own tokens (drafted ones: 64), else all of a table
+  const int64_t span = window > 0 ? std::min<int64_t>(MB * block_size, int64_t(window) + 256) : MB * block_size;
   for (const pa_tensor* x : {q, key_cache, value_cache, block_tables, seq_lens, query_start, tree ? tree_mask : q})
     if (overlaps(out, x)) return fail(PA_ERR_INVALID_ARG, "out overlaps an input");
   if (B == 0 || T == 0) return ok();
@@ -203,9 +196,9 @@ pa_status packed_attention(const pa_tensor* out, const pa_tensor* q, const pa_te
     p.tpu = z.tpu;
     p.kv = z.kv;
     p.ctas = z.ctas;
-    p.min_tiles = kMinTiles;
-    p.unit_tiles = kUnitTiles;
-    p.split_tiles = kSplitTiles;
+    p.tpg = z.tpg;
+    p.min_places = kMinPlaces;
+    p.split_places = kSplitPlaces;
     p.tree = tree;
     cudaError_t e = packed_plan_launch(p, cs, true);
     if (e != cudaSuccess) return cuda_fail(e, "packed plan launch");

@@ -22,9 +22,9 @@ struct PackedPlanArgs {
   int tpu;                      // tokens a unit
   int kv;                       // tokens a K/V tile
   int ctas;                     // of the attention
-  int min_tiles;                // least tiles a CTA in split mode
-  int unit_tiles;               // an item's way in and out, in tiles
-  int split_tiles;              // what a split costs, in tiles of one CTA
+  int tpg;                      // tokens a row tile
+  int min_places;               // least places a CTA in split mode
+  int split_places;             // what a split costs a CTA
   bool tree;
 };
 cudaError_t packed_plan_launch(const PackedPlanArgs& a, cudaStream_t s, bool pdl);

@@ -5,17 +5,16 @@
 // Sequence b's queries are the packed rows [query_start[b], query_start[b + 1]).
 // They are cut into units of tpu tokens; the (token, head) rows of a unit and a KV
 // head, at most 256 (128 with head_dim 256), are one matrix Q, and the unit's
-// K/V range is walked in tiles of kv tokens. An item is a run of a unit's tiles
-// that one CTA works through.
-//   - whole mode: every unit is one item; items are sorted by their tiles, most
-//     first, and dealt out to the CTAs there and back (0 .. C-1, C-1 .. 0, ...).
-//   - split mode: the tiles of all units form one flat index space, unit- then KV
-//     head-major, with a few places before each unit's for its way in and out, and
-//     CTA w takes [w * wsz, (w + 1) * wsz) of it. Item u + w is what CTA w has of the
-//     tiles of unit u (counted over KV heads): unique, because the walk through the
-//     (unit, CTA) grid is a monotone staircase. A unit cut between CTAs
-//     leaves a partial result with each, in slot 2 w if it is CTA w's first item,
-//     else 2 w + 1 (its last); the merge joins them.
+// K/V range is walked in tiles of kv tokens. Pair p = unit * Hkv + KV head. An item is
+// what a CTA works through of a pair:
+//   - whole mode: every pair is one item. Units are sorted by their cost, most first; CTA
+//     w begins with pair w and then takes the next one that is left (a counter).
+//   - split mode: the costs of all pairs form one space of places, in which a pair has
+//     kOutPlaces for its way in and out and then tile_places() a tile, and CTA w has the
+//     tiles that begin in [w * wsz, (w + 1) * wsz). A pair cut between CTAs leaves a
+//     partial result with each, in slot 2 w + 1 with the one that has its first tile and
+//     2 w with the others (each CTA has one of either kind at most); the merge joins
+//     them.
 // A unit that attends to nothing counts as one tile (its rows are zeros).
 #pragma once
 
@@ -24,24 +23,30 @@
 
 namespace pa {
 
-struct PackedItem {  // 12 words an item
-  int b, kvh;        // sequence, KV head
+struct PackedUnit {  // 12 words a unit
+  int b;             // sequence
   int row0, ntok;    // first packed row and tokens of the unit
   int pos0;          // position of its first token
   int first;         // position of the sequence's first query
   int lo, hi;        // positions that its rows may attend to
-  int tile0, nt;     // K/V tiles of it, from lo rounded down to 16 tokens
-  int slot;          // partial result, -1: the unit is whole
-  int pad;
+  int nt;            // K/V tiles of it, from lo rounded down to 16 tokens
+  int place;         // split mode: places before it
+  int pad[3];
 };
-struct PackedJoin {  // 8 words a CTA: the unit cut at the CTA's end that starts in it
+struct PackedJoin {  // 8 words a CTA: the pair that begins in it and goes on in the next
   int row0, ntok, kvh;
-  int n;             // partials, 0: none
-  int slot0, slot1;  // the first and the second; each other one is 2 behind the last
-  int pad[2];
+  int n;             // partial results, 0: none
+  int pad[4];
 };
+// Header words: mode, pairs, places a CTA, counter of the pairs taken behind the first.
 constexpr int kPackedHead = 8;
-enum { kPkWhole = 0, kPkItems = 1 };  // header words: mode, items in whole mode
+enum { kPkWhole = 0, kPkPairs = 1, kPkWsz = 2, kPkNext = 3 };
+
+// Costs, in quarters of a tile of two row tiles: a pair's way in and out, a tile. (Of a
+// 16-prompt batch a tile took 3,650 cycles, with one row tile 2,400 where the products
+// bound it and 3,050 where memory did, and a pair 5,500 besides.)
+constexpr int kOutPlaces = 6;
+__host__ __device__ constexpr inline int tile_places(bool dual) { return dual ? 4 : 3; }
 
 struct PackedShape {
   int kv;    // tokens a K/V tile
@@ -56,15 +61,21 @@ __host__ __device__ constexpr inline size_t packed_ctas_at() { return kPackedHea
 __host__ __device__ constexpr inline size_t packed_joins_at(int ctas) {
   return packed_ctas_at() + 2 * static_cast<size_t>((ctas + 1) & ~1);
 }
-__host__ __device__ constexpr inline size_t packed_items_at(int ctas) {
+__host__ __device__ constexpr inline size_t packed_units_at(int ctas) {
   return packed_joins_at(ctas) + 8 * static_cast<size_t>(ctas);
 }
-__host__ __device__ constexpr inline size_t packed_plan_words(int ctas, size_t items) {
-  return packed_items_at(ctas) + 12 * items;
+__host__ __device__ constexpr inline size_t packed_plan_words(int ctas, size_t units) {
+  return packed_units_at(ctas) + 12 * units;
 }
 // Floats of a partial result: `rows` rows of D, their maxima and their sums.
 __host__ __device__ constexpr inline size_t packed_slot_floats(int rows, int D) {
   return static_cast<size_t>(rows) * (D + 2);
+}
+
+// Tiles of a pair that begin before place x, counted from its first tile's.
+__host__ __device__ constexpr inline int tiles_before(int x, int nt, int per) {
+  const int t = x <= 0 ? 0 : (x + per - 1) / per;
+  return t < nt ? t : nt;
 }
 
 }  // namespace pa

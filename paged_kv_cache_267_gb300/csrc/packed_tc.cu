@@ -8,7 +8,8 @@
 // with a running reference m per row, which moves only when a score exceeds it by
 // more than 2^8, and out = O / l.
 //
-// Roles: one warp streams K tiles and one V tiles through rings (TMA through the block
+// Roles: one warp works out the CTA's items, in a ring that all others read them from, and
+// streams K tiles, one streams V tiles (TMA through the block
 // table), one loads Q and issues the products S, one issues the products O, groups of four softmax
 // warps serve a 128-row tile each (one row a thread), and four warps store the results,
 // so that a group goes on with its next item while the last one's output is written.
@@ -54,38 +55,7 @@ constexpr float kRescaleAbove = 8.f;         // log2 units
 // subnormal below 2^-21 of it instead of 2^-14.
 constexpr float kF16Lift = 7.f;              // log2 units
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kMaxStages = 4;
-
-// Barriers: K and V rings (full, empty); per S buffer: computed, half of P written, the
-// other half, product with V complete; Q loaded, ready (items in turn) and done with; per
-// group: last product of an item complete,
-// O and statistics read, statistics written; FP8: converted K and V (two buffers each)
-// written and read; per group: a tile's V looked through; per softmax warp:
-// its weights of a job taken; the end.
-enum {
-  kBarKFull = 0,
-  kBarKEmpty = kBarKFull + kMaxStages,
-  kBarVFull = kBarKEmpty + kMaxStages,
-  kBarVEmpty = kBarVFull + kMaxStages,
-  kBarS = kBarVEmpty + kMaxStages,
-  kBarP = kBarS + 2,
-  kBarP2 = kBarP + 2,
-  kBarO = kBarP2 + 2,
-  kBarQRaw = kBarO + 2,
-  kBarQFull = kBarQRaw + 1,
-  kBarQFree = kBarQFull + 2,
-  kBarOFull = kBarQFree + 1,
-  kBarOFree = kBarOFull + 2,
-  kBarStat = kBarOFree + 2,
-  kBarCKFull = kBarStat + 2,
-  kBarCKFree = kBarCKFull + 2,
-  kBarCVFull = kBarCKFree + 2,
-  kBarCVFree = kBarCVFull + 2,
-  kBarLook = kBarCVFree + 2,
-  kBarTurn = kBarLook + 2,
-  kBarDrain = kBarTurn + 8,
-  kNumBars = kBarDrain + 2
-};
+constexpr int kItemRing = 3;                 // items known at once
 
 template <int D, bool FP8>
 struct Cfg {
@@ -94,6 +64,37 @@ struct Cfg {
   static constexpr int kSlices = kKv / 16;
   static constexpr int kBoxes = D / 64;  // 64-dim boxes of a 16-bit tile
   static constexpr int kKStages = FP8 ? 1 : (D == 64 ? 4 : 2), kVStages = FP8 ? 1 : (D == 64 ? 4 : 3);
+  static constexpr int kStages = kKStages > kVStages ? kKStages : kVStages;
+  // Barriers: K and V rings (full, empty); per S buffer: computed, half of P written, the
+  // other half, product with V complete; Q loaded, ready (items in turn) and done with; per
+  // group: last product of an item complete, O and statistics read, statistics written,
+  // a tile's V looked through; FP8: converted K and V (two buffers each) written and
+  // read; items known and read; the ends of the two product warps.
+  enum {
+    kBarKFull = 0,
+    kBarKEmpty = kBarKFull + kStages,
+    kBarVFull = kBarKEmpty + kStages,
+    kBarVEmpty = kBarVFull + kStages,
+    kBarS = kBarVEmpty + kStages,
+    kBarP = kBarS + 2,
+    kBarP2 = kBarP + 2,
+    kBarO = kBarP2 + 2,
+    kBarQRaw = kBarO + 2,
+    kBarQFull = kBarQRaw + 1,
+    kBarQFree = kBarQFull + 2,
+    kBarOFull = kBarQFree + 1,
+    kBarOFree = kBarOFull + 2,
+    kBarStat = kBarOFree + 2,
+    kBarLook = kBarStat + 2,
+    kBarCKFull = kBarLook + 2,
+    kBarCKFree = kBarCKFull + 2,
+    kBarCVFull = kBarCKFree + 2,
+    kBarCVFree = kBarCVFull + 2,
+    kBarItem = kBarCVFree + 2,
+    kBarItemFree = kBarItem + kItemRing,
+    kBarDrain = kBarItemFree + kItemRing,
+    kNumBars = kBarDrain + 2
+  };
   static constexpr int kStoreWarp = 4 * kGroups, kMmaS = kStoreWarp + 4,
                        kLoadK = kMmaS + 2, kLoadV = kMmaS + 3;  // (the products O behind S)
   static constexpr int kThreads = (kMmaS + 4) * 32;
@@ -104,7 +105,7 @@ struct Cfg {
   // times slower.)
   static constexpr bool kSplitRegs = kThreads == 512;
   static constexpr int kLaunchRegs = kSplitRegs ? 128 : 168;
-  static constexpr int kSoftmaxRegs = FP8 ? 184 : 192, kStoreRegs = FP8 ? 104 : 88, kOtherRegs = 40;
+  static constexpr int kSoftmaxRegs = FP8 ? 176 : 184, kStoreRegs = FP8 ? 104 : 80, kOtherRegs = FP8 ? 56 : 64;
   static_assert(kThreads == 384 || (kThreads == 512 && kGroups == 2 && 2 * kSoftmaxRegs + kStoreRegs +
                                                                            kOtherRegs == 4 * kLaunchRegs),
                 "registers of the block");
@@ -114,14 +115,14 @@ struct Cfg {
   static constexpr uint32_t kRing = kRawBoxes * kBox;                       // ring tile
   // small things first, then the tiles, which start on 1 KB
   static constexpr uint32_t kBar = 0, kSlot = (8 * kNumBars + 15) & ~15, kSkip = kSlot + 8, kLook = kSkip + 8,
-                            kShift = kLook + 32,
+                            kItem = kLook + 32, kShift = kItem + 48 * kItemRing,
                             kStat = kShift + (FP8 ? 2 * kGroups * kRows : 0),
                             kSmall = kStat + kGroups * 2 * kRows * 4;
   static constexpr uint32_t kQ = (kSmall + 1023) / 1024 * 1024, kK = kQ + kGroups * kQBytes,
                             kV = kK + kKStages * kRing, kKc = kV + kVStages * kRing,
                             kVc = kKc + (FP8 ? 2 * kTile : 0), kBytes = kVc + (FP8 ? 2 * kTile : 0);
   static constexpr uint32_t kColS = 0, kColO = 2 * kKv;
-  static_assert(kLook % 16 == 0 && kStat % 8 == 0, "alignment of what is read at once");
+  static_assert(kLook % 16 == 0 && kItem % 16 == 0 && kStat % 8 == 0, "alignment of what is read at once");
   static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
   static_assert(kColO + kGroups * D <= kTmemCols, "tensor memory");
 };
@@ -208,33 +209,16 @@ struct Ring {
   }
 };
 
-// The items of this CTA, in order.
-struct Items {
-  const PackedItem* at;
-  int count, whole, ctas;
-  __device__ __forceinline__ Items(const int32_t* plan, int n) {
-    const PackedItem* items = reinterpret_cast<const PackedItem*>(plan + packed_items_at(n));
-    ctas = n;
-    whole = plan[kPkWhole];
-    const int w = blockIdx.x;
-    if (whole) {  // dealt out there and back
-      const int total = plan[kPkItems], rounds = total / n, left = total - rounds * n;
-      at = items;
-      count = rounds + (((rounds & 1) ? n - 1 - w : w) < left ? 1 : 0);
-    } else {
-      const int2 c = reinterpret_cast<const int2*>(plan + packed_ctas_at())[w];
-      at = items + c.x;
-      count = c.y - c.x;
-    }
-  }
-  // Item k, an empty one behind the last.
-  __device__ __forceinline__ PackedItem get(int k) const {
-    const int w = blockIdx.x;
-    if (k >= count) return PackedItem{};
-    const int4* p = reinterpret_cast<const int4*>(at + (whole ? k * ctas + ((k & 1) ? ctas - 1 - w : w) : k));
-    const int4 x = p[0], y = p[1], z = p[2];
-    return PackedItem{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
-  }
+// What a CTA works through of a pair (packed_plan.cuh).
+struct PackedItem {
+  int b, kvh;        // sequence, KV head
+  int row0, ntok;    // first packed row and tokens of the unit
+  int pos0;          // position of its first token
+  int first;         // position of the sequence's first query
+  int lo, hi;        // positions that its rows may attend to
+  int tile0, nt;     // K/V tiles of it; nt -1: no more items
+  int slot;          // partial result, -1: the unit is whole
+  int pad;
 };
 
 template <int QT>
@@ -304,11 +288,15 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
   constexpr bool kConvertQ = FP8 && QT == kBF16;
   constexpr float kLift = kBf16 ? 0.f : kF16Lift;
   constexpr int NX = C::kGroups, KV = C::kKv;
+  constexpr int kBarS = C::kBarS, kBarP = C::kBarP, kBarP2 = C::kBarP2, kBarO = C::kBarO, kBarQRaw = C::kBarQRaw,
+                kBarQFull = C::kBarQFull, kBarQFree = C::kBarQFree, kBarOFull = C::kBarOFull,
+                kBarOFree = C::kBarOFree, kBarStat = C::kBarStat, kBarLook = C::kBarLook, kBarItem = C::kBarItem,
+                kBarItemFree = C::kBarItemFree;
   // Positions of the K and V tiles in use, and the barriers that say they are ready:
   // the ring's, or the converted buffers' (two of each).
   constexpr int KB = FP8 ? 2 : C::kKStages, VB = FP8 ? 2 : C::kVStages;
-  constexpr int kKReady = FP8 ? kBarCKFull : kBarKFull, kKFree = FP8 ? kBarCKFree : kBarKEmpty;
-  constexpr int kVReady = FP8 ? kBarCVFull : kBarVFull, kVFree = FP8 ? kBarCVFree : kBarVEmpty;
+  constexpr int kKReady = FP8 ? C::kBarCKFull : C::kBarKFull, kKFree = FP8 ? C::kBarCKFree : C::kBarKEmpty;
+  constexpr int kVReady = FP8 ? C::kBarCVFull : C::kBarVFull, kVFree = FP8 ? C::kBarCVFree : C::kBarVEmpty;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t base = smem_addr(smem_raw);
   const uint32_t sQ = base + C::kQ, sK = base + C::kK, sV = base + C::kV;
@@ -326,33 +314,34 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
     tma_prefetch_desc(&tmQ);
-    for (int i = 0; i < kMaxStages; ++i) {
-      mbar_init(bar(kBarKFull + i), 1);
-      mbar_init(bar(kBarKEmpty + i), FP8 ? 128 : 1);
-      mbar_init(bar(kBarVFull + i), 1);
-      mbar_init(bar(kBarVEmpty + i), FP8 ? 128 : 1);
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(bar(C::kBarKFull + i), 1);
+      mbar_init(bar(C::kBarKEmpty + i), FP8 ? 128 : 1);
+      mbar_init(bar(C::kBarVFull + i), 1);
+      mbar_init(bar(C::kBarVEmpty + i), FP8 ? 128 : 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kBarS + i), 1);
       mbar_init(bar(kBarP + i), kGroupThreads);
       mbar_init(bar(kBarP2 + i), kGroupThreads);
       mbar_init(bar(kBarO + i), 1);
+      mbar_init(bar(kBarQFull + i), kConvertQ ? 128 : 1);
       mbar_init(bar(kBarOFull + i), 1);
       mbar_init(bar(kBarOFree + i), 128);
       mbar_init(bar(kBarStat + i), kGroupThreads);
-      mbar_init(bar(kBarCKFull + i), 128);
-      mbar_init(bar(kBarCKFree + i), 1);
-      mbar_init(bar(kBarCVFull + i), 128);
-      mbar_init(bar(kBarCVFree + i), 1);
       mbar_init(bar(kBarLook + i), 4);
+      mbar_init(bar(C::kBarCKFull + i), 128);
+      mbar_init(bar(C::kBarCKFree + i), 1);
+      mbar_init(bar(C::kBarCVFull + i), 128);
+      mbar_init(bar(C::kBarCVFree + i), 1);
+      mbar_init(bar(C::kBarDrain + i), 1);
+    }
+    for (int i = 0; i < kItemRing; ++i) {
+      mbar_init(bar(kBarItem + i), 1);
+      mbar_init(bar(kBarItemFree + i), C::kThreads / 32);
     }
     mbar_init(bar(kBarQRaw), 1);
-    mbar_init(bar(kBarQFull), kConvertQ ? 128 : 1);
-    mbar_init(bar(kBarQFull + 1), kConvertQ ? 128 : 1);
     mbar_init(bar(kBarQFree), 1);
-    for (int i = 0; i < 8; ++i) mbar_init(bar(kBarTurn + i), 1);
-    mbar_init(bar(kBarDrain), 1);
-    mbar_init(bar(kBarDrain + 1), 1);
     sts_b32(base + C::kSkip, 0);
     sts_b32(base + C::kSkip + 4, 0);
     fence_mbar_init();
@@ -364,11 +353,24 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
   const uint32_t tmem = *tslot;
   griddep_wait();  // the plan, and behind it the caches and queries, are written
   griddep_launch_dependents();
-  const Items items(a.plan, a.ctas);
 
-  // An item with more tokens than a row tile has rows for both groups.
-  auto is_dual = [&](const PackedItem& it) { return NX == 2 && it.ntok > a.tpg; };
-  auto jobs_of = [&](const PackedItem& it) { return is_dual(it) ? 2 * it.nt : it.nt; };
+  // Item k from the ring, and done with it (every warp says so, of every item).
+  auto item_at = [&](int k, PackedItem* it) -> bool {
+    const int at = k % kItemRing;
+    if (!wait_all(bar(kBarItem + at), k / kItemRing)) return false;
+    uint32_t w[12];
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      lds_v4(base + C::kItem + 48 * at + 16 * i, w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    *it = PackedItem{static_cast<int>(w[0]), static_cast<int>(w[1]), static_cast<int>(w[2]),  static_cast<int>(w[3]),
+                     static_cast<int>(w[4]), static_cast<int>(w[5]), static_cast<int>(w[6]),  static_cast<int>(w[7]),
+                     static_cast<int>(w[8]), static_cast<int>(w[9]), static_cast<int>(w[10]), 0};
+    return true;
+  };
+  auto item_done = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(kBarItemFree + k % kItemRing));
+  };
 
   if (warp >= C::kMmaS) {
     if constexpr (C::kSplitRegs)
@@ -381,29 +383,79 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       const CUtensorMap* map = is_v ? &tmV : &tmK;
       const int stages = is_v ? C::kVStages : C::kKStages;
       const uint32_t dst0 = (is_v ? sV : sK) + lane * 2048;
-      const int full0 = is_v ? kBarVFull : kBarKFull, empty0 = is_v ? kBarVEmpty : kBarKEmpty;
+      const int full0 = is_v ? C::kBarVFull : C::kBarKFull, empty0 = is_v ? C::kBarVEmpty : C::kBarKEmpty;
       bool ok = true;
       Ring r;
       int c = 0;  // tiles so far
       // first row of this lane's slice of tile n, -1 behind the range
-      auto row_of = [&](const PackedItem& it, int n) -> int {
-        const int pos0 = (it.lo & ~15) + (it.tile0 + n) * KV + 16 * lane;
-        if (lane >= C::kSlices || pos0 > it.hi || n >= it.nt) return -1;
+      auto row_of = [&](int b, int kvh, int start, int hi, int n, int nt) -> int {
+        const int pos0 = start + n * KV + 16 * lane;
+        if (lane >= C::kSlices || pos0 > hi || n >= nt) return -1;
         const int lb = pos0 / a.bs;
-        int blk = a.block_tables[static_cast<size_t>(it.b) * a.MB + lb];
+        int blk = a.block_tables[static_cast<size_t>(b) * a.MB + lb];
         if (static_cast<unsigned>(blk) >= static_cast<unsigned>(a.NB)) {
           atomicOr(a.err, PA_DEVERR_BLOCK_ID);
           blk = 0;
         }
-        return (blk * a.Hkv + it.kvh) * a.bs + (pos0 - lb * a.bs);
+        return (blk * a.Hkv + kvh) * a.bs + (pos0 - lb * a.bs);
       };
-      PackedItem it = items.get(0);
-      int row = row_of(it, 0);
-      for (int k = 0; ok && k < items.count; ++k) {
-        const PackedItem ahead = items.get(k + 1);
-        for (int n = 0; n < it.nt; ++n, ++c) {
-          // looked up while the wait below runs
-          const int next = n + 1 < it.nt ? row_of(it, n + 1) : row_of(ahead, 0);
+      // Works out item k and puts it into the ring (the K warp); returns its first row.
+      const int whole = a.plan[kPkWhole], pairs = a.plan[kPkPairs], wsz = a.plan[kPkWsz];
+      const int me = blockIdx.x;
+      const int2 share = reinterpret_cast<const int2*>(a.plan + packed_ctas_at())[me];
+      auto publish = [&](int k) -> int {
+        PackedItem it = {};
+        it.nt = -1;
+        int p = whole ? me : share.x + k;
+        if (whole && k > 0) {
+          int taken = 0;
+          if (lane == 0) taken = atomicAdd(const_cast<int32_t*>(a.plan) + kPkNext, 1);
+          p = a.ctas + __shfl_sync(kFull, taken, 0);
+        }
+        if (p < (whole ? pairs : share.y)) {
+          const int u = p / a.Hkv;
+          const int4* rec = reinterpret_cast<const int4*>(a.plan + packed_units_at(a.ctas)) + 3 * static_cast<size_t>(u);
+          const int4 x = rec[0], y = rec[1];
+          it = PackedItem{x.x, p - u * a.Hkv, x.y, x.z, x.w, y.x, y.y, y.z, 0, y.w, -1, 0};
+          if (!whole) {
+            const int per = tile_places(it.ntok > a.tpg), nt = max(it.nt, 1);
+            const int g0 = rec[2].x + it.kvh * (kOutPlaces + nt * per) + kOutPlaces;
+            const int from = tiles_before(me * wsz - g0, nt, per), to = tiles_before((me + 1) * wsz - g0, nt, per);
+            if (from > 0 || to < nt) it.slot = 2 * me + (from == 0 ? 1 : 0);
+            it.tile0 = from;
+            if (it.nt > 0) it.nt = to - from;
+          }
+        }
+        const int at = k % kItemRing;
+        if (k >= kItemRing) ok = wait_all(bar(kBarItemFree + at), k / kItemRing - 1) && ok;
+        if (lane == 0 && ok) {
+          const uint32_t to = base + C::kItem + 48 * at;
+          sts_v4(to, make_uint4(it.b, it.kvh, it.row0, it.ntok));
+          sts_v4(to + 16, make_uint4(it.pos0, it.first, it.lo, it.hi));
+          sts_v4(to + 32, make_uint4(it.tile0, it.nt, it.slot, 0));
+          mbar_arrive(bar(kBarItem + at));
+        }
+        __syncwarp();
+        return row_of(it.b, it.kvh, (it.lo & ~15) + it.tile0 * KV, it.hi, 0, it.nt);
+      };
+      int row = -1, later = -1;
+      if (!is_v) row = publish(0);
+      for (int k = 0; ok; ++k) {
+        int b, kvh, start, hi, nt;  // (in uniform registers)
+        {
+          PackedItem it;
+          if (!(ok = item_at(k, &it))) break;
+          b = __shfl_sync(kFull, it.b, 0);
+          kvh = __shfl_sync(kFull, it.kvh, 0);
+          start = __shfl_sync(kFull, (it.lo & ~15) + it.tile0 * KV, 0);
+          hi = __shfl_sync(kFull, it.hi, 0);
+          nt = __shfl_sync(kFull, it.nt, 0);
+        }
+        item_done(k);
+        if (nt < 0) break;
+        if (is_v) row = row_of(b, kvh, start, hi, 0, nt);
+        for (int n = 0; n < nt; ++n, ++c) {
+          const int next = row_of(b, kvh, start, hi, n + 1, nt);  // looked up while the wait below runs
           if (c >= stages && !(ok = wait_all(bar(empty0 + r.stage), r.phase ^ 1))) break;
           const uint32_t full = bar(full0 + r.stage);
           const int nslices = __popc(__ballot_sync(kFull, row >= 0));
@@ -418,9 +470,16 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           __syncwarp();
           r.next(stages);
           row = next;
+          // the next item, once this one's first copies are on their way
+          if (!is_v && n == min(nt, 2) - 1) {
+            later = publish(k + 1);
+            if (!ok) break;
+          }
         }
-        if (it.nt == 0) row = row_of(ahead, 0);
-        it = ahead;
+        if (!is_v) {
+          if (nt == 0) later = publish(k + 1);
+          row = later;
+        }
       }
       if (!ok) {
         if (lane == 0) atomicOr(a.err, PA_DEVERR_TIMEOUT);
@@ -432,7 +491,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       // The warps stay together, so that what they issue with is uniform; their own
       // instructions are on the critical path.
       const uint32_t tm = __shfl_sync(kFull, tmem, 0);
-      const int count = __shfl_sync(kFull, items.count, 0);
       bool ok = true;
       Ring ring;
       uint32_t jobs = 0, live = 0;
@@ -455,12 +513,14 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           commit_all(bar(kBarS + x));
           ++jobs;
         };
-        PackedItem ahead = items.get(0);
-        for (int k = 0; ok && k < count; ++k) {
-          const PackedItem it = ahead;
-          ahead = items.get(k + 1);
-          const int nt = __shfl_sync(kFull, it.nt, 0);
-          const bool dual = __any_sync(kFull, is_dual(it));
+        for (int k = 0; ok; ++k) {
+          PackedItem it;
+          if (!(ok = item_at(k, &it))) break;
+          const int nt = __shfl_sync(kFull, it.nt, 0), row0 = __shfl_sync(kFull, it.row0, 0);
+          const int head = __shfl_sync(kFull, it.kvh, 0) * a.G;
+          const bool dual = NX == 2 && __shfl_sync(kFull, it.ntok, 0) > a.tpg;
+          item_done(k);
+          if (nt < 0) break;
           if (nt == 0) continue;
           {
             // Q, once the last item's products are done with it: a row tile's tokens times
@@ -474,8 +534,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
               for (int xt = 0; xt < row_tiles; ++xt)
 #pragma unroll
                 for (int box = 0; box < C::kBoxes; ++box)
-                  tma_load_3d(sQ + xt * C::kQBytes + box * C::kQBox, &tmQ, box * 64, it.kvh * a.G,
-                              it.row0 + xt * a.tpg, full);
+                  tma_load_3d(sQ + xt * C::kQBytes + box * C::kQBox, &tmQ, box * 64, head, row0 + xt * a.tpg, full);
             }
             __syncwarp();
           }
@@ -537,12 +596,13 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             begun &= ~(1u << g);
           }
         };
-        PackedItem ahead = items.get(0);
-        for (int k = 0; ok && k < count; ++k) {
-          const PackedItem it = ahead;
-          ahead = items.get(k + 1);
+        for (int k = 0; ok; ++k) {
+          PackedItem it;
+          if (!(ok = item_at(k, &it))) break;
           const int nt = __shfl_sync(kFull, it.nt, 0);
-          const bool dual = __any_sync(kFull, is_dual(it));
+          const bool dual = NX == 2 && __shfl_sync(kFull, it.ntok, 0) > a.tpg;
+          item_done(k);
+          if (nt < 0) break;
           if (nt == 0) continue;
           left = dual ? 2 * nt : nt;
 #pragma unroll 1
@@ -560,7 +620,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       // no product and no arrival outlives the CTA
       if (!ok && lane == 0) atomicOr(a.err, PA_DEVERR_TIMEOUT);
       const uint64_t limit = ok ? kWaitNs : kDrainNs;
-      const int drain = warp == C::kMmaS ? kBarDrain : kBarDrain + 1;
+      const int drain = warp == C::kMmaS ? C::kBarDrain : C::kBarDrain + 1;
       const int free0 = warp == C::kMmaS ? kKFree : kVFree, bufs = warp == C::kMmaS ? KB : VB;
       commit_all(bar(drain));
       (void)mbar_wait_bounded(bar(drain), 0, limit);
@@ -581,10 +641,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     uint32_t jobs = 0;
     // the results of an item, items in order
     auto store = [&](int k) {
-      const PackedItem item = items.get(k);  // (into uniform registers)
+      PackedItem item;  // (into uniform registers)
+      if (!(ok = item_at(k, &item))) return;
       const int ntok = __shfl_sync(kFull, item.ntok, 0), nt = __shfl_sync(kFull, item.nt, 0);
       const int row0 = __shfl_sync(kFull, item.row0, 0), kvh = __shfl_sync(kFull, item.kvh, 0);
       const int slot = __shfl_sync(kFull, item.slot, 0);
+      item_done(k);
       const bool dual = NX == 2 && ntok > a.tpg;
       const int nj = dual ? 2 * nt : nt;
       const uint32_t s = jobs & 1;  // group of the item's first job
@@ -778,38 +840,44 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       uint32_t live = 0;          // items with tiles so far
       int last = -1;              // the item whose results are to be stored
 #pragma unroll 1
-      for (int k = 0; ok && k < items.count; ++k) {
-        int nt, v_lo, v_hi;  // tiles, range of V rows from the first tile on
+      for (int k = 0; ok; ++k) {
+        int nt, ntok, v_lo, v_hi;  // tiles, tokens, range of V rows from the first tile on
         {
-          const PackedItem it = items.get(k);
+          PackedItem it;
+          if (!(ok = item_at(k, &it)) || it.nt < 0) break;
           const int start = (it.lo & ~15) + it.tile0 * KV;
           nt = it.nt;
+          ntok = it.ntok;
           v_lo = it.lo - start;
           v_hi = it.hi + 1 - start;
         }
-        if (nt == 0) store(k);
+        if (nt == 0) {  // (the ring goes on only behind the last item's results)
+          if (last >= 0) store(last);
+          last = -1;
+          if (ok) store(k);
+        }
 #pragma unroll 1
         for (int n = 0; ok && n < nt; ++n, ++c) {
           const uint32_t free_par = (c - 2) >> 1;  // of the buffers' last tile
-          if (!(ok = wait_all(bar(kBarKFull), c))) break;
-          if (c > 1 && !(ok = wait_all(bar(kBarCKFree + (c & 1)), free_par))) break;
+          if (!(ok = wait_all(bar(C::kBarKFull), c))) break;
+          if (c > 1 && !(ok = wait_all(bar(C::kBarCKFree + (c & 1)), free_par))) break;
           convert(sK, sKc + (c & 1) * C::kTile, 0, KV);
           fence_proxy_async();  // the f16 tile, visible to the tensor core
-          mbar_arrive(bar(kBarCKFull + (c & 1)));
-          mbar_arrive(bar(kBarKEmpty));  // reload the stage
+          mbar_arrive(bar(C::kBarCKFull + (c & 1)));
+          mbar_arrive(bar(C::kBarKEmpty));  // reload the stage
           if (n == 0) {
             if (kConvertQ) {
               if (!(ok = wait_all(bar(kBarQRaw), live))) break;
-              convert_q(items.get(k).ntok, live);
+              convert_q(ntok, live);
             }
             ++live;
           }
-          if (!(ok = wait_all(bar(kBarVFull), c))) break;
-          if (c > 1 && !(ok = wait_all(bar(kBarCVFree + (c & 1)), free_par))) break;
+          if (!(ok = wait_all(bar(C::kBarVFull), c))) break;
+          if (c > 1 && !(ok = wait_all(bar(C::kBarCVFree + (c & 1)), free_par))) break;
           convert(sV, sVc + (c & 1) * C::kTile, v_lo - n * KV, v_hi - n * KV);
           fence_proxy_async();
-          mbar_arrive(bar(kBarCVFull + (c & 1)));
-          mbar_arrive(bar(kBarVEmpty));
+          mbar_arrive(bar(C::kBarCVFull + (c & 1)));
+          mbar_arrive(bar(C::kBarVEmpty));
           if (n == 0 && last >= 0) store(last);
         }
         if (nt > 0) last = k;
@@ -817,7 +885,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       if (ok && last >= 0) store(last);
     } else {
 #pragma unroll 1
-      for (int k = 0; ok && k < items.count; ++k) store(k);
+      for (int k = 0; ok; ++k) {
+        PackedItem it;
+        if (!(ok = item_at(k, &it)) || it.nt < 0) break;
+        store(k);
+      }
     }
     if (!ok && lane == 0) atomicOr(a.err, PA_DEVERR_TIMEOUT);
   } else {
@@ -836,14 +908,14 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     uint32_t live = 0;   // items with tiles
     uint32_t tiles = 0;  // K/V tiles of the items before
     uint32_t looks = 0;  // tiles whose V was looked through
-    const int count = __shfl_sync(kFull, items.count, 0);
 #pragma unroll 1
-    for (int k = 0; ok && k < count; ++k) {
+    for (int k = 0; ok; ++k) {
       // What is the same for the whole group, in uniform registers; positions from the
       // first tile's first token on.
       int nt, row0, ntok, first, u_lo, u_hi, pos0, start;
       {
-        const PackedItem it = items.get(k);
+        PackedItem it;
+        if (!(ok = item_at(k, &it))) break;
         start = __shfl_sync(kFull, (it.lo & ~15) + it.tile0 * KV, 0);
         nt = __shfl_sync(kFull, it.nt, 0);
         row0 = __shfl_sync(kFull, it.row0, 0);
@@ -853,6 +925,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         u_hi = __shfl_sync(kFull, it.hi, 0) + 1 - start;  // (its end)
         pos0 = __shfl_sync(kFull, it.pos0, 0) - start;
       }
+      item_done(k);
+      if (nt < 0) break;
       const bool dual = NX == 2 && ntok > a.tpg;
       const int nj = dual ? 2 * nt : nt;
       if (nj == 0) continue;
@@ -955,11 +1029,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         }
         if (!(ok = wait_all(bar(kBarS + buf), phase))) break;
         tc::fence_after_sync();
-        // the other group's warp has taken the weights of the job before
-        auto my_turn = [&]() {
-          if (NX == 2 && (mine > 0 || x == 1)) ok = wait_all(bar(kBarTurn + (warp ^ 4)), mine - (x ^ 1)) && ok;
-          return ok;
-        };
         if (alive) {
           uint32_t sv[KV / 32][32];
           const bool old = j != j0;  // O holds something
@@ -1049,10 +1118,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
               tc::st16(tS + col + 16 * q, pk);
             }
           };
-          // The two warps of a processor share its exponential unit (1,024 cycles for both
-          // of 2,100 of products): they take turns, job by job, so that one group's weights
-          // are ready while the products of the other's run, and not both at once.
-          if (!my_turn()) break;
           if (skip) {
             // Infinities or NaN in V: weights times rows on the CUDA cores, attended
             // positions only.
@@ -1125,11 +1190,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             l += st.x + st.y;
           }
         } else {
-          if (!my_turn()) break;
           mbar_arrive(bar(kBarP + buf));
         }
         if (!ok) break;
-        if (NX == 2 && lane == 0) mbar_arrive(bar(kBarTurn + warp));
         tc::wait_st();
         tc::fence_before_sync();
         mbar_arrive(bar(kBarP2 + buf));
