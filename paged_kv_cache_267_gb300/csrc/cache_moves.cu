@@ -4,6 +4,8 @@
 // Both are bound by the bytes they move, and where those are few by one launch and two
 // dependent round trips (indexes, then rows). A thread moves 16 bytes at a time with
 // eight loads in flight.
+#include <algorithm>
+
 #include "packed_ops.h"
 #include "pa_internal.h"
 #include "ptx.cuh"
@@ -44,26 +46,39 @@ __global__ void __launch_bounds__(kThreads) copy_blocks_kernel(const CopyBlocksA
     if (at + i * kThreads < a.units) dst[at + i * kThreads] = v[i];
 }
 
-// One CTA a (sequence, plane): every thread has its 16-byte units of a row of all heads,
-// and moves them from kept token to kept token: a target lies before every later source
-// (the kept tokens ascend), so a thread's own order is all that is needed.
+__device__ __forceinline__ int fast_quotient(int x, FastDiv d) {
+  return d.mul == 0 ? x : static_cast<int>(__umulhi(static_cast<uint32_t>(x), d.mul) >> d.shift);
+}
+
+// One CTA a (sequence, share of the planes). The rows that move, from where to where, are
+// worked out once, into shared memory, and then moved plane by plane, kChunk 16-byte units
+// at a time: all of them are loaded before any is stored, and a target lies before every
+// later source (the kept tokens ascend), so that passes need no order but their own.
+// (A CTA a plane, with 64 of 256 threads at work and the three dependent round trips of
+// lengths, list and table in each, took 82 us for 256 sequences of 32 layers.)
 __global__ void __launch_bounds__(kThreads) compact_cache_kernel(const CompactArgs a) {
-  const int b = blockIdx.x, plane = blockIdx.y;
+  __shared__ long long s_from[kThreads], s_to[kThreads];  // rows of KV head 0, -1: none
+  const int b = blockIdx.x, tid = threadIdx.x;
   griddep_wait();
   const int cap = a.MB * a.bs;
   const int L0 = a.seq_lens[b], L = min(max(L0, 0), cap);
   const int q0 = a.query_start[b], q1 = a.query_start[b + 1];
-  const int n = max(q1 - q0, 0), base = L - n, count = a.num_kept[b];
+  const int count = a.num_kept[b];
+  const int n = q1 > q0 ? static_cast<int>(min(static_cast<long long>(q1) - q0, 0x7fffffffll)) : 0;
+  const int base = L - n;
   const int32_t* kept = a.kept + static_cast<size_t>(b) * a.M;
+  const int32_t* table = a.block_tables + static_cast<size_t>(b) * a.MB;
   // the whole list is looked at before anything moves
   bool bad = q1 < q0 || base < 0 || count < 0 || count > min(a.M, n);
+  int stay = 0;  // tokens of this thread's that stay in their place
   if (!bad)
-    for (int i = threadIdx.x; i < count; i += kThreads) {
+    for (int i = tid; i < count; i += kThreads) {
       const int k = kept[i];
       bad = bad || k < 0 || k >= n || (i > 0 && kept[i - 1] >= k);
+      stay += k == i;
     }
   bad = __syncthreads_or(bad);
-  if (threadIdx.x == 0 && plane == 0) {
+  if (tid == 0 && blockIdx.y == 0) {
     if (L0 != L) atomicOr(a.err, PA_DEVERR_SEQ_LEN);
     if (bad) atomicOr(a.err, PA_DEVERR_QUERY);
     const int len = bad ? L : base + count;
@@ -71,45 +86,55 @@ __global__ void __launch_bounds__(kThreads) compact_cache_kernel(const CompactAr
     if (a.kept_tokens) a.kept_tokens[b] = (len + a.bs - 1) / a.bs * a.bs;
   }
   if (bad) return;
-  const int32_t* table = a.block_tables + static_cast<size_t>(b) * a.MB;
-  const int layer = plane >> 1;
-  char* const cache = (plane & 1) ? static_cast<char*>(a.vc) + layer * a.v_layer
-                                  : static_cast<char*>(a.kc) + layer * a.k_layer;
-  const size_t row_bytes = static_cast<size_t>(a.row_units) * 16;
-  bool wrong = false;
-  // the row of KV head 0 at a position; blocks outside of the pool move nothing
-  auto row_of = [&](int pos) -> char* {
-    const int lb = pos / a.bs, blk = table[lb];
-    if (blk < 0 || blk >= a.NB) {
-      wrong = true;
-      return nullptr;
-    }
-    return cache + (static_cast<size_t>(blk) * a.Hkv * a.bs + (pos - lb * a.bs)) * row_bytes;
-  };
+  // (an ascending list stays in place up to its first gap)
+  __shared__ int s_stay;
+  if (tid == 0) s_stay = 0;
+  __syncthreads();
+  if (stay) atomicAdd(&s_stay, stay);
+  __syncthreads();
   const int units = a.row_units * a.Hkv;
-  for (int u = threadIdx.x; u < units; u += kThreads) {
-    const int h = u / a.row_units, c = u - h * a.row_units;
-    const size_t off = static_cast<size_t>(h) * a.bs * row_bytes + static_cast<size_t>(c) * 16;
-    for (int i0 = 0; i0 < count; i0 += kFlight) {
+  const long long head = static_cast<long long>(a.bs) * a.row_units;  // units between KV heads
+  const int plane0 = blockIdx.y * a.share, planes = min(a.share, 2 * a.layers - plane0);
+  for (int i0 = s_stay; i0 < count; i0 += kThreads) {
+    const int rows = min(count - i0, kThreads);
+    if (tid < rows) {
+      auto row_of = [&](int pos) -> long long {
+        const int lb = pos / a.bs, blk = table[lb];
+        return blk < 0 || blk >= a.NB ? -1 : static_cast<long long>(blk) * a.Hkv * a.bs + (pos - lb * a.bs);
+      };
+      const long long from = row_of(base + kept[i0 + tid]), to = row_of(base + i0 + tid);
+      if (from < 0 || to < 0) atomicOr(a.err, PA_DEVERR_BLOCK_ID);
+      s_from[tid] = from;
+      s_to[tid] = from < 0 ? -1 : to;
+    }
+    __syncthreads();
+    const int all = planes * rows * units;  // (below 2^31 - kChunk: the launcher sees to it)
+    for (int e0 = 0; e0 < all; e0 += kChunk) {
       uint4 v[kFlight];
-      char* to[kFlight];
+      uint4* to[kFlight];
 #pragma unroll
       for (int i = 0; i < kFlight; ++i) {
+        const int e = e0 + i * kThreads + tid;
         to[i] = nullptr;
-        if (i0 + i >= count) continue;
-        const int k = kept[i0 + i];
-        if (k == i0 + i) continue;  // in its place already
-        const char* from = row_of(base + k);
-        to[i] = row_of(base + i0 + i);
-        if (!from) to[i] = nullptr;
-        if (to[i]) v[i] = *reinterpret_cast<const uint4*>(from + off);
+        if (e >= all) continue;
+        const int r = fast_quotient(e, a.unit_div), u = e - r * units;
+        const int p = static_cast<unsigned>(r) / static_cast<unsigned>(rows), row = r - p * rows;
+        const int plane = plane0 + p, layer = plane >> 1;
+        const int h = fast_quotient(u, a.row_div), c = u - h * a.row_units;
+        if (s_to[row] < 0) continue;
+        uint4* const cache = reinterpret_cast<uint4*>(
+            (plane & 1) ? static_cast<char*>(a.vc) + layer * a.v_layer : static_cast<char*>(a.kc) + layer * a.k_layer);
+        const long long off = h * head + c;
+        v[i] = cache[s_from[row] * a.row_units + off];
+        to[i] = cache + s_to[row] * a.row_units + off;
       }
+      __syncthreads();
 #pragma unroll
       for (int i = 0; i < kFlight; ++i)
-        if (to[i]) *reinterpret_cast<uint4*>(to[i] + off) = v[i];
+        if (to[i]) *to[i] = v[i];
     }
+    __syncthreads();  // the list is written over
   }
-  if (wrong) atomicOr(a.err, PA_DEVERR_BLOCK_ID);
 }
 
 template <typename K, typename A>
@@ -136,8 +161,16 @@ cudaError_t copy_blocks_launch(const CopyBlocksArgs& a, cudaStream_t s) {
   return launch(copy_blocks_kernel, dim3(static_cast<unsigned>(grid)), a, s);
 }
 
-cudaError_t compact_cache_launch(const CompactArgs& a, cudaStream_t s) {
-  return launch(compact_cache_kernel, dim3(a.B, 2 * a.layers), a, s);
+cudaError_t compact_cache_launch(const CompactArgs& a, int num_sms, cudaStream_t s) {
+  CompactArgs x = a;
+  // as many planes a CTA as leave the GPU a few waves of CTAs
+  const long long ctas = static_cast<long long>(a.B) * 2 * a.layers;
+  const long long units = static_cast<long long>(a.row_units) * a.Hkv;
+  x.share = static_cast<int>(std::min<long long>(std::max<long long>(ctas / (num_sms * 16ll), 1), 2 * a.layers));
+  x.share = static_cast<int>(std::min<long long>(x.share, std::max<long long>(0x7fff0000ll / (kThreads * std::max(units, 1ll)), 1)));
+  x.unit_div = fast_div(static_cast<uint32_t>(units));
+  x.row_div = fast_div(static_cast<uint32_t>(a.row_units));
+  return launch(compact_cache_kernel, dim3(a.B, (2 * a.layers + x.share - 1) / x.share), x, s);
 }
 
 }  // namespace pa

@@ -284,7 +284,8 @@ pa_status check_moved(const pa_tensor* kc, const pa_tensor* vc, MovedCaches* m) 
   m->v_layer = o ? vc->strides[0] * m->elt : 0;
   if (m->D * m->elt % 16) return fail(PA_ERR_UNSUPPORTED, "rows must be a multiple of 16 bytes");
   if (m->layers > 1024) return fail(PA_ERR_UNSUPPORTED, "more than 1024 layers");
-  if (double(m->NB) >= k2p31 || dprod({double(m->Hkv), double(m->bs), double(m->D)}) >= k2p31)
+  if (double(m->NB) >= k2p31 || dprod({double(m->Hkv), double(m->bs), double(m->D)}) >= k2p31 ||
+      dprod({double(m->Hkv), double(m->D)}) >= 4194304)  // (256 rows of all heads in 31 bits)
     return fail(PA_ERR_UNSUPPORTED, "pool exceeds 32-bit indexing");
   if (overlaps(kc, vc)) return fail(PA_ERR_INVALID_ARG, "key and value cache overlap");
   return PA_OK;
@@ -443,7 +444,7 @@ pa_status pa_compact_cache(const pa_tensor* key_cache, const pa_tensor* value_ca
     a.bs = block_size;
     a.M = static_cast<int>(kept->shape[1]);
     a.row_units = static_cast<int>(m.D * m.elt / 16);
-    const cudaError_t e = compact_cache_launch(a, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = compact_cache_launch(a, dev.num_sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "compact_cache launch");
     count_launches(1);
     return ok();

@@ -83,7 +83,9 @@ struct CompactArgs {
   int64_t k_layer, v_layer;     // bytes
   int layers, B, MB, NB, Hkv, bs, M;
   int row_units;                // 16-byte units a row
+  int share;                    // planes (layer, K or V) a CTA, set by the launcher
+  FastDiv unit_div, row_div;    // by a row of all heads, by a row; set by the launcher
 };
-cudaError_t compact_cache_launch(const CompactArgs& a, cudaStream_t s);
+cudaError_t compact_cache_launch(const CompactArgs& a, int num_sms, cudaStream_t s);
 
 }  // namespace pa

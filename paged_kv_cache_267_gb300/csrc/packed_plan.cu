@@ -10,13 +10,13 @@
 namespace pa {
 namespace {
 
-constexpr int kThreads = 1024;
 constexpr int kBins = 256;
+constexpr int kSmallUnits = 512;  // fewer units: a small block, whose scans are shorter
 constexpr unsigned kFull = 0xffffffffu;
 
 // Inclusive scan of x over the block with op (identity `zero`); *total receives the
 // whole block's value.
-template <typename T, typename Op>
+template <int kThreads, typename T, typename Op>
 __device__ __forceinline__ T scan(T x, T zero, Op op, T* total) {
   __shared__ T s_w[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -27,7 +27,7 @@ __device__ __forceinline__ T scan(T x, T zero, Op op, T* total) {
   }
   if (lane == 31) s_w[warp] = x;
   __syncthreads();
-  T v = s_w[lane];
+  T v = lane < kThreads / 32 ? s_w[lane] : zero;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const T y = __shfl_up_sync(kFull, v, o);
@@ -39,6 +39,7 @@ __device__ __forceinline__ T scan(T x, T zero, Op op, T* total) {
   return op(x, warp > 0 ? before : zero);
 }
 
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads, 1) packed_plan_kernel(const PackedPlanArgs a) {
   extern __shared__ int s_dyn[];
   int* s_q = s_dyn;             // [B + 1] query starts, made non-decreasing in [0, T]
@@ -66,7 +67,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_plan_kernel(const PackedPl
       if (L != M) atomicOr(a.err, PA_DEVERR_SEQ_LEN);
       if (b < a.B) s_len[b] = M;
     }
-    const int y = most(scan(x, 0, most, &total), run);
+    const int y = most(scan<kThreads>(x, 0, most, &total), run);
     if (b <= a.B) {
       s_q[b] = y;
       if (y != x) atomicOr(a.err, PA_DEVERR_QUERY);
@@ -83,7 +84,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_plan_kernel(const PackedPl
       nu = (n + a.tpu - 1) / a.tpu;
       if (a.tree && n > 64) atomicOr(a.err, PA_DEVERR_QUERY);
     }
-    const int y = scan(nu, 0, add, &total);
+    const int y = scan<kThreads>(nu, 0, add, &total);
     if (b < a.B) s_u[b] = units + y - nu;
     units += total;
   }
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_plan_kernel(const PackedPl
   for (int u0 = 0; u0 < units; u0 += kThreads) {
     const int u = u0 + tid;
     const int c = u < units ? cost_of(unit(u)) : 0;
-    scan(static_cast<long long>(c), 0ll, add, &sum);
+    scan<kThreads>(static_cast<long long>(c), 0ll, add, &sum);
     places += sum;
     if (c > 0) atomicMax(&s_max, c);
   }
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_plan_kernel(const PackedPl
   for (int u = tid; u < units; u += kThreads) atomicAdd(&s_bin[bin_of(cost_of(unit(u)))], 1);
   __syncthreads();
   const int in_bin = tid < kBins ? s_bin[tid] : 0;
-  const int upto = scan(in_bin, 0, add, &total);
+  const int upto = scan<kThreads>(in_bin, 0, add, &total);
   // Whole pairs, or places split evenly? A split takes every CTA the mean, and what the
   // partial results and their join cost. Whole pairs, taken most first, take the mean
   // as well, but not less than the longest, nor than k + 1 of the k C-th longest (some
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_plan_kernel(const PackedPl
       it = unit(u);
       c = cost_of(it);
     }
-    const int upto_c = scan(c, 0, add, &total);
+    const int upto_c = scan<kThreads>(c, 0, add, &total);
     s_place[tid] = (before + upto_c - c) * a.Hkv;  // (all places are below 2^31)
     if (u < units) {
       it.place = s_place[tid];
@@ -237,10 +238,12 @@ __global__ void __launch_bounds__(kThreads, 1) packed_plan_kernel(const PackedPl
 cudaError_t packed_plan_launch(const PackedPlanArgs& a, cudaStream_t s, bool pdl) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(kThreads);
+  const bool small = a.T / a.tpu + (a.B < a.T ? a.B : a.T) <= kSmallUnits;
+  const auto kernel = small ? packed_plan_kernel<256> : packed_plan_kernel<1024>;
+  cfg.blockDim = dim3(small ? 256 : 1024);
   cfg.dynamicSmemBytes = (3 * static_cast<size_t>(a.B) + 2) * sizeof(int);
-  if (cfg.dynamicSmemBytes > 40 * 1024) {  // (48 KB, the static part counted)
-    const cudaError_t e = cudaFuncSetAttribute(packed_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
+  if (cfg.dynamicSmemBytes > 32 * 1024) {  // (48 KB, the static part counted)
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
     if (e != cudaSuccess) return e;
   }
   cfg.stream = s;
@@ -249,7 +252,7 @@ cudaError_t packed_plan_launch(const PackedPlanArgs& a, cudaStream_t s, bool pdl
   attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, packed_plan_kernel, a);
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 }  // namespace pa
