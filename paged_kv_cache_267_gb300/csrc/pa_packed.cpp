@@ -25,6 +25,7 @@ constexpr int64_t kMaxRowStride = int64_t(1) << 23;
 // partial results of a split and their join.
 constexpr int kMinPlaces = 8;
 constexpr int kSplitPlaces = 16;
+constexpr int kSmallPairs = 3;  // a CTA, of a step that is planned without a kernel
 
 bool misaligned(const pa_tensor* t, uintptr_t n) {
   return numel(t) > 0 && reinterpret_cast<uintptr_t>(t->data) % n;
@@ -70,6 +71,7 @@ pa_status check_rows(const pa_tensor* t, const char* name) {
 // What a ragged step launches, from its host-known sizes.
 struct PackedSizes {
   int tpg, tpu, kv, slot_rows, ctas;
+  bool small;  // each CTA plans by itself
   size_t plan_words, part_at, bytes;
 };
 
@@ -81,6 +83,11 @@ PackedSizes packed_sizes(int64_t T, int64_t B, int64_t span, int G, int64_t Hkv,
   z.kv = shape.kv;
   z.slot_rows = shape.rows == 2 && T > z.tpg ? 256 : 128;
   const int64_t units = T / z.tpu + std::min(B, T);  // at most
+  // lane b of a warp plans sequence b; with more pairs than a few a CTA, whole ones, sorted,
+  // are better (a batch of 16 prompts takes 343 us split, 232 whole)
+  z.small = B <= 32 && units * Hkv <= kSmallPairs * num_sms &&
+            dprod({double(units), double(Hkv), double(pair_places(static_cast<int>(std::min<int64_t>(span / z.kv + 2, 1 << 28)), true))}) <
+                k2p31 - 65536;
   const double tiles = dprod({double(units), double(Hkv), double(span / z.kv + 2)});
   z.ctas = static_cast<int>(std::min<double>(num_sms, std::max(1.0, std::ceil(tiles * 4 / kMinPlaces))));
   z.plan_words = packed_plan_words(z.ctas, static_cast<size_t>(units));
@@ -200,7 +207,7 @@ pa_status packed_attention(const pa_tensor* out, const pa_tensor* q, const pa_te
     p.min_places = kMinPlaces;
     p.split_places = kSplitPlaces;
     p.tree = tree;
-    cudaError_t e = packed_plan_launch(p, cs, true);
+    cudaError_t e = z.small ? cudaSuccess : packed_plan_launch(p, cs, true);
     if (e != cudaSuccess) return cuda_fail(e, "packed plan launch");
     PackedArgs a;
     a.q = q->data;
@@ -210,6 +217,13 @@ pa_status packed_attention(const pa_tensor* out, const pa_tensor* q, const pa_te
     a.plan = p.plan;
     a.part = reinterpret_cast<float*>(ws + z.part_at);
     a.err = dev.err_word;
+    a.query_start = p.query_start;
+    a.seq_lens = p.seq_lens;
+    a.B = p.B;
+    a.T = p.T;
+    a.tpu = z.tpu;
+    a.kv = z.kv;
+    a.min_places = kMinPlaces;
     a.q_stride = q->strides[0];
     a.out_stride = out->strides[0];
     a.ctas = z.ctas;
@@ -225,7 +239,7 @@ pa_status packed_attention(const pa_tensor* out, const pa_tensor* q, const pa_te
     a.score_scale = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634 *
                                        (fp8 ? static_cast<double>(k_scale) : 1.0));
     a.v_scale = fp8 ? v_scale : 1.f;
-    e = packed_launch(q->dtype, fp8, static_cast<int>(D), tk, tv, tq, a, cs, true);
+    e = (z.small ? packed_launch_small : packed_launch)(q->dtype, fp8, static_cast<int>(D), tk, tv, tq, a, cs, true);
     if (e != cudaSuccess) return cuda_fail(e, "packed attention launch");
     PackedMergeArgs m;
     m.out = out->data;
@@ -238,9 +252,10 @@ pa_status packed_attention(const pa_tensor* out, const pa_tensor* q, const pa_te
     m.D = static_cast<int>(D);
     m.tpg = z.tpg;
     m.slot_rows = z.slot_rows;
+    m.small = z.small;
     e = packed_merge_launch(q->dtype, m, cs, true);
     if (e != cudaSuccess) return cuda_fail(e, "packed merge launch");
-    count_launches(3);
+    count_launches(z.small ? 2 : 3);
     return ok();
   });
 }

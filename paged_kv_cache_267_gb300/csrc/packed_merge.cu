@@ -4,7 +4,8 @@
 //   out = sum_k w_k o_k / sum_k w_k l_k,  w_k = 2^(m_k - max m).
 // A warp takes four rows, eight lanes each, so that a few partials already give every
 // lane eight 16-byte loads in flight. Which unit is to be joined is in the plan, which is
-// complete when this kernel starts; CTAs without one leave at once. Two dependent round
+// complete when this kernel starts (in small steps, whose CTAs write it, when they are
+// done); CTAs without one leave at once. Two dependent round
 // trips and the partials' bytes through L2 bound it.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -27,11 +28,12 @@ __global__ void __launch_bounds__(kWarps * 32) packed_merge_kernel(const PackedM
   constexpr int N = D / (4 * kLanes);          // groups of four floats a lane
   constexpr int kFlight = N >= 8 ? 1 : 8 / N;  // partials in flight
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % kLanes;
+  if (a.small) griddep_wait();
   const PackedJoin j = reinterpret_cast<const PackedJoin*>(a.plan + packed_joins_at(a.ctas))[blockIdx.x];
   const int row = (blockIdx.y * kWarps + warp) * kRowsWarp + lane / kLanes;
   // (one CTA stays in any case: the next kernel must not overtake the attention)
   if ((j.n == 0 || blockIdx.y * kWarps * kRowsWarp >= j.ntok * a.G) && (blockIdx.x | blockIdx.y) != 0) return;
-  griddep_wait();
+  if (!a.small) griddep_wait();
   if (j.n == 0) return;
   // rows of the unit, those of its row tiles one after the other; lanes of rows behind
   // them work on the last one and store nothing

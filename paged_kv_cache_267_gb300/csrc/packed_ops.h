@@ -34,9 +34,12 @@ struct PackedArgs {
   void* out;                    // [T, Hq, D], rows of out_stride elements
   const int32_t* block_tables;  // [B, MB]
   const int64_t* tree;          // [T] ancestor bits, or null: causal
-  const int32_t* plan;
+  int32_t* plan;
   float* part;                  // partial results
   int32_t* err;
+  const int32_t* query_start;   // [B + 1], small steps: each CTA plans by itself
+  const int32_t* seq_lens;      // [B]
+  int B, T, tpu, kv, min_places;  // as in PackedPlanArgs
   int64_t q_stride, out_stride;
   int ctas, Hq, Hkv, G, bs, MB, NB, window;
   int tpg;                      // tokens a row tile: 128 / G
@@ -46,6 +49,8 @@ struct PackedArgs {
 };
 cudaError_t packed_launch(int qt, bool fp8, int D, const CUtensorMap& tk, const CUtensorMap& tv,
                           const CUtensorMap& tq, const PackedArgs& a, cudaStream_t s, bool pdl);
+cudaError_t packed_launch_small(int qt, bool fp8, int D, const CUtensorMap& tk, const CUtensorMap& tv,
+                                const CUtensorMap& tq, const PackedArgs& a, cudaStream_t s, bool pdl);
 
 struct PackedMergeArgs {
   void* out;
@@ -53,6 +58,7 @@ struct PackedMergeArgs {
   const int32_t* plan;
   int64_t out_stride;
   int ctas, Hq, G, D, tpg, slot_rows;
+  bool small;                   // the plan is complete only behind the attention
 };
 cudaError_t packed_merge_launch(int out_type, const PackedMergeArgs& a, cudaStream_t s, bool pdl);
 

@@ -99,25 +99,10 @@ __global__ void __launch_bounds__(kThreads, 1) packed_plan_kernel(const PackedPl
       if (s_u[mid] <= u) lo = mid;
       else hi = mid;
     }
-    PackedUnit it;
-    const int b = lo, n = s_q[b + 1] - s_q[b], t0 = (u - s_u[b]) * a.tpu;
-    it.b = b;
-    it.row0 = s_q[b] + t0;
-    it.ntok = min(a.tpu, n - t0);
-    it.first = s_len[b] - n;
-    it.pos0 = it.first + t0;
-    // causal: from the first token's window to the last token; tree: from the
-    // window of a row with no ancestor to the last drafted token that a bit can name
-    it.hi = a.tree ? it.first + min(n, 64) - 1 : it.pos0 + it.ntok - 1;
-    const int from = a.tree ? it.first : it.pos0 + 1;
-    it.lo = a.window > 0 && from > a.window ? from - a.window : 0;
-    it.nt = it.hi >= it.lo ? (it.hi + 1 - (it.lo & ~15) + a.kv - 1) / a.kv : 0;
-    it.place = 0;
-    it.pad[0] = it.pad[1] = it.pad[2] = 0;
-    return it;
+    return packed_unit(lo, u - s_u[lo], s_q[lo], s_q[lo + 1] - s_q[lo], s_len[lo], a.tpu, a.kv, a.window, a.tree);
   };
   auto per_tile = [&](const PackedUnit& it) { return tile_places(it.ntok > a.tpg); };
-  auto cost_of = [&](const PackedUnit& it) { return kOutPlaces + max(it.nt, 1) * per_tile(it); };
+  auto cost_of = [&](const PackedUnit& it) { return pair_places(it.nt, it.ntok > a.tpg); };
   int* const plan = a.plan;
   int2* const ctas = reinterpret_cast<int2*>(plan + packed_ctas_at());
   PackedJoin* const joins = reinterpret_cast<PackedJoin*>(plan + packed_joins_at(a.ctas));

@@ -16,6 +16,8 @@
 //     2 w with the others (each CTA has one of either kind at most); the merge joins
 //     them.
 // A unit that attends to nothing counts as one tile (its rows are zeros).
+// Steps of few sequences and pairs have no plan kernel: every CTA works out its own part of
+// split mode, and leaves the merge its note.
 #pragma once
 
 #include <stddef.h>
@@ -70,6 +72,31 @@ __host__ __device__ constexpr inline size_t packed_plan_words(int ctas, size_t u
 // Floats of a partial result: `rows` rows of D, their maxima and their sums.
 __host__ __device__ constexpr inline size_t packed_slot_floats(int rows, int D) {
   return static_cast<size_t>(rows) * (D + 2);
+}
+
+__host__ __device__ constexpr inline int pair_places(int nt, bool dual) {
+  return kOutPlaces + (nt > 1 ? nt : 1) * tile_places(dual);
+}
+
+// Unit u of sequence b, whose n new tokens begin at row q0 and end at position len.
+__host__ __device__ __forceinline__ PackedUnit packed_unit(int b, int u, int q0, int n, int len, int tpu, int kv,
+                                                           int window, bool tree) {
+  PackedUnit it;
+  const int t0 = u * tpu;
+  it.b = b;
+  it.row0 = q0 + t0;
+  it.ntok = n - t0 < tpu ? n - t0 : tpu;
+  it.first = len - n;
+  it.pos0 = it.first + t0;
+  // causal: from the first token's window to the last token; tree: from the window of a
+  // row with no ancestor to the last drafted token that a bit can name
+  it.hi = tree ? it.first + (n < 64 ? n : 64) - 1 : it.pos0 + it.ntok - 1;
+  const int from = tree ? it.first : it.pos0 + 1;
+  it.lo = window > 0 && from > window ? from - window : 0;
+  it.nt = it.hi >= it.lo ? (it.hi + 1 - (it.lo & ~15) + kv - 1) / kv : 0;
+  it.place = 0;
+  it.pad[0] = it.pad[1] = it.pad[2] = 0;
+  return it;
 }
 
 // Tiles of a pair that begin before place x, counted from its first tile's.
