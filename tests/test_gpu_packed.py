@@ -515,3 +515,11 @@ def test_nothing_to_do():
     st = Step([0], [0], seed=37)
     n0 = pa.launch_count()
     assert st.run().numel() == 0 and pa.launch_count() == n0
+
+
+@pytest.mark.parametrize("B", [1365, 2700, 4096])
+def test_large_batches(B):
+    """Batches around and at the most, whose lists the plan keeps in shared memory."""
+    new = [(7 * b) % 4 for b in range(B)]
+    Step(new, [(5 * b) % 23 for b in range(B)], Hq=2, Hkv=1, D=64, seed=38).check()
+    Step(new, [(5 * b) % 23 for b in range(B)], Hq=2, Hkv=1, D=64, seed=38, tree=True).check()
