@@ -447,9 +447,9 @@ pa_status pa_prefill_chunk_workspace_size(int64_t batch, int32_t num_queries,
  * with K_j, V_j as in pa_decode. A token with p < 0 (seq_lens[b] < n) gives zeros. What
  * a token does not attend to does not reach its row, infinities and NaN included.
  *
- *   out, q        [T, Hq, D]; dims 1 and 2 contiguous, dim 0 any stride (of out: rows
- *                 that do not overlap); rows 16-byte aligned. Rows of out outside of
- *                 [query_start[0], query_start[B]) are not written.
+ *   out, q        [T, Hq, D]; dims 1 and 2 contiguous, dim 0 any stride below 2^23
+ *                 elements whose rows do not overlap; rows 16-byte aligned. Rows of out
+ *                 outside of [query_start[0], query_start[B]) are not written.
  *   query_start   [B + 1] int32, non-decreasing in [0, T]. A start that decreases or
  *                 leaves the range is raised to the one before it or clamped, and
  *                 flagged (PA_DEVERR_QUERY).
@@ -505,8 +505,10 @@ pa_status pa_packed_workspace_size(int64_t num_rows, int64_t batch, int32_t num_
  * of two pairs, or of one and the source of another, is a caller error (which contents
  * it gets is unspecified).
  *   key_cache,    [NB, Hkv, bs, D] contiguous, or [layers, NB, Hkv, bs, D] whose layers
- *   value_cache   are contiguous and any stride apart (the pairs hold for all layers);
- *                 f16, bf16 or e4m3, rows a multiple of 16 bytes, 16-byte aligned.
+ *   value_cache   are contiguous and any stride apart (the pairs hold for all layers; K
+ *                 and V may be layers of one tensor in turn); f16, bf16 or e4m3, rows a
+ *                 multiple of 16 bytes, 16-byte aligned. At most 1024 layers,
+ *                 Hkv * D < 2^22, Hkv * bs * D < 2^31.
  *   block_pairs   [n, 2] int32 contiguous, 8-byte aligned.
  */
 pa_status pa_copy_blocks(const pa_tensor* key_cache, const pa_tensor* value_cache,

@@ -302,7 +302,14 @@ pa_status check_moved(const pa_tensor* kc, const pa_tensor* vc, MovedCaches* m) 
   if (double(m->NB) >= k2p31 || dprod({double(m->Hkv), double(m->bs), double(m->D)}) >= k2p31 ||
       dprod({double(m->Hkv), double(m->D)}) >= 4194304)  // (256 rows of all heads in 31 bits)
     return fail(PA_ERR_UNSUPPORTED, "pool exceeds 32-bit indexing");
-  if (overlaps(kc, vc)) return fail(PA_ERR_INVALID_ARG, "key and value cache overlap");
+  if (overlaps(kc, vc)) {
+    // (layers of one tensor in turn: K, V, K, V ...)
+    const int64_t layer = m->NB * want[0] * m->elt, step = m->k_layer;
+    const int64_t ahead = static_cast<const char*>(vc->data) - static_cast<const char*>(kc->data);
+    const int64_t r = step > 0 ? (ahead % step + step) % step : 0;
+    if (m->layers < 2 || m->v_layer != step || r < layer || r > step - layer)
+      return fail(PA_ERR_INVALID_ARG, "key and value cache overlap");
+  }
   return PA_OK;
 }
 

@@ -52,6 +52,20 @@ def test_copy(dtype, Hkv, bs, D, layers):
         assert torch.equal(bits(c), w)
 
 
+def test_layers_in_turn():
+    """K and V as every other layer of one tensor."""
+    g = torch.Generator(device="cuda").manual_seed(11)
+    pool = torch.randn(4, 2, 12, 2, 16, 64, generator=g, device="cuda").bfloat16()
+    want = pool.clone()
+    want[:, :, 5] = pool[:, :, 1]
+    pa.copy_blocks(pool[:, 0], pool[:, 1], ints([(1, 5)]))
+    assert torch.equal(pool, want)
+    want[:, :, 7, :, 3] = pool[:, :, 7, :, 5]
+    pa.compact_cache(pool[:, 0], pool[:, 1], ints([[2, 7]]), ints([24]), ints([0, 5]), ints([[2]]), ints([1]), block_size=16)
+    assert torch.equal(pool, want)
+    assert pa.check_device_error() == 0
+
+
 def test_copy_beyond_the_pool():
     g = torch.Generator(device="cuda").manual_seed(2)
     kc, vc = caches((9, 2, 16, 64), torch.bfloat16, g)

@@ -183,6 +183,19 @@ def test_move_refusals(moves):
     assert compact(**none) == 0
 
 
+def test_layers_in_turn(moves):
+    """K and V as every other layer of one tensor; layers that touch another's are refused."""
+    pa, _, copy, _ = moves
+    block = Hkv * bs * D
+    layers = lambda at, stride: strided(pa, pa.PA_BF16, (3, NB, Hkv, bs, D), (stride, block, bs * D, D, 1), BASE + at)  # noqa: E731
+    size, pairs = 2 * NB * block, _desc(pa, pa.PA_I32, (5, 2), BASE + 0x8000000)
+    for vk, step, want in [(size, size, -4), (-size, size, -4), (3 * size, size, -4), (size, size + 32, -4),
+                           (size - 16, size, ARG), (size + 16, size, ARG), (2 * size, size, ARG), (size, size - 8, ARG)]:
+        at = 0x1000000
+        assert copy(kc=layers(at, step), vc=layers(at + vk, step), pairs=pairs) == want, (vk, step, pa.last_error())
+    assert copy(kc=layers(0, size), vc=layers(size, size + 8), pairs=pairs) == ARG
+
+
 def test_workspace_query_refusals(pa_lib):
     pa = pa_lib
     n = ctypes.c_size_t(0)
