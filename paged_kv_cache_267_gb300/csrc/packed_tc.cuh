@@ -107,7 +107,7 @@ struct Cfg {
   // times slower.)
   static constexpr bool kSplitRegs = kThreads == 512;
   static constexpr int kLaunchRegs = kSplitRegs ? 128 : 168;
-  static constexpr int kSoftmaxRegs = FP8 ? 176 : 184, kStoreRegs = FP8 ? 104 : 80, kOtherRegs = FP8 ? 56 : 64;
+  static constexpr int kSoftmaxRegs = FP8 ? 176 : 184, kStoreRegs = FP8 ? 96 : 80, kOtherRegs = 64;
   static_assert(kThreads == 384 || (kThreads == 512 && kGroups == 2 && 2 * kSoftmaxRegs + kStoreRegs +
                                                                            kOtherRegs == 4 * kLaunchRegs),
                 "registers of the block");
@@ -373,23 +373,11 @@ __device__ __forceinline__ int lds_s8(uint32_t addr) {
   asm volatile("ld.shared.s8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-// 16-byte pieces k = 0..3 of a row in each lane -> piece (lane & 3) of the four rows of
-// the lanes around: a store then covers 64 bytes of a row instead of 16 of each.
-__device__ __forceinline__ void transpose4(uint32_t (&v)[16], int lane) {
-#pragma unroll
-  for (int bit = 1; bit <= 2; bit <<= 1) {
-    const bool up = lane & bit;
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const int lo = bit == 1 ? 2 * m : m, hi = lo + bit;  // pieces that change places
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint32_t got = __shfl_xor_sync(kFull, up ? v[4 * lo + c] : v[4 * hi + c], bit);
-        if (up) v[4 * lo + c] = got;
-        else v[4 * hi + c] = got;
-      }
-    }
-  }
+// 32 bytes, aligned to them.
+__device__ __forceinline__ void stg_b32x8(void* to, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 // Low k bits (none for k <= 0, all for k >= 32).
 __device__ __forceinline__ uint32_t below(int k) {
@@ -764,6 +752,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     const int r = wr0 + lane;                   // row = tensor-memory lane
     const uint32_t trow = tmem + (static_cast<uint32_t>(wr0) << 16);
     const uint32_t mul = (65536u + a.G - 1) / a.G;  // row / G = row * mul >> 16, rows < 256
+    // rows of out start on 32 bytes
+    const bool wide = ((reinterpret_cast<uintptr_t>(a.out) | (static_cast<uintptr_t>(a.out_stride) << 1)) & 31) == 0;
     bool ok = true;
     uint32_t o_items = 0;  // items of each group so far (the parity, a bit each)
     uint32_t jobs = 0;
@@ -819,78 +809,83 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
               m = top;
             }
           }
-          // 16 columns of this row, joined and scaled
+          // O by 32 columns, the next ones on their way while these are stored. A lane has a
+          // row: it stores whole 32-byte sectors of it. (Rows turned around between four
+          // lanes first, for 64-byte pieces, held O 3,000 cycles longer.)
           const uint32_t t_own = trow + C::kColO + D * ga, t_other = trow + C::kColO + D * (ga ^ 1);
-          auto take = [&](int d0, uint32_t (&v)[16]) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = 0u;
-            if (nj > 0) tc::ld16(t_own + d0, v);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f_own);
-            if (join) {
-              uint32_t w[16];
-              tc::ld16(t_other + d0, w);
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                v[i] = __float_as_uint(fmaf(__uint_as_float(w[i]), f_other, __uint_as_float(v[i])));
-            }
-          };
-          const int r4 = wr0 + (lane & ~3);  // rows r4 .. r4 + 3 are this lane's to store
+          char* to;  // this row's
           if (slot < 0) {
             // an empty row is zeros (its O is, as its weights were); a NaN in the sum stays one
             const float inv = l == 0.f ? 0.f : a.v_scale / l;
             f_own *= inv;
             f_other *= inv;
-            uint16_t* const out = static_cast<uint16_t*>(a.out) +
-                                  static_cast<size_t>(row0 + xt * a.tpg) * a.out_stride +
-                                  static_cast<size_t>(kvh) * a.G * D + 8 * (lane & 3);
-            int at[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int t = static_cast<int>(((r4 + i) * mul) >> 16), h = r4 + i - t * a.G;
-              at[i] = r4 + i < rows ? t * static_cast<int>(a.out_stride) + h * D : -1;
-            }
-#pragma unroll 1
-            for (int d0 = 0; d0 < D; d0 += 32) {
-              uint32_t p[16];
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                uint32_t v[16];
-                take(d0 + 16 * e, v);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  p[8 * e + i] = pack16x2<QT == kBF16>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-              }
-              if (d0 + 32 == D) release();  // before the last stores
-              transpose4(p, lane);
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (at[i] >= 0)
-                  *reinterpret_cast<uint4*>(out + at[i] + d0) =
-                      make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
-            }
+            const int t = static_cast<int>((r * mul) >> 16), h = r - t * a.G;
+            to = static_cast<char*>(a.out) + 2 * (static_cast<size_t>(row0 + xt * a.tpg + t) * a.out_stride +
+                                                  static_cast<size_t>(kvh * a.G + h) * D);
           } else {
             f_own *= a.v_scale;
             f_other *= a.v_scale;
-            float* const part = a.part + static_cast<size_t>(slot) * packed_slot_floats(a.slot_rows, D);
-            float* const to = part + static_cast<size_t>(xt * kRows + r4) * D + 4 * (lane & 3);
+            to = reinterpret_cast<char*>(a.part + static_cast<size_t>(slot) * packed_slot_floats(a.slot_rows, D) +
+                                         static_cast<size_t>(xt * kRows + r) * D);
+          }
+          // columns d0 .. d0 + 15, taken and scaled
+          auto put = [&](int d0, uint32_t (&v)[16]) {
+            if (slot >= 0) {
+              if (r < rows) stg_b32x8(to + 4 * d0, v), stg_b32x8(to + 4 * d0 + 32, v + 8);
+            } else {
+              uint32_t p[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                p[i] = pack16x2<QT == kBF16>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+              if (r < rows) {
+                if (wide) {
+                  stg_b32x8(to + 2 * d0, p);
+                } else {
+                  reinterpret_cast<uint4*>(to + 2 * d0)[0] = make_uint4(p[0], p[1], p[2], p[3]);
+                  reinterpret_cast<uint4*>(to + 2 * d0)[1] = make_uint4(p[4], p[5], p[6], p[7]);
+                }
+              }
+            }
+            __syncwarp();
+          };
+          uint32_t v[16], w[16];
+          if (nj == 0 || join) {
 #pragma unroll 1
             for (int d0 = 0; d0 < D; d0 += 16) {
-              uint32_t v[16];
-              take(d0, v);
-              transpose4(v, lane);
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (r4 + i < rows)
-                  *reinterpret_cast<uint4*>(to + i * D + d0) =
-                      make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+              for (int i = 0; i < 16; ++i) v[i] = w[i] = 0u;
+              if (join) tc::ld16(t_own + d0, v), tc::ld16(t_other + d0, w);
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                v[i] = __float_as_uint(fmaf(__uint_as_float(w[i]), f_other, __uint_as_float(v[i]) * f_own));
+              if (d0 + 16 == D) release();  // before the last stores
+              put(d0, v);
             }
-            if (r < rows) {
-              float* stat = part + static_cast<size_t>(a.slot_rows) * D + xt * kRows + r;
-              stat[0] = m - kLift;
-              stat[a.slot_rows] = l;
+          } else {
+            tc::ld16_async(t_own, v);
+            tc::ld16_async(t_own + 16, w);
+#pragma unroll 1
+            for (int d0 = 32;; d0 += 32) {
+              tc::wait_ld();
+              tc::pin(v);
+              tc::pin(w);
+              if (d0 == D) release();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f_own);
+              put(d0 - 32, v);
+              if (d0 < D) tc::ld16_async(t_own + d0, v);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * f_own);
+              put(d0 - 16, w);
+              if (d0 == D) break;
+              tc::ld16_async(t_own + d0 + 16, w);
             }
-            release();
+          }
+          if (slot >= 0 && r < rows) {
+            float* stat = a.part + static_cast<size_t>(slot) * packed_slot_floats(a.slot_rows, D) +
+                          static_cast<size_t>(a.slot_rows) * D + xt * kRows + r;
+            stat[0] = m - kLift;
+            stat[a.slot_rows] = l;
           }
         }
       }
@@ -966,51 +961,47 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       };
       int c = 0;                  // tiles so far
       uint32_t live = 0;          // items with tiles so far
-      int last = -1;              // the item whose results are to be stored
 #pragma unroll 1
       for (int k = 0; ok; ++k) {
         int nt, ntok, v_lo, v_hi;  // tiles, tokens, range of V rows from the first tile on
         {
           PackedItem it;
-          if (!(ok = item_at(k, &it)) || it.nt < 0) break;
+          if (!(ok = item_at(k, &it))) break;
           const int start = (it.lo & ~15) + it.tile0 * KV;
           nt = it.nt;
           ntok = it.ntok;
           v_lo = it.lo - start;
           v_hi = it.hi + 1 - start;
         }
-        if (nt == 0) {  // (the ring goes on only behind the last item's results)
-          if (last >= 0) store(last);
-          last = -1;
-          if (ok) store(k);
-        }
-#pragma unroll 1
-        for (int n = 0; ok && n < nt; ++n, ++c) {
-          const uint32_t free_par = (c - 2) >> 1;  // of the buffers' last tile
-          if (!(ok = wait_all(bar(C::kBarKFull), c))) break;
-          if (c > 1 && !(ok = wait_all(bar(C::kBarCKFree + (c & 1)), free_par))) break;
-          convert(sK, sKc + (c & 1) * C::kTile, 0, KV);
-          fence_proxy_async();  // the f16 tile, visible to the tensor core
-          mbar_arrive(bar(C::kBarCKFull + (c & 1)));
-          mbar_arrive(bar(C::kBarKEmpty));  // reload the stage
-          if (n == 0) {
-            if (kConvertQ) {
-              if (!(ok = wait_all(bar(kBarQRaw), live))) break;
-              convert_q(ntok, live);
+        int n = 0;
+        do {
+          if (n < nt) {
+            const uint32_t free_par = (c - 2) >> 1;  // of the buffers' last tile
+            if (!(ok = wait_all(bar(C::kBarKFull), c))) break;
+            if (c > 1 && !(ok = wait_all(bar(C::kBarCKFree + (c & 1)), free_par))) break;
+            convert(sK, sKc + (c & 1) * C::kTile, 0, KV);
+            fence_proxy_async();  // the f16 tile, visible to the tensor core
+            mbar_arrive(bar(C::kBarCKFull + (c & 1)));
+            mbar_arrive(bar(C::kBarKEmpty));  // reload the stage
+            if (n == 0) {
+              if (kConvertQ) {
+                if (!(ok = wait_all(bar(kBarQRaw), live))) break;
+                convert_q(ntok, live);
+              }
+              ++live;
             }
-            ++live;
+            if (!(ok = wait_all(bar(C::kBarVFull), c))) break;
+            if (c > 1 && !(ok = wait_all(bar(C::kBarCVFree + (c & 1)), free_par))) break;
+            convert(sV, sVc + (c & 1) * C::kTile, v_lo - n * KV, v_hi - n * KV);
+            fence_proxy_async();
+            mbar_arrive(bar(C::kBarCVFull + (c & 1)));
+            mbar_arrive(bar(C::kBarVEmpty));
+            ++c;
           }
-          if (!(ok = wait_all(bar(C::kBarVFull), c))) break;
-          if (c > 1 && !(ok = wait_all(bar(C::kBarCVFree + (c & 1)), free_par))) break;
-          convert(sV, sVc + (c & 1) * C::kTile, v_lo - n * KV, v_hi - n * KV);
-          fence_proxy_async();
-          mbar_arrive(bar(C::kBarCVFull + (c & 1)));
-          mbar_arrive(bar(C::kBarVEmpty));
-          if (n == 0 && last >= 0) store(last);
-        }
-        if (nt > 0) last = k;
+          if (n == 0 && k > 0) store(k - 1);
+        } while (++n < nt && ok);
+        if (nt < 0) break;
       }
-      if (ok && last >= 0) store(last);
     } else {
 #pragma unroll 1
       for (int k = 0; ok; ++k) {
