@@ -350,11 +350,12 @@ template <bool BF16>
 __device__ __forceinline__ float op_f32(uint32_t w, int hi) {
   return f32_of<BF16 ? kBF16 : kF16>(w, hi);
 }
-// Whether one of a pair's exponents is all ones (an infinity or NaN), in bits 15, 31.
+// Whether one of a pair's exponents is all ones (an infinity or NaN), in bits 15, 31 (the
+// others are of no meaning).
 template <bool BF16>
 __device__ __forceinline__ uint32_t nonfinite(uint32_t w) {
   constexpr uint32_t m = BF16 ? 0x7f807f80u : 0x7c007c00u, one = BF16 ? 0x00800080u : 0x04000400u;
-  return ((w & m) + one) & 0x80008000u;
+  return (w & m) + one;
 }
 __device__ __forceinline__ void lds_f32x2(uint32_t addr, float& a, float& b) {
   asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(a), "=f"(b) : "r"(addr) : "memory");
@@ -554,11 +555,13 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         __syncwarp();
         return row_of(it.b, it.kvh, (it.lo & ~15) + it.tile0 * KV, it.hi, 0, it.nt);
       };
+      // Item -1 stands for the start: nothing but the first item to be worked out. (One copy
+      // of each piece of code: what the warps of a CTA run in turn has to share the
+      // instruction cache, whose misses show in every kernel time here.)
       int row = -1, later = -1;
-      if (!is_v) row = publish(0);
-      for (int k = 0; ok; ++k) {
-        int b, kvh, start, hi, nt;  // (in uniform registers)
-        {
+      for (int k = -1; ok; ++k) {
+        int b = 0, kvh = 0, start = 0, hi = 0, nt = 0;  // (in uniform registers)
+        if (k >= 0) {
           PackedItem it;
           if (!(ok = item_at(k, &it))) break;
           b = __shfl_sync(kFull, it.b, 0);
@@ -566,36 +569,36 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           start = __shfl_sync(kFull, (it.lo & ~15) + it.tile0 * KV, 0);
           hi = __shfl_sync(kFull, it.hi, 0);
           nt = __shfl_sync(kFull, it.nt, 0);
+          item_done(k);
+          if (nt < 0) break;
         }
-        item_done(k);
-        if (nt < 0) break;
-        if (is_v) row = row_of(b, kvh, start, hi, 0, nt);
-        for (int n = 0; n < nt; ++n, ++c) {
+#pragma unroll 1
+        for (int n = is_v ? -1 : 0; n < max(nt, 1); ++n) {
           const int next = row_of(b, kvh, start, hi, n + 1, nt);  // looked up while the wait below runs
-          if (c >= stages && !(ok = wait_all(bar(empty0 + r.stage), r.phase ^ 1))) break;
-          const uint32_t full = bar(full0 + r.stage);
-          const int nslices = __popc(__ballot_sync(kFull, row >= 0));
-          if (lane == 0) mbar_arrive_expect_tx(full, nslices * C::kRawBoxes * 2048);
-          __syncwarp();
-          if (row >= 0) {
-            const uint32_t dst = dst0 + r.stage * C::kRing;
+          if (n >= 0 && n < nt) {
+            if (c >= stages && !(ok = wait_all(bar(empty0 + r.stage), r.phase ^ 1))) break;
+            const uint32_t full = bar(full0 + r.stage);
+            const int nslices = __popc(__ballot_sync(kFull, row >= 0));
+            if (lane == 0) mbar_arrive_expect_tx(full, nslices * C::kRawBoxes * 2048);
+            __syncwarp();
+            if (row >= 0) {
+              const uint32_t dst = dst0 + r.stage * C::kRing;
 #pragma unroll
-            for (int box = 0; box < static_cast<int>(C::kRawBoxes); ++box)
-              tma_load_2d(dst + box * C::kBox, map, box * (FP8 ? 128 : 64), row, full);
+              for (int box = 0; box < static_cast<int>(C::kRawBoxes); ++box)
+                tma_load_2d(dst + box * C::kBox, map, box * (FP8 ? 128 : 64), row, full);
+            }
+            __syncwarp();
+            r.next(stages);
+            ++c;
           }
-          __syncwarp();
-          r.next(stages);
           row = next;
           // the next item, once this one's first copies are on their way
-          if (!is_v && n == min(nt, 2) - 1) {
+          if (!is_v && n == max(min(nt, 2), 1) - 1) {
             later = publish(k + 1);
             if (!ok) break;
           }
         }
-        if (!is_v) {
-          if (nt == 0) later = publish(k + 1);
-          row = later;
-        }
+        if (!is_v) row = later;
       }
       if (!ok) {
         if (lane == 0) atomicOr(a.err, PA_DEVERR_TIMEOUT);
@@ -663,8 +666,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
 #pragma unroll 1
           for (int n = 0; n < nt; ++n) {
             if (!(ok = wait_all(bar(kKReady + ring.stage), ring.phase))) break;
-            job(dual);
-            if (dual && ok) job(true);
+#pragma unroll 1
+            for (int i = dual ? 2 : 1; i > 0 && ok; --i) job(dual);
             if (!ok) break;
             commit_all(bar(kKFree + ring.stage));
             ring.next(KB);
@@ -724,8 +727,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
 #pragma unroll 1
           for (int n = 0; n < nt; ++n) {
             if (!(ok = wait_all(bar(kVReady + ring.stage), ring.phase))) break;
-            job();
-            if (dual && ok) job();
+#pragma unroll 1
+            for (int i = dual ? 2 : 1; i > 0 && ok; --i) job();
             if (!ok) break;
             commit_all(bar(kVFree + ring.stage));
             ring.next(VB);
@@ -891,33 +894,39 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       }
     };
     if constexpr (FP8) {
-      constexpr int kChunks = D / 16, kPer = 32 / kChunks;  // chunks a row, rows a pass
-      constexpr int kOctets = KV / 8;                       // of rows: a warp takes every fourth
-      const int o0 = warp - C::kStoreWarp;
-      const int ch = lane % kChunks, q0 = lane / kChunks;
-      const int c16 = 2 * (ch & 3);
-      // rows [r_lo, r_hi) are converted, the others become zeros
+      // A warp takes every fourth octet of rows, a lane a row of it and every fourth
+      // 16-byte chunk: the eight lanes of an access then have eight rows, whose chunks the
+      // swizzle puts into different banks, in the raw tile as in the f16 one.
+      constexpr int kOctets = KV / 32, kParts = D / 64;
+      const int o0 = warp - C::kStoreWarp, sub = lane & 7, ch = lane >> 3;
+      const uint32_t from0 = (8 * o0 + sub) * 128 + ((ch ^ sub) << 4);
+      const uint32_t to_lo = (8 * o0 + sub) * 128 + (((2 * ch) ^ sub) << 4), to_hi = to_lo ^ 16;
+      // Rows [r_lo, r_hi) are converted, the others become zeros.
       auto convert = [&](uint32_t src, uint32_t dst, int r_lo, int r_hi) {
-        src += (ch >> 3) * C::kBox;
-        dst += (ch >> 2) * C::kBox;
-        static_assert(8 % kPer == 0, "passes of a row octet");
+        constexpr int N = NX == 2 ? 2 : 8;  // chunks of a lane at once
+        static_assert(kOctets * kParts == 8, "chunks a lane");
+        const bool part = r_lo > 0 || r_hi < KV;
 #pragma unroll 1
-        for (int p = 0; p < 8 / kPer; ++p) {
-          const int r0 = 8 * o0 + q0 + kPer * p;  // rows r0, r0 + 32, ... share one swizzle
-          const uint32_t from = src + r0 * 128 + (((ch & 7) ^ (r0 & 7)) << 4);
-          const uint32_t lo = dst + r0 * 128 + ((c16 ^ (r0 & 7)) << 4);
-          const uint32_t hi = dst + r0 * 128 + (((c16 + 1) ^ (r0 & 7)) << 4);
-#pragma unroll 2
-          for (int k = 0; k < kOctets; k += 4) {
-            uint32_t w[4] = {0u, 0u, 0u, 0u}, h[8];
-            if (r0 + 8 * k >= r_lo && r0 + 8 * k < r_hi) lds_v4(from + 1024 * k, w[0], w[1], w[2], w[3]);
+        for (int g = 0; g < 8; g += N) {
+          uint32_t w[N][4];
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            const int p = (g + j) / kOctets, k = (g + j) % kOctets;
+            lds_v4(src + (from0 ^ ((p & 1) << 6)) + (p >> 1) * C::kBox + 4096 * k, w[j][0], w[j][1], w[j][2], w[j][3]);
+          }
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            const int p = (g + j) / kOctets, k = (g + j) % kOctets, row = 8 * (o0 + 4 * k) + sub;
+            uint32_t (&x)[4] = w[j];
+            if (part && (row < r_lo || row >= r_hi)) x[0] = x[1] = x[2] = x[3] = 0u;
+            uint32_t h[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              h[2 * i] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] & 0xffffu));
-              h[2 * i + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] >> 16));
+              h[2 * i] = e4m3x2_to_f16x2(static_cast<uint16_t>(x[i] & 0xffffu));
+              h[2 * i + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(x[i] >> 16));
             }
-            sts_v4(lo + 1024 * k, make_uint4(h[0], h[1], h[2], h[3]));
-            sts_v4(hi + 1024 * k, make_uint4(h[4], h[5], h[6], h[7]));
+            sts_v4(dst + to_lo + p * C::kBox + 4096 * k, make_uint4(h[0], h[1], h[2], h[3]));
+            sts_v4(dst + to_hi + p * C::kBox + 4096 * k, make_uint4(h[4], h[5], h[6], h[7]));
           }
         }
       };
@@ -977,25 +986,24 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         do {
           if (n < nt) {
             const uint32_t free_par = (c - 2) >> 1;  // of the buffers' last tile
-            if (!(ok = wait_all(bar(C::kBarKFull), c))) break;
-            if (c > 1 && !(ok = wait_all(bar(C::kBarCKFree + (c & 1)), free_par))) break;
-            convert(sK, sKc + (c & 1) * C::kTile, 0, KV);
-            fence_proxy_async();  // the f16 tile, visible to the tensor core
-            mbar_arrive(bar(C::kBarCKFull + (c & 1)));
-            mbar_arrive(bar(C::kBarKEmpty));  // reload the stage
-            if (n == 0) {
-              if (kConvertQ) {
-                if (!(ok = wait_all(bar(kBarQRaw), live))) break;
-                convert_q(ntok, live);
+            constexpr int kCopies = NX == 2 ? 1 : 2;
+#pragma unroll kCopies
+            for (int h = 0; h < 2; ++h) {  // K, V
+              if (!(ok = wait_all(bar(h ? C::kBarVFull : C::kBarKFull), c))) break;
+              if (c > 1 && !(ok = wait_all(bar((h ? C::kBarCVFree : C::kBarCKFree) + (c & 1)), free_par))) break;
+              convert(h ? sV : sK, (h ? sVc : sKc) + (c & 1) * C::kTile, h ? v_lo - n * KV : 0, h ? v_hi - n * KV : KV);
+              fence_proxy_async();  // the f16 tile, visible to the tensor core
+              mbar_arrive(bar((h ? C::kBarCVFull : C::kBarCKFull) + (c & 1)));
+              mbar_arrive(bar(h ? C::kBarVEmpty : C::kBarKEmpty));  // reload the stage
+              if (h == 0 && n == 0) {
+                if (kConvertQ) {
+                  if (!(ok = wait_all(bar(kBarQRaw), live))) break;
+                  convert_q(ntok, live);
+                }
+                ++live;
               }
-              ++live;
             }
-            if (!(ok = wait_all(bar(C::kBarVFull), c))) break;
-            if (c > 1 && !(ok = wait_all(bar(C::kBarCVFree + (c & 1)), free_par))) break;
-            convert(sV, sVc + (c & 1) * C::kTile, v_lo - n * KV, v_hi - n * KV);
-            fence_proxy_async();
-            mbar_arrive(bar(C::kBarCVFull + (c & 1)));
-            mbar_arrive(bar(C::kBarVEmpty));
+            if (!ok) break;
             ++c;
           }
           if (n == 0 && k > 0) store(k - 1);
@@ -1087,6 +1095,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         if (valid) sc = fmaxf(FLT_MIN, ldexpf(sc, lds_s8(base + C::kShift + (which & 1) * NX * kRows + xt * kRows + r)));
       }
       float ms = kFloor, l = 0.f;  // reference max (scaled, log2 units) and running sum
+#pragma unroll 1
       for (int j = j0; j < nj; j += step, ++mine) {
         const int n = dual ? j >> 1 : j, t0 = n * KV;
         const int buf = NX == 2 ? x : ((s + j) & 1);
@@ -1114,23 +1123,25 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           uint32_t bad = 0;
           if (r < KV) {
             const int pos = t0 + r;
+            const uint32_t at = vt + r * 128;
             if (pos >= u_lo && pos < u_hi) {
+#pragma unroll 1
+              for (int i = 0; i < 8 * C::kBoxes; i += 4) {
+                uint32_t w[4][4];
 #pragma unroll
-              for (int box = 0; box < C::kBoxes; ++box)
+                for (int e = 0; e < 4; ++e)
+                  lds_v4(at + (i >> 3) * C::kBox + ((((i & 4) + e) ^ (r & 7)) << 4), w[e][0], w[e][1], w[e][2], w[e][3]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  uint32_t w[4];
-                  lds_v4(vt + box * C::kBox + r * 128 + ((i ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
-                  bad |= nonfinite<kBf16>(w[0]) | nonfinite<kBf16>(w[1]) | nonfinite<kBf16>(w[2]) |
-                         nonfinite<kBf16>(w[3]);
-                }
+                for (int e = 0; e < 4; ++e)
+                  bad |= nonfinite<kBf16>(w[e][0]) | nonfinite<kBf16>(w[e][1]) | nonfinite<kBf16>(w[e][2]) |
+                         nonfinite<kBf16>(w[e][3]);
+              }
+              bad &= 0x80008000u;
             } else if (!FP8 && (!dual || !(j & 1))) {
               // outside of the range: zeros, before the tile's first product
-#pragma unroll
-              for (int box = 0; box < C::kBoxes; ++box)
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  sts_v4(vt + box * C::kBox + r * 128 + i * 16, make_uint4(0u, 0u, 0u, 0u));
+#pragma unroll 1
+              for (int i = 0; i < 8 * C::kBoxes; ++i)
+                sts_v4(at + (i >> 3) * C::kBox + (i & 7) * 16, make_uint4(0u, 0u, 0u, 0u));
             }
           }
           fence_proxy_async();
@@ -1162,9 +1173,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           auto mask_out = [&](int c) {
             if (!all_in) {
 #pragma unroll
-              for (int q = 0; q < 2; ++q)
+              for (int q = 0; q < 2; ++q) {
+                if (__all_sync(kFull, !valid || mask[c + q] == 0xffffffffu)) continue;
 #pragma unroll
                 for (int i = 0; i < 32; ++i) sv[c + q][i] = (mask[c + q] >> i) & 1 ? sv[c + q][i] : 0xff800000u;
+              }
             }
           };
           mask_out(0);
