@@ -625,7 +625,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           if (jobs >= 2 && !(ok = wait_all(bar(kBarO + x), (jobs - 2) >> 1))) return;
           tc::fence_after_sync();
           const uint64_t q = dQ + (own_rows && x ? C::kQBytes >> 4 : 0);
-#pragma unroll
+          constexpr int kAtOnce = NX == 2 ? 1 : C::kBoxes;
+#pragma unroll kAtOnce
           for (int box = 0; box < C::kBoxes; ++box)
             mma4_ss_all(tm + C::kColS + KV * x, q + ((box * C::kQBox) >> 4),
                         dK + ((ring.stage * C::kTile + box * C::kBox) >> 4), idS, box > 0);
@@ -682,7 +683,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         // of each group: items begun in its O (the parity is all that counts, a bit each),
         // whether there was one, whether O holds something of this item
         uint32_t o_items = 0, o_any = 0, begun = 0;
-        auto job = [&]() {
+        auto job = [&](bool masked) {
           const int x = jobs & 1, g = NX == 2 ? x : 0;
           if (!(begun >> g & 1)) {  // the last item's result has been read
             if ((o_any >> g & 1) && !(ok = wait_all(bar(kBarOFree + g), (o_items >> g) ^ 1))) return;
@@ -692,7 +693,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           if (!(ok = wait_all(bar(kBarP + x), jobs >> 1))) return;
           tc::fence_after_sync();
           volatile uint32_t* skip = reinterpret_cast<volatile uint32_t*>(smem_raw + C::kSkip) + x;
-          if (__any_sync(kFull, *skip != 0)) {  // the group has added this tile itself
+          if (masked && __any_sync(kFull, *skip != 0)) {  // the group has added this tile itself
             if (lane == 0) *skip = 0;
             __syncwarp();
           } else {
@@ -719,7 +720,13 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           PackedItem it;
           if (!(ok = item_at(k, &it))) break;
           const int nt = __shfl_sync(kFull, it.nt, 0);
-          const bool dual = NX == 2 && __shfl_sync(kFull, it.ntok, 0) > a.tpg;
+          const int ntok = __shfl_sync(kFull, it.ntok, 0), start = __shfl_sync(kFull, (it.lo & ~15) + it.tile0 * KV, 0);
+          const bool dual = NX == 2 && ntok > a.tpg;
+          // tiles that all rows attend to in full lie between (the groups look through the others)
+          const int sure_hi = (a.tree ? __shfl_sync(kFull, it.first, 0) : __shfl_sync(kFull, it.pos0, 0) + 1) - start;
+          const int sure_lo =
+              a.window <= 0 ? -start
+                            : (a.tree ? __shfl_sync(kFull, it.hi, 0) + 1 : __shfl_sync(kFull, it.pos0, 0) + ntok) - a.window - start;
           item_done(k);
           if (nt < 0) break;
           if (nt == 0) continue;
@@ -728,7 +735,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           for (int n = 0; n < nt; ++n) {
             if (!(ok = wait_all(bar(kVReady + ring.stage), ring.phase))) break;
 #pragma unroll 1
-            for (int i = dual ? 2 : 1; i > 0 && ok; --i) job();
+            for (int i = dual ? 2 : 1; i > 0 && ok; --i) job(n * KV < sure_lo || (n + 1) * KV > sure_hi);
             if (!ok) break;
             commit_all(bar(kVFree + ring.stage));
             ring.next(VB);
