@@ -1122,12 +1122,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           }
         }
         bool skip = false;
-        // (S before V: behind this S are the group's last products, so that V's barrier is
-        // at most one phase behind the one that is waited for below)
-        if (!(ok = wait_all(bar(kBarS + buf), phase))) break;
         // A tile that some row does not attend to in full.
         if (t0 < sure_lo || t0 + KV > sure_hi) {
           const uint32_t c = tiles + n, stage = c % VB;
+          // (S before V, where V's barrier has phases behind it: this S follows the group's last
+          // products, so that the phase before the one that is waited for is complete)
+          if (c >= VB && !(ok = wait_all(bar(kBarS + buf), phase))) break;
           if (!(ok = wait_all(bar(kVReady + stage), c / VB))) break;
           const uint32_t vt = sVt + stage * C::kTile;
           uint32_t bad = 0;
@@ -1167,6 +1167,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           lds_v4(look, w[0], w[1], w[2], w[3]);
           skip = (w[0] | w[1] | w[2] | w[3]) != 0;
         }
+        if (!(ok = wait_all(bar(kBarS + buf), phase))) break;
         tc::fence_after_sync();
         if (alive) {
           uint32_t sv[KV / 32][32];
