@@ -8,18 +8,26 @@
 // with a running reference m per row, which moves only when a score exceeds it by
 // more than 2^8, and out = O / l.
 //
-// Roles: one warp works out the CTA's items, in a ring that all others read them from, and
-// streams K tiles, one streams V tiles (TMA through the block
-// table), one loads Q and issues the products S, one issues the products O, groups of four softmax
-// warps serve a 128-row tile each (one row a thread), and four warps store the results,
-// so that a group goes on with its next item while the last one's output is written.
-// (With one warp for all products, its own waits and instruction fetches, 700 cycles a job
-// beside 1,050 of tensor work, came in the way of both.)
+// Roles: one warp works out the CTA's items, in a ring that all others read them from,
+// and streams K tiles, one streams V tiles (TMA through the block table), one loads Q and
+// issues the products S, one issues the products O, groups of four softmax warps serve a
+// 128-row tile each (one row a thread), and four warps store the results, so that a group
+// goes on with its next item while the last one's output is written. (With one warp for
+// all products, its own waits and instruction fetches, 700 cycles a job beside 1,050 of
+// tensor work, came in the way of both.)
 // A job is the product of a row tile and a K/V tile; jobs alternate between the two
 // groups (a unit of more than 128 rows: each group has its rows and every tile; one of
 // at most 128: both groups have the same rows, each every other tile, joined by the
-// storing warps). S runs two jobs ahead of the softmax, across items. head_dim 256 has one group, whose S has two buffers (its O fills
-// half of the tensor memory).
+// storing warps). S runs two jobs ahead of the softmax, across items. head_dim 256 has one
+// group, whose S has two buffers (its O fills half of the tensor memory).
+//
+// Bound: a K/V tile of two row tiles is 2,112 cycles of tensor work (M128 N128 K16: 66)
+// and takes 2,650, as S, softmax and O of a row tile follow each other in one buffer and
+// only the other group's fill the gaps; one prompt of 16,384 tokens, 32 heads: 1.40 ms,
+// 1,570 TFLOP/s at 1.39 kW. An item costs about 7,000 cycles besides: Q's load behind the
+// last products, the masked tiles, O read out. What the warps run must stay small: some
+// 5,000 instructions a kernel share the instruction cache, and one copy of each piece of
+// code in place of two or three gave 4 to 13%.
 //
 // Masks: a row's attended positions in a tile are a bit word per 32 tokens (a range,
 // and for a tree the ancestor bits moved to the tile); tiles that every row of a
@@ -557,9 +565,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       };
       // Item -1 stands for the start: nothing but the first item to be worked out. (One copy
       // of each piece of code: what the warps of a CTA run in turn has to share the
-      // instruction cache, whose misses show in every kernel time here.)
+      // instruction cache, whose misses show in every kernel time here. A small step is
+      // over too soon for that, and 0.3 us faster with the first item by itself.)
       int row = -1, later = -1;
-      for (int k = -1; ok; ++k) {
+      if (SMALL && !is_v) row = publish(0);
+      for (int k = SMALL ? 0 : -1; ok; ++k) {
         int b = 0, kvh = 0, start = 0, hi = 0, nt = 0;  // (in uniform registers)
         if (k >= 0) {
           PackedItem it;
