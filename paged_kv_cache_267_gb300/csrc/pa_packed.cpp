@@ -86,8 +86,7 @@ PackedSizes packed_sizes(int64_t T, int64_t B, int64_t span, int G, int64_t Hkv,
   // lane b of a warp plans sequence b; with more pairs than a few a CTA, whole ones, sorted,
   // are better (a batch of 16 prompts takes 343 us split, 232 whole)
   z.small = B <= 32 && units * Hkv <= kSmallPairs * num_sms &&
-            dprod({double(units), double(Hkv), double(pair_places(static_cast<int>(std::min<int64_t>(span / z.kv + 2, 1 << 28)), true))}) <
-                k2p31 - 65536;
+            dprod({double(units), double(Hkv), 4.0 * double(span / z.kv + 2) + kOutPlaces}) < k2p31 - 65536;
   const double tiles = dprod({double(units), double(Hkv), double(span / z.kv + 2)});
   z.ctas = static_cast<int>(std::min<double>(num_sms, std::max(1.0, std::ceil(tiles * 4 / kMinPlaces))));
   z.plan_words = packed_plan_words(z.ctas, static_cast<size_t>(units));
@@ -210,7 +209,6 @@ pa_status packed_attention(const pa_tensor* out, const pa_tensor* q, const pa_te
     cudaError_t e = z.small ? cudaSuccess : packed_plan_launch(p, cs, true);
     if (e != cudaSuccess) return cuda_fail(e, "packed plan launch");
     PackedArgs a;
-    a.q = q->data;
     a.out = out->data;
     a.block_tables = static_cast<const int32_t*>(block_tables->data);
     a.tree = tree ? static_cast<const int64_t*>(tree_mask->data) : nullptr;
@@ -224,10 +222,8 @@ pa_status packed_attention(const pa_tensor* out, const pa_tensor* q, const pa_te
     a.tpu = z.tpu;
     a.kv = z.kv;
     a.min_places = kMinPlaces;
-    a.q_stride = q->strides[0];
     a.out_stride = out->strides[0];
     a.ctas = z.ctas;
-    a.Hq = static_cast<int>(Hq);
     a.Hkv = p.Hkv;
     a.G = G;
     a.bs = block_size;
@@ -247,7 +243,6 @@ pa_status packed_attention(const pa_tensor* out, const pa_tensor* q, const pa_te
     m.plan = p.plan;
     m.out_stride = a.out_stride;
     m.ctas = z.ctas;
-    m.Hq = a.Hq;
     m.G = G;
     m.D = static_cast<int>(D);
     m.tpg = z.tpg;

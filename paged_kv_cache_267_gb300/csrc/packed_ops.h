@@ -30,7 +30,6 @@ struct PackedPlanArgs {
 cudaError_t packed_plan_launch(const PackedPlanArgs& a, cudaStream_t s, bool pdl);
 
 struct PackedArgs {
-  const void* q;                // [T, Hq, D], rows of q_stride elements
   void* out;                    // [T, Hq, D], rows of out_stride elements
   const int32_t* block_tables;  // [B, MB]
   const int64_t* tree;          // [T] ancestor bits, or null: causal
@@ -40,8 +39,8 @@ struct PackedArgs {
   const int32_t* query_start;   // [B + 1], small steps: each CTA plans by itself
   const int32_t* seq_lens;      // [B]
   int B, T, tpu, kv, min_places;  // as in PackedPlanArgs
-  int64_t q_stride, out_stride;
-  int ctas, Hq, Hkv, G, bs, MB, NB, window;
+  int64_t out_stride;
+  int ctas, Hkv, G, bs, MB, NB, window;
   int tpg;                      // tokens a row tile: 128 / G
   int slot_rows;                // rows of a partial result
   float score_scale;            // scale * log2(e) (* k_scale for FP8)
@@ -57,7 +56,7 @@ struct PackedMergeArgs {
   const float* part;
   const int32_t* plan;
   int64_t out_stride;
-  int ctas, Hq, G, D, tpg, slot_rows;
+  int ctas, G, D, tpg, slot_rows;
   bool small;                   // the plan is complete only behind the attention
 };
 cudaError_t packed_merge_launch(int out_type, const PackedMergeArgs& a, cudaStream_t s, bool pdl);

@@ -197,9 +197,9 @@ __device__ __forceinline__ void mma_ts_all(uint32_t d, uint32_t a, uint64_t b, u
         : "memory");
   }
 }
-// Column of S where half h of a tile's weights begins: 128 tokens' sit over columns 0-31
-// and 64-95, 64 tokens' over 0-15 and 16-31.
-__device__ __forceinline__ constexpr int half_col(int kv, int h) { return h * (kv == 128 ? 64 : 16); }
+// Column of S where the second half of a tile's weights begins: 128 tokens' sit over
+// columns 0-31 and 64-95, 64 tokens' over 0-15 and 16-31.
+__device__ __forceinline__ constexpr int half_col(int kv) { return kv == 128 ? 64 : 16; }
 __device__ __forceinline__ void commit_all(uint32_t bar) {
   asm volatile(
       "{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\n"
@@ -709,13 +709,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           } else {
             // the half of the weights that is written first, then the other
             constexpr int kSteps = KV / 32;  // of 16 tokens a half
-            constexpr int h0 = 0, h1 = 1;
             const uint32_t o = tm + C::kColO + D * g, p = tm + C::kColS + KV * x;
             const uint64_t v = dV + ((ring.stage * C::kTile) >> 4);
-            mma_ts_all<kSteps>(o, p + half_col(KV, h0), v + 128 * kSteps * h0, idO, begun >> g & 1);
+            mma_ts_all<kSteps>(o, p, v, idO, begun >> g & 1);
             if (!(ok = wait_all(bar(kBarP2 + x), jobs >> 1))) return;
             tc::fence_after_sync();
-            mma_ts_all<kSteps>(o, p + half_col(KV, h1), v + 128 * kSteps * h1, idO, 1u);
+            mma_ts_all<kSteps>(o, p + half_col(KV), v + 128 * kSteps, idO, 1u);
           }
           commit_all(bar(kBarO + x));
           begun |= 1u << g;
@@ -734,9 +733,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           const bool dual = NX == 2 && ntok > a.tpg;
           // tiles that all rows attend to in full lie between (the groups look through the others)
           const int sure_hi = (a.tree ? __shfl_sync(kFull, it.first, 0) : __shfl_sync(kFull, it.pos0, 0) + 1) - start;
-          const int sure_lo =
-              a.window <= 0 ? -start
-                            : (a.tree ? __shfl_sync(kFull, it.hi, 0) + 1 : __shfl_sync(kFull, it.pos0, 0) + ntok) - a.window - start;
+          const int end = a.tree ? __shfl_sync(kFull, it.hi, 0) + 1 : __shfl_sync(kFull, it.pos0, 0) + ntok;
+          const int sure_lo = (a.window > 0 ? end - a.window : 0) - start;
           item_done(k);
           if (nt < 0) break;
           if (nt == 0) continue;
@@ -913,7 +911,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     if constexpr (FP8) {
       // A warp takes every fourth octet of rows, a lane a row of it and every fourth
       // 16-byte chunk: the eight lanes of an access then have eight rows, whose chunks the
-      // swizzle puts into different banks, in the raw tile as in the f16 one.
+      // swizzle puts into different banks, in the raw tile as in the f16 one. Two chunks at a
+      // time: with 1 or 4, 64 trees take 277 or 268 us instead of 256 (more of them are
+      // faster by themselves, but their instructions displace the other warps'). With one
+      // softmax group there is room for 8 and a copy each for K and V: 1,024 rows on 16,384
+      // tokens at head_dim 256 take 590 us instead of 650.
       constexpr int kOctets = KV / 32, kParts = D / 64;
       const int o0 = warp - C::kStoreWarp, sub = lane & 7, ch = lane >> 3;
       const uint32_t from0 = (8 * o0 + sub) * 128 + ((ch ^ sub) << 4);
@@ -1336,7 +1338,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             tc::wait_st();
             tc::fence_before_sync();
             mbar_arrive(bar(kBarP + buf));
-            weigh(KV == 128 ? 2 : 0, KV == 128 ? 0 : 32, half_col(KV, 1));
+            weigh(KV == 128 ? 2 : 0, KV == 128 ? 0 : 32, half_col(KV));
             const float2 s01 = __fadd2_rn(sp[0], sp[1]), s23 = __fadd2_rn(sp[2], sp[3]);
             const float2 st = __fadd2_rn(s01, s23);
             l += st.x + st.y;
