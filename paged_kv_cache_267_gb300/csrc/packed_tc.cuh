@@ -1137,9 +1137,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         // A tile that some row does not attend to in full.
         if (t0 < sure_lo || t0 + KV > sure_hi) {
           const uint32_t c = tiles + n, stage = c % VB;
-          // (S before V, where V's barrier has phases behind it: this S follows the group's last
-          // products, so that the phase before the one that is waited for is complete)
-          if (c >= VB && !(ok = wait_all(bar(kBarS + buf), phase))) break;
+          // S before V, but for a first look at a first tile: this S follows earlier products of
+          // the group, so that the phase of V's barrier before the one that is waited for is
+          // complete, and all warps have read what the last look found (one group: the last but one).
+          if ((c >= VB || looks > 0) && !(ok = wait_all(bar(kBarS + buf), phase))) break;
           if (!(ok = wait_all(bar(kVReady + stage), c / VB))) break;
           const uint32_t vt = sVt + stage * C::kTile;
           uint32_t bad = 0;
@@ -1168,7 +1169,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           }
           fence_proxy_async();
           // what any warp of the group has found
-          const uint32_t look = base + C::kLook + 16 * x;
+          const uint32_t look = base + C::kLook + 16 * (NX == 2 ? x : looks & 1);
           const bool any_bad = __any_sync(kFull, bad != 0);
           if (lane == 0) {
             sts_b32(look + 4 * (warp & 3), any_bad ? 1u : 0u);
