@@ -67,19 +67,21 @@ constexpr float kF16Lift = 7.f;              // log2 units
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kItemRing = 3;                 // items known at once
 
-template <int D, bool FP8>
+template <int QT, int D, bool FP8>
 struct Cfg {
   static constexpr int kGroups = packed_shape(D).rows;  // softmax groups
   static constexpr int kKv = packed_shape(D).kv;        // tokens a tile
   static constexpr int kSlices = kKv / 16;
   static constexpr int kBoxes = D / 64;  // 64-dim boxes of a 16-bit tile
-  static constexpr int kKStages = FP8 ? 1 : (D == 64 ? 4 : 2), kVStages = FP8 ? 1 : (D == 64 ? 4 : 3);
+  // FP8: Q as a sum of e4m3 values, as many as its type's bits need
+  static constexpr int kTerms = FP8 ? (QT == kBF16 ? 2 : 3) : 1;
+  static constexpr int kKStages = FP8 ? (kTerms == 2 ? 3 : 2) : (D == 64 ? 4 : 2);
+  static constexpr int kVStages = FP8 ? 2 : (D == 64 ? 4 : 3);
   static constexpr int kStages = kKStages > kVStages ? kKStages : kVStages;
   // Barriers: K and V rings (full, empty); per S buffer: computed, half of P written, the
   // other half, product with V complete; Q loaded, ready (items in turn) and done with; per
   // group: last product of an item complete, O and statistics read, statistics written,
-  // a tile's V looked through; FP8: converted K and V (two buffers each) written and
-  // read; items known and read; the ends of the two product warps.
+  // a tile's V looked through; FP8: converted V (two buffers) written and read; items known and read; the ends of the two product warps.
   enum {
     kBarKFull = 0,
     kBarKEmpty = kBarKFull + kStages,
@@ -96,9 +98,7 @@ struct Cfg {
     kBarOFree = kBarOFull + 2,
     kBarStat = kBarOFree + 2,
     kBarLook = kBarStat + 2,
-    kBarCKFull = kBarLook + 2,
-    kBarCKFree = kBarCKFull + 2,
-    kBarCVFull = kBarCKFree + 2,
+    kBarCVFull = kBarLook + 2,
     kBarCVFree = kBarCVFull + 2,
     kBarItem = kBarCVFree + 2,
     kBarItemFree = kBarItem + kItemRing,
@@ -119,7 +119,7 @@ struct Cfg {
   static_assert(kThreads == 384 || (kThreads == 512 && kGroups == 2 && 2 * kSoftmaxRegs + kStoreRegs +
                                                                            kOtherRegs == 4 * kLaunchRegs),
                 "registers of the block");
-  static constexpr uint32_t kQBox = kRows * 128, kQBytes = kBoxes * kQBox;  // one row tile's Q
+  static constexpr uint32_t kQBox = kRows * 128, kQBytes = (FP8 ? kTerms * D / 128 : kBoxes) * kQBox;  // one row tile's Q
   static constexpr uint32_t kBox = kKv * 128, kTile = kBoxes * kBox;        // 16-bit K or V tile
   static constexpr uint32_t kRawBoxes = FP8 ? D / 128 : kBoxes;             // 128-byte boxes
   static constexpr uint32_t kRing = kRawBoxes * kBox;                       // ring tile
@@ -129,8 +129,11 @@ struct Cfg {
                             kStat = kShift + (FP8 ? 2 * kGroups * kRows : 0),
                             kSmall = kStat + kGroups * 2 * kRows * 4;
   static constexpr uint32_t kQ = (kSmall + 1023) / 1024 * 1024, kK = kQ + kGroups * kQBytes,
-                            kV = kK + kKStages * kRing, kKc = kV + kVStages * kRing,
-                            kVc = kKc + (FP8 ? 2 * kTile : 0), kBytes = kVc + (FP8 ? 2 * kTile : 0);
+                            kV = kK + kKStages * kRing, kVc = kV + kVStages * kRing,
+                            kBytes = kVc + (FP8 ? 2 * kTile : 0);
+  // where term t of Q's head dims 128 b .. 128 b + 127 is, in boxes: terms 0 and 1 in the
+  // place of the 16-bit values that they are made of
+  __device__ static constexpr int q_region(int t, int b) { return t < 2 ? 2 * b + t : D / 64 + b; }
   static constexpr uint32_t kColS = 0, kColO = 2 * kKv;
   static_assert(kLook % 16 == 0 && kItem % 16 == 0 && kStat % 8 == 0, "alignment of what is read at once");
   static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
@@ -147,23 +150,40 @@ __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity) {
 // Products issued by a whole warp in step: every lane comes here with the same values,
 // which then sit in uniform registers, and one elected lane issues. (Issued by one lane
 // of a diverged warp, each product took 60 to 90 cycles to move its descriptors, 1,300 a
-// job of 1,024 cycles of tensor work.) Four M128 K16 steps over one 64-element swizzled
-// box, A and B in shared memory; the first accumulates iff acc0 != 0.
+// job of 1,024 cycles of tensor work.) Four M128 steps of 32 bytes (K16, of e4m3 K32) over
+// one swizzled box, A and B in shared memory; the first accumulates iff acc0 != 0.
+template <bool F8>
 __device__ __forceinline__ void mma4_ss_all(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                             uint32_t acc0) {
+  if constexpr (F8) {
   asm volatile(
-      "{\n.reg .pred p0, p1, e;\n.reg .b64 ad, bd;\n"
-      "elect.sync _|e, 0xffffffff;\n"
-      "setp.ne.b32 p0, %4, 0;\nsetp.eq.b32 p1, 0, 0;\n"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p0;\n"
-      "add.u64 ad, %1, 2;\nadd.u64 bd, %2, 2;\n"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %3, p1;\n"
-      "add.u64 ad, %1, 4;\nadd.u64 bd, %2, 4;\n"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %3, p1;\n"
-      "add.u64 ad, %1, 6;\nadd.u64 bd, %2, 6;\n"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %3, p1;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc0)
-      : "memory");
+        "{\n.reg .pred p0, p1, e;\n.reg .b64 ad, bd;\n"
+        "elect.sync _|e, 0xffffffff;\n"
+        "setp.ne.b32 p0, %4, 0;\nsetp.eq.b32 p1, 0, 0;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p0;\n"
+        "add.u64 ad, %1, 2;\nadd.u64 bd, %2, 2;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], ad, bd, %3, p1;\n"
+        "add.u64 ad, %1, 4;\nadd.u64 bd, %2, 4;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], ad, bd, %3, p1;\n"
+        "add.u64 ad, %1, 6;\nadd.u64 bd, %2, 6;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], ad, bd, %3, p1;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc0)
+        : "memory");
+  } else {
+  asm volatile(
+        "{\n.reg .pred p0, p1, e;\n.reg .b64 ad, bd;\n"
+        "elect.sync _|e, 0xffffffff;\n"
+        "setp.ne.b32 p0, %4, 0;\nsetp.eq.b32 p1, 0, 0;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p0;\n"
+        "add.u64 ad, %1, 2;\nadd.u64 bd, %2, 2;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %3, p1;\n"
+        "add.u64 ad, %1, 4;\nadd.u64 bd, %2, 4;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %3, p1;\n"
+        "add.u64 ad, %1, 6;\nadd.u64 bd, %2, 6;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %3, p1;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc0)
+        : "memory");
+  }
 }
 // 2 or 4 M128 K16 steps with A in tensor memory: step k reads A 8 k columns on and B 16 k
 // rows (2048 k bytes) on.
@@ -365,6 +385,12 @@ __device__ __forceinline__ uint32_t nonfinite(uint32_t w) {
   constexpr uint32_t m = BF16 ? 0x7f807f80u : 0x7c007c00u, one = BF16 ? 0x00800080u : 0x04000400u;
   return (w & m) + one;
 }
+// Two e4m3 values, nearest.
+__device__ __forceinline__ uint32_t e4m3x2_of(float lo, float hi) {
+  uint16_t v;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(v) : "f"(hi), "f"(lo));
+  return v;
+}
 __device__ __forceinline__ void lds_f32x2(uint32_t addr, float& a, float& b) {
   asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(a), "=f"(b) : "r"(addr) : "memory");
 }
@@ -395,28 +421,27 @@ __device__ __forceinline__ uint32_t below(int k) {
 
 // SMALL: a small step, which has no plan kernel.
 template <int QT, int D, bool FP8, bool SMALL>
-__global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
+__global__ void __launch_bounds__(Cfg<QT, D, FP8>::kThreads, 1)
     packed_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK,
                           const __grid_constant__ CUtensorMap tmV,
                           const __grid_constant__ CUtensorMap tmQ, const PackedArgs a) {
-  using C = Cfg<D, FP8>;
+  using C = Cfg<QT, D, FP8>;
   constexpr bool kBf16 = !FP8 && QT == kBF16;  // operand type of the products
-  constexpr bool kConvertQ = FP8 && QT == kBF16;
   constexpr float kLift = kBf16 ? 0.f : kF16Lift;
   constexpr int NX = C::kGroups, KV = C::kKv;
   constexpr int kBarS = C::kBarS, kBarP = C::kBarP, kBarP2 = C::kBarP2, kBarO = C::kBarO, kBarQRaw = C::kBarQRaw,
                 kBarQFull = C::kBarQFull, kBarQFree = C::kBarQFree, kBarOFull = C::kBarOFull,
                 kBarOFree = C::kBarOFree, kBarStat = C::kBarStat, kBarLook = C::kBarLook, kBarItem = C::kBarItem,
                 kBarItemFree = C::kBarItemFree;
-  // Positions of the K and V tiles in use, and the barriers that say they are ready:
-  // the ring's, or the converted buffers' (two of each).
-  constexpr int KB = FP8 ? 2 : C::kKStages, VB = FP8 ? 2 : C::kVStages;
-  constexpr int kKReady = FP8 ? C::kBarCKFull : C::kBarKFull, kKFree = FP8 ? C::kBarCKFree : C::kBarKEmpty;
+  // Positions of the V tiles in use, and the barriers that say they are ready: the ring's,
+  // or the two converted buffers'.
+  constexpr int KB = C::kKStages, VB = FP8 ? 2 : C::kVStages;
+  constexpr int kKReady = C::kBarKFull, kKFree = C::kBarKEmpty;
   constexpr int kVReady = FP8 ? C::kBarCVFull : C::kBarVFull, kVFree = FP8 ? C::kBarCVFree : C::kBarVEmpty;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t base = smem_addr(smem_raw);
   const uint32_t sQ = base + C::kQ, sK = base + C::kK, sV = base + C::kV;
-  const uint32_t sKc = base + C::kKc, sVc = base + C::kVc;
+  const uint32_t sVc = base + C::kVc;
   const uint32_t sVt = FP8 ? sVc : sV;  // 16-bit V tiles
   auto bar = [&](int i) -> uint32_t { return base + C::kBar + 8u * i; };
   const uint32_t* tslot = reinterpret_cast<const uint32_t*>(smem_raw + C::kSlot);
@@ -432,7 +457,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     tma_prefetch_desc(&tmQ);
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(bar(C::kBarKFull + i), 1);
-      mbar_init(bar(C::kBarKEmpty + i), FP8 ? 128 : 1);
+      mbar_init(bar(C::kBarKEmpty + i), 1);
       mbar_init(bar(C::kBarVFull + i), 1);
       mbar_init(bar(C::kBarVEmpty + i), FP8 ? 128 : 1);
     }
@@ -441,13 +466,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       mbar_init(bar(kBarP + i), kGroupThreads);
       mbar_init(bar(kBarP2 + i), kGroupThreads);
       mbar_init(bar(kBarO + i), 1);
-      mbar_init(bar(kBarQFull + i), kConvertQ ? 128 : 1);
+      mbar_init(bar(kBarQFull + i), FP8 ? 128 : 1);
       mbar_init(bar(kBarOFull + i), 1);
       mbar_init(bar(kBarOFree + i), 128);
       mbar_init(bar(kBarStat + i), kGroupThreads);
       mbar_init(bar(kBarLook + i), 4);
-      mbar_init(bar(C::kBarCKFull + i), 128);
-      mbar_init(bar(C::kBarCKFree + i), 1);
       mbar_init(bar(C::kBarCVFull + i), 128);
       mbar_init(bar(C::kBarCVFree + i), 1);
       mbar_init(bar(C::kBarDrain + i), 1);
@@ -628,18 +651,22 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         // (a negative scale flips the sign of A, Q)
         const uint32_t idS = tc::idesc_f16(kRows, KV, kBf16, false) | (a.score_scale < 0.f ? 1u << 13 : 0u);
         const uint64_t dQ = tc::sdesc_sw128(sQ, 16, 1024);
-        const uint64_t dK = tc::sdesc_sw128(FP8 ? sKc : sK, 16, 1024);
+        const uint64_t dK = tc::sdesc_sw128(sK, 16, 1024);
         auto job = [&](bool own_rows) {
           const int x = jobs & 1;
           // the buffer's last P has been used
           if (jobs >= 2 && !(ok = wait_all(bar(kBarO + x), (jobs - 2) >> 1))) return;
           tc::fence_after_sync();
           const uint64_t q = dQ + (own_rows && x ? C::kQBytes >> 4 : 0);
-          constexpr int kAtOnce = NX == 2 ? 1 : C::kBoxes;
+          // FP8: the terms of Q's e4m3 sum, box by box of 128 head dims
+          constexpr int kParts = FP8 ? C::kTerms * static_cast<int>(C::kRawBoxes) : C::kBoxes;
+          constexpr int kAtOnce = NX == 2 ? 1 : kParts;
 #pragma unroll kAtOnce
-          for (int box = 0; box < C::kBoxes; ++box)
-            mma4_ss_all(tm + C::kColS + KV * x, q + ((box * C::kQBox) >> 4),
-                        dK + ((ring.stage * C::kTile + box * C::kBox) >> 4), idS, box > 0);
+          for (int i = 0; i < kParts; ++i) {
+            const int box = FP8 ? i / C::kTerms : i;
+            mma4_ss_all<FP8>(tm + C::kColS + KV * x, q + (((FP8 ? C::q_region(i % C::kTerms, box) : i) * C::kQBox) >> 4),
+                             dK + ((ring.stage * C::kRing + box * C::kBox) >> 4), idS, i > 0);
+          }
           commit_all(bar(kBarS + x));
           ++jobs;
         };
@@ -659,7 +686,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             if (live > 0 && !(ok = wait_all(bar(kBarQFree), live - 1))) break;
             if (lane == 0) {
               const int row_tiles = dual ? 2 : 1;
-              const uint32_t full = bar(kConvertQ ? kBarQRaw : kBarQFull + (live & 1));
+              const uint32_t full = bar(FP8 ? kBarQRaw : kBarQFull + (live & 1));
               mbar_arrive_expect_tx(full, row_tiles * C::kBoxes * a.tpg * a.G * 128);
               for (int xt = 0; xt < row_tiles; ++xt)
 #pragma unroll
@@ -669,7 +696,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             __syncwarp();
           }
           if (!(ok = wait_all(bar(kBarQFull + (live & 1)), live >> 1))) {
-            if (kConvertQ) (void)mbar_wait_bounded(bar(kBarQRaw), live & 1, kDrainNs);
+            if (FP8) (void)mbar_wait_bounded(bar(kBarQRaw), live & 1, kDrainNs);
             else (void)mbar_wait_bounded(bar(kBarQFull + (live & 1)), (live >> 1) & 1, kDrainNs);
             break;  // (no copy outlives the CTA)
           }
@@ -949,40 +976,55 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           }
         }
       };
-      // this thread's rows of Q, bf16 -> f16 in their place: largest magnitude in
-      // [2^14, 2^15); rows beside the unit's stay whatever they are
+      // This warp's rows of Q as sums of e4m3 values, D / 16 lanes a row. A row is scaled by a
+      // power of two to a largest magnitude in [2^7, 2^8), and each term is what the ones
+      // before it leave: of 4 bits each, two hold a bf16 and three an f16 exactly, but
+      // for what lies below 2^-10, 2^-17 of the row's largest. A row with an infinity or NaN
+      // is NaN.
       auto convert_q = [&](int ntok, uint32_t which) {
+        constexpr int kLanes = D / 16, kPass = 32 / kLanes;  // lanes a row, rows a pass
+        const int l = lane % kLanes;
 #pragma unroll 1
         for (int xt = 0; xt < (NX == 2 && ntok > a.tpg ? 2 : 1); ++xt) {
-          if (r >= min(ntok - xt * a.tpg, a.tpg) * a.G) continue;
-          const uint32_t row = sQ + xt * C::kQBytes + r * 128;
-          auto chunk = [&](int i) { return row + (i >> 3) * C::kQBox + (((i & 7) ^ (r & 7)) << 4); };
-          uint32_t top = 0;  // largest magnitudes of the even and the odd elements, as bits
-#pragma unroll 4
-          for (int i = 0; i < D / 8; ++i) {
-            uint32_t w[4];
-            lds_v4(chunk(i), w[0], w[1], w[2], w[3]);
+          const uint32_t tile = sQ + xt * C::kQBytes;
+          const int rows = min(ntok - xt * a.tpg, a.tpg) * a.G;
+#pragma unroll 1
+          for (int r0 = wr0; r0 < min(rows, wr0 + 32); r0 += kPass) {
+            const int row = r0 + lane / kLanes;
+            const uint32_t at = tile + row * 128;
+            uint32_t w[8];
+            lds_v4(at + (l >> 2) * C::kQBox + (((2 * (l & 3)) ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
+            lds_v4(at + (l >> 2) * C::kQBox + (((2 * (l & 3) + 1) ^ (row & 7)) << 4), w[4], w[5], w[6], w[7]);
+            uint32_t top = 0;  // largest magnitudes of the even and the odd elements, as bits
 #pragma unroll
-            for (int e = 0; e < 4; ++e) top = __vmaxu2(top, w[e] & 0x7fff7fffu);
-          }
-          // 2^-sh from its exponent bits; below 2^-111 (scores that are zero for any
-          // weight) the largest stays under 2^14, as does zero
-          const int ex = static_cast<int>(max(top >> 16, top & 0xffffu) >> 7);  // 255: inf
-          const int sh = ex == 255 ? 0 : max(ex - 141, -126);
-          const float m = __int_as_float((127 - sh) << 23);
-          const float2 m2 = make_float2(m, m);
-#pragma unroll 4
-          for (int i = 0; i < D / 8; ++i) {
-            uint32_t w[4];
-            lds_v4(chunk(i), w[0], w[1], w[2], w[3]);
+            for (int i = 0; i < 8; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 t = __fmul2_rn(make_float2(f32_of<QT>(w[e], 0), f32_of<QT>(w[e], 1)), m2);
-              w[e] = pack16x2<false>(t.x, t.y);
+            for (int o = kLanes / 2; o > 0; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(kFull, top, o));
+            const int ex = __float_as_int(f32_of<QT>(max(top >> 16, top & 0xffffu), 0)) >> 23;  // 255: not finite
+            // (a row below 2^-119 has scores of zero for any weight)
+            const int sh = ex == 255 ? 0 : max(ex - 134, -126);
+            const float m = __int_as_float(ex == 255 ? 0x7fc00000 : (127 - sh) << 23);
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = f32_of<QT>(w[i >> 1], i & 1) * m;
+            __syncwarp();  // (all of the row has been read)
+#pragma unroll
+            for (int t = 0; t < C::kTerms; ++t) {
+              uint32_t e[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) {
+                const uint32_t pair = e4m3x2_of(v[i], v[i + 1]);
+                e[i >> 2] |= pair << (8 * (i & 2));
+                const uint32_t back = e4m3x2_to_f16x2(static_cast<uint16_t>(pair));
+                v[i] -= f32_of<kF16>(back, 0);
+                v[i + 1] -= f32_of<kF16>(back, 1);
+              }
+              if (row < rows)
+                sts_v4(at + C::q_region(t, l >> 3) * C::kQBox + (((l & 7) ^ (row & 7)) << 4), make_uint4(e[0], e[1], e[2], e[3]));
             }
-            sts_v4(chunk(i), make_uint4(w[0], w[1], w[2], w[3]));
+            if (l == 0 && row < rows) sts_s8(base + C::kShift + (which & 1) * NX * kRows + xt * kRows + row, sh);
+            __syncwarp();
           }
-          sts_s8(base + C::kShift + (which & 1) * NX * kRows + xt * kRows + r, sh);
         }
         fence_proxy_async();
         mbar_arrive(bar(kBarQFull + (which & 1)));
@@ -1004,25 +1046,18 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         int n = 0;
         do {
           if (n < nt) {
-            const uint32_t free_par = (c - 2) >> 1;  // of the buffers' last tile
-            constexpr int kCopies = NX == 2 ? 1 : 2;
-#pragma unroll kCopies
-            for (int h = 0; h < 2; ++h) {  // K, V
-              if (!(ok = wait_all(bar(h ? C::kBarVFull : C::kBarKFull), c))) break;
-              if (c > 1 && !(ok = wait_all(bar((h ? C::kBarCVFree : C::kBarCKFree) + (c & 1)), free_par))) break;
-              convert(h ? sV : sK, (h ? sVc : sKc) + (c & 1) * C::kTile, h ? v_lo - n * KV : 0, h ? v_hi - n * KV : KV);
-              fence_proxy_async();  // the f16 tile, visible to the tensor core
-              mbar_arrive(bar((h ? C::kBarCVFull : C::kBarCKFull) + (c & 1)));
-              mbar_arrive(bar(h ? C::kBarVEmpty : C::kBarKEmpty));  // reload the stage
-              if (h == 0 && n == 0) {
-                if (kConvertQ) {
-                  if (!(ok = wait_all(bar(kBarQRaw), live))) break;
-                  convert_q(ntok, live);
-                }
-                ++live;
-              }
+            if (n == 0) {
+              if (!(ok = wait_all(bar(kBarQRaw), live))) break;
+              convert_q(ntok, live);
+              ++live;
             }
-            if (!ok) break;
+            const int stage = c % C::kVStages;
+            if (!(ok = wait_all(bar(C::kBarVFull + stage), c / C::kVStages))) break;
+            if (c > 1 && !(ok = wait_all(bar(C::kBarCVFree + (c & 1)), (c - 2) >> 1))) break;
+            convert(sV + stage * C::kRing, sVc + (c & 1) * C::kTile, v_lo - n * KV, v_hi - n * KV);
+            fence_proxy_async();  // the f16 tile, visible to the tensor core
+            mbar_arrive(bar(C::kBarCVFull + (c & 1)));
+            mbar_arrive(bar(C::kBarVEmpty + stage));  // reload the stage
             ++c;
           }
           if (n == 0 && k > 0) store(k - 1);
@@ -1109,7 +1144,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       const int sure_lo = a.window > 0 ? last - a.window : -start;
       // (never zero, so that a masked score stays -inf)
       float sc = fmaxf(fabsf(a.score_scale), FLT_MIN);
-      if constexpr (kConvertQ) {
+      if constexpr (FP8) {
         if (!(ok = wait_all(bar(kBarQFull + (which & 1)), which >> 1))) break;
         if (valid) sc = fmaxf(FLT_MIN, ldexpf(sc, lds_s8(base + C::kShift + (which & 1) * NX * kRows + xt * kRows + r)));
       }
@@ -1375,7 +1410,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
 template <int QT, int D, bool FP8, bool SMALL>
 cudaError_t launch_typed(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                          const PackedArgs& a, cudaStream_t s, bool pdl) {
-  using C = Cfg<D, FP8>;
+  using C = Cfg<QT, D, FP8>;
   // a function attribute of the current device's context: set every time, a host-side
   // store
   cudaError_t e = cudaFuncSetAttribute(packed_attn_tc_kernel<QT, D, FP8, SMALL>,
