@@ -36,11 +36,13 @@
 // through for infinities and NaN, which a weight of zero would not keep out of the
 // other rows, and such a tile is added up without the tensor cores.
 //
-// FP8 caches: the storing warps turn each raw e4m3 tile into the f16 tile that the products
-// read (exact), in two buffers each for K and V, and store an item's results between the
-// next one's first tiles. A bf16 Q becomes f16 in its place, a thread a row, after a
-// rescale of the row by a power of two to f16's range, which its score scale undoes.
-// (Through registers, loaded by warps along the rows, it had taken 10 us an item.)
+// FP8 caches: S is a product of e4m3 values, K as it is cached and Q as a sum of two (bf16)
+// or three (f16) of them, made in its place by the storing warps; two terms at twice the
+// rate cost as much as one 16-bit product, and K needs no conversion. (With K converted to
+// f16 as V is, 19 trees of 32 tokens on 16,384 took 221 us instead of 157, 1,024 rows at
+// head_dim 256 600 instead of 412.) The weights have to span more than e4m3 does, so V's
+// tiles become f16 (exact), in two buffers, by the storing warps, which store an item's
+// results between the next one's first tiles.
 #pragma once
 
 #include <float.h>
@@ -938,18 +940,17 @@ __global__ void __launch_bounds__(Cfg<QT, D, FP8>::kThreads, 1)
     if constexpr (FP8) {
       // A warp takes every fourth octet of rows, a lane a row of it and every fourth
       // 16-byte chunk: the eight lanes of an access then have eight rows, whose chunks the
-      // swizzle puts into different banks, in the raw tile as in the f16 one. Two chunks at a
-      // time: with 1 or 4, 64 trees take 277 or 268 us instead of 256 (more of them are
-      // faster by themselves, but their instructions displace the other warps'). With one
-      // softmax group there is room for 8 and a copy each for K and V: 1,024 rows on 16,384
-      // tokens at head_dim 256 take 590 us instead of 650.
+      // swizzle puts into different banks, in the raw tile as in the f16 one. One chunk at a
+      // time: with 2, 4 at once 1,024 rows on 16,384 tokens take 229, 242 us instead of 216 (more
+      // are faster by themselves, but their instructions displace the other warps'). With
+      // one softmax group there is room for 8: 411 us at head_dim 256, with 4 417.
       constexpr int kOctets = KV / 32, kParts = D / 64;
       const int o0 = warp - C::kStoreWarp, sub = lane & 7, ch = lane >> 3;
       const uint32_t from0 = (8 * o0 + sub) * 128 + ((ch ^ sub) << 4);
       const uint32_t to_lo = (8 * o0 + sub) * 128 + (((2 * ch) ^ sub) << 4), to_hi = to_lo ^ 16;
       // Rows [r_lo, r_hi) are converted, the others become zeros.
       auto convert = [&](uint32_t src, uint32_t dst, int r_lo, int r_hi) {
-        constexpr int N = NX == 2 ? 2 : 8;  // chunks of a lane at once
+        constexpr int N = NX == 2 ? 1 : 8;  // chunks of a lane at once
         static_assert(kOctets * kParts == 8, "chunks a lane");
         const bool part = r_lo > 0 || r_hi < KV;
 #pragma unroll 1

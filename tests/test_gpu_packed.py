@@ -523,3 +523,31 @@ def test_large_batches(B):
     new = [(7 * b) % 4 for b in range(B)]
     Step(new, [(5 * b) % 23 for b in range(B)], Hq=2, Hkv=1, D=64, seed=38).check()
     Step(new, [(5 * b) % 23 for b in range(B)], Hq=2, Hkv=1, D=64, seed=38, tree=True).check()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("D", [128, 256])
+def test_query_ranges_on_an_e4m3_cache(D, dtype):
+    """Rows of small and large values side by side (up to 2^27: f16 has infinities there), of
+    subnormal ones, zeros, NaN. Next to a row's largest magnitude m an element may be off by
+    2^-17 m, and so a score by 2^-17 m sum |k| scale, a weight by twice that of its own value."""
+    st = Step([70, 9, 33], [40, 300, 0], D=D, fp8=True, dtype=dtype, seed=39)
+    g = torch.Generator(device="cuda").manual_seed(40)
+    T, Hq = st.q.shape[:2]
+    small = torch.exp2(-24 * torch.rand(T, Hq, D, generator=g, device="cuda"))
+    sign = torch.where(torch.rand(T, Hq, D, generator=g, device="cuda") < 0.5, -1.0, 1.0)
+    row = torch.exp2(-torch.arange(T, device="cuda").float() % 26)[:, None, None]
+    st.q = (sign * small * 4 * row).to(dtype)
+    st.q[3] = 0
+    st.q[5] = torch.finfo(dtype).smallest_normal / 4
+    st.q[7, 0, 5] = float("inf")
+    st.q[8, 1, 6] = float("nan")
+    st.q[9, 2, 7] = float("-inf")
+    out, (ref, A) = st.run().double(), st.expect()
+    bad = ~st.q.isfinite().all(-1)
+    assert bad.sum() >= 3 and out[bad].isnan().all() and ref[bad].isnan().all()
+    ks = max(float(values(k, st.k_scale, True).abs().sum(-1).max()) for k in st.k)
+    ds = st.scale * ks * 2.0 ** -17 * st.q.double().abs().amax(-1, keepdim=True)
+    tol = (2.0 ** -11 + 2.0 ** -14 + 2 * ds) * A + U[dtype] * ref.abs() + 2.0 ** -24
+    err = ((out - ref).abs() / tol)[~bad]
+    assert err.max() <= 1, err.max()
