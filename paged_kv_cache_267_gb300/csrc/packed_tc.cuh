@@ -990,40 +990,48 @@ __global__ void __launch_bounds__(Cfg<QT, D, FP8>::kThreads, 1)
           const uint32_t tile = sQ + xt * C::kQBytes;
           const int rows = min(ntok - xt * a.tpg, a.tpg) * a.G;
 #pragma unroll 1
-          for (int r0 = wr0; r0 < min(rows, wr0 + 32); r0 += kPass) {
-            const int row = r0 + lane / kLanes;
-            const uint32_t at = tile + row * 128;
-            uint32_t w[8];
-            lds_v4(at + (l >> 2) * C::kQBox + (((2 * (l & 3)) ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
-            lds_v4(at + (l >> 2) * C::kQBox + (((2 * (l & 3) + 1) ^ (row & 7)) << 4), w[4], w[5], w[6], w[7]);
-            uint32_t top = 0;  // largest magnitudes of the even and the odd elements, as bits
+          for (int r0 = wr0; r0 < min(rows, wr0 + 32); r0 += 2 * kPass) {
+            float v[2][16];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
+            for (int u = 0; u < 2; ++u) {  // two passes at once
+              const int row = r0 + u * kPass + lane / kLanes;
+              const uint32_t at = tile + row * 128 + (l >> 2) * C::kQBox;
+              uint32_t w[8];
+              lds_v4(at + (((2 * (l & 3)) ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
+              lds_v4(at + (((2 * (l & 3) + 1) ^ (row & 7)) << 4), w[4], w[5], w[6], w[7]);
+              uint32_t top = 0;  // largest magnitudes of the even and the odd elements, as bits
 #pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(kFull, top, o));
-            const int ex = __float_as_int(f32_of<QT>(max(top >> 16, top & 0xffffu), 0)) >> 23;  // 255: not finite
-            // (a row below 2^-119 has scores of zero for any weight)
-            const int sh = ex == 255 ? 0 : max(ex - 134, -126);
-            const float m = __int_as_float(ex == 255 ? 0x7fc00000 : (127 - sh) << 23);
-            float v[16];
+              for (int i = 0; i < 8; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = f32_of<QT>(w[i >> 1], i & 1) * m;
-            __syncwarp();  // (all of the row has been read)
+              for (int o = kLanes / 2; o > 0; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(kFull, top, o));
+              const int ex = __float_as_int(f32_of<QT>(max(top >> 16, top & 0xffffu), 0)) >> 23;  // 255: not finite
+              // (a row below 2^-119 has scores of zero for any weight)
+              const int sh = ex == 255 ? 0 : max(ex - 134, -126);
+              const float m = __int_as_float(ex == 255 ? 0x7fc00000 : (127 - sh) << 23);
 #pragma unroll
-            for (int t = 0; t < C::kTerms; ++t) {
-              uint32_t e[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-              for (int i = 0; i < 16; i += 2) {
-                const uint32_t pair = e4m3x2_of(v[i], v[i + 1]);
-                e[i >> 2] |= pair << (8 * (i & 2));
-                const uint32_t back = e4m3x2_to_f16x2(static_cast<uint16_t>(pair));
-                v[i] -= f32_of<kF16>(back, 0);
-                v[i + 1] -= f32_of<kF16>(back, 1);
-              }
-              if (row < rows)
-                sts_v4(at + C::q_region(t, l >> 3) * C::kQBox + (((l & 7) ^ (row & 7)) << 4), make_uint4(e[0], e[1], e[2], e[3]));
+              for (int i = 0; i < 16; ++i) v[u][i] = f32_of<QT>(w[i >> 1], i & 1) * m;
+              if (l == 0 && row < rows) sts_s8(base + C::kShift + (which & 1) * NX * kRows + xt * kRows + row, sh);
             }
-            if (l == 0 && row < rows) sts_s8(base + C::kShift + (which & 1) * NX * kRows + xt * kRows + row, sh);
+            __syncwarp();  // (all of the rows has been read)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int row = r0 + u * kPass + lane / kLanes;
+#pragma unroll
+              for (int t = 0; t < C::kTerms; ++t) {
+                uint32_t e[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                  const uint32_t pair = e4m3x2_of(v[u][i], v[u][i + 1]);
+                  e[i >> 2] |= pair << (8 * (i & 2));
+                  const uint32_t back = e4m3x2_to_f16x2(static_cast<uint16_t>(pair));
+                  v[u][i] -= f32_of<kF16>(back, 0);
+                  v[u][i + 1] -= f32_of<kF16>(back, 1);
+                }
+                if (row < rows)
+                  sts_v4(tile + row * 128 + C::q_region(t, l >> 3) * C::kQBox + (((l & 7) ^ (row & 7)) << 4),
+                         make_uint4(e[0], e[1], e[2], e[3]));
+              }
+            }
             __syncwarp();
           }
         }
