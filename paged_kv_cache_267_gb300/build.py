@@ -27,7 +27,8 @@ CU_SOURCES = ["decode_bf16.cu", "decode_f16.cu", "decode_fp8.cu", "decode_mq_bf1
               "decode_mq_f16.cu", "decode_mq_fp8.cu", "chunk_tc.cu", "merge_reshape.cu",
               "decode_noalloc.cu", "selftest.cu", "pool_ops.cu", "norm_cache.cu",
               "shared_plan.cu", "prefix_tc.cu", "shared_merge.cu", "decode_sh_bf16.cu", "decode_sh_f16.cu",
-              "decode_sh_fp8.cu", "packed_plan.cu", "packed_tc.cu", "packed_tc_small.cu", "packed_merge.cu", "cache_moves.cu"]
+              "decode_sh_fp8.cu", "packed_plan.cu", "packed_tc.cu", "packed_tc_small.cu",
+              "packed_tc_whole.cu", "packed_merge.cu", "cache_moves.cu"]
 CPP_SOURCES = ["pa_api.cpp", "pa_step.cpp", "pa_packed.cpp", "pa_alloc.cpp"]
 
 

@@ -48,7 +48,10 @@ struct PackedArgs {
 };
 cudaError_t packed_launch(int qt, bool fp8, int D, const CUtensorMap& tk, const CUtensorMap& tv,
                           const CUtensorMap& tq, const PackedArgs& a, cudaStream_t s, bool pdl);
+// Small steps, which have no plan kernel: pairs cut between CTAs, or whole pairs and no join.
 cudaError_t packed_launch_small(int qt, bool fp8, int D, const CUtensorMap& tk, const CUtensorMap& tv,
+                                const CUtensorMap& tq, const PackedArgs& a, cudaStream_t s, bool pdl);
+cudaError_t packed_launch_whole(int qt, bool fp8, int D, const CUtensorMap& tk, const CUtensorMap& tv,
                                 const CUtensorMap& tq, const PackedArgs& a, cudaStream_t s, bool pdl);
 
 struct PackedMergeArgs {

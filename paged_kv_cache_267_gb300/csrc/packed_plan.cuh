@@ -17,7 +17,7 @@
 //     them.
 // A unit that attends to nothing counts as one tile (its rows are zeros).
 // Steps of few sequences and pairs have no plan kernel: every CTA works out its own part of
-// split mode, and leaves the merge its note.
+// split mode, and leaves the merge its note, or takes whole pairs in turn.
 #pragma once
 
 #include <stddef.h>

@@ -68,6 +68,10 @@ constexpr float kRescaleAbove = 8.f;         // log2 units
 constexpr float kF16Lift = 7.f;              // log2 units
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kItemRing = 3;                 // items known at once
+// Who works out a CTA's items: the plan kernel, or the CTA itself (small steps), by cutting
+// the space of places or taking whole pairs. (Kernels of their own: each would hold the
+// others' registers, 131 us instead of 119 for one tree on 131,072 tokens.)
+enum { kPlanned = 0, kSmallCut = 1, kSmallWhole = 2 };
 
 template <int QT, int D, bool FP8>
 struct Cfg {
@@ -83,7 +87,8 @@ struct Cfg {
   // Barriers: K and V rings (full, empty); per S buffer: computed, half of P written, the
   // other half, product with V complete; Q loaded, ready (items in turn) and done with; per
   // group: last product of an item complete, O and statistics read, statistics written,
-  // a tile's V looked through; FP8: converted V (two buffers) written and read; items known and read; the ends of the two product warps.
+  // a tile's V looked through; FP8: converted V (two buffers) written and read; items
+  // known and read; the ends of the two product warps.
   enum {
     kBarKFull = 0,
     kBarKEmpty = kBarKFull + kStages,
@@ -265,13 +270,17 @@ __device__ __forceinline__ int cut(int f0, int tpg, int wsz, int me, PackedItem*
 }
 
 // The plan of a small step (at most 32 sequences), which every CTA's K warp works out by
-// itself: split mode, lane b has sequence b. It saves the plan kernel in front, 4 us of a
-// step of 11.
+// itself, lane b with sequence b: split mode or, where no pair can have more than a few
+// tiles, whole pairs in turn, which need no join. It saves the plan kernel in front, 4 us of
+// a step of 11, and the join's launch behind.
+template <bool WHOLE>
 struct SmallPlan {
   int n, q0, len;  // of this lane's sequence: new tokens, first row, length
   int wsz;
   // the next pair: sequence, unit of it, KV head, places before it
   int b, u, h, f0;
+  // (WHOLE: f0 is the next pair's number, u and h the units of this lane's sequence and those
+  // up to its end)
 
   __device__ __forceinline__ PackedUnit unit(const PackedArgs& a, int b, int u) const {
     const int n_b = __shfl_sync(kFull, n, b), len_b = __shfl_sync(kFull, len, b), q_b = __shfl_sync(kFull, q0, b);
@@ -301,6 +310,16 @@ struct SmallPlan {
     if (me == 0) {
       if (bad || (a.tree && n > 64)) atomicOr(a.err, PA_DEVERR_QUERY);
       if (len != l0) atomicOr(a.err, PA_DEVERR_SEQ_LEN);
+    }
+    if constexpr (WHOLE) {
+      f0 = me;
+      u = h = (n + a.tpu - 1) / a.tpu;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(kFull, h, o);
+        if (lane >= o) h += x;
+      }
+      return;
     }
     // places of this lane's sequence, one KV head
     int mine = 0;
@@ -334,6 +353,16 @@ struct SmallPlan {
   // CTA `me`'s part of the next pair that it has one of, and its join's note for the merge
   // where the pair begins here and goes on in the next CTA.
   __device__ __forceinline__ void next(const PackedArgs& a, int lane, int me, PackedItem* it) {
+    if constexpr (WHOLE) {  // every a.ctas'th pair
+      const int un = f0 / a.Hkv, kvh = f0 - un * a.Hkv;
+      const unsigned behind = __ballot_sync(kFull, h > un);
+      if (behind == 0) return;
+      const int at = __ffs(behind) - 1;
+      const PackedUnit x = unit(a, at, un - __shfl_sync(kFull, h - u, at));
+      *it = PackedItem{x.b, kvh, x.row0, x.ntok, x.pos0, x.first, x.lo, x.hi, 0, x.nt, -1, 0};
+      f0 += a.ctas;
+      return;
+    }
     while (b < 32) {
       const PackedUnit x = unit(a, b, u);
       const int c = places(a, x), whole_nt = max(x.nt, 1);
@@ -421,13 +450,13 @@ __device__ __forceinline__ uint32_t below(int k) {
   return k <= 0 ? 0u : (k >= 32 ? 0xffffffffu : (1u << k) - 1u);
 }
 
-// SMALL: a small step, which has no plan kernel.
-template <int QT, int D, bool FP8, bool SMALL>
+template <int QT, int D, bool FP8, int PLAN>
 __global__ void __launch_bounds__(Cfg<QT, D, FP8>::kThreads, 1)
     packed_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK,
                           const __grid_constant__ CUtensorMap tmV,
                           const __grid_constant__ CUtensorMap tmQ, const PackedArgs a) {
   using C = Cfg<QT, D, FP8>;
+  constexpr bool SMALL = PLAN != kPlanned;
   constexpr bool kBf16 = !FP8 && QT == kBF16;  // operand type of the products
   constexpr float kLift = kBf16 ? 0.f : kF16Lift;
   constexpr int NX = C::kGroups, KV = C::kKv;
@@ -495,7 +524,7 @@ __global__ void __launch_bounds__(Cfg<QT, D, FP8>::kThreads, 1)
   griddep_wait();  // the plan, and behind it the caches and queries, are written
   griddep_launch_dependents();
   if constexpr (SMALL) {
-    if (tid == 0) reinterpret_cast<PackedJoin*>(a.plan + packed_joins_at(a.ctas))[blockIdx.x].n = 0;
+    if (tid == 0 && PLAN == kSmallCut) reinterpret_cast<PackedJoin*>(a.plan + packed_joins_at(a.ctas))[blockIdx.x].n = 0;
     __syncthreads();  // (before the K warp may note a join)
   }
 
@@ -552,7 +581,7 @@ __global__ void __launch_bounds__(Cfg<QT, D, FP8>::kThreads, 1)
         whole = a.plan[kPkWhole], pairs = a.plan[kPkPairs], wsz = a.plan[kPkWsz];
         share = reinterpret_cast<const int2*>(a.plan + packed_ctas_at())[me];
       }
-      SmallPlan sp;
+      SmallPlan<PLAN == kSmallWhole> sp;
       if constexpr (SMALL) {
         if (!is_v) sp.begin(a, lane, me);
       }
@@ -1416,20 +1445,20 @@ __global__ void __launch_bounds__(Cfg<QT, D, FP8>::kThreads, 1)
   }
 }
 
-template <int QT, int D, bool FP8, bool SMALL>
+template <int QT, int D, bool FP8, int PLAN>
 cudaError_t launch_typed(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                          const PackedArgs& a, cudaStream_t s, bool pdl) {
   using C = Cfg<QT, D, FP8>;
   // a function attribute of the current device's context: set every time, a host-side
   // store
-  cudaError_t e = cudaFuncSetAttribute(packed_attn_tc_kernel<QT, D, FP8, SMALL>,
+  cudaError_t e = cudaFuncSetAttribute(packed_attn_tc_kernel<QT, D, FP8, PLAN>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
   if (e != cudaSuccess) return e;
   if constexpr (C::kSplitRegs) {
     // the softmax warps wait for registers that the block must have been given
     static const int regs = [] {
       cudaFuncAttributes f;
-      return cudaFuncGetAttributes(&f, packed_attn_tc_kernel<QT, D, FP8, SMALL>) == cudaSuccess ? f.numRegs : 0;
+      return cudaFuncGetAttributes(&f, packed_attn_tc_kernel<QT, D, FP8, PLAN>) == cudaSuccess ? f.numRegs : 0;
     }();
     if (regs < C::kLaunchRegs) return cudaErrorLaunchOutOfResources;
   }
@@ -1443,28 +1472,28 @@ cudaError_t launch_typed(const CUtensorMap& tk, const CUtensorMap& tv, const CUt
   attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, packed_attn_tc_kernel<QT, D, FP8, SMALL>, tk, tv, tq, a);
+  return cudaLaunchKernelEx(&cfg, packed_attn_tc_kernel<QT, D, FP8, PLAN>, tk, tv, tq, a);
 }
 
-template <int QT, bool SMALL>
+template <int QT, int PLAN>
 cudaError_t launch_dim(bool fp8, int D, const CUtensorMap& tk, const CUtensorMap& tv,
                        const CUtensorMap& tq, const PackedArgs& a, cudaStream_t s, bool pdl) {
   if (fp8) {
-    if (D == 128) return launch_typed<QT, 128, true, SMALL>(tk, tv, tq, a, s, pdl);
-    if (D == 256) return launch_typed<QT, 256, true, SMALL>(tk, tv, tq, a, s, pdl);
+    if (D == 128) return launch_typed<QT, 128, true, PLAN>(tk, tv, tq, a, s, pdl);
+    if (D == 256) return launch_typed<QT, 256, true, PLAN>(tk, tv, tq, a, s, pdl);
     return cudaErrorInvalidValue;
   }
-  if (D == 64) return launch_typed<QT, 64, false, SMALL>(tk, tv, tq, a, s, pdl);
-  if (D == 128) return launch_typed<QT, 128, false, SMALL>(tk, tv, tq, a, s, pdl);
-  if (D == 256) return launch_typed<QT, 256, false, SMALL>(tk, tv, tq, a, s, pdl);
+  if (D == 64) return launch_typed<QT, 64, false, PLAN>(tk, tv, tq, a, s, pdl);
+  if (D == 128) return launch_typed<QT, 128, false, PLAN>(tk, tv, tq, a, s, pdl);
+  if (D == 256) return launch_typed<QT, 256, false, PLAN>(tk, tv, tq, a, s, pdl);
   return cudaErrorInvalidValue;
 }
 
-template <bool SMALL>
+template <int PLAN>
 cudaError_t launch_packed(int qt, bool fp8, int D, const CUtensorMap& tk, const CUtensorMap& tv,
                           const CUtensorMap& tq, const PackedArgs& a, cudaStream_t s, bool pdl) {
-  return qt == kBF16 ? launch_dim<kBF16, SMALL>(fp8, D, tk, tv, tq, a, s, pdl)
-                     : launch_dim<kF16, SMALL>(fp8, D, tk, tv, tq, a, s, pdl);
+  return qt == kBF16 ? launch_dim<kBF16, PLAN>(fp8, D, tk, tv, tq, a, s, pdl)
+                     : launch_dim<kF16, PLAN>(fp8, D, tk, tv, tq, a, s, pdl);
 }
 
 }  // namespace
