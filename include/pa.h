@@ -481,6 +481,12 @@ pa_status pa_prefill_packed(const pa_tensor* out, const pa_tensor* q, const pa_t
  * as above. A row with no bit attends to the tokens before the drafted ones; where there
  * are none it is zeros. Of more than 64 drafted tokens the rows are computed against the
  * first 64 (flagged PA_DEVERR_QUERY). Drafted tokens at negative positions are not there.
+ * A row's place in its sequence, for the positions of pa_norm_rope_and_cache, is that of
+ * its own continuation: L - n + (its bits) - 1, its own bit among them; siblings share it.
+ * pa_pool_extend writes L - n + i for row i of the sequence, as it does not know the tree:
+ * add (bits - 1 - i) to the drafted rows' positions before that call. The rows of K and V
+ * stay in the slots of L - n + i, and the token that an accepted path has in place d is
+ * the one that pa_compact_cache moves to L - n + d.
  *
  *   tree_mask     [T] int64, bit j: drafted token j of the row's sequence.
  *   window        <= 0: none, else at least 64 (it never cuts through the tree).
@@ -525,10 +531,11 @@ pa_status pa_copy_blocks(const pa_tensor* key_cache, const pa_tensor* value_cach
  * kept_tokens[b], if given, is that rounded up to whole blocks: pa_pool_release with
  * released = 1 and shared_tokens = kept_tokens gives the blocks behind it back (its own
  * lengths then go to a buffer that is not used). Positions behind the kept ones keep
- * their rows. A list that is not strictly ascending in [0, n), a count that is negative
- * or beyond n or the list, or a negative base leaves the sequence as it is
- * (PA_DEVERR_QUERY); a table entry outside of the pool moves nothing
- * (PA_DEVERR_BLOCK_ID). Sequences that share the blocks that rows are moved in are a
+ * their rows. Rows move as they are: a key that was rotated for another place than its
+ * new one keeps that rotation (pa_decode_tree says which place a drafted token has). A
+ * list that is not strictly ascending in [0, n), a count that is negative or beyond n or
+ * the list, or a negative base leaves the sequence as it is (PA_DEVERR_QUERY); a table
+ * entry outside of the pool moves nothing (PA_DEVERR_BLOCK_ID). Sequences that share the blocks that rows are moved in are a
  * caller error.
  *   caches        as for pa_copy_blocks; block_tables, seq_lens as for pa_decode.
  *   query_start   [B + 1] int32; kept [B, M] int32 contiguous; num_kept, seq_lens_out,

@@ -372,6 +372,9 @@ def decode_tree(q, key_cache, value_cache, block_tables, seq_lens, query_start, 
     query_start[b + 1]) of q [T, Hq, D] are the last (at most 64) tokens of
     sequence b; each attends to the tokens before them and to drafted token j of
     its sequence where bit j of tree_mask [T] (int64) is set (itself included).
+    Its place in the sequence, which q and k are to be rotated for, is that behind
+    its ancestors: add (bits set - 1 - its place among the drafted rows) to the
+    positions that pool_extend gives before norm_rope_and_cache.
     Returns out [T, Hq, D] (allocated if not given); rows outside of every
     sequence are not written."""
     if out is None:
