@@ -535,8 +535,9 @@ pa_status pa_copy_blocks(const pa_tensor* key_cache, const pa_tensor* value_cach
  * new one keeps that rotation (pa_decode_tree says which place a drafted token has). A
  * list that is not strictly ascending in [0, n), a count that is negative or beyond n or
  * the list, or a negative base leaves the sequence as it is (PA_DEVERR_QUERY); a table
- * entry outside of the pool moves nothing (PA_DEVERR_BLOCK_ID). Sequences that share the blocks that rows are moved in are a
- * caller error.
+ * entry outside of the pool moves nothing (PA_DEVERR_BLOCK_ID). Caches of no layers, heads
+ * or elements have no rows to move: lengths only. Sequences that share the blocks that
+ * rows are moved in are a caller error.
  *   caches        as for pa_copy_blocks; block_tables, seq_lens as for pa_decode.
  *   query_start   [B + 1] int32; kept [B, M] int32 contiguous; num_kept, seq_lens_out,
  *                 kept_tokens [B] int32 (kept_tokens may be NULL). Outputs overlap

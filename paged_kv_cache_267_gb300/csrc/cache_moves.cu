@@ -164,13 +164,14 @@ cudaError_t copy_blocks_launch(const CopyBlocksArgs& a, cudaStream_t s) {
 cudaError_t compact_cache_launch(const CompactArgs& a, int num_sms, cudaStream_t s) {
   CompactArgs x = a;
   // as many planes a CTA as leave the GPU a few waves of CTAs
-  const long long ctas = static_cast<long long>(a.B) * 2 * a.layers;
+  const int planes = std::max(2 * a.layers, 1);  // (no layers: lengths only)
+  const long long ctas = static_cast<long long>(a.B) * planes;
   const long long units = static_cast<long long>(a.row_units) * a.Hkv;
-  x.share = static_cast<int>(std::min<long long>(std::max<long long>(ctas / (num_sms * 16ll), 1), 2 * a.layers));
+  x.share = static_cast<int>(std::min<long long>(std::max<long long>(ctas / (num_sms * 16ll), 1), planes));
   x.share = static_cast<int>(std::min<long long>(x.share, std::max<long long>(0x7fff0000ll / (kThreads * std::max(units, 1ll)), 1)));
   x.unit_div = fast_div(static_cast<uint32_t>(units));
   x.row_div = fast_div(static_cast<uint32_t>(a.row_units));
-  return launch(compact_cache_kernel, dim3(a.B, (2 * a.layers + x.share - 1) / x.share), x, s);
+  return launch(compact_cache_kernel, dim3(a.B, (planes + x.share - 1) / x.share), x, s);
 }
 
 }  // namespace pa

@@ -463,11 +463,11 @@ pa_status pa_compact_cache(const pa_tensor* key_cache, const pa_tensor* value_ca
     a.err = dev.err_word;
     a.k_layer = m.k_layer;
     a.v_layer = m.v_layer;
-    // (no layers or no heads: lengths only)
-    a.layers = static_cast<int>(std::max<int64_t>(m.layers, 1));
+    // (without layers, heads or elements rows have no bytes, but lists and tables are looked at)
+    a.layers = static_cast<int>(m.layers);
     a.B = static_cast<int>(B);
     a.MB = static_cast<int>(MB);
-    a.NB = numel(key_cache) ? static_cast<int>(m.NB) : 0;
+    a.NB = static_cast<int>(m.NB);
     a.Hkv = numel(key_cache) ? static_cast<int>(m.Hkv) : 0;
     a.bs = block_size;
     a.M = static_cast<int>(kept->shape[1]);
