@@ -26,10 +26,17 @@ constexpr int64_t kMaxRowStride = int64_t(1) << 23;
 constexpr int kMinPlaces = 8;
 constexpr int kSplitPlaces = 16;
 constexpr int kSmallPairs = 3;  // a CTA, of a step that is planned without a kernel
-// Of a pair of such a step, at most, where pairs are not cut, which saves the join: 4 trees of
-// 16 tokens on 800 take 15.0 us instead of 17.3, one token each of 4 requests on 800 11.7
-// instead of 13.0, but on 1,800 18.3 instead of 14.1.
+// Tiles of a pair of such a step, at most, where pairs are not cut, which saves the join: one
+// token each of 4 requests on 800 takes 11.7 us instead of 13.0, but on 1,800 18.3 instead of
+// 14.1.
 constexpr int kWholeTiles = 10;
+// What a cut costs a CTA of such a step, and what a tile of one or of two row tiles takes
+// there, in places of 0.38 us: whole pairs take whole rounds, cut ones an even share and this.
+// (152 CTAs, 8 KV heads, 48 tokens on 1,000: whole against cut, 20 requests, in two rounds,
+// 47.9 and 38.9 us, 24 49.2 and 44.2, 28 49.6 and 50.9; 4 requests 25.7 and 22.7, 16 26.8 and
+// 34.5. 16 tokens on 1,000: 20 requests 25.7 and 25.6, 32 32.9 and 38.7.)
+constexpr int kCutPlaces = 32;
+constexpr int kTileWhole = 3, kTileWhole2 = 5;
 
 bool misaligned(const pa_tensor* t, uintptr_t n) {
   return numel(t) > 0 && reinterpret_cast<uintptr_t>(t->data) % n;
@@ -94,7 +101,13 @@ PackedSizes packed_sizes(int64_t T, int64_t B, int64_t span, int G, int64_t Hkv,
             dprod({double(units), double(Hkv), 4.0 * double(span / z.kv + 2) + kOutPlaces}) < k2p31 - 65536;
   const double tiles = dprod({double(units), double(Hkv), double(span / z.kv + 2)});
   z.ctas = static_cast<int>(std::min<double>(num_sms, std::max(1.0, std::ceil(tiles * 4 / kMinPlaces))));
-  z.whole = z.small && span / z.kv + 2 <= kWholeTiles;
+  // (lengths and how the rows are spread are not known here: full tables, even shares)
+  const int64_t seqs = std::max<int64_t>(std::min(B, T), 1), each = (T + seqs * z.tpu - 1) / (seqs * z.tpu);
+  const double pairs = dprod({double(seqs), double(each), double(Hkv)});
+  const double cost = kOutPlaces + double((span + z.kv - 1) / z.kv) *
+                                       (shape.rows == 2 && T > seqs * z.tpg ? kTileWhole2 : kTileWhole);
+  z.whole = z.small && span / z.kv + 2 <= kWholeTiles &&
+            std::ceil(pairs / num_sms) * cost <= pairs * cost / num_sms + kCutPlaces;
   if (z.whole) z.ctas = static_cast<int>(std::min<int64_t>(num_sms, std::max<int64_t>(units * Hkv, 1)));
   z.plan_words = packed_plan_words(z.ctas, static_cast<size_t>(units));
   // behind the decode workspace's counters, which stay zero
