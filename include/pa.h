@@ -458,8 +458,11 @@ pa_status pa_prefill_chunk_workspace_size(int64_t batch, int32_t num_queries,
  * 2^-8 of each weight, else f16: 2^-11), against sums of the unrounded ones. On e4m3
  * caches an element of q is off by at most 2^-17 of its row's largest magnitude (elements
  * of 2^-9, f16 2^-6, of it and more are exact), and a row of q with an infinity or NaN is
- * NaN. The order of summation depends on the lengths, the tables' width and the GPU's SM
- * count only: results are bit-reproducible.
+ * NaN. The order of summation depends on the lengths, the query starts and what the host knows
+ * of the step (rows of q with their padding, batch, head counts, head_dim, types, the tables'
+ * width, the window, the GPU's SM count) and on nothing else: a call on the same sizes and
+ * values gives the same bits. With q or the batch padded to another size, or in wider tables,
+ * a step may be cut at other places and differ in its last bits.
  * All inputs are read behind the dependency wait: any kernel may have written them just
  * before. Workspace: pa_packed_workspace_size() bytes, from the same source as
  * pa_decode's and under the same rules. Errors as for pa_decode.

@@ -30,3 +30,21 @@ def test_rounds_of_whole_pairs(R, n, ctx, route):
     out, got = launches(st)
     assert got == route
     st.check(got=out)
+
+
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("D,fp8", [(64, False), (128, False), (128, True), (256, False)])
+def test_padded_steps_repeat_their_bits(D, fp8, tree):
+    """Other paddings of the rows, the batch and the tables may cut a step elsewhere: each gives the
+    same bits every time, and all of them values within the tolerance."""
+    new, ctx = [40, 3, 17], [600, 900, 0] if D < 256 else [300, 200, 0]
+    ways = set()
+    for pad, wide, empty in ((0, 0, 0), (64, 0, 0), (5000, 0, 0), (0, 40, 0), (64, 200, 0), (0, 0, 20), (0, 0, 31), (300, 90, 40)):
+        st = Step(new + [0] * empty, ctx + [0] * empty, D=D, fp8=fp8, seed=50, tree=tree, pad=pad, wide=wide)
+        out, route = launches(st)
+        ways.add(route)
+        st.check(got=out)
+        n = sum(new)
+        for _ in range(2):
+            assert torch.equal(st.run()[:n], out[:n])
+    assert ways == {WHOLE, CUT, PLANNED}
