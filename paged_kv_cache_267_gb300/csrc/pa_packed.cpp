@@ -96,7 +96,7 @@ PackedSizes packed_sizes(int64_t T, int64_t B, int64_t span, int G, int64_t Hkv,
   z.slot_rows = shape.rows == 2 && T > z.tpg ? 256 : 128;
   const int64_t units = T / z.tpu + std::min(B, T);  // at most
   // lane b of a warp plans sequence b; with more pairs than a few a CTA, whole ones, sorted,
-  // are better (a batch of 16 prompts takes 343 us split, 232 whole)
+  // are better (a batch of 16 prompts takes 240 us cut, 197 whole)
   z.small = B <= 32 && units * Hkv <= kSmallPairs * num_sms &&
             dprod({double(units), double(Hkv), 4.0 * double(span / z.kv + 2) + kOutPlaces}) < k2p31 - 65536;
   const double tiles = dprod({double(units), double(Hkv), double(span / z.kv + 2)});

@@ -23,11 +23,12 @@
 //
 // Bound: a K/V tile of two row tiles is 2,112 cycles of tensor work (M128 N128 K16: 66)
 // and takes 2,650, as S, softmax and O of a row tile follow each other in one buffer and
-// only the other group's fill the gaps; one prompt of 16,384 tokens, 32 heads: 1.40 ms,
-// 1,570 TFLOP/s at 1.39 kW. An item costs about 7,000 cycles besides (e4m3: 11,000): Q's load
-// behind the last products and its conversion, the masked tiles, O read out. What the warps run must stay small: some
-// 5,000 instructions a kernel share the instruction cache, and one copy of each piece of
-// code in place of two or three gave 4 to 13%.
+// only the other group's fill the gaps; one prompt of 16,384 tokens, 32 heads: 1.46 to 1.51
+// ms, 1,460 to 1,510 TFLOP/s under the limit of 1.4 kW. An item costs about 7,000 cycles
+// besides (e4m3: 11,000): Q's load behind the last products and its conversion, the masked
+// tiles, O read out. What the warps run must stay small: some 5,000 instructions a kernel
+// share the instruction cache, and one copy of each piece of code in place of two or three
+// gave 4 to 13%.
 //
 // Masks: a row's attended positions in a tile are a bit word per 32 tokens (a range,
 // and for a tree the ancestor bits moved to the tile); tiles that every row of a
